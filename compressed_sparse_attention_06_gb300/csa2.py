@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -34,6 +34,9 @@ EXPORTS = (
     "csa2_compress_step", "csa2_compress_state_bytes", "csa2_compress_state_seed", "csa2_dense_attn",
     "csa2_compress_varlen", "csa2_pool_topk", "csa2_block_hist", "csa2_attn_prepare", "csa2_visible_entries",
     "csa2_index_score_mxq",
+    "csa2_sparse_attn_bwd", "csa2_dense_attn_bwd", "csa2_attn_bwd_workspace_bytes",
+    "csa2_compress_bwd", "csa2_compress_bwd_workspace_bytes",
+    "csa2_attn_mass", "csa2_attn_mass_workspace_bytes", "csa2_evict_select", "csa2_cache_gather",
 )
 
 
@@ -47,6 +50,7 @@ _LIB = None
 _CTX = {}
 
 _vp, _i, _i64, _u, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint, ctypes.c_float
+_sz = ctypes.c_size_t
 
 
 def _declare(lib):
@@ -87,6 +91,19 @@ def _declare(lib):
                                  _i, _i, _i, _i, _f, _u, _vp, _i, _vp, _vp, ctypes.c_size_t, _vp]),
         "csa2_sparse_attn_noalloc": (_i, [_vp, _vp, _i, _vp, _i, _i64, _vp, _i, _vp, _i, _i64, _i64, _i, _vp, _vp,
                                           _i, _i, _i, _i, _f, _u, _vp, _i, _vp, _vp]),
+        "csa2_attn_bwd_workspace_bytes": (_sz, [_vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i64, _i64, _u]),
+        "csa2_sparse_attn_bwd": (_i, [_vp, _vp, _i, _vp, _i, _i64, _vp, _i, _vp, _i, _i64, _i64, _i, _vp, _vp,
+                                      _vp, _vp, _i, _vp, _i, _i, _i, _i, _f, _u, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+        "csa2_dense_attn_bwd": (_i, [_vp, _vp, _i, _vp, _i, _i64, _vp, _i, _vp, _i, _i64, _i64, _i, _vp, _vp,
+                                     _vp, _vp, _i, _vp, _i, _i, _i, _i, _f, _u, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+        "csa2_compress_bwd_workspace_bytes": (_sz, [_i, _i64, _i, _i, _i]),
+        "csa2_compress_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i64, _i, _i, _vp, _f, _u,
+                                   _vp, _i, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+        "csa2_attn_mass_workspace_bytes": (_sz, [_vp, _i, _i, _i, _i, _i64]),
+        "csa2_attn_mass": (_i, [_vp, _vp, _i, _vp, _i, _i64, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _f, _u, _vp, _vp,
+                                _vp, _sz, _vp]),
+        "csa2_evict_select": (_i, [_vp, _vp, _i, _i64, _vp, _i, _i, _vp, _vp]),
+        "csa2_cache_gather": (_i, [_vp, _vp, _i64, _i, _i64, _vp, _i, _vp, _vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -563,3 +580,193 @@ def csa2_sparse_attn_noalloc(q, kv, idx, swa, q_pos, out: torch.Tensor, sink=Non
                                          rope_base, flags, _p(out), _dt(out), _p(lse), _stream(q))
     _check("csa2_sparse_attn_noalloc", st)
     return out, lse
+
+
+def _want(name, t, shape, dtype, device) -> torch.Tensor:
+    """An output or buffer the caller gave: the kernels write (read) it by the call's sizes, so
+    its shape, dtype, device and layout are checked before its pointer is passed on."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t
+
+
+def _given(name, t, shape, dtype, device) -> torch.Tensor:
+    """`t` checked by _want, or a new buffer where it is None."""
+    return alloc(shape, dtype=dtype, device=device) if t is None else _want(name, t, shape, dtype, device)
+
+
+def _attn_bwd(fn, q, kv, sel, k, swa, q_pos, sink, out, lse, dout, window, swa_pos0, rope_base, flags, dq, dkv, dswa,
+              dsink, ws, want_dkv, want_dswa, want_dsink):
+    B, Q, H, c = q.shape
+    dev = q.device
+    _want("out", out, q.shape, out.dtype, dev)
+    _want("dout", dout, q.shape, out.dtype, dev)
+    _want("lse", lse, (B, Q, H), torch.float32, dev)
+    _want("q_pos", q_pos, (B, Q), torch.int64, dev)
+    if sink is not None:
+        _want("sink", sink, (H,), torch.float32, dev)
+    if kv is not None:
+        _want("kv", kv, (B, kv.shape[1], c), kv.dtype, dev)
+    if swa is not None:
+        _want("swa", swa, (B, swa.shape[1], c), swa.dtype, dev)
+    N = kv.shape[1] if kv is not None else 0
+    cap = swa.shape[1] if swa is not None else 0
+    kv_dt = _dt(kv) if kv is not None else F32
+    swa_dt = _dt(swa) if swa is not None else F32
+    dq = _given("dq", dq, q.shape, q.dtype, dev)
+    if kv is not None and (want_dkv or dkv is not None):
+        dkv = _given("dkv", dkv, kv.shape, kv.dtype, dev)
+    if swa is not None and (want_dswa or dswa is not None):
+        dswa = _given("dswa", dswa, swa.shape, swa.dtype, dev)
+    if want_dsink or dsink is not None:
+        dsink = _given("dsink", dsink, (H,), torch.float32, dev)
+    if ws is None:
+        ws = _ws(_lib().csa2_attn_bwd_workspace_bytes(ctx(dev.index), _dt(q), kv_dt, swa_dt, _dt(out), B, Q, H, k, window,
+                                                      N, cap, flags), dev)
+    st = getattr(_lib(), fn)(ctx(dev.index), _p(q), _dt(q), _p(kv), kv_dt, N, _p(sel), k, _p(swa), swa_dt, cap, swa_pos0,
+                             window, _p(q_pos), _p(sink), _p(out), _p(dout), _dt(out), _p(lse), B, Q, H, c, rope_base,
+                             flags, _p(dq), _p(dkv), _p(dswa), _p(dsink), _p(ws), ws.numel() * ws.element_size(),
+                             _stream(q))
+    _check(fn, st)
+    return dq, dkv, dswa, dsink
+
+
+def csa2_sparse_attn_bwd(q, kv, idx, swa, q_pos, sink, out, lse, dout, window: int = 128, swa_pos0: int = 0,
+                         rope_base: float = 10000.0, flags: int = ATTN_DEFAULT, dq: Optional[torch.Tensor] = None,
+                         dkv: Optional[torch.Tensor] = None, dswa: Optional[torch.Tensor] = None,
+                         dsink: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                         want_dkv: bool = True, want_dswa: bool = True, want_dsink: bool = True):
+    """Backward pass of csa2_sparse_attn: its inputs, its out [B,Q,H,c] and lse [B,Q,H], and
+    dout (out's dtype).  Returns (dq, dkv, dswa, dsink), each like the tensor it is the
+    gradient of (dsink [H] f32); None where that tensor is None or the gradient not wanted.
+    `ws` is the workspace (allocated here when not given)."""
+    k = idx.shape[-1] if idx is not None else 0
+    if idx is not None:
+        _want("idx", idx, (*q.shape[:2], k), torch.int32, q.device)
+    return _attn_bwd("csa2_sparse_attn_bwd", q, kv, idx, k, swa, q_pos, sink, out, lse, dout, window, swa_pos0,
+                     rope_base, flags, dq, dkv, dswa, dsink, ws, want_dkv, want_dswa, want_dsink)
+
+
+def csa2_dense_attn_bwd(q, kv, n_visible, k_max: int, swa, q_pos, sink, out, lse, dout, window: int = 128,
+                        swa_pos0: int = 0, rope_base: float = 10000.0, flags: int = ATTN_DEFAULT,
+                        dq: Optional[torch.Tensor] = None, dkv: Optional[torch.Tensor] = None,
+                        dswa: Optional[torch.Tensor] = None, dsink: Optional[torch.Tensor] = None,
+                        ws: Optional[torch.Tensor] = None, want_dkv: bool = True, want_dswa: bool = True,
+                        want_dsink: bool = True):
+    """Backward pass of csa2_dense_attn; arguments and result as csa2_sparse_attn_bwd with
+    n_visible [B,Q] int64 <= k_max in idx's place."""
+    _want("n_visible", n_visible, q.shape[:2], torch.int64, q.device)
+    return _attn_bwd("csa2_dense_attn_bwd", q, kv, n_visible, k_max, swa, q_pos, sink, out, lse, dout, window, swa_pos0,
+                     rope_base, flags, dq, dkv, dswa, dsink, ws, want_dkv, want_dswa, want_dsink)
+
+
+class CompressGrads(NamedTuple):
+    """Gradients of csa2_compress's inputs; None where the input is None or not wanted."""
+    dca: torch.Tensor
+    dza: torch.Tensor
+    dcb: Optional[torch.Tensor]
+    dzb: Optional[torch.Tensor]
+    dprev_cb: Optional[torch.Tensor]
+    dprev_zb: Optional[torch.Tensor]
+    dba: Optional[torch.Tensor]
+    dbb: Optional[torch.Tensor]
+
+
+def csa2_compress_bwd(ca, za, m: int, dout, cb=None, zb=None, ba=None, bb=None, prev_cb=None, prev_zb=None, pos0=0,
+                      rope_base: float = 10000.0, flags: int = 0, ws: Optional[torch.Tensor] = None) -> CompressGrads:
+    """Backward pass of csa2_compress over one stream [n, c] or a batch [B, n, c]: dout
+    [.., n/m, c] (f32 or bf16) is the gradient of the entries.  pos0: int or [B] int64
+    tensor.  Bias gradients come for the biases given."""
+    batched = ca.dim() == 3
+    B, n, c = (ca.shape if batched else (1, *ca.shape))
+    dev = ca.device
+    for name, t in (("za", za), ("cb", cb), ("zb", zb)):
+        if t is not None:
+            _want(name, t, ca.shape, ca.dtype, dev)
+    hist = (B, m, c) if batched else (m, c)
+    for name, t in (("prev_cb", prev_cb), ("prev_zb", prev_zb)):
+        if t is not None:
+            _want(name, t, hist, ca.dtype, dev)
+    for name, t in (("ba", ba), ("bb", bb)):
+        if t is not None:
+            _want(name, t, (m, c), torch.float32, dev)
+    _want("dout", dout, (B, n // m, c) if batched else (n // m, c), dout.dtype, dev)
+    if isinstance(pos0, torch.Tensor):
+        pos_t = _want("pos0", pos0.to(device=dev, dtype=torch.int64).contiguous(), (B,), torch.int64, dev)
+    else:
+        pos_t = torch.full((B,), int(pos0), dtype=torch.int64, device=dev)
+
+    def like(t):
+        return alloc(tuple(t.shape), dtype=t.dtype, device=dev) if t is not None else None
+
+    g = CompressGrads(like(ca), like(za), like(cb), like(zb), like(prev_cb), like(prev_zb), like(ba), like(bb))
+    if ws is None and (ba is not None or bb is not None):
+        ws = _ws(_lib().csa2_compress_bwd_workspace_bytes(B, n, c, m, int(cb is not None)), dev)
+    st = _lib().csa2_compress_bwd(ctx(dev.index), _p(ca), _p(za), _p(cb), _p(zb), _dt(ca), _p(ba), _p(bb), _p(prev_cb),
+                                  _p(prev_zb), B, n, c, m, _p(pos_t), rope_base, flags, _p(dout), _dt(dout), n // m,
+                                  _p(g.dca), _p(g.dza), _p(g.dcb), _p(g.dzb), _p(g.dprev_cb), _p(g.dprev_zb), _p(g.dba),
+                                  _p(g.dbb), _p(ws), ws.numel() * ws.element_size() if ws is not None else 0, _stream(ca))
+    _check("csa2_compress_bwd", st)
+    return g
+
+
+def csa2_attn_mass(q, kv, q_pos, lse, idx=None, n_visible=None, k_max: int = 0, kv_fmt: Optional[int] = None,
+                   rope_base: float = 10000.0, flags: int = ATTN_DEFAULT, weights: Optional[torch.Tensor] = None,
+                   acc: Optional[torch.Tensor] = None, want_weights: bool = False, ws: Optional[torch.Tensor] = None):
+    """Attention weight of the entries a forward call attended to, from its lse [B,Q,H]: the
+    sum over heads of each slot (weights [B,Q,k] f32, if wanted), added into acc [B,N] f32
+    (if given).  idx [B,Q,k] int32, or n_visible [B,Q] int64 <= k_max for the dense form.
+    Returns (weights, acc)."""
+    B, Q, H, c = q.shape
+    N = kv.shape[1]
+    dev = q.device
+    if (idx is None) == (n_visible is None):
+        raise ValueError("give idx or n_visible, not both")
+    k = idx.shape[-1] if idx is not None else k_max
+    if idx is not None:
+        _want("idx", idx, (B, Q, k), torch.int32, dev)
+    else:
+        _want("n_visible", n_visible, (B, Q), torch.int64, dev)
+    kv_dt = (FP4_E4M3x16 if kv_fmt is None else kv_fmt) if kv.dtype == torch.uint8 else _dt(kv)
+    _want("kv", kv, (B, N, fp4_row_bytes(c) if kv.dtype == torch.uint8 else c), kv.dtype, dev)
+    _want("lse", lse, (B, Q, H), torch.float32, dev)
+    _want("q_pos", q_pos, (B, Q), torch.int64, dev)
+    if acc is not None:
+        _want("acc", acc, (B, N), torch.float32, dev)
+    if want_weights or weights is not None:
+        weights = _given("weights", weights, (B, Q, k), torch.float32, dev)
+    if ws is None:
+        ws = _ws(_lib().csa2_attn_mass_workspace_bytes(ctx(dev.index), B, Q, H, k, N if acc is not None else 0), dev)
+    st = _lib().csa2_attn_mass(ctx(dev.index), _p(q), _dt(q), _p(kv), kv_dt, N, _p(idx), _p(n_visible), k, _p(q_pos),
+                               _p(lse), B, Q, H, c, rope_base, flags, _p(weights), _p(acc), _p(ws),
+                               ws.numel() * ws.element_size(), _stream(q))
+    _check("csa2_attn_mass", st)
+    return weights, acc
+
+
+def csa2_evict_select(acc, n_entries, keep: int, recent: int = 0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Entries [B, keep] int32 (ascending, -1 padded) that stay when rows of n_entries[b]
+    entries are cut to `keep`: the newest `recent`, and the best others by acc [B, ld] f32."""
+    B, ld = acc.shape
+    _want("acc", acc, (B, ld), torch.float32, acc.device)
+    _want("n_entries", n_entries, (B,), torch.int64, acc.device)
+    out = _given("out", out, (B, keep), torch.int32, acc.device)
+    st = _lib().csa2_evict_select(ctx(acc.device.index), _p(acc), B, ld, _p(n_entries), keep, recent, _p(out),
+                                  _stream(acc))
+    _check("csa2_evict_select", st)
+    return out
+
+
+def csa2_cache_gather(src, idx, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rows out[b, i] = src[b, idx[b, i]] of a cache [B, N, ..] for idx [B, keep] int32; rows
+    whose idx is -1 are left as they are in `out` (uninitialised when allocated here)."""
+    B, N = src.shape[:2]
+    keep = idx.shape[-1]
+    _want("idx", idx, (B, keep), torch.int32, src.device)
+    row_bytes = src.element_size()
+    for n in src.shape[2:]:
+        row_bytes *= n
+    out = _given("out", out, (B, keep, *src.shape[2:]), src.dtype, src.device)
+    st = _lib().csa2_cache_gather(ctx(src.device.index), _p(src), row_bytes, B, N, _p(idx), keep, _p(out), _stream(src))
+    _check("csa2_cache_gather", st)
+    return out

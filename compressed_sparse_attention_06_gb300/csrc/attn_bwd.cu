@@ -1,0 +1,736 @@
+// Backward pass of the shared-KV MQA (csa2_sparse_attn_bwd, csa2_dense_attn_bwd).
+//
+// With qn = RMS(q), q^ = RoPE_t(qn), k^_j = r_j x_j (r_j the row's RMS factor) and the
+// forward's lse, per query and head:
+//     p_j  = exp(q^.k^_j / sqrt(c) - lse)             (recomputed, nothing else is kept)
+//     do'  = RoPE_t(dout),  D = dout . out
+//     dS_j = p_j (do'.k^_j - D) / sqrt(c)
+//     dq^  = sum_j dS_j k^_j,   dq = rq (RoPE_-t dq^ - qn mean(qn . RoPE_-t dq^))
+//     row gradient: G_j = r_j sum over queries and heads of (dS_j q^ + p_j do'),
+//     dx_j = G_j - k^_j mean(k^_j . G_j)
+//     dsink = - sum over queries of exp(sink - lse) D
+// The row gradients are a scatter: every (query, slot) adds 512 values to its row.  They
+// are summed without atomics, in query order, so a call's results are the same bits every
+// time: a plan gives every (query, slot) its place in a list sorted by row and query (a
+// counting sort over groups of queries), the main kernels write each contribution there,
+// and one pass sums every row's stretch of the list, applies the row's norm and stores.
+//
+// Queries run in chunks of as many as the workspace holds; with more than one chunk the
+// rows' sums are carried in fp32 in the workspace.
+#include <algorithm>
+#include <atomic>
+#include <cstring>
+
+#include "attn_grad.cuh"
+
+namespace {
+
+constexpr int MAX_GROUPS = 152;          // query groups of the scatter plan
+constexpr int64_t MAX_COUNTERS = 1 << 24;
+constexpr int SCAN_ROWS = 1024;          // rows per block of the plan's scan
+
+size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// ---------------------------------------------------------------- scatter plan
+
+// rank[q][s] = how many (query, slot) pairs of the group before this one (in query order)
+// lie in the same row.  A block walks its group's queries in order: the barrier between
+// two queries orders their counter updates.  Slots of one query in the same row (the same
+// index twice) hold the same contribution, so their order does not matter.
+__global__ void __launch_bounds__(512) bwd_rank_kernel(SlotArgs a, int64_t bq0, int nb, int group_q, int n_slots,
+                                                       int64_t rows, uint32_t* cnt, int32_t* rank) {
+    const int g = blockIdx.x;
+    uint32_t* c = cnt + (int64_t)g * rows;
+    const int q1 = min(nb, (g + 1) * group_q);
+    for (int q = g * group_q; q < q1; ++q) {
+        for (int s = threadIdx.x; s < n_slots; s += blockDim.x) {
+            const int64_t row = slot_row(a, bq0 + q, s, true);
+            int32_t r = -1;
+            if (row >= 0) r = (int32_t)atomicAdd(&c[row], 1u);
+            rank[(int64_t)q * n_slots + s] = r;
+        }
+        __syncthreads();
+    }
+}
+
+// Block-wide exclusive scan of one value per thread; returns the prefix, total in *tot.
+__device__ __forceinline__ uint32_t block_excl_scan(uint32_t v, uint32_t* warp_tot, uint32_t* tot) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    uint32_t incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+    }
+    if (lane == 31) warp_tot[w] = incl;
+    __syncthreads();
+    if (w == 0) {
+        uint32_t t = lane < nw ? warp_tot[lane] : 0u, ti = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(0xffffffffu, ti, o);
+            if (lane >= o) ti += u;
+        }
+        warp_tot[lane] = ti - t;
+        if (lane == 31) *tot = ti;
+    }
+    __syncthreads();
+    return warp_tot[w] + incl - v;
+}
+
+// Counts -> places: base[g][row] (in place of cnt) = first place of group g's stretch of
+// the row, relative to the row's block of 1,024 rows; loc / tot: the row's own start
+// (relative) and length; blk[b] = the block's length (scanned by bwd_scan_kernel).
+__global__ void __launch_bounds__(SCAN_ROWS) bwd_place_kernel(uint32_t* cnt, int groups, int64_t rows, uint32_t* loc,
+                                                              uint32_t* tot, uint32_t* blk) {
+    __shared__ uint32_t wt[32], total;
+    const int64_t row = (int64_t)blockIdx.x * SCAN_ROWS + threadIdx.x;
+    uint32_t n = 0;
+    if (row < rows) {
+#pragma unroll 8
+        for (int g = 0; g < groups; ++g) n += cnt[(int64_t)g * rows + row];
+    }
+    const uint32_t start = block_excl_scan(n, wt, &total);
+    if (row < rows) {
+        uint32_t at = start;
+#pragma unroll 8
+        for (int g = 0; g < groups; ++g) {
+            const uint32_t here = cnt[(int64_t)g * rows + row];
+            cnt[(int64_t)g * rows + row] = at;
+            at += here;
+        }
+        loc[row] = start;
+        tot[row] = n;
+    }
+    if (threadIdx.x == 0) blk[blockIdx.x] = total;
+}
+
+__global__ void __launch_bounds__(1024) bwd_scan_kernel(uint32_t* blk, int64_t n) {
+    __shared__ uint32_t wt[32], total;
+    uint32_t carry = 0;
+    for (int64_t i0 = 0; i0 < n; i0 += 1024) {
+        const int64_t i = i0 + threadIdx.x;
+        const uint32_t v = i < n ? blk[i] : 0u;
+        const uint32_t p = block_excl_scan(v, wt, &total);
+        if (i < n) blk[i] = carry + p;
+        carry += total;
+        __syncthreads();
+    }
+}
+
+__device__ __forceinline__ int64_t pair_place(const BwdChunk& c, int q, int slot, int64_t row) {
+    const int32_t r = c.rank[(int64_t)q * c.n_slots + slot];
+    return (int64_t)c.blk[row >> 10] + c.base[(int64_t)(q / c.group_q) * c.rows + row] + r;
+}
+
+// ---------------------------------------------------------------- preparation
+
+// RMS factor of every row (cache rows, then window rows); a warp per row.
+__global__ void __launch_bounds__(256) bwd_rinv_kernel(const void* kv, int kv_dt, int64_t n_kv, const void* swa,
+                                                       int swa_dt, int64_t rows, unsigned flags, float* rinv) {
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= rows) return;
+    float r = 1.0f;
+    if (flags & CSA2_KVNORM) {
+        float v[16];
+        if (row < n_kv)
+            ag_load_row16(kv, kv_dt, row, lane, v);
+        else
+            ag_load_row16(swa, swa_dt, row - n_kv, lane, v);
+        r = ag_rms_factor(warp_sum(ag_sumsq16(v)));
+    }
+    if (lane == 0) rinv[row] = r;
+}
+
+// D = dout . out of every (query, head); a warp per head row.
+template <typename TO>
+__global__ void __launch_bounds__(256) bwd_dot_kernel(const TO* dout, const TO* out, int64_t n, float* D) {
+    const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (r >= n) return;
+    float a[16], b[16], s = 0.0f;
+    ag_load16<TO>(dout + r * AG_C + 16 * lane, a);
+    ag_load16<TO>(out + r * AG_C + 16 * lane, b);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s = fmaf(a[i], b[i], s);
+    s = warp_sum(s);
+    if (lane == 0) D[r] = s;
+}
+
+// dsink[h] = - sum over queries of exp(sink_h - lse) D, added in a fixed order (a block
+// per head; each thread's stretch, then a tree).
+__global__ void __launch_bounds__(256) bwd_sink_kernel(const float* sink, const float* lse, const float* D, int64_t n_bq,
+                                                       int H, float* dsink) {
+    __shared__ float red[8];
+    const int h = blockIdx.x;
+    const float zs = sink ? sink[h] : -INFINITY;
+    float s = 0.0f;
+    if (zs != -INFINITY) {
+        for (int64_t i = threadIdx.x; i < n_bq; i += 256) {
+            const float l = lse[i * H + h];
+            if (l != -INFINITY) s = fmaf(-expf(zs - l), D[i * H + h], s);
+        }
+    }
+    s = warp_sum(s);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float t = 0.0f;
+        for (int i = 0; i < 8; ++i) t += red[i];
+        dsink[h] = t;
+    }
+}
+
+// q^ and do' of every (query, head) of the chunk in fp32 (CUDA-core path); a warp per row.
+template <typename TQ, typename TO>
+__global__ void __launch_bounds__(256) bwd_prep_kernel(const TQ* q, const TO* dout, const int64_t* q_pos, int64_t bq0,
+                                                       int64_t n_rows, int H, RopeTable rope, unsigned flags, float* qh,
+                                                       float* dh) {
+    __shared__ float cs[8][32], sn[8][32];
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t r = (int64_t)blockIdx.x * 8 + w;
+    if (r >= n_rows) return;
+    rope_cos_sin(rope, q_pos[bq0 + r / H], lane, cs[w][lane], sn[w][lane]);
+    __syncwarp();
+    const int64_t src = (bq0 * H + r) * AG_C + 16 * lane, dst = r * AG_C + 16 * lane;
+    float v[16];
+    ag_load16<TQ>(q + src, v);
+    if (flags & CSA2_QNORM) {
+        const float f = ag_rms_factor(warp_sum(ag_sumsq16(v)));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] *= f;
+    }
+    if (flags & CSA2_ROPE) ag_rope16(v, lane, cs[w], sn[w], 1.0f);
+    ag_store16<float>(qh + dst, v);
+    if (!dout) return;
+    ag_load16<TO>(dout + src, v);
+    if (flags & CSA2_ROPE) ag_rope16(v, lane, cs[w], sn[w], 1.0f);
+    ag_store16<float>(dh + dst, v);
+}
+
+// ---------------------------------------------------------------- CUDA-core path (fp32)
+
+constexpr int SB_HG = 8;                 // heads per CTA of the query pass
+constexpr int SB_KC = 32;                // key rows per staged chunk
+
+// Query pass: p and dS of every slot (kept for the row pass) and dq; a CTA per (8 heads,
+// query), a warp per head, key rows staged 32 at a time in fp32.
+template <typename TQ>
+__global__ void __launch_bounds__(256, 2) bwd_simt_q_kernel(BwdChunk c, const float* qh, const float* dh, float2* pds,
+                                                            TQ* dq) {
+    extern __shared__ float smem[];
+    float* xs = smem;                                        // [32][512] normalised rows
+    int* ok = reinterpret_cast<int*>(xs + SB_KC * AG_C);     // [32]
+    float* cs = reinterpret_cast<float*>(ok + SB_KC);        // [32]
+    float* sn = cs + 32;
+    const int q = blockIdx.y, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.x * SB_HG + w;
+    const bool live = h < c.H;
+    const int64_t bq = c.bq0 + q;
+    if (threadIdx.x < 32) rope_cos_sin(c.rope, c.slots.q_pos[bq], lane, cs[lane], sn[lane]);
+    float qv[16], dv[16], acc[16];
+    const int64_t hr = (int64_t)q * c.H + h;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) qv[i] = dv[i] = acc[i] = 0.0f;
+    float lse = -INFINITY, D = 0.0f;
+    if (live) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            qv[i] = qh[hr * AG_C + lane + 32 * i];
+            dv[i] = dh[hr * AG_C + lane + 32 * i];
+        }
+        lse = c.lse[bq * c.H + h];
+        D = c.D[bq * c.H + h];
+    }
+    const float isc = 1.0f / sqrtf((float)AG_C);
+    for (int s0 = 0; s0 < c.n_slots; s0 += SB_KC) {
+        __syncthreads();
+        for (int r = w; r < SB_KC; r += 8) {
+            const int64_t row = s0 + r < c.n_slots ? slot_row(c.slots, bq, s0 + r, false) : -1;
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+            if (row >= 0) {
+                if (row < c.slots.n_kv)
+                    ag_load_row16(c.kv, c.kv_dt, row, lane, v);
+                else
+                    ag_load_row16(c.swa, c.swa_dt, row - c.slots.n_kv, lane, v);
+                const float f = c.rinv[row];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] *= f;
+            }
+            ag_store16<float>(xs + r * AG_C + 16 * lane, v);
+            if (lane == 0) ok[r] = row >= 0;
+        }
+        __syncthreads();
+        float z = 0.0f, dp = 0.0f;
+        for (int j = 0; j < SB_KC; ++j) {
+            float a = 0.0f, b = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float x = xs[j * AG_C + lane + 32 * i];
+                a = fmaf(qv[i], x, a);
+                b = fmaf(dv[i], x, b);
+            }
+            a = warp_sum(a);
+            b = warp_sum(b);
+            if (lane == j) {
+                z = a * isc;
+                dp = b;
+            }
+        }
+        float p = 0.0f, ds = 0.0f;
+        if (ok[lane] && lse != -INFINITY) {
+            p = expf(z - lse);
+            ds = p * (dp - D) * isc;
+        }
+        if (live && s0 + lane < c.n_slots) pds[hr * c.n_slots + s0 + lane] = make_float2(p, ds);
+        for (int j = 0; j < SB_KC; ++j) {
+            const float d = __shfl_sync(0xffffffffu, ds, j);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[i] = fmaf(d, xs[j * AG_C + lane + 32 * i], acc[i]);
+        }
+    }
+    if (!live) return;
+    // dq: back through RoPE and the query's RMSNorm (on q^ and dq^: a rotation keeps their product)
+    const int64_t o = (bq * c.H + h) * AG_C;
+    const TQ* qraw = reinterpret_cast<const TQ*>(c.q) + o;
+    if (c.flags & CSA2_QNORM) {
+        float ss = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float x = to_f32<TQ>(qraw[lane + 32 * i]);
+            ss = fmaf(x, x, ss);
+            dot = fmaf(qv[i], acc[i], dot);
+        }
+        const float f = ag_rms_factor(warp_sum(ss));
+        dot = warp_sum(dot) / (float)AG_C;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[i] = f * (acc[i] - qv[i] * dot);
+    }
+    if (c.flags & CSA2_ROPE) rope_lanes(acc, lane, cs, sn, -1.0f);
+    // a query that attends to nothing has no gradient, whatever its values
+    if (lse == -INFINITY)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) dq[o + lane + 32 * i] = from_f32<TQ>(acc[i]);
+}
+
+// Row pass: the contribution r_j sum_h (dS_hj q^_h + p_hj do'_h) of every (query, slot);
+// a CTA per (32 slots, query), two channels a thread.
+__global__ void __launch_bounds__(256) bwd_simt_row_kernel(BwdChunk c, const float* qh, const float* dh,
+                                                           const float2* pds) {
+    __shared__ float2 sp[32][33];
+    const int q = blockIdx.y, s0 = blockIdx.x * 32, t = threadIdx.x;
+    const int64_t bq = c.bq0 + q;
+    float acc0[32], acc1[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) acc0[j] = acc1[j] = 0.0f;
+    for (int h0 = 0; h0 < c.H; h0 += 32) {
+        __syncthreads();
+        for (int i = t; i < 32 * 32; i += 256) {
+            const int h = h0 + (i >> 5), s = s0 + (i & 31);
+            sp[i >> 5][i & 31] = h < c.H && s < c.n_slots ? pds[((int64_t)q * c.H + h) * c.n_slots + s] : make_float2(0.0f, 0.0f);
+        }
+        __syncthreads();
+        const int hn = min(32, c.H - h0);
+        for (int h = 0; h < hn; ++h) {
+            const int64_t o = ((int64_t)q * c.H + h0 + h) * AG_C + 2 * t;
+            const float2 qv = *reinterpret_cast<const float2*>(qh + o), dv = *reinterpret_cast<const float2*>(dh + o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const float2 pd = sp[h][j];
+                acc0[j] = fmaf(pd.y, qv.x, fmaf(pd.x, dv.x, acc0[j]));
+                acc1[j] = fmaf(pd.y, qv.y, fmaf(pd.x, dv.y, acc1[j]));
+            }
+        }
+    }
+    float2* part = reinterpret_cast<float2*>(c.part);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const int s = s0 + j;
+        if (s >= c.n_slots) continue;
+        const int64_t row = slot_row(c.slots, bq, s, false);
+        if (row < 0) continue;
+        const float f = c.rinv[row];
+        part[pair_place(c, q, s, row) * (AG_C / 2) + t] = make_float2(acc0[j] * f, acc1[j] * f);
+    }
+}
+
+// ---------------------------------------------------------------- row sums
+
+template <typename TP>
+__device__ __forceinline__ float4 part4(const TP* p);
+template <>
+__device__ __forceinline__ float4 part4<float>(const float* p) {
+    return __ldcs(reinterpret_cast<const float4*>(p));
+}
+template <>
+__device__ __forceinline__ float4 part4<__nv_bfloat16>(const __nv_bfloat16* p) {
+    const uint2 u = __ldcs(reinterpret_cast<const uint2*>(p));
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ void store4(void* base, int dt, int64_t off, float4 v) {
+    if (dt == CSA2_F32) {
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + off) = v;
+    } else {
+        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(base) + off) =
+            make_uint2(ag_pack_bf16x2(v.x, v.y), ag_pack_bf16x2(v.z, v.w));
+    }
+}
+
+__device__ __forceinline__ float4 load4_any(const void* base, int dt, int64_t off) {
+    if (dt == CSA2_F32) return *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + off);
+    const uint2 u = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(base) + off);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xFFFF0000u));
+}
+
+struct RowSumArgs {
+    const void* part;
+    int passes;               // entries per place (head passes of the tensor-core path)
+    const uint32_t *loc, *tot, *blk;
+    int64_t rows, n_kv;
+    const void *kv, *swa;
+    int kv_dt, swa_dt;
+    const float* rinv;
+    unsigned flags;
+    float* acc;               // [rows, 512] sums carried between chunks, or NULL (one chunk)
+    int first, last;
+    void *dkv, *dswa;         // NULL: not wanted
+};
+
+// Sum of a row's contributions in list order, then (last chunk) the row's norm; a CTA of
+// 128 threads per row, four channels a thread.
+template <typename TP>
+__global__ void __launch_bounds__(128) bwd_rowsum_kernel(RowSumArgs a) {
+    __shared__ float red[4];
+    const int64_t row = blockIdx.x;
+    const int t = threadIdx.x, ch = 4 * t;
+    void* dst = row < a.n_kv ? a.dkv : a.dswa;
+    if (!dst) return;
+    float4 g = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (a.acc && !a.first) g = *reinterpret_cast<const float4*>(a.acc + row * AG_C + ch);
+    const int64_t n = (int64_t)a.tot[row] * a.passes;
+    if (n > 0) {
+        const TP* p = reinterpret_cast<const TP*>(a.part) +
+                      ((int64_t)a.blk[row >> 10] + a.loc[row]) * a.passes * AG_C + ch;
+        int64_t i = 0;
+        for (; i + 8 <= n; i += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = part4<TP>(p + (i + j) * AG_C);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                g.x += v[j].x;
+                g.y += v[j].y;
+                g.z += v[j].z;
+                g.w += v[j].w;
+            }
+        }
+        for (; i < n; ++i) {
+            const float4 v = part4<TP>(p + i * AG_C);
+            g.x += v.x;
+            g.y += v.y;
+            g.z += v.z;
+            g.w += v.w;
+        }
+    }
+    if (!a.last) {
+        *reinterpret_cast<float4*>(a.acc + row * AG_C + ch) = g;
+        return;
+    }
+    const int64_t off = (row < a.n_kv ? row : row - a.n_kv) * AG_C + ch;
+    const int dt = row < a.n_kv ? a.kv_dt : a.swa_dt;
+    if ((a.flags & CSA2_KVNORM) && (n > 0 || a.acc)) {
+        const float f = a.rinv[row];
+        const float4 x = load4_any(row < a.n_kv ? a.kv : a.swa, dt, off);
+        const float4 k = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+        float d = warp_sum(fmaf(k.x, g.x, fmaf(k.y, g.y, fmaf(k.z, g.z, k.w * g.w))));
+        if ((t & 31) == 0) red[t >> 5] = d;
+        __syncthreads();
+        d = (red[0] + red[1] + red[2] + red[3]) / (float)AG_C;
+        g.x = fmaf(-k.x, d, g.x);
+        g.y = fmaf(-k.y, d, g.y);
+        g.z = fmaf(-k.z, d, g.z);
+        g.w = fmaf(-k.w, d, g.w);
+    }
+    store4(dst, dt, off, g);
+}
+
+constexpr size_t SB_SMEM = (size_t)SB_KC * AG_C * 4 + SB_KC * 4 + 64 * 4;
+
+// Raises a kernel's dynamic shared memory once per device (bit `device` of `done`).
+template <typename K>
+csa2_status raise_smem(K kern, size_t bytes, int device, std::atomic<uint64_t>& done) {
+    const uint64_t bit = 1ull << (device & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return CSA2_OK;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
+        return CSA2_ERR_CUDA;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return CSA2_OK;
+}
+
+// ---------------------------------------------------------------- workspace
+
+struct BwdLayout {
+    size_t D, rinv, cnt, loc, tot, blk, rank, qh, dh, pds, part, acc, total;
+    int groups, group_q;
+    int64_t rows;
+};
+
+BwdLayout bwd_layout(int64_t n_bq, int H, int n_slots, int64_t rows, int64_t nb, bool chunked) {
+    BwdLayout L;
+    L.rows = rows;
+    const int64_t g = std::min<int64_t>({nb, MAX_GROUPS, std::max<int64_t>(1, MAX_COUNTERS / std::max<int64_t>(1, rows))});
+    L.group_q = (int)((nb + g - 1) / g);
+    L.groups = (int)((nb + L.group_q - 1) / L.group_q);
+    size_t at = 0;
+    auto take = [&at](size_t bytes) {
+        const size_t o = at;
+        at = align_up(at + bytes, 256);
+        return o;
+    };
+    L.D = take((size_t)n_bq * H * 4);
+    L.rinv = take((size_t)rows * 4);
+    L.cnt = take((size_t)L.groups * rows * 4);
+    L.loc = take((size_t)rows * 4);
+    L.tot = take((size_t)rows * 4);
+    L.blk = take((size_t)((rows + SCAN_ROWS - 1) / SCAN_ROWS) * 4);
+    L.rank = take((size_t)nb * n_slots * 4);
+    L.qh = take((size_t)nb * H * AG_C * 4);
+    L.dh = take((size_t)nb * H * AG_C * 4);
+    L.pds = take((size_t)nb * H * n_slots * 8);
+    L.part = take((size_t)nb * n_slots * AG_C * 4);
+    L.acc = take(chunked ? (size_t)rows * AG_C * 4 : 0);
+    L.total = at;
+    return L;
+}
+
+constexpr size_t WS_TARGET = (size_t)16 << 30;   // the recommended workspace stays below this
+
+int64_t chunk_for(int64_t n_bq, int H, int n_slots, int64_t rows, size_t bytes) {
+    auto fits = [&](int64_t nb) { return bwd_layout(n_bq, H, n_slots, rows, nb, nb < n_bq).total <= bytes; };
+    // at most 2^31 - 1 places, and grid.y slices, in a chunk
+    int64_t hi = std::min<int64_t>(n_bq, n_slots > 0 ? 0x7FFFFFFFll / n_slots : n_bq);
+    hi = std::min<int64_t>(hi, 65535);
+    if (fits(hi)) return hi;
+    int64_t lo = 0;                              // the largest nb < hi that fits (0: none)
+    while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) / 2;
+        (fits(mid) ? lo : hi) = mid;
+    }
+    return lo;
+}
+
+struct BwdCall {
+    const void *q, *kv, *swa, *out, *dout;
+    csa2_dtype q_dt, kv_dt, swa_dt, out_dt;
+    int64_t N, swa_cap, swa_pos0;
+    const int32_t* idx;
+    const int64_t *nv, *q_pos;
+    int k, window, B, Q, H;
+    const float *sink, *lse;
+    float rope_base;
+    unsigned flags;
+    void *dq, *dkv, *dswa;
+    float* dsink;
+};
+
+csa2_status zero_bytes(void* p, size_t bytes, cudaStream_t s) {
+    if (!p || bytes == 0) return CSA2_OK;
+    return cudaMemsetAsync(p, 0, bytes, s) == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
+}
+
+size_t dt_bytes(csa2_dtype d) { return d == CSA2_F32 ? 4 : 2; }
+
+template <typename TQ, typename TO>
+csa2_status simt_chunk(const csa2_ctx* ctx, const BwdCall& a, const BwdChunk& c, float* qh, float* dh, float2* pds,
+                       cudaStream_t s) {
+    static std::atomic<uint64_t> done{0};
+    const csa2_status r = raise_smem(bwd_simt_q_kernel<TQ>, SB_SMEM, ctx->device, done);
+    if (r != CSA2_OK) return r;
+    const int64_t n_rows = (int64_t)c.nb * a.H;
+    bwd_prep_kernel<TQ, TO><<<(unsigned)((n_rows + 7) / 8), 256, 0, s>>>(
+        reinterpret_cast<const TQ*>(a.q), reinterpret_cast<const TO*>(a.dout), a.q_pos, c.bq0, n_rows, a.H, c.rope,
+        a.flags, qh, dh);
+    bwd_simt_q_kernel<TQ><<<dim3((unsigned)((a.H + SB_HG - 1) / SB_HG), (unsigned)c.nb), 256, SB_SMEM, s>>>(
+        c, qh, dh, pds, reinterpret_cast<TQ*>(a.dq));
+    if (c.n_slots > 0)
+        bwd_simt_row_kernel<<<dim3((unsigned)((c.n_slots + 31) / 32), (unsigned)c.nb), 256, 0, s>>>(c, qh, dh, pds);
+    return csa2_launch_status();
+}
+
+csa2_status bwd_run(csa2_ctx* ctx, const BwdCall& a, void* ws, size_t ws_bytes, cudaStream_t s) {
+    const int64_t n_bq = (int64_t)a.B * a.Q;
+    const int n_slots = a.k + a.window;
+    const int64_t n_kv = a.k > 0 ? (int64_t)a.B * a.N : 0, n_sw = a.window > 0 ? (int64_t)a.B * a.swa_cap : 0;
+    const int64_t rows = n_kv + n_sw;
+    const int64_t nb_max = chunk_for(n_bq, a.H, n_slots, rows, ws_bytes);
+    if (nb_max < 1) return CSA2_ERR_INVALID_ARG;
+    const BwdLayout L = bwd_layout(n_bq, a.H, n_slots, rows, nb_max, nb_max < n_bq);
+    uint8_t* base = reinterpret_cast<uint8_t*>(ws);
+    float* D = reinterpret_cast<float*>(base + L.D);
+    float* rinv = reinterpret_cast<float*>(base + L.rinv);
+    const int64_t heads = n_bq * a.H;
+    if (a.out_dt == CSA2_F32)
+        bwd_dot_kernel<float><<<(unsigned)((heads + 7) / 8), 256, 0, s>>>(reinterpret_cast<const float*>(a.dout),
+                                                                         reinterpret_cast<const float*>(a.out), heads, D);
+    else
+        bwd_dot_kernel<__nv_bfloat16><<<(unsigned)((heads + 7) / 8), 256, 0, s>>>(
+            reinterpret_cast<const __nv_bfloat16*>(a.dout), reinterpret_cast<const __nv_bfloat16*>(a.out), heads, D);
+    if (a.dsink) bwd_sink_kernel<<<(unsigned)a.H, 256, 0, s>>>(a.sink, a.lse, D, n_bq, a.H, a.dsink);
+    if (rows > 0)
+        bwd_rinv_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a.kv, a.kv_dt, n_kv, a.swa, a.swa_dt, rows, a.flags,
+                                                                  rinv);
+    BwdChunk c;
+    c.slots = {a.idx, a.nv, a.q_pos, a.N, a.swa_cap, a.swa_pos0, a.k, a.window, a.Q, n_kv, ctx->status};
+    c.q = a.q;
+    c.q_dt = a.q_dt;
+    c.kv = a.kv;
+    c.kv_dt = a.kv_dt;
+    c.swa = a.swa;
+    c.swa_dt = a.swa_dt;
+    c.lse = a.lse;
+    c.D = D;
+    c.rinv = rinv;
+    c.H = a.H;
+    c.n_slots = n_slots;
+    c.flags = a.flags;
+    c.rope = make_rope_table(a.rope_base);
+    uint32_t* cnt = reinterpret_cast<uint32_t*>(base + L.cnt);
+    uint32_t* loc = reinterpret_cast<uint32_t*>(base + L.loc);
+    uint32_t* tot = reinterpret_cast<uint32_t*>(base + L.tot);
+    uint32_t* blk = reinterpret_cast<uint32_t*>(base + L.blk);
+    int32_t* rank = reinterpret_cast<int32_t*>(base + L.rank);
+    c.rank = rank;
+    c.base = cnt;
+    c.blk = blk;
+    c.rows = rows;
+    c.group_q = L.group_q;
+    c.part = base + L.part;
+    c.dq = a.dq;
+    const int64_t n_blk = (rows + SCAN_ROWS - 1) / SCAN_ROWS;
+    for (int64_t bq0 = 0; bq0 < n_bq; bq0 += nb_max) {
+        c.bq0 = bq0;
+        c.nb = (int)std::min<int64_t>(nb_max, n_bq - bq0);
+        if (rows > 0) {
+            const csa2_status z = zero_bytes(cnt, (size_t)L.groups * rows * 4, s);
+            if (z != CSA2_OK) return z;
+            bwd_rank_kernel<<<(unsigned)L.groups, 512, 0, s>>>(c.slots, bq0, c.nb, L.group_q, n_slots, rows, cnt, rank);
+            bwd_place_kernel<<<(unsigned)n_blk, SCAN_ROWS, 0, s>>>(cnt, L.groups, rows, loc, tot, blk);
+            bwd_scan_kernel<<<1, 1024, 0, s>>>(blk, n_blk);
+        }
+        float* qh = reinterpret_cast<float*>(base + L.qh);
+        float* dh = reinterpret_cast<float*>(base + L.dh);
+        float2* pds = reinterpret_cast<float2*>(base + L.pds);
+        csa2_status r;
+        if (a.q_dt == CSA2_F32)
+            r = a.out_dt == CSA2_F32 ? simt_chunk<float, float>(ctx, a, c, qh, dh, pds, s)
+                                     : simt_chunk<float, __nv_bfloat16>(ctx, a, c, qh, dh, pds, s);
+        else
+            r = a.out_dt == CSA2_F32 ? simt_chunk<__nv_bfloat16, float>(ctx, a, c, qh, dh, pds, s)
+                                     : simt_chunk<__nv_bfloat16, __nv_bfloat16>(ctx, a, c, qh, dh, pds, s);
+        if (r != CSA2_OK) return r;
+        if (rows > 0 && (a.dkv || a.dswa)) {
+            RowSumArgs ra;
+            ra.part = c.part;
+            ra.passes = 1;
+            ra.loc = loc;
+            ra.tot = tot;
+            ra.blk = blk;
+            ra.rows = rows;
+            ra.n_kv = n_kv;
+            ra.kv = a.kv;
+            ra.swa = a.swa;
+            ra.kv_dt = a.kv_dt;
+            ra.swa_dt = a.swa_dt;
+            ra.rinv = rinv;
+            ra.flags = a.flags;
+            ra.acc = nb_max < n_bq ? reinterpret_cast<float*>(base + L.acc) : nullptr;
+            ra.first = bq0 == 0;
+            ra.last = bq0 + c.nb == n_bq;
+            ra.dkv = a.dkv;
+            ra.dswa = a.dswa;
+            bwd_rowsum_kernel<float><<<(unsigned)rows, 128, 0, s>>>(ra);
+        }
+        if (csa2_launch_status() != CSA2_OK) return CSA2_ERR_CUDA;
+    }
+    return CSA2_OK;
+}
+
+csa2_status bwd_impl(csa2_ctx* ctx, const BwdCall& a, int c, void* ws, size_t ws_bytes, void* stream) {
+    if (!ctx || a.B < 0 || a.Q < 0 || a.N < 0 || a.k < 0 || a.window < 0 || a.window > 1024) return CSA2_ERR_INVALID_ARG;
+    if (a.H < 1 || a.H > 128) return CSA2_ERR_INVALID_ARG;
+    if (c != AG_C) return CSA2_ERR_UNSUPPORTED;
+    if (a.flags & ~CSA2_ATTN_DEFAULT) return CSA2_ERR_INVALID_ARG;
+    for (csa2_dtype d : {a.q_dt, a.kv_dt, a.swa_dt, a.out_dt})
+        if (d != CSA2_F32 && d != CSA2_BF16) return CSA2_ERR_UNSUPPORTED;
+    const int64_t n_bq = (int64_t)a.B * a.Q;
+    if (n_bq > 65535) return CSA2_ERR_UNSUPPORTED;
+    if (a.window > 0 && (!a.swa || a.swa_cap < a.window)) return CSA2_ERR_INVALID_ARG;
+    if (a.swa_cap < 0) return CSA2_ERR_INVALID_ARG;
+    const int64_t rows = (int64_t)a.B * (a.N + a.swa_cap);
+    if (rows > 0x7FFFFFFF) return CSA2_ERR_UNSUPPORTED;
+    if (!aligned(a.q, 16) || !aligned(a.kv, 16) || !aligned(a.swa, 16) || !aligned(a.out, 16) || !aligned(a.dout, 16) ||
+        !aligned(a.dq, 16) || !aligned(a.dkv, 16) || !aligned(a.dswa, 16) || !aligned(ws, 16) || !aligned(a.lse, 4) ||
+        !aligned(a.dsink, 4) || !aligned(a.q_pos, 8))
+        return CSA2_ERR_INVALID_ARG;
+    if (a.B == 0) return CSA2_OK;
+    if (a.Q > 0 && (!a.q || !a.q_pos || !a.out || !a.dout || !a.lse || !a.dq || !ws)) return CSA2_ERR_INVALID_ARG;
+    if (a.Q > 0 && a.k > 0 && ((!a.idx && !a.nv) || !a.kv)) return CSA2_ERR_INVALID_ARG;
+    DeviceGuard dev(ctx);
+    if (!dev.ok) return CSA2_ERR_CUDA;
+    cudaStream_t s = as_stream(stream);
+    // rows that no call below visits have no gradient
+    csa2_status r = CSA2_OK;
+    if (a.k == 0 || a.Q == 0) r = zero_bytes(a.dkv, (size_t)a.B * a.N * AG_C * dt_bytes(a.kv_dt), s);
+    if (r == CSA2_OK && (a.window == 0 || a.Q == 0))
+        r = zero_bytes(a.dswa, (size_t)a.B * a.swa_cap * AG_C * dt_bytes(a.swa_dt), s);
+    if (r == CSA2_OK && a.Q == 0) r = zero_bytes(a.dsink, (size_t)a.H * 4, s);
+    if (r != CSA2_OK || a.Q == 0) return r;
+    return bwd_run(ctx, a, ws, ws_bytes, s);
+}
+
+}  // namespace
+
+extern "C" size_t csa2_attn_bwd_workspace_bytes(csa2_ctx* ctx, csa2_dtype q_dt, csa2_dtype kv_dt, csa2_dtype swa_dt,
+                                                csa2_dtype out_dt, int B, int Q, int H, int k, int window, int64_t N,
+                                                int64_t swa_cap, unsigned flags) {
+    if (!ctx || B <= 0 || Q <= 0 || H < 1 || H > 128 || k < 0 || window < 0 || N < 0 || swa_cap < 0) return 0;
+    (void)q_dt, (void)kv_dt, (void)swa_dt, (void)out_dt, (void)flags;
+    const int64_t n_bq = (int64_t)B * Q;
+    const int64_t rows = (k > 0 ? (int64_t)B * N : 0) + (window > 0 ? (int64_t)B * swa_cap : 0);
+    const int64_t nb = std::max<int64_t>(1, chunk_for(n_bq, H, k + window, rows, WS_TARGET));
+    return bwd_layout(n_bq, H, k + window, rows, nb, nb < n_bq).total;
+}
+
+extern "C" csa2_status csa2_sparse_attn_bwd(csa2_ctx* ctx, const void* q, csa2_dtype q_dt, const void* kv,
+                                            csa2_dtype kv_dt, int64_t N, const int32_t* idx, int k, const void* swa,
+                                            csa2_dtype swa_dt, int64_t swa_cap, int64_t swa_pos0, int window,
+                                            const int64_t* q_pos, const float* sink, const void* out, const void* dout,
+                                            csa2_dtype out_dt, const float* lse, int B, int Q, int H, int c,
+                                            float rope_base, unsigned flags, void* dq, void* dkv, void* dswa,
+                                            float* dsink, void* ws, size_t ws_bytes, void* stream) {
+    if (k > 2048) return CSA2_ERR_INVALID_ARG;
+    const BwdCall a = {q, kv, swa, out, dout, q_dt, kv_dt, swa_dt, out_dt, N, swa_cap, swa_pos0, idx, nullptr, q_pos, k,
+                       window, B, Q, H, sink, lse, rope_base, flags, dq, dkv, dswa, dsink};
+    return bwd_impl(ctx, a, c, ws, ws_bytes, stream);
+}
+
+extern "C" csa2_status csa2_dense_attn_bwd(csa2_ctx* ctx, const void* q, csa2_dtype q_dt, const void* kv,
+                                           csa2_dtype kv_dt, int64_t N, const int64_t* n_visible, int k_max,
+                                           const void* swa, csa2_dtype swa_dt, int64_t swa_cap, int64_t swa_pos0,
+                                           int window, const int64_t* q_pos, const float* sink, const void* out,
+                                           const void* dout, csa2_dtype out_dt, const float* lse, int B, int Q, int H,
+                                           int c, float rope_base, unsigned flags, void* dq, void* dkv, void* dswa,
+                                           float* dsink, void* ws, size_t ws_bytes, void* stream) {
+    if (k_max < 0 || k_max > (1 << 22) || (k_max > 0 && !n_visible)) return CSA2_ERR_INVALID_ARG;
+    const BwdCall a = {q, kv, swa, out, dout, q_dt, kv_dt, swa_dt, out_dt, N, swa_cap, swa_pos0, nullptr, n_visible,
+                       q_pos, k_max, window, B, Q, H, sink, lse, rope_base, flags, dq, dkv, dswa, dsink};
+    return bwd_impl(ctx, a, c, ws, ws_bytes, stream);
+}

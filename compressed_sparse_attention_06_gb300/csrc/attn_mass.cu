@@ -1,0 +1,207 @@
+// Accumulated attention weight of the cache entries (csa2_attn_mass), from the forward's lse:
+//     w[b,q,j] = sum over heads of exp(q^_h . k^_j / sqrt(c) - lse_h)
+//     acc[b, entry of slot j] += w[b,q,j]
+//
+// The sums into acc do not depend on the order the queries finish in.  With one query per
+// sequence an entry gets one addend (the same index twice gives equal addends), added
+// straight to acc.  With more, the addends of a call meet as 64-bit integers in units of
+// 2^-39 in the workspace (integer sums are the same in any order; an addend is at most H
+// and B*Q*H at most 2^24, so the sum stays below 2^63; the rounding of an addend, 2^-40,
+// is far below fp32's of the weights), and a last pass adds them to acc.
+#include <algorithm>
+#include <atomic>
+
+#include "attn_grad.cuh"
+
+namespace {
+
+constexpr int MS_KC = 32;
+constexpr float FIX_ONE = 549755813888.0f;          // 2^39
+constexpr float FIX_MAX = 256.0f;
+
+size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// One addend of an entry.  A weight that no softmax gives (an lse that is not the
+// forward's, NaN) is added as it is, so that acc shows it.
+__device__ __forceinline__ void add_mass(float* acc, unsigned long long* fix, int64_t at, float w) {
+    if (fix && w >= 0.0f && w <= FIX_MAX) {
+        if (w > 0.0f) atomicAdd(fix + at, (unsigned long long)__float2ull_rn(w * FIX_ONE));
+    } else {
+        atomicAdd(acc + at, w);
+    }
+}
+
+__global__ void __launch_bounds__(256) mass_finish_kernel(const unsigned long long* fix, float* acc, int64_t n) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    const unsigned long long v = fix[i];
+    if (v) acc[i] += __ull2float_rn(v) * (1.0f / FIX_ONE);
+}
+
+// q^ of every (query, head) in fp32; a warp per head row.
+template <typename TQ>
+__global__ void __launch_bounds__(256) mass_prep_kernel(const TQ* q, const int64_t* q_pos, int64_t n_rows, int H,
+                                                        RopeTable rope, unsigned flags, float* qh) {
+    __shared__ float cs[8][32], sn[8][32];
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t r = (int64_t)blockIdx.x * 8 + w;
+    if (r >= n_rows) return;
+    rope_cos_sin(rope, q_pos[r / H], lane, cs[w][lane], sn[w][lane]);
+    __syncwarp();
+    float v[16];
+    ag_load16<TQ>(q + r * AG_C + 16 * lane, v);
+    if (flags & CSA2_QNORM) {
+        const float f = ag_rms_factor(warp_sum(ag_sumsq16(v)));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] *= f;
+    }
+    if (flags & CSA2_ROPE) ag_rope16(v, lane, cs[w], sn[w], 1.0f);
+    ag_store16<float>(qh + r * AG_C + 16 * lane, v);
+}
+
+struct MassArgs {
+    SlotArgs slots;
+    const void* kv;
+    int kv_dt;
+    const float *qh, *lse;
+    int H;
+    unsigned flags;
+    float *weights, *acc;
+    unsigned long long* fix;
+};
+
+// CUDA-core path (fp32): a CTA per (32 slots, query), rows staged in fp32, a warp per head
+// in turn.
+__global__ void __launch_bounds__(256, 2) mass_simt_kernel(MassArgs a) {
+    extern __shared__ float smem[];
+    float* xs = smem;                                         // [32][512]
+    float* ws = xs + MS_KC * AG_C;                            // [8][32]
+    int64_t* rid = reinterpret_cast<int64_t*>(ws + 8 * 32);   // [32]
+    const int64_t bq = blockIdx.y;
+    const int s0 = blockIdx.x * MS_KC, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int r = w; r < MS_KC; r += 8) {
+        const int64_t row = s0 + r < a.slots.k ? slot_row(a.slots, bq, s0 + r, true) : -1;
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+        if (row >= 0) {
+            ag_load_row16(a.kv, a.kv_dt, row, lane, v);
+            if (a.flags & CSA2_KVNORM) {
+                const float f = ag_rms_factor(warp_sum(ag_sumsq16(v)));
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] *= f;
+            }
+        }
+        ag_store16<float>(xs + r * AG_C + 16 * lane, v);
+        if (lane == 0) rid[r] = row;
+    }
+    __syncthreads();
+    const float isc = 1.0f / sqrtf((float)AG_C);
+    float sum = 0.0f;
+    for (int h = w; h < a.H; h += 8) {
+        const float* qr = a.qh + (bq * a.H + h) * AG_C;
+        float qv[16], z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) qv[i] = qr[lane + 32 * i];
+        for (int j = 0; j < MS_KC; ++j) {
+            float d = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) d = fmaf(qv[i], xs[j * AG_C + lane + 32 * i], d);
+            d = warp_sum(d);
+            if (lane == j) z = d * isc;
+        }
+        const float lse = a.lse[bq * a.H + h];
+        if (lse != -INFINITY) sum += expf(z - lse);
+    }
+    ws[w * 32 + lane] = sum;
+    __syncthreads();
+    if (w == 0 && s0 + lane < a.slots.k) {
+        float t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t += ws[i * 32 + lane];
+        const int64_t row = rid[lane];
+        if (row < 0) t = 0.0f;
+        if (a.weights) a.weights[bq * a.slots.k + s0 + lane] = t;
+        if (a.acc && row >= 0) add_mass(a.acc, a.fix, row, t);
+    }
+}
+
+constexpr size_t MS_SMEM = (size_t)MS_KC * AG_C * 4 + 8 * 32 * 4 + MS_KC * 8;
+
+struct MassLayout {
+    size_t qh, fix, total;
+};
+
+MassLayout mass_layout(int B, int Q, int H, int64_t N, bool want_acc) {
+    MassLayout L;
+    L.qh = 0;
+    L.fix = align_up((size_t)B * Q * H * AG_C * 4, 256);
+    L.total = L.fix + (want_acc && Q > 1 ? (size_t)B * N * 8 : 0);
+    return L;
+}
+
+}  // namespace
+
+extern "C" size_t csa2_attn_mass_workspace_bytes(csa2_ctx* ctx, int B, int Q, int H, int k, int64_t N) {
+    if (!ctx || B <= 0 || Q <= 0 || H < 1 || H > 128 || k < 0 || N < 0) return 0;
+    return mass_layout(B, Q, H, N, true).total;
+}
+
+extern "C" csa2_status csa2_attn_mass(csa2_ctx* ctx, const void* q, csa2_dtype q_dt, const void* kv, csa2_dtype kv_dt,
+                                      int64_t N, const int32_t* idx, const int64_t* n_visible, int k,
+                                      const int64_t* q_pos, const float* lse, int B, int Q, int H, int c,
+                                      float rope_base, unsigned flags, float* weights, float* acc, void* ws,
+                                      size_t ws_bytes, void* stream) {
+    if (!ctx || B < 0 || Q < 0 || N < 0 || k < 0 || k > (1 << 22) || (idx && k > 2048)) return CSA2_ERR_INVALID_ARG;
+    if (H < 1 || H > 128) return CSA2_ERR_INVALID_ARG;
+    if (c != AG_C) return CSA2_ERR_UNSUPPORTED;
+    if (flags & ~CSA2_ATTN_DEFAULT) return CSA2_ERR_INVALID_ARG;
+    if (q_dt != CSA2_F32 && q_dt != CSA2_BF16) return CSA2_ERR_UNSUPPORTED;
+    if (kv_dt != CSA2_F32 && kv_dt != CSA2_BF16 && kv_dt != CSA2_FP4_E4M3x16) return CSA2_ERR_UNSUPPORTED;
+    if ((int64_t)B * Q > 65535) return CSA2_ERR_UNSUPPORTED;
+    if (!weights && !acc) return CSA2_ERR_INVALID_ARG;
+    if (B == 0 || Q == 0 || k == 0) return CSA2_OK;
+    if (!q || !kv || !q_pos || !lse || (!idx == !n_visible)) return CSA2_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(ws, 16) || !aligned(lse, 4) || !aligned(q_pos, 8) ||
+        !aligned(idx, 4) || !aligned(n_visible, 8) || !aligned(weights, 4) || !aligned(acc, 4))
+        return CSA2_ERR_INVALID_ARG;
+    const MassLayout L = mass_layout(B, Q, H, N, acc != nullptr);
+    if (!ws || ws_bytes < L.total) return CSA2_ERR_INVALID_ARG;
+    DeviceGuard dev(ctx);
+    if (!dev.ok) return CSA2_ERR_CUDA;
+    cudaStream_t s = as_stream(stream);
+    static std::atomic<uint64_t> done{0};
+    const uint64_t bit = 1ull << (ctx->device & 63);
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
+        CSA2_CHECK_CUDA(cudaFuncSetAttribute(mass_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)MS_SMEM));
+        done.fetch_or(bit, std::memory_order_relaxed);
+    }
+    uint8_t* base = reinterpret_cast<uint8_t*>(ws);
+    MassArgs a;
+    a.slots = {idx, n_visible, q_pos, N, 1, 0, k, 0, Q, (int64_t)B * N, ctx->status};
+    a.kv = kv;
+    a.kv_dt = kv_dt;
+    a.qh = reinterpret_cast<const float*>(base + L.qh);
+    a.lse = lse;
+    a.H = H;
+    a.flags = flags;
+    a.weights = weights;
+    a.acc = acc;
+    a.fix = acc && Q > 1 ? reinterpret_cast<unsigned long long*>(base + L.fix) : nullptr;
+    if (a.fix) CSA2_CHECK_CUDA(cudaMemsetAsync(a.fix, 0, (size_t)B * N * 8, s));
+    const int64_t heads = (int64_t)B * Q * H;
+    const unsigned hb = (unsigned)((heads + 7) / 8);
+    const RopeTable rope = make_rope_table(rope_base);
+    float* qh = reinterpret_cast<float*>(base + L.qh);
+    if (q_dt == CSA2_F32)
+        mass_prep_kernel<float><<<hb, 256, 0, s>>>(reinterpret_cast<const float*>(q), q_pos, heads, H, rope, flags, qh);
+    else
+        mass_prep_kernel<__nv_bfloat16><<<hb, 256, 0, s>>>(reinterpret_cast<const __nv_bfloat16*>(q), q_pos, heads, H,
+                                                          rope, flags, qh);
+    mass_simt_kernel<<<dim3((unsigned)((k + MS_KC - 1) / MS_KC), (unsigned)(B * Q)), 256, MS_SMEM, s>>>(a);
+    if (a.fix) {
+        const int64_t n = (int64_t)B * N;
+        mass_finish_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a.fix, acc, n);
+    }
+    return csa2_launch_status();
+}

@@ -1,0 +1,426 @@
+// Backward pass of the gated token compressor (csa2_compress_bwd).
+//
+// Per entry and channel, with the softmax weights s_j over the window's rows (the block's m
+// rows; overlapping form: and the previous block's m history rows) and E = sum s_j C_j:
+//     g   = RoPE_-pos(dout)                      (with CSA2_W_ROPE)
+//     dE  = r (g - E^ mean(E^ . g)), E^ = r E    (with CSA2_W_NORM, r the RMS factor; else g)
+//     dC_j = s_j dE,   dZ_j = s_j dE (C_j - E),   dB_j = sum over entries of dZ_j
+// The weights and E are computed again from the inputs; nothing of the forward is kept.
+//
+// Memory bound: every input row is read once and every gradient row written once.  A CTA of
+// c/4 threads (four adjacent channels each) takes a run of entries; windows of up to 8 rows
+// stay in registers between the softmax and the gradients, longer ones are read again (from
+// the caches).  The bias gradients are sums over all entries: each CTA sums its run in
+// registers (long windows: in its slab of the workspace), and a last pass adds the CTAs'
+// sums in order, so the results do not depend on timing.
+#include <algorithm>
+
+#include "attn_grad.cuh"
+
+namespace {
+
+constexpr int CB_CTAS = 152 * 8;
+
+template <typename T>
+__device__ __forceinline__ float4 ld4(const T* p);
+template <>
+__device__ __forceinline__ float4 ld4<float>(const float* p) {
+    return *reinterpret_cast<const float4*>(p);
+}
+template <>
+__device__ __forceinline__ float4 ld4<__nv_bfloat16>(const __nv_bfloat16* p) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xFFFF0000u));
+}
+template <typename T>
+__device__ __forceinline__ void st4(T* p, const float (&v)[4]);
+template <>
+__device__ __forceinline__ void st4<float>(float* p, const float (&v)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+template <>
+__device__ __forceinline__ void st4<__nv_bfloat16>(__nv_bfloat16* p, const float (&v)[4]) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(ag_pack_bf16x2(v[0], v[1]), ag_pack_bf16x2(v[2], v[3]));
+}
+__device__ __forceinline__ void unpack4(const float4& u, float (&v)[4]) {
+    v[0] = u.x;
+    v[1] = u.y;
+    v[2] = u.z;
+    v[3] = u.w;
+}
+
+template <typename T>
+struct CompressBwdArgs {
+    const T *ca, *za, *cb, *zb, *prev_cb, *prev_zb;
+    const float *ba, *bb;
+    int64_t n_tokens, n_ent, entries;   // entries of one stream, of all
+    int c, m;
+    const int64_t* pos0;
+    RopeTable rope;
+    unsigned flags;
+    const void* dout;
+    int dout_f32;
+    int64_t dout_stride;
+    T *dca, *dza, *dcb, *dzb, *dprev_cb, *dprev_zb;
+    float* slab;              // [CTAs, (1 or 2) m, c] sums of dZ, or NULL (no bias gradient)
+    int64_t run;              // entries per CTA
+};
+
+// Where the rows of an entry's window and their gradients are.
+template <typename T>
+struct Window {
+    const T *c0, *z0, *c1, *z1;   // block rows, history rows (NULL: none)
+    T *g0, *h0, *g1, *h1;         // their gradients (history: NULL = not wanted)
+};
+
+template <typename T>
+__device__ __forceinline__ Window<T> window_of(const CompressBwdArgs<T>& a, int64_t b, int64_t i) {
+    Window<T> w;
+    const int64_t at = (b * a.n_tokens + i * a.m) * a.c, before = at - (int64_t)a.m * a.c;
+    w.c0 = a.ca + at;
+    w.z0 = a.za + at;
+    w.g0 = a.dca + at;
+    w.h0 = a.dza + at;
+    w.c1 = w.z1 = nullptr;
+    w.g1 = w.h1 = nullptr;
+    if (a.cb) {
+        if (i > 0) {
+            w.c1 = a.cb + before;
+            w.z1 = a.zb + before;
+            w.g1 = a.dcb + before;
+            w.h1 = a.dzb + before;
+        } else if (a.prev_cb) {
+            const int64_t p = b * (int64_t)a.m * a.c;
+            w.c1 = a.prev_cb + p;
+            w.z1 = a.prev_zb + p;
+            if (a.dprev_cb) w.g1 = a.dprev_cb + p;
+            if (a.dprev_zb) w.h1 = a.dprev_zb + p;
+        }
+    }
+    return w;
+}
+
+// Sums of two values over the CTA (at most 8 warps), two alternating buffers.
+__device__ __forceinline__ void block_sum2(float& x, float& y, float2* red) {
+    x = warp_sum(x);
+    y = warp_sum(y);
+    const int nw = blockDim.x >> 5;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(x, y);
+    __syncthreads();
+    x = y = 0.0f;
+    for (int i = 0; i < nw; ++i) {
+        x += red[i].x;
+        y += red[i].y;
+    }
+}
+
+// MR > 0: windows of at most MR rows, kept in registers; MR == 0: any m, rows read again.
+template <typename T, int MR>
+__global__ void __launch_bounds__(256) compress_bwd_kernel(CompressBwdArgs<T> a) {
+    __shared__ float2 red[2][8];
+    const int ch = 4 * threadIdx.x;
+    const int m = a.m, c = a.c;
+    const int R = MR > 0 ? MR : 1;
+    const int64_t e0 = (int64_t)blockIdx.x * a.run, e1 = min(a.entries, e0 + a.run);
+    const int tables = a.cb ? 2 : 1;
+    float* slab = a.slab ? a.slab + (int64_t)blockIdx.x * tables * m * c + ch : nullptr;
+    float db[R][4];
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) db[j][k] = 0.0f;
+    if (MR == 0 && slab)
+        for (int j = 0; j < tables * m; ++j) *reinterpret_cast<float4*>(slab + (int64_t)j * c) = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int64_t e = e0; e < e1; ++e) {
+        const int64_t b = e / a.n_ent, i = e - b * a.n_ent;
+        const Window<T> w = window_of(a, b, i);
+        const int rows = w.c1 ? 2 * m : m;
+        auto src = [&](const T* cur, const T* hist, int j) { return (j < m ? cur + (int64_t)j * c : hist + (int64_t)(j - m) * c) + ch; };
+        auto logit = [&](int j, float (&z)[4]) {
+            unpack4(ld4<T>(src(w.z0, w.z1, j)), z);
+            const float* bias = j < m ? a.ba : a.bb;
+            if (bias) {
+                const float4 u = *reinterpret_cast<const float4*>(bias + (int64_t)(j < m ? j : j - m) * c + ch);
+                z[0] += u.x;
+                z[1] += u.y;
+                z[2] += u.z;
+                z[3] += u.w;
+            }
+        };
+        float z[R][4], v[R][4], mx[4], den[4], E[4], g[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            mx[k] = -INFINITY;
+            den[k] = E[k] = 0.0f;
+        }
+        const int64_t go = (b * a.dout_stride + i) * c + ch;
+        unpack4(a.dout_f32 ? ld4<float>(reinterpret_cast<const float*>(a.dout) + go)
+                           : ld4<__nv_bfloat16>(reinterpret_cast<const __nv_bfloat16*>(a.dout) + go), g);
+        if (MR > 0) {
+#pragma unroll
+            for (int j = 0; j < MR; ++j) {
+                if (j >= rows) break;
+                logit(j, z[j]);
+                unpack4(ld4<T>(src(w.c0, w.c1, j)), v[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < MR; ++j) {
+                if (j >= rows) break;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], z[j][k]);
+            }
+#pragma unroll
+            for (int j = 0; j < MR; ++j) {
+                if (j >= rows) break;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    z[j][k] = expf(z[j][k] - mx[k]);
+                    den[k] += z[j][k];
+                    E[k] = fmaf(z[j][k], v[j][k], E[k]);
+                }
+            }
+        } else {
+            float t[4], x[4];
+#pragma unroll 4
+            for (int j = 0; j < rows; ++j) {
+                logit(j, t);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], t[k]);
+            }
+#pragma unroll 4
+            for (int j = 0; j < rows; ++j) {
+                logit(j, t);
+                unpack4(ld4<T>(src(w.c0, w.c1, j)), x);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float p = expf(t[k] - mx[k]);
+                    den[k] += p;
+                    E[k] = fmaf(p, x[k], E[k]);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) E[k] /= den[k];
+        if ((a.flags & CSA2_W_ROPE) && ch >= c - 64) {
+            const int64_t pos = (a.pos0 ? a.pos0[b] : 0) + (int64_t)m * i;
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                float cs, sn;
+                rope_cos_sin(a.rope, pos, (ch + 2 * p - (c - 64)) >> 1, cs, sn);
+                const float x0 = g[2 * p], x1 = g[2 * p + 1];
+                g[2 * p] = x0 * cs + x1 * sn;
+                g[2 * p + 1] = x1 * cs - x0 * sn;
+            }
+        }
+        if (a.flags & CSA2_W_NORM) {
+            float ss = 0.0f, dot = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                ss = fmaf(E[k], E[k], ss);
+                dot = fmaf(E[k], g[k], dot);
+            }
+            block_sum2(ss, dot, red[(e - e0) & 1]);
+            const float r = 1.0f / sqrtf(ss / (float)c + 1e-6f);
+            const float d = dot * r * r / (float)c;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) g[k] = r * fmaf(-E[k], d, g[k]);
+        }
+        float inv[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) inv[k] = 1.0f / den[k];
+        auto emit = [&](int j, const float (&p)[4], const float (&x)[4], float (&sum)[4]) {
+            float dc[4], dz[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                dc[k] = p[k] * inv[k] * g[k];
+                dz[k] = dc[k] * (x[k] - E[k]);
+                sum[k] += dz[k];
+            }
+            const int64_t o = (int64_t)(j < m ? j : j - m) * c + ch;
+            T* gc = j < m ? w.g0 : w.g1;
+            T* gz = j < m ? w.h0 : w.h1;
+            if (gc) st4<T>(gc + o, dc);
+            if (gz) st4<T>(gz + o, dz);
+        };
+        if (MR > 0) {
+#pragma unroll
+            for (int j = 0; j < MR; ++j) {
+                if (j >= rows) break;
+                emit(j, z[j], v[j], db[j]);
+            }
+        } else {
+            float t[4], x[4];
+#pragma unroll 2
+            for (int j = 0; j < rows; ++j) {
+                logit(j, t);
+                unpack4(ld4<T>(src(w.c0, w.c1, j)), x);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) t[k] = expf(t[k] - mx[k]);
+                float s[4] = {0.f, 0.f, 0.f, 0.f};
+                emit(j, t, x, s);
+                if (slab) {
+                    float4* d = reinterpret_cast<float4*>(slab + (int64_t)j * c);
+                    float4 u = *d;
+                    u.x += s[0];
+                    u.y += s[1];
+                    u.z += s[2];
+                    u.w += s[3];
+                    *d = u;
+                }
+            }
+        }
+        if (a.cb && i == a.n_ent - 1) {
+            // the stream's last block is nobody's history within this call
+            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+            const int64_t at = (b * a.n_tokens + i * m) * c + ch;
+            for (int j = 0; j < m; ++j) {
+                st4<T>(a.dcb + at + (int64_t)j * c, zero);
+                st4<T>(a.dzb + at + (int64_t)j * c, zero);
+            }
+        }
+    }
+    if (MR > 0 && slab) {
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+            if (j < tables * m) *reinterpret_cast<float4*>(slab + (int64_t)j * c) = make_float4(db[j][0], db[j][1], db[j][2], db[j][3]);
+    }
+}
+
+// db[x] = sum of the CTAs' slabs in a fixed order: warp w of a block takes slabs w, w + 8, ..
+// of 32 adjacent columns, then the eight sums are added.
+__global__ void __launch_bounds__(256) compress_bias_kernel(const float* slab, int ctas, int64_t cols, int64_t split,
+                                                            float* dba, float* dbb) {
+    __shared__ float red[8][32];
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t x = (int64_t)blockIdx.x * 32 + lane;
+    float s = 0.0f;
+#pragma unroll 8
+    for (int i = w; i < ctas; i += 8) s += slab[(int64_t)i * cols + x];
+    red[w][lane] = s;
+    __syncthreads();
+    if (w == 0) {
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += red[i][lane];
+        float* d = x < split ? dba : dbb;
+        if (d) d[x < split ? x : x - split] = s;
+    }
+}
+
+int64_t cb_ctas(int64_t entries) {
+    const int64_t run = (entries + CB_CTAS - 1) / CB_CTAS;
+    return run > 0 ? (entries + run - 1) / run : 0;
+}
+
+struct CompressBwdCall {
+    const void *ca, *za, *cb, *zb, *prev_cb, *prev_zb;
+    const float *ba, *bb;
+    int B;
+    int64_t n_tokens;
+    int c, m;
+    const int64_t* pos0;
+    float rope_base;
+    unsigned flags;
+    const void* dout;
+    csa2_dtype dout_dt;
+    int64_t dout_stride;
+    void *dca, *dza, *dcb, *dzb, *dprev_cb, *dprev_zb;
+    float *dba, *dbb, *slab;
+};
+
+template <typename T>
+csa2_status cb_launch(const CompressBwdCall& p, cudaStream_t s) {
+    CompressBwdArgs<T> a;
+    a.ca = reinterpret_cast<const T*>(p.ca);
+    a.za = reinterpret_cast<const T*>(p.za);
+    a.cb = reinterpret_cast<const T*>(p.cb);
+    a.zb = reinterpret_cast<const T*>(p.zb);
+    a.prev_cb = reinterpret_cast<const T*>(p.prev_cb);
+    a.prev_zb = reinterpret_cast<const T*>(p.prev_zb);
+    a.ba = p.ba;
+    a.bb = p.bb;
+    a.n_tokens = p.n_tokens;
+    a.n_ent = p.n_tokens / p.m;
+    a.entries = a.n_ent * p.B;
+    a.c = p.c;
+    a.m = p.m;
+    a.pos0 = p.pos0;
+    a.rope = make_rope_table(p.rope_base);
+    a.flags = p.flags;
+    a.dout = p.dout;
+    a.dout_f32 = p.dout_dt == CSA2_F32;
+    a.dout_stride = p.dout_stride;
+    a.dca = reinterpret_cast<T*>(p.dca);
+    a.dza = reinterpret_cast<T*>(p.dza);
+    a.dcb = reinterpret_cast<T*>(p.dcb);
+    a.dzb = reinterpret_cast<T*>(p.dzb);
+    a.dprev_cb = reinterpret_cast<T*>(p.dprev_cb);
+    a.dprev_zb = reinterpret_cast<T*>(p.dprev_zb);
+    a.slab = p.dba || p.dbb ? p.slab : nullptr;
+    const int64_t ctas = cb_ctas(a.entries);
+    a.run = (a.entries + ctas - 1) / ctas;
+    const int rows = p.cb ? 2 * p.m : p.m;
+    const dim3 grid((unsigned)ctas), block((unsigned)(p.c / 4));
+    if (rows <= 2)
+        compress_bwd_kernel<T, 2><<<grid, block, 0, s>>>(a);
+    else if (rows <= 4)
+        compress_bwd_kernel<T, 4><<<grid, block, 0, s>>>(a);
+    else if (rows <= 8)
+        compress_bwd_kernel<T, 8><<<grid, block, 0, s>>>(a);
+    else
+        compress_bwd_kernel<T, 0><<<grid, block, 0, s>>>(a);
+    if (a.slab) {
+        const int64_t split = (int64_t)p.m * p.c, cols = split * (p.cb ? 2 : 1);
+        compress_bias_kernel<<<(unsigned)(cols / 32), 256, 0, s>>>(a.slab, (int)ctas, cols, split, p.dba, p.dbb);
+    }
+    return csa2_launch_status();
+}
+
+}  // namespace
+
+extern "C" size_t csa2_compress_bwd_workspace_bytes(int B, int64_t n_tokens, int c, int m, int overlap) {
+    if (B <= 0 || n_tokens <= 0 || c <= 0 || m < 1) return 0;
+    return (size_t)cb_ctas(n_tokens / m * B) * (overlap ? 2 : 1) * m * c * sizeof(float);
+}
+
+extern "C" csa2_status csa2_compress_bwd(csa2_ctx* ctx, const void* ca, const void* za, const void* cb, const void* zb,
+                                         csa2_dtype in_dt, const float* ba, const float* bb, const void* prev_cb,
+                                         const void* prev_zb, int B, int64_t n_tokens, int c, int m,
+                                         const int64_t* pos0, float rope_base, unsigned flags, const void* dout,
+                                         csa2_dtype dout_dt, int64_t dout_seq_stride, void* dca, void* dza, void* dcb,
+                                         void* dzb, void* dprev_cb, void* dprev_zb, float* dba, float* dbb, void* ws,
+                                         size_t ws_bytes, void* stream) {
+    if (!ctx || B < 0 || B > 65535 || n_tokens < 0 || m < 1 || c <= 0) return CSA2_ERR_INVALID_ARG;
+    if (n_tokens % m || c % 128 || c > 1024) return CSA2_ERR_INVALID_ARG;
+    if (!cb != !zb || !prev_cb != !prev_zb || (prev_cb && !cb)) return CSA2_ERR_INVALID_ARG;
+    if (flags & ~(CSA2_W_NORM | CSA2_W_ROPE)) return CSA2_ERR_INVALID_ARG;
+    if (in_dt != CSA2_F32 && in_dt != CSA2_BF16) return CSA2_ERR_UNSUPPORTED;
+    if (dout_dt != CSA2_F32 && dout_dt != CSA2_BF16) return CSA2_ERR_UNSUPPORTED;
+    if ((dbb || bb) && !cb) return CSA2_ERR_INVALID_ARG;
+    if ((dprev_cb || dprev_zb) && !prev_cb) return CSA2_ERR_INVALID_ARG;
+    for (const void* p : {ca, za, cb, zb, prev_cb, prev_zb, (const void*)ba, (const void*)bb, dout, (const void*)dca,
+                          (const void*)dza, (const void*)dcb, (const void*)dzb, (const void*)dprev_cb,
+                          (const void*)dprev_zb, (const void*)dba, (const void*)dbb, (const void*)ws})
+        if (!aligned(p, 16)) return CSA2_ERR_INVALID_ARG;
+    if (!aligned(pos0, 8)) return CSA2_ERR_INVALID_ARG;
+    DeviceGuard dev(ctx);
+    if (!dev.ok) return CSA2_ERR_CUDA;
+    cudaStream_t s = as_stream(stream);
+    if (B == 0 || n_tokens == 0) {
+        const size_t e = in_dt == CSA2_F32 ? 4 : 2, prev = (size_t)B * m * c * e;
+        if (prev && dprev_cb) CSA2_CHECK_CUDA(cudaMemsetAsync(dprev_cb, 0, prev, s));
+        if (prev && dprev_zb) CSA2_CHECK_CUDA(cudaMemsetAsync(dprev_zb, 0, prev, s));
+        if (dba) CSA2_CHECK_CUDA(cudaMemsetAsync(dba, 0, (size_t)m * c * 4, s));
+        if (dbb) CSA2_CHECK_CUDA(cudaMemsetAsync(dbb, 0, (size_t)m * c * 4, s));
+        return CSA2_OK;
+    }
+    if (!ca || !za || !dout || !dca || !dza || (cb && (!dcb || !dzb))) return CSA2_ERR_INVALID_ARG;
+    if (dout_seq_stride < n_tokens / m && B > 1) return CSA2_ERR_INVALID_ARG;
+    if ((dba || dbb) && (!ws || ws_bytes < csa2_compress_bwd_workspace_bytes(B, n_tokens, c, m, cb != nullptr)))
+        return CSA2_ERR_INVALID_ARG;
+    const CompressBwdCall p = {ca, za, cb, zb, prev_cb, prev_zb, ba, bb, B, n_tokens, c, m, pos0, rope_base, flags,
+                               dout, dout_dt, dout_seq_stride, dca, dza, dcb, dzb, dprev_cb, dprev_zb, dba, dbb,
+                               reinterpret_cast<float*>(ws)};
+    return in_dt == CSA2_F32 ? cb_launch<float>(p, s) : cb_launch<__nv_bfloat16>(p, s);
+}

@@ -11,7 +11,7 @@ Layer modes (CSA2 page, «三种模式：谁算、谁复用»):
 from __future__ import annotations
 
 from dataclasses import dataclass
-from typing import Optional
+from typing import Dict, Optional
 
 import torch
 
@@ -219,3 +219,40 @@ def prefill_chunk_step(Ca, Cb, Za, Zb, Ba, Bb, prev_Cb, prev_Zb, kv_cache, n_ctx
     C.csa2_sparse_attn(q, kv_cache, buf.idx, swa, q_pos, sink, window=window, swa_pos0=swa_pos0, out=buf.out,
                        ws=buf.attn_ws)
     return buf
+
+
+def layer_backward(q, kv, idx, swa, q_pos, sink, out, lse, dout, ca, za, m: int, *, cb=None, zb=None, ba=None, bb=None,
+                   prev_cb=None, prev_zb=None, pos0=0, window: int = 128, swa_pos0: int = 0,
+                   flags: int = C.ATTN_DEFAULT, write_flags: int = C.W_NORM | C.W_ROPE):
+    """Backward pass of a layer whose whole cache kv [B, N, c] csa2_compress made in one call
+    (N = n_tokens / m entries a sequence): the attention's gradients, then the compressor's
+    from the rows' gradient.  Returns ((dq, dkv, dswa, dsink), CompressGrads)."""
+    att = C.csa2_sparse_attn_bwd(q, kv, idx, swa, q_pos, sink, out, lse, dout, window=window, swa_pos0=swa_pos0,
+                                 flags=flags)
+    dkv = att[1] if ca.dim() == 3 else att[1][0]
+    com = C.csa2_compress_bwd(ca, za, m, dkv, cb=cb, zb=zb, ba=ba, bb=bb, prev_cb=prev_cb, prev_zb=prev_zb, pos0=pos0,
+                              flags=write_flags)
+    return att, com
+
+
+@dataclass
+class CutCaches:
+    """What an eviction leaves: the kept entries' old ids, and every cache cut to them."""
+    idx: torch.Tensor            # [B, keep] int32 ascending, -1 padded
+    n_entries: torch.Tensor      # [B] int64: entries each sequence kept
+    acc: torch.Tensor            # [B, keep] f32: their accumulated weights
+    caches: Dict[str, torch.Tensor]
+
+
+def evict_caches(acc, n_entries, caches: Dict[str, torch.Tensor], keep: int, recent: int = 0) -> CutCaches:
+    """Cut every sequence to `keep` entries: its newest `recent` and the others of the largest
+    accumulated attention weight (csa2_attn_mass).  caches: any [B, N, ..] tensors whose row j
+    belongs to entry j (main KV, indexer keys); new ones are returned, with acc cut alike.
+    Rows behind a shorter sequence's entries are zero in them."""
+    idx = C.csa2_evict_select(acc, n_entries, keep, recent=recent)
+    B = acc.shape[0]
+
+    def cut(t):
+        return C.csa2_cache_gather(t, idx, out=C.alloc((B, keep, *t.shape[2:]), dtype=t.dtype, device=t.device).zero_())
+
+    return CutCaches(idx, n_entries.clamp(min=0, max=keep), cut(acc), {name: cut(t) for name, t in caches.items()})

@@ -487,6 +487,140 @@ csa2_status csa2_sparse_attn_noalloc(csa2_ctx* ctx,
                                      int B, int Q, int H, int c, float rope_base, unsigned flags,
                                      void* out, csa2_dtype out_dt, float* lse, void* stream);
 
+/*
+ * csa2_sparse_attn_bwd / csa2_dense_attn_bwd -- the backward pass of csa2_sparse_attn and
+ * csa2_dense_attn (DSA-to-CSA/HCA page eqs. (18)-(19), (26), (27)): the gradients of a loss
+ * with respect to the query, the cache rows, the window rows and the sink, from dout, the
+ * gradient with respect to out.  The probabilities are computed again from the forward
+ * call's lse; with D = dout . out, do' = RoPE_t(dout), k^_j = RMSNorm(row_j):
+ *     p_j = e^{z_j - lse},   dS_j = p_j (do' . k^_j - D) / sqrt(c)
+ *     dq^ = sum_j dS_j k^_j,   dk^_j = sum over queries and heads of dS_j q^ + p_j do'
+ *     dsink_i = - sum over queries of e^{sink_i - lse} D
+ * and dq, dkv, dswa follow through the norms and the rotation the flags ask for (stored rows
+ * are leaves: their own write-side rotation and norm belong to csa2_compress_bwd).
+ *
+ *   q, kv, idx (n_visible, k_max), swa, q_pos, sink, B .. flags: as the forward call (flags
+ *               without CSA2_ATTN_PREPARED; kv F32 or BF16 -- unpack FP4 rows first)
+ *   out, dout : [B, Q, H, c] in out_dt (F32 or BF16), out as the forward wrote it
+ *   lse       : [B, Q, H] f32 as the forward wrote it; -inf marks a query that attends to
+ *               nothing, whose gradients are 0
+ *   dq        : [B, Q, H, c] in q_dt
+ *   dkv       : [B, N, c] in kv_dt or NULL;  dswa: [B, swa_cap, c] in swa_dt or NULL;
+ *   dsink     : [H] f32 or NULL (0 without a sink).  A NULL gradient is not wanted.
+ * Every wanted gradient is written in full: rows that no query attends to get 0.  An index
+ * that appears twice in a query's idx counts twice, as in the forward.  Gradients must not
+ * overlap the inputs or each other.  Row sums are added in query order without atomics:
+ * the same call gives the same bits.
+ *
+ * Workspace: csa2_attn_bwd_workspace_bytes() bytes (16-byte aligned) run the queries in one
+ * chunk (in chunks that keep it under 16 GiB for the largest calls); any smaller one that
+ * holds one query runs them in smaller chunks, one with less returns CSA2_ERR_INVALID_ARG.
+ * Calls that share a workspace must not overlap on the GPU.
+ * c == 512, 1 <= H <= 128, k <= 2048 (k_max <= 4,194,304), window <= 1024, B*Q <= 65535.
+ */
+size_t csa2_attn_bwd_workspace_bytes(csa2_ctx* ctx, csa2_dtype q_dt, csa2_dtype kv_dt, csa2_dtype swa_dt,
+                                     csa2_dtype out_dt, int B, int Q, int H, int k, int window, int64_t N,
+                                     int64_t swa_cap, unsigned flags);
+csa2_status csa2_sparse_attn_bwd(csa2_ctx* ctx,
+                                 const void* q, csa2_dtype q_dt,
+                                 const void* kv, csa2_dtype kv_dt, int64_t N,
+                                 const int32_t* idx, int k,
+                                 const void* swa, csa2_dtype swa_dt, int64_t swa_cap,
+                                 int64_t swa_pos0, int window,
+                                 const int64_t* q_pos, const float* sink,
+                                 const void* out, const void* dout, csa2_dtype out_dt, const float* lse,
+                                 int B, int Q, int H, int c, float rope_base, unsigned flags,
+                                 void* dq, void* dkv, void* dswa, float* dsink,
+                                 void* ws, size_t ws_bytes, void* stream);
+csa2_status csa2_dense_attn_bwd(csa2_ctx* ctx,
+                                const void* q, csa2_dtype q_dt,
+                                const void* kv, csa2_dtype kv_dt, int64_t N,
+                                const int64_t* n_visible, int k_max,
+                                const void* swa, csa2_dtype swa_dt, int64_t swa_cap,
+                                int64_t swa_pos0, int window,
+                                const int64_t* q_pos, const float* sink,
+                                const void* out, const void* dout, csa2_dtype out_dt, const float* lse,
+                                int B, int Q, int H, int c, float rope_base, unsigned flags,
+                                void* dq, void* dkv, void* dswa, float* dsink,
+                                void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * csa2_compress_bwd -- the backward pass of csa2_compress (both forms, with its RMSNorm and
+ * RoPE epilogue), from dout, the gradient with respect to the entries:
+ *     dC_j = s_j dE,   dZ_j = s_j dE (C_j - E),   dB_j = sum over entries of dZ_j
+ * per channel, s_j the softmax weights of the entry's window, E = sum_j s_j C_j, dE from dout
+ * back through the rotation and the norm.
+ *   ca .. pos0, flags : as the forward call (in_dt F32 or BF16)
+ *   dout      : row b*dout_seq_stride + i is the gradient of entry i of stream b, c values in
+ *               dout_dt (F32 or BF16); dout_seq_stride >= n_tokens/m
+ *   dca, dza (dcb, dzb) : [B, n_tokens, c] in in_dt, written in full.  Block i's overlap
+ *               rows get the gradient of entry i+1; the last block's get 0 (its entry
+ *               i+1 belongs to a later call, whose dprev rows are to be added there)
+ *   dprev_cb, dprev_zb : [B, m, c] in in_dt or NULL (not wanted); need prev_cb / prev_zb
+ *   dba, dbb  : [m, c] f32 or NULL (not wanted)
+ *   ws        : csa2_compress_bwd_workspace_bytes() bytes, used when a bias gradient is
+ *               wanted (else NULL will do)
+ * Sizes as csa2_compress; every pointer 16-byte aligned.  Sums are added in a fixed order.
+ */
+size_t csa2_compress_bwd_workspace_bytes(int B, int64_t n_tokens, int c, int m, int overlap);
+csa2_status csa2_compress_bwd(csa2_ctx* ctx,
+                              const void* ca, const void* za, const void* cb, const void* zb,
+                              csa2_dtype in_dt, const float* ba, const float* bb,
+                              const void* prev_cb, const void* prev_zb,
+                              int B, int64_t n_tokens, int c, int m, const int64_t* pos0,
+                              float rope_base, unsigned flags,
+                              const void* dout, csa2_dtype dout_dt, int64_t dout_seq_stride,
+                              void* dca, void* dza, void* dcb, void* dzb, void* dprev_cb, void* dprev_zb,
+                              float* dba, float* dbb, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * csa2_attn_mass -- how much attention the cache entries of a call received, from the
+ * forward call's lse (sparse form: idx; dense form: n_visible; the other NULL):
+ *     weights[b,q,j] = sum over heads of e^{z_j - lse}     (0 for an empty slot)
+ *     acc[b, s_j]   += weights[b,q,j],   s_j the entry of slot j
+ * the running score that csa2_evict_select goes by.  The window's rows are not counted.
+ *   q, kv (F32, BF16 or FP4), N, idx, n_visible, q_pos, rope_base, flags: as the forward
+ *   k       : slots of a query: idx's row length (<= 2048), or an upper bound of n_visible
+ *   lse     : [B, Q, H] f32 as the forward wrote it (-inf: the query counts nothing)
+ *   weights : [B, Q, k] f32 or NULL;  acc: [B, N] f32, updated, or NULL (one is needed)
+ *   ws      : csa2_attn_mass_workspace_bytes() bytes, 16-byte aligned
+ * The sums into acc do not depend on timing: with one query per sequence each entry gets
+ * one addend; with more they meet as 64-bit integers in units of 2^-39 first.
+ */
+size_t csa2_attn_mass_workspace_bytes(csa2_ctx* ctx, int B, int Q, int H, int k, int64_t N);
+csa2_status csa2_attn_mass(csa2_ctx* ctx,
+                           const void* q, csa2_dtype q_dt,
+                           const void* kv, csa2_dtype kv_dt, int64_t N,
+                           const int32_t* idx, const int64_t* n_visible, int k,
+                           const int64_t* q_pos, const float* lse,
+                           int B, int Q, int H, int c, float rope_base, unsigned flags,
+                           float* weights, float* acc, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * csa2_evict_select -- the entries of a cache that stay when it is cut to `keep`: the newest
+ * `recent` of row b's n_entries[b] entries, and of the others the best by (acc descending,
+ * entry ascending; -0 equals +0, NaN ranks above every number).  All stay if there are no
+ * more than `keep`.
+ *   acc       : [B, ld] f32 (the first n_entries[b] of a row are read)
+ *   n_entries : [B] int64, device; one above ld is taken as ld and flagged
+ *   out_idx   : [B, keep] int32, entry ids ascending, -1 padded
+ * keep >= 1, 0 <= recent <= keep, B <= 65535.
+ *
+ * csa2_cache_gather -- moves the kept rows of a cache together: dst[b, i] = src[b, idx[b, i]]
+ * for rows of row_bytes bytes (any cache: FP4, MXFP4, bf16 or f32 rows, or acc with 4-byte
+ * rows).  A row of dst whose idx is -1 is left as it is; ids outside [0, N) are skipped and
+ * flagged.
+ *   src : [B, N, row_bytes];  idx: [B, keep];  dst: [B, keep, row_bytes]
+ * row_bytes a multiple of 4, at most 2^20; dst must not overlap src (CSA2_ERR_INVALID_ARG).
+ * After an eviction entry i of the cut cache is the old entry idx[b, i]: stored rows carry
+ * their own rotation, so attention over them is unchanged, while the visible count of a
+ * sequence becomes the number of entries it kept.
+ */
+csa2_status csa2_evict_select(csa2_ctx* ctx, const float* acc, int B, int64_t ld, const int64_t* n_entries,
+                              int keep, int recent, int32_t* out_idx, void* stream);
+csa2_status csa2_cache_gather(csa2_ctx* ctx, const void* src, int64_t row_bytes, int B, int64_t N,
+                              const int32_t* idx, int keep, void* dst, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,256 @@
+"""Backward pass of the attention against the f64 gradient oracle: both dtypes' paths, sparse
+and dense form, odd sizes, head counts, queries without keys, repeated indices, chunked
+workspaces, flags, and the same bits from every run.
+
+Tolerances, as |g - o| <= tol (|o| + rms(o)):
+  * fp32 path (fp32 inputs): products and sums of at most 2,048 terms in fp32; the sums' rounding
+    is about sqrt(2048) 2^-24 = 3e-6 of the terms' rms, a logit of size up to 23 moves by
+    23 * 2^-22, so p by 6e-6; 1e-4 as for the forward pass.
+  * the same path with bf16 inputs and outputs: one rounding of the result more, at most 2^-8 of
+    |o| (8 significant bits).
+  * tensor-core path: q^, p r, dS r and a row's contribution are each rounded to bf16 (at most
+    2^-8 of their value, 2^-8 * 0.42 = 1.65e-3 rms over a uniform mantissa), and q^'s rounding
+    moves a logit, and so p, by about 1.65e-3 of a logit of order one.  Four such independent
+    errors are 3.3e-3 of the rms; the largest of up to 1e6 elements is six times that, 2e-2,
+    and the result's own rounding adds 4e-3: 2.5e-2."""
+import numpy as np
+import pytest
+import torch
+
+from compressed_sparse_attention_06_gb300 import csa2 as C
+from compressed_sparse_attention_06_gb300 import workloads as W
+from oracle import csa2_oracle as O
+from oracle import csa2_oracle_grad as G
+from tests.helpers import assert_close, to_np
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+F32_TOL, BF16_TOL, TC_TOL = 1e-4, 1e-4 + 2.0 ** -8, 2.5e-2
+
+
+def _case(seed, B, Q, H, N, k, window, cap, pos, dtype, n_pad=0, sink=True, dense=False, flags=C.ATTN_DEFAULT, scale=1.0):
+    s = dict(window=window, flags=flags, k=k)
+    s["q"] = W.normal_tensor((B, Q, H, 512), seed, 1, dtype, DEV, std=scale)
+    s["kv"] = W.normal_tensor((B, N, 512), seed, 2, dtype, DEV, std=1.3 * scale)
+    s["swa"] = W.normal_tensor((B, max(cap, 1), 512), seed, 3, dtype, DEV, std=scale)
+    s["q_pos"] = torch.tensor(pos, dtype=torch.int64, device=DEV).reshape(B, Q)
+    s["sink"] = W.normal_tensor((H,), seed, 4, torch.float32, DEV) if sink else None
+    s["dout"] = W.normal_tensor((B, Q, H, 512), seed, 5, dtype, DEV)
+    if dense:
+        s["nv"] = torch.tensor([[(37 * (b + 3 * i)) % (k + 1) for i in range(Q)] for b in range(B)], dtype=torch.int64,
+                               device=DEV)
+    else:
+        idx = torch.full((B, Q, k), -1, dtype=torch.int32)
+        for b in range(B):
+            for i in range(Q):
+                n = max(0, k - (n_pad if (b + i) % 2 else 0))
+                if n:
+                    idx[b, i, :n] = W.distinct_sample(N, n, seed + 7 + b, i).to(torch.int32)
+        s["idx"] = idx.to(DEV)
+    return s
+
+
+def _forward(s):
+    """out and lse in the case's dtype from the library's own forward pass."""
+    kw = dict(window=s["window"], flags=s["flags"], want_lse=True)
+    if "nv" in s:
+        o, l = C.csa2_dense_attn(s["q"], s["kv"], s["nv"], s["k"], s["swa"], s["q_pos"], s["sink"], **kw)
+    else:
+        o, l = C.csa2_sparse_attn(s["q"], s["kv"], s["idx"], s["swa"], s["q_pos"], s["sink"], **kw)
+    s["out"], s["lse"] = o, l
+    return s
+
+
+def _backward(s, **kw):
+    kw = dict(window=s["window"], flags=s["flags"], **kw)
+    if "nv" in s:
+        return C.csa2_dense_attn_bwd(s["q"], s["kv"], s["nv"], s["k"], s["swa"], s["q_pos"], s["sink"], s["out"], s["lse"],
+                                     s["dout"], **kw)
+    return C.csa2_sparse_attn_bwd(s["q"], s["kv"], s["idx"], s["swa"], s["q_pos"], s["sink"], s["out"], s["lse"],
+                                  s["dout"], **kw)
+
+
+def _oracle(s):
+    B, Q = s["q"].shape[:2]
+    parts = []
+    for b in range(B):
+        sel = [np.arange(int(s["nv"][b, i])) for i in range(Q)] if "nv" in s else to_np(s["idx"][b])
+        parts.append(G.attn_bwd(to_np(s["q"][b]), to_np(s["kv"][b]), sel, to_np(s["swa"][b]), 0, to_np(s["q_pos"][b]),
+                                None if s["sink"] is None else to_np(s["sink"]), s["window"], to_np(s["out"][b]),
+                                to_np(s["lse"][b]), to_np(s["dout"][b]), s["flags"]))
+    return [np.stack([p[i] for p in parts]) for i in range(3)] + [sum(p[3] for p in parts)]
+
+
+def _check(s, got, tol, sink_tol=1e-4):
+    want = _oracle(s)
+    for name, g, o, t in zip(("dq", "dkv", "dswa", "dsink"), got, want, (tol, tol, tol, sink_tol)):
+        assert_close(to_np(g.float()), o, t, name)
+
+
+@pytest.mark.parametrize("B,Q,H,N,k,window,cap,pos,n_pad", [
+    (1, 1, 1, 1, 1, 1, 1, [[0]], 0),                                   # one of everything
+    (1, 4, 16, 300, 65, 33, 40, [[299, 5, 0, 600]], 3),                # ragged chunks, partial windows
+    (2, 2, 9, 50, 31, 0, 0, [[4, 9], [1, 2]], 30),                     # no window
+    (2, 3, 24, 40, 0, 17, 64, [[3, 90, 16], [0, 1, 63]], 0),           # window only
+])
+def test_fp32_path(B, Q, H, N, k, window, cap, pos, n_pad):
+    s = _forward(_case(11, B, Q, H, N, k, window, cap, pos, torch.float32, n_pad))
+    got = _backward(s)
+    C.csa2_ctx_check()
+    _check(s, got, F32_TOL)
+
+
+@pytest.mark.parametrize("flags", [0, C.QNORM, C.KVNORM, C.ROPE, C.QNORM | C.KVNORM])
+@pytest.mark.parametrize("dtype,tol", [(torch.float32, F32_TOL), (torch.bfloat16, BF16_TOL)])
+def test_flags(flags, dtype, tol):
+    """Without both norms bf16 inputs run the fp32 path too (both norms alone: the tensor cores).
+    Small values keep unnormalised logits of order one."""
+    s = _forward(_case(12, 1, 3, 10, 60, 20, 9, 12, [[70, 3, 11]], dtype, 4, flags=flags, scale=0.25))
+    _check(s, _backward(s), TC_TOL if dtype == torch.bfloat16 and flags == C.QNORM | C.KVNORM else tol)
+
+
+@pytest.mark.parametrize("B,Q,H,N,k,window,cap,pos,n_pad", [
+    (1, 1, 64, 700, 512, 128, 128, [[699]], 0),                        # one query
+    (1, 3, 64, 300, 100, 128, 128, [[5, 127, 900]], 41),               # partial windows, ragged tile
+    (2, 5, 40, 997, 301, 100, 140, [[9, 4000, 301, 99, 77], [0, 50, 3, 1000, 2]], 57),
+    (1, 2, 1, 20, 1, 0, 0, [[3, 4]], 0),                               # one head, one key
+    (1, 2, 100, 600, 300, 64, 64, [[70, 500]], 10),                    # two head passes, the second partial
+    (1, 2, 128, 1500, 1024, 128, 128, [[1499, 20]], 0),
+    (2, 3, 64, 50, 0, 128, 256, [[3, 200, 127], [0, 1, 5000]], 0),     # window only
+])
+def test_tensor_core_path(B, Q, H, N, k, window, cap, pos, n_pad):
+    s = _forward(_case(13, B, Q, H, N, k, window, cap, pos, torch.bfloat16, n_pad))
+    got = _backward(s)
+    C.csa2_ctx_check()
+    _check(s, got, TC_TOL)
+
+
+def test_many_queries_share_rows():
+    """More queries than SMs over few entries: long lists per row."""
+    Q = 330
+    s = _forward(_case(14, 1, Q, 64, 90, 40, 16, 64, [[20 + i for i in range(Q)]], torch.bfloat16, 7))
+    got = _backward(s)
+    C.csa2_ctx_check()
+    _check(s, got, TC_TOL)
+
+
+@pytest.mark.parametrize("dtype,tol", [(torch.float32, F32_TOL), (torch.bfloat16, TC_TOL)])
+def test_dense(dtype, tol):
+    s = _forward(_case(15, 2, 4, 20, 150, 150, 20, 30, [[5, 40, 0, 300], [7, 8, 9, 100]], dtype, dense=True))
+    got = _backward(s)
+    C.csa2_ctx_check()
+    _check(s, got, tol)
+
+
+@pytest.mark.parametrize("dtype,tol", [(torch.float32, F32_TOL), (torch.bfloat16, TC_TOL)])
+@pytest.mark.parametrize("sink", [True, False])
+def test_queries_without_keys_and_repeated_indices(dtype, tol, sink):
+    """Query 1 attends to nothing (no index, a negative position): its gradient is 0 even where its
+    values are NaN; query 2 has the same index five times over."""
+    s = _case(16, 1, 4, 64, 80, 12, 10, 16, [[30, -1, 31, 2]], dtype, 0, sink=sink)
+    s["idx"][0, 1] = -1
+    s["idx"][0, 2, :5] = 33
+    _forward(s)
+    clean = _backward(s)
+    _check(s, clean, tol)
+    assert not clean[0][0, 1].any()
+    if not sink:
+        assert torch.isinf(s["lse"][0, 1]).all()
+        s["q"][0, 1] = float("nan")
+        s["dout"][0, 1] = float("nan")
+        again = _backward(s)
+        C.csa2_ctx_check()
+        for a, b in zip(again, clean):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_behind_empty_slots_are_not_read(dtype):
+    """NaN and infinity in rows that no slot points to stay out of every gradient."""
+    s = _forward(_case(17, 1, 3, 64, 100, 20, 8, 64, [[12, 20, 30]], dtype, 5))
+    clean = _backward(s)
+    used = set(s["idx"].flatten().tolist())
+    free = [i for i in range(100) if i not in used]
+    s["kv"][0, free] = float("nan")
+    s["swa"][0, 40:] = float("inf")
+    got = _backward(s)
+    C.csa2_ctx_check()
+    assert torch.equal(got[0], clean[0]) and torch.equal(got[3], clean[3])
+    keep = sorted(used - {-1})
+    assert torch.equal(got[1][0, keep], clean[1][0, keep])
+    assert torch.equal(got[2][0, :31], clean[2][0, :31])
+
+
+@pytest.mark.parametrize("dtype,tol", [(torch.float32, F32_TOL), (torch.bfloat16, TC_TOL)])
+def test_chunked_workspace_and_same_bits(dtype, tol):
+    """A workspace for a few queries at a time gives the gradients too (rows' sums carried in
+    fp32); two calls give the same bits; one too small for a query is refused."""
+    s = _forward(_case(18, 2, 23, 33, 70, 30, 12, 40, [[i * 3 for i in range(23)], [i + 9 for i in range(23)]], dtype, 3))
+    one = _backward(s)
+    two = _backward(s)
+    for a, b in zip(one, two):
+        assert torch.equal(a, b)
+    dt = {torch.float32: C.F32, torch.bfloat16: C.BF16}[dtype]
+    full = C._lib().csa2_attn_bwd_workspace_bytes(C.ctx(0), dt, dt, dt, dt, 2, 23, 33, 30, 12, 70, 40, 7)
+    for part in (2, 5):
+        ws = torch.empty(full // part, dtype=torch.uint8, device=DEV)
+        got = _backward(s, ws=ws)
+        C.csa2_ctx_check()
+        _check(s, got, tol)
+        assert torch.equal(got[0], one[0]) and torch.equal(got[3], one[3])
+    with pytest.raises(C.Csa2Error) as e:
+        _backward(s, ws=torch.empty(4096, dtype=torch.uint8, device=DEV))
+    assert e.value.status == C.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_out_of_range_index_is_flagged(dtype):
+    s = _forward(_case(19, 1, 2, 64, 50, 6, 4, 8, [[9, 10]], dtype))
+    clean_idx = s["idx"].clone()
+    clean_idx[0, 0, 5] = -1
+    s["idx"][0, 0, 5] = 50
+    got = _backward(s)
+    with pytest.raises(C.Csa2Error) as e:
+        C.csa2_ctx_check()
+    assert e.value.status == C.ERR_DEVICE
+    s["idx"] = clean_idx
+    for a, b in zip(got, _backward(s)):
+        assert torch.equal(a, b)
+    C.csa2_ctx_check()
+
+
+def test_unwanted_gradients_and_no_queries():
+    s = _forward(_case(20, 1, 2, 8, 30, 5, 4, 8, [[9, 10]], torch.bfloat16))
+    full = _backward(s)
+    dq, dkv, dswa, dsink = _backward(s, want_dkv=False, want_dswa=False, want_dsink=False)
+    assert dkv is None and dswa is None and dsink is None and torch.equal(dq, full[0])
+    for n in ("q", "out", "dout", "lse", "q_pos", "idx"):
+        s[n] = s[n][:, :0].contiguous()
+    dq, dkv, dswa, dsink = _backward(s)
+    C.csa2_ctx_check()
+    assert dq.numel() == 0 and not dkv.any() and not dswa.any() and not dsink.any()
+
+
+def test_captured_and_on_another_stream():
+    """A captured call, replayed after its inputs changed in place, equals an eager call."""
+    s = _forward(_case(21, 1, 5, 64, 200, 90, 20, 32, [[40, 41, 42, 43, 44]], torch.bfloat16, 8))
+    ref = _backward(s)
+    ws = torch.empty(C._lib().csa2_attn_bwd_workspace_bytes(C.ctx(0), 1, 1, 1, 1, 1, 5, 64, 90, 20, 200, 32, 7),
+                     dtype=torch.uint8, device=DEV)
+    outs = [torch.empty_like(x) for x in ref]
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    kw = dict(dq=outs[0], dkv=outs[1], dswa=outs[2], dsink=outs[3], ws=ws)
+    check, C._check = C._check, lambda fn, st: None if st == C.OK else (_ for _ in ()).throw(C.Csa2Error(fn, st))
+    try:
+        with torch.cuda.graph(graph, stream=stream):
+            _backward(s, **kw)
+    finally:
+        C._check = check
+    s["dout"].mul_(-2.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(outs, _backward(s)):
+        assert torch.equal(a, b)
+    C.csa2_ctx_check()

@@ -1,0 +1,250 @@
+"""Accumulated attention weight and eviction against the f64 oracle, and the decode that goes on
+over the cut cache.
+
+Tolerance of the weights: p = exp(z - lse) in fp32 with |z| <= 23: z to 23 * 2^-22 (sums of 512
+products, its rounding and exp's), so p to 6e-6; the lse given is the same number on both sides.
+The tensor-core path keeps q^ as two bf16 numbers (2^-17 of it left out, z to 23 * 2^-17 / sqrt(3)
+at the very worst, about 1e-5 of a typical z of one).  5e-5 (|o| + rms) covers both."""
+import numpy as np
+import pytest
+import torch
+
+from compressed_sparse_attention_06_gb300 import csa2 as C
+from compressed_sparse_attention_06_gb300 import pipeline as P
+from compressed_sparse_attention_06_gb300 import workloads as W
+from oracle import csa2_oracle as O
+from oracle import csa2_oracle_grad as G
+from tests.helpers import assert_close, to_np
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+TOL = 5e-5
+
+
+def _cache(seed, B, N, kind):
+    x = W.normal_tensor((B, N, 512), seed, 2, torch.float32, DEV) * 1.3
+    if kind == "fp4":
+        kv = C.csa2_fp4_pack(x)
+        return kv, O.nvfp4_unpack(to_np(kv).reshape(-1, 288)).reshape(B, N, 512)
+    kv = x.to(torch.bfloat16) if kind == "bf16" else x
+    return kv, to_np(kv)
+
+
+def _idx(seed, B, Q, N, k, pad=0):
+    idx = torch.full((B, Q, k), -1, dtype=torch.int32)
+    for b in range(B):
+        for i in range(Q):
+            n = k - (pad if (b + i) % 2 else 0)
+            idx[b, i, :n] = W.distinct_sample(N, n, seed + b, i).to(torch.int32)
+    return idx.to(DEV)
+
+
+@pytest.mark.parametrize("kind,q_dtype", [("bf16", torch.bfloat16), ("fp4", torch.bfloat16), ("f32", torch.float32),
+                                          ("fp4", torch.float32)])
+@pytest.mark.parametrize("B,Q,H,N,k,pad", [(2, 1, 64, 900, 512, 100), (1, 1, 1, 1, 1, 0), (2, 7, 40, 300, 65, 64),
+                                           (1, 3, 128, 400, 200, 1), (1, 170, 64, 100, 33, 5)])
+def test_mass(kind, q_dtype, B, Q, H, N, k, pad):
+    kv, kv_np = _cache(31, B, N, kind)
+    q = W.normal_tensor((B, Q, H, 512), 31, 1, q_dtype, DEV)
+    idx = _idx(31, B, Q, N, k, pad)
+    if k > 4:
+        idx[0, 0, 1] = idx[0, 0, 0]                        # the same entry twice
+    q_pos = torch.arange(B * Q, device=DEV).view(B, Q) * 11
+    _, lse = C.csa2_sparse_attn(q, kv, idx, None, q_pos, None, window=0, want_lse=True)
+    acc0 = torch.rand(B, N, generator=torch.Generator(DEV).manual_seed(5), device=DEV)
+    acc = acc0.clone()
+    w, same = C.csa2_attn_mass(q, kv, q_pos, lse, idx=idx, acc=acc, want_weights=True)
+    C.csa2_ctx_check()
+    assert same is acc
+    again = acc0.clone()
+    C.csa2_attn_mass(q, kv, q_pos, lse, idx=idx, acc=again)
+    assert torch.equal(acc, again)                         # the same bits every time
+    only, none = C.csa2_attn_mass(q, kv, q_pos, lse, idx=idx, want_weights=True)
+    assert none is None and torch.equal(only, w)
+    for b in range(B):
+        ow, om = G.attn_mass(to_np(q[b]), kv_np[b], to_np(idx[b]), to_np(q_pos[b]), to_np(lse[b]))
+        assert_close(to_np(w[b]), ow, TOL, "weights")
+        assert_close(to_np(acc[b]), to_np(acc0[b]) + om, TOL, "acc")
+    assert not w[idx < 0].any()
+    free = torch.ones(B, N, dtype=torch.bool, device=DEV)
+    free.scatter_(1, idx.clamp(min=0).flatten(1).long(), False)
+    assert torch.equal(acc[free], acc0[free])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_mass_dense(kind):
+    B, Q, H, N = 2, 5, 24, 140
+    kv, kv_np = _cache(32, B, N, kind)
+    q = W.normal_tensor((B, Q, H, 512), 32, 1, torch.float32 if kind == "f32" else torch.bfloat16, DEV)
+    nv = torch.tensor([[0, 1, 64, 139, 140], [128, 65, 7, 140, 2]], dtype=torch.int64, device=DEV)
+    q_pos = nv * 128 + 5
+    _, lse = C.csa2_dense_attn(q, kv, nv, N, None, q_pos, None, window=0, want_lse=True)
+    acc = torch.zeros(B, N, device=DEV)
+    w, _ = C.csa2_attn_mass(q, kv, q_pos, lse, n_visible=nv, k_max=N, acc=acc, want_weights=True)
+    C.csa2_ctx_check()
+    for b in range(B):
+        sel = np.where(np.arange(N) < to_np(nv[b])[:, None], np.arange(N), -1)
+        ow, om = G.attn_mass(to_np(q[b]), kv_np[b], sel, to_np(q_pos[b]), to_np(lse[b]))
+        assert_close(to_np(w[b]), ow, TOL, "weights")
+        assert_close(to_np(acc[b]), om, TOL, "acc")
+
+
+@pytest.mark.parametrize("Q", [1, 2])
+def test_mass_shows_a_query_of_nan_and_skips_an_empty_one(Q):
+    """A NaN query makes its entries' sums NaN (and no others); an lse of -inf counts nothing."""
+    kv, _ = _cache(33, 1, 20, "bf16")
+    q = W.normal_tensor((1, Q, 64, 512), 33, 1, torch.bfloat16, DEV)
+    q[0, 0] = float("nan")
+    idx = torch.full((1, Q, 4), -1, dtype=torch.int32, device=DEV)
+    idx[0, 0] = torch.tensor([3, 5, 7, -1])
+    if Q > 1:
+        idx[0, 1] = torch.tensor([8, 9, 10, 11])
+    lse = torch.zeros(1, Q, 64, device=DEV)
+    acc = torch.ones(1, 20, device=DEV)
+    C.csa2_attn_mass(q, kv, torch.zeros(1, Q, dtype=torch.int64, device=DEV), lse, idx=idx, acc=acc)
+    assert torch.isnan(acc[0]).nonzero().flatten().tolist() == [3, 5, 7]
+    acc = torch.ones(1, 20, device=DEV)
+    q[0, 0] = 1.0
+    w, _ = C.csa2_attn_mass(q, kv, torch.zeros(1, Q, dtype=torch.int64, device=DEV), torch.full_like(lse, -float("inf")),
+                            idx=idx, acc=acc, want_weights=True)
+    C.csa2_ctx_check()
+    assert not w.any() and bool((acc == 1).all())
+
+
+def test_mass_flags_an_out_of_range_index():
+    kv, _ = _cache(34, 1, 20, "bf16")
+    q = W.normal_tensor((1, 1, 64, 512), 34, 1, torch.bfloat16, DEV)
+    acc = torch.zeros(1, 20, device=DEV)
+    idx = torch.tensor([[[1, 20, -5]]], dtype=torch.int32, device=DEV)
+    w, _ = C.csa2_attn_mass(q, kv, torch.zeros(1, 1, dtype=torch.int64, device=DEV), torch.zeros(1, 1, 64, device=DEV),
+                            idx=idx, acc=acc, want_weights=True)
+    with pytest.raises(C.Csa2Error) as e:
+        C.csa2_ctx_check()
+    assert e.value.status == C.ERR_DEVICE
+    assert w[0, 0, 0] > 0 and not w[0, 0, 1:].any() and acc.count_nonzero() == 1
+
+
+@pytest.mark.parametrize("B,ld,keep,recent", [
+    (1, 1, 1, 0), (3, 7, 3, 1), (2, 1000, 400, 400), (2, 1000, 999, 0), (4, 9001, 4001, 128), (2, 20000, 1, 0),
+    (1, 70001, 35000, 1000), (3, 65536, 65535, 7), (2, 8192, 9000, 100), (70, 300, 100, 10)])
+def test_select(B, ld, keep, recent):
+    """Ties (a coarse grid of weights), rows of any length from 0 to ld, signed zeros, infinities."""
+    g = torch.Generator(DEV).manual_seed(ld)
+    acc = torch.randint(-3, 60, (B, ld), generator=g, device=DEV).float() / 7.0
+    acc[:, ::5] = torch.rand(acc[:, ::5].shape, generator=g, device=DEV) ** 8
+    acc[:, 3::11] = -0.0
+    acc[:, 4::13] = 0.0
+    if ld > 100:
+        acc[0, 50], acc[0, 60], acc[-1, 70] = float("inf"), -float("inf"), float("nan")
+    n = torch.randint(0, ld + 1, (B,), generator=g, device=DEV)
+    n[0] = ld
+    if B > 2:
+        n[1] = 0
+        n[2] = min(keep, ld)
+    idx = C.csa2_evict_select(acc, n, keep, recent=recent)
+    C.csa2_ctx_check()
+    a = acc.cpu().numpy()
+    for b in range(B):
+        assert np.array_equal(idx[b].cpu().numpy(), G.evict_keep(a[b], int(n[b]), keep, recent)), f"row {b}"
+
+
+def test_select_all_equal_and_length_above_ld():
+    acc = torch.full((2, 30000), 0.25, device=DEV)
+    idx = C.csa2_evict_select(acc, torch.tensor([30000, 30001], device=DEV), 12345, recent=45)
+    want = torch.cat([torch.arange(12300), torch.arange(29955, 30000)]).to(torch.int32)
+    assert torch.equal(idx[0].cpu(), want) and torch.equal(idx[1].cpu(), want)
+    with pytest.raises(C.Csa2Error) as e:
+        C.csa2_ctx_check()
+    assert e.value.status == C.ERR_DEVICE
+
+
+@pytest.mark.parametrize("shape,dtype", [((288,), torch.uint8), ((68,), torch.uint8), ((512,), torch.bfloat16),
+                                         ((), torch.float32), ((512,), torch.float32), ((4,), torch.uint8)])
+def test_gather(shape, dtype):
+    B, N, keep = 3, 501, 233
+    g = torch.Generator(DEV).manual_seed(9)
+    n = B * N * (int(np.prod(shape)) if shape else 1) * torch.empty((), dtype=dtype).element_size()
+    src = torch.randint(0, 255, (n,), generator=g, device=DEV, dtype=torch.uint8).view(dtype).view(B, N, *shape)
+    idx = torch.stack([W.distinct_sample(N, keep, 9, b, DEV) for b in range(B)]).to(torch.int32)
+    idx[1, 200:] = -1
+    out = torch.zeros((B, keep, *shape), dtype=dtype, device=DEV)
+    C.csa2_cache_gather(src, idx, out=out)
+    C.csa2_ctx_check()
+    want = torch.zeros_like(out)
+    for b in range(B):
+        at = idx[b] >= 0
+        want[b, at] = src[b, idx[b, at].long()]
+    assert torch.equal(out.view(torch.uint8), want.view(torch.uint8))       # the -1 rows are as they were
+    idx[2, 0] = N
+    C.csa2_cache_gather(src, idx, out=out)
+    with pytest.raises(C.Csa2Error) as e:
+        C.csa2_ctx_check()
+    assert e.value.status == C.ERR_DEVICE
+    inside = src.view(-1)[:out[:, :2].numel()].view(B, 2, *shape)            # rows moved within one buffer
+    with pytest.raises(C.Csa2Error) as e:
+        C.csa2_cache_gather(src, torch.zeros((B, 2), dtype=torch.int32, device=DEV), out=inside)
+    assert e.value.status == C.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp4"])
+def test_decode_goes_on_over_the_cut_cache(kind):
+    """Decode steps account their weights, the cache is cut, and attention over the kept entries of a
+    query's selection is what it was over the full cache."""
+    B, N, H, keep = 2, 3000, 64, 1200
+    kv, kv_np = _cache(35, B, N, kind)
+    ki = C.csa2_fp4_pack(W.normal_tensor((B, N, 128), 35, 6, torch.float32, DEV), C.MXFP4_E8M0x32)
+    swa = W.normal_tensor((B, 128, 512), 35, 3, torch.bfloat16, DEV)
+    sink = W.normal_tensor((H,), 35, 4, torch.float32, DEV)
+    acc = torch.zeros(B, N, device=DEV)
+    total = [np.zeros(N) for _ in range(B)]
+    for step in range(3):
+        q = W.normal_tensor((B, 1, H, 512), 36, step, torch.bfloat16, DEV)
+        idx = _idx(40 + step, B, 1, N, 512)
+        q_pos = torch.full((B, 1), N + step, dtype=torch.int64, device=DEV)
+        _, lse = C.csa2_sparse_attn(q, kv, idx, swa, q_pos, sink, want_lse=True)
+        C.csa2_attn_mass(q, kv, q_pos, lse, idx=idx, acc=acc)
+        for b in range(B):
+            total[b] += G.attn_mass(to_np(q[b]), kv_np[b], to_np(idx[b]), to_np(q_pos[b]), to_np(lse[b]))[1]
+    for b in range(B):
+        assert_close(to_np(acc[b]), total[b], TOL, "acc")
+    n = torch.tensor([N, N - 100], dtype=torch.int64, device=DEV)
+    cut = P.evict_caches(acc, n, {"kv": kv, "ki": ki}, keep, recent=64)
+    C.csa2_ctx_check()
+    assert cut.n_entries.tolist() == [keep, keep]
+    a = acc.cpu().numpy()
+    for b in range(B):
+        ids = G.evict_keep(a[b], int(n[b]), keep, 64)
+        assert np.array_equal(to_np(cut.idx[b]), ids)
+        assert torch.equal(cut.caches["kv"][b], kv[b, torch.tensor(ids).long()])
+        assert torch.equal(cut.caches["ki"][b], ki[b, torch.tensor(ids).long()])
+        assert torch.equal(cut.acc[b], acc[b, torch.tensor(ids).long()])
+    # a selection over the cut cache, and the same entries in the full one
+    new = _idx(50, B, 1, keep, 512)
+    old = torch.gather(cut.idx, 1, new[:, 0].long())[:, None].contiguous()
+    q = W.normal_tensor((B, 1, H, 512), 37, 0, torch.bfloat16, DEV)
+    q_pos = torch.full((B, 1), N + 9, dtype=torch.int64, device=DEV)
+    o1, _ = C.csa2_sparse_attn(q, cut.caches["kv"], new, swa, q_pos, sink)
+    o2, _ = C.csa2_sparse_attn(q, kv, old, swa, q_pos, sink)
+    assert torch.equal(o1, o2)
+
+
+def test_mass_captured():
+    kv, _ = _cache(38, 1, 400, "fp4")
+    q = W.normal_tensor((1, 3, 64, 512), 38, 1, torch.bfloat16, DEV)
+    idx = _idx(38, 1, 3, 400, 100)
+    q_pos = torch.tensor([[5, 6, 7]], dtype=torch.int64, device=DEV)
+    _, lse = C.csa2_sparse_attn(q, kv, idx, None, q_pos, None, window=0, want_lse=True)
+    ws = torch.empty(C._lib().csa2_attn_mass_workspace_bytes(C.ctx(0), 1, 3, 64, 100, 400), dtype=torch.uint8, device=DEV)
+    acc, ref = torch.zeros(1, 400, device=DEV), torch.zeros(1, 400, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    check, C._check = C._check, lambda fn, st: None if st == C.OK else (_ for _ in ()).throw(C.Csa2Error(fn, st))
+    try:
+        with torch.cuda.graph(graph):
+            C.csa2_attn_mass(q, kv, q_pos, lse, idx=idx, acc=acc, ws=ws)
+    finally:
+        C._check = check
+    for _ in range(3):
+        graph.replay()
+        C.csa2_attn_mass(q, kv, q_pos, lse, idx=idx, acc=ref)
+    torch.cuda.synchronize()
+    assert torch.equal(acc, ref)
