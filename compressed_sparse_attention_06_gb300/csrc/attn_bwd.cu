@@ -21,6 +21,7 @@
 #include <atomic>
 #include <cstring>
 
+#include "attn_bwd_tc.cuh"
 #include "attn_grad.cuh"
 
 namespace {
@@ -477,54 +478,62 @@ csa2_status raise_smem(K kern, size_t bytes, int device, std::atomic<uint64_t>& 
 
 // ---------------------------------------------------------------- workspace
 
-struct BwdLayout {
-    size_t D, rinv, cnt, loc, tot, blk, rank, qh, dh, pds, part, acc, total;
-    int groups, group_q;
-    int64_t rows;
+struct BwdSizes {
+    int64_t n_bq;
+    int H, n_slots;
+    int64_t rows;             // cache and window rows
+    bool tc;                  // tensor-core path
+    int num_sms;
 };
 
-BwdLayout bwd_layout(int64_t n_bq, int H, int n_slots, int64_t rows, int64_t nb, bool chunked) {
+struct BwdLayout {
+    size_t D, rinv, cnt, loc, tot, blk, rank, qh, dh, pds, img, dqh, part, acc, total;
+    int groups, group_q, n_pass, n_split, tps;
+};
+
+// Workspace of chunks of nb queries.
+BwdLayout bwd_layout(const BwdSizes& z, int64_t nb) {
     BwdLayout L;
-    L.rows = rows;
-    const int64_t g = std::min<int64_t>({nb, MAX_GROUPS, std::max<int64_t>(1, MAX_COUNTERS / std::max<int64_t>(1, rows))});
+    const int64_t g = std::min<int64_t>({nb, MAX_GROUPS, std::max<int64_t>(1, MAX_COUNTERS / std::max<int64_t>(1, z.rows))});
     L.group_q = (int)((nb + g - 1) / g);
     L.groups = (int)((nb + L.group_q - 1) / L.group_q);
+    L.n_pass = z.tc ? (z.H + 63) / 64 : 1;
+    bwd_tc_splits(z.num_sms, nb * L.n_pass, z.n_slots, &L.n_split, &L.tps);
     size_t at = 0;
     auto take = [&at](size_t bytes) {
         const size_t o = at;
         at = align_up(at + bytes, 256);
         return o;
     };
-    L.D = take((size_t)n_bq * H * 4);
-    L.rinv = take((size_t)rows * 4);
-    L.cnt = take((size_t)L.groups * rows * 4);
-    L.loc = take((size_t)rows * 4);
-    L.tot = take((size_t)rows * 4);
-    L.blk = take((size_t)((rows + SCAN_ROWS - 1) / SCAN_ROWS) * 4);
-    L.rank = take((size_t)nb * n_slots * 4);
-    L.qh = take((size_t)nb * H * AG_C * 4);
-    L.dh = take((size_t)nb * H * AG_C * 4);
-    L.pds = take((size_t)nb * H * n_slots * 8);
-    L.part = take((size_t)nb * n_slots * AG_C * 4);
-    L.acc = take(chunked ? (size_t)rows * AG_C * 4 : 0);
+    const size_t row_f32 = (size_t)AG_C * 4, heads = (size_t)nb * z.H, pairs = (size_t)nb * z.n_slots;
+    L.D = take((size_t)z.n_bq * z.H * 4);
+    L.rinv = take((size_t)z.rows * 4);
+    L.cnt = take((size_t)L.groups * z.rows * 4);
+    L.loc = take((size_t)z.rows * 4);
+    L.tot = take((size_t)z.rows * 4);
+    L.blk = take((size_t)((z.rows + SCAN_ROWS - 1) / SCAN_ROWS) * 4);
+    L.rank = take(pairs * 4);
+    L.qh = take(z.tc ? 0 : heads * row_f32);
+    L.dh = take(z.tc ? 0 : heads * row_f32);
+    L.pds = take(z.tc ? 0 : heads * z.n_slots * 8);
+    L.img = take(z.tc ? (size_t)nb * L.n_pass * bwd_tc_image_bytes() : 0);
+    L.dqh = take(z.tc ? (size_t)nb * L.n_pass * L.n_split * 64 * row_f32 : 0);
+    L.part = take(z.tc ? pairs * L.n_pass * AG_C * 2 : pairs * row_f32);
+    L.acc = take(nb < z.n_bq ? (size_t)z.rows * row_f32 : 0);
     L.total = at;
     return L;
 }
 
 constexpr size_t WS_TARGET = (size_t)16 << 30;   // the recommended workspace stays below this
 
-int64_t chunk_for(int64_t n_bq, int H, int n_slots, int64_t rows, size_t bytes) {
-    auto fits = [&](int64_t nb) { return bwd_layout(n_bq, H, n_slots, rows, nb, nb < n_bq).total <= bytes; };
-    // at most 2^31 - 1 places, and grid.y slices, in a chunk
-    int64_t hi = std::min<int64_t>(n_bq, n_slots > 0 ? 0x7FFFFFFFll / n_slots : n_bq);
-    hi = std::min<int64_t>(hi, 65535);
-    if (fits(hi)) return hi;
-    int64_t lo = 0;                              // the largest nb < hi that fits (0: none)
-    while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) / 2;
-        (fits(mid) ? lo : hi) = mid;
-    }
-    return lo;
+// The most queries a chunk can have in `bytes` of workspace (0: not one fits).
+int64_t chunk_for(const BwdSizes& z, size_t bytes) {
+    // fewer queries may split their keys further, so sizes are not monotonic where splits set
+    // in; what fits is looked for from above, halving
+    int64_t nb = std::min<int64_t>(z.n_bq, 65535);
+    if (z.n_slots > 0) nb = std::min<int64_t>(nb, 0x7FFFFFFFll / z.n_slots);   // places fit an int
+    while (nb > 0 && bwd_layout(z, nb).total > bytes) nb = nb > 1 ? (nb + 1) / 2 : 0;
+    return nb;
 }
 
 struct BwdCall {
@@ -570,9 +579,11 @@ csa2_status bwd_run(csa2_ctx* ctx, const BwdCall& a, void* ws, size_t ws_bytes, 
     const int n_slots = a.k + a.window;
     const int64_t n_kv = a.k > 0 ? (int64_t)a.B * a.N : 0, n_sw = a.window > 0 ? (int64_t)a.B * a.swa_cap : 0;
     const int64_t rows = n_kv + n_sw;
-    const int64_t nb_max = chunk_for(n_bq, a.H, n_slots, rows, ws_bytes);
+    const BwdSizes z = {n_bq, a.H, n_slots, rows,
+                        bwd_tc_applies(a.q_dt, a.kv_dt, a.k, a.swa_dt, a.window, a.out_dt, a.flags), ctx->num_sms};
+    const int64_t nb_max = chunk_for(z, ws_bytes);
     if (nb_max < 1) return CSA2_ERR_INVALID_ARG;
-    const BwdLayout L = bwd_layout(n_bq, a.H, n_slots, rows, nb_max, nb_max < n_bq);
+    const BwdLayout L = bwd_layout(z, nb_max);
     uint8_t* base = reinterpret_cast<uint8_t*>(ws);
     float* D = reinterpret_cast<float*>(base + L.D);
     float* rinv = reinterpret_cast<float*>(base + L.rinv);
@@ -619,8 +630,8 @@ csa2_status bwd_run(csa2_ctx* ctx, const BwdCall& a, void* ws, size_t ws_bytes, 
         c.bq0 = bq0;
         c.nb = (int)std::min<int64_t>(nb_max, n_bq - bq0);
         if (rows > 0) {
-            const csa2_status z = zero_bytes(cnt, (size_t)L.groups * rows * 4, s);
-            if (z != CSA2_OK) return z;
+            const csa2_status zr = zero_bytes(cnt, (size_t)L.groups * rows * 4, s);
+            if (zr != CSA2_OK) return zr;
             bwd_rank_kernel<<<(unsigned)L.groups, 512, 0, s>>>(c.slots, bq0, c.nb, L.group_q, n_slots, rows, cnt, rank);
             bwd_place_kernel<<<(unsigned)n_blk, SCAN_ROWS, 0, s>>>(cnt, L.groups, rows, loc, tot, blk);
             bwd_scan_kernel<<<1, 1024, 0, s>>>(blk, n_blk);
@@ -629,7 +640,15 @@ csa2_status bwd_run(csa2_ctx* ctx, const BwdCall& a, void* ws, size_t ws_bytes, 
         float* dh = reinterpret_cast<float*>(base + L.dh);
         float2* pds = reinterpret_cast<float2*>(base + L.pds);
         csa2_status r;
-        if (a.q_dt == CSA2_F32)
+        if (z.tc) {
+            BwdTcArgs t;
+            t.c = c;
+            t.dqh = reinterpret_cast<float*>(base + L.dqh);
+            t.n_pass = L.n_pass;
+            t.n_split = L.n_split;
+            t.tps = L.tps;
+            r = bwd_tc_chunk(ctx, t, a.dout, base + L.img, s);
+        } else if (a.q_dt == CSA2_F32)
             r = a.out_dt == CSA2_F32 ? simt_chunk<float, float>(ctx, a, c, qh, dh, pds, s)
                                      : simt_chunk<float, __nv_bfloat16>(ctx, a, c, qh, dh, pds, s);
         else
@@ -639,7 +658,7 @@ csa2_status bwd_run(csa2_ctx* ctx, const BwdCall& a, void* ws, size_t ws_bytes, 
         if (rows > 0 && (a.dkv || a.dswa)) {
             RowSumArgs ra;
             ra.part = c.part;
-            ra.passes = 1;
+            ra.passes = L.n_pass;
             ra.loc = loc;
             ra.tot = tot;
             ra.blk = blk;
@@ -656,7 +675,10 @@ csa2_status bwd_run(csa2_ctx* ctx, const BwdCall& a, void* ws, size_t ws_bytes, 
             ra.last = bq0 + c.nb == n_bq;
             ra.dkv = a.dkv;
             ra.dswa = a.dswa;
-            bwd_rowsum_kernel<float><<<(unsigned)rows, 128, 0, s>>>(ra);
+            if (z.tc)
+                bwd_rowsum_kernel<__nv_bfloat16><<<(unsigned)rows, 128, 0, s>>>(ra);
+            else
+                bwd_rowsum_kernel<float><<<(unsigned)rows, 128, 0, s>>>(ra);
         }
         if (csa2_launch_status() != CSA2_OK) return CSA2_ERR_CUDA;
     }
@@ -702,11 +724,10 @@ extern "C" size_t csa2_attn_bwd_workspace_bytes(csa2_ctx* ctx, csa2_dtype q_dt, 
                                                 csa2_dtype out_dt, int B, int Q, int H, int k, int window, int64_t N,
                                                 int64_t swa_cap, unsigned flags) {
     if (!ctx || B <= 0 || Q <= 0 || H < 1 || H > 128 || k < 0 || window < 0 || N < 0 || swa_cap < 0) return 0;
-    (void)q_dt, (void)kv_dt, (void)swa_dt, (void)out_dt, (void)flags;
-    const int64_t n_bq = (int64_t)B * Q;
     const int64_t rows = (k > 0 ? (int64_t)B * N : 0) + (window > 0 ? (int64_t)B * swa_cap : 0);
-    const int64_t nb = std::max<int64_t>(1, chunk_for(n_bq, H, k + window, rows, WS_TARGET));
-    return bwd_layout(n_bq, H, k + window, rows, nb, nb < n_bq).total;
+    const BwdSizes z = {(int64_t)B * Q, H, k + window, rows,
+                        bwd_tc_applies(q_dt, kv_dt, k, swa_dt, window, out_dt, flags), ctx->num_sms};
+    return bwd_layout(z, std::max<int64_t>(1, chunk_for(z, WS_TARGET))).total;
 }
 
 extern "C" csa2_status csa2_sparse_attn_bwd(csa2_ctx* ctx, const void* q, csa2_dtype q_dt, const void* kv,

@@ -1,0 +1,24 @@
+// Tensor-core path of the attention's backward pass (attn_bwd_tc.cu), called per chunk of
+// queries by attn_bwd.cu, which owns validation, the scatter plan and the row sums.
+#pragma once
+
+#include "attn_grad.cuh"
+
+struct BwdTcArgs {
+    BwdChunk c;               // part: bf16 [places, n_pass, 512]
+    const uint8_t* img;       // [n_pass, nb] stacked images of the chunk's queries
+    float* dqh;               // [n_pass, nb, n_split, 64, 512] dq^ of every item
+    int n_pass, n_split, tps; // 64-head passes; key splits of a query, 64-slot tiles of a split
+    int64_t items;
+    long long budget;
+    int stall;                // test hook: no image is copied
+};
+
+// Whether the path takes these types and flags.
+bool bwd_tc_applies(csa2_dtype q_dt, csa2_dtype kv_dt, int k, csa2_dtype swa_dt, int window, csa2_dtype out_dt,
+                    unsigned flags);
+// Key splits of `queries` (times head passes) of n_slots slots each.
+void bwd_tc_splits(int num_sms, int64_t queries, int n_slots, int* n_split, int* tps);
+size_t bwd_tc_image_bytes();
+// Images, products and dq of a chunk (c.rank .. c.part filled in by the caller).
+csa2_status bwd_tc_chunk(csa2_ctx* ctx, BwdTcArgs& a, const void* dout, uint8_t* img, cudaStream_t s);

@@ -194,7 +194,3 @@ struct BwdChunk {
     void* part;
     void* dq;                 // [n_bq, H, 512] in q_dt
 };
-
-// Tensor-core path (attn_bwd_tc.cu): bf16 query, rows, window and dout, both RMSNorms.
-bool bwd_tc_applies(csa2_dtype q_dt, csa2_dtype kv_dt, int k, csa2_dtype swa_dt, int window, csa2_dtype out_dt,
-                    unsigned flags);

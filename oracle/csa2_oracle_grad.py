@@ -49,13 +49,15 @@ def attn_bwd(q, kv, sel, swa, swa_pos0: int, q_pos, sink, window: int, out, lse,
              flags: int = O.QNORM | O.KVNORM | O.ROPE, base=O.ROPE_BASE):
     """Gradients of one sequence: q, out, dout [Q, H, c], kv [N, c], sel: per query the entry
     ids (-1 = none), swa [cap, c], q_pos [Q], sink [H] or None, lse [Q, H].  Returns
-    (dq, dkv, dswa, dsink)."""
+    (dq, dkv, dswa, dsink), and the root sums of squares of the terms that dq, dkv and dswa
+    are sums of (what independent relative errors of the terms add up by)."""
     q, dout, out = (np.asarray(x, dtype=np.float64) for x in (q, dout, out))
     kv, swa = np.asarray(kv, dtype=np.float64), np.asarray(swa, dtype=np.float64)
     Q, H, c = q.shape
     dq = np.zeros_like(q)
     gk, gw = np.zeros_like(kv), np.zeros_like(swa)          # of the normalised rows
     dsink = np.zeros(H)
+    tq, tk, tw = np.zeros_like(q), np.zeros_like(kv), np.zeros_like(swa)
     for i in range(Q):
         t = int(q_pos[i])
         rows = key_rows(kv.shape[0], sel[i], swa.shape[0], swa_pos0, t, window)
@@ -73,11 +75,30 @@ def attn_bwd(q, kv, sel, swa, swa_pos0: int, q_pos, sink, window: int, out, lse,
         if flags & O.ROPE:
             g = O.rope(g, t, inverse=True, base=base)
         dq[i] = rms_norm_bwd(q[i], g) if flags & O.QNORM else g
-        for (w, j), r in zip(rows, dS.T @ qh + p.T @ do):
+        # dP is itself a sum whose rotated channels may be rounded: p times its root sum of squares
+        # there counts with dS (dS is small where dP comes close to D, that rounding is not)
+        d2 = dS ** 2 + p ** 2 * (do[:, -O.ROPE_DIMS:] ** 2 @ (K[:, -O.ROPE_DIMS:] ** 2).T) / c
+        # (a norm's projection takes the same errors along its direction from every channel)
+        along_q, along_do = (qh @ K.T / c) ** 2, (do @ K.T / c) ** 2
+        # (and the rotation back mixes the two channels of a pair)
+        tq[i] = d2 @ K ** 2
+        if flags & O.ROPE:
+            pair = tq[i][:, -O.ROPE_DIMS::2] + tq[i][:, -O.ROPE_DIMS + 1::2]
+            tq[i][:, -O.ROPE_DIMS::2] = tq[i][:, -O.ROPE_DIMS + 1::2] = pair
+        if flags & O.QNORM:
+            tq[i] += O.rms_norm(q[i]) ** 2 * (d2 * along_q).sum(axis=1, keepdims=True)
+            tq[i] /= np.mean(q[i] ** 2, axis=-1, keepdims=True) + O.RMS_EPS
+        squares = d2.T @ qh ** 2 + (p ** 2).T @ do ** 2
+        if flags & O.KVNORM:
+            squares += K ** 2 * (d2 * along_q + p ** 2 * along_do).sum(axis=0)[:, None]
+        for (w, j), r, r2 in zip(rows, dS.T @ qh + p.T @ do, squares):
             (gk if w == "kv" else gw)[j] += r
+            (tk if w == "kv" else tw)[j] += r2
+    tq, tk, tw = np.sqrt(tq), np.sqrt(tk), np.sqrt(tw)
     if flags & O.KVNORM:
         gk, gw = rms_norm_bwd(kv, gk), rms_norm_bwd(swa, gw)
-    return dq, gk, gw, dsink
+        tk, tw = (t / np.sqrt(np.mean(x * x, axis=-1, keepdims=True) + O.RMS_EPS) for t, x in ((tk, kv), (tw, swa)))
+    return (dq, gk, gw, dsink), (tq, tk, tw)
 
 
 def attn_mass(q, kv, sel, q_pos, lse, flags: int = O.QNORM | O.KVNORM | O.ROPE, base=O.ROPE_BASE):

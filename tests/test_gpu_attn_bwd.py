@@ -8,11 +8,17 @@ Tolerances, as |g - o| <= tol (|o| + rms(o)):
     23 * 2^-22, so p by 6e-6; 1e-4 as for the forward pass.
   * the same path with bf16 inputs and outputs: one rounding of the result more, at most 2^-8 of
     |o| (8 significant bits).
-  * tensor-core path: q^, p r, dS r and a row's contribution are each rounded to bf16 (at most
-    2^-8 of their value, 2^-8 * 0.42 = 1.65e-3 rms over a uniform mantissa), and q^'s rounding
-    moves a logit, and so p, by about 1.65e-3 of a logit of order one.  Four such independent
-    errors are 3.3e-3 of the rms; the largest of up to 1e6 elements is six times that, 2e-2,
-    and the result's own rounding adds 4e-3: 2.5e-2."""
+  * tensor-core path: a gradient is a sum of terms dS k^, or dS q^ and p do'.  In each term p r (or
+    dS r) and the other factor are rounded to bf16, q^'s rounding moves the logit by as much as
+    one more rounding, and the terms' sum over a query's heads is rounded too: four independent
+    relative errors of at most 2^-8 each, 2^-8 * 0.42 = 1.65e-3 rms over a uniform mantissa, so
+    3.3e-3 of the root sum of squares T of the element's terms; the largest of 1e6 elements is
+    6.5 times that, 2.2e-2 T (a single term: at most 4 * 2^-8 = 1.6e-2 T).  do' is rounded in its
+    64 rotated channels only, which moves dP = do'.k^ by 1.65e-3 of the root sum of squares of
+    those 64 products; p / sqrt(c) times that enters T beside dS, because it does not shrink
+    where dP comes close to D (a peaked softmax).  The result's own rounding adds 2^-8 |o|.  T also holds what the
+    norms' projections make of the same errors, which is all there is where a channel of the
+    only key is near 0."""
 import numpy as np
 import pytest
 import torch
@@ -25,7 +31,7 @@ from tests.helpers import assert_close, to_np
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
-F32_TOL, BF16_TOL, TC_TOL = 1e-4, 1e-4 + 2.0 ** -8, 2.5e-2
+F32_TOL, BF16_TOL, TC_TOL = 1e-4, 1e-4 + 2.0 ** -8, "terms"
 
 
 def _case(seed, B, Q, H, N, k, window, cap, pos, dtype, n_pad=0, sink=True, dense=False, flags=C.ATTN_DEFAULT, scale=1.0):
@@ -78,13 +84,23 @@ def _oracle(s):
         parts.append(G.attn_bwd(to_np(s["q"][b]), to_np(s["kv"][b]), sel, to_np(s["swa"][b]), 0, to_np(s["q_pos"][b]),
                                 None if s["sink"] is None else to_np(s["sink"]), s["window"], to_np(s["out"][b]),
                                 to_np(s["lse"][b]), to_np(s["dout"][b]), s["flags"]))
-    return [np.stack([p[i] for p in parts]) for i in range(3)] + [sum(p[3] for p in parts)]
+    want = [np.stack([p[0][i] for p in parts]) for i in range(3)] + [sum(p[0][3] for p in parts)]
+    return want, [np.stack([p[1][i] for p in parts]) for i in range(3)]
 
 
-def _check(s, got, tol, sink_tol=1e-4):
-    want = _oracle(s)
-    for name, g, o, t in zip(("dq", "dkv", "dswa", "dsink"), got, want, (tol, tol, tol, sink_tol)):
-        assert_close(to_np(g.float()), o, t, name)
+def _check(s, got, tol):
+    want, terms = _oracle(s)
+    assert_close(to_np(got[3]), want[3], 1e-4, "dsink")
+    for name, g, o, t in zip(("dq", "dkv", "dswa"), got, want, terms):
+        g = to_np(g.float())
+        if tol != TC_TOL:
+            assert_close(g, o, tol, name)
+            continue
+        err, bound = np.abs(g - o), 2.2e-2 * t + 2.0 ** -8 * np.abs(o) + 1e-30
+        assert bool(np.isfinite(g).all()), name
+        worst = float((err / bound).max())
+        at = np.unravel_index(int((err / bound).argmax()), err.shape)
+        assert worst <= 1.0, f"{name}{at}: {worst:.2f} times the bound, {g[at]:.6g} for {o[at]:.6g} (T {t[at]:.3g})"
 
 
 @pytest.mark.parametrize("B,Q,H,N,k,window,cap,pos,n_pad", [
@@ -101,7 +117,7 @@ def test_fp32_path(B, Q, H, N, k, window, cap, pos, n_pad):
 
 
 @pytest.mark.parametrize("flags", [0, C.QNORM, C.KVNORM, C.ROPE, C.QNORM | C.KVNORM])
-@pytest.mark.parametrize("dtype,tol", [(torch.float32, F32_TOL), (torch.bfloat16, BF16_TOL)])
+@pytest.mark.parametrize("dtype,tol", [(torch.float32, F32_TOL), (torch.bfloat16, BF16_TOL)], ids=["f32", "bf16"])
 def test_flags(flags, dtype, tol):
     """Without both norms bf16 inputs run the fp32 path too (both norms alone: the tensor cores).
     Small values keep unnormalised logits of order one."""
@@ -252,5 +268,21 @@ def test_captured_and_on_another_stream():
     graph.replay()
     torch.cuda.synchronize()
     for a, b in zip(outs, _backward(s)):
+        assert torch.equal(a, b)
+    C.csa2_ctx_check()
+
+
+def test_expired_wait_is_reported_and_the_context_stays_usable():
+    """The image producer issues nothing: every role's bounded wait expires, the call reports a
+    timeout, and the next call is right."""
+    s = _forward(_case(22, 1, 2, 64, 200, 90, 20, 32, [[40, 41]], torch.bfloat16))
+    ref = _backward(s)
+    C.csa2_ctx_check()
+    C.csa2_ctx_test_stall_next(2_000_000)
+    _backward(s)
+    with pytest.raises(C.Csa2Error) as e:
+        C.csa2_ctx_check()
+    assert e.value.status == C.ERR_TIMEOUT
+    for a, b in zip(ref, _backward(s)):
         assert torch.equal(a, b)
     C.csa2_ctx_check()

@@ -46,7 +46,7 @@ def test_attention_gradients_match_differences(flags, sink):
         return float((run(q, kv, swa, z)[0] * dout).sum())
 
     out, lse = run(q, kv, swa, z)
-    dq, dkv, dswa, dsink = G.attn_bwd(q, kv, sel, swa, 1, pos, z, window, out, lse, dout, flags)
+    (dq, dkv, dswa, dsink), _ = G.attn_bwd(q, kv, sel, swa, 1, pos, z, window, out, lse, dout, flags)
     cases = [(dq, q, lambda x: loss(x, kv, swa, z)), (dkv, kv, lambda x: loss(q, x, swa, z)),
              (dswa, swa, lambda x: loss(q, kv, x, z))]
     if sink:
@@ -63,7 +63,7 @@ def test_query_without_keys_has_no_gradient():
     rng = np.random.default_rng(3)
     q, out = rng.standard_normal((1, 2, 64)), np.zeros((1, 2, 64))
     for lse in (np.full((1, 2), -np.inf), np.zeros((1, 2))):
-        g = G.attn_bwd(q, rng.standard_normal((4, 64)), np.array([[-1, -1]]), rng.standard_normal((3, 64)), 0, [-1], None,
+        g, _ = G.attn_bwd(q, rng.standard_normal((4, 64)), np.array([[-1, -1]]), rng.standard_normal((3, 64)), 0, [-1], None,
                        2, out, lse, rng.standard_normal((1, 2, 64)))
         assert all(not x.any() for x in g)
 
