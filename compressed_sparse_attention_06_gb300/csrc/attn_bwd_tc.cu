@@ -64,6 +64,8 @@ struct Item {
     int64_t bq;
     int q, pass, split;          // query within the chunk
     int kq, nw, n, t0, nt;       // cache slots, window slots, both; tiles t0 .. t0 + nt - 1
+    int64_t kv0, sw0;            // row ids of the sequence's first cache row and window row
+    int win0;                    // window row of the first window slot
 };
 
 __device__ __forceinline__ Item item_of(const BwdTcArgs& a, int64_t i) {
@@ -80,15 +82,45 @@ __device__ __forceinline__ Item item_of(const BwdTcArgs& a, int64_t i) {
     const int tiles = (r.n + BT_TILE - 1) / BT_TILE;
     r.t0 = r.split * a.tps;
     r.nt = max(0, min(tiles, r.t0 + a.tps) - r.t0);
+    const int64_t b = r.bq / a.c.slots.Q;
+    r.kv0 = b * a.c.slots.N;
+    r.sw0 = a.c.slots.n_kv + b * a.c.slots.swa_cap;
+    r.win0 = 0;
+    if (r.nw > 0) {
+        const int64_t w = (t - r.nw + 1 - a.c.slots.swa_pos0) % a.c.slots.swa_cap;
+        r.win0 = (int)(w < 0 ? w + a.c.slots.swa_cap : w);
+    }
     return r;
 }
 
-// Key slot of a tile position (the item's cache slots, then its window slots without the
-// positions before 0); -1 past the end.
-__device__ __forceinline__ int slot_of(const BwdTcArgs& a, const Item& it, int s) {
+// Row id (slot_row's) of position s of the item's slots -- its cache slots, then its window
+// slots without the positions before 0 -- and in *slot the slot's number; -1 if it is empty.
+__device__ __forceinline__ int64_t row_of(const BwdTcArgs& a, const Item& it, int s, int* slot) {
+    *slot = 0;
     if (s >= it.n) return -1;
-    return s < it.kq ? s : a.c.slots.k + (a.c.slots.window - it.nw) + (s - it.kq);
+    if (s < it.kq) {
+        *slot = s;
+        const int id = a.c.slots.dense_nv ? s : a.c.slots.idx[it.bq * a.c.slots.k + s];
+        return id >= 0 && id < a.c.slots.N ? it.kv0 + id : -1;
+    }
+    const int w = s - it.kq;
+    *slot = a.c.slots.k + (a.c.slots.window - it.nw) + w;
+    int64_t at = (int64_t)it.win0 + w;
+    if (at >= a.c.slots.swa_cap) at -= a.c.slots.swa_cap;
+    return it.sw0 + at;
 }
+
+// Position in a ring of n stages and the parity of its current round.
+struct Ring {
+    int i = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++i == n) {
+            i = 0;
+            ++round;
+        }
+    }
+};
 
 // Whether the phase with the given parity has completed, without waiting.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
@@ -273,8 +305,9 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
             constexpr uint32_t ID_DQ = idesc_f16_major(128, BT_H, true, true, false);
             constexpr uint32_t ID_DK = idesc_f16_major(128, BT_TILE, true, true, true);
             const uint32_t img = smem_u32(sImg), x0 = smem_u32(sX), dsp = smem_u32(sDsp);
-            int64_t g = 0;                           // tiles so far
+            uint32_t g = 0;                          // tiles so far
             int n = 0;                               // items with tiles so far
+            Ring xs, xq, dk;                         // X blocks of S and of dQ, dK accumulators
             bool ok = true;
             auto wait = [&](uint64_t* b, uint32_t par) {
                 ok = ok && mbar_wait(b, par, a.budget, a.c.slots.st);
@@ -285,49 +318,49 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
                 if (it.nt == 0) continue;
                 for (int tt = 0; tt < it.nt && ok; ++tt, ++g) {
                     const bool last = tt == it.nt - 1;
-                    if (g > 0 && !wait(sempty, (uint32_t)(g - 1) & 1)) break;
-                    for (int db = 0; db < 4 && ok; ++db) {
-                        const int64_t p = 4 * g + db;
-                        const int slot = (int)(p % X_RING);
+                    if (g > 0 && !wait(sempty, (g - 1) & 1)) break;
+                    for (int db = 0; db < 4; ++db) {
                         if (tt == 0 && !wait(&imgfull[db], n & 1)) break;
-                        if (!wait(&xfull[slot], (uint32_t)(p / X_RING) & 1)) break;
+                        if (!wait(&xfull[xs.i], xs.round & 1)) break;
                         tc_fence_after();
+                        const uint64_t da = sdesc_sw128(img + 2 * db * IMG_CHUNK), dx = sdesc_sw128(x0 + xs.i * X_BLOCK);
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk) {
-                            const int ch = kk >> 2;
-                            const uint32_t ko = (uint32_t)(kk & 3) * 32u;
-                            mma_ss(tmem + COL_S, sdesc_sw128(img + (2 * db + ch) * IMG_CHUNK + ko),
-                                   sdesc_sw128(x0 + slot * X_BLOCK + ch * X_CHUNK + ko), ID_S, (db | kk) != 0);
-                        }
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_ss(tmem + COL_S, da + (((kk >> 2) * IMG_CHUNK + (kk & 3) * 32) >> 4),
+                                   dx + (((kk >> 2) * X_CHUNK + (kk & 3) * 32) >> 4), ID_S, (db | kk) != 0);
+                        xs.next(X_RING);
                     }
                     if (!ok) break;
                     mma_commit(sfull);
-                    if (!wait(dspfull, (uint32_t)g & 1)) break;
+                    if (!wait(dspfull, g & 1)) break;
                     if (tt == 0 && n > 0 && !wait(dqempty, (n - 1) & 1)) break;
                     tc_fence_after();
+                    const uint64_t dds = sdesc_sw128(dsp);
                     for (int db = 0; db < 4; ++db) {
-                        const int slot = (int)((4 * g + db) % X_RING);
+                        const uint64_t dx = sdesc_sw128_mn(x0 + xq.i * X_BLOCK, X_CHUNK, 1024);
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            mma_ss(tmem + COL_DQ + db * BT_H, sdesc_sw128_mn(x0 + slot * X_BLOCK + ks * 2048, X_CHUNK, 1024),
-                                   sdesc_sw128(dsp + ks * 32), ID_DQ, tt > 0 || ks > 0);
-                        mma_commit(&xempty[slot]);
+                            mma_ss(tmem + COL_DQ + db * BT_H, dx + (ks * 2048 >> 4), dds + (ks * 32 >> 4), ID_DQ,
+                                   tt > 0 || ks > 0);
+                        mma_commit(&xempty[xq.i]);
+                        xq.next(X_RING);
                     }
                     if (last) mma_commit(dqfull);
+                    const uint64_t dsp_mn = sdesc_sw128_mn(dsp, 1024, 1024);
                     for (int db = 0; db < 4; ++db) {
-                        const int64_t p = 4 * g + db;
-                        const int reg = (int)(p % DK_RING);
-                        if (p >= DK_RING && !wait(&dkempty[reg], (uint32_t)(p / DK_RING - 1) & 1)) break;
+                        if (dk.round > 0 && !wait(&dkempty[dk.i], (dk.round - 1) & 1)) break;
                         tc_fence_after();
+                        const uint64_t da = sdesc_sw128_mn(img + 2 * db * IMG_CHUNK, IMG_CHUNK, 1024);
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks) {
                             // image rows 16 ks .. : q^ (even ks) or do' (odd) of heads 16 (ks / 2) ..
                             const uint32_t row = 16u * (ks >> 1) + (ks & 1 ? 64u : 0u);
-                            mma_ss(tmem + COL_DK + reg * BT_TILE, sdesc_sw128_mn(img + 2 * db * IMG_CHUNK + ks * 2048, IMG_CHUNK, 1024),
-                                   sdesc_sw128_mn(dsp + row * 128, 1024, 1024), ID_DK, ks > 0);
+                            mma_ss(tmem + COL_DK + dk.i * BT_TILE, da + (ks * 2048 >> 4), dsp_mn + (row * 128 >> 4), ID_DK,
+                                   ks > 0);
                         }
-                        mma_commit(&dkfull[reg]);
+                        mma_commit(&dkfull[dk.i]);
                         if (last) mma_commit(&imgempty[db]);
+                        dk.next(DK_RING);
                     }
                     if (!ok) break;
                     mma_commit(dspempty);
@@ -346,7 +379,7 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
         const uint32_t lane_base = (uint32_t)(qd * 32) << 16;
         float* rv = reinterpret_cast<float*>(smem + OFF_RINV) + qd * 72;
         const float isc = 1.0f / sqrtf((float)BT_C);
-        int64_t g = 0;
+        uint32_t g = 0;
         bool ok = true;
         for (int64_t i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
             const Item it = item_of(a, i);
@@ -364,12 +397,12 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
                 // RMS factors of the tile's rows, 0 for empty slots (this warp's copy)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const int s = slot_of(a, it, (it.t0 + tt) * BT_TILE + 32 * j + lane);
-                    const int64_t row = s >= 0 ? slot_row(a.c.slots, it.bq, s, false) : -1;
+                    int slot;
+                    const int64_t row = row_of(a, it, (it.t0 + tt) * BT_TILE + 32 * j + lane, &slot);
                     rv[36 * j + lane] = row >= 0 ? a.c.rinv[row] : 0.0f;
                 }
                 __syncwarp();
-                bool w = mbar_wait(sfull, (uint32_t)g & 1, a.budget, a.c.slots.st);
+                bool w = mbar_wait(sfull, g & 1, a.budget, a.c.slots.st);
                 if (!__all_sync(FULL, w)) {
                     ok = false;
                     break;
@@ -406,7 +439,7 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
                     pp[2 * c4] = ag_pack_bf16x2(pv[0], pv[1]);
                     pp[2 * c4 + 1] = ag_pack_bf16x2(pv[2], pv[3]);
                 }
-                if (g > 0) w = mbar_wait(dspempty, (uint32_t)(g - 1) & 1, a.budget, a.c.slots.st);
+                if (g > 0) w = mbar_wait(dspempty, (g - 1) & 1, a.budget, a.c.slots.st);
                 if (!__all_sync(FULL, w)) {
                     ok = false;
                     break;
@@ -430,11 +463,11 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
         const int half = lane >> 4, piece = lane & 15;        // a copy moves 256 bytes of two rows
         const uint8_t* kv = reinterpret_cast<const uint8_t*>(a.c.kv);
         const uint8_t* swa = reinterpret_cast<const uint8_t*>(a.c.swa);
-        int64_t p = 0, done = 0;                              // blocks issued, blocks signalled
+        Ring in, out;                                         // blocks issued, blocks signalled
+        int behind = 0;                                       // in flight: issued, not signalled
         bool ok = true;
-        auto signal = [&]() {                                 // the oldest block still in flight
-            const int64_t behind = p - done;
-            if (behind > 3)
+        auto signal = [&]() {                                 // the oldest block in flight
+            if (behind == 4)
                 cp_async_wait<3>();
             else if (behind == 3)
                 cp_async_wait<2>();
@@ -444,14 +477,15 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
                 cp_async_wait<0>();
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&xfull[done % X_RING]);
-            ++done;
+            if (lane == 0) mbar_arrive(&xfull[out.i]);
+            out.next(X_RING);
+            --behind;
         };
         for (int64_t i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
             const Item it = item_of(a, i);
             for (int tt = 0; tt < it.nt && ok; ++tt) {
-                const int s = lane < 16 ? slot_of(a, it, (it.t0 + tt) * BT_TILE + 16 * lw + lane) : -1;
-                const int64_t row = s >= 0 ? slot_row(a.c.slots, it.bq, s, false) : -1;
+                int slot;
+                const int64_t row = lane < 16 ? row_of(a, it, (it.t0 + tt) * BT_TILE + 16 * lw + lane, &slot) : -1;
                 const uint8_t* src = nullptr;
                 if (row >= 0)
                     src = row < a.c.slots.n_kv ? kv + row * (BT_C * 2) : swa + (row - a.c.slots.n_kv) * (BT_C * 2);
@@ -460,21 +494,20 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
                 for (int j = 0; j < 8; ++j)
                     from[j] = reinterpret_cast<const uint8_t*>(
                         (uintptr_t)__shfl_sync(FULL, (unsigned long long)(uintptr_t)src, 2 * j + half));
-                for (int db = 0; db < 4; ++db, ++p) {
-                    const int slot = (int)(p % X_RING);
-                    if (p >= X_RING) {
-                        const uint32_t par = (uint32_t)(p / X_RING - 1) & 1;
+                for (int db = 0; db < 4; ++db) {
+                    if (in.round > 0) {
+                        const uint32_t par = (in.round - 1) & 1;
                         // blocks in flight are signalled before a wait that they may be needed for
-                        if (!__all_sync(FULL, mbar_test(&xempty[slot], par))) {
-                            while (done < p) signal();
-                            const bool w = mbar_wait(&xempty[slot], par, a.budget, a.c.slots.st);
+                        if (!__all_sync(FULL, mbar_test(&xempty[in.i], par))) {
+                            while (behind > 0) signal();
+                            const bool w = mbar_wait(&xempty[in.i], par, a.budget, a.c.slots.st);
                             if (!__all_sync(FULL, w)) {
                                 ok = false;
                                 break;
                             }
                         }
                     }
-                    uint8_t* dst = sX + slot * X_BLOCK + (piece >> 3) * X_CHUNK;
+                    uint8_t* dst = sX + in.i * X_BLOCK + (piece >> 3) * X_CHUNK;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         uint8_t* d = dst + sw128_offset((uint32_t)(16 * lw + 2 * j + half), (uint32_t)(piece & 7));
@@ -484,27 +517,24 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
                             *reinterpret_cast<uint4*>(d) = make_uint4(0u, 0u, 0u, 0u);
                     }
                     cp_async_commit();
-                    // three blocks stay in flight
-                    if (p + 1 - done > 3) {
-                        cp_async_wait<3>();
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&xfull[done % X_RING]);
-                        ++done;
-                    }
+                    in.next(X_RING);
+                    if (++behind > 3) signal();               // three blocks stay in flight
                 }
             }
         }
-        while (ok && done < p) signal();
+        while (ok && behind > 0) signal();
         cp_async_wait_all();
     } else {
         // ============================ drain ============================
         const int qd = warp & 3;
         const uint32_t lane_base = (uint32_t)(qd * 32) << 16;
-        const bool odd = lane & 1;
-        const int d0 = 32 * qd + (lane & ~1);                 // the two dims of a 128-dim block this lane stores
-        uint32_t* part = reinterpret_cast<uint32_t*>(a.c.part);
-        int64_t p = 0;
+        // after the exchanges below lane l stores 8 dims (its group of 8 lanes') of the slots
+        // s = 8 (l & 7 with its three bits reversed) .. + 7 of the tile
+        const int sg = ((lane & 1) << 2) | (lane & 2) | ((lane & 4) >> 2);
+        const int d0 = 32 * qd + (lane & 24);
+        uint8_t* part = reinterpret_cast<uint8_t*>(a.c.part);
+        const uint32_t row_bytes = (uint32_t)a.n_pass * BT_C * 2;
+        Ring dk;
         int n = 0;
         bool ok = true;
         for (int64_t i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
@@ -514,48 +544,67 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
                 for (int k = 0; k < BT_H * 4; ++k) dqh[(k >> 2) * BT_C + (k & 3) * 128] = 0.0f;
                 continue;
             }
+            uint8_t* base = part + it.pass * (BT_C * 2) + d0 * 2;
             for (int tt = 0; tt < it.nt && ok; ++tt) {
-                // places of the tile's slots: pl2[j] has those of slots 16 j .. in lanes 0-15 and
-                // of slots 32 + 16 j .. in lanes 16-31
+                // places of the tile's slots: slot s in register s >> 5 of lane s & 31
                 int pl2[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const int s = slot_of(a, it, (it.t0 + tt) * BT_TILE + 16 * j + (lane & 15) + (lane & 16 ? 32 : 0));
-                    int pl = -1;
-                    if (s >= 0) {
-                        const int32_t rk = a.c.rank[(int64_t)it.q * a.c.n_slots + s];
-                        if (rk >= 0) {
-                            const int64_t row = slot_row(a.c.slots, it.bq, s, false);
-                            pl = (int)(a.c.blk[row >> 10] + a.c.base[(int64_t)(it.q / a.c.group_q) * a.c.rows + row] + rk);
-                        }
-                    }
+                    int slot, pl = -1;
+                    const int64_t row = row_of(a, it, (it.t0 + tt) * BT_TILE + 32 * j + lane, &slot);
+                    if (row >= 0)
+                        pl = (int)(a.c.blk[row >> 10] + a.c.base[(int64_t)(it.q / a.c.group_q) * a.c.rows + row]) +
+                             a.c.rank[(int64_t)it.q * a.c.n_slots + slot];
                     pl2[j] = pl;
                 }
-                for (int db = 0; db < 4; ++db, ++p) {
-                    const int reg = (int)(p % DK_RING);
-                    const bool w = mbar_wait(&dkfull[reg], (uint32_t)(p / DK_RING) & 1, a.budget, a.c.slots.st);
+                for (int db = 0; db < 4; ++db) {
+                    const bool w = mbar_wait(&dkfull[dk.i], dk.round & 1, a.budget, a.c.slots.st);
                     if (!__all_sync(FULL, w)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     uint32_t lo[32], hi[32];
-                    tmem_ld32(tmem + lane_base + COL_DK + reg * BT_TILE, lo);
-                    tmem_ld32(tmem + lane_base + COL_DK + reg * BT_TILE + 32, hi);
+                    tmem_ld32(tmem + lane_base + COL_DK + dk.i * BT_TILE, lo);
+                    tmem_ld32(tmem + lane_base + COL_DK + dk.i * BT_TILE + 32, hi);
                     tmem_wait_ld();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&dkempty[reg]);
-                    // lane = dim, columns = slots: adjacent lanes swap halves, so that an even lane
-                    // stores dims (d, d + 1) of slots 0 .. 31 and an odd lane those of 32 .. 63
-                    const int64_t dim = (db * 128 + d0) >> 1;
+                    if (lane == 0) mbar_arrive(&dkempty[dk.i]);
+                    dk.next(DK_RING);
+                    // lane = dim, registers = slots -> 16-byte stores of 8 dims: lanes one, two and
+                    // four apart swap the halves they do not keep (as bf16 pairs from the first
+                    // swap on)
+                    uint32_t u[32], v[16][2], x[8][4];
+                    const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
 #pragma unroll
-                    for (int s = 0; s < 32; ++s) {
-                        const float keep = __uint_as_float(odd ? hi[s] : lo[s]);
-                        const float got = __uint_as_float(__shfl_xor_sync(FULL, odd ? lo[s] : hi[s], 1));
-                        const int pl = __shfl_sync(FULL, pl2[s >> 4], (odd ? 16 : 0) + (s & 15));
-                        const uint32_t v = odd ? ag_pack_bf16x2(got, keep) : ag_pack_bf16x2(keep, got);
-                        if (pl >= 0) part[((int64_t)pl * a.n_pass + it.pass) * (BT_C / 2) + dim] = v;
+                    for (int k = 0; k < 32; ++k) {            // slots k (even lanes), 32 + k (odd)
+                        const uint32_t keep = b0 ? hi[k] : lo[k], got = __shfl_xor_sync(FULL, b0 ? lo[k] : hi[k], 1);
+                        u[k] = ag_pack_bf16x2(__uint_as_float(b0 ? got : keep), __uint_as_float(b0 ? keep : got));
+                    }
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const uint32_t keep = b1 ? u[16 + k] : u[k], got = __shfl_xor_sync(FULL, b1 ? u[k] : u[16 + k], 2);
+                        v[k][0] = b1 ? got : keep;
+                        v[k][1] = b1 ? keep : got;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t keep = b2 ? v[8 + k][e] : v[k][e];
+                            const uint32_t got = __shfl_xor_sync(FULL, b2 ? v[k][e] : v[8 + k][e], 4);
+                            x[k][e] = b2 ? got : keep;
+                            x[k][2 + e] = b2 ? keep : got;
+                        }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int slot = 8 * sg + k;
+                        const int p0 = __shfl_sync(FULL, pl2[0], slot & 31), p1 = __shfl_sync(FULL, pl2[1], slot & 31);
+                        const int pl = slot & 32 ? p1 : p0;
+                        if (pl >= 0)
+                            *reinterpret_cast<uint4*>(base + (uint64_t)(uint32_t)pl * row_bytes + db * 256) =
+                                make_uint4(x[k][0], x[k][1], x[k][2], x[k][3]);
                     }
                 }
             }
