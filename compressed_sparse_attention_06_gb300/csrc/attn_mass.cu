@@ -11,31 +11,18 @@
 #include <algorithm>
 #include <atomic>
 
-#include "attn_grad.cuh"
+#include "attn_mass.cuh"
 
 namespace {
 
 constexpr int MS_KC = 32;
-constexpr float FIX_ONE = 549755813888.0f;          // 2^39
-constexpr float FIX_MAX = 256.0f;
-
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
-// One addend of an entry.  A weight that no softmax gives (an lse that is not the
-// forward's, NaN) is added as it is, so that acc shows it.
-__device__ __forceinline__ void add_mass(float* acc, unsigned long long* fix, int64_t at, float w) {
-    if (fix && w >= 0.0f && w <= FIX_MAX) {
-        if (w > 0.0f) atomicAdd(fix + at, (unsigned long long)__float2ull_rn(w * FIX_ONE));
-    } else {
-        atomicAdd(acc + at, w);
-    }
-}
 
 __global__ void __launch_bounds__(256) mass_finish_kernel(const unsigned long long* fix, float* acc, int64_t n) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n) return;
     const unsigned long long v = fix[i];
-    if (v) acc[i] += __ull2float_rn(v) * (1.0f / FIX_ONE);
+    if (v) acc[i] += __ull2float_rn(v) * (1.0f / MASS_FIX_ONE);
 }
 
 // q^ of every (query, head) in fp32; a warp per head row.
@@ -58,17 +45,6 @@ __global__ void __launch_bounds__(256) mass_prep_kernel(const TQ* q, const int64
     if (flags & CSA2_ROPE) ag_rope16(v, lane, cs[w], sn[w], 1.0f);
     ag_store16<float>(qh + r * AG_C + 16 * lane, v);
 }
-
-struct MassArgs {
-    SlotArgs slots;
-    const void* kv;
-    int kv_dt;
-    const float *qh, *lse;
-    int H;
-    unsigned flags;
-    float *weights, *acc;
-    unsigned long long* fix;
-};
 
 // CUDA-core path (fp32): a CTA per (32 slots, query), rows staged in fp32, a warp per head
 // in turn.
@@ -128,23 +104,45 @@ __global__ void __launch_bounds__(256, 2) mass_simt_kernel(MassArgs a) {
 
 constexpr size_t MS_SMEM = (size_t)MS_KC * AG_C * 4 + 8 * 32 * 4 + MS_KC * 8;
 
+csa2_status simt_run(const csa2_ctx* ctx, const MassArgs& a, cudaStream_t s) {
+    static std::atomic<uint64_t> done{0};
+    const uint64_t bit = 1ull << (ctx->device & 63);
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
+        CSA2_CHECK_CUDA(cudaFuncSetAttribute(mass_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)MS_SMEM));
+        done.fetch_or(bit, std::memory_order_relaxed);
+    }
+    const int64_t heads = a.n_bq * a.H;
+    const unsigned hb = (unsigned)((heads + 7) / 8);
+    float* qh = const_cast<float*>(a.qh);
+    if (a.q_dt == CSA2_F32)
+        mass_prep_kernel<float><<<hb, 256, 0, s>>>(reinterpret_cast<const float*>(a.q), a.slots.q_pos, heads, a.H, a.rope,
+                                                  a.flags, qh);
+    else
+        mass_prep_kernel<__nv_bfloat16><<<hb, 256, 0, s>>>(reinterpret_cast<const __nv_bfloat16*>(a.q), a.slots.q_pos,
+                                                          heads, a.H, a.rope, a.flags, qh);
+    mass_simt_kernel<<<dim3((unsigned)((a.slots.k + MS_KC - 1) / MS_KC), (unsigned)a.n_bq), 256, MS_SMEM, s>>>(a);
+    return csa2_launch_status();
+}
+
 struct MassLayout {
-    size_t qh, fix, total;
+    size_t qh, fix, passes, total;
 };
 
-MassLayout mass_layout(int B, int Q, int H, int64_t N, bool want_acc) {
+MassLayout mass_layout(csa2_dtype kv_dt, int B, int Q, int H, int k, int64_t N) {
     MassLayout L;
     L.qh = 0;
-    L.fix = align_up((size_t)B * Q * H * AG_C * 4, 256);
-    L.total = L.fix + (want_acc && Q > 1 ? (size_t)B * N * 8 : 0);
+    L.fix = kv_dt == CSA2_F32 ? align_up((size_t)B * Q * H * AG_C * 4, 256) : 0;
+    L.passes = align_up(L.fix + (Q > 1 ? (size_t)B * N * 8 : 0), 256);
+    L.total = L.passes + (H > 64 ? (size_t)B * Q * k * 4 : 0);
     return L;
 }
 
 }  // namespace
 
-extern "C" size_t csa2_attn_mass_workspace_bytes(csa2_ctx* ctx, int B, int Q, int H, int k, int64_t N) {
+extern "C" size_t csa2_attn_mass_workspace_bytes(csa2_ctx* ctx, csa2_dtype kv_dt, int B, int Q, int H, int k,
+                                                 int64_t N) {
     if (!ctx || B <= 0 || Q <= 0 || H < 1 || H > 128 || k < 0 || N < 0) return 0;
-    return mass_layout(B, Q, H, N, true).total;
+    return mass_layout(kv_dt, B, Q, H, k, N).total;
 }
 
 extern "C" csa2_status csa2_attn_mass(csa2_ctx* ctx, const void* q, csa2_dtype q_dt, const void* kv, csa2_dtype kv_dt,
@@ -165,22 +163,21 @@ extern "C" csa2_status csa2_attn_mass(csa2_ctx* ctx, const void* q, csa2_dtype q
     if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(ws, 16) || !aligned(lse, 4) || !aligned(q_pos, 8) ||
         !aligned(idx, 4) || !aligned(n_visible, 8) || !aligned(weights, 4) || !aligned(acc, 4))
         return CSA2_ERR_INVALID_ARG;
-    const MassLayout L = mass_layout(B, Q, H, N, acc != nullptr);
-    if (!ws || ws_bytes < L.total) return CSA2_ERR_INVALID_ARG;
+    const MassLayout L = mass_layout(kv_dt, B, Q, H, k, acc ? N : 0);
+    if (ws_bytes < L.total || (L.total > 0 && !ws)) return CSA2_ERR_INVALID_ARG;
     DeviceGuard dev(ctx);
     if (!dev.ok) return CSA2_ERR_CUDA;
     cudaStream_t s = as_stream(stream);
-    static std::atomic<uint64_t> done{0};
-    const uint64_t bit = 1ull << (ctx->device & 63);
-    if (!(done.load(std::memory_order_relaxed) & bit)) {
-        CSA2_CHECK_CUDA(cudaFuncSetAttribute(mass_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)MS_SMEM));
-        done.fetch_or(bit, std::memory_order_relaxed);
-    }
     uint8_t* base = reinterpret_cast<uint8_t*>(ws);
     MassArgs a;
     a.slots = {idx, n_visible, q_pos, N, 1, 0, k, 0, Q, (int64_t)B * N, ctx->status};
+    a.q = q;
+    a.q_dt = q_dt;
     a.kv = kv;
     a.kv_dt = kv_dt;
+    a.rope = make_rope_table(rope_base);
+    a.n_bq = (int64_t)B * Q;
+    a.passes = H > 64 && !weights ? reinterpret_cast<float*>(base + L.passes) : nullptr;
     a.qh = reinterpret_cast<const float*>(base + L.qh);
     a.lse = lse;
     a.H = H;
@@ -189,16 +186,8 @@ extern "C" csa2_status csa2_attn_mass(csa2_ctx* ctx, const void* q, csa2_dtype q
     a.acc = acc;
     a.fix = acc && Q > 1 ? reinterpret_cast<unsigned long long*>(base + L.fix) : nullptr;
     if (a.fix) CSA2_CHECK_CUDA(cudaMemsetAsync(a.fix, 0, (size_t)B * N * 8, s));
-    const int64_t heads = (int64_t)B * Q * H;
-    const unsigned hb = (unsigned)((heads + 7) / 8);
-    const RopeTable rope = make_rope_table(rope_base);
-    float* qh = reinterpret_cast<float*>(base + L.qh);
-    if (q_dt == CSA2_F32)
-        mass_prep_kernel<float><<<hb, 256, 0, s>>>(reinterpret_cast<const float*>(q), q_pos, heads, H, rope, flags, qh);
-    else
-        mass_prep_kernel<__nv_bfloat16><<<hb, 256, 0, s>>>(reinterpret_cast<const __nv_bfloat16*>(q), q_pos, heads, H,
-                                                          rope, flags, qh);
-    mass_simt_kernel<<<dim3((unsigned)((k + MS_KC - 1) / MS_KC), (unsigned)(B * Q)), 256, MS_SMEM, s>>>(a);
+    const csa2_status r = kv_dt == CSA2_F32 ? simt_run(ctx, a, s) : mass_tc_run(ctx, a, s);
+    if (r != CSA2_OK) return r;
     if (a.fix) {
         const int64_t n = (int64_t)B * N;
         mass_finish_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a.fix, acc, n);

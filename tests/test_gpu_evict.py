@@ -234,7 +234,7 @@ def test_mass_captured():
     idx = _idx(38, 1, 3, 400, 100)
     q_pos = torch.tensor([[5, 6, 7]], dtype=torch.int64, device=DEV)
     _, lse = C.csa2_sparse_attn(q, kv, idx, None, q_pos, None, window=0, want_lse=True)
-    ws = torch.empty(C._lib().csa2_attn_mass_workspace_bytes(C.ctx(0), 1, 3, 64, 100, 400), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(C._lib().csa2_attn_mass_workspace_bytes(C.ctx(0), C.FP4_E4M3x16, 1, 3, 64, 100, 400), dtype=torch.uint8, device=DEV)
     acc, ref = torch.zeros(1, 400, device=DEV), torch.zeros(1, 400, device=DEV)
     graph = torch.cuda.CUDAGraph()
     check, C._check = C._check, lambda fn, st: None if st == C.OK else (_ for _ in ()).throw(C.Csa2Error(fn, st))
@@ -248,3 +248,21 @@ def test_mass_captured():
         C.csa2_attn_mass(q, kv, q_pos, lse, idx=idx, acc=ref)
     torch.cuda.synchronize()
     assert torch.equal(acc, ref)
+
+
+def test_mass_expired_wait_is_reported_and_the_context_stays_usable():
+    kv, _ = _cache(39, 1, 300, "bf16")
+    q = W.normal_tensor((1, 1, 64, 512), 39, 1, torch.bfloat16, DEV)
+    idx = _idx(39, 1, 1, 300, 200)
+    q_pos = torch.zeros(1, 1, dtype=torch.int64, device=DEV)
+    _, lse = C.csa2_sparse_attn(q, kv, idx, None, q_pos, None, window=0, want_lse=True)
+    ref, _ = C.csa2_attn_mass(q, kv, q_pos, lse, idx=idx, want_weights=True)
+    C.csa2_ctx_check()
+    C.csa2_ctx_test_stall_next(2_000_000)
+    C.csa2_attn_mass(q, kv, q_pos, lse, idx=idx, want_weights=True)
+    with pytest.raises(C.Csa2Error) as e:
+        C.csa2_ctx_check()
+    assert e.value.status == C.ERR_TIMEOUT
+    w, _ = C.csa2_attn_mass(q, kv, q_pos, lse, idx=idx, want_weights=True)
+    C.csa2_ctx_check()
+    assert torch.equal(w, ref)

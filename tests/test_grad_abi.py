@@ -56,7 +56,8 @@ def test_dense_backward_refuses(lib, ctx):
     (dict(ctx=None), BAD), (dict(k=2049), BAD), (dict(H=129), BAD), (dict(c=128), UNS), (dict(flags=16), BAD),
     (dict(kv_dt=C.MXFP4_E8M0x32), UNS), (dict(q_dt=2), UNS), (dict(weights=None, acc=None), BAD), (dict(q=None), BAD),
     (dict(kv=None), BAD), (dict(lse=None), BAD), (dict(q_pos=None), BAD), (dict(nv=P), BAD), (dict(idx=None), BAD),
-    (dict(B=65536), UNS), (dict(kv=P + 8), BAD), (dict(ws_bytes=15), BAD), (dict(ws=None), BAD), (dict(N=-1), BAD),
+    (dict(B=65536), UNS), (dict(kv=P + 8), BAD), (dict(ws_bytes=799), BAD), (dict(ws=None, ws_bytes=800), BAD), (dict(N=-1), BAD),
+    (dict(Q=1, kv_dt=C.F32, ws_bytes=64 * 2048 - 1), BAD), (dict(Q=1, H=100, ws_bytes=63), BAD),
 ])
 def test_mass_refuses(lib, ctx, kw, want):
     a = dict(ctx=ctx, q=P, q_dt=C.BF16, kv=P, kv_dt=C.BF16, N=100, idx=P, nv=None, k=16, q_pos=P, lse=P, B=1, Q=4, H=64,
@@ -108,7 +109,7 @@ def test_workspace_sizes(lib, ctx):
     big = lib.csa2_attn_bwd_workspace_bytes(ctx, C.F32, C.F32, C.F32, C.F32, 1, 65535, 128, 2048, 1024, 34816, 70000, 7)
     assert big <= 16 << 30
     assert lib.csa2_attn_bwd_workspace_bytes(None, 1, 1, 1, 1, 1, 4, 64, 512, 128, 2048, 128, 7) == 0
-    assert lib.csa2_attn_mass_workspace_bytes(ctx, 8, 1, 64, 512, 1 << 20) < 1 << 24      # no per-entry table for Q = 1
+    assert lib.csa2_attn_mass_workspace_bytes(ctx, C.BF16, 8, 1, 64, 512, 1 << 20) == 0      # no per-entry table for Q = 1
     assert lib.csa2_compress_bwd_workspace_bytes(1, 8192, 512, 4, 1) > 0
     assert lib.csa2_compress_bwd_workspace_bytes(0, 8192, 512, 4, 1) == 0
 
