@@ -99,7 +99,7 @@ def _declare(lib):
         "csa2_compress_bwd_workspace_bytes": (_sz, [_i, _i64, _i, _i, _i]),
         "csa2_compress_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i64, _i, _i, _vp, _f, _u,
                                    _vp, _i, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
-        "csa2_attn_mass_workspace_bytes": (_sz, [_vp, _i, _i, _i, _i, _i, _i64]),
+        "csa2_attn_mass_workspace_bytes": (_sz, [_vp, _i, _i, _i, _i, _i, _i64, _i]),
         "csa2_attn_mass": (_i, [_vp, _vp, _i, _vp, _i, _i64, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _f, _u, _vp, _vp,
                                 _vp, _sz, _vp]),
         "csa2_evict_select": (_i, [_vp, _vp, _i, _i64, _vp, _i, _i, _vp, _vp]),
@@ -736,8 +736,7 @@ def csa2_attn_mass(q, kv, q_pos, lse, idx=None, n_visible=None, k_max: int = 0, 
     if want_weights or weights is not None:
         weights = _given("weights", weights, (B, Q, k), torch.float32, dev)
     if ws is None:
-        ws = _ws(_lib().csa2_attn_mass_workspace_bytes(ctx(dev.index), kv_dt, B, Q, H, k, N if acc is not None else 0),
-                 dev)
+        ws = _ws(_lib().csa2_attn_mass_workspace_bytes(ctx(dev.index), kv_dt, B, Q, H, k, N, int(acc is not None)), dev)
     st = _lib().csa2_attn_mass(ctx(dev.index), _p(q), _dt(q), _p(kv), kv_dt, N, _p(idx), _p(n_visible), k, _p(q_pos),
                                _p(lse), B, Q, H, c, rope_base, flags, _p(weights), _p(acc), _p(ws),
                                ws.numel() * ws.element_size(), _stream(q))

@@ -124,15 +124,30 @@ csa2_status simt_run(const csa2_ctx* ctx, const MassArgs& a, cudaStream_t s) {
     return csa2_launch_status();
 }
 
+// RMS factor of every bf16 row; a warp per row.
+__global__ void __launch_bounds__(256) mass_rinv_kernel(const __nv_bfloat16* kv, int64_t rows, float* rinv) {
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= rows) return;
+    float v[16];
+    ag_load16<__nv_bfloat16>(kv + row * AG_C + 16 * lane, v);
+    const float f = ag_rms_factor(warp_sum(ag_sumsq16(v)));
+    if (lane == 0) rinv[row] = f;
+}
+
 struct MassLayout {
-    size_t qh, fix, passes, total;
+    size_t qh, fix, rinv, passes, total;
+    bool table;
 };
 
-MassLayout mass_layout(csa2_dtype kv_dt, int B, int Q, int H, int k, int64_t N) {
+MassLayout mass_layout(csa2_dtype kv_dt, int B, int Q, int H, int k, int64_t N, bool want_acc) {
     MassLayout L;
+    // a table of RMS factors pays when every row is gathered several times (prefill)
+    L.table = kv_dt == CSA2_BF16 && (int64_t)Q * k >= 4 * N;
     L.qh = 0;
     L.fix = kv_dt == CSA2_F32 ? align_up((size_t)B * Q * H * AG_C * 4, 256) : 0;
-    L.passes = align_up(L.fix + (Q > 1 ? (size_t)B * N * 8 : 0), 256);
+    L.rinv = align_up(L.fix + (want_acc && Q > 1 ? (size_t)B * N * 8 : 0), 256);
+    L.passes = align_up(L.rinv + (L.table ? (size_t)B * N * 4 : 0), 256);
     L.total = L.passes + (H > 64 ? (size_t)B * Q * k * 4 : 0);
     return L;
 }
@@ -140,9 +155,9 @@ MassLayout mass_layout(csa2_dtype kv_dt, int B, int Q, int H, int k, int64_t N) 
 }  // namespace
 
 extern "C" size_t csa2_attn_mass_workspace_bytes(csa2_ctx* ctx, csa2_dtype kv_dt, int B, int Q, int H, int k,
-                                                 int64_t N) {
+                                                 int64_t N, int want_acc) {
     if (!ctx || B <= 0 || Q <= 0 || H < 1 || H > 128 || k < 0 || N < 0) return 0;
-    return mass_layout(kv_dt, B, Q, H, k, N).total;
+    return mass_layout(kv_dt, B, Q, H, k, N, want_acc != 0).total;
 }
 
 extern "C" csa2_status csa2_attn_mass(csa2_ctx* ctx, const void* q, csa2_dtype q_dt, const void* kv, csa2_dtype kv_dt,
@@ -163,7 +178,7 @@ extern "C" csa2_status csa2_attn_mass(csa2_ctx* ctx, const void* q, csa2_dtype q
     if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(ws, 16) || !aligned(lse, 4) || !aligned(q_pos, 8) ||
         !aligned(idx, 4) || !aligned(n_visible, 8) || !aligned(weights, 4) || !aligned(acc, 4))
         return CSA2_ERR_INVALID_ARG;
-    const MassLayout L = mass_layout(kv_dt, B, Q, H, k, acc ? N : 0);
+    const MassLayout L = mass_layout(kv_dt, B, Q, H, k, N, acc != nullptr);
     if (ws_bytes < L.total || (L.total > 0 && !ws)) return CSA2_ERR_INVALID_ARG;
     DeviceGuard dev(ctx);
     if (!dev.ok) return CSA2_ERR_CUDA;
@@ -186,6 +201,14 @@ extern "C" csa2_status csa2_attn_mass(csa2_ctx* ctx, const void* q, csa2_dtype q
     a.acc = acc;
     a.fix = acc && Q > 1 ? reinterpret_cast<unsigned long long*>(base + L.fix) : nullptr;
     if (a.fix) CSA2_CHECK_CUDA(cudaMemsetAsync(a.fix, 0, (size_t)B * N * 8, s));
+    a.rinv = nullptr;
+    if (L.table) {
+        float* t = reinterpret_cast<float*>(base + L.rinv);
+        const int64_t rows = (int64_t)B * N;
+        if (rows > 0)
+            mass_rinv_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(reinterpret_cast<const __nv_bfloat16*>(kv), rows, t);
+        a.rinv = t;
+    }
     const csa2_status r = kv_dt == CSA2_F32 ? simt_run(ctx, a, s) : mass_tc_run(ctx, a, s);
     if (r != CSA2_OK) return r;
     if (a.fix) {

@@ -16,6 +16,7 @@ struct MassArgs {
     int64_t n_bq;
     float *weights, *acc;     // either may be NULL
     unsigned long long* fix;  // addends of acc meet here in units of 2^-39, or NULL: straight to acc
+    const float* rinv;        // RMS factors of the bf16 rows, made once per call, or NULL: taken from the rows
     float* passes;            // [n_bq, k] weights summed over head passes (H > 64) if weights is NULL
 };
 

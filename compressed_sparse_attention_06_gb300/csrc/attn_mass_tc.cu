@@ -10,13 +10,16 @@
 // warps add the two partial logits, take exp(z - lse), and sum over the heads (a butterfly over
 // a warp's 16 heads, then the four warps).
 //
-// Bound by the MMAs: 32 a tile (1.27 us) for 128 KB of rows.
+// Bound by shared memory: the MMAs of a tile read 256 KB (32 at 39.5 ns would be 1.27 us), the
+// copies write 128 KB, 3,072 cycles of the 128-byte port (1.6 us).  So the rows' squares are not
+// taken from there when rows are gathered many times over: a table of RMS factors is made once.
 //
-// Warp roles (544 threads, one CTA per SM, persistent over items = (query, range of tiles)):
+// Warp roles (672 threads, one CTA per SM, persistent over items = (query, range of tiles)):
 //   warps 0-3    softmax: one thread per stacked row; owns one slot of the tile's result
 //   warp 4       MMA issuer; owns the tensor memory (a ring of four [128 x 128] accumulators)
-//   warps 5-8    image: norm, rotation, hi and lo of 16 heads each
-//   warps 9-16   loaders: bf16 rows by 16-byte cp.async, a warp 16 slots of every tile; FP4 rows a
+//   warps 5-12   image: norm, rotation, hi and lo of 8 heads each, loaded while the previous
+//                image is in use
+//   warps 13-20  loaders: bf16 rows by 16-byte cp.async, a warp 16 slots of every tile; FP4 rows a
 //                thread per slot, the two groups of four warps taking tiles in turn
 // Every wait is bounded; a wait that expires flags a timeout and the roles wind down.
 #include <algorithm>
@@ -33,7 +36,7 @@ using namespace sm100;
 constexpr int MT_C = 512;
 constexpr int MT_H = 64;
 constexpr int MT_TILE = 128;
-constexpr int MT_THREADS = 544;
+constexpr int MT_THREADS = 672;
 constexpr int CHUNK = 128 * 128;                 // 128 rows x 64 dims, image and tile alike
 constexpr int BLOCK = 2 * CHUNK;                 // 128 dims
 constexpr int X_RING = 3;
@@ -44,7 +47,7 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int OFF_IMG = 0;
 constexpr int OFF_X = OFF_IMG + 4 * BLOCK;
 constexpr int OFF_RINV = OFF_X + X_RING * BLOCK;         // [2][128] RMS factors, -1 = empty slot
-constexpr int OFF_RED = OFF_RINV + 2 * MT_TILE * 4;      // [4 owners][3 others][32] partial sums
+constexpr int OFF_RED = OFF_RINV + 2 * MT_TILE * 4;      // [4 owners][3 other warps][32] partial sums
 constexpr int OFF_BAR = OFF_RED + 4 * 3 * 32 * 4;
 constexpr int N_BAR = 2 + 2 * X_RING + 2 * S_RING + 4 + 2 + 1;
 constexpr int OFF_TMEMPTR = OFF_BAR + N_BAR * 8;
@@ -147,7 +150,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs
         return;
     }
     if (threadIdx.x == 0) {
-        mbar_init(imgfull, 4);
+        mbar_init(imgfull, 8);
         mbar_init(imgempty, 1);
         for (int i = 0; i < X_RING; ++i) {
             mbar_init(&xfull[i], FP4 ? 4 : 8);
@@ -208,17 +211,17 @@ __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs
                     }
                     tc_fence_after();
                     const float* rv = sRinv + rb * MT_TILE + (up ? 64 : 0);
-                    float part[2][2];                         // slots (up ? 64 : 0) + 32 b + 2 (lane & 15) + e
+                    float part[4];                            // slots (up ? 64 : 0) + 16 b + (lane & 15)
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        uint32_t lo[32], hi[32];
-                        tmem_ld32(tmem + lane_base + sr.i * MT_TILE + 32 * b, lo);
-                        tmem_ld32(tmem + lane_base + sr.i * MT_TILE + 64 + 32 * b, hi);
+                    for (int b = 0; b < 4; ++b) {
+                        uint32_t lo[16], hi[16];
+                        tmem_ld16(tmem + lane_base + sr.i * MT_TILE + 16 * b, lo);
+                        tmem_ld16(tmem + lane_base + sr.i * MT_TILE + 64 + 16 * b, hi);
                         tmem_wait_ld();
-                        float p[32];
+                        float p[16];
 #pragma unroll
-                        for (int c4 = 0; c4 < 8; ++c4) {
-                            const float4 r4 = *reinterpret_cast<const float4*>(rv + 32 * b + 4 * c4);
+                        for (int c4 = 0; c4 < 4; ++c4) {
+                            const float4 r4 = *reinterpret_cast<const float4*>(rv + 16 * b + 4 * c4);
                             const float rr[4] = {r4.x, r4.y, r4.z, r4.w};
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
@@ -228,18 +231,17 @@ __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs
                                 p[c] = count && rr[k] >= 0.0f ? ex2_approx(fmaf(z * rr[k], c1, -lse2)) : 0.0f;
                             }
                         }
-                        // sum over the warp's 16 heads
+                        // sum over the warp's 16 heads: every lane ends with one slot
 #pragma unroll
                         for (int d = 8; d >= 1; d >>= 1) {
                             const bool top = lane & d;
 #pragma unroll
-                            for (int k = 0; k < 2 * d; ++k) {
-                                const float send = top ? p[k] : p[k + 2 * d], keep = top ? p[k + 2 * d] : p[k];
+                            for (int k = 0; k < d; ++k) {
+                                const float send = top ? p[k] : p[k + d], keep = top ? p[k + d] : p[k];
                                 p[k] = keep + __shfl_xor_sync(FULL, send, d);
                             }
                         }
-                        part[b][0] = p[0];
-                        part[b][1] = p[1];
+                        part[b] = p[0];
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -258,14 +260,12 @@ __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs
                         }
                     }
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const int dest = (up ? 2 : 0) + b;
+                    for (int b = 0; b < 4; ++b) {
+                        const int dest = (up ? 2 : 0) + (b >> 1);
                         if (dest != warp)
-                            *reinterpret_cast<float2*>(sRed + (dest * 3 + (warp < dest ? warp : warp - 1)) * 32 +
-                                                       2 * (lane & 15)) = make_float2(part[b][0], part[b][1]);
-                        const int from = ((warp & 2) << 3) | (lane >> 1);
-                        const float v0 = __shfl_sync(FULL, part[b][0], from), v1 = __shfl_sync(FULL, part[b][1], from);
-                        if (b == (warp & 1)) mine = lane & 1 ? v1 : v0;
+                            sRed[(dest * 3 + (warp < dest ? warp : warp - 1)) * 32 + 16 * (b & 1) + (lane & 15)] = part[b];
+                        const float v = __shfl_sync(FULL, part[b], ((warp & 2) << 3) | (lane & 15));
+                        if (b == 2 * (warp & 1) + (lane >> 4)) mine = v;
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(redfull);
@@ -329,9 +329,12 @@ __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs
             mma_commit(alldone);
             mbar_wait(alldone, 0, a.budget, st);
         }
-    } else if (warp < 9) {
+    } else if (warp < 13) {
         // ============================ images ============================
         const int iw = warp - 5;
+        struct alignas(16) Raw {
+            TQ v[16];
+        };
         const TQ* q = reinterpret_cast<const TQ*>(a.m.q);
         int n = 0;
         bool ok = true;
@@ -344,16 +347,12 @@ __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs
 #pragma unroll
                 for (int j = 0; j < 8; ++j) rope_cos_sin(a.m.rope, t, 8 * (lane - 28) + j, cs[j], sn[j]);
             for (int pass = 0; pass < a.n_pass && ok; ++pass, ++n) {
-                // heads of this warp, two at a time with the next two's loads in flight
-                float v[2][16];
-                auto load = [&](int j, float (&x)[16]) {
-                    const int h = pass * MT_H + 16 * iw + j;
+                // this warp's 8 heads, loaded before the image is free
+                const int h0 = pass * MT_H + 8 * iw;
+                Raw raw[8];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) x[k] = 0.0f;
-                    if (h < a.m.H) ag_load16<TQ>(q + (it.bq * a.m.H + h) * (int64_t)MT_C + 16 * lane, x);
-                };
-                load(0, v[0]);
-                load(1, v[1]);
+                for (int j = 0; j < 8; ++j)
+                    if (h0 + j < a.m.H) raw[j] = *reinterpret_cast<const Raw*>(q + (it.bq * a.m.H + h0 + j) * (int64_t)MT_C + 16 * lane);
                 if (n > 0) {
                     const bool w = mbar_wait(imgempty, (n - 1) & 1, a.budget, st);
                     if (!__all_sync(FULL, w)) {
@@ -361,44 +360,40 @@ __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs
                         break;
                     }
                 }
-                for (int j = 0; j < 16; j += 2) {
-                    float nx[2][16];
-                    if (j + 2 < 16) {
-                        load(j + 2, nx[0]);
-                        load(j + 3, nx[1]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float v[16];
+                    if (h0 + j < a.m.H) {
+                        ag_load16<TQ>(reinterpret_cast<const TQ*>(&raw[j]), v);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) v[k] = 0.0f;
                     }
+                    float f = 1.0f;
+                    if (a.m.flags & CSA2_QNORM) f = ag_rms_factor(warp_sum(ag_sumsq16(v)));
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float f = 1.0f;
-                        if (a.m.flags & CSA2_QNORM) f = ag_rms_factor(warp_sum(ag_sumsq16(v[e])));
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) v[e][k] *= f;
-                        if ((a.m.flags & CSA2_ROPE) && lane >= 28)
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const float x0 = v[e][2 * k], x1 = v[e][2 * k + 1];
-                                v[e][2 * k] = x0 * cs[k] - x1 * sn[k];
-                                v[e][2 * k + 1] = x1 * cs[k] + x0 * sn[k];
-                            }
-                        uint32_t ph[8], pl[8];
+                    for (int k = 0; k < 16; ++k) v[k] *= f;
+                    if ((a.m.flags & CSA2_ROPE) && lane >= 28)
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            ph[k] = ag_pack_bf16x2(v[e][2 * k], v[e][2 * k + 1]);
-                            pl[k] = ag_pack_bf16x2(v[e][2 * k] - __uint_as_float(ph[k] << 16),
-                                                   v[e][2 * k + 1] - __uint_as_float(ph[k] & 0xFFFF0000u));
+                            const float x0 = v[2 * k], x1 = v[2 * k + 1];
+                            v[2 * k] = x0 * cs[k] - x1 * sn[k];
+                            v[2 * k + 1] = x1 * cs[k] + x0 * sn[k];
                         }
-                        uint8_t* c = sImg + (lane >> 2) * CHUNK;
-                        const uint32_t r = 32u * iw + j + e, u = 2u * (lane & 3);
-                        *reinterpret_cast<uint4*>(c + sw128_offset(r, u)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-                        *reinterpret_cast<uint4*>(c + sw128_offset(r, u + 1)) = make_uint4(ph[4], ph[5], ph[6], ph[7]);
-                        *reinterpret_cast<uint4*>(c + sw128_offset(r + 16, u)) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
-                        *reinterpret_cast<uint4*>(c + sw128_offset(r + 16, u + 1)) = make_uint4(pl[4], pl[5], pl[6], pl[7]);
-                    }
+                    uint32_t ph[8], pl[8];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        v[0][k] = nx[0][k];
-                        v[1][k] = nx[1][k];
+                    for (int k = 0; k < 8; ++k) {
+                        ph[k] = ag_pack_bf16x2(v[2 * k], v[2 * k + 1]);
+                        pl[k] = ag_pack_bf16x2(v[2 * k] - __uint_as_float(ph[k] << 16),
+                                               v[2 * k + 1] - __uint_as_float(ph[k] & 0xFFFF0000u));
                     }
+                    uint8_t* c = sImg + (lane >> 2) * CHUNK;
+                    const int hl = 8 * iw + j;
+                    const uint32_t r = 32u * (hl >> 4) + (hl & 15), u = 2u * (lane & 3);
+                    *reinterpret_cast<uint4*>(c + sw128_offset(r, u)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+                    *reinterpret_cast<uint4*>(c + sw128_offset(r, u + 1)) = make_uint4(ph[4], ph[5], ph[6], ph[7]);
+                    *reinterpret_cast<uint4*>(c + sw128_offset(r + 16, u)) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+                    *reinterpret_cast<uint4*>(c + sw128_offset(r + 16, u + 1)) = make_uint4(pl[4], pl[5], pl[6], pl[7]);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -407,7 +402,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs
         }
     } else if (FP4) {
         // ============================ loaders, FP4 rows ============================
-        const int lt = threadIdx.x - 288, grp = lt >> 7, r = lt & 127;
+        const int lt = threadIdx.x - 416, grp = lt >> 7, r = lt & 127;
         const uint8_t* kv = reinterpret_cast<const uint8_t*>(a.m.kv);
         Ring xr;
         uint32_t g = 0;
@@ -478,13 +473,14 @@ __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs
         }
     } else {
         // ============================ loaders, bf16 rows ============================
-        const int lw = warp - 9;                              // slots 16 lw .. 16 lw + 15 of the tile
+        const int lw = warp - 13;                             // slots 16 lw .. 16 lw + 15 of the tile
         const int half = lane >> 4, piece = lane & 15;        // a copy moves 256 bytes of two rows
         const uint8_t* kv = reinterpret_cast<const uint8_t*>(a.m.kv);
         Ring in, out;                                         // blocks issued, blocks signalled
         int behind = 0, odb = 0;                              // in flight; dim block of the oldest
         uint32_t og = 0, g = 0;                               // tile of the oldest, tiles issued
         unsigned live[2] = {0u, 0u};                          // valid slots of the last two tiles
+        float known[2] = {0.0f, 0.0f};                        // lanes 0-15: their RMS factors from the table
         float ss[8];
         bool ok = true;
 #pragma unroll
@@ -502,6 +498,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs
             // squares of the pieces this lane copied (before the block can be overwritten: the
             // ring comes back here only through this warp)
             const uint8_t* src = sX + out.i * BLOCK + (piece >> 3) * CHUNK;
+            if (!a.m.rinv)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint4 v = *reinterpret_cast<const uint4*>(
@@ -528,6 +525,9 @@ __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs
                 }
             }
             const unsigned lv = rb ? live[1] : live[0];
+            if (a.m.rinv) {
+                if (lane < 16) sRinv[rb * MT_TILE + 16 * lw + lane] = rb ? known[1] : known[0];
+            } else
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 float s = ss[j];
@@ -550,10 +550,14 @@ __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs
                 const int tt = tp % it.nt;
                 const int64_t row = lane < 16 ? row_of(a.m.slots, it, (it.t0 + tt) * MT_TILE + 16 * lw + lane, false) : -1;
                 const unsigned lv = __ballot_sync(FULL, row >= 0);
-                if (g & 1)
+                const float kn = !a.m.rinv || row < 0 ? -1.0f : (a.m.flags & CSA2_KVNORM) ? a.m.rinv[row] : 1.0f;
+                if (g & 1) {
                     live[1] = lv;
-                else
+                    known[1] = kn;
+                } else {
                     live[0] = lv;
+                    known[0] = kn;
+                }
                 const uint8_t* src = row >= 0 ? kv + row * (MT_C * 2) : nullptr;
                 const uint8_t* from[8];
 #pragma unroll

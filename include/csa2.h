@@ -583,14 +583,15 @@ csa2_status csa2_compress_bwd(csa2_ctx* ctx,
  *   k       : slots of a query: idx's row length (<= 2048), or an upper bound of n_visible
  *   lse     : [B, Q, H] f32 as the forward wrote it (-inf: the query counts nothing)
  *   weights : [B, Q, k] f32 or NULL;  acc: [B, N] f32, updated, or NULL (one is needed)
- *   ws      : csa2_attn_mass_workspace_bytes() bytes, 16-byte aligned (N = 0 there if acc is
- *             NULL; NULL if that is 0)
+ *   ws      : csa2_attn_mass_workspace_bytes() bytes, 16-byte aligned (want_acc: acc is
+ *             given; NULL will do if that is 0)
  * BF16 and FP4 rows run on the tensor cores, with q^ as the sum of two bf16 numbers (2^-17 of it
  * left out) and fp32 sums; F32 rows in fp32 on the CUDA cores.
  * The sums into acc do not depend on timing: with one query per sequence each entry gets
  * one addend; with more they meet as 64-bit integers in units of 2^-39 first.
  */
-size_t csa2_attn_mass_workspace_bytes(csa2_ctx* ctx, csa2_dtype kv_dt, int B, int Q, int H, int k, int64_t N);
+size_t csa2_attn_mass_workspace_bytes(csa2_ctx* ctx, csa2_dtype kv_dt, int B, int Q, int H, int k, int64_t N,
+                                      int want_acc);
 csa2_status csa2_attn_mass(csa2_ctx* ctx,
                            const void* q, csa2_dtype q_dt,
                            const void* kv, csa2_dtype kv_dt, int64_t N,

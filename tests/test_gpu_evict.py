@@ -234,7 +234,7 @@ def test_mass_captured():
     idx = _idx(38, 1, 3, 400, 100)
     q_pos = torch.tensor([[5, 6, 7]], dtype=torch.int64, device=DEV)
     _, lse = C.csa2_sparse_attn(q, kv, idx, None, q_pos, None, window=0, want_lse=True)
-    ws = torch.empty(C._lib().csa2_attn_mass_workspace_bytes(C.ctx(0), C.FP4_E4M3x16, 1, 3, 64, 100, 400), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(C._lib().csa2_attn_mass_workspace_bytes(C.ctx(0), C.FP4_E4M3x16, 1, 3, 64, 100, 400, 1), dtype=torch.uint8, device=DEV)
     acc, ref = torch.zeros(1, 400, device=DEV), torch.zeros(1, 400, device=DEV)
     graph = torch.cuda.CUDAGraph()
     check, C._check = C._check, lambda fn, st: None if st == C.OK else (_ for _ in ()).throw(C.Csa2Error(fn, st))

@@ -109,7 +109,7 @@ def test_workspace_sizes(lib, ctx):
     big = lib.csa2_attn_bwd_workspace_bytes(ctx, C.F32, C.F32, C.F32, C.F32, 1, 65535, 128, 2048, 1024, 34816, 70000, 7)
     assert big <= 16 << 30
     assert lib.csa2_attn_bwd_workspace_bytes(None, 1, 1, 1, 1, 1, 4, 64, 512, 128, 2048, 128, 7) == 0
-    assert lib.csa2_attn_mass_workspace_bytes(ctx, C.BF16, 8, 1, 64, 512, 1 << 20) == 0      # no per-entry table for Q = 1
+    assert lib.csa2_attn_mass_workspace_bytes(ctx, C.BF16, 8, 1, 64, 512, 1 << 20, 1) == 0      # no per-entry table for Q = 1
     assert lib.csa2_compress_bwd_workspace_bytes(1, 8192, 512, 4, 1) > 0
     assert lib.csa2_compress_bwd_workspace_bytes(0, 8192, 512, 4, 1) == 0
 
