@@ -122,6 +122,8 @@ __device__ __forceinline__ float ex2_approx(float x) {
     return y;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 template <typename TQ, bool FP4>
 __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -211,9 +213,16 @@ __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs
                     }
                     tc_fence_after();
                     const float* rv = sRinv + rb * MT_TILE + (up ? 64 : 0);
-                    float part[4];                            // slots (up ? 64 : 0) + 16 b + (lane & 15)
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
+                    if (g > 0) {
+                        w = mbar_wait(redempty, (g - 1) & 1, a.budget, st);
+                        if (!__all_sync(FULL, w)) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    float mine = 0.0f;
+#pragma unroll 1
+                    for (int b = 0; b < 4; ++b) {             // slots (up ? 64 : 0) + 16 b ..
                         uint32_t lo[16], hi[16];
                         tmem_ld16(tmem + lane_base + sr.i * MT_TILE + 16 * b, lo);
                         tmem_ld16(tmem + lane_base + sr.i * MT_TILE + 64 + 16 * b, hi);
@@ -231,7 +240,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs
                                 p[c] = count && rr[k] >= 0.0f ? ex2_approx(fmaf(z * rr[k], c1, -lse2)) : 0.0f;
                             }
                         }
-                        // sum over the warp's 16 heads: every lane ends with one slot
+                        // sum over the warp's 16 heads: every lane ends with one slot, 16 b + (lane & 15)
 #pragma unroll
                         for (int d = 8; d >= 1; d >>= 1) {
                             const bool top = lane & d;
@@ -241,7 +250,12 @@ __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs
                                 p[k] = keep + __shfl_xor_sync(FULL, send, d);
                             }
                         }
-                        part[b] = p[0];
+                        // the four warps' sums meet at the slot's owner
+                        const int dest = (up ? 2 : 0) + (b >> 1);
+                        if (dest != warp)
+                            sRed[(dest * 3 + (warp < dest ? warp : warp - 1)) * 32 + 16 * (b & 1) + (lane & 15)] = p[0];
+                        const float v = __shfl_sync(FULL, p[0], ((warp & 2) << 3) | (lane & 15));
+                        if (b == 2 * (warp & 1) + (lane >> 4)) mine = v;
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -250,23 +264,6 @@ __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs
                         mbar_arrive(&rempty[rb]);
                     }
                     sr.next(S_RING);
-                    // the four warps' sums meet at the slot's owner
-                    float mine = 0.0f;
-                    if (g > 0) {
-                        w = mbar_wait(redempty, (g - 1) & 1, a.budget, st);
-                        if (!__all_sync(FULL, w)) {
-                            ok = false;
-                            break;
-                        }
-                    }
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const int dest = (up ? 2 : 0) + (b >> 1);
-                        if (dest != warp)
-                            sRed[(dest * 3 + (warp < dest ? warp : warp - 1)) * 32 + 16 * (b & 1) + (lane & 15)] = part[b];
-                        const float v = __shfl_sync(FULL, part[b], ((warp & 2) << 3) | (lane & 15));
-                        if (b == 2 * (warp & 1) + (lane >> 4)) mine = v;
-                    }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(redfull);
                     w = mbar_wait(redfull, g & 1, a.budget, st);
@@ -332,9 +329,6 @@ __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs
     } else if (warp < 13) {
         // ============================ images ============================
         const int iw = warp - 5;
-        struct alignas(16) Raw {
-            TQ v[16];
-        };
         const TQ* q = reinterpret_cast<const TQ*>(a.m.q);
         int n = 0;
         bool ok = true;
@@ -342,17 +336,32 @@ __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs
             const Item it = item_of(a, i);
             if (it.nt == 0) continue;
             const int64_t t = a.m.slots.q_pos[it.bq];
-            float cs[8], sn[8];                               // lanes 28-31: the angles of their 8 pairs
-            if ((a.m.flags & CSA2_ROPE) && lane >= 28)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) rope_cos_sin(a.m.rope, t, 8 * (lane - 28) + j, cs[j], sn[j]);
+            float c1 = 1.0f, s1 = 0.0f;                       // lane j: angle j (64-bit arithmetic: one a lane)
+            if (a.m.flags & CSA2_ROPE) rope_cos_sin(a.m.rope, t, lane, c1, s1);
             for (int pass = 0; pass < a.n_pass && ok; ++pass, ++n) {
-                // this warp's 8 heads, loaded before the image is free
-                const int h0 = pass * MT_H + 8 * iw;
-                Raw raw[8];
+                // this warp's 8 heads, two at a time: half a warp a head, lane l its channels
+                // 16 (l & 15) + 256 e, e = 0, 1.  The first two are loaded, the others are on their
+                // way to L2, before the image is free.  (Kept small and not unrolled: a decode
+                // call runs it once, from a cold instruction cache.)
+                constexpr int NW = sizeof(TQ);                // 16-byte words of 16 channels, twice over / 2
+                const int sub = lane >> 4, l16 = lane & 15;
+                const int h0 = pass * MT_H + 8 * iw + sub;
+                uint4 nx[2][NW];
+                auto load = [&](int h) {
+                    const uint4* src = reinterpret_cast<const uint4*>(q + (it.bq * a.m.H + h) * (int64_t)MT_C + 16 * l16);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (h0 + j < a.m.H) raw[j] = *reinterpret_cast<const Raw*>(q + (it.bq * a.m.H + h0 + j) * (int64_t)MT_C + 16 * lane);
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int k = 0; k < NW; ++k)
+                            nx[e][k] = h < a.m.H ? src[e * 16 * NW + k] : make_uint4(0u, 0u, 0u, 0u);
+                };
+                load(h0);
+                for (int j = 2; j < 8; j += 2)
+                    if (h0 + j < a.m.H) {
+                        const TQ* src = q + (it.bq * a.m.H + h0 + j) * (int64_t)MT_C + 16 * l16;
+                        prefetch_l2(src);
+                        prefetch_l2(src + 256);
+                    }
                 if (n > 0) {
                     const bool w = mbar_wait(imgempty, (n - 1) & 1, a.budget, st);
                     if (!__all_sync(FULL, w)) {
@@ -360,40 +369,43 @@ __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs
                         break;
                     }
                 }
+#pragma unroll 1
+                for (int j = 0; j < 8; j += 2) {
+                    float v[2][16];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float v[16];
-                    if (h0 + j < a.m.H) {
-                        ag_load16<TQ>(reinterpret_cast<const TQ*>(&raw[j]), v);
-                    } else {
+                    for (int e = 0; e < 2; ++e) ag_load16<TQ>(reinterpret_cast<const TQ*>(nx[e]), v[e]);
+                    if (j < 6) load(h0 + j + 2);
+                    float f = ag_sumsq16(v[0]) + ag_sumsq16(v[1]);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) v[k] = 0.0f;
-                    }
-                    float f = 1.0f;
-                    if (a.m.flags & CSA2_QNORM) f = ag_rms_factor(warp_sum(ag_sumsq16(v)));
+                    for (int o = 8; o > 0; o >>= 1) f += __shfl_xor_sync(FULL, f, o);
+                    f = (a.m.flags & CSA2_QNORM) ? ag_rms_factor(f) : 1.0f;
+                    const int hl = 8 * iw + j + sub;
+                    const uint32_t r = 32u * (hl >> 4) + (hl & 15), u = 2u * (l16 & 3);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] *= f;
-                    if ((a.m.flags & CSA2_ROPE) && lane >= 28)
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t ph[8], pl[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            const float x0 = v[2 * k], x1 = v[2 * k + 1];
-                            v[2 * k] = x0 * cs[k] - x1 * sn[k];
-                            v[2 * k + 1] = x1 * cs[k] + x0 * sn[k];
+                            float x0 = v[e][2 * k] * f, x1 = v[e][2 * k + 1] * f;
+                            if (e == 1) {                     // lanes l16 = 12 .. 15: channels 448 .. 511, pair 8 (l16 - 12) + k
+                                const float c = __shfl_sync(FULL, c1, (8 * l16 + k) & 31);
+                                const float s = __shfl_sync(FULL, s1, (8 * l16 + k) & 31);
+                                if (l16 >= 12) {
+                                    const float y0 = x0 * c - x1 * s;
+                                    x1 = x1 * c + x0 * s;
+                                    x0 = y0;
+                                }
+                            }
+                            ph[k] = ag_pack_bf16x2(x0, x1);
+                            pl[k] = ag_pack_bf16x2(x0 - __uint_as_float(ph[k] << 16),
+                                                   x1 - __uint_as_float(ph[k] & 0xFFFF0000u));
                         }
-                    uint32_t ph[8], pl[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        ph[k] = ag_pack_bf16x2(v[2 * k], v[2 * k + 1]);
-                        pl[k] = ag_pack_bf16x2(v[2 * k] - __uint_as_float(ph[k] << 16),
-                                               v[2 * k + 1] - __uint_as_float(ph[k] & 0xFFFF0000u));
+                        uint8_t* c = sImg + ((l16 >> 2) + 4 * e) * CHUNK;
+                        *reinterpret_cast<uint4*>(c + sw128_offset(r, u)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+                        *reinterpret_cast<uint4*>(c + sw128_offset(r, u + 1)) = make_uint4(ph[4], ph[5], ph[6], ph[7]);
+                        *reinterpret_cast<uint4*>(c + sw128_offset(r + 16, u)) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+                        *reinterpret_cast<uint4*>(c + sw128_offset(r + 16, u + 1)) = make_uint4(pl[4], pl[5], pl[6], pl[7]);
                     }
-                    uint8_t* c = sImg + (lane >> 2) * CHUNK;
-                    const int hl = 8 * iw + j;
-                    const uint32_t r = 32u * (hl >> 4) + (hl & 15), u = 2u * (lane & 3);
-                    *reinterpret_cast<uint4*>(c + sw128_offset(r, u)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-                    *reinterpret_cast<uint4*>(c + sw128_offset(r, u + 1)) = make_uint4(ph[4], ph[5], ph[6], ph[7]);
-                    *reinterpret_cast<uint4*>(c + sw128_offset(r + 16, u)) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
-                    *reinterpret_cast<uint4*>(c + sw128_offset(r + 16, u + 1)) = make_uint4(pl[4], pl[5], pl[6], pl[7]);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
