@@ -19,16 +19,16 @@
 // rows' sums are carried in fp32 in the workspace.
 #include <algorithm>
 #include <atomic>
-#include <cstring>
+#include <cmath>
 
 #include "attn_bwd_tc.cuh"
 #include "attn_grad.cuh"
 
 namespace {
 
-constexpr int MAX_GROUPS = 152;          // query groups of the scatter plan
+constexpr int MAX_GROUPS = 304;          // query groups of the scatter plan: a block of 1,024 threads each,
+                                         // two on an SM
 constexpr int64_t MAX_COUNTERS = 1 << 24;
-constexpr int SCAN_ROWS = 1024;          // rows per block of the plan's scan
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -38,17 +38,19 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // lie in the same row.  A block walks its group's queries in order: the barrier between
 // two queries orders their counter updates.  Slots of one query in the same row (the same
 // index twice) hold the same contribution, so their order does not matter.
-__global__ void __launch_bounds__(512) bwd_rank_kernel(SlotArgs a, int64_t bq0, int nb, int group_q, int n_slots,
-                                                       int64_t rows, uint32_t* cnt, int32_t* rank) {
-    const int g = blockIdx.x;
+__global__ void __launch_bounds__(1024, 2) bwd_rank_kernel(SlotArgs a, int64_t bq0, int nb, int group_q, int n_slots,
+                                                          int64_t rows, uint32_t* cnt, int32_t* rank) {
+    const int g = blockIdx.x, t = threadIdx.x;
     uint32_t* c = cnt + (int64_t)g * rows;
-    const int q1 = min(nb, (g + 1) * group_q);
-    for (int q = g * group_q; q < q1; ++q) {
-        for (int s = threadIdx.x; s < n_slots; s += blockDim.x) {
-            const int64_t row = slot_row(a, bq0 + q, s, true);
-            int32_t r = -1;
-            if (row >= 0) r = (int32_t)atomicAdd(&c[row], 1u);
-            rank[(int64_t)q * n_slots + s] = r;
+    const int q0 = g * group_q, q1 = min(nb, q0 + group_q);
+    // the first 1,024 slots' rows of the next query are looked up while this one counts
+    int64_t next = q0 < q1 && t < n_slots ? slot_row(a, bq0 + q0, t, true) : -1;
+    for (int q = q0; q < q1; ++q) {
+        int64_t row = next;
+        if (q + 1 < q1 && t < n_slots) next = slot_row(a, bq0 + q + 1, t, true);
+        for (int s = t; s < n_slots; s += 1024) {
+            if (s != t) row = slot_row(a, bq0 + q, s, true);
+            rank[(int64_t)q * n_slots + s] = row >= 0 ? (int32_t)atomicAdd(&c[row], 1u) : -1;
         }
         __syncthreads();
     }
@@ -80,22 +82,33 @@ __device__ __forceinline__ uint32_t block_excl_scan(uint32_t v, uint32_t* warp_t
 }
 
 // Counts -> places: base[g][row] (in place of cnt) = first place of group g's stretch of
-// the row, relative to the row's block of 1,024 rows; loc / tot: the row's own start
-// (relative) and length; blk[b] = the block's length (scanned by bwd_scan_kernel).
-__global__ void __launch_bounds__(SCAN_ROWS) bwd_place_kernel(uint32_t* cnt, int groups, int64_t rows, uint32_t* loc,
-                                                              uint32_t* tot, uint32_t* blk) {
+// the row, relative to the row's block of BWD_SCAN_ROWS rows; loc / tot: the row's own start
+// (relative) and length; blk[b] = the block's length (scanned by bwd_scan_kernel).  Small
+// blocks: the walk over the groups is a chain of strided loads, so it wants many of them.
+__global__ void __launch_bounds__(BWD_SCAN_ROWS) bwd_place_kernel(uint32_t* cnt, int groups, int64_t rows,
+                                                                  uint32_t* loc, uint32_t* tot, uint32_t* blk) {
     __shared__ uint32_t wt[32], total;
-    const int64_t row = (int64_t)blockIdx.x * SCAN_ROWS + threadIdx.x;
+    const int64_t row = (int64_t)blockIdx.x * BWD_SCAN_ROWS + threadIdx.x;
     uint32_t n = 0;
     if (row < rows) {
-#pragma unroll 8
+#pragma unroll 16
         for (int g = 0; g < groups; ++g) n += cnt[(int64_t)g * rows + row];
     }
     const uint32_t start = block_excl_scan(n, wt, &total);
     if (row < rows) {
         uint32_t at = start;
-#pragma unroll 8
-        for (int g = 0; g < groups; ++g) {
+        int g = 0;
+        for (; g + 16 <= groups; g += 16) {
+            uint32_t here[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) here[i] = cnt[(int64_t)(g + i) * rows + row];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                cnt[(int64_t)(g + i) * rows + row] = at;
+                at += here[i];
+            }
+        }
+        for (; g < groups; ++g) {
             const uint32_t here = cnt[(int64_t)g * rows + row];
             cnt[(int64_t)g * rows + row] = at;
             at += here;
@@ -121,7 +134,7 @@ __global__ void __launch_bounds__(1024) bwd_scan_kernel(uint32_t* blk, int64_t n
 
 __device__ __forceinline__ int64_t pair_place(const BwdChunk& c, int q, int slot, int64_t row) {
     const int32_t r = c.rank[(int64_t)q * c.n_slots + slot];
-    return (int64_t)c.blk[row >> 10] + c.base[(int64_t)(q / c.group_q) * c.rows + row] + r;
+    return (int64_t)c.blk[row / BWD_SCAN_ROWS] + c.base[(int64_t)(q / c.group_q) * c.rows + row] + r;
 }
 
 // ---------------------------------------------------------------- preparation
@@ -144,50 +157,48 @@ __global__ void __launch_bounds__(256) bwd_rinv_kernel(const void* kv, int kv_dt
     if (lane == 0) rinv[row] = r;
 }
 
-// D = dout . out of every (query, head); a warp per head row.
-template <typename TO>
-__global__ void __launch_bounds__(256) bwd_dot_kernel(const TO* dout, const TO* out, int64_t n, float* D) {
-    const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (r >= n) return;
-    float a[16], b[16], s = 0.0f;
-    ag_load16<TO>(dout + r * AG_C + 16 * lane, a);
-    ag_load16<TO>(out + r * AG_C + 16 * lane, b);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s = fmaf(a[i], b[i], s);
-    s = warp_sum(s);
-    if (lane == 0) D[r] = s;
-}
-
-// dsink[h] = - sum over queries of exp(sink_h - lse) D, added in a fixed order (a block
-// per head; each thread's stretch, then a tree).
+// dsink[h] = - sum over queries of exp(sink_h - lse) D, added in a fixed order: block (x, y)
+// sums stretch y of the queries for the heads 32 x .. (a lane a head, a warp every eighth query,
+// then the warps), and the stretches' sums go to `part` [y][H], or to dsink if there is only one.
 __global__ void __launch_bounds__(256) bwd_sink_kernel(const float* sink, const float* lse, const float* D, int64_t n_bq,
-                                                       int H, float* dsink) {
-    __shared__ float red[8];
-    const int h = blockIdx.x;
-    const float zs = sink ? sink[h] : -INFINITY;
+                                                       int H, int64_t per, float* part) {
+    __shared__ float red[8][32];
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.x * 32 + lane;
+    const int64_t i1 = min(n_bq, ((int64_t)blockIdx.y + 1) * per);
+    const float zs = sink && h < H ? sink[h] : -INFINITY;
     float s = 0.0f;
     if (zs != -INFINITY) {
-        for (int64_t i = threadIdx.x; i < n_bq; i += 256) {
+#pragma unroll 4
+        for (int64_t i = blockIdx.y * per + w; i < i1; i += 8) {
             const float l = lse[i * H + h];
             if (l != -INFINITY) s = fmaf(-expf(zs - l), D[i * H + h], s);
         }
     }
-    s = warp_sum(s);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+    red[w][lane] = s;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        float t = 0.0f;
-        for (int i = 0; i < 8; ++i) t += red[i];
-        dsink[h] = t;
+    if (w == 0 && h < H) {
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += red[i][lane];
+        part[(int64_t)blockIdx.y * H + h] = s;
     }
 }
 
-// q^ and do' of every (query, head) of the chunk in fp32 (CUDA-core path); a warp per row.
+__global__ void __launch_bounds__(128) bwd_sink_sum_kernel(const float* part, int n, int H, float* dsink) {
+    const int h = threadIdx.x;
+    if (h >= H) return;
+    float s = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) s += part[(int64_t)i * H + h];
+    dsink[h] = s;
+}
+
+// q^ and do' of every (query, head) of the chunk in fp32 and D = dout . out (CUDA-core path); a
+// warp per row.
 template <typename TQ, typename TO>
-__global__ void __launch_bounds__(256) bwd_prep_kernel(const TQ* q, const TO* dout, const int64_t* q_pos, int64_t bq0,
-                                                       int64_t n_rows, int H, RopeTable rope, unsigned flags, float* qh,
-                                                       float* dh) {
+__global__ void __launch_bounds__(256) bwd_prep_kernel(const TQ* q, const TO* dout, const TO* out, const int64_t* q_pos,
+                                                       int64_t bq0, int64_t n_rows, int H, RopeTable rope,
+                                                       unsigned flags, float* qh, float* dh, float* D) {
     __shared__ float cs[8][32], sn[8][32];
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r = (int64_t)blockIdx.x * 8 + w;
@@ -204,8 +215,13 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const TQ* q, const TO* do
     }
     if (flags & CSA2_ROPE) ag_rope16(v, lane, cs[w], sn[w], 1.0f);
     ag_store16<float>(qh + dst, v);
-    if (!dout) return;
     ag_load16<TO>(dout + src, v);
+    float o[16], dot = 0.0f;
+    ag_load16<TO>(out + src, o);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) dot = fmaf(v[i], o[i], dot);
+    dot = warp_sum(dot);
+    if (lane == 0) D[bq0 * H + r] = dot;
     if (flags & CSA2_ROPE) ag_rope16(v, lane, cs[w], sn[w], 1.0f);
     ag_store16<float>(dh + dst, v);
 }
@@ -215,11 +231,40 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const TQ* q, const TO* do
 constexpr int SB_HG = 8;                 // heads per CTA of the query pass
 constexpr int SB_KC = 32;                // key rows per staged chunk
 
+// dq of one head row by a warp, lane l holding channels l + 32 i: dq^ back through RoPE and the
+// query's RMSNorm (on q^ and dq^: a rotation keeps their product).  A query that attends to
+// nothing has no gradient, whatever its values.
+template <typename TQ>
+__device__ __forceinline__ void finish_dq(const BwdChunk& c, int64_t bq, int h, int lane, const float (&qv)[16],
+                                          float (&acc)[16], const float* cs, const float* sn, TQ* dq) {
+    const int64_t o = (bq * c.H + h) * AG_C;
+    const TQ* qraw = reinterpret_cast<const TQ*>(c.q) + o;
+    if (c.flags & CSA2_QNORM) {
+        float ss = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float x = to_f32<TQ>(qraw[lane + 32 * i]);
+            ss = fmaf(x, x, ss);
+            dot = fmaf(qv[i], acc[i], dot);
+        }
+        const float f = ag_rms_factor(warp_sum(ss));
+        dot = warp_sum(dot) / (float)AG_C;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[i] = f * (acc[i] - qv[i] * dot);
+    }
+    if (c.flags & CSA2_ROPE) rope_lanes(acc, lane, cs, sn, -1.0f);
+    const bool none = c.lse[bq * c.H + h] == -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) dq[o + lane + 32 * i] = from_f32<TQ>(none ? 0.0f : acc[i]);
+}
+
 // Query pass: p and dS of every slot (kept for the row pass) and dq; a CTA per (8 heads,
-// query), a warp per head, key rows staged 32 at a time in fp32.
+// query, range of slots), a warp per head, key rows staged 32 at a time in fp32.  With few
+// queries the slots are split over CTAs (p needs no other slot, the lse is given) and
+// bwd_simt_dq_kernel adds the ranges' dq^.
 template <typename TQ>
 __global__ void __launch_bounds__(256, 2) bwd_simt_q_kernel(BwdChunk c, const float* qh, const float* dh, float2* pds,
-                                                            TQ* dq) {
+                                                            float* dqh, int per, TQ* dq) {
     extern __shared__ float smem[];
     float* xs = smem;                                        // [32][512] normalised rows
     int* ok = reinterpret_cast<int*>(xs + SB_KC * AG_C);     // [32]
@@ -245,7 +290,8 @@ __global__ void __launch_bounds__(256, 2) bwd_simt_q_kernel(BwdChunk c, const fl
         D = c.D[bq * c.H + h];
     }
     const float isc = 1.0f / sqrtf((float)AG_C);
-    for (int s0 = 0; s0 < c.n_slots; s0 += SB_KC) {
+    const int s_end = min(c.n_slots, ((int)blockIdx.z + 1) * per);
+    for (int s0 = blockIdx.z * per; s0 < s_end; s0 += SB_KC) {
         __syncthreads();
         for (int r = w; r < SB_KC; r += 8) {
             const int64_t row = s0 + r < c.n_slots ? slot_row(c.slots, bq, s0 + r, false) : -1;
@@ -293,30 +339,37 @@ __global__ void __launch_bounds__(256, 2) bwd_simt_q_kernel(BwdChunk c, const fl
             for (int i = 0; i < 16; ++i) acc[i] = fmaf(d, xs[j * AG_C + lane + 32 * i], acc[i]);
         }
     }
+    __syncthreads();                                         // (cs, sn; every warp is past its rows)
     if (!live) return;
-    // dq: back through RoPE and the query's RMSNorm (on q^ and dq^: a rotation keeps their product)
-    const int64_t o = (bq * c.H + h) * AG_C;
-    const TQ* qraw = reinterpret_cast<const TQ*>(c.q) + o;
-    if (c.flags & CSA2_QNORM) {
-        float ss = 0.0f, dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float x = to_f32<TQ>(qraw[lane + 32 * i]);
-            ss = fmaf(x, x, ss);
-            dot = fmaf(qv[i], acc[i], dot);
-        }
-        const float f = ag_rms_factor(warp_sum(ss));
-        dot = warp_sum(dot) / (float)AG_C;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = f * (acc[i] - qv[i] * dot);
+    if (gridDim.z == 1) {
+        finish_dq<TQ>(c, bq, h, lane, qv, acc, cs, sn, dq);
+        return;
     }
-    if (c.flags & CSA2_ROPE) rope_lanes(acc, lane, cs, sn, -1.0f);
-    // a query that attends to nothing has no gradient, whatever its values
-    if (lse == -INFINITY)
+    float* o = dqh + (hr * gridDim.z + blockIdx.z) * AG_C;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+    for (int i = 0; i < 16; ++i) o[lane + 32 * i] = acc[i];
+}
+
+// dq from the slot ranges' dq^; a warp per (query, head).
+template <typename TQ>
+__global__ void __launch_bounds__(256) bwd_simt_dq_kernel(BwdChunk c, const float* qh, const float* dqh, int n_split, TQ* dq) {
+    __shared__ float cs[8][32], sn[8][32];
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t hr = (int64_t)blockIdx.x * 8 + w;
+    if (hr >= (int64_t)c.nb * c.H) return;
+    const int64_t bq = c.bq0 + hr / c.H;
+    rope_cos_sin(c.rope, c.slots.q_pos[bq], lane, cs[w][lane], sn[w][lane]);
+    __syncwarp();
+    float qv[16], acc[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) dq[o + lane + 32 * i] = from_f32<TQ>(acc[i]);
+    for (int i = 0; i < 16; ++i) {
+        qv[i] = qh[hr * AG_C + lane + 32 * i];
+        acc[i] = 0.0f;
+    }
+    for (int k = 0; k < n_split; ++k)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[i] += dqh[(hr * n_split + k) * AG_C + lane + 32 * i];
+    finish_dq<TQ>(c, bq, (int)(hr % c.H), lane, qv, acc, cs[w], sn[w], dq);
 }
 
 // Row pass: the contribution r_j sum_h (dS_hj q^_h + p_hj do'_h) of every (query, slot);
@@ -419,7 +472,7 @@ __global__ void __launch_bounds__(128) bwd_rowsum_kernel(RowSumArgs a) {
     const int64_t n = (int64_t)a.tot[row] * a.passes;
     if (n > 0) {
         const TP* p = reinterpret_cast<const TP*>(a.part) +
-                      ((int64_t)a.blk[row >> 10] + a.loc[row]) * a.passes * AG_C + ch;
+                      ((int64_t)a.blk[row / BWD_SCAN_ROWS] + a.loc[row]) * a.passes * AG_C + ch;
         int64_t i = 0;
         for (; i + 8 <= n; i += 8) {
             float4 v[8];
@@ -487,18 +540,37 @@ struct BwdSizes {
 };
 
 struct BwdLayout {
-    size_t D, rinv, cnt, loc, tot, blk, rank, qh, dh, pds, img, dqh, part, acc, total;
+    size_t D, sink, rinv, cnt, loc, tot, blk, rank, qh, dh, pds, img, dqh, part, acc, total;
     int groups, group_q, n_pass, n_split, tps;
 };
+
+// Stretches of queries that dsink is summed in: 32 queries are four a warp.
+int64_t sink_stretches(int64_t n_bq) { return std::max<int64_t>(1, std::min<int64_t>(64, n_bq / 32)); }
+
+// Slot ranges (of `per` slots) of the CUDA-core query pass: with few (query, 8 heads) groups, as
+// many as give every SM two CTAs.
+void simt_splits(int num_sms, int64_t groups, int n_slots, int* n_split, int* per) {
+    const int chunks = std::max(1, (n_slots + SB_KC - 1) / SB_KC);
+    const int want = (int)std::min<int64_t>(chunks, std::max<int64_t>(1, 2LL * num_sms / std::max<int64_t>(1, groups)));
+    const int cps = (chunks + want - 1) / want;
+    *per = cps * SB_KC;
+    *n_split = (chunks + cps - 1) / cps;
+}
 
 // Workspace of chunks of nb queries.
 BwdLayout bwd_layout(const BwdSizes& z, int64_t nb) {
     BwdLayout L;
-    const int64_t g = std::min<int64_t>({nb, MAX_GROUPS, std::max<int64_t>(1, MAX_COUNTERS / std::max<int64_t>(1, z.rows))});
+    // counting walks a group's queries one by one (about 1 us each), placing walks the groups 16
+    // at a time: the two walks are about as long with sqrt(16 nb) groups
+    const int64_t even = (int64_t)std::ceil(std::sqrt(16.0 * (double)nb));
+    const int64_t g = std::min<int64_t>({nb, even, MAX_GROUPS, std::max<int64_t>(1, MAX_COUNTERS / std::max<int64_t>(1, z.rows))});
     L.group_q = (int)((nb + g - 1) / g);
     L.groups = (int)((nb + L.group_q - 1) / L.group_q);
     L.n_pass = z.tc ? (z.H + 63) / 64 : 1;
-    bwd_tc_splits(z.num_sms, nb * L.n_pass, z.n_slots, &L.n_split, &L.tps);
+    if (z.tc)
+        bwd_tc_splits(z.num_sms, nb * L.n_pass, z.n_slots, &L.n_split, &L.tps);
+    else
+        simt_splits(z.num_sms, nb * ((z.H + SB_HG - 1) / SB_HG), z.n_slots, &L.n_split, &L.tps);
     size_t at = 0;
     auto take = [&at](size_t bytes) {
         const size_t o = at;
@@ -507,17 +579,19 @@ BwdLayout bwd_layout(const BwdSizes& z, int64_t nb) {
     };
     const size_t row_f32 = (size_t)AG_C * 4, heads = (size_t)nb * z.H, pairs = (size_t)nb * z.n_slots;
     L.D = take((size_t)z.n_bq * z.H * 4);
+    L.sink = take((size_t)sink_stretches(z.n_bq) * z.H * 4);
     L.rinv = take((size_t)z.rows * 4);
     L.cnt = take((size_t)L.groups * z.rows * 4);
     L.loc = take((size_t)z.rows * 4);
     L.tot = take((size_t)z.rows * 4);
-    L.blk = take((size_t)((z.rows + SCAN_ROWS - 1) / SCAN_ROWS) * 4);
+    L.blk = take((size_t)((z.rows + BWD_SCAN_ROWS - 1) / BWD_SCAN_ROWS) * 4);
     L.rank = take(pairs * 4);
     L.qh = take(z.tc ? 0 : heads * row_f32);
     L.dh = take(z.tc ? 0 : heads * row_f32);
     L.pds = take(z.tc ? 0 : heads * z.n_slots * 8);
     L.img = take(z.tc ? (size_t)nb * L.n_pass * bwd_tc_image_bytes() : 0);
-    L.dqh = take(z.tc ? (size_t)nb * L.n_pass * L.n_split * 64 * row_f32 : 0);
+    L.dqh = take(z.tc ? (size_t)nb * L.n_pass * L.n_split * 64 * row_f32
+                      : (L.n_split > 1 ? heads * L.n_split * row_f32 : 0));
     L.part = take(z.tc ? pairs * L.n_pass * AG_C * 2 : pairs * row_f32);
     L.acc = take(nb < z.n_bq ? (size_t)z.rows * row_f32 : 0);
     L.total = at;
@@ -559,16 +633,18 @@ size_t dt_bytes(csa2_dtype d) { return d == CSA2_F32 ? 4 : 2; }
 
 template <typename TQ, typename TO>
 csa2_status simt_chunk(const csa2_ctx* ctx, const BwdCall& a, const BwdChunk& c, float* qh, float* dh, float2* pds,
-                       cudaStream_t s) {
+                       float* dqh, int n_split, int per, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
     const csa2_status r = raise_smem(bwd_simt_q_kernel<TQ>, SB_SMEM, ctx->device, done);
     if (r != CSA2_OK) return r;
     const int64_t n_rows = (int64_t)c.nb * a.H;
     bwd_prep_kernel<TQ, TO><<<(unsigned)((n_rows + 7) / 8), 256, 0, s>>>(
-        reinterpret_cast<const TQ*>(a.q), reinterpret_cast<const TO*>(a.dout), a.q_pos, c.bq0, n_rows, a.H, c.rope,
-        a.flags, qh, dh);
-    bwd_simt_q_kernel<TQ><<<dim3((unsigned)((a.H + SB_HG - 1) / SB_HG), (unsigned)c.nb), 256, SB_SMEM, s>>>(
-        c, qh, dh, pds, reinterpret_cast<TQ*>(a.dq));
+        reinterpret_cast<const TQ*>(a.q), reinterpret_cast<const TO*>(a.dout), reinterpret_cast<const TO*>(a.out), a.q_pos,
+        c.bq0, n_rows, a.H, c.rope, a.flags, qh, dh, const_cast<float*>(c.D));
+    bwd_simt_q_kernel<TQ><<<dim3((unsigned)((a.H + SB_HG - 1) / SB_HG), (unsigned)c.nb, (unsigned)n_split), 256, SB_SMEM,
+                           s>>>(c, qh, dh, pds, dqh, per, reinterpret_cast<TQ*>(a.dq));
+    if (n_split > 1)
+        bwd_simt_dq_kernel<TQ><<<(unsigned)((n_rows + 7) / 8), 256, 0, s>>>(c, qh, dqh, n_split, reinterpret_cast<TQ*>(a.dq));
     if (c.n_slots > 0)
         bwd_simt_row_kernel<<<dim3((unsigned)((c.n_slots + 31) / 32), (unsigned)c.nb), 256, 0, s>>>(c, qh, dh, pds);
     return csa2_launch_status();
@@ -587,14 +663,6 @@ csa2_status bwd_run(csa2_ctx* ctx, const BwdCall& a, void* ws, size_t ws_bytes, 
     uint8_t* base = reinterpret_cast<uint8_t*>(ws);
     float* D = reinterpret_cast<float*>(base + L.D);
     float* rinv = reinterpret_cast<float*>(base + L.rinv);
-    const int64_t heads = n_bq * a.H;
-    if (a.out_dt == CSA2_F32)
-        bwd_dot_kernel<float><<<(unsigned)((heads + 7) / 8), 256, 0, s>>>(reinterpret_cast<const float*>(a.dout),
-                                                                         reinterpret_cast<const float*>(a.out), heads, D);
-    else
-        bwd_dot_kernel<__nv_bfloat16><<<(unsigned)((heads + 7) / 8), 256, 0, s>>>(
-            reinterpret_cast<const __nv_bfloat16*>(a.dout), reinterpret_cast<const __nv_bfloat16*>(a.out), heads, D);
-    if (a.dsink) bwd_sink_kernel<<<(unsigned)a.H, 256, 0, s>>>(a.sink, a.lse, D, n_bq, a.H, a.dsink);
     if (rows > 0)
         bwd_rinv_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a.kv, a.kv_dt, n_kv, a.swa, a.swa_dt, rows, a.flags,
                                                                   rinv);
@@ -625,20 +693,21 @@ csa2_status bwd_run(csa2_ctx* ctx, const BwdCall& a, void* ws, size_t ws_bytes, 
     c.group_q = L.group_q;
     c.part = base + L.part;
     c.dq = a.dq;
-    const int64_t n_blk = (rows + SCAN_ROWS - 1) / SCAN_ROWS;
+    const int64_t n_blk = (rows + BWD_SCAN_ROWS - 1) / BWD_SCAN_ROWS;
     for (int64_t bq0 = 0; bq0 < n_bq; bq0 += nb_max) {
         c.bq0 = bq0;
         c.nb = (int)std::min<int64_t>(nb_max, n_bq - bq0);
         if (rows > 0) {
             const csa2_status zr = zero_bytes(cnt, (size_t)L.groups * rows * 4, s);
             if (zr != CSA2_OK) return zr;
-            bwd_rank_kernel<<<(unsigned)L.groups, 512, 0, s>>>(c.slots, bq0, c.nb, L.group_q, n_slots, rows, cnt, rank);
-            bwd_place_kernel<<<(unsigned)n_blk, SCAN_ROWS, 0, s>>>(cnt, L.groups, rows, loc, tot, blk);
+            bwd_rank_kernel<<<(unsigned)L.groups, 1024, 0, s>>>(c.slots, bq0, c.nb, L.group_q, n_slots, rows, cnt, rank);
+            bwd_place_kernel<<<(unsigned)n_blk, BWD_SCAN_ROWS, 0, s>>>(cnt, L.groups, rows, loc, tot, blk);
             bwd_scan_kernel<<<1, 1024, 0, s>>>(blk, n_blk);
         }
         float* qh = reinterpret_cast<float*>(base + L.qh);
         float* dh = reinterpret_cast<float*>(base + L.dh);
         float2* pds = reinterpret_cast<float2*>(base + L.pds);
+        float* dqh = reinterpret_cast<float*>(base + L.dqh);
         csa2_status r;
         if (z.tc) {
             BwdTcArgs t;
@@ -647,13 +716,13 @@ csa2_status bwd_run(csa2_ctx* ctx, const BwdCall& a, void* ws, size_t ws_bytes, 
             t.n_pass = L.n_pass;
             t.n_split = L.n_split;
             t.tps = L.tps;
-            r = bwd_tc_chunk(ctx, t, a.dout, base + L.img, s);
+            r = bwd_tc_chunk(ctx, t, a.dout, a.out, D, base + L.img, s);
         } else if (a.q_dt == CSA2_F32)
-            r = a.out_dt == CSA2_F32 ? simt_chunk<float, float>(ctx, a, c, qh, dh, pds, s)
-                                     : simt_chunk<float, __nv_bfloat16>(ctx, a, c, qh, dh, pds, s);
+            r = a.out_dt == CSA2_F32 ? simt_chunk<float, float>(ctx, a, c, qh, dh, pds, dqh, L.n_split, L.tps, s)
+                                     : simt_chunk<float, __nv_bfloat16>(ctx, a, c, qh, dh, pds, dqh, L.n_split, L.tps, s);
         else
-            r = a.out_dt == CSA2_F32 ? simt_chunk<__nv_bfloat16, float>(ctx, a, c, qh, dh, pds, s)
-                                     : simt_chunk<__nv_bfloat16, __nv_bfloat16>(ctx, a, c, qh, dh, pds, s);
+            r = a.out_dt == CSA2_F32 ? simt_chunk<__nv_bfloat16, float>(ctx, a, c, qh, dh, pds, dqh, L.n_split, L.tps, s)
+                                     : simt_chunk<__nv_bfloat16, __nv_bfloat16>(ctx, a, c, qh, dh, pds, dqh, L.n_split, L.tps, s);
         if (r != CSA2_OK) return r;
         if (rows > 0 && (a.dkv || a.dswa)) {
             RowSumArgs ra;
@@ -682,7 +751,13 @@ csa2_status bwd_run(csa2_ctx* ctx, const BwdCall& a, void* ws, size_t ws_bytes, 
         }
         if (csa2_launch_status() != CSA2_OK) return CSA2_ERR_CUDA;
     }
-    return CSA2_OK;
+    if (a.dsink) {
+        const int64_t n = sink_stretches(n_bq), per = (n_bq + n - 1) / n;
+        float* part = n > 1 ? reinterpret_cast<float*>(base + L.sink) : a.dsink;
+        bwd_sink_kernel<<<dim3((unsigned)((a.H + 31) / 32), (unsigned)n), 256, 0, s>>>(a.sink, a.lse, D, n_bq, a.H, per, part);
+        if (n > 1) bwd_sink_sum_kernel<<<1, 128, 0, s>>>(part, (int)n, a.H, a.dsink);
+    }
+    return csa2_launch_status();
 }
 
 csa2_status bwd_impl(csa2_ctx* ctx, const BwdCall& a, int c, void* ws, size_t ws_bytes, void* stream) {

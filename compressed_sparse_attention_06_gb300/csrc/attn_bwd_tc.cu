@@ -144,8 +144,9 @@ __device__ __forceinline__ float ex2_approx(float x) {
 // Stacked images of the chunk's queries and D; a warp per head, 8 heads a CTA.  Image row of
 // head h (within its pass): 32 (h / 16) + h % 16 for q^, 16 more for do'.  Heads past H are 0.
 __global__ void __launch_bounds__(256) bwd_tc_prep_kernel(const __nv_bfloat16* q, const __nv_bfloat16* dout,
-                                                          const int64_t* q_pos, int64_t bq0, int nb, int H,
-                                                          RopeTable rope, unsigned flags, uint8_t* img) {
+                                                          const __nv_bfloat16* out, const int64_t* q_pos, int64_t bq0,
+                                                          int nb, int H, RopeTable rope, unsigned flags, uint8_t* img,
+                                                          float* D) {
     __shared__ float cs[32], sn[32];
     const int qi = blockIdx.y, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t bq = bq0 + qi;
@@ -158,6 +159,12 @@ __global__ void __launch_bounds__(256) bwd_tc_prep_kernel(const __nv_bfloat16* q
         const int64_t o = (bq * H + h) * (int64_t)BT_C + 16 * lane;
         ag_load16<__nv_bfloat16>(q + o, v);
         ag_load16<__nv_bfloat16>(dout + o, g);
+        float x[16], dot = 0.0f;
+        ag_load16<__nv_bfloat16>(out + o, x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dot = fmaf(g[i], x[i], dot);
+        dot = warp_sum(dot);
+        if (lane == 0) D[bq * H + h] = dot;
     }
     __syncthreads();
     if (flags & CSA2_QNORM) {
@@ -553,7 +560,7 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
                     int slot, pl = -1;
                     const int64_t row = row_of(a, it, (it.t0 + tt) * BT_TILE + 32 * j + lane, &slot);
                     if (row >= 0)
-                        pl = (int)(a.c.blk[row >> 10] + a.c.base[(int64_t)(it.q / a.c.group_q) * a.c.rows + row]) +
+                        pl = (int)(a.c.blk[row / BWD_SCAN_ROWS] + a.c.base[(int64_t)(it.q / a.c.group_q) * a.c.rows + row]) +
                              a.c.rank[(int64_t)it.q * a.c.n_slots + slot];
                     pl2[j] = pl;
                 }
@@ -654,7 +661,8 @@ void bwd_tc_splits(int num_sms, int64_t queries, int n_slots, int* n_split, int*
 
 size_t bwd_tc_image_bytes() { return IMG_BYTES; }
 
-csa2_status bwd_tc_chunk(csa2_ctx* ctx, BwdTcArgs& a, const void* dout, uint8_t* img, cudaStream_t s) {
+csa2_status bwd_tc_chunk(csa2_ctx* ctx, BwdTcArgs& a, const void* dout, const void* out, float* D, uint8_t* img,
+                         cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
     const uint64_t bit = 1ull << (ctx->device & 63);
     if (!(done.load(std::memory_order_relaxed) & bit)) {
@@ -663,8 +671,8 @@ csa2_status bwd_tc_chunk(csa2_ctx* ctx, BwdTcArgs& a, const void* dout, uint8_t*
     }
     const BwdChunk& c = a.c;
     bwd_tc_prep_kernel<<<dim3((unsigned)(8 * a.n_pass), (unsigned)c.nb), 256, 0, s>>>(
-        reinterpret_cast<const __nv_bfloat16*>(c.q), reinterpret_cast<const __nv_bfloat16*>(dout), c.slots.q_pos, c.bq0,
-        c.nb, c.H, c.rope, c.flags, img);
+        reinterpret_cast<const __nv_bfloat16*>(c.q), reinterpret_cast<const __nv_bfloat16*>(dout),
+        reinterpret_cast<const __nv_bfloat16*>(out), c.slots.q_pos, c.bq0, c.nb, c.H, c.rope, c.flags, img, D);
     a.img = img;
     a.items = (int64_t)c.nb * a.n_pass * a.n_split;
     a.budget = WAIT_BUDGET;

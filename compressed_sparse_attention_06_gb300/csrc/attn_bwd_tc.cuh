@@ -20,5 +20,6 @@ bool bwd_tc_applies(csa2_dtype q_dt, csa2_dtype kv_dt, int k, csa2_dtype swa_dt,
 // Key splits of `queries` (times head passes) of n_slots slots each.
 void bwd_tc_splits(int num_sms, int64_t queries, int n_slots, int* n_split, int* tps);
 size_t bwd_tc_image_bytes();
-// Images, products and dq of a chunk (c.rank .. c.part filled in by the caller).
-csa2_status bwd_tc_chunk(csa2_ctx* ctx, BwdTcArgs& a, const void* dout, uint8_t* img, cudaStream_t s);
+// Images, D, products and dq of a chunk (c.rank .. c.part filled in by the caller).
+csa2_status bwd_tc_chunk(csa2_ctx* ctx, BwdTcArgs& a, const void* dout, const void* out, float* D, uint8_t* img,
+                         cudaStream_t s);

@@ -167,6 +167,8 @@ struct DeviceGuard {
 
 // ---- host side of the backward pass shared by its two paths ------------------------
 
+constexpr int BWD_SCAN_ROWS = 256;       // rows per block of the scatter plan's scan
+
 // One chunk of queries of the backward pass, as both paths take it.
 struct BwdChunk {
     SlotArgs slots;           // pointers at the whole call's queries
@@ -185,7 +187,7 @@ struct BwdChunk {
     unsigned flags;
     RopeTable rope;
     // the chunk's scatter plan: the contribution of (query bq, slot s) to its row goes to
-    // place blk[row >> 10] + base[group][row] + rank[bq - bq0][s] of `part`
+    // place blk[row / BWD_SCAN_ROWS] + base[group][row] + rank[bq - bq0][s] of `part`
     const int32_t* rank;      // [nb, n_slots], -1 = empty slot
     const uint32_t* base;     // [groups, rows]
     const uint32_t* blk;

@@ -7,10 +7,11 @@
 //     dC_j = s_j dE,   dZ_j = s_j dE (C_j - E),   dB_j = sum over entries of dZ_j
 // The weights and E are computed again from the inputs; nothing of the forward is kept.
 //
-// Memory bound: every input row is read once and every gradient row written once.  A CTA of
-// c/4 threads (four adjacent channels each) takes a run of entries; windows of up to 8 rows
-// stay in registers between the softmax and the gradients, longer ones are read again (from
-// the caches).  The bias gradients are sums over all entries: each CTA sums its run in
+// Memory bound: every input row is read once and every gradient row written once.  A CTA takes
+// a run of entries, a thread a few adjacent channels of each.  The usual windows (up to 8 rows:
+// m = 1, 2, 4, 8, and overlapping m = 1, 2, 4) are compiled for their size: all of an entry's
+// rows are loaded together, one entry ahead of the arithmetic, and stay in registers between the
+// softmax and the gradients; other windows are read again (from the caches).  The bias gradients are sums over all entries: each CTA sums its run in
 // registers (long windows: in its slab of the workspace), and a last pass adds the CTAs'
 // sums in order, so the results do not depend on timing.
 #include <algorithm>
@@ -101,7 +102,7 @@ __device__ __forceinline__ Window<T> window_of(const CompressBwdArgs<T>& a, int6
     return w;
 }
 
-// Sums of two values over the CTA (at most 8 warps), two alternating buffers.
+// Sums of two values over the CTA (at most 16 warps), two alternating buffers.
 __device__ __forceinline__ void block_sum2(float& x, float& y, float2* red) {
     x = warp_sum(x);
     y = warp_sum(y);
@@ -115,22 +116,215 @@ __device__ __forceinline__ void block_sum2(float& x, float& y, float2* red) {
     }
 }
 
-// MR > 0: windows of at most MR rows, kept in registers; MR == 0: any m, rows read again.
-template <typename T, int MR>
-__global__ void __launch_bounds__(256) compress_bwd_kernel(CompressBwdArgs<T> a) {
-    __shared__ float2 red[2][8];
-    const int ch = 4 * threadIdx.x;
-    const int m = a.m, c = a.c;
-    const int R = MR > 0 ? MR : 1;
+// CH adjacent channels of a row as they are stored, and as fp32.
+template <typename T, int CH>
+struct Raw;
+template <>
+struct Raw<float, 2> {
+    float2 v;
+};
+template <>
+struct Raw<float, 4> {
+    float4 v;
+};
+template <>
+struct Raw<__nv_bfloat16, 2> {
+    uint32_t v;
+};
+template <>
+struct Raw<__nv_bfloat16, 4> {
+    uint2 v;
+};
+template <typename T, int CH>
+__device__ __forceinline__ void ld(Raw<T, CH>& r, const T* p) {
+    r.v = __ldcs(reinterpret_cast<const decltype(r.v)*>(p));
+}
+__device__ __forceinline__ void values(const Raw<float, 2>& r, float (&x)[2]) {
+    x[0] = r.v.x;
+    x[1] = r.v.y;
+}
+__device__ __forceinline__ void values(const Raw<float, 4>& r, float (&x)[4]) { unpack4(r.v, x); }
+__device__ __forceinline__ void values(const Raw<__nv_bfloat16, 2>& r, float (&x)[2]) {
+    x[0] = __uint_as_float(r.v << 16);
+    x[1] = __uint_as_float(r.v & 0xFFFF0000u);
+}
+__device__ __forceinline__ void values(const Raw<__nv_bfloat16, 4>& r, float (&x)[4]) {
+    x[0] = __uint_as_float(r.v.x << 16);
+    x[1] = __uint_as_float(r.v.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(r.v.y << 16);
+    x[3] = __uint_as_float(r.v.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void st(float* p, const float (&v)[2]) { *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]); }
+__device__ __forceinline__ void st(float* p, const float (&v)[4]) { st4<float>(p, v); }
+__device__ __forceinline__ void st(__nv_bfloat16* p, const float (&v)[2]) {
+    *reinterpret_cast<uint32_t*>(p) = ag_pack_bf16x2(v[0], v[1]);
+}
+__device__ __forceinline__ void st(__nv_bfloat16* p, const float (&v)[4]) { st4<__nv_bfloat16>(p, v); }
+
+// Windows of M block rows and (OV) M history rows; CH channels a thread, c / CH threads.
+template <typename T, int M, bool OV, int CH>
+__global__ void __launch_bounds__(1024 / CH) compress_bwd_kernel(CompressBwdArgs<T> a) {
+    constexpr int R = OV ? 2 * M : M;
+    __shared__ float2 red[2][16];
+    const int ch = CH * threadIdx.x, c = a.c;
     const int64_t e0 = (int64_t)blockIdx.x * a.run, e1 = min(a.entries, e0 + a.run);
-    const int tables = a.cb ? 2 : 1;
-    float* slab = a.slab ? a.slab + (int64_t)blockIdx.x * tables * m * c + ch : nullptr;
-    float db[R][4];
+    float db[R][CH];
 #pragma unroll
     for (int j = 0; j < R; ++j)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) db[j][k] = 0.0f;
-    if (MR == 0 && slab)
+        for (int k = 0; k < CH; ++k) db[j][k] = 0.0f;
+    int64_t b = e0 / a.n_ent, i = e0 - b * a.n_ent;
+    // the entry ahead: its rows as stored, its gradient, whether it has history
+    Raw<T, CH> nz[R], nc[R];
+    float ng[CH];
+    auto fetch = [&](int64_t b, int64_t i) {
+        const Window<T> w = window_of(a, b, i);
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            if (!OV || j < M) {
+                ld<T, CH>(nz[j], w.z0 + (int64_t)j * c + ch);
+                ld<T, CH>(nc[j], w.c0 + (int64_t)j * c + ch);
+            } else if (w.c1) {
+                ld<T, CH>(nz[j], w.z1 + (int64_t)(j - M) * c + ch);
+                ld<T, CH>(nc[j], w.c1 + (int64_t)(j - M) * c + ch);
+            }
+        }
+        const int64_t go = (b * a.dout_stride + i) * c + ch;
+        if (a.dout_f32) {
+            Raw<float, CH> g;
+            ld<float, CH>(g, reinterpret_cast<const float*>(a.dout) + go);
+            values(g, ng);
+        } else {
+            Raw<__nv_bfloat16, CH> g;
+            ld<__nv_bfloat16, CH>(g, reinterpret_cast<const __nv_bfloat16*>(a.dout) + go);
+            values(g, ng);
+        }
+    };
+    if (e0 < e1) fetch(b, i);
+    for (int64_t e = e0; e < e1; ++e) {
+        const Window<T> w = window_of(a, b, i);
+        const bool hist = OV && w.c1;
+        const int64_t here_b = b, here_i = i;
+        float z[R][CH], v[R][CH], mx[CH], den[CH], E[CH], g[CH];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            if (!OV || j < M || hist) {
+                values(nz[j], z[j]);
+                values(nc[j], v[j]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < CH; ++k) {              // no history: logit -inf, value 0
+                    z[j][k] = -INFINITY;
+                    v[j][k] = 0.0f;
+                }
+            }
+            const float* bias = j < M ? a.ba : a.bb;
+            if (bias) {
+                Raw<float, CH> r;
+                r.v = *reinterpret_cast<const decltype(r.v)*>(bias + (int64_t)(j < M ? j : j - M) * c + ch);
+                float x[CH];
+                values(r, x);
+#pragma unroll
+                for (int k = 0; k < CH; ++k) z[j][k] += x[k];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < CH; ++k) g[k] = ng[k];
+        if (++i == a.n_ent) {
+            i = 0;
+            ++b;
+        }
+        if (e + 1 < e1) fetch(b, i);
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            mx[k] = z[0][k];
+#pragma unroll
+            for (int j = 1; j < R; ++j) mx[k] = fmaxf(mx[k], z[j][k]);
+            den[k] = E[k] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                z[j][k] = expf(z[j][k] - mx[k]);
+                den[k] += z[j][k];
+                E[k] = fmaf(z[j][k], v[j][k], E[k]);
+            }
+            E[k] /= den[k];
+        }
+        if ((a.flags & CSA2_W_ROPE) && ch >= c - 64) {
+            const int64_t pos = (a.pos0 ? a.pos0[here_b] : 0) + (int64_t)M * here_i;
+#pragma unroll
+            for (int p = 0; p < CH / 2; ++p) {
+                float cs, sn;
+                rope_cos_sin(a.rope, pos, (ch + 2 * p - (c - 64)) >> 1, cs, sn);
+                const float x0 = g[2 * p], x1 = g[2 * p + 1];
+                g[2 * p] = x0 * cs + x1 * sn;
+                g[2 * p + 1] = x1 * cs - x0 * sn;
+            }
+        }
+        if (a.flags & CSA2_W_NORM) {
+            float ss = 0.0f, dot = 0.0f;
+#pragma unroll
+            for (int k = 0; k < CH; ++k) {
+                ss = fmaf(E[k], E[k], ss);
+                dot = fmaf(E[k], g[k], dot);
+            }
+            block_sum2(ss, dot, red[(e - e0) & 1]);
+            const float r = 1.0f / sqrtf(ss / (float)c + 1e-6f);
+            const float d = dot * r * r / (float)c;
+#pragma unroll
+            for (int k = 0; k < CH; ++k) g[k] = r * fmaf(-E[k], d, g[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < CH; ++k) den[k] = 1.0f / den[k];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            float dc[CH], dz[CH];
+#pragma unroll
+            for (int k = 0; k < CH; ++k) {
+                dc[k] = z[j][k] * den[k] * g[k];
+                dz[k] = dc[k] * (v[j][k] - E[k]);
+            }
+            const int64_t o = (int64_t)(j < M ? j : j - M) * c + ch;
+            if (!OV || j < M) {
+                st(w.g0 + o, dc);
+                st(w.h0 + o, dz);
+            } else if (hist) {
+                if (w.g1) st(w.g1 + o, dc);
+                if (w.h1) st(w.h1 + o, dz);
+            }
+            if (!OV || j < M || hist)
+#pragma unroll
+                for (int k = 0; k < CH; ++k) db[j][k] += dz[k];
+        }
+        if (OV && here_i == a.n_ent - 1) {
+            // the stream's last block is nobody's history within this call
+            float zero[CH];
+#pragma unroll
+            for (int k = 0; k < CH; ++k) zero[k] = 0.0f;
+            const int64_t at = (here_b * a.n_tokens + here_i * M) * c + ch;
+            for (int j = 0; j < M; ++j) {
+                st(a.dcb + at + (int64_t)j * c, zero);
+                st(a.dzb + at + (int64_t)j * c, zero);
+            }
+        }
+    }
+    if (a.slab) {
+        float* slab = a.slab + (int64_t)blockIdx.x * R * c + ch;
+#pragma unroll
+        for (int j = 0; j < R; ++j) st(slab + (int64_t)j * c, db[j]);
+    }
+}
+
+// Any m: four channels a thread, the window's rows read once for the maximum, once for the sums
+// and once for the gradients.
+template <typename T>
+__global__ void __launch_bounds__(256) compress_bwd_any_kernel(CompressBwdArgs<T> a) {
+    __shared__ float2 red[2][16];
+    const int ch = 4 * threadIdx.x;
+    const int m = a.m, c = a.c;
+    const int64_t e0 = (int64_t)blockIdx.x * a.run, e1 = min(a.entries, e0 + a.run);
+    const int tables = a.cb ? 2 : 1;
+    float* slab = a.slab ? a.slab + (int64_t)blockIdx.x * tables * m * c + ch : nullptr;
+    if (slab)
         for (int j = 0; j < tables * m; ++j) *reinterpret_cast<float4*>(slab + (int64_t)j * c) = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int64_t e = e0; e < e1; ++e) {
         const int64_t b = e / a.n_ent, i = e - b * a.n_ent;
@@ -148,7 +342,7 @@ __global__ void __launch_bounds__(256) compress_bwd_kernel(CompressBwdArgs<T> a)
                 z[3] += u.w;
             }
         };
-        float z[R][4], v[R][4], mx[4], den[4], E[4], g[4];
+        float mx[4], den[4], E[4], g[4], t[4], x[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             mx[k] = -INFINITY;
@@ -157,47 +351,21 @@ __global__ void __launch_bounds__(256) compress_bwd_kernel(CompressBwdArgs<T> a)
         const int64_t go = (b * a.dout_stride + i) * c + ch;
         unpack4(a.dout_f32 ? ld4<float>(reinterpret_cast<const float*>(a.dout) + go)
                            : ld4<__nv_bfloat16>(reinterpret_cast<const __nv_bfloat16*>(a.dout) + go), g);
-        if (MR > 0) {
+#pragma unroll 8
+        for (int j = 0; j < rows; ++j) {
+            logit(j, t);
 #pragma unroll
-            for (int j = 0; j < MR; ++j) {
-                if (j >= rows) break;
-                logit(j, z[j]);
-                unpack4(ld4<T>(src(w.c0, w.c1, j)), v[j]);
-            }
-#pragma unroll
-            for (int j = 0; j < MR; ++j) {
-                if (j >= rows) break;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], z[j][k]);
-            }
-#pragma unroll
-            for (int j = 0; j < MR; ++j) {
-                if (j >= rows) break;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    z[j][k] = expf(z[j][k] - mx[k]);
-                    den[k] += z[j][k];
-                    E[k] = fmaf(z[j][k], v[j][k], E[k]);
-                }
-            }
-        } else {
-            float t[4], x[4];
+            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], t[k]);
+        }
 #pragma unroll 4
-            for (int j = 0; j < rows; ++j) {
-                logit(j, t);
+        for (int j = 0; j < rows; ++j) {
+            logit(j, t);
+            unpack4(ld4<T>(src(w.c0, w.c1, j)), x);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], t[k]);
-            }
-#pragma unroll 4
-            for (int j = 0; j < rows; ++j) {
-                logit(j, t);
-                unpack4(ld4<T>(src(w.c0, w.c1, j)), x);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float p = expf(t[k] - mx[k]);
-                    den[k] += p;
-                    E[k] = fmaf(p, x[k], E[k]);
-                }
+            for (int k = 0; k < 4; ++k) {
+                const float p = expf(t[k] - mx[k]);
+                den[k] += p;
+                E[k] = fmaf(p, x[k], E[k]);
             }
         }
 #pragma unroll
@@ -226,52 +394,34 @@ __global__ void __launch_bounds__(256) compress_bwd_kernel(CompressBwdArgs<T> a)
 #pragma unroll
             for (int k = 0; k < 4; ++k) g[k] = r * fmaf(-E[k], d, g[k]);
         }
-        float inv[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) inv[k] = 1.0f / den[k];
-        auto emit = [&](int j, const float (&p)[4], const float (&x)[4], float (&sum)[4]) {
+        for (int k = 0; k < 4; ++k) den[k] = 1.0f / den[k];
+#pragma unroll 4
+        for (int j = 0; j < rows; ++j) {
+            logit(j, t);
+            unpack4(ld4<T>(src(w.c0, w.c1, j)), x);
             float dc[4], dz[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                dc[k] = p[k] * inv[k] * g[k];
+                dc[k] = expf(t[k] - mx[k]) * den[k] * g[k];
                 dz[k] = dc[k] * (x[k] - E[k]);
-                sum[k] += dz[k];
             }
             const int64_t o = (int64_t)(j < m ? j : j - m) * c + ch;
             T* gc = j < m ? w.g0 : w.g1;
             T* gz = j < m ? w.h0 : w.h1;
             if (gc) st4<T>(gc + o, dc);
             if (gz) st4<T>(gz + o, dz);
-        };
-        if (MR > 0) {
-#pragma unroll
-            for (int j = 0; j < MR; ++j) {
-                if (j >= rows) break;
-                emit(j, z[j], v[j], db[j]);
-            }
-        } else {
-            float t[4], x[4];
-#pragma unroll 2
-            for (int j = 0; j < rows; ++j) {
-                logit(j, t);
-                unpack4(ld4<T>(src(w.c0, w.c1, j)), x);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) t[k] = expf(t[k] - mx[k]);
-                float s[4] = {0.f, 0.f, 0.f, 0.f};
-                emit(j, t, x, s);
-                if (slab) {
-                    float4* d = reinterpret_cast<float4*>(slab + (int64_t)j * c);
-                    float4 u = *d;
-                    u.x += s[0];
-                    u.y += s[1];
-                    u.z += s[2];
-                    u.w += s[3];
-                    *d = u;
-                }
+            if (slab) {
+                float4* d = reinterpret_cast<float4*>(slab + (int64_t)j * c);
+                float4 u = *d;
+                u.x += dz[0];
+                u.y += dz[1];
+                u.z += dz[2];
+                u.w += dz[3];
+                *d = u;
             }
         }
         if (a.cb && i == a.n_ent - 1) {
-            // the stream's last block is nobody's history within this call
             const float zero[4] = {0.f, 0.f, 0.f, 0.f};
             const int64_t at = (b * a.n_tokens + i * m) * c + ch;
             for (int j = 0; j < m; ++j) {
@@ -280,29 +430,24 @@ __global__ void __launch_bounds__(256) compress_bwd_kernel(CompressBwdArgs<T> a)
             }
         }
     }
-    if (MR > 0 && slab) {
-#pragma unroll
-        for (int j = 0; j < R; ++j)
-            if (j < tables * m) *reinterpret_cast<float4*>(slab + (int64_t)j * c) = make_float4(db[j][0], db[j][1], db[j][2], db[j][3]);
-    }
 }
 
-// db[x] = sum of the CTAs' slabs in a fixed order: warp w of a block takes slabs w, w + 8, ..
-// of 32 adjacent columns, then the eight sums are added.
-__global__ void __launch_bounds__(256) compress_bias_kernel(const float* slab, int ctas, int64_t cols, int64_t split,
+// db[x] = sum of the CTAs' slabs in a fixed order: warp w of a block takes slabs w, w + 32, ..
+// of 32 adjacent columns, then the 32 sums are added.
+__global__ void __launch_bounds__(1024) compress_bias_kernel(const float* slab, int ctas, int64_t cols, int64_t split,
                                                             float* dba, float* dbb) {
-    __shared__ float red[8][32];
+    __shared__ float red[32][32];
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t x = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.0f;
 #pragma unroll 8
-    for (int i = w; i < ctas; i += 8) s += slab[(int64_t)i * cols + x];
+    for (int i = w; i < ctas; i += 32) s += slab[(int64_t)i * cols + x];
     red[w][lane] = s;
     __syncthreads();
     if (w == 0) {
         s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += red[i][lane];
+        for (int i = 0; i < 32; ++i) s += red[i][lane];
         float* d = x < split ? dba : dbb;
         if (d) d[x < split ? x : x - split] = s;
     }
@@ -360,19 +505,26 @@ csa2_status cb_launch(const CompressBwdCall& p, cudaStream_t s) {
     a.slab = p.dba || p.dbb ? p.slab : nullptr;
     const int64_t ctas = cb_ctas(a.entries);
     a.run = (a.entries + ctas - 1) / ctas;
-    const int rows = p.cb ? 2 * p.m : p.m;
-    const dim3 grid((unsigned)ctas), block((unsigned)(p.c / 4));
-    if (rows <= 2)
-        compress_bwd_kernel<T, 2><<<grid, block, 0, s>>>(a);
-    else if (rows <= 4)
-        compress_bwd_kernel<T, 4><<<grid, block, 0, s>>>(a);
-    else if (rows <= 8)
-        compress_bwd_kernel<T, 8><<<grid, block, 0, s>>>(a);
+    const unsigned grid = (unsigned)ctas, c4 = (unsigned)(p.c / 4), c2 = (unsigned)(p.c / 2);
+    if (!p.cb && p.m == 1)
+        compress_bwd_kernel<T, 1, false, 4><<<grid, c4, 0, s>>>(a);
+    else if (!p.cb && p.m == 2)
+        compress_bwd_kernel<T, 2, false, 4><<<grid, c4, 0, s>>>(a);
+    else if (!p.cb && p.m == 4)
+        compress_bwd_kernel<T, 4, false, 4><<<grid, c4, 0, s>>>(a);
+    else if (!p.cb && p.m == 8)
+        compress_bwd_kernel<T, 8, false, 2><<<grid, c2, 0, s>>>(a);
+    else if (p.cb && p.m == 1)
+        compress_bwd_kernel<T, 1, true, 4><<<grid, c4, 0, s>>>(a);
+    else if (p.cb && p.m == 2)
+        compress_bwd_kernel<T, 2, true, 4><<<grid, c4, 0, s>>>(a);
+    else if (p.cb && p.m == 4)
+        compress_bwd_kernel<T, 4, true, 2><<<grid, c2, 0, s>>>(a);
     else
-        compress_bwd_kernel<T, 0><<<grid, block, 0, s>>>(a);
+        compress_bwd_any_kernel<T><<<grid, c4, 0, s>>>(a);
     if (a.slab) {
         const int64_t split = (int64_t)p.m * p.c, cols = split * (p.cb ? 2 : 1);
-        compress_bias_kernel<<<(unsigned)(cols / 32), 256, 0, s>>>(a.slab, (int)ctas, cols, split, p.dba, p.dbb);
+        compress_bias_kernel<<<(unsigned)(cols / 32), 1024, 0, s>>>(a.slab, (int)ctas, cols, split, p.dba, p.dbb);
     }
     return csa2_launch_status();
 }

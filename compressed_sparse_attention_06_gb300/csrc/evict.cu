@@ -23,7 +23,9 @@ namespace {
 
 constexpr int EV_THREADS = 1024;
 constexpr int EV_BINS = 2048;
-constexpr int EV_CLUSTER_MAX = 8;
+constexpr int EV_CLUSTER_MAX = 16;      // where the device runs such clusters (more than 8 is not portable)
+constexpr int EV_PER_CTA = 8192;        // entries of a row that are worth another CTA
+constexpr unsigned FULL = 0xffffffffu;
 
 // Key of a weight: larger weight, larger key; NaN (of any sign) above +inf.
 __device__ __forceinline__ uint32_t evict_key(float x) { return isnan(x) ? 0xFFFFFFFFu : order_key(x); }
@@ -85,7 +87,7 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(EvictArgs a) {
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), nc = (int)cl.num_blocks();
     const int64_t b = blockIdx.x / nc;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     int64_t n = a.n_entries[b];
     if (n > a.ld) {
         if (rank == 0 && tid == 0) csa2_flag(a.st, CSA2_DEVBIT_RANGE);
@@ -114,9 +116,25 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(EvictArgs a) {
         const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
         for (int i = tid; i < EV_BINS; i += EV_THREADS) sh.hist[i] = 0;
         __syncthreads();
-        for (int64_t e = e0 + tid; e < e1; e += EV_THREADS) {
-            const uint32_t k = evict_key(acc[e]);
-            if ((k & mask) == prefix) atomicAdd(&sh.hist[(k >> shift) & ((1u << bits) - 1)], 1u);
+        // eight loads in flight a thread; lanes with lane 0's digit count together (weights that
+        // were never touched are all 0)
+        for (int64_t base = e0; base < e1; base += 8 * EV_THREADS) {
+            uint32_t key[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int64_t e = base + j * EV_THREADS + tid;
+                key[j] = e < e1 ? evict_key(acc[e]) : 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bool in = base + j * EV_THREADS + tid < e1 && (key[j] & mask) == prefix;
+                const uint32_t d = (key[j] >> shift) & ((1u << bits) - 1), d0 = __shfl_sync(FULL, d, 0);
+                const unsigned same = __ballot_sync(FULL, in && d == d0);
+                if (in && d != d0)
+                    atomicAdd(&sh.hist[d], 1u);
+                else if (same && lane == 0)
+                    atomicAdd(&sh.hist[d0], (uint32_t)__popc(same));
+            }
         }
         cl.sync();
         // the cluster's counts: two bins a thread, highest digit first
@@ -142,55 +160,124 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(EvictArgs a) {
         rest = sh.rest;
         __syncthreads();
     }
-    // kept: keys above the threshold, and the first `rest` of those at it, in entry order
+    // kept: keys above the threshold, and the first `rest` of those at it, in entry order.  Warp w
+    // owns a stretch of the CTA's entries: it counts both kinds, then writes its own.
+    const int64_t per_w = ((e1 - e0 + EV_THREADS - 1) / EV_THREADS) * 32;
+    const int64_t w0 = min(e1, e0 + wid * per_w), w1 = min(e1, w0 + per_w);
     uint32_t gt = 0, eq = 0;
-    for (int64_t e = e0 + tid; e < e1; e += EV_THREADS) {
-        const uint32_t k = evict_key(acc[e]);
-        gt += k > prefix;
-        eq += k == prefix;
+    for (int64_t base = w0; base < w1; base += 8 * 32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t e = base + j * 32 + lane;
+            const uint32_t k = e < w1 ? evict_key(acc[e]) : 0u;
+            gt += e < w1 && k > prefix;
+            eq += e < w1 && k == prefix;
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        gt += __shfl_xor_sync(FULL, gt, o);
+        eq += __shfl_xor_sync(FULL, eq, o);
     }
     uint32_t pg, pe, tg, te;
-    block_scan2(sh, gt, eq, pg, pe, tg, te);
+    block_scan2(sh, lane == 0 ? gt : 0u, lane == 0 ? eq : 0u, pg, pe, tg, te);
+    pg = __shfl_sync(FULL, pg, 0);                 // lane 0's prefixes: the warps before this one
+    pe = __shfl_sync(FULL, pe, 0);
     if (tid == 0) {
         sh.cnt_gt = tg;
         sh.cnt_eq = te;
     }
     cl.sync();
-    uint32_t gt0 = 0, eq0 = 0;                     // of the CTAs before this one
-    for (int r = 0; r < rank; ++r) {
-        gt0 += *cl.map_shared_rank(&sh.cnt_gt, r);
-        eq0 += *cl.map_shared_rank(&sh.cnt_eq, r);
+    for (int r = 0; r < rank; ++r) {               // and the CTAs before this one
+        pg += *cl.map_shared_rank(&sh.cnt_gt, r);
+        pe += *cl.map_shared_rank(&sh.cnt_eq, r);
     }
-    for (int64_t base = e0; base < e1; base += EV_THREADS) {
-        const int64_t e = base + tid;
-        const uint32_t k = e < e1 ? evict_key(acc[e]) : 0u;
-        const uint32_t g = e < e1 && k > prefix, q = e < e1 && k == prefix;
-        block_scan2(sh, g, q, pg, pe, tg, te);
-        // kept before this entry: all above the threshold, and of those at it at most `rest`
-        const uint32_t at = gt0 + pg + min(rest, eq0 + pe);
-        if (g || (q && eq0 + pe < rest)) out[at] = (int32_t)e;
-        gt0 += tg;
-        eq0 += te;
+    const unsigned below = (1u << lane) - 1u;
+    for (int64_t base = w0; base < w1; base += 8 * 32) {
+        uint32_t key[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t e = base + j * 32 + lane;
+            key[j] = e < w1 ? evict_key(acc[e]) : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t e = base + j * 32 + lane;
+            const bool g = e < w1 && key[j] > prefix, q = e < w1 && key[j] == prefix;
+            const unsigned mg = __ballot_sync(FULL, g), mq = __ballot_sync(FULL, q);
+            const uint32_t eqb = pe + __popc(mq & below);
+            // kept before this entry: all above the threshold, and of those at it at most `rest`
+            if (g || (q && eqb < rest)) out[pg + __popc(mg & below) + min(rest, eqb)] = (int32_t)e;
+            pg += __popc(mg);
+            pe += __popc(mq);
+        }
     }
     cl.sync();                                     // no CTA leaves while another reads its counts
 }
 
-// Rows dst[b, i] = src[b, idx[b, i]] in pieces of V; -1 leaves dst's row as it is.
+// Rows dst[b, i] = src[b, idx[b, i]] in pieces of V; -1 leaves dst's row as it is.  A block
+// moves `rows_b` rows: their ids go to shared memory, then each thread has up to eight pieces
+// in flight, adjacent threads adjacent pieces, so both sides are read and written in full
+// lines where rows are long and the destination always is.
+constexpr int GA_THREADS = 256, GA_PIECES = 8, GA_ROWS = 2048;
+
 template <typename V>
-__global__ void __launch_bounds__(256) cache_gather_kernel(const V* src, int pieces, int64_t N, const int32_t* idx,
-                                                           int64_t rows, int keep, V* dst, unsigned* st) {
-    const int64_t total = rows * pieces;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / pieces;
-        const int p = (int)(i - r * pieces);
-        const int32_t id = idx[r];
-        if (id < 0) continue;
-        if (id >= N) {
-            if (p == 0) csa2_flag(st, CSA2_DEVBIT_RANGE);
-            continue;
-        }
-        dst[i] = src[((r / keep) * N + id) * pieces + p];
+__global__ void __launch_bounds__(GA_THREADS) cache_gather_kernel(const V* src, uint32_t pieces, int64_t N,
+                                                                  const int32_t* idx, int64_t rows, uint32_t rows_b,
+                                                                  int keep, V* dst, unsigned* st) {
+    __shared__ int64_t from[GA_ROWS];              // first piece of the source row, -1 = leave
+    const int64_t r0 = (int64_t)blockIdx.x * rows_b;
+    const uint32_t nr = (uint32_t)min((int64_t)rows_b, rows - r0), total = nr * pieces;
+    for (uint32_t r = threadIdx.x; r < nr; r += GA_THREADS) {
+        const int64_t row = r0 + r;
+        const int32_t id = idx[row];
+        if (id >= N) csa2_flag(st, CSA2_DEVBIT_RANGE);
+        from[r] = id >= 0 && id < N ? ((row / keep) * N + id) * (int64_t)pieces : -1;
     }
+    __syncthreads();
+    V* out = dst + r0 * pieces;
+    for (uint32_t u0 = threadIdx.x; u0 < total; u0 += GA_THREADS * GA_PIECES) {
+        V v[GA_PIECES];
+        bool live[GA_PIECES];
+#pragma unroll
+        for (int j = 0; j < GA_PIECES; ++j) {
+            const uint32_t u = u0 + j * GA_THREADS;
+            const uint32_t r = u / pieces;
+            const int64_t f = u < total ? from[r] : -1;
+            live[j] = f >= 0;
+            if (live[j]) v[j] = __ldcs(src + f + (u - r * pieces));
+        }
+#pragma unroll
+        for (int j = 0; j < GA_PIECES; ++j)
+            if (live[j]) __stcs(out + u0 + j * GA_THREADS, v[j]);
+    }
+}
+
+// Whether clusters of 16 CTAs of the selection run on the device (asked once per device).
+bool evict_cluster16(int device) {
+    static std::atomic<int> known[64];             // 0 = not asked, 1 = no, 2 = yes
+    std::atomic<int>& k = known[device & 63];
+    int v = k.load(std::memory_order_relaxed);
+    if (v == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(16);
+        cfg.blockDim = dim3(EV_THREADS);
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 16;
+        at[0].val.clusterDim.y = 1;
+        at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        const bool ok = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+                            cudaSuccess &&
+                        cudaOccupancyMaxActiveClusters(&n, evict_select_kernel, &cfg) == cudaSuccess && n > 0;
+        (void)cudaGetLastError();
+        v = ok ? 2 : 1;
+        k.store(v, std::memory_order_relaxed);
+    }
+    return v == 2;
 }
 
 }  // namespace
@@ -204,9 +291,9 @@ extern "C" csa2_status csa2_evict_select(csa2_ctx* ctx, const float* acc, int B,
     if (!aligned(acc, 4) || !aligned(n_entries, 8) || !aligned(out_idx, 4)) return CSA2_ERR_INVALID_ARG;
     DeviceGuard dev(ctx);
     if (!dev.ok) return CSA2_ERR_CUDA;
-    // a CTA for every 8,192 entries of a row, at most a portable cluster of 8
     int nc = 1;
-    while (nc < EV_CLUSTER_MAX && (int64_t)nc * 8192 < ld) nc *= 2;
+    while (nc < 8 && (int64_t)nc * EV_PER_CTA < ld) nc *= 2;
+    if (nc == 8 && (int64_t)nc * EV_PER_CTA < ld && evict_cluster16(ctx->device)) nc = EV_CLUSTER_MAX;
     const EvictArgs a = {acc, ld, n_entries, keep, recent, out_idx, ctx->status};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(B * nc));
@@ -227,6 +314,7 @@ extern "C" csa2_status csa2_cache_gather(csa2_ctx* ctx, const void* src, int64_t
                                          const int32_t* idx, int keep, void* dst, void* stream) {
     if (!ctx || B < 0 || N < 0 || keep < 0 || row_bytes < 4 || row_bytes > (1 << 20)) return CSA2_ERR_INVALID_ARG;
     if (row_bytes % 4) return CSA2_ERR_UNSUPPORTED;
+    if (B > 65535) return CSA2_ERR_UNSUPPORTED;
     if (B == 0 || keep == 0) return CSA2_OK;
     if (!src || !idx || !dst || !aligned(src, 4) || !aligned(dst, 4) || !aligned(idx, 4)) return CSA2_ERR_INVALID_ARG;
     // moving rows within one buffer would overwrite rows before they are read
@@ -239,14 +327,16 @@ extern "C" csa2_status csa2_cache_gather(csa2_ctx* ctx, const void* src, int64_t
     const int64_t rows = (int64_t)B * keep;
     const bool wide = row_bytes % 16 == 0 && aligned(src, 16) && aligned(dst, 16);
     const int64_t pieces = row_bytes / (wide ? 16 : 4);
-    const int64_t blocks = std::min<int64_t>((rows * pieces + 255) / 256, (int64_t)ctx->num_sms * 64);
+    const int64_t rows_b = std::min<int64_t>(GA_ROWS, std::max<int64_t>(1, GA_THREADS * GA_PIECES / pieces));
+    const int64_t blocks = (rows + rows_b - 1) / rows_b;
+    if (blocks > 0x7FFFFFFF) return CSA2_ERR_UNSUPPORTED;
     if (wide)
-        cache_gather_kernel<uint4><<<(unsigned)blocks, 256, 0, s>>>(reinterpret_cast<const uint4*>(src), (int)pieces, N,
-                                                                   idx, rows, keep, reinterpret_cast<uint4*>(dst),
-                                                                   ctx->status);
+        cache_gather_kernel<uint4><<<(unsigned)blocks, GA_THREADS, 0, s>>>(
+            reinterpret_cast<const uint4*>(src), (uint32_t)pieces, N, idx, rows, (uint32_t)rows_b, keep,
+            reinterpret_cast<uint4*>(dst), ctx->status);
     else
-        cache_gather_kernel<uint32_t><<<(unsigned)blocks, 256, 0, s>>>(reinterpret_cast<const uint32_t*>(src),
-                                                                      (int)pieces, N, idx, rows, keep,
-                                                                      reinterpret_cast<uint32_t*>(dst), ctx->status);
+        cache_gather_kernel<uint32_t><<<(unsigned)blocks, GA_THREADS, 0, s>>>(
+            reinterpret_cast<const uint32_t*>(src), (uint32_t)pieces, N, idx, rows, (uint32_t)rows_b, keep,
+            reinterpret_cast<uint32_t*>(dst), ctx->status);
     return csa2_launch_status();
 }

@@ -510,7 +510,7 @@ csa2_status csa2_sparse_attn_noalloc(csa2_ctx* ctx,
  * Every wanted gradient is written in full: rows that no query attends to get 0.  An index
  * that appears twice in a query's idx counts twice, as in the forward.  Gradients must not
  * overlap the inputs or each other.  Row sums are added in query order without atomics:
- * the same call gives the same bits.
+ * the same call with the same workspace size gives the same bits.
  *
  * Workspace: csa2_attn_bwd_workspace_bytes() bytes (16-byte aligned) run the queries in one
  * chunk (in chunks that keep it under 16 GiB for the largest calls); any smaller one that
