@@ -36,7 +36,8 @@ EXPORTS = (
     "csa2_index_score_mxq",
     "csa2_sparse_attn_bwd", "csa2_dense_attn_bwd", "csa2_attn_bwd_workspace_bytes",
     "csa2_compress_bwd", "csa2_compress_bwd_workspace_bytes",
-    "csa2_attn_mass", "csa2_attn_mass_workspace_bytes", "csa2_evict_select", "csa2_cache_gather",
+    "csa2_attn_mass", "csa2_attn_mass_workspace_bytes", "csa2_evict_select",
+    "csa2_evict_select_workspace_bytes", "csa2_cache_gather",
 )
 
 
@@ -102,7 +103,8 @@ def _declare(lib):
         "csa2_attn_mass_workspace_bytes": (_sz, [_vp, _i, _i, _i, _i, _i, _i64, _i]),
         "csa2_attn_mass": (_i, [_vp, _vp, _i, _vp, _i, _i64, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _f, _u, _vp, _vp,
                                 _vp, _sz, _vp]),
-        "csa2_evict_select": (_i, [_vp, _vp, _i, _i64, _vp, _i, _i, _vp, _vp]),
+        "csa2_evict_select_workspace_bytes": (_sz, [_i, _i64]),
+        "csa2_evict_select": (_i, [_vp, _vp, _i, _i64, _vp, _i, _i, _vp, _vp, _sz, _vp]),
         "csa2_cache_gather": (_i, [_vp, _vp, _i64, _i, _i64, _vp, _i, _vp, _vp]),
     }
     for name, (res, args) in sig.items():
@@ -744,15 +746,20 @@ def csa2_attn_mass(q, kv, q_pos, lse, idx=None, n_visible=None, k_max: int = 0, 
     return weights, acc
 
 
-def csa2_evict_select(acc, n_entries, keep: int, recent: int = 0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+def csa2_evict_select(acc, n_entries, keep: int, recent: int = 0, out: Optional[torch.Tensor] = None,
+                      ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Entries [B, keep] int32 (ascending, -1 padded) that stay when rows of n_entries[b]
-    entries are cut to `keep`: the newest `recent`, and the best others by acc [B, ld] f32."""
+    entries are cut to `keep`: the newest `recent`, and the best others by acc [B, ld] f32.
+    `ws` is the workspace of long rows (allocated here when not given)."""
     B, ld = acc.shape
     _want("acc", acc, (B, ld), torch.float32, acc.device)
     _want("n_entries", n_entries, (B,), torch.int64, acc.device)
     out = _given("out", out, (B, keep), torch.int32, acc.device)
-    st = _lib().csa2_evict_select(ctx(acc.device.index), _p(acc), B, ld, _p(n_entries), keep, recent, _p(out),
-                                  _stream(acc))
+    need = int(_lib().csa2_evict_select_workspace_bytes(B, ld))
+    if ws is None and need:
+        ws = _ws(need, acc.device)
+    st = _lib().csa2_evict_select(ctx(acc.device.index), _p(acc), B, ld, _p(n_entries), keep, recent, _p(out), _p(ws),
+                                  ws.numel() * ws.element_size() if ws is not None else 0, _stream(acc))
     _check("csa2_evict_select", st)
     return out
 

@@ -608,6 +608,8 @@ csa2_status csa2_attn_mass(csa2_ctx* ctx,
  *   acc       : [B, ld] f32 (the first n_entries[b] of a row are read)
  *   n_entries : [B] int64, device; one above ld is taken as ld and flagged
  *   out_idx   : [B, keep] int32, entry ids ascending, -1 padded
+ *   ws        : csa2_evict_select_workspace_bytes() bytes, 16-byte aligned (NULL will do if
+ *               that is 0: rows of up to 65,536 entries)
  * keep >= 1, 0 <= recent <= keep, B <= 65535.
  *
  * csa2_cache_gather -- moves the kept rows of a cache together: dst[b, i] = src[b, idx[b, i]]
@@ -620,8 +622,9 @@ csa2_status csa2_attn_mass(csa2_ctx* ctx,
  * their own rotation, so attention over them is unchanged, while the visible count of a
  * sequence becomes the number of entries it kept.
  */
+size_t csa2_evict_select_workspace_bytes(int B, int64_t ld);
 csa2_status csa2_evict_select(csa2_ctx* ctx, const float* acc, int B, int64_t ld, const int64_t* n_entries,
-                              int keep, int recent, int32_t* out_idx, void* stream);
+                              int keep, int recent, int32_t* out_idx, void* ws, size_t ws_bytes, void* stream);
 csa2_status csa2_cache_gather(csa2_ctx* ctx, const void* src, int64_t row_bytes, int B, int64_t N,
                               const int32_t* idx, int keep, void* dst, void* stream);
 

@@ -126,7 +126,7 @@ def test_mass_flags_an_out_of_range_index():
 
 @pytest.mark.parametrize("B,ld,keep,recent", [
     (1, 1, 1, 0), (3, 7, 3, 1), (2, 1000, 400, 400), (2, 1000, 999, 0), (4, 9001, 4001, 128), (2, 20000, 1, 0),
-    (1, 70001, 35000, 1000), (3, 65536, 65535, 7), (2, 8192, 9000, 100), (70, 300, 100, 10)])
+    (1, 70001, 35000, 1000), (3, 65536, 65535, 7), (3, 65537, 60000, 0), (2, 300001, 299999, 131072), (3, 200000, 17, 16), (2, 8192, 9000, 100), (70, 300, 100, 10)])
 def test_select(B, ld, keep, recent):
     """Ties (a coarse grid of weights), rows of any length from 0 to ld, signed zeros, infinities."""
     g = torch.Generator(DEV).manual_seed(ld)
@@ -148,10 +148,11 @@ def test_select(B, ld, keep, recent):
         assert np.array_equal(idx[b].cpu().numpy(), G.evict_keep(a[b], int(n[b]), keep, recent)), f"row {b}"
 
 
-def test_select_all_equal_and_length_above_ld():
-    acc = torch.full((2, 30000), 0.25, device=DEV)
-    idx = C.csa2_evict_select(acc, torch.tensor([30000, 30001], device=DEV), 12345, recent=45)
-    want = torch.cat([torch.arange(12300), torch.arange(29955, 30000)]).to(torch.int32)
+@pytest.mark.parametrize("ld", [30000, 130000])
+def test_select_all_equal_and_length_above_ld(ld):
+    acc = torch.full((2, ld), 0.25, device=DEV)
+    idx = C.csa2_evict_select(acc, torch.tensor([ld, ld + 1], device=DEV), 12345, recent=45)
+    want = torch.cat([torch.arange(12300), torch.arange(ld - 45, ld)]).to(torch.int32)
     assert torch.equal(idx[0].cpu(), want) and torch.equal(idx[1].cpu(), want)
     with pytest.raises(C.Csa2Error) as e:
         C.csa2_ctx_check()

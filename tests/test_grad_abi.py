@@ -69,10 +69,11 @@ def test_mass_refuses(lib, ctx, kw, want):
 @pytest.mark.parametrize("kw,want", [
     (dict(ctx=None), BAD), (dict(B=-1), BAD), (dict(ld=-1), BAD), (dict(ld=1 << 31), BAD), (dict(keep=0), BAD),
     (dict(recent=-1), BAD), (dict(recent=9), BAD), (dict(n=None), BAD), (dict(out=None), BAD), (dict(acc=None), BAD),
-    (dict(B=65536), UNS), (dict(n=P + 4), BAD),
+    (dict(B=65536), UNS), (dict(n=P + 4), BAD), (dict(ld=65537), BAD), (dict(ld=65537, ws=P, ws_bytes=49152 + 79), BAD),
+    (dict(ld=65537, ws=P + 8, ws_bytes=1 << 20), BAD),
 ])
 def test_select_refuses(lib, ctx, kw, want):
-    a = dict(ctx=ctx, acc=P, B=2, ld=100, n=P, keep=8, recent=2, out=P, stream=None)
+    a = dict(ctx=ctx, acc=P, B=2, ld=100, n=P, keep=8, recent=2, out=P, ws=None, ws_bytes=0, stream=None)
     a.update(kw)
     assert lib.csa2_evict_select(*a.values()) == want
 
@@ -110,6 +111,8 @@ def test_workspace_sizes(lib, ctx):
     assert big <= 16 << 30
     assert lib.csa2_attn_bwd_workspace_bytes(None, 1, 1, 1, 1, 1, 4, 64, 512, 128, 2048, 128, 7) == 0
     assert lib.csa2_attn_mass_workspace_bytes(ctx, C.BF16, 8, 1, 64, 512, 1 << 20, 1) == 0      # no per-entry table for Q = 1
+    assert lib.csa2_evict_select_workspace_bytes(8, 65536) == 0
+    assert lib.csa2_evict_select_workspace_bytes(2, 65537) == 2 * 3 * 2048 * 4 + 2 * 5 * 2 * 4
     assert lib.csa2_compress_bwd_workspace_bytes(1, 8192, 512, 4, 1) > 0
     assert lib.csa2_compress_bwd_workspace_bytes(0, 8192, 512, 4, 1) == 0
 
