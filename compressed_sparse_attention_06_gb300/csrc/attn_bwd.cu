@@ -197,13 +197,13 @@ __global__ void __launch_bounds__(128) bwd_sink_sum_kernel(const float* part, in
 // warp per row.
 template <typename TQ, typename TO>
 __global__ void __launch_bounds__(256) bwd_prep_kernel(const TQ* q, const TO* dout, const TO* out, const int64_t* q_pos,
-                                                       int64_t bq0, int64_t n_rows, int H, RopeTable rope,
+                                                       int64_t bq0, int64_t n_rows, int H, AgRope rope,
                                                        unsigned flags, float* qh, float* dh, float* D) {
     __shared__ float cs[8][32], sn[8][32];
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r = (int64_t)blockIdx.x * 8 + w;
     if (r >= n_rows) return;
-    rope_cos_sin(rope, q_pos[bq0 + r / H], lane, cs[w][lane], sn[w][lane]);
+    ag_cos_sin(rope, q_pos[bq0 + r / H], lane, cs[w][lane], sn[w][lane]);
     __syncwarp();
     const int64_t src = (bq0 * H + r) * AG_C + 16 * lane, dst = r * AG_C + 16 * lane;
     float v[16];
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(256, 2) bwd_simt_q_kernel(BwdChunk c, const fl
     const int h = blockIdx.x * SB_HG + w;
     const bool live = h < c.H;
     const int64_t bq = c.bq0 + q;
-    if (threadIdx.x < 32) rope_cos_sin(c.rope, c.slots.q_pos[bq], lane, cs[lane], sn[lane]);
+    if (threadIdx.x < 32) ag_cos_sin(c.rope, c.slots.q_pos[bq], lane, cs[lane], sn[lane]);
     float qv[16], dv[16], acc[16];
     const int64_t hr = (int64_t)q * c.H + h;
 #pragma unroll
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(256) bwd_simt_dq_kernel(BwdChunk c, const floa
     const int64_t hr = (int64_t)blockIdx.x * 8 + w;
     if (hr >= (int64_t)c.nb * c.H) return;
     const int64_t bq = c.bq0 + hr / c.H;
-    rope_cos_sin(c.rope, c.slots.q_pos[bq], lane, cs[w][lane], sn[w][lane]);
+    ag_cos_sin(c.rope, c.slots.q_pos[bq], lane, cs[w][lane], sn[w][lane]);
     __syncwarp();
     float qv[16], acc[16];
 #pragma unroll
@@ -680,7 +680,7 @@ csa2_status bwd_run(csa2_ctx* ctx, const BwdCall& a, void* ws, size_t ws_bytes, 
     c.H = a.H;
     c.n_slots = n_slots;
     c.flags = a.flags;
-    c.rope = make_rope_table(a.rope_base);
+    c.rope = make_ag_rope(a.rope_base);
     uint32_t* cnt = reinterpret_cast<uint32_t*>(base + L.cnt);
     uint32_t* loc = reinterpret_cast<uint32_t*>(base + L.loc);
     uint32_t* tot = reinterpret_cast<uint32_t*>(base + L.tot);

@@ -145,13 +145,13 @@ __device__ __forceinline__ float ex2_approx(float x) {
 // head h (within its pass): 32 (h / 16) + h % 16 for q^, 16 more for do'.  Heads past H are 0.
 __global__ void __launch_bounds__(256) bwd_tc_prep_kernel(const __nv_bfloat16* q, const __nv_bfloat16* dout,
                                                           const __nv_bfloat16* out, const int64_t* q_pos, int64_t bq0,
-                                                          int nb, int H, RopeTable rope, unsigned flags, uint8_t* img,
+                                                          int nb, int H, AgRope rope, unsigned flags, uint8_t* img,
                                                           float* D) {
     __shared__ float cs[32], sn[32];
     const int qi = blockIdx.y, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t bq = bq0 + qi;
     const int h = blockIdx.x * 8 + w;
-    if (threadIdx.x < 32) rope_cos_sin(rope, q_pos[bq], lane, cs[lane], sn[lane]);
+    if (threadIdx.x < 32) ag_cos_sin(rope, q_pos[bq], lane, cs[lane], sn[lane]);
     float v[16], g[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = g[i] = 0.0f;
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(256) bwd_tc_dq_kernel(BwdTcArgs a, const float
     if (r >= (int64_t)a.c.nb * a.c.H) return;
     const int qi = (int)(r / a.c.H), h = (int)(r % a.c.H);
     const int64_t bq = a.c.bq0 + qi, o = (bq * a.c.H + h) * BT_C + 16 * lane;
-    rope_cos_sin(a.c.rope, a.c.slots.q_pos[bq], lane, cs[w][lane], sn[w][lane]);
+    ag_cos_sin(a.c.rope, a.c.slots.q_pos[bq], lane, cs[w][lane], sn[w][lane]);
     __syncwarp();
     float g[16], v[16];
 #pragma unroll

@@ -11,6 +11,24 @@
 constexpr int AG_C = 512;                // head dim
 constexpr float AG_LOG2E = 1.4426950408889634f;
 
+// RoPE angles in turns, as 64-bit fractions of a turn: position * fraction modulo 2^64 is the
+// angle modulo a turn for any position, in integer arithmetic (64-bit floating point, which the
+// exact product would take otherwise, is very slow on this part: a kernel that turned every
+// entry's rows waited for it).  theta_j = base^(-2j/64); the fraction is exact to 2^-53 of it.
+struct AgRope {
+    uint64_t frac[32];
+};
+static inline AgRope make_ag_rope(float base) {
+    AgRope r;
+    for (int j = 0; j < 32; ++j)
+        r.frac[j] = (uint64_t)ldexp(pow((double)base, -2.0 * (double)j / 64.0) / 6.283185307179586, 64);
+    return r;
+}
+__device__ __forceinline__ void ag_cos_sin(const AgRope& r, int64_t pos, int j, float& c, float& s) {
+    const uint64_t turn = (uint64_t)pos * r.frac[j];
+    sincospif((float)(uint32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);     // 2 turns / 2^32 = 2^-31
+}
+
 // The key slots of the queries: first the k cache slots (idx, or entries 0 .. nv-1 in
 // the dense form), then `window` window slots.  Window slot w of a query at position t
 // is position t - window + 1 + w; slots at negative positions are empty.
@@ -185,7 +203,7 @@ struct BwdChunk {
     int nb;                   // its queries
     int H, n_slots;
     unsigned flags;
-    RopeTable rope;
+    AgRope rope;
     // the chunk's scatter plan: the contribution of (query bq, slot s) to its row goes to
     // place blk[row / BWD_SCAN_ROWS] + base[group][row] + rank[bq - bq0][s] of `part`
     const int32_t* rank;      // [nb, n_slots], -1 = empty slot

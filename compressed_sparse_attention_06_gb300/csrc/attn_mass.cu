@@ -28,12 +28,12 @@ __global__ void __launch_bounds__(256) mass_finish_kernel(const unsigned long lo
 // q^ of every (query, head) in fp32; a warp per head row.
 template <typename TQ>
 __global__ void __launch_bounds__(256) mass_prep_kernel(const TQ* q, const int64_t* q_pos, int64_t n_rows, int H,
-                                                        RopeTable rope, unsigned flags, float* qh) {
+                                                        AgRope rope, unsigned flags, float* qh) {
     __shared__ float cs[8][32], sn[8][32];
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r = (int64_t)blockIdx.x * 8 + w;
     if (r >= n_rows) return;
-    rope_cos_sin(rope, q_pos[r / H], lane, cs[w][lane], sn[w][lane]);
+    ag_cos_sin(rope, q_pos[r / H], lane, cs[w][lane], sn[w][lane]);
     __syncwarp();
     float v[16];
     ag_load16<TQ>(q + r * AG_C + 16 * lane, v);
@@ -190,7 +190,7 @@ extern "C" csa2_status csa2_attn_mass(csa2_ctx* ctx, const void* q, csa2_dtype q
     a.q_dt = q_dt;
     a.kv = kv;
     a.kv_dt = kv_dt;
-    a.rope = make_rope_table(rope_base);
+    a.rope = make_ag_rope(rope_base);
     a.n_bq = (int64_t)B * Q;
     a.passes = H > 64 && !weights ? reinterpret_cast<float*>(base + L.passes) : nullptr;
     a.qh = reinterpret_cast<const float*>(base + L.qh);

@@ -12,7 +12,7 @@ struct MassArgs {
     const float *qh, *lse;    // qh: CUDA-core path only
     int H;
     unsigned flags;
-    RopeTable rope;
+    AgRope rope;
     int64_t n_bq;
     float *weights, *acc;     // either may be NULL
     unsigned long long* fix;  // addends of acc meet here in units of 2^-39, or NULL: straight to acc

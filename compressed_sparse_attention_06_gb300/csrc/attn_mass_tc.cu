@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) mass_tc_kernel(const MassTcArgs
             if (it.nt == 0) continue;
             const int64_t t = a.m.slots.q_pos[it.bq];
             float c1 = 1.0f, s1 = 0.0f;                       // lane j: angle j (64-bit arithmetic: one a lane)
-            if (a.m.flags & CSA2_ROPE) rope_cos_sin(a.m.rope, t, lane, c1, s1);
+            if (a.m.flags & CSA2_ROPE) ag_cos_sin(a.m.rope, t, lane, c1, s1);
             for (int pass = 0; pass < a.n_pass && ok; ++pass, ++n) {
                 // this warp's 8 heads, two at a time: half a warp a head, lane l its channels
                 // 16 (l & 15) + 256 e, e = 0, 1.  The first two are loaded, the others are on their

@@ -20,6 +20,8 @@
 
 namespace {
 
+// CTAs: what the registers keep resident at c = 512 -- windows of 1 or 2 rows, and the general
+// kernel, 8 an SM; of 4 rows 4; of 8 rows 2.
 constexpr int CB_CTAS = 152 * 8;
 
 template <typename T>
@@ -58,7 +60,7 @@ struct CompressBwdArgs {
     int64_t n_tokens, n_ent, entries;   // entries of one stream, of all
     int c, m;
     const int64_t* pos0;
-    RopeTable rope;
+    AgRope rope;
     unsigned flags;
     const void* dout;
     int dout_f32;
@@ -162,15 +164,15 @@ __device__ __forceinline__ void st(__nv_bfloat16* p, const float (&v)[2]) {
 __device__ __forceinline__ void st(__nv_bfloat16* p, const float (&v)[4]) { st4<__nv_bfloat16>(p, v); }
 
 // Windows of M block rows and (OV) M history rows; CH channels a thread, c / CH threads.
-template <typename T, int M, bool OV, int CH>
-__global__ void __launch_bounds__(1024 / CH) compress_bwd_kernel(CompressBwdArgs<T> a) {
+template <typename T, int M, bool OV, int CH, bool BIAS>
+__global__ void __launch_bounds__(1024 / CH, (OV ? 2 * M : M) <= 2 ? 4 : (CH == 4 ? 2 : 1)) compress_bwd_kernel(CompressBwdArgs<T> a) {
     constexpr int R = OV ? 2 * M : M;
     __shared__ float2 red[2][16];
     const int ch = CH * threadIdx.x, c = a.c;
     const int64_t e0 = (int64_t)blockIdx.x * a.run, e1 = min(a.entries, e0 + a.run);
-    float db[R][CH];
+    float db[BIAS ? R : 1][CH];
 #pragma unroll
-    for (int j = 0; j < R; ++j)
+    for (int j = 0; j < (BIAS ? R : 1); ++j)
 #pragma unroll
         for (int k = 0; k < CH; ++k) db[j][k] = 0.0f;
     int64_t b = e0 / a.n_ent, i = e0 - b * a.n_ent;
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(1024 / CH) compress_bwd_kernel(CompressBwdArgs
 #pragma unroll
             for (int p = 0; p < CH / 2; ++p) {
                 float cs, sn;
-                rope_cos_sin(a.rope, pos, (ch + 2 * p - (c - 64)) >> 1, cs, sn);
+                ag_cos_sin(a.rope, pos, (ch + 2 * p - (c - 64)) >> 1, cs, sn);
                 const float x0 = g[2 * p], x1 = g[2 * p + 1];
                 g[2 * p] = x0 * cs + x1 * sn;
                 g[2 * p + 1] = x1 * cs - x0 * sn;
@@ -291,9 +293,9 @@ __global__ void __launch_bounds__(1024 / CH) compress_bwd_kernel(CompressBwdArgs
                 if (w.g1) st(w.g1 + o, dc);
                 if (w.h1) st(w.h1 + o, dz);
             }
-            if (!OV || j < M || hist)
+            if (BIAS && (!OV || j < M || hist))
 #pragma unroll
-                for (int k = 0; k < CH; ++k) db[j][k] += dz[k];
+                for (int k = 0; k < CH; ++k) db[BIAS ? j : 0][k] += dz[k];
         }
         if (OV && here_i == a.n_ent - 1) {
             // the stream's last block is nobody's history within this call
@@ -307,11 +309,21 @@ __global__ void __launch_bounds__(1024 / CH) compress_bwd_kernel(CompressBwdArgs
             }
         }
     }
-    if (a.slab) {
+    if (BIAS) {
         float* slab = a.slab + (int64_t)blockIdx.x * R * c + ch;
 #pragma unroll
-        for (int j = 0; j < R; ++j) st(slab + (int64_t)j * c, db[j]);
+        for (int j = 0; j < (BIAS ? R : 1); ++j) st(slab + (int64_t)j * c, db[j]);
     }
+}
+
+// The usual windows; the bias sums' registers only where a bias gradient is wanted.
+template <typename T, int M, bool OV, int CH>
+void usual_window(const CompressBwdArgs<T>& a, unsigned grid, cudaStream_t s) {
+    const unsigned threads = (unsigned)(a.c / CH);
+    if (a.slab)
+        compress_bwd_kernel<T, M, OV, CH, true><<<grid, threads, 0, s>>>(a);
+    else
+        compress_bwd_kernel<T, M, OV, CH, false><<<grid, threads, 0, s>>>(a);
 }
 
 // Any m: four channels a thread, the window's rows read once for the maximum, once for the sums
@@ -375,7 +387,7 @@ __global__ void __launch_bounds__(256) compress_bwd_any_kernel(CompressBwdArgs<T
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 float cs, sn;
-                rope_cos_sin(a.rope, pos, (ch + 2 * p - (c - 64)) >> 1, cs, sn);
+                ag_cos_sin(a.rope, pos, (ch + 2 * p - (c - 64)) >> 1, cs, sn);
                 const float x0 = g[2 * p], x1 = g[2 * p + 1];
                 g[2 * p] = x0 * cs + x1 * sn;
                 g[2 * p + 1] = x1 * cs - x0 * sn;
@@ -453,8 +465,8 @@ __global__ void __launch_bounds__(1024) compress_bias_kernel(const float* slab, 
     }
 }
 
-int64_t cb_ctas(int64_t entries) {
-    const int64_t run = (entries + CB_CTAS - 1) / CB_CTAS;
+int64_t cb_ctas(int64_t entries, int most = CB_CTAS) {
+    const int64_t run = (entries + most - 1) / most;
     return run > 0 ? (entries + run - 1) / run : 0;
 }
 
@@ -491,7 +503,7 @@ csa2_status cb_launch(const CompressBwdCall& p, cudaStream_t s) {
     a.c = p.c;
     a.m = p.m;
     a.pos0 = p.pos0;
-    a.rope = make_rope_table(p.rope_base);
+    a.rope = make_ag_rope(p.rope_base);
     a.flags = p.flags;
     a.dout = p.dout;
     a.dout_f32 = p.dout_dt == CSA2_F32;
@@ -503,23 +515,24 @@ csa2_status cb_launch(const CompressBwdCall& p, cudaStream_t s) {
     a.dprev_cb = reinterpret_cast<T*>(p.dprev_cb);
     a.dprev_zb = reinterpret_cast<T*>(p.dprev_zb);
     a.slab = p.dba || p.dbb ? p.slab : nullptr;
-    const int64_t ctas = cb_ctas(a.entries);
+    const int rows = p.cb ? 2 * p.m : p.m;
+    const int64_t ctas = cb_ctas(a.entries, rows == 8 ? CB_CTAS / 4 : (rows == 4 ? CB_CTAS / 2 : CB_CTAS));
     a.run = (a.entries + ctas - 1) / ctas;
-    const unsigned grid = (unsigned)ctas, c4 = (unsigned)(p.c / 4), c2 = (unsigned)(p.c / 2);
+    const unsigned grid = (unsigned)ctas, c4 = (unsigned)(p.c / 4);
     if (!p.cb && p.m == 1)
-        compress_bwd_kernel<T, 1, false, 4><<<grid, c4, 0, s>>>(a);
+        usual_window<T, 1, false, 4>(a, grid, s);
     else if (!p.cb && p.m == 2)
-        compress_bwd_kernel<T, 2, false, 4><<<grid, c4, 0, s>>>(a);
+        usual_window<T, 2, false, 4>(a, grid, s);
     else if (!p.cb && p.m == 4)
-        compress_bwd_kernel<T, 4, false, 4><<<grid, c4, 0, s>>>(a);
+        usual_window<T, 4, false, 4>(a, grid, s);
     else if (!p.cb && p.m == 8)
-        compress_bwd_kernel<T, 8, false, 2><<<grid, c2, 0, s>>>(a);
+        usual_window<T, 8, false, 2>(a, grid, s);
     else if (p.cb && p.m == 1)
-        compress_bwd_kernel<T, 1, true, 4><<<grid, c4, 0, s>>>(a);
+        usual_window<T, 1, true, 4>(a, grid, s);
     else if (p.cb && p.m == 2)
-        compress_bwd_kernel<T, 2, true, 4><<<grid, c4, 0, s>>>(a);
+        usual_window<T, 2, true, 4>(a, grid, s);
     else if (p.cb && p.m == 4)
-        compress_bwd_kernel<T, 4, true, 2><<<grid, c2, 0, s>>>(a);
+        usual_window<T, 4, true, 2>(a, grid, s);
     else
         compress_bwd_any_kernel<T><<<grid, c4, 0, s>>>(a);
     if (a.slab) {

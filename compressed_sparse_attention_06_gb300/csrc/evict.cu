@@ -115,6 +115,16 @@ __device__ __forceinline__ void block_scan2(uint32_t (*tot)[32], uint32_t a, uin
     pb = (w > 0 ? bb : 0u) + ib - b;
 }
 
+// Keys of 16 entries, `step` apart from `e` on; past `end` the last one's (end > 0; the caller
+// masks them).  Loads without a condition, so that all are in flight together.
+__device__ __forceinline__ void load_keys(const float* __restrict__ acc, int64_t e, int step, int64_t end, uint32_t (&key)[16]) {
+    float x[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] = __ldg(acc + min(e + j * step, end - 1));
+#pragma unroll
+    for (int j = 0; j < 16; ++j) key[j] = evict_key(x[j]);
+}
+
 __device__ __forceinline__ int digit_shift(int pass) { return pass == 0 ? 21 : (pass == 1 ? 10 : 0); }
 __device__ __forceinline__ int digit_bits(int pass) { return pass == 2 ? 10 : 11; }
 
@@ -292,11 +302,7 @@ __global__ void __launch_bounds__(EL_THREADS) evict_long_count_kernel(EvictArgs 
     const float* acc = a.acc + b * a.ld;
     for (int64_t base = e0; base < e1; base += 16 * EL_THREADS) {
         uint32_t key[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const int64_t e = base + j * EL_THREADS + threadIdx.x;
-            key[j] = e < e1 ? evict_key(acc[e]) : 0u;
-        }
+        load_keys(acc, base + threadIdx.x, EL_THREADS, e1, key);
 #pragma unroll
         for (int j = 0; j < 16; ++j)
             count_digit(hist, base + j * EL_THREADS + threadIdx.x < e1 && (key[j] & mask) == prefix,
@@ -328,11 +334,7 @@ __global__ void __launch_bounds__(EL_THREADS) evict_long_write_kernel(EvictArgs 
     uint32_t gt = 0, eq = 0;
     for (int64_t base = w0; base < w1; base += 16 * 32) {
         uint32_t key[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const int64_t e = base + j * 32 + lane;
-            key[j] = e < w1 ? evict_key(acc[e]) : 0u;
-        }
+        load_keys(acc, base + lane, 32, w1, key);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
             const bool in = base + j * 32 + lane < w1;
@@ -372,11 +374,7 @@ __global__ void __launch_bounds__(EL_THREADS) evict_long_write_kernel(EvictArgs 
     int32_t* out = a.out + b * (int64_t)a.keep;
     for (int64_t base = w0; base < w1; base += 16 * 32) {
         uint32_t key[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const int64_t e = base + j * 32 + lane;
-            key[j] = e < w1 ? evict_key(acc[e]) : 0u;
-        }
+        load_keys(acc, base + lane, 32, w1, key);
 #pragma unroll
         for (int j = 0; j < 16; ++j) emit(out, base + j * 32 + lane, base + j * 32 + lane < w1, key[j], T, rest, pg, pe);
     }
