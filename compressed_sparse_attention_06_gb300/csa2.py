@@ -587,9 +587,28 @@ def csa2_sparse_attn_noalloc(q, kv, idx, swa, q_pos, out: torch.Tensor, sink=Non
 def _want(name, t, shape, dtype, device) -> torch.Tensor:
     """An output or buffer the caller gave: the kernels write (read) it by the call's sizes, so
     its shape, dtype, device and layout are checked before its pointer is passed on."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t
+
+
+def _a(t: Optional[torch.Tensor]):
+    """The address of a tensor that _want or _main has checked (None: NULL)."""
+    return None if t is None else t.data_ptr()
+
+
+def _main(t: torch.Tensor) -> int:
+    """The address of the tensor that gives a call its device: a contiguous CUDA tensor."""
+    if not t.is_cuda:
+        raise ValueError("CSA2 tensors must be CUDA tensors")
+    if not t.is_contiguous():
+        raise ValueError("CSA2 tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _on(device: torch.device) -> int:
+    """The current stream of a device, as the library takes it."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _given(name, t, shape, dtype, device) -> torch.Tensor:
@@ -625,10 +644,10 @@ def _attn_bwd(fn, q, kv, sel, k, swa, q_pos, sink, out, lse, dout, window, swa_p
     if ws is None:
         ws = _ws(_lib().csa2_attn_bwd_workspace_bytes(ctx(dev.index), _dt(q), kv_dt, swa_dt, _dt(out), B, Q, H, k, window,
                                                       N, cap, flags), dev)
-    st = getattr(_lib(), fn)(ctx(dev.index), _p(q), _dt(q), _p(kv), kv_dt, N, _p(sel), k, _p(swa), swa_dt, cap, swa_pos0,
-                             window, _p(q_pos), _p(sink), _p(out), _p(dout), _dt(out), _p(lse), B, Q, H, c, rope_base,
-                             flags, _p(dq), _p(dkv), _p(dswa), _p(dsink), _p(ws), ws.numel() * ws.element_size(),
-                             _stream(q))
+    st = getattr(_lib(), fn)(ctx(dev.index), _main(q), _dt(q), _a(kv), kv_dt, N, _a(sel), k, _a(swa), swa_dt, cap,
+                             swa_pos0, window, _a(q_pos), _a(sink), _a(out), _a(dout), _dt(out), _a(lse), B, Q, H, c,
+                             rope_base, flags, _a(dq), _a(dkv), _a(dswa), _a(dsink), _p(ws),
+                             ws.numel() * ws.element_size(), _on(dev))
     _check(fn, st)
     return dq, dkv, dswa, dsink
 
@@ -696,18 +715,18 @@ def csa2_compress_bwd(ca, za, m: int, dout, cb=None, zb=None, ba=None, bb=None, 
     if isinstance(pos0, torch.Tensor):
         pos_t = _want("pos0", pos0.to(device=dev, dtype=torch.int64).contiguous(), (B,), torch.int64, dev)
     else:
-        pos_t = torch.full((B,), int(pos0), dtype=torch.int64, device=dev)
+        pos_t = torch.full((B,), int(pos0), dtype=torch.int64, device=dev) if pos0 else None
 
     def like(t):
-        return alloc(tuple(t.shape), dtype=t.dtype, device=dev) if t is not None else None
+        return alloc(t.shape, dtype=t.dtype, device=dev) if t is not None else None
 
     g = CompressGrads(like(ca), like(za), like(cb), like(zb), like(prev_cb), like(prev_zb), like(ba), like(bb))
     if ws is None and (ba is not None or bb is not None):
         ws = _ws(_lib().csa2_compress_bwd_workspace_bytes(B, n, c, m, int(cb is not None)), dev)
-    st = _lib().csa2_compress_bwd(ctx(dev.index), _p(ca), _p(za), _p(cb), _p(zb), _dt(ca), _p(ba), _p(bb), _p(prev_cb),
-                                  _p(prev_zb), B, n, c, m, _p(pos_t), rope_base, flags, _p(dout), _dt(dout), n // m,
-                                  _p(g.dca), _p(g.dza), _p(g.dcb), _p(g.dzb), _p(g.dprev_cb), _p(g.dprev_zb), _p(g.dba),
-                                  _p(g.dbb), _p(ws), ws.numel() * ws.element_size() if ws is not None else 0, _stream(ca))
+    st = _lib().csa2_compress_bwd(ctx(dev.index), _main(ca), _a(za), _a(cb), _a(zb), _dt(ca), _a(ba), _a(bb), _a(prev_cb),
+                                  _a(prev_zb), B, n, c, m, _a(pos_t), rope_base, flags, _a(dout), _dt(dout), n // m,
+                                  _a(g.dca), _a(g.dza), _a(g.dcb), _a(g.dzb), _a(g.dprev_cb), _a(g.dprev_zb), _a(g.dba),
+                                  _a(g.dbb), _p(ws), ws.numel() * ws.element_size() if ws is not None else 0, _on(dev))
     _check("csa2_compress_bwd", st)
     return g
 
@@ -738,10 +757,11 @@ def csa2_attn_mass(q, kv, q_pos, lse, idx=None, n_visible=None, k_max: int = 0, 
     if want_weights or weights is not None:
         weights = _given("weights", weights, (B, Q, k), torch.float32, dev)
     if ws is None:
-        ws = _ws(_lib().csa2_attn_mass_workspace_bytes(ctx(dev.index), kv_dt, B, Q, H, k, N, int(acc is not None)), dev)
-    st = _lib().csa2_attn_mass(ctx(dev.index), _p(q), _dt(q), _p(kv), kv_dt, N, _p(idx), _p(n_visible), k, _p(q_pos),
-                               _p(lse), B, Q, H, c, rope_base, flags, _p(weights), _p(acc), _p(ws),
-                               ws.numel() * ws.element_size(), _stream(q))
+        need = _lib().csa2_attn_mass_workspace_bytes(ctx(dev.index), kv_dt, B, Q, H, k, N, int(acc is not None))
+        ws = _ws(need, dev) if need else None
+    st = _lib().csa2_attn_mass(ctx(dev.index), _main(q), _dt(q), _a(kv), kv_dt, N, _a(idx), _a(n_visible), k, _a(q_pos),
+                               _a(lse), B, Q, H, c, rope_base, flags, _a(weights), _a(acc), _p(ws),
+                               ws.numel() * ws.element_size() if ws is not None else 0, _on(dev))
     _check("csa2_attn_mass", st)
     return weights, acc
 
@@ -758,8 +778,8 @@ def csa2_evict_select(acc, n_entries, keep: int, recent: int = 0, out: Optional[
     need = int(_lib().csa2_evict_select_workspace_bytes(B, ld))
     if ws is None and need:
         ws = _ws(need, acc.device)
-    st = _lib().csa2_evict_select(ctx(acc.device.index), _p(acc), B, ld, _p(n_entries), keep, recent, _p(out), _p(ws),
-                                  ws.numel() * ws.element_size() if ws is not None else 0, _stream(acc))
+    st = _lib().csa2_evict_select(ctx(acc.device.index), _main(acc), B, ld, _a(n_entries), keep, recent, _a(out), _p(ws),
+                                  ws.numel() * ws.element_size() if ws is not None else 0, _on(acc.device))
     _check("csa2_evict_select", st)
     return out
 
@@ -774,6 +794,7 @@ def csa2_cache_gather(src, idx, out: Optional[torch.Tensor] = None) -> torch.Ten
     for n in src.shape[2:]:
         row_bytes *= n
     out = _given("out", out, (B, keep, *src.shape[2:]), src.dtype, src.device)
-    st = _lib().csa2_cache_gather(ctx(src.device.index), _p(src), row_bytes, B, N, _p(idx), keep, _p(out), _stream(src))
+    st = _lib().csa2_cache_gather(ctx(src.device.index), _main(src), row_bytes, B, N, _a(idx), keep, _a(out),
+                                  _on(src.device))
     _check("csa2_cache_gather", st)
     return out

@@ -9,14 +9,18 @@
 //
 // Memory bound: every input row is read once and every gradient row written once.  A CTA takes
 // a run of entries, a thread a few adjacent channels of each.  The usual windows (up to 8 rows:
-// m = 1, 2, 4, 8, and overlapping m = 1, 2, 4) are compiled for their size: all of an entry's
-// rows are loaded together, one entry ahead of the arithmetic, and stay in registers between the
+// m = 1, 2, 4, 8, and overlapping m = 1, 2, 4) are compiled for their size: an entry's rows
+// (contiguous stretches) come by bulk copies into a ring of stages in shared memory, several
+// entries ahead of the arithmetic (loads into registers one entry ahead kept 41 KB an SM in
+// flight, 3.7 TB/s over four streams of 131,072 tokens), and stay in registers between the
 // softmax and the gradients; other windows are read again (from the caches).  The bias gradients are sums over all entries: each CTA sums its run in
 // registers (long windows: in its slab of the workspace), and a last pass adds the CTAs'
 // sums in order, so the results do not depend on timing.
 #include <algorithm>
+#include <atomic>
 
 #include "attn_grad.cuh"
+#include "sm100_ptx.cuh"
 
 namespace {
 
@@ -68,6 +72,8 @@ struct CompressBwdArgs {
     T *dca, *dza, *dcb, *dzb, *dprev_cb, *dprev_zb;
     float* slab;              // [CTAs, (1 or 2) m, c] sums of dZ, or NULL (no bias gradient)
     int64_t run;              // entries per CTA
+    int stages;               // usual windows: entries in the ring
+    unsigned* st;
 };
 
 // Where the rows of an entry's window and their gradients are.
@@ -118,44 +124,19 @@ __device__ __forceinline__ void block_sum2(float& x, float& y, float2* red) {
     }
 }
 
-// CH adjacent channels of a row as they are stored, and as fp32.
-template <typename T, int CH>
-struct Raw;
-template <>
-struct Raw<float, 2> {
-    float2 v;
-};
-template <>
-struct Raw<float, 4> {
-    float4 v;
-};
-template <>
-struct Raw<__nv_bfloat16, 2> {
-    uint32_t v;
-};
-template <>
-struct Raw<__nv_bfloat16, 4> {
-    uint2 v;
-};
-template <typename T, int CH>
-__device__ __forceinline__ void ld(Raw<T, CH>& r, const T* p) {
-    r.v = __ldcs(reinterpret_cast<const decltype(r.v)*>(p));
+// CH adjacent channels from (to) memory.
+__device__ __forceinline__ void get(const float* p, float (&x)[2]) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    x[0] = v.x;
+    x[1] = v.y;
 }
-__device__ __forceinline__ void values(const Raw<float, 2>& r, float (&x)[2]) {
-    x[0] = r.v.x;
-    x[1] = r.v.y;
+__device__ __forceinline__ void get(const float* p, float (&x)[4]) { unpack4(ld4<float>(p), x); }
+__device__ __forceinline__ void get(const __nv_bfloat16* p, float (&x)[2]) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+    x[0] = __uint_as_float(v << 16);
+    x[1] = __uint_as_float(v & 0xFFFF0000u);
 }
-__device__ __forceinline__ void values(const Raw<float, 4>& r, float (&x)[4]) { unpack4(r.v, x); }
-__device__ __forceinline__ void values(const Raw<__nv_bfloat16, 2>& r, float (&x)[2]) {
-    x[0] = __uint_as_float(r.v << 16);
-    x[1] = __uint_as_float(r.v & 0xFFFF0000u);
-}
-__device__ __forceinline__ void values(const Raw<__nv_bfloat16, 4>& r, float (&x)[4]) {
-    x[0] = __uint_as_float(r.v.x << 16);
-    x[1] = __uint_as_float(r.v.x & 0xFFFF0000u);
-    x[2] = __uint_as_float(r.v.y << 16);
-    x[3] = __uint_as_float(r.v.y & 0xFFFF0000u);
-}
+__device__ __forceinline__ void get(const __nv_bfloat16* p, float (&x)[4]) { unpack4(ld4<__nv_bfloat16>(p), x); }
 __device__ __forceinline__ void st(float* p, const float (&v)[2]) { *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]); }
 __device__ __forceinline__ void st(float* p, const float (&v)[4]) { st4<float>(p, v); }
 __device__ __forceinline__ void st(__nv_bfloat16* p, const float (&v)[2]) {
@@ -163,80 +144,102 @@ __device__ __forceinline__ void st(__nv_bfloat16* p, const float (&v)[2]) {
 }
 __device__ __forceinline__ void st(__nv_bfloat16* p, const float (&v)[4]) { st4<__nv_bfloat16>(p, v); }
 
-// Windows of M block rows and (OV) M history rows; CH channels a thread, c / CH threads.
+constexpr int CB_STAGES = 8;                     // most entries in the ring
+constexpr long long CB_BUDGET = 1ll << 31;       // cycles a wait for a copy may take
+
+// Bytes of one entry in the ring: gate and value rows of the block (and the history), dout's row.
+__host__ __device__ inline size_t cb_stage_bytes(int rows, int c, size_t elem, size_t dout_elem) {
+    return (size_t)c * (2 * rows * elem + dout_elem);
+}
+
+// Windows of M block rows and (OV) M history rows; CH channels a thread, c / CH threads.  The
+// arithmetic, not the memory, came first here (about 350 instructions a thread and entry of two
+// rows), so exponentials, the reciprocal and the square root are the hardware's approximations:
+// the exponents are at most 0, where __expf is good to a few 2^-22 of every weight that counts.
 template <typename T, int M, bool OV, int CH, bool BIAS>
 __global__ void __launch_bounds__(1024 / CH, (OV ? 2 * M : M) <= 2 ? 4 : (CH == 4 ? 2 : 1)) compress_bwd_kernel(CompressBwdArgs<T> a) {
+    using namespace sm100;
     constexpr int R = OV ? 2 * M : M;
+    extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float2 red[2][16];
+    __shared__ uint64_t full[CB_STAGES];
     const int ch = CH * threadIdx.x, c = a.c;
+    const float inv_c = 1.0f / (float)c;
     const int64_t e0 = (int64_t)blockIdx.x * a.run, e1 = min(a.entries, e0 + a.run);
+    const uint32_t block_bytes = (uint32_t)(M * c * sizeof(T)), dout_bytes = (uint32_t)(c * (a.dout_f32 ? 4 : 2));
+    const uint32_t stage_bytes = 2 * (R / M) * block_bytes + dout_bytes;
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < a.stages; ++k) mbar_init(&full[k], 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    // one thread copies an entry: [gates, values of the block][of the history][dout]
+    auto fetch = [&](int64_t b, int64_t i, int stage) {
+        const Window<T> w = window_of(a, b, i);
+        uint8_t* dst = ring + (size_t)stage * stage_bytes;
+        const bool hist = OV && w.c1;
+        mbar_arrive_expect_tx(&full[stage], 2 * (hist ? 2 : 1) * block_bytes + dout_bytes);
+        bulk_g2s(dst, w.z0, block_bytes, &full[stage]);
+        bulk_g2s(dst + block_bytes, w.c0, block_bytes, &full[stage]);
+        if (hist) {
+            bulk_g2s(dst + 2 * block_bytes, w.z1, block_bytes, &full[stage]);
+            bulk_g2s(dst + 3 * block_bytes, w.c1, block_bytes, &full[stage]);
+        }
+        bulk_g2s(dst + 2 * (R / M) * block_bytes,
+                 reinterpret_cast<const uint8_t*>(a.dout) + (size_t)(b * a.dout_stride + i) * dout_bytes, dout_bytes,
+                 &full[stage]);
+    };
+    auto step = [&](int64_t& b, int64_t& i) {
+        if (++i == a.n_ent) {
+            i = 0;
+            ++b;
+        }
+    };
+    int64_t b = e0 / a.n_ent, i = e0 - b * a.n_ent;
+    int64_t fb = b, fi = i, fe = e0;             // the next entry to copy (thread 0)
+    if (threadIdx.x == 0)
+        for (int k = 0; k < a.stages && fe < e1; ++k, ++fe, step(fb, fi)) fetch(fb, fi, k);
     float db[BIAS ? R : 1][CH];
 #pragma unroll
     for (int j = 0; j < (BIAS ? R : 1); ++j)
 #pragma unroll
         for (int k = 0; k < CH; ++k) db[j][k] = 0.0f;
-    int64_t b = e0 / a.n_ent, i = e0 - b * a.n_ent;
-    // the entry ahead: its rows as stored, its gradient, whether it has history
-    Raw<T, CH> nz[R], nc[R];
-    float ng[CH];
-    auto fetch = [&](int64_t b, int64_t i) {
-        const Window<T> w = window_of(a, b, i);
-#pragma unroll
-        for (int j = 0; j < R; ++j) {
-            if (!OV || j < M) {
-                ld<T, CH>(nz[j], w.z0 + (int64_t)j * c + ch);
-                ld<T, CH>(nc[j], w.c0 + (int64_t)j * c + ch);
-            } else if (w.c1) {
-                ld<T, CH>(nz[j], w.z1 + (int64_t)(j - M) * c + ch);
-                ld<T, CH>(nc[j], w.c1 + (int64_t)(j - M) * c + ch);
-            }
-        }
-        const int64_t go = (b * a.dout_stride + i) * c + ch;
-        if (a.dout_f32) {
-            Raw<float, CH> g;
-            ld<float, CH>(g, reinterpret_cast<const float*>(a.dout) + go);
-            values(g, ng);
-        } else {
-            Raw<__nv_bfloat16, CH> g;
-            ld<__nv_bfloat16, CH>(g, reinterpret_cast<const __nv_bfloat16*>(a.dout) + go);
-            values(g, ng);
-        }
-    };
-    if (e0 < e1) fetch(b, i);
+    int stage = 0;
+    uint32_t par = 0;
+    bool ok = true;
+    // streams lie back to back, so entry e's block starts at row M e
+    int64_t at = e0 * M * c + ch;
     for (int64_t e = e0; e < e1; ++e) {
-        const Window<T> w = window_of(a, b, i);
-        const bool hist = OV && w.c1;
-        const int64_t here_b = b, here_i = i;
+        ok = mbar_wait(&full[stage], par, ok ? CB_BUDGET : 0, a.st) && ok;   // (a copy that never lands is flagged)
+        const bool hist = OV && (i > 0 || a.prev_cb);
+        const T* rows = reinterpret_cast<const T*>(ring + (size_t)stage * stage_bytes) + ch;
         float z[R][CH], v[R][CH], mx[CH], den[CH], E[CH], g[CH];
 #pragma unroll
         for (int j = 0; j < R; ++j) {
             if (!OV || j < M || hist) {
-                values(nz[j], z[j]);
-                values(nc[j], v[j]);
+                const T* p = rows + (j < M ? j : j + M) * c;    // history gates follow the block's 2 M rows
+                get(p, z[j]);
+                get(p + M * c, v[j]);
             } else {
 #pragma unroll
-                for (int k = 0; k < CH; ++k) {              // no history: logit -inf, value 0
+                for (int k = 0; k < CH; ++k) {                  // no history: logit -inf, value 0
                     z[j][k] = -INFINITY;
                     v[j][k] = 0.0f;
                 }
             }
             const float* bias = j < M ? a.ba : a.bb;
             if (bias) {
-                Raw<float, CH> r;
-                r.v = *reinterpret_cast<const decltype(r.v)*>(bias + (int64_t)(j < M ? j : j - M) * c + ch);
                 float x[CH];
-                values(r, x);
+                get(bias + (int64_t)(j < M ? j : j - M) * c + ch, x);
 #pragma unroll
                 for (int k = 0; k < CH; ++k) z[j][k] += x[k];
             }
         }
-#pragma unroll
-        for (int k = 0; k < CH; ++k) g[k] = ng[k];
-        if (++i == a.n_ent) {
-            i = 0;
-            ++b;
-        }
-        if (e + 1 < e1) fetch(b, i);
+        const uint8_t* gd = ring + (size_t)stage * stage_bytes + 2 * (R / M) * block_bytes;
+        if (a.dout_f32)
+            get(reinterpret_cast<const float*>(gd) + ch, g);
+        else
+            get(reinterpret_cast<const __nv_bfloat16*>(gd) + ch, g);
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
             mx[k] = z[0][k];
@@ -245,14 +248,15 @@ __global__ void __launch_bounds__(1024 / CH, (OV ? 2 * M : M) <= 2 ? 4 : (CH == 
             den[k] = E[k] = 0.0f;
 #pragma unroll
             for (int j = 0; j < R; ++j) {
-                z[j][k] = expf(z[j][k] - mx[k]);
+                z[j][k] = __expf(z[j][k] - mx[k]);
                 den[k] += z[j][k];
                 E[k] = fmaf(z[j][k], v[j][k], E[k]);
             }
-            E[k] /= den[k];
+            den[k] = __fdividef(1.0f, den[k]);
+            E[k] *= den[k];
         }
         if ((a.flags & CSA2_W_ROPE) && ch >= c - 64) {
-            const int64_t pos = (a.pos0 ? a.pos0[here_b] : 0) + (int64_t)M * here_i;
+            const int64_t pos = (a.pos0 ? a.pos0[b] : 0) + (int64_t)M * i;
 #pragma unroll
             for (int p = 0; p < CH / 2; ++p) {
                 float cs, sn;
@@ -262,6 +266,7 @@ __global__ void __launch_bounds__(1024 / CH, (OV ? 2 * M : M) <= 2 ? 4 : (CH == 
                 g[2 * p + 1] = x1 * cs - x0 * sn;
             }
         }
+        // (either barrier: every thread has read the stage)
         if (a.flags & CSA2_W_NORM) {
             float ss = 0.0f, dot = 0.0f;
 #pragma unroll
@@ -270,44 +275,60 @@ __global__ void __launch_bounds__(1024 / CH, (OV ? 2 * M : M) <= 2 ? 4 : (CH == 
                 dot = fmaf(E[k], g[k], dot);
             }
             block_sum2(ss, dot, red[(e - e0) & 1]);
-            const float r = 1.0f / sqrtf(ss / (float)c + 1e-6f);
-            const float d = dot * r * r / (float)c;
+            const float r = rsqrtf(fmaf(ss, inv_c, 1e-6f));
+            const float d = dot * r * r * inv_c;
 #pragma unroll
             for (int k = 0; k < CH; ++k) g[k] = r * fmaf(-E[k], d, g[k]);
+        } else {
+            __syncthreads();
+        }
+        if (threadIdx.x == 0 && fe < e1) {
+            fetch(fb, fi, stage);
+            ++fe;
+            step(fb, fi);
+        }
+        if (++stage == a.stages) {
+            stage = 0;
+            par ^= 1;
         }
 #pragma unroll
-        for (int k = 0; k < CH; ++k) den[k] = 1.0f / den[k];
+        for (int k = 0; k < CH; ++k) g[k] *= den[k];             // dE / sum of the exponentials
 #pragma unroll
         for (int j = 0; j < R; ++j) {
             float dc[CH], dz[CH];
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
-                dc[k] = z[j][k] * den[k] * g[k];
+                dc[k] = z[j][k] * g[k];
                 dz[k] = dc[k] * (v[j][k] - E[k]);
             }
-            const int64_t o = (int64_t)(j < M ? j : j - M) * c + ch;
+            const int o = (j < M ? j : j - M) * c;
             if (!OV || j < M) {
-                st(w.g0 + o, dc);
-                st(w.h0 + o, dz);
+                st(a.dca + at + o, dc);
+                st(a.dza + at + o, dz);
+            } else if (i > 0) {
+                st(a.dcb + (at - M * c) + o, dc);
+                st(a.dzb + (at - M * c) + o, dz);
             } else if (hist) {
-                if (w.g1) st(w.g1 + o, dc);
-                if (w.h1) st(w.h1 + o, dz);
+                const int64_t p = b * (int64_t)M * c + o + ch;
+                if (a.dprev_cb) st(a.dprev_cb + p, dc);
+                if (a.dprev_zb) st(a.dprev_zb + p, dz);
             }
             if (BIAS && (!OV || j < M || hist))
 #pragma unroll
                 for (int k = 0; k < CH; ++k) db[BIAS ? j : 0][k] += dz[k];
         }
-        if (OV && here_i == a.n_ent - 1) {
+        if (OV && i == a.n_ent - 1) {
             // the stream's last block is nobody's history within this call
             float zero[CH];
 #pragma unroll
             for (int k = 0; k < CH; ++k) zero[k] = 0.0f;
-            const int64_t at = (here_b * a.n_tokens + here_i * M) * c + ch;
             for (int j = 0; j < M; ++j) {
                 st(a.dcb + at + (int64_t)j * c, zero);
                 st(a.dzb + at + (int64_t)j * c, zero);
             }
         }
+        step(b, i);
+        at += M * c;
     }
     if (BIAS) {
         float* slab = a.slab + (int64_t)blockIdx.x * R * c + ch;
@@ -316,14 +337,28 @@ __global__ void __launch_bounds__(1024 / CH, (OV ? 2 * M : M) <= 2 ? 4 : (CH == 
     }
 }
 
-// The usual windows; the bias sums' registers only where a bias gradient is wanted.
+// The usual windows; the bias sums' registers only where a bias gradient is wanted.  The ring
+// takes an even share of an SM's shared memory for the CTAs that the registers let in.
+template <typename T, int M, bool OV, int CH, bool BIAS>
+csa2_status launch_window(const csa2_ctx* ctx, CompressBwdArgs<T> a, unsigned grid, cudaStream_t s) {
+    constexpr int R = OV ? 2 * M : M;
+    const size_t stage = cb_stage_bytes(R, a.c, sizeof(T), a.dout_f32 ? 4 : 2);
+    const size_t share = (size_t)(226 * 1024) / (R == 8 ? 2 : (R == 4 ? 4 : 8)) - 2048;
+    a.stages = (int)std::max<size_t>(2, std::min<size_t>(CB_STAGES, share / stage));
+    static std::atomic<uint64_t> done{0};
+    const uint64_t bit = 1ull << (ctx->device & 63);
+    auto kern = compress_bwd_kernel<T, M, OV, CH, BIAS>;
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
+        CSA2_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024));
+        done.fetch_or(bit, std::memory_order_relaxed);
+    }
+    kern<<<grid, (unsigned)(a.c / CH), (size_t)a.stages * stage, s>>>(a);
+    return csa2_launch_status();
+}
+
 template <typename T, int M, bool OV, int CH>
-void usual_window(const CompressBwdArgs<T>& a, unsigned grid, cudaStream_t s) {
-    const unsigned threads = (unsigned)(a.c / CH);
-    if (a.slab)
-        compress_bwd_kernel<T, M, OV, CH, true><<<grid, threads, 0, s>>>(a);
-    else
-        compress_bwd_kernel<T, M, OV, CH, false><<<grid, threads, 0, s>>>(a);
+csa2_status usual_window(const csa2_ctx* ctx, const CompressBwdArgs<T>& a, unsigned grid, cudaStream_t s) {
+    return a.slab ? launch_window<T, M, OV, CH, true>(ctx, a, grid, s) : launch_window<T, M, OV, CH, false>(ctx, a, grid, s);
 }
 
 // Any m: four channels a thread, the window's rows read once for the maximum, once for the sums
@@ -487,7 +522,7 @@ struct CompressBwdCall {
 };
 
 template <typename T>
-csa2_status cb_launch(const CompressBwdCall& p, cudaStream_t s) {
+csa2_status cb_launch(const csa2_ctx* ctx, const CompressBwdCall& p, cudaStream_t s) {
     CompressBwdArgs<T> a;
     a.ca = reinterpret_cast<const T*>(p.ca);
     a.za = reinterpret_cast<const T*>(p.za);
@@ -518,23 +553,27 @@ csa2_status cb_launch(const CompressBwdCall& p, cudaStream_t s) {
     const int rows = p.cb ? 2 * p.m : p.m;
     const int64_t ctas = cb_ctas(a.entries, rows == 8 ? CB_CTAS / 4 : (rows == 4 ? CB_CTAS / 2 : CB_CTAS));
     a.run = (a.entries + ctas - 1) / ctas;
+    a.stages = 0;
+    a.st = ctx->status;
+    csa2_status r = CSA2_OK;
     const unsigned grid = (unsigned)ctas, c4 = (unsigned)(p.c / 4);
     if (!p.cb && p.m == 1)
-        usual_window<T, 1, false, 4>(a, grid, s);
+        r = usual_window<T, 1, false, 4>(ctx, a, grid, s);
     else if (!p.cb && p.m == 2)
-        usual_window<T, 2, false, 4>(a, grid, s);
+        r = usual_window<T, 2, false, 4>(ctx, a, grid, s);
     else if (!p.cb && p.m == 4)
-        usual_window<T, 4, false, 4>(a, grid, s);
+        r = usual_window<T, 4, false, 4>(ctx, a, grid, s);
     else if (!p.cb && p.m == 8)
-        usual_window<T, 8, false, 2>(a, grid, s);
+        r = usual_window<T, 8, false, 2>(ctx, a, grid, s);
     else if (p.cb && p.m == 1)
-        usual_window<T, 1, true, 4>(a, grid, s);
+        r = usual_window<T, 1, true, 4>(ctx, a, grid, s);
     else if (p.cb && p.m == 2)
-        usual_window<T, 2, true, 4>(a, grid, s);
+        r = usual_window<T, 2, true, 4>(ctx, a, grid, s);
     else if (p.cb && p.m == 4)
-        usual_window<T, 4, true, 2>(a, grid, s);
+        r = usual_window<T, 4, true, 2>(ctx, a, grid, s);
     else
         compress_bwd_any_kernel<T><<<grid, c4, 0, s>>>(a);
+    if (r != CSA2_OK) return r;
     if (a.slab) {
         const int64_t split = (int64_t)p.m * p.c, cols = split * (p.cb ? 2 : 1);
         compress_bias_kernel<<<(unsigned)(cols / 32), 1024, 0, s>>>(a.slab, (int)ctas, cols, split, p.dba, p.dbb);
@@ -587,5 +626,5 @@ extern "C" csa2_status csa2_compress_bwd(csa2_ctx* ctx, const void* ca, const vo
     const CompressBwdCall p = {ca, za, cb, zb, prev_cb, prev_zb, ba, bb, B, n_tokens, c, m, pos0, rope_base, flags,
                                dout, dout_dt, dout_seq_stride, dca, dza, dcb, dzb, dprev_cb, dprev_zb, dba, dbb,
                                reinterpret_cast<float*>(ws)};
-    return in_dt == CSA2_F32 ? cb_launch<float>(p, s) : cb_launch<__nv_bfloat16>(p, s);
+    return in_dt == CSA2_F32 ? cb_launch<float>(ctx, p, s) : cb_launch<__nv_bfloat16>(ctx, p, s);
 }
