@@ -540,7 +540,7 @@ struct BwdSizes {
 };
 
 struct BwdLayout {
-    size_t D, sink, rinv, cnt, loc, tot, blk, rank, qh, dh, pds, img, dqh, part, acc, total;
+    size_t D, sink, rinv, cnt, loc, tot, blk, rank, qh, dh, pds, img, slots, dqh, part, acc, total;
     int groups, group_q, n_pass, n_split, tps;
 };
 
@@ -590,6 +590,7 @@ BwdLayout bwd_layout(const BwdSizes& z, int64_t nb) {
     L.dh = take(z.tc ? 0 : heads * row_f32);
     L.pds = take(z.tc ? 0 : heads * z.n_slots * 8);
     L.img = take(z.tc ? (size_t)nb * L.n_pass * bwd_tc_image_bytes() : 0);
+    L.slots = take(z.tc ? bwd_tc_slots_bytes(nb, z.n_slots) : 0);
     L.dqh = take(z.tc ? (size_t)nb * L.n_pass * L.n_split * 64 * row_f32
                       : (L.n_split > 1 ? heads * L.n_split * row_f32 : 0));
     L.part = take(z.tc ? pairs * L.n_pass * AG_C * 2 : pairs * row_f32);
@@ -716,7 +717,7 @@ csa2_status bwd_run(csa2_ctx* ctx, const BwdCall& a, void* ws, size_t ws_bytes, 
             t.n_pass = L.n_pass;
             t.n_split = L.n_split;
             t.tps = L.tps;
-            r = bwd_tc_chunk(ctx, t, a.dout, a.out, D, base + L.img, s);
+            r = bwd_tc_chunk(ctx, t, a.dout, a.out, D, base + L.img, base + L.slots, s);
         } else if (a.q_dt == CSA2_F32)
             r = a.out_dt == CSA2_F32 ? simt_chunk<float, float>(ctx, a, c, qh, dh, pds, dqh, L.n_split, L.tps, s)
                                      : simt_chunk<float, __nv_bfloat16>(ctx, a, c, qh, dh, pds, dqh, L.n_split, L.tps, s);

@@ -8,8 +8,14 @@ struct BwdTcArgs {
     BwdChunk c;               // part: bf16 [places, n_pass, 512]
     const uint8_t* img;       // [n_pass, nb] stacked images of the chunk's queries
     float* dqh;               // [n_pass, nb, n_split, 64, 512] dq^ of every item
-    int n_pass, n_split, tps; // 64-head passes; key splits of a query, 64-slot tiles of a split
-    int64_t items;
+    int n_pass, n_split, tps; // 64-head passes; key splits of a query, 128-slot tiles of a split
+    uint32_t items;
+    // the queries' slots, padded to whole tiles (filled in by bwd_tc_chunk)
+    int n_pad;
+    const int32_t* code;      // [nb, n_pad]
+    const int32_t* place;     // [nb, n_pad]
+    const float* fac;         // [nb, n_pad]
+    const int32_t* n_of;      // [nb]
     long long budget;
     int stall;                // test hook: no image is copied
 };
@@ -20,6 +26,7 @@ bool bwd_tc_applies(csa2_dtype q_dt, csa2_dtype kv_dt, int k, csa2_dtype swa_dt,
 // Key splits of `queries` (times head passes) of n_slots slots each.
 void bwd_tc_splits(int num_sms, int64_t queries, int n_slots, int* n_split, int* tps);
 size_t bwd_tc_image_bytes();
+size_t bwd_tc_slots_bytes(int64_t nb, int n_slots);
 // Images, D, products and dq of a chunk (c.rank .. c.part filled in by the caller).
 csa2_status bwd_tc_chunk(csa2_ctx* ctx, BwdTcArgs& a, const void* dout, const void* out, float* D, uint8_t* img,
-                         cudaStream_t s);
+                         void* slots, cudaStream_t s);
