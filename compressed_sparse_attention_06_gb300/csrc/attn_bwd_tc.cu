@@ -46,18 +46,16 @@ constexpr int BT_TILE = 128;
 constexpr int BT_THREADS = 448;
 constexpr int CHUNK = 128 * 128;                 // 128 rows (of the image, or slots) x 64 dims
 constexpr int IMG_BYTES = 8 * CHUNK;
-constexpr int X_RING = 4;                        // chunks of X
+constexpr int X_RING = 4;                        // chunks of X (the roles below count on four)
 constexpr uint32_t COL_DQ = 0, COL_S = 256, COL_DK = 384;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr long long WAIT_BUDGET = 1ll << 31;
 constexpr unsigned FULL = 0xffffffffu;
-// chunks of the next tile's logits that run after each dK block
-constexpr uint32_t S_AFTER = 0x0332;             // 2, 3, 3, 0
 
 constexpr int OFF_IMG = 0;
 constexpr int OFF_X = OFF_IMG + IMG_BYTES;
 constexpr int OFF_DSP = OFF_X + X_RING * CHUNK;  // r dS, then r P: [128 slots][64 heads]
-constexpr int OFF_LD = OFF_DSP + 2 * CHUNK;      // [4 warps][64 heads] lse (base 2), D
+constexpr int OFF_LD = OFF_DSP + 2 * CHUNK;      // [4 warps][64 heads] -lse (base 2), -D / sqrt(c)
 constexpr int OFF_BAR = OFF_LD + 4 * BT_H * 8;
 constexpr int N_BAR = 4 + 4 + 2 * X_RING + 9;
 constexpr int OFF_TMEMPTR = OFF_BAR + N_BAR * 8;
@@ -257,7 +255,7 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
             mbar_init(&imgempty[i], 1);
         }
         for (int i = 0; i < X_RING; ++i) {
-            mbar_init(&xfull[i], 4);
+            mbar_init(&xfull[i], 1);
             mbar_init(&xempty[i], 1);
         }
         mbar_init(sfull, 1);
@@ -314,75 +312,79 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
             constexpr uint32_t ID_DQ = idesc_f16_major(128, BT_H, true, true, true);
             constexpr uint32_t ID_DK = idesc_f16_major(128, 128, true, false, true);
             const uint32_t img = smem_u32(sImg), x0 = smem_u32(sX), dsp = smem_u32(sDsp);
-            uint32_t c = 0, g = 0, t = 0, k = 0;     // X chunks used; tiles with logits; tiles; dK blocks
+            uint32_t g = 0, t = 0, k = 0;            // tiles with logits; tiles done; dK blocks
             int n = 0;                               // items with tiles so far
             bool ok = true;
             auto wait = [&](uint64_t* b, uint32_t par) {
                 ok = ok && mbar_wait(b, par, a.budget, st);
                 return ok;
             };
+            // A place of the ring is filled three times a tile: with chunk x and chunk x + 4 for the
+            // logits -- the latter stays for dQ -- and with chunk x again for dQ.
             // chunk ch (64 dims) of the logits of tile g
             auto scores = [&](int ch) {
-                if (ch == 0 && g > 0 && !wait(sempty, (g - 1) & 1)) return;
-                const uint32_t x = c & (X_RING - 1);
-                if (!wait(&xfull[x], c / X_RING & 1)) return;
+                const int x = ch & 3;
+                if (!wait(&xfull[x], (3 * g + (ch >> 2)) & 1)) return;
                 tc_fence_after();
                 const uint64_t dx = sdesc_sw128(x0 + x * CHUNK), di = sdesc_sw128(img + ch * CHUNK);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     mma_ss(tmem + COL_S, dx + (kk * 32 >> 4), di + (kk * 32 >> 4), ID_S, (ch | kk) != 0);
-                mma_commit(&xempty[x]);
-                ++c;
+                if (ch < 4) mma_commit(&xempty[x]);
                 if (ch == 7) {
                     mma_commit(sfull);
                     ++g;
                 }
             };
+            // dims block db of dQ, from two places of the ring
+            auto dq = [&](int db, bool fresh) {
+                const int x = 2 * (db & 1);
+                if (db < 2 && (!wait(&xfull[x], (3 * t + 2) & 1) || !wait(&xfull[x + 1], (3 * t + 2) & 1))) return;
+                tc_fence_after();
+                const uint64_t dx = sdesc_sw128_mn(x0 + x * CHUNK, CHUNK, 1024), dds = sdesc_sw128_mn(dsp, CHUNK, 1024);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_ss(tmem + COL_DQ + db * BT_H, dx + (ks * 2048 >> 4), dds + (ks * 2048 >> 4), ID_DQ, !fresh || ks > 0);
+                mma_commit(&xempty[x]);
+                mma_commit(&xempty[x + 1]);
+            };
+            auto dk = [&](int db, bool last) {
+                if (k > 0 && !wait(dkempty, (k - 1) & 1)) return;
+                tc_fence_after();
+                const uint64_t da = sdesc_sw128(dsp), di = sdesc_sw128_mn(img + 2 * db * CHUNK, CHUNK, 1024);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_ss(tmem + COL_DK, da + (((ks >> 2) * CHUNK + (ks & 3) * 32) >> 4), di + (ks * 2048 >> 4), ID_DK, ks > 0);
+                mma_commit(dkfull);
+                ++k;
+                if (last) mma_commit(&imgempty[db]);
+                if (db == 3) mma_commit(dspempty);
+            };
             for (Items items(a); items.more() && ok;) {
                 const Item it = items.next();
                 if (it.nt == 0) continue;
+                if (g > 0 && !wait(sempty, (g - 1) & 1)) break;
                 for (int ch = 0; ch < 8 && ok; ++ch)
                     if ((ch & 1) || wait(&imgfull[ch >> 1], n & 1)) scores(ch);
                 for (int tt = 0; tt < it.nt && ok; ++tt, ++t) {
                     const bool last = tt == it.nt - 1;
                     if (tt == 0 && n > 0 && !wait(dqempty, (n - 1) & 1)) break;
                     if (!wait(dspfull, t & 1)) break;
-                    const uint64_t dds = sdesc_sw128_mn(dsp, CHUNK, 1024);
-#pragma unroll 1
-                    for (int db = 0; db < 4; ++db, c += 2) {
-                        const uint32_t x = c & (X_RING - 1);
-                        if (!wait(&xfull[x], c / X_RING & 1) || !wait(&xfull[x + 1], c / X_RING & 1)) break;
-                        tc_fence_after();
-                        const uint64_t dx = sdesc_sw128_mn(x0 + x * CHUNK, CHUNK, 1024);
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            mma_ss(tmem + COL_DQ + db * BT_H, dx + (ks * 2048 >> 4), dds + (ks * 2048 >> 4), ID_DQ,
-                                   tt > 0 || ks > 0);
-                        mma_commit(&xempty[x]);
-                        mma_commit(&xempty[x + 1]);
-                    }
-                    if (!ok) break;
-                    if (last) mma_commit(dqfull);
-                    const uint64_t da = sdesc_sw128(dsp);
-                    int ch = 0;
-#pragma unroll
-                    for (int db = 0; db < 4; ++db) {
-                        if (k > 0 && !wait(dkempty, (k - 1) & 1)) break;
-                        tc_fence_after();
-                        const uint64_t di = sdesc_sw128_mn(img + 2 * db * CHUNK, CHUNK, 1024);
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            mma_ss(tmem + COL_DK, da + (((ks >> 2) * CHUNK + (ks & 3) * 32) >> 4), di + (ks * 2048 >> 4),
-                                   ID_DK, ks > 0);
-                        mma_commit(dkfull);
-                        ++k;
-                        if (last) mma_commit(&imgempty[db]);
-                        if (db == 3) mma_commit(dspempty);
-                        // the next tile's logits while the block is drained
-                        if (!last)
-                            for (int j = 0; j < (int)(S_AFTER >> (4 * db) & 15u) && ok; ++j) scores(ch++);
-                        if (!ok) break;
-                    }
+                    // the dK blocks run where the others would wait for chunks that were just made room for
+                    dq(2, tt == 0);
+                    if (ok) dq(3, tt == 0);
+                    if (ok) dk(0, last);
+                    if (ok) dq(0, tt == 0);
+                    if (ok) dq(1, tt == 0);
+                    if (ok && last) mma_commit(dqfull);
+                    if (ok) dk(1, last);
+                    if (ok) dk(2, last);
+                    if (ok && !last && wait(sempty, (g - 1) & 1))
+                        for (int ch = 0; ch < 8 && ok; ++ch) {
+                            scores(ch);
+                            if (ch == 3 && ok) dk(3, false);
+                        }
+                    if (ok && last) dk(3, true);
                 }
                 if (ok) ++n;
             }
@@ -406,11 +408,11 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int h = it.pass * BT_H + 32 * j + lane;
-                float2 v = make_float2(INFINITY, 0.0f);       // p = 0 for heads past H and empty queries
+                float2 v = make_float2(-INFINITY, 0.0f);      // p = 0 for heads past H and empty queries
                 if (h < a.c.H) {
                     const int64_t o = (a.c.bq0 + it.q) * a.c.H + h;
                     const float l = a.c.lse[o], d = a.c.D[o];
-                    if (l != -INFINITY) v = make_float2(l * AG_LOG2E, d);
+                    if (l != -INFINITY) v = make_float2(-l * AG_LOG2E, -d * isc);
                 }
                 ld[32 * j + lane] = v;
             }
@@ -419,7 +421,7 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
             const float* fac = a.fac + (int64_t)it.q * a.n_pad + it.t0 * BT_TILE + slot;
             float next = *fac;
             for (int tt = 0; tt < it.nt; ++tt, ++t) {
-                const float r = next;
+                const float r = next, rs = r * isc, rz = rs * AG_LOG2E;
                 if (tt + 1 < it.nt) next = fac[(tt + 1) * BT_TILE];
                 bool w = mbar_wait(sfull, t & 1, a.budget, st);
                 if (!__all_sync(FULL, w)) {
@@ -437,14 +439,13 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const float4 h2 = *reinterpret_cast<const float4*>(&ld[16 * q + 2 * j]);   // lse, D of two heads
-                        float p0 = ex2_approx(fmaf(__uint_as_float(s[2 * j]) * r, isc * AG_LOG2E, -h2.x));
-                        float p1 = ex2_approx(fmaf(__uint_as_float(s[2 * j + 1]) * r, isc * AG_LOG2E, -h2.z));
-                        if (r == 0.0f) p0 = p1 = 0.0f;
-                        const float v0 = p0 * r, v1 = p1 * r;
+                        const float4 h2 = *reinterpret_cast<const float4*>(&ld[16 * q + 2 * j]);   // two heads
+                        float v0 = ex2_approx(fmaf(__uint_as_float(s[2 * j]), rz, h2.x)) * r;
+                        float v1 = ex2_approx(fmaf(__uint_as_float(s[2 * j + 1]), rz, h2.z)) * r;
+                        if (r == 0.0f) v0 = v1 = 0.0f;
                         ppq[j] = ag_pack_bf16x2(v0, v1);
-                        dsq[j] = ag_pack_bf16x2(p0 == 0.0f ? 0.0f : v0 * (fmaf(__uint_as_float(d[2 * j]), r, -h2.y) * isc),
-                                                p1 == 0.0f ? 0.0f : v1 * (fmaf(__uint_as_float(d[2 * j + 1]), r, -h2.w) * isc));
+                        dsq[j] = ag_pack_bf16x2(v0 * fmaf(__uint_as_float(d[2 * j]), rs, h2.y),
+                                                v1 * fmaf(__uint_as_float(d[2 * j + 1]), rs, h2.w));
                     }
                 };
                 auto put = [&](int u, const uint32_t* dsq, const uint32_t* ppq) {
@@ -475,79 +476,66 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
         }
     } else if (warp < 10) {
         // ============================ loaders ============================
-        const int lw = warp - 6;                              // slots 32 lw .. of the tile
+        // A warp fills one place of the ring, every fourth chunk: copies in flight in one warp then
+        // never wait for another's.
+        const int x = warp - 6;
         const int sub = lane >> 3, piece = lane & 7;          // a copy moves 128 bytes of four rows
         // (an empty slot's copy reads nothing; its address is a row of whichever array there is)
         const uint8_t* kv = reinterpret_cast<const uint8_t*>(a.c.slots.n_kv > 0 ? a.c.kv : a.c.swa) + piece * 16;
         const uint8_t* swa = reinterpret_cast<const uint8_t*>(a.c.swa) + piece * 16;
-        const uint32_t off = sw128_offset((uint32_t)(32 * lw + sub), (uint32_t)piece);
-        const uint32_t off4 = sw128_offset((uint32_t)(32 * lw + sub + 4), (uint32_t)piece);
-        uint32_t c = 0;                                       // chunks issued
-        int behind = 0;                                       // of them in flight
+        // rows 8 apart have the same swizzle
+        uint8_t* dst0 = sX + x * CHUNK + sw128_offset((uint32_t)sub, (uint32_t)piece);
+        uint8_t* dst4 = sX + x * CHUNK + sw128_offset((uint32_t)(sub + 4), (uint32_t)piece);
+        uint32_t c = 0;                                       // chunks filled
         bool ok = true;
-        auto signal = [&]() {                                 // the oldest chunk in flight
-            if (behind == 4)
-                cp_async_wait<3>();
-            else if (behind == 3)
-                cp_async_wait<2>();
-            else if (behind == 2)
-                cp_async_wait<1>();
-            else
-                cp_async_wait<0>();
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&xfull[(c - behind) & (X_RING - 1)]);
-            --behind;
-        };
-        // the eight chunks of a tile whose slots `code` holds
-        auto stream = [&](int code) {
-            const uint8_t* src[8];
-            uint32_t read = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int o = __shfl_sync(FULL, code, 4 * j + sub);
-                read |= (o != -1 ? 1u : 0u) << j;
-                src[j] = o >= -1 ? kv + (int64_t)max(o, 0) * (BT_C * 2) : swa + (int64_t)(-2 - o) * (BT_C * 2);
-            }
+        // chunks x and, for the logits, x + 4 of a tile; code[q]: slot 32 q + lane
+        auto stream = [&](const int (&code)[4], int end) {
 #pragma unroll 1
-            for (int ch = 0; ch < 8; ++ch) {
-                const uint32_t x = c & (X_RING - 1);
-                if (c >= X_RING) {
-                    const uint32_t par = (c / X_RING - 1) & 1;
-                    // chunks in flight are signalled before a wait that they may be needed for
-                    if (!__all_sync(FULL, mbar_test(&xempty[x], par))) {
-                        while (behind > 0) signal();
-                        const bool w = mbar_wait(&xempty[x], par, a.budget, st);
-                        if (!__all_sync(FULL, w)) {
-                            ok = false;
-                            return;
-                        }
-                    }
+            for (int ch = x; ch < end && ok; ch += 4, ++c) {
+                bool w = true;
+                if (c > 0) w = mbar_wait(&xempty[x], (c - 1) & 1, a.budget, st);
+                if (!__all_sync(FULL, w)) {
+                    ok = false;
+                    return;
                 }
-                uint8_t* dst = sX + x * CHUNK;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)                   // rows 8 apart have the same swizzle
-                    cp_async16_or_zero(dst + (j & 1 ? off4 : off) + (j >> 1) * 1024, src[j] + ch * 128, read >> j & 1);
-                cp_async_commit();
-                ++c;
-                if (++behind > 3) signal();                   // three chunks stay in flight
+                for (int q = 0; q < 4; ++q) {                 // eight addresses, then eight copies
+                    const uint8_t* src[8];
+                    bool read[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int o = __shfl_sync(FULL, code[q], 4 * j + sub);
+                        read[j] = o != -1;
+                        src[j] = (o >= -1 ? kv : swa) + ((uint64_t)(uint32_t)(o >= -1 ? max(o, 0) : -2 - o) * (BT_C * 2) + ch * 128);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        cp_async16_or_zero((j & 1 ? dst4 : dst0) + (4 * q + (j >> 1)) * 1024, src[j], read[j]);
+                }
+                cp_async_wait_all();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&xfull[x]);
             }
         };
         for (Items items(a); items.more() && ok;) {
             const Item it = items.next();
             if (it.nt == 0) continue;
-            const int32_t* codes = a.code + (int64_t)it.q * a.n_pad + it.t0 * BT_TILE + 32 * lw + lane;
-            int code = *codes;                                // slot `lane` of the warp's 32, read a tile ahead
-            stream(code);                                     // logits
+            const int32_t* codes = a.code + (int64_t)it.q * a.n_pad + it.t0 * BT_TILE + lane;
+            int code[4], next[4];                             // read a tile ahead
+#pragma unroll
+            for (int q = 0; q < 4; ++q) code[q] = next[q] = codes[32 * q];
+            stream(code, 8);                                  // logits
             for (int tt = 0; tt < it.nt && ok; ++tt) {
-                const int next = tt + 1 < it.nt ? codes[(tt + 1) * BT_TILE] : -1;
-                stream(code);                                 // dQ
-                if (ok && tt + 1 < it.nt) stream(next);       // the next tile's logits
-                code = next;
+                if (tt + 1 < it.nt)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) next[q] = codes[(tt + 1) * BT_TILE + 32 * q];
+                stream(code, 4);                              // dQ
+                if (ok && tt + 1 < it.nt) stream(next, 8);    // the next tile's logits
+#pragma unroll
+                for (int q = 0; q < 4; ++q) code[q] = next[q];
             }
         }
-        while (ok && behind > 0) signal();
-        cp_async_wait_all();
     } else {
         // ============================ drain ============================
         const int qd = warp & 3;
