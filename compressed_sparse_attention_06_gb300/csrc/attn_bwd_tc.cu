@@ -429,46 +429,44 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
                     break;
                 }
                 tc_fence_after();
-                // half of the heads wait in registers for the last tile's products; the rest (all of it
-                // would spill) is made after them
-                uint32_t ds[16], pp[16];
-                auto quarter = [&](int q, uint32_t* dsq, uint32_t* ppq) {
-                    uint32_t s[16], d[16];
-                    tmem_ld16(tmem + lane_base + COL_S + 16 * q, s);
-                    tmem_ld16(tmem + lane_base + COL_S + 64 + 16 * q, d);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float4 h2 = *reinterpret_cast<const float4*>(&ld[16 * q + 2 * j]);   // two heads
-                        float v0 = ex2_approx(fmaf(__uint_as_float(s[2 * j]), rz, h2.x)) * r;
-                        float v1 = ex2_approx(fmaf(__uint_as_float(s[2 * j + 1]), rz, h2.z)) * r;
-                        if (r == 0.0f) v0 = v1 = 0.0f;
-                        ppq[j] = ag_pack_bf16x2(v0, v1);
-                        dsq[j] = ag_pack_bf16x2(v0 * fmaf(__uint_as_float(d[2 * j]), rs, h2.y),
-                                                v1 * fmaf(__uint_as_float(d[2 * j + 1]), rs, h2.w));
-                    }
-                };
-                auto put = [&](int u, const uint32_t* dsq, const uint32_t* ppq) {
-                    uint8_t* dst = sDsp + sw128_offset(slot, u);
-                    *reinterpret_cast<uint4*>(dst) = make_uint4(dsq[0], dsq[1], dsq[2], dsq[3]);
-                    *reinterpret_cast<uint4*>(dst + CHUNK) = make_uint4(ppq[0], ppq[1], ppq[2], ppq[3]);
-                };
-#pragma unroll
-                for (int q = 0; q < 2; ++q) quarter(q, ds + 8 * q, pp + 8 * q);
                 if (t > 0) w = mbar_wait(dspempty, (t - 1) & 1, a.budget, st);
                 if (!__all_sync(FULL, w)) {
                     ok = false;
                     break;
                 }
+                // 16 heads at a time; the next ones are read from tensor memory meanwhile
+                uint32_t s[2][16], d[2][16];
+                tmem_ld16(tmem + lane_base + COL_S, s[0]);
+                tmem_ld16(tmem + lane_base + COL_S + 64, d[0]);
 #pragma unroll
-                for (int u = 0; u < 4; ++u) put(u, ds + 4 * u, pp + 4 * u);
+                for (int q = 0; q < 4; ++q) {
+                    tmem_wait_ld();
+                    if (q < 3) {
+                        tmem_ld16(tmem + lane_base + COL_S + 16 * (q + 1), s[(q + 1) & 1]);
+                        tmem_ld16(tmem + lane_base + COL_S + 64 + 16 * (q + 1), d[(q + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(sempty);
+                    }
+                    uint32_t ds[8], pp[8];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) quarter(2 + q, ds + 8 * q, pp + 8 * q);
-                tc_fence_before();
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 h2 = *reinterpret_cast<const float4*>(&ld[16 * q + 2 * j]);   // two heads
+                        float v0 = ex2_approx(fmaf(__uint_as_float(s[q & 1][2 * j]), rz, h2.x)) * r;
+                        float v1 = ex2_approx(fmaf(__uint_as_float(s[q & 1][2 * j + 1]), rz, h2.z)) * r;
+                        if (r == 0.0f) v0 = v1 = 0.0f;
+                        pp[j] = ag_pack_bf16x2(v0, v1);
+                        ds[j] = ag_pack_bf16x2(v0 * fmaf(__uint_as_float(d[q & 1][2 * j]), rs, h2.y),
+                                               v1 * fmaf(__uint_as_float(d[q & 1][2 * j + 1]), rs, h2.w));
+                    }
 #pragma unroll
-                for (int u = 0; u < 4; ++u) put(4 + u, ds + 4 * u, pp + 4 * u);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sempty);
+                    for (int u = 0; u < 2; ++u) {
+                        uint8_t* dst = sDsp + sw128_offset(slot, 2 * q + u);
+                        *reinterpret_cast<uint4*>(dst) = make_uint4(ds[4 * u], ds[4 * u + 1], ds[4 * u + 2], ds[4 * u + 3]);
+                        *reinterpret_cast<uint4*>(dst + CHUNK) = make_uint4(pp[4 * u], pp[4 * u + 1], pp[4 * u + 2], pp[4 * u + 3]);
+                    }
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(dspfull);
