@@ -366,7 +366,8 @@ __global__ void __launch_bounds__(256) bwd_simt_dq_kernel(BwdChunk c, const floa
         qv[i] = qh[hr * AG_C + lane + 32 * i];
         acc[i] = 0.0f;
     }
-    for (int k = 0; k < n_split; ++k)
+#pragma unroll 4
+    for (int k = 0; k < n_split; ++k)                 // unrolled: 64 loads in flight, not 16
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[i] += dqh[(hr * n_split + k) * AG_C + lane + 32 * i];
     finish_dq<TQ>(c, bq, (int)(hr % c.H), lane, qv, acc, cs[w], sn[w], dq);
@@ -377,8 +378,16 @@ __global__ void __launch_bounds__(256) bwd_simt_dq_kernel(BwdChunk c, const floa
 __global__ void __launch_bounds__(256) bwd_simt_row_kernel(BwdChunk c, const float* qh, const float* dh,
                                                            const float2* pds) {
     __shared__ float2 sp[32][33];
+    __shared__ int64_t at[32];                        // places, -1 = no contribution
+    __shared__ float fac[32];
     const int q = blockIdx.y, s0 = blockIdx.x * 32, t = threadIdx.x;
     const int64_t bq = c.bq0 + q;
+    if (t < 32) {
+        const int64_t row = s0 + t < c.n_slots ? slot_row(c.slots, bq, s0 + t, false) : -1;
+        at[t] = row >= 0 ? pair_place(c, q, s0 + t, row) : -1;
+        fac[t] = row >= 0 ? c.rinv[row] : 0.0f;
+    }
+    __syncthreads();
     float acc0[32], acc1[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) acc0[j] = acc1[j] = 0.0f;
@@ -404,12 +413,8 @@ __global__ void __launch_bounds__(256) bwd_simt_row_kernel(BwdChunk c, const flo
     float2* part = reinterpret_cast<float2*>(c.part);
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-        const int s = s0 + j;
-        if (s >= c.n_slots) continue;
-        const int64_t row = slot_row(c.slots, bq, s, false);
-        if (row < 0) continue;
-        const float f = c.rinv[row];
-        part[pair_place(c, q, s, row) * (AG_C / 2) + t] = make_float2(acc0[j] * f, acc1[j] * f);
+        if (at[j] < 0) continue;
+        part[at[j] * (AG_C / 2) + t] = make_float2(acc0[j] * fac[j], acc1[j] * fac[j]);
     }
 }
 

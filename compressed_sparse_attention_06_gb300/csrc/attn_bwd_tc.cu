@@ -637,11 +637,19 @@ bool bwd_tc_applies(csa2_dtype q_dt, csa2_dtype kv_dt, int k, csa2_dtype swa_dt,
 }
 
 void bwd_tc_splits(int num_sms, int64_t queries, int n_slots, int* n_split, int* tps) {
-    // as many key splits as keep every (query, split) item in one wave of CTAs
+    // the split whose waves of CTAs are shortest; an item costs about half a tile besides its tiles
+    // (192 queries of 401 slots: 168 us with one item each, two uneven waves)
     const int tiles = std::max(1, (n_slots + BT_TILE - 1) / BT_TILE);
-    const int want = (int)std::min<int64_t>(tiles, std::max<int64_t>(1, num_sms / std::max<int64_t>(1, queries)));
-    *tps = (tiles + want - 1) / want;
-    *n_split = (tiles + *tps - 1) / *tps;
+    int64_t best = INT64_MAX;
+    for (int t = tiles; t >= 1; --t) {
+        const int n = (tiles + t - 1) / t;
+        const int64_t cost = (queries * n + num_sms - 1) / num_sms * (2 * t + 1);
+        if (cost < best) {
+            best = cost;
+            *tps = t;
+            *n_split = n;
+        }
+    }
 }
 
 size_t bwd_tc_image_bytes() { return IMG_BYTES; }
