@@ -640,10 +640,11 @@ void bwd_tc_splits(int num_sms, int64_t queries, int n_slots, int* n_split, int*
     // the split whose waves of CTAs are shortest; an item costs about half a tile besides its tiles
     // (192 queries of 401 slots: 168 us with one item each, two uneven waves)
     const int tiles = std::max(1, (n_slots + BT_TILE - 1) / BT_TILE);
+    const int64_t sms = std::max(1, num_sms);         // (sizes are also asked for without a GPU)
     int64_t best = INT64_MAX;
     for (int t = tiles; t >= 1; --t) {
         const int n = (tiles + t - 1) / t;
-        const int64_t cost = (queries * n + num_sms - 1) / num_sms * (2 * t + 1);
+        const int64_t cost = (queries * n + sms - 1) / sms * (2 * t + 1);
         if (cost < best) {
             best = cost;
             *tps = t;
