@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const TQ* q, const TO* do
 
 // ---------------------------------------------------------------- CUDA-core path (fp32)
 
-constexpr int SB_HG = 8;                 // heads per CTA of the query pass
+constexpr int SB_HG = 16;                // heads per CTA of the query pass
 constexpr int SB_KC = 32;                // key rows per staged chunk
 
 // dq of one head row by a warp, lane l holding channels l + 32 i: dq^ back through RoPE and the
@@ -258,12 +258,14 @@ __device__ __forceinline__ void finish_dq(const BwdChunk& c, int64_t bq, int h, 
     for (int i = 0; i < 16; ++i) dq[o + lane + 32 * i] = from_f32<TQ>(none ? 0.0f : acc[i]);
 }
 
-// Query pass: p and dS of every slot (kept for the row pass) and dq; a CTA per (8 heads,
-// query, range of slots), a warp per head, key rows staged 32 at a time in fp32.  With few
+// Query pass: p and dS of every slot (kept for the row pass) and dq; a CTA per (16 heads,
+// query, range of slots), a warp per two heads, key rows staged 32 at a time in fp32.  With few
 // queries the slots are split over CTAs (p needs no other slot, the lse is given) and
-// bwd_simt_dq_kernel adds the ranges' dq^.
+// bwd_simt_dq_kernel adds the ranges' dq^.  Bound by shared memory's port, which the loads of a
+// row (32 a warp, shared by its two heads) and the sums' shuffles go through: 20 cycles a (head,
+// slot) against 12 of the FMAs; with one head a warp and a sum of its own for each row it was 42.
 template <typename TQ>
-__global__ void __launch_bounds__(256, 2) bwd_simt_q_kernel(BwdChunk c, const float* qh, const float* dh, float2* pds,
+__global__ void __launch_bounds__(256, 1) bwd_simt_q_kernel(BwdChunk c, const float* qh, const float* dh, float2* pds,
                                                             float* dqh, int per, TQ* dq) {
     extern __shared__ float smem[];
     float* xs = smem;                                        // [32][512] normalised rows
@@ -271,83 +273,121 @@ __global__ void __launch_bounds__(256, 2) bwd_simt_q_kernel(BwdChunk c, const fl
     float* cs = reinterpret_cast<float*>(ok + SB_KC);        // [32]
     float* sn = cs + 32;
     const int q = blockIdx.y, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.x * SB_HG + w;
-    const bool live = h < c.H;
+    const int h0 = blockIdx.x * SB_HG + 2 * w;
     const int64_t bq = c.bq0 + q;
     if (threadIdx.x < 32) ag_cos_sin(c.rope, c.slots.q_pos[bq], lane, cs[lane], sn[lane]);
-    float qv[16], dv[16], acc[16];
-    const int64_t hr = (int64_t)q * c.H + h;
+    float qv[2][16], dv[2][16], acc[2][16], lse[2], D[2];
+    const int64_t hr = (int64_t)q * c.H + h0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) qv[i] = dv[i] = acc[i] = 0.0f;
-    float lse = -INFINITY, D = 0.0f;
-    if (live) {
+    for (int e = 0; e < 2; ++e) {
+        const bool live = h0 + e < c.H;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            qv[i] = qh[hr * AG_C + lane + 32 * i];
-            dv[i] = dh[hr * AG_C + lane + 32 * i];
+            qv[e][i] = live ? qh[(hr + e) * AG_C + lane + 32 * i] : 0.0f;
+            dv[e][i] = live ? dh[(hr + e) * AG_C + lane + 32 * i] : 0.0f;
+            acc[e][i] = 0.0f;
         }
-        lse = c.lse[bq * c.H + h];
-        D = c.D[bq * c.H + h];
+        lse[e] = live ? c.lse[bq * c.H + h0 + e] : -INFINITY;
+        D[e] = live ? c.D[bq * c.H + h0 + e] : 0.0f;
     }
     const float isc = 1.0f / sqrtf((float)AG_C);
     const int s_end = min(c.n_slots, ((int)blockIdx.z + 1) * per);
     for (int s0 = blockIdx.z * per; s0 < s_end; s0 += SB_KC) {
         __syncthreads();
-        for (int r = w; r < SB_KC; r += 8) {
-            const int64_t row = s0 + r < c.n_slots ? slot_row(c.slots, bq, s0 + r, false) : -1;
-            float v[16];
+        {
+            // rows w, w + 8, w + 16, w + 24 of the chunk: all looked up, then all loaded
+            int64_t mine = -1;
+            float fm = 0.0f;
+            const int sr = s0 + w + 8 * lane;
+            if (lane < SB_KC / 8 && sr < c.n_slots) mine = slot_row(c.slots, bq, sr, false);
+            if (mine >= 0) fm = c.rinv[mine];
+            float v[SB_KC / 8][16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-            if (row >= 0) {
-                if (row < c.slots.n_kv)
-                    ag_load_row16(c.kv, c.kv_dt, row, lane, v);
-                else
-                    ag_load_row16(c.swa, c.swa_dt, row - c.slots.n_kv, lane, v);
-                const float f = c.rinv[row];
+            for (int j = 0; j < SB_KC / 8; ++j) {
+                const int64_t row = __shfl_sync(0xffffffffu, mine, j);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] *= f;
+                for (int i = 0; i < 16; ++i) v[j][i] = 0.0f;
+                if (row >= 0) {
+                    if (row < c.slots.n_kv)
+                        ag_load_row16(c.kv, c.kv_dt, row, lane, v[j]);
+                    else
+                        ag_load_row16(c.swa, c.swa_dt, row - c.slots.n_kv, lane, v[j]);
+                }
             }
-            ag_store16<float>(xs + r * AG_C + 16 * lane, v);
-            if (lane == 0) ok[r] = row >= 0;
+#pragma unroll
+            for (int j = 0; j < SB_KC / 8; ++j) {
+                const float f = __shfl_sync(0xffffffffu, fm, j);
+                const bool there = __shfl_sync(0xffffffffu, mine, j) >= 0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[j][i] *= f;
+                ag_store16<float>(xs + (w + 8 * j) * AG_C + 16 * lane, v[j]);
+                if (lane == 0) ok[w + 8 * j] = there;
+            }
         }
         __syncthreads();
-        float z = 0.0f, dp = 0.0f;
+        if (h0 >= c.H) continue;
+        float z[2] = {0.0f, 0.0f}, dp[2] = {0.0f, 0.0f};
+#pragma unroll 1
+        for (int j0 = 0; j0 < SB_KC; j0 += 8) {
+            float a[2][8], b[2][8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) a[e][j] = b[e][j] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float x = xs[(j0 + j) * AG_C + lane + 32 * i];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        a[e][j] = fmaf(qv[e][i], x, a[e][j]);
+                        b[e][j] = fmaf(dv[e][i], x, b[e][j]);
+                    }
+                }
+            }
+            const bool mine = (lane & 24) == j0;             // slots j0 .. j0 + 7 belong to these lanes
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float sa = ag_sums_of_8(a[e], lane), sb = ag_sums_of_8(b[e], lane);
+                if (mine) {
+                    z[e] = sa * isc;
+                    dp[e] = sb;
+                }
+            }
+        }
+        float ds[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float p = 0.0f;
+            ds[e] = 0.0f;
+            if (ok[lane] && lse[e] != -INFINITY) {
+                p = expf(z[e] - lse[e]);
+                ds[e] = p * (dp[e] - D[e]) * isc;
+            }
+            if (h0 + e < c.H && s0 + lane < c.n_slots) pds[(hr + e) * c.n_slots + s0 + lane] = make_float2(p, ds[e]);
+        }
+#pragma unroll 4
         for (int j = 0; j < SB_KC; ++j) {
-            float a = 0.0f, b = 0.0f;
+            const float d0 = __shfl_sync(0xffffffffu, ds[0], j), d1 = __shfl_sync(0xffffffffu, ds[1], j);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const float x = xs[j * AG_C + lane + 32 * i];
-                a = fmaf(qv[i], x, a);
-                b = fmaf(dv[i], x, b);
+                acc[0][i] = fmaf(d0, x, acc[0][i]);
+                acc[1][i] = fmaf(d1, x, acc[1][i]);
             }
-            a = warp_sum(a);
-            b = warp_sum(b);
-            if (lane == j) {
-                z = a * isc;
-                dp = b;
-            }
-        }
-        float p = 0.0f, ds = 0.0f;
-        if (ok[lane] && lse != -INFINITY) {
-            p = expf(z - lse);
-            ds = p * (dp - D) * isc;
-        }
-        if (live && s0 + lane < c.n_slots) pds[hr * c.n_slots + s0 + lane] = make_float2(p, ds);
-        for (int j = 0; j < SB_KC; ++j) {
-            const float d = __shfl_sync(0xffffffffu, ds, j);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[i] = fmaf(d, xs[j * AG_C + lane + 32 * i], acc[i]);
         }
     }
     __syncthreads();                                         // (cs, sn; every warp is past its rows)
-    if (!live) return;
-    if (gridDim.z == 1) {
-        finish_dq<TQ>(c, bq, h, lane, qv, acc, cs, sn, dq);
-        return;
-    }
-    float* o = dqh + (hr * gridDim.z + blockIdx.z) * AG_C;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[lane + 32 * i] = acc[i];
+    for (int e = 0; e < 2; ++e) {
+        if (h0 + e >= c.H) break;
+        if (gridDim.z == 1) {
+            finish_dq<TQ>(c, bq, h0 + e, lane, qv[e], acc[e], cs, sn, dq);
+            continue;
+        }
+        float* o = dqh + ((hr + e) * gridDim.z + blockIdx.z) * AG_C;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[lane + 32 * i] = acc[e][i];
+    }
 }
 
 // dq from the slot ranges' dq^; a warp per (query, head).
@@ -377,7 +417,7 @@ __global__ void __launch_bounds__(256) bwd_simt_dq_kernel(BwdChunk c, const floa
 // a CTA per (32 slots, query), two channels a thread.
 __global__ void __launch_bounds__(256) bwd_simt_row_kernel(BwdChunk c, const float* qh, const float* dh,
                                                            const float2* pds) {
-    __shared__ float2 sp[32][33];
+    __shared__ __align__(16) float2 sp[32][34];       // (rows of whole float4)
     __shared__ int64_t at[32];                        // places, -1 = no contribution
     __shared__ float fac[32];
     const int q = blockIdx.y, s0 = blockIdx.x * 32, t = threadIdx.x;
@@ -399,14 +439,20 @@ __global__ void __launch_bounds__(256) bwd_simt_row_kernel(BwdChunk c, const flo
         }
         __syncthreads();
         const int hn = min(32, c.H - h0);
-        for (int h = 0; h < hn; ++h) {
-            const int64_t o = ((int64_t)q * c.H + h0 + h) * AG_C + 2 * t;
-            const float2 qv = *reinterpret_cast<const float2*>(qh + o), dv = *reinterpret_cast<const float2*>(dh + o);
+        const int64_t o = ((int64_t)q * c.H + h0) * AG_C + 2 * t;
+        float2 qn = *reinterpret_cast<const float2*>(qh + o), dn = *reinterpret_cast<const float2*>(dh + o);
+        for (int h = 0; h < hn; ++h) {                // a head's values are loaded during the one before
+            const float2 qv = qn, dv = dn;
+            const int64_t on = o + (int64_t)min(h + 1, hn - 1) * AG_C;
+            qn = *reinterpret_cast<const float2*>(qh + on);
+            dn = *reinterpret_cast<const float2*>(dh + on);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const float2 pd = sp[h][j];
+            for (int j = 0; j < 32; j += 2) {
+                const float4 pd = *reinterpret_cast<const float4*>(&sp[h][j]);
                 acc0[j] = fmaf(pd.y, qv.x, fmaf(pd.x, dv.x, acc0[j]));
                 acc1[j] = fmaf(pd.y, qv.y, fmaf(pd.x, dv.y, acc1[j]));
+                acc0[j + 1] = fmaf(pd.w, qv.x, fmaf(pd.z, dv.x, acc0[j + 1]));
+                acc1[j + 1] = fmaf(pd.w, qv.y, fmaf(pd.z, dv.y, acc1[j + 1]));
             }
         }
     }
@@ -552,7 +598,7 @@ struct BwdLayout {
 // Stretches of queries that dsink is summed in: 32 queries are four a warp.
 int64_t sink_stretches(int64_t n_bq) { return std::max<int64_t>(1, std::min<int64_t>(64, n_bq / 32)); }
 
-// Slot ranges (of `per` slots) of the CUDA-core query pass: with few (query, 8 heads) groups, as
+// Slot ranges (of `per` slots) of the CUDA-core query pass: with few (query, 16 heads) groups, as
 // many as give every SM two CTAs.
 void simt_splits(int num_sms, int64_t groups, int n_slots, int* n_split, int* per) {
     const int chunks = std::max(1, (n_slots + SB_KC - 1) / SB_KC);

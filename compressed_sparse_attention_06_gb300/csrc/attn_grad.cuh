@@ -99,6 +99,23 @@ __device__ __forceinline__ void ag_load16<__nv_bfloat16>(const __nv_bfloat16* p,
     }
 }
 
+// The lanes' sums of v[0 .. 7]: lane l gets that of v[l & 7].
+__device__ __forceinline__ float ag_sums_of_8(float (&v)[8], int lane) {
+#pragma unroll
+    for (int n = 4, d = 16; n >= 1; n >>= 1, d >>= 1) {
+        const bool top = lane & d;
+#pragma unroll
+        for (int k = 0; k < n; ++k) {
+            const float send = top ? v[k] : v[k + n], keep = top ? v[k + n] : v[k];
+            v[k] = keep + __shfl_xor_sync(0xffffffffu, send, d);
+        }
+    }
+    float s = v[0];                                          // of v[lane >> 2], over four lanes still
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    return __shfl_sync(0xffffffffu, s, (lane & 7) << 2);
+}
+
 // The same of a row of dtype dt (F32, BF16 or FP4) at row index `row` of `base`.
 __device__ __forceinline__ void ag_load_row16(const void* base, int dt, int64_t row, int lane, float (&v)[16]) {
     if (dt == CSA2_F32) {

@@ -46,8 +46,9 @@ __global__ void __launch_bounds__(256) mass_prep_kernel(const TQ* q, const int64
     ag_store16<float>(qh + r * AG_C + 16 * lane, v);
 }
 
-// CUDA-core path (fp32): a CTA per (32 slots, query), rows staged in fp32, a warp per head
-// in turn.
+// CUDA-core path (fp32): a CTA per (32 slots, query), rows staged in fp32, a warp per four
+// heads at a time, which share the loads of a row from shared memory (its port is the bound with
+// one head a warp, the FMAs with four).
 __global__ void __launch_bounds__(256, 2) mass_simt_kernel(MassArgs a) {
     extern __shared__ float smem[];
     float* xs = smem;                                         // [32][512]
@@ -55,39 +56,65 @@ __global__ void __launch_bounds__(256, 2) mass_simt_kernel(MassArgs a) {
     int64_t* rid = reinterpret_cast<int64_t*>(ws + 8 * 32);   // [32]
     const int64_t bq = blockIdx.y;
     const int s0 = blockIdx.x * MS_KC, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int r = w; r < MS_KC; r += 8) {
-        const int64_t row = s0 + r < a.slots.k ? slot_row(a.slots, bq, s0 + r, true) : -1;
-        float v[16];
+    {
+        // rows w, w + 8, w + 16, w + 24: all looked up, then all loaded
+        int64_t mine = -1;
+        const int sr = s0 + w + 8 * lane;
+        if (lane < MS_KC / 8 && sr < a.slots.k) mine = slot_row(a.slots, bq, sr, true);
+        float v[MS_KC / 8][16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-        if (row >= 0) {
-            ag_load_row16(a.kv, a.kv_dt, row, lane, v);
-            if (a.flags & CSA2_KVNORM) {
-                const float f = ag_rms_factor(warp_sum(ag_sumsq16(v)));
+        for (int j = 0; j < MS_KC / 8; ++j) {
+            const int64_t row = __shfl_sync(0xffffffffu, mine, j);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] *= f;
-            }
+            for (int i = 0; i < 16; ++i) v[j][i] = 0.0f;
+            if (row >= 0) ag_load_row16(a.kv, a.kv_dt, row, lane, v[j]);
         }
-        ag_store16<float>(xs + r * AG_C + 16 * lane, v);
-        if (lane == 0) rid[r] = row;
+#pragma unroll
+        for (int j = 0; j < MS_KC / 8; ++j) {
+            const int64_t row = __shfl_sync(0xffffffffu, mine, j);
+            const float f = (a.flags & CSA2_KVNORM) ? ag_rms_factor(warp_sum(ag_sumsq16(v[j]))) : 1.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[j][i] *= f;
+            ag_store16<float>(xs + (w + 8 * j) * AG_C + 16 * lane, v[j]);
+            if (lane == 0) rid[w + 8 * j] = row;
+        }
     }
     __syncthreads();
     const float isc = 1.0f / sqrtf((float)AG_C);
     float sum = 0.0f;
-    for (int h = w; h < a.H; h += 8) {
-        const float* qr = a.qh + (bq * a.H + h) * AG_C;
-        float qv[16], z = 0.0f;
+    for (int h0 = 4 * w; h0 < a.H; h0 += 32) {
+        float qv[4][16], z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < 16; ++i) qv[i] = qr[lane + 32 * i];
-        for (int j = 0; j < MS_KC; ++j) {
-            float d = 0.0f;
+        for (int e = 0; e < 4; ++e) {
+            const float* qr = a.qh + (bq * a.H + min(h0 + e, a.H - 1)) * AG_C;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) d = fmaf(qv[i], xs[j * AG_C + lane + 32 * i], d);
-            d = warp_sum(d);
-            if (lane == j) z = d * isc;
+            for (int i = 0; i < 16; ++i) qv[e][i] = qr[lane + 32 * i];
         }
-        const float lse = a.lse[bq * a.H + h];
-        if (lse != -INFINITY) sum += expf(z - lse);
+#pragma unroll 1
+        for (int j0 = 0; j0 < MS_KC; j0 += 8) {
+            float d[4][8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[e][j] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float x = xs[(j0 + j) * AG_C + lane + 32 * i];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d[e][j] = fmaf(qv[e][i], x, d[e][j]);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float t = ag_sums_of_8(d[e], lane);
+                if ((lane & 24) == j0) z[e] = t * isc;       // slots j0 .. j0 + 7 belong to these lanes
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float lse = h0 + e < a.H ? a.lse[bq * a.H + h0 + e] : -INFINITY;
+            if (lse != -INFINITY) sum += expf(z[e] - lse);
+        }
     }
     ws[w * 32 + lane] = sum;
     __syncthreads();
