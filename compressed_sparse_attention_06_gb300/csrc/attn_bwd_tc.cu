@@ -4,7 +4,8 @@
 // Work item = (head pass, query, range of 128-slot tiles).  A query's image -- 128 rows of 512
 // dims, the normalised rotated heads q^ and then the rotated gradients do' -- stays in shared
 // memory for the whole item.  A tile's raw key rows X [128 slots x 512] pass through a ring of
-// four 64-dim chunks, twice: once for the logits, once for dQ (from L2 the second time):
+// four 64-dim chunks; the second half of them stays there from the logits to dQ, the first half
+// is read again (from L2):
 //   [S  dP] [128 slots x 128]  = X . image^T
 //   dQ^T [512 dims x 64 heads] += X^T . (r dS)
 //   dK [128 slots x 512 dims]  = [r dS  r P] . image
@@ -13,21 +14,29 @@
 // over the item; dK leaves per tile, in 128-dim blocks, to its place in the sorted list of
 // contributions, as bf16: the list is written and read once from device memory and its size is
 // what bounds the row sums.  The addends' rounding (2^-8 at most, of values that p and dS rounded
-// to bf16 made) is no larger than theirs; the sums over them are fp32.
+// to bf16 made) is no larger than theirs; the sums over them are fp32.  dq^ leaves as fp32: a
+// query of few keys has one that is nearly parallel to q^, and the norm's backward pass takes
+// that part away (as bf16, 50 us less at 2,048 queries, its rounding was 3 times the rest there).
 //
-// What bounds it: the MMAs.  One of M = 128 costs the same for N = 64 and N = 128 (81 cycles
-// K-major, 92 to 105 with MN-major operands here), so what counts is that no product runs with
-// less than 128 slots in it.  The image and a whole tile do not fit shared memory together;
-// with X kept there between its two uses, half a tile at a time, S ran at N = 64 (64 MMAs for
-// 128 slots, here 32) and every half waited for the one before: 919 us for 2,048 queries of 640
-// slots.
+// What bounds it: the MMAs (96 a tile; one of M = 128 costs the same for N = 64 and N = 128, 81
+// cycles K-major and 92 to 105 with MN-major operands here, about 9,000 a tile) and the waits
+// between them: for chunks on their way from L2 (2,000 cycles under load, with room for half a
+// tile only) and for the softmax (1,300).  2,048 queries of 640 slots: 626 us, 15,000 cycles a
+// tile.  What was measured against it (product kernel, the same call):
+//   870 us  64 slots a tile, so that S, dQ and dK all run at N = 64
+//   919 us  X kept in shared memory between its two uses, half a tile at a time: 64 MMAs for S
+//           instead of 32, and every half waits for the one before
+//   922 us  a lane storing its own slot's 32-byte pieces of dK; whole 128-byte lines by a 4 x 4
+//           exchange between neighbouring lanes, as below: 704
+//   1,132 us  two CTAs of a cluster with 256 dims each (every product N >= 128, but the halves of
+//           S and dP are summed through distributed shared memory, 48 KB a tile at 12 bytes a cycle)
 //
-// Warp roles (448 threads: 144 registers each, so nothing spills -- beside 226 KB of shared
-// memory there is no L1, and a spilled register is read from L2; one CTA per SM, persistent):
+// Warp roles (448 threads of 128 registers, so nothing spills -- beside 226 KB of shared memory
+// there is no L1, and a spilled register is read from L2; one CTA per SM, persistent):
 //   warp 0        the images (four 32 KB bulk copies, each freed by its dK block)
 //   warp 1        MMA issuer; owns the tensor memory
 //   warps 2-5     softmax: one thread per slot
-//   warps 6-9     loaders: 16-byte cp.async, 32 slots each
+//   warps 6-9     loaders: 16-byte cp.async, a warp one place of the ring
 //   warps 10-13   drain: dK blocks, one thread per slot; dQ at the end of the item
 // Every wait is bounded; a wait that expires flags a timeout and the roles wind down.
 #include <algorithm>
@@ -479,7 +488,7 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
         const int x = warp - 6;
         const int sub = lane >> 3, piece = lane & 7;          // a copy moves 128 bytes of four rows
         // (an empty slot's copy reads nothing; its address is a row of whichever array there is)
-        const uint8_t* kv = reinterpret_cast<const uint8_t*>(a.c.slots.n_kv > 0 ? a.c.kv : a.c.swa) + piece * 16;
+        const uint8_t* kv = reinterpret_cast<const uint8_t*>(a.c.kv ? a.c.kv : a.c.swa) + piece * 16;
         const uint8_t* swa = reinterpret_cast<const uint8_t*>(a.c.swa) + piece * 16;
         // rows 8 apart have the same swizzle
         uint8_t* dst0 = sX + x * CHUNK + sw128_offset((uint32_t)sub, (uint32_t)piece);

@@ -71,6 +71,25 @@ def test_mass(kind, q_dtype, B, Q, H, N, k, pad):
     assert torch.equal(acc[free], acc0[free])
 
 
+@pytest.mark.parametrize("kind,Q,flags", [("bf16", 330, 7), ("fp4", 330, 7), ("bf16", 3, 0), ("fp4", 3, 0), ("f32", 3, 0),
+                                          ("bf16", 200, 4), ("fp4", 200, 2), ("f32", 200, 1)])
+def test_mass_flags_and_many_tiles_of_a_cta(kind, Q, flags):
+    """Several queries of several tiles for each CTA, so every ring and image turns over.  q enters
+    as two bf16 numbers, 2^-18 of each value away at most: of a logit with normalised rows that is
+    an RSS of 2^-18 x 1.3, a weight's relative error below 2e-5 at five deviations."""
+    H, N, k = 16, 600, 290
+    kv, kv_np = _cache(41, 1, N, kind)
+    q = W.normal_tensor((1, Q, H, 512), 41, 1, torch.float32 if kind == "f32" else torch.bfloat16, DEV)
+    idx = _idx(41, 1, Q, N, k, 130)
+    q_pos = torch.arange(Q, device=DEV).view(1, Q) * 13
+    _, lse = C.csa2_sparse_attn(q, kv, idx, None, q_pos, None, window=0, want_lse=True, flags=flags)
+    w, _ = C.csa2_attn_mass(q, kv, q_pos, lse, idx=idx, want_weights=True, flags=flags)
+    C.csa2_ctx_check()
+    ow, _ = G.attn_mass(to_np(q[0]), kv_np[0], to_np(idx[0]), to_np(q_pos[0]), to_np(lse[0]), flags=flags)
+    assert_close(to_np(w[0]), ow, TOL, "weights")
+    assert not w[idx < 0].any()
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 def test_mass_dense(kind):
     B, Q, H, N = 2, 5, 24, 140
