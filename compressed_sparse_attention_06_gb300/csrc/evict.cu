@@ -31,7 +31,7 @@ constexpr int EV_CTA = EV_THREADS * EV_KEYS;
 constexpr int EV_CLUSTER = 8;
 constexpr int64_t EV_SHORT = (int64_t)EV_CTA * EV_CLUSTER;   // the longest row of the one-launch path
 constexpr int EL_THREADS = 512;
-constexpr int EL_CHUNK = 16384;         // entries a block of the long path takes
+constexpr int EL_CHUNK = 8192;          // least entries a block of the long path takes, and their step
 constexpr unsigned FULL = 0xffffffffu;
 
 // Key of a weight: larger weight, larger key; NaN (of any sign) above +inf.
@@ -46,7 +46,7 @@ struct EvictArgs {
     unsigned* st;
     uint32_t* hist;                     // long path: [B][3][EV_BINS]
     uint32_t* cnt;                      // long path: [B][chunks][2] entries above / at the threshold
-    int chunks;
+    int chunks, chunk;                  // chunks of a row, entries of a chunk
 };
 
 // A row's entries: n (clamped to ld), of which the last `recent` stay without a contest when
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(EL_THREADS) evict_long_count_kernel(EvictArgs 
     if (pass == 0)
         write_sure(a, r, a.out + b * (int64_t)a.keep, (int64_t)blockIdx.x * EL_THREADS + threadIdx.x,
                    (int64_t)gridDim.x * EL_THREADS);
-    const int64_t e0 = (int64_t)blockIdx.x * EL_CHUNK, e1 = min(r.m, e0 + EL_CHUNK);
+    const int64_t e0 = (int64_t)blockIdx.x * a.chunk, e1 = min(r.m, e0 + a.chunk);
     if (r.want == 0 || e0 >= e1) return;
     uint32_t* rows = a.hist + b * 3 * EV_BINS;
     uint32_t prefix, mask, rest;
@@ -323,13 +323,13 @@ __global__ void __launch_bounds__(EL_THREADS) evict_long_write_kernel(EvictArgs 
     pdl_trigger();
     const int64_t b = blockIdx.y;
     const Row r = row_of(a, b, false);
-    const int64_t e0 = (int64_t)blockIdx.x * EL_CHUNK, e1 = min(r.m, e0 + EL_CHUNK);
+    const int64_t e0 = (int64_t)blockIdx.x * a.chunk, e1 = min(r.m, e0 + a.chunk);
     if (r.want == 0 || e0 >= e1) return;
     uint32_t T, mask, rest;
     long_prefix(a.hist + b * 3 * EV_BINS, 3, r.want, tot, found, T, mask, rest);
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    constexpr int PER_W = EL_CHUNK / (EL_THREADS / 32);
-    const int64_t w0 = min(e1, e0 + wid * PER_W), w1 = min(e1, w0 + PER_W);
+    const int per_w = a.chunk / (EL_THREADS / 32);
+    const int64_t w0 = min(e1, e0 + wid * per_w), w1 = min(e1, w0 + per_w);
     const float* acc = a.acc + b * a.ld;
     uint32_t gt = 0, eq = 0;
     for (int64_t base = w0; base < w1; base += 16 * 32) {
@@ -439,11 +439,16 @@ extern "C" csa2_status csa2_evict_select(csa2_ctx* ctx, const float* acc, int B,
     DeviceGuard dev(ctx);
     if (!dev.ok) return CSA2_ERR_CUDA;
     cudaStream_t s = as_stream(stream);
-    EvictArgs a = {acc, ld, n_entries, keep, recent, out_idx, ctx->status, nullptr, nullptr, 0};
+    EvictArgs a = {acc, ld, n_entries, keep, recent, out_idx, ctx->status, nullptr, nullptr, 0, 0};
     if (need > 0) {
         a.hist = reinterpret_cast<uint32_t*>(ws);
         a.cnt = a.hist + (size_t)B * 3 * EV_BINS;
-        a.chunks = (int)((ld + EL_CHUNK - 1) / EL_CHUNK);
+        // one wave of blocks, two an SM, if the rows give them work (eight 1M rows in chunks of 16,384,
+        // 1.7 waves: 140 us)
+        const int64_t even = ((int64_t)B * ld + 2 * ctx->num_sms - 1) / (2 * ctx->num_sms);
+        const int64_t chunk = std::min<int64_t>(std::max<int64_t>(1, (even + EL_CHUNK - 1) / EL_CHUNK), 1 << 16) * EL_CHUNK;
+        a.chunk = (int)chunk;
+        a.chunks = (int)((ld + chunk - 1) / chunk);
         CSA2_CHECK_CUDA(cudaMemsetAsync(a.hist, 0, long_hist_bytes(B), s));
         const dim3 grid((unsigned)a.chunks, (unsigned)B), block(EL_THREADS);
         csa2_status r = CSA2_OK;
