@@ -610,7 +610,8 @@ struct BwdSizes {
 
 struct BwdLayout {
     size_t D, sink, rinv, cnt, loc, tot, blk, rank, qh, dh, pds, img, slots, dqh, part, acc, total;
-    int groups, group_q, n_pass, n_split, tps;
+    int groups, group_q, n_pass;
+    int n_split, tps;         // CUDA cores: slot ranges of a query, slots of one
 };
 
 // Stretches of queries that dsink is summed in: 32 queries are four a warp.
@@ -636,9 +637,8 @@ BwdLayout bwd_layout(const BwdSizes& z, int64_t nb) {
     L.group_q = (int)((nb + g - 1) / g);
     L.groups = (int)((nb + L.group_q - 1) / L.group_q);
     L.n_pass = z.tc ? (z.H + 63) / 64 : 1;
-    if (z.tc)
-        bwd_tc_splits(z.num_sms, nb * L.n_pass, z.n_slots, &L.n_split, &L.tps);
-    else
+    L.n_split = L.tps = 0;
+    if (!z.tc)
         simt_splits(z.num_sms, nb * ((z.H + SB_HG - 1) / SB_HG), z.n_slots, &L.n_split, &L.tps);
     size_t at = 0;
     auto take = [&at](size_t bytes) {
@@ -660,7 +660,7 @@ BwdLayout bwd_layout(const BwdSizes& z, int64_t nb) {
     L.pds = take(z.tc ? 0 : heads * z.n_slots * 8);
     L.img = take(z.tc ? (size_t)nb * L.n_pass * bwd_tc_image_bytes() : 0);
     L.slots = take(z.tc ? bwd_tc_slots_bytes(nb, z.n_slots) : 0);
-    L.dqh = take(z.tc ? (size_t)nb * L.n_pass * L.n_split * 64 * row_f32
+    L.dqh = take(z.tc ? bwd_tc_dq_bytes(z.num_sms, nb * L.n_pass, z.n_slots)
                       : (L.n_split > 1 ? heads * L.n_split * row_f32 : 0));
     L.part = take(z.tc ? pairs * L.n_pass * AG_C * 2 : pairs * row_f32);
     L.acc = take(nb < z.n_bq ? (size_t)z.rows * row_f32 : 0);
@@ -772,7 +772,7 @@ csa2_status bwd_run(csa2_ctx* ctx, const BwdCall& a, void* ws, size_t ws_bytes, 
             if (zr != CSA2_OK) return zr;
             bwd_rank_kernel<<<(unsigned)L.groups, 1024, 0, s>>>(c.slots, bq0, c.nb, L.group_q, n_slots, rows, cnt, rank);
             bwd_place_kernel<<<(unsigned)n_blk, BWD_SCAN_ROWS, 0, s>>>(cnt, L.groups, rows, loc, tot, blk);
-            bwd_scan_kernel<<<1, 1024, 0, s>>>(blk, n_blk);
+            bwd_scan(blk, n_blk, s);
         }
         float* qh = reinterpret_cast<float*>(base + L.qh);
         float* dh = reinterpret_cast<float*>(base + L.dh);
@@ -784,8 +784,6 @@ csa2_status bwd_run(csa2_ctx* ctx, const BwdCall& a, void* ws, size_t ws_bytes, 
             t.c = c;
             t.dqh = reinterpret_cast<float*>(base + L.dqh);
             t.n_pass = L.n_pass;
-            t.n_split = L.n_split;
-            t.tps = L.tps;
             r = bwd_tc_chunk(ctx, t, a.dout, a.out, D, base + L.img, base + L.slots, s);
         } else if (a.q_dt == CSA2_F32)
             r = a.out_dt == CSA2_F32 ? simt_chunk<float, float>(ctx, a, c, qh, dh, pds, dqh, L.n_split, L.tps, s)
@@ -864,6 +862,8 @@ csa2_status bwd_impl(csa2_ctx* ctx, const BwdCall& a, int c, void* ws, size_t ws
 }
 
 }  // namespace
+
+void bwd_scan(uint32_t* blk, int64_t n, cudaStream_t s) { bwd_scan_kernel<<<1, 1024, 0, s>>>(blk, n); }
 
 extern "C" size_t csa2_attn_bwd_workspace_bytes(csa2_ctx* ctx, csa2_dtype q_dt, csa2_dtype kv_dt, csa2_dtype swa_dt,
                                                 csa2_dtype out_dt, int B, int Q, int H, int k, int window, int64_t N,

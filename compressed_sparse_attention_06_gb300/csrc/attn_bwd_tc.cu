@@ -65,11 +65,12 @@ constexpr int OFF_IMG = 0;
 constexpr int OFF_X = OFF_IMG + IMG_BYTES;
 constexpr int OFF_DSP = OFF_X + X_RING * CHUNK;  // r dS, then r P: [128 slots][64 heads]
 constexpr int OFF_LD = OFF_DSP + 2 * CHUNK;      // [4 warps][64 heads] -lse (base 2), -D / sqrt(c)
-constexpr int OFF_BAR = OFF_LD + 4 * BT_H * 8;
+constexpr int OFF_START = OFF_LD + 4 * BT_H * 8;
+constexpr int OFF_BAR = OFF_START + 16;
 constexpr int N_BAR = 4 + 4 + 2 * X_RING + 9;
 constexpr int OFF_TMEMPTR = OFF_BAR + N_BAR * 8;
 constexpr int SMEM_BYTES = OFF_TMEMPTR + 16;
-static_assert(OFF_BAR % 8 == 0, "barrier alignment");
+static_assert(OFF_START % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 
 // The 8 words lo of the upper lane of a pair `d` apart and hi of the lower one change places.
@@ -87,10 +88,11 @@ __device__ __forceinline__ void swap_pieces(uint32_t* lo, uint32_t* hi, int d, b
 // The slots of a query that hold something, in order -- its cache slots, then the window slots
 // whose position is not before 0 -- as the roles below want them: code[q][s] = a cache row's
 // number, -2 - a window row's, or -1 (empty); fac[q][s] = the row's RMS factor, 0 if empty;
-// place[q][s] = its contribution's place, -1 if empty; n_of[q] = how many.  A chain of three
+// place[q][s] = its contribution's place, -1 if empty; n_of[q] = how many, tile0[q] = the tiles
+// they fill (scanned afterwards: the tiles of the queries before).  A chain of three
 // dependent lookups a slot, made here with every slot at once and read back in one access.
 __global__ void __launch_bounds__(256) bwd_tc_slots_kernel(BwdTcArgs a, int32_t* code, float* fac, int32_t* place,
-                                                           int32_t* n_of) {
+                                                           int32_t* n_of, uint32_t* tile0) {
     const SlotArgs& sl = a.c.slots;
     const int q = blockIdx.y, s = blockIdx.x * 256 + threadIdx.x;
     if (s >= a.n_pad) return;
@@ -105,33 +107,105 @@ __global__ void __launch_bounds__(256) bwd_tc_slots_kernel(BwdTcArgs a, int32_t*
     place[at] = row >= 0 ? (int32_t)(a.c.blk[row / BWD_SCAN_ROWS] + a.c.base[(int64_t)(q / a.c.group_q) * a.c.rows + row]) +
                                a.c.rank[(int64_t)q * a.c.n_slots + slot]
                          : -1;
-    if (s == 0) n_of[q] = kq + nw;
+    if (s == 0) {
+        n_of[q] = kq + nw;
+        tile0[q] = (uint32_t)((kq + nw + BT_TILE - 1) / BT_TILE);
+        if (q == 0) tile0[a.c.nb] = 0u;
+    }
+}
+
+// The (pass, query) pairs v = pass * nb + query are dealt out whole, one a CTA and wave, as long as
+// that fills the wave; the tiles of the rest are shared evenly, so there a query's may go to
+// several CTAs (whose dq^ are added) and a CTA have the end of one query and the beginning of
+// another.  (Whole queries, or equal parts of them, to the end leave the last wave half empty:
+// 666 pairs of 9 tiles took 399 us.  Even shares of everything, 410 us and 2,048 queries 10 %
+// more: neighbouring queries' contributions are neighbours in the list, and are written
+// together only if they run together.)
+struct Tail {
+    uint32_t first, before, all, per;                // first pair; tiles before it and in all; a CTA's share
+};
+
+__device__ __forceinline__ Tail tail_of(const BwdTcArgs& a) {
+    const uint32_t total = a.tile0[a.c.nb];
+    Tail r;
+    r.first = a.waves * a.ctas;
+    r.before = r.first / a.c.nb * total + a.tile0[r.first % a.c.nb];
+    r.all = total * a.n_pass;
+    r.per = max(1u, (r.all - r.before + a.ctas - 1) / a.ctas);
+    return r;
 }
 
 struct Item {
     int v;                       // pass * nb + query: the image
     int q, pass;                 // query within the chunk
-    int n, t0, nt;               // the query's slots; tiles t0 .. t0 + nt - 1
+    int t0, nt;                  // tiles t0 .. t0 + nt - 1 of the query's
+    int dq;                      // its dq^: v in the waves, v + CTA in the shared rest
 };
 
-// The CTA's items one after the other; the next item's number of slots is read ahead.
+// Where a CTA's share of the rest begins, and how many tiles it has.
+struct Start {
+    int pass, q, t0, tiles;
+};
+
+// (by one warp: the last query whose tiles begin at or before the share's first)
+__device__ __forceinline__ Start find_start(const BwdTcArgs& a, int lane) {
+    const Tail tail = tail_of(a);
+    const uint32_t total = a.tile0[a.c.nb], g = tail.before + blockIdx.x * tail.per;
+    Start r = {0, 0, 0, 0};
+    if (g >= tail.all) return r;
+    r.tiles = (int)min(tail.per, tail.all - g);
+    r.pass = (int)(g / total);
+    const uint32_t t = g - r.pass * total;
+    int lo = 0, n = a.c.nb;                          // the query is one of lo .. lo + n - 1
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = lo + lane * step;
+        const unsigned le = __ballot_sync(FULL, at < lo + n && a.tile0[min(at, a.c.nb)] <= t);
+        const int k = 31 - __clz(le);                // (lane 0's is one of them)
+        n = min(step, n - k * step);
+        lo += k * step;
+    }
+    r.q = lo;
+    r.t0 = (int)(t - a.tile0[lo]);
+    return r;
+}
+
+// The CTA's items one after the other (one without tiles where a query has none); the next
+// one's number of slots is read ahead.
 struct Items {
     const BwdTcArgs& a;
-    uint32_t i;
-    int n;
-    __device__ __forceinline__ explicit Items(const BwdTcArgs& args) : a(args), i(blockIdx.x) { look(); }
-    __device__ __forceinline__ void look() { n = a.n_of[(min(i, a.items - 1) / a.n_split) % a.c.nb]; }
-    __device__ __forceinline__ bool more() const { return i < a.items; }
-    __device__ __forceinline__ Item next() {
+    uint32_t v, step;                                // the next item's pair; pairs to the one after it
+    int t0, left, n;                                 // its first tile; the rest's tiles; its slots
+    __device__ __forceinline__ Items(const BwdTcArgs& args, const Start& s)
+        : a(args), v(blockIdx.x), step(args.ctas), t0(0), left(s.tiles) {
+        if (a.waves == 0) rest(s);
+        n = a.n_of[v % a.c.nb];
+    }
+    __device__ __forceinline__ void rest(const Start& s) {
+        v = (uint32_t)(s.pass * a.c.nb + s.q);
+        step = 1;
+        t0 = s.t0;
+    }
+    __device__ __forceinline__ bool more() const { return step > 1 || left > 0; }
+    __device__ __forceinline__ Item next(const Start& s) {
+        const int tiles = (n + BT_TILE - 1) / BT_TILE;
         Item r;
-        r.v = (int)(i / a.n_split);
+        r.v = (int)v;
         r.pass = r.v / a.c.nb;
         r.q = r.v - r.pass * a.c.nb;
-        r.n = n;
-        r.t0 = (int)(i - (uint32_t)r.v * a.n_split) * a.tps;
-        r.nt = max(0, min((r.n + BT_TILE - 1) / BT_TILE, r.t0 + a.tps) - r.t0);
-        i += gridDim.x;
-        look();
+        r.t0 = t0;
+        r.dq = r.v;
+        r.nt = tiles;
+        if (step > 1) {
+            v += step;
+            if (v >= a.waves * a.ctas) rest(s);
+        } else {
+            r.dq += blockIdx.x;
+            r.nt = min(tiles - t0, left);
+            left -= r.nt;
+            t0 = 0;
+            ++v;
+        }
+        n = a.n_of[v % a.c.nb];
         return r;
     }
 };
@@ -195,7 +269,7 @@ __global__ void __launch_bounds__(256) bwd_tc_prep_kernel(const __nv_bfloat16* q
     }
 }
 
-// dq from dq^ (the sum of the item's splits): back through RoPE and the query's RMSNorm.  A
+// dq from dq^ (the sum over the CTAs that had tiles of the query): back through RoPE and the query's RMSNorm.  A
 // warp per (query, head); a query that attends to nothing has no gradient.
 __global__ void __launch_bounds__(256) bwd_tc_dq_kernel(BwdTcArgs a, const float* dqh, __nv_bfloat16* dq) {
     __shared__ float cs[8][32], sn[8][32];
@@ -204,19 +278,31 @@ __global__ void __launch_bounds__(256) bwd_tc_dq_kernel(BwdTcArgs a, const float
     if (r >= (int64_t)a.c.nb * a.c.H) return;
     const int qi = (int)(r / a.c.H), h = (int)(r % a.c.H);
     const int64_t bq = a.c.bq0 + qi, o = (bq * a.c.H + h) * BT_C + 16 * lane;
+    const int pass = h >> 6;
+    const uint32_t v0 = (uint32_t)pass * a.c.nb + qi;
+    auto sum_at = [&](uint32_t k) { return dqh + ((int64_t)k * BT_H + (h & 63)) * BT_C + 16 * lane; };
+    const bool whole = v0 < a.waves * a.ctas;
+    float g[16], v[16];
+    if (whole) ag_load16<float>(sum_at(v0), g);
+    ag_load16<__nv_bfloat16>(reinterpret_cast<const __nv_bfloat16*>(a.c.q) + o, v);
+    const uint32_t tiles = a.tile0[qi + 1] - a.tile0[qi];
     ag_cos_sin(a.c.rope, a.c.slots.q_pos[bq], lane, cs[w][lane], sn[w][lane]);
     __syncwarp();
-    float g[16], v[16];
+    if (!whole || tiles == 0) {                      // (nobody wrote the sum of a query without keys)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) g[i] = 0.0f;
-    const int64_t item = ((int64_t)(h >> 6) * a.c.nb + qi) * a.n_split;
-    for (int s = 0; s < a.n_split; ++s) {
-        float p[16];
-        ag_load16<float>(dqh + ((item + s) * BT_H + (h & 63)) * BT_C + 16 * lane, p);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) g[i] += p[i];
+        for (int i = 0; i < 16; ++i) g[i] = 0.0f;
     }
-    ag_load16<__nv_bfloat16>(reinterpret_cast<const __nv_bfloat16*>(a.c.q) + o, v);
+    if (!whole && tiles > 0) {
+        const Tail tail = tail_of(a);
+        const uint32_t begin = pass * a.tile0[a.c.nb] + a.tile0[qi] - tail.before;
+        const uint32_t last = (begin + tiles - 1) / tail.per;
+        for (uint32_t s = begin / tail.per; s <= last; ++s) {
+            float p[16];
+            ag_load16<float>(sum_at(v0 + s), p);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) g[i] += p[i];
+        }
+    }
     const float f = ag_rms_factor(warp_sum(ag_sumsq16(v)));
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] *= f;
@@ -282,10 +368,15 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
         tmem_alloc(sTmem, TMEM_COLS);
         tmem_relinquish();
     }
+    if (warp == 2) {
+        const Start s = find_start(a, lane);
+        if (lane == 0) *reinterpret_cast<Start*>(smem + OFF_START) = s;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *sTmem;
+    const Start* start = reinterpret_cast<const Start*>(smem + OFF_START);
 
     if (warp == 0) {
         // ============================ images ============================
@@ -294,8 +385,8 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
             bool ok = true;
             int issued = 0;                          // blocks issued in the last item, and their phase
             uint32_t par = 0;
-            for (Items items(a); items.more() && ok && !a.stall;) {
-                const Item it = items.next();
+            for (Items items(a, *start); items.more() && ok && !a.stall;) {
+                const Item it = items.next(*start);
                 if (it.nt == 0) continue;
                 issued = 0;
                 par = n & 1;
@@ -369,8 +460,8 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
                 if (last) mma_commit(&imgempty[db]);
                 if (db == 3) mma_commit(dspempty);
             };
-            for (Items items(a); items.more() && ok;) {
-                const Item it = items.next();
+            for (Items items(a, *start); items.more() && ok;) {
+                const Item it = items.next(*start);
                 if (it.nt == 0) continue;
                 if (g > 0 && !wait(sempty, (g - 1) & 1)) break;
                 for (int ch = 0; ch < 8 && ok; ++ch)
@@ -410,8 +501,8 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
         const float isc = 1.0f / sqrtf((float)BT_C);
         uint32_t t = 0;
         bool ok = true;
-        for (Items items(a); items.more() && ok;) {
-            const Item it = items.next();
+        for (Items items(a, *start); items.more() && ok;) {
+            const Item it = items.next(*start);
             if (it.nt == 0) continue;
             __syncwarp();
 #pragma unroll
@@ -525,8 +616,8 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
                 if (lane == 0) mbar_arrive(&xfull[x]);
             }
         };
-        for (Items items(a); items.more() && ok;) {
-            const Item it = items.next();
+        for (Items items(a, *start); items.more() && ok;) {
+            const Item it = items.next(*start);
             if (it.nt == 0) continue;
             const int32_t* codes = a.code + (int64_t)it.q * a.n_pad + it.t0 * BT_TILE + lane;
             int code[4], next[4];                             // read a tile ahead
@@ -552,13 +643,11 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
         uint32_t k = 0;
         int n = 0;
         bool ok = true;
-        for (Items items(a); items.more() && ok;) {
-            const Item it = items.next();
-            float* dqh = a.dqh + (int64_t)(items.i - gridDim.x) * (BT_H * BT_C) + slot;      // here: dim of a block
-            if (it.nt == 0) {
-                for (int j = 0; j < BT_H * 4; ++j) dqh[(j >> 2) * BT_C + (j & 3) * 128] = 0.0f;
-                continue;
-            }
+        for (Items items(a, *start); items.more() && ok;) {
+            const Item it = items.next(*start);
+            if (it.nt == 0) continue;
+            // (slot: here the dim of a block)
+            float* dqh = a.dqh + (int64_t)it.dq * (BT_H * BT_C) + slot;
             uint8_t* base = reinterpret_cast<uint8_t*>(a.c.part) + it.pass * (BT_C * 2) + (lane & 3) * 32;
             // the place of the slot's contribution (-1: empty), read a tile ahead
             const int32_t* place = a.place + (int64_t)it.q * a.n_pad + it.t0 * BT_TILE + slot;
@@ -637,6 +726,12 @@ __global__ void __launch_bounds__(BT_THREADS, 1) attn_bwd_tc_kernel(const BwdTcA
 
 int pad_slots(int n) { return std::max(1, (n + BT_TILE - 1) / BT_TILE) * BT_TILE; }
 
+// CTAs for `queries` (times head passes): one a tile, at most one an SM (sizes are also asked for
+// without a GPU).
+int64_t ctas_for(int num_sms, int64_t queries, int n_slots) {
+    return std::min<int64_t>(std::max(1, num_sms), queries * (pad_slots(n_slots) / BT_TILE));
+}
+
 }  // namespace
 
 bool bwd_tc_applies(csa2_dtype q_dt, csa2_dtype kv_dt, int k, csa2_dtype swa_dt, int window, csa2_dtype out_dt,
@@ -645,27 +740,15 @@ bool bwd_tc_applies(csa2_dtype q_dt, csa2_dtype kv_dt, int k, csa2_dtype swa_dt,
            out_dt == CSA2_BF16 && (flags & (CSA2_QNORM | CSA2_KVNORM)) == (CSA2_QNORM | CSA2_KVNORM);
 }
 
-void bwd_tc_splits(int num_sms, int64_t queries, int n_slots, int* n_split, int* tps) {
-    // the split whose waves of CTAs are shortest; an item costs about half a tile besides its tiles
-    // (192 queries of 401 slots: 168 us with one item each, two uneven waves)
-    const int tiles = std::max(1, (n_slots + BT_TILE - 1) / BT_TILE);
-    const int64_t sms = std::max(1, num_sms);         // (sizes are also asked for without a GPU)
-    int64_t best = INT64_MAX;
-    for (int t = tiles; t >= 1; --t) {
-        const int n = (tiles + t - 1) / t;
-        const int64_t cost = (queries * n + sms - 1) / sms * (2 * t + 1);
-        if (cost < best) {
-            best = cost;
-            *tps = t;
-            *n_split = n;
-        }
-    }
+// dq^ of every (query, CTA that has tiles of it).
+size_t bwd_tc_dq_bytes(int num_sms, int64_t queries, int n_slots) {
+    return (size_t)(queries + ctas_for(num_sms, queries, n_slots) - 1) * BT_H * BT_C * 4;
 }
 
 size_t bwd_tc_image_bytes() { return IMG_BYTES; }
 
 size_t bwd_tc_slots_bytes(int64_t nb, int n_slots) {
-    return (size_t)(nb * (3 * (int64_t)pad_slots(n_slots) + 1)) * 4;
+    return (size_t)(nb * (3 * (int64_t)pad_slots(n_slots) + 2) + 1) * 4;
 }
 
 csa2_status bwd_tc_chunk(csa2_ctx* ctx, BwdTcArgs& a, const void* dout, const void* out, float* D, uint8_t* img,
@@ -686,12 +769,15 @@ csa2_status bwd_tc_chunk(csa2_ctx* ctx, BwdTcArgs& a, const void* dout, const vo
     int32_t* place = code + (int64_t)c.nb * a.n_pad;
     float* fac = reinterpret_cast<float*>(place + (int64_t)c.nb * a.n_pad);
     int32_t* n_of = reinterpret_cast<int32_t*>(fac + (int64_t)c.nb * a.n_pad);
+    uint32_t* tile0 = reinterpret_cast<uint32_t*>(n_of + c.nb);
     a.code = code;
     a.place = place;
     a.fac = fac;
     a.n_of = n_of;
-    bwd_tc_slots_kernel<<<dim3((unsigned)((a.n_pad + 255) / 256), (unsigned)c.nb), 256, 0, s>>>(a, code, fac, place, n_of);
-    a.items = (uint32_t)c.nb * a.n_pass * a.n_split;
+    a.tile0 = tile0;
+    bwd_tc_slots_kernel<<<dim3((unsigned)((a.n_pad + 255) / 256), (unsigned)c.nb), 256, 0, s>>>(a, code, fac, place, n_of, tile0);
+    bwd_scan(tile0, (int64_t)c.nb + 1, s);
+    a.ctas = (uint32_t)ctas_for(ctx->num_sms, (int64_t)c.nb * a.n_pass, c.n_slots);
     a.budget = WAIT_BUDGET;
     a.stall = 0;
     if (ctx->stall_next) {
@@ -699,8 +785,8 @@ csa2_status bwd_tc_chunk(csa2_ctx* ctx, BwdTcArgs& a, const void* dout, const vo
         if (ctx->stall_budget > 0) a.budget = ctx->stall_budget;
         ctx->stall_next = 0;
     }
-    const int64_t grid = std::min<int64_t>(a.items, ctx->num_sms);
-    attn_bwd_tc_kernel<<<(unsigned)grid, BT_THREADS, SMEM_BYTES, s>>>(a);
+    a.waves = a.ctas > 1 ? (uint32_t)c.nb * a.n_pass / a.ctas : 0;      // (a step of 1 marks the shared rest)
+    attn_bwd_tc_kernel<<<a.ctas, BT_THREADS, SMEM_BYTES, s>>>(a);
     const int64_t heads = (int64_t)c.nb * c.H;
     bwd_tc_dq_kernel<<<(unsigned)((heads + 7) / 8), 256, 0, s>>>(a, a.dqh, reinterpret_cast<__nv_bfloat16*>(c.dq));
     return csa2_launch_status();
