@@ -21,7 +21,7 @@
 // What bounds it: the MMAs (96 a tile; one of M = 128 costs the same for N = 64 and N = 128, 81
 // cycles K-major and 92 to 105 with MN-major operands here, about 9,000 a tile) and the waits
 // between them: for chunks on their way from L2 (2,000 cycles under load, with room for half a
-// tile only) and for the softmax (1,300).  2,048 queries of 640 slots: 626 us, 15,000 cycles a
+// tile only) and for the softmax (1,300).  2,048 queries of 640 slots: 618 us, 15,000 cycles a
 // tile.  What was measured against it (product kernel, the same call):
 //   870 us  64 slots a tile, so that S, dQ and dK all run at N = 64
 //   919 us  X kept in shared memory between its two uses, half a tile at a time: 64 MMAs for S

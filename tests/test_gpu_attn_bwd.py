@@ -158,6 +158,20 @@ def test_dense(dtype, tol):
     _check(s, got, tol)
 
 
+@pytest.mark.parametrize("Q,H,k,window", [(200, 70, 300, 0), (153, 16, 200, 100), (40, 128, 700, 3)])
+def test_whole_waves_and_a_shared_rest(Q, H, k, window):
+    """More (head pass, query) pairs than CTAs, so some are dealt out whole and the tiles of the rest
+    are shared, or fewer, so all are; queries of 0 to 6 tiles, some of none."""
+    pos = [[(11 * i) % 400 - 5 for i in range(Q)]]
+    s = _forward(_case(23, 1, Q, H, k, k, window, max(window, 1), pos, torch.bfloat16, dense=True))
+    assert bool((s["nv"] == 0).any())
+    got = _backward(s)
+    C.csa2_ctx_check()
+    _check(s, got, TC_TOL)
+    for a, b in zip(got, _backward(s)):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("dtype,tol", [(torch.float32, F32_TOL), (torch.bfloat16, TC_TOL)])
 @pytest.mark.parametrize("sink", [True, False])
 def test_queries_without_keys_and_repeated_indices(dtype, tol, sink):
