@@ -717,16 +717,10 @@ def csa2_compress_bwd(ca, za, m: int, dout, cb=None, zb=None, ba=None, bb=None, 
     else:
         pos_t = torch.full((B,), int(pos0), dtype=torch.int64, device=dev) if pos0 else None
 
-    # one allocation for the streams' gradients, one for the history's, one for the biases'
-    def like(*ts):
-        n = sum(t is not None for t in ts)
-        if n == 0:
-            return [None] * len(ts)
-        t0 = next(t for t in ts if t is not None)
-        parts = iter(alloc((n, *t0.shape), dtype=t0.dtype, device=dev).unbind(0))
-        return [next(parts) if t is not None else None for t in ts]
+    def like(t):
+        return alloc(t.shape, dtype=t.dtype, device=dev) if t is not None else None
 
-    g = CompressGrads(*like(ca, za, cb, zb), *like(prev_cb, prev_zb), *like(ba, bb))
+    g = CompressGrads(like(ca), like(za), like(cb), like(zb), like(prev_cb), like(prev_zb), like(ba), like(bb))
     if ws is None and (ba is not None or bb is not None):
         ws = _ws(_lib().csa2_compress_bwd_workspace_bytes(B, n, c, m, int(cb is not None)), dev)
     st = _lib().csa2_compress_bwd(ctx(dev.index), _main(ca), _a(za), _a(cb), _a(zb), _dt(ca), _a(ba), _a(bb), _a(prev_cb),

@@ -169,8 +169,10 @@ struct MassLayout {
 
 MassLayout mass_layout(csa2_dtype kv_dt, int B, int Q, int H, int k, int64_t N, bool want_acc) {
     MassLayout L;
-    // a table of RMS factors pays when every row is gathered several times (prefill)
-    L.table = kv_dt == CSA2_BF16 && (int64_t)Q * k >= 4 * N;
+    // A table of the rows' RMS factors (one pass over the cache) or the factors of each tile from its
+    // rows: 33,792 entries, 512 slots, 32 queries (0.5 slots an entry) 33 and 32 us, 66 queries 31 and
+    // 36, 132 queries 31 and 55, 1,056 queries 100 and 315.
+    L.table = kv_dt == CSA2_BF16 && 2 * (int64_t)Q * k >= N;
     L.qh = 0;
     L.fix = kv_dt == CSA2_F32 ? align_up((size_t)B * Q * H * AG_C * 4, 256) : 0;
     L.rinv = align_up(L.fix + (want_acc && Q > 1 ? (size_t)B * N * 8 : 0), 256);

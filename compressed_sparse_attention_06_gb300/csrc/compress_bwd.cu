@@ -9,7 +9,7 @@
 //
 // Memory bound: every input row is read once and every gradient row written once.  A CTA takes
 // a run of entries, a thread a few adjacent channels of each.  The usual windows (up to 8 rows:
-// m = 1, 2, 4, 8, and overlapping m = 1, 2, 4) are compiled for their size: an entry's rows
+// m = 1, 2, 3, 4, 8, and overlapping m = 1, 2, 3, 4) are compiled for their size: an entry's rows
 // (contiguous stretches) come by bulk copies into a ring of stages in shared memory, several
 // entries ahead of the arithmetic (loads into registers one entry ahead kept 41 KB an SM in
 // flight, 3.7 TB/s over four streams of 131,072 tokens; now 448 us there, 5.4 TB/s), and stay in
@@ -25,8 +25,8 @@
 
 namespace {
 
-// CTAs: what the registers keep resident at c = 512 -- windows of 1 or 2 rows, and the general
-// kernel, 8 an SM; of 4 rows 4; of 8 rows 2.
+// CTAs: what the registers keep resident at c = 512 -- windows of 1 or 2 rows 8 an SM; of 3 or 4
+// rows 4; of 6 or 8 rows 2; of the general kernel 1,024 threads.
 constexpr int CB_CTAS = 152 * 8;
 
 template <typename T>
@@ -111,12 +111,13 @@ __device__ __forceinline__ Window<T> window_of(const CompressBwdArgs<T>& a, int6
     return w;
 }
 
-// Sums of two values over the CTA (at most 16 warps), two alternating buffers.
+// Sums of two values over the CTA's threads along x (at most 16 warps; others along y have the
+// same values), two alternating buffers.
 __device__ __forceinline__ void block_sum2(float& x, float& y, float2* red) {
     x = warp_sum(x);
     y = warp_sum(y);
     const int nw = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(x, y);
+    if ((threadIdx.x & 31) == 0 && threadIdx.y == 0) red[threadIdx.x >> 5] = make_float2(x, y);
     __syncthreads();
     x = y = 0.0f;
     for (int i = 0; i < nw; ++i) {
@@ -362,18 +363,25 @@ csa2_status usual_window(const csa2_ctx* ctx, const CompressBwdArgs<T>& a, unsig
     return a.slab ? launch_window<T, M, OV, CH, true>(ctx, a, grid, s) : launch_window<T, M, OV, CH, false>(ctx, a, grid, s);
 }
 
-// Any m: four channels a thread, the window's rows read once for the maximum, once for the sums
-// and once for the gradients.
+// Any m: four channels a thread; the window's rows are dealt out to groups of c / 4 threads, read once for the maximum, once for the sums and once for the gradients (the
+// latter two from L2).  The groups' maxima and sums meet in shared memory, in group order.
+// (512 entries of 128 rows, with biases: 197 us; one group for the whole window 431 us; groups of
+// half as many threads, each with four rows' loads in flight, 256 us.)  __expf: the exponents are
+// at most 0.
 template <typename T>
-__global__ void __launch_bounds__(256) compress_bwd_any_kernel(CompressBwdArgs<T> a) {
+__global__ void __launch_bounds__(1024) compress_bwd_any_kernel(CompressBwdArgs<T> a) {
     __shared__ float2 red[2][16];
-    const int ch = 4 * threadIdx.x;
+    __shared__ __align__(16) float meet[2][4096];             // [group][channel]
+    const int ch = 4 * threadIdx.x, grp = threadIdx.y, groups = blockDim.y;
     const int m = a.m, c = a.c;
     const int64_t e0 = (int64_t)blockIdx.x * a.run, e1 = min(a.entries, e0 + a.run);
     const int tables = a.cb ? 2 : 1;
     float* slab = a.slab ? a.slab + (int64_t)blockIdx.x * tables * m * c + ch : nullptr;
+    // (the first entry writes the block rows' sums; one without history leaves the second table's as
+    // they are, so those start at 0)
     if (slab)
-        for (int j = 0; j < tables * m; ++j) *reinterpret_cast<float4*>(slab + (int64_t)j * c) = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = e0 < e1 ? m + grp : grp; j < tables * m; j += groups) *reinterpret_cast<float4*>(slab + (int64_t)j * c) = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto mine = [&](int which, int g) { return reinterpret_cast<float4*>(&meet[which][g * c + ch]); };
     for (int64_t e = e0; e < e1; ++e) {
         const int64_t b = e / a.n_ent, i = e - b * a.n_ent;
         const Window<T> w = window_of(a, b, i);
@@ -400,22 +408,49 @@ __global__ void __launch_bounds__(256) compress_bwd_any_kernel(CompressBwdArgs<T
         unpack4(a.dout_f32 ? ld4<float>(reinterpret_cast<const float*>(a.dout) + go)
                            : ld4<__nv_bfloat16>(reinterpret_cast<const __nv_bfloat16*>(a.dout) + go), g);
 #pragma unroll 8
-        for (int j = 0; j < rows; ++j) {
+        for (int j = grp; j < rows; j += groups) {
             logit(j, t);
 #pragma unroll
             for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], t[k]);
         }
+        *mine(0, grp) = make_float4(mx[0], mx[1], mx[2], mx[3]);
+        __syncthreads();
+        for (int o = 0; o < groups; ++o) {
+            const float4 u = *mine(0, o);
+            mx[0] = fmaxf(mx[0], u.x);
+            mx[1] = fmaxf(mx[1], u.y);
+            mx[2] = fmaxf(mx[2], u.z);
+            mx[3] = fmaxf(mx[3], u.w);
+        }
+        __syncthreads();
 #pragma unroll 4
-        for (int j = 0; j < rows; ++j) {
+        for (int j = grp; j < rows; j += groups) {
             logit(j, t);
             unpack4(ld4<T>(src(w.c0, w.c1, j)), x);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float p = expf(t[k] - mx[k]);
+                const float p = __expf(t[k] - mx[k]);
                 den[k] += p;
                 E[k] = fmaf(p, x[k], E[k]);
             }
         }
+        *mine(0, grp) = make_float4(den[0], den[1], den[2], den[3]);
+        *mine(1, grp) = make_float4(E[0], E[1], E[2], E[3]);
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) den[k] = E[k] = 0.0f;
+        for (int o = 0; o < groups; ++o) {
+            const float4 u = *mine(0, o), v = *mine(1, o);
+            den[0] += u.x;
+            den[1] += u.y;
+            den[2] += u.z;
+            den[3] += u.w;
+            E[0] += v.x;
+            E[1] += v.y;
+            E[2] += v.z;
+            E[3] += v.w;
+        }
+        __syncthreads();
 #pragma unroll
         for (int k = 0; k < 4; ++k) E[k] /= den[k];
         if ((a.flags & CSA2_W_ROPE) && ch >= c - 64) {
@@ -445,13 +480,13 @@ __global__ void __launch_bounds__(256) compress_bwd_any_kernel(CompressBwdArgs<T
 #pragma unroll
         for (int k = 0; k < 4; ++k) den[k] = 1.0f / den[k];
 #pragma unroll 4
-        for (int j = 0; j < rows; ++j) {
+        for (int j = grp; j < rows; j += groups) {
             logit(j, t);
             unpack4(ld4<T>(src(w.c0, w.c1, j)), x);
             float dc[4], dz[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                dc[k] = expf(t[k] - mx[k]) * den[k] * g[k];
+                dc[k] = __expf(t[k] - mx[k]) * den[k] * g[k];
                 dz[k] = dc[k] * (x[k] - E[k]);
             }
             const int64_t o = (int64_t)(j < m ? j : j - m) * c + ch;
@@ -461,7 +496,7 @@ __global__ void __launch_bounds__(256) compress_bwd_any_kernel(CompressBwdArgs<T
             if (gz) st4<T>(gz + o, dz);
             if (slab) {
                 float4* d = reinterpret_cast<float4*>(slab + (int64_t)j * c);
-                float4 u = *d;
+                float4 u = e == e0 && j < m ? make_float4(0.f, 0.f, 0.f, 0.f) : *d;
                 u.x += dz[0];
                 u.y += dz[1];
                 u.z += dz[2];
@@ -472,7 +507,7 @@ __global__ void __launch_bounds__(256) compress_bwd_any_kernel(CompressBwdArgs<T
         if (a.cb && i == a.n_ent - 1) {
             const float zero[4] = {0.f, 0.f, 0.f, 0.f};
             const int64_t at = (b * a.n_tokens + i * m) * c + ch;
-            for (int j = 0; j < m; ++j) {
+            for (int j = grp; j < m; j += groups) {
                 st4<T>(a.dcb + at + (int64_t)j * c, zero);
                 st4<T>(a.dzb + at + (int64_t)j * c, zero);
             }
@@ -552,7 +587,11 @@ csa2_status cb_launch(const csa2_ctx* ctx, const CompressBwdCall& p, cudaStream_
     a.dprev_zb = reinterpret_cast<T*>(p.dprev_zb);
     a.slab = p.dba || p.dbb ? p.slab : nullptr;
     const int rows = p.cb ? 2 * p.m : p.m;
-    const int64_t ctas = cb_ctas(a.entries, rows == 8 ? CB_CTAS / 4 : (rows == 4 ? CB_CTAS / 2 : CB_CTAS));
+    const bool usual = p.m <= 4 || (p.m == 8 && !p.cb);
+    // groups of the other windows: four rows each, as many as 1,024 threads take
+    const int groups = usual ? 1 : std::max(1, std::min(4096 / p.c, rows / 4));
+    const int64_t ctas = cb_ctas(a.entries, usual ? (rows > 4 ? CB_CTAS / 4 : rows > 2 ? CB_CTAS / 2 : CB_CTAS)
+                                                  : std::max(1, CB_CTAS * 128 / (p.c / 4 * groups)));
     a.run = (a.entries + ctas - 1) / ctas;
     a.stages = 0;
     a.st = ctx->status;
@@ -562,6 +601,8 @@ csa2_status cb_launch(const csa2_ctx* ctx, const CompressBwdCall& p, cudaStream_
         r = usual_window<T, 1, false, 4>(ctx, a, grid, s);
     else if (!p.cb && p.m == 2)
         r = usual_window<T, 2, false, 4>(ctx, a, grid, s);
+    else if (!p.cb && p.m == 3)
+        r = usual_window<T, 3, false, 4>(ctx, a, grid, s);
     else if (!p.cb && p.m == 4)
         r = usual_window<T, 4, false, 4>(ctx, a, grid, s);
     else if (!p.cb && p.m == 8)
@@ -570,10 +611,12 @@ csa2_status cb_launch(const csa2_ctx* ctx, const CompressBwdCall& p, cudaStream_
         r = usual_window<T, 1, true, 4>(ctx, a, grid, s);
     else if (p.cb && p.m == 2)
         r = usual_window<T, 2, true, 4>(ctx, a, grid, s);
+    else if (p.cb && p.m == 3)
+        r = usual_window<T, 3, true, 2>(ctx, a, grid, s);
     else if (p.cb && p.m == 4)
         r = usual_window<T, 4, true, 2>(ctx, a, grid, s);
     else
-        compress_bwd_any_kernel<T><<<grid, c4, 0, s>>>(a);
+        compress_bwd_any_kernel<T><<<grid, dim3(c4, (unsigned)groups), 0, s>>>(a);
     if (r != CSA2_OK) return r;
     if (a.slab) {
         const int64_t split = (int64_t)p.m * p.c, cols = split * (p.cb ? 2 : 1);

@@ -31,7 +31,7 @@ constexpr int EV_CTA = EV_THREADS * EV_KEYS;
 constexpr int EV_CLUSTER = 8;
 constexpr int64_t EV_SHORT = (int64_t)EV_CTA * EV_CLUSTER;   // the longest row of the one-launch path
 constexpr int EL_THREADS = 512;
-constexpr int EL_CHUNK = 8192;          // least entries a block of the long path takes, and their step
+constexpr int EL_CHUNK = 16384;         // least entries a block of the long path takes, and their step
 constexpr unsigned FULL = 0xffffffffu;
 
 // Key of a weight: larger weight, larger key; NaN (of any sign) above +inf.
