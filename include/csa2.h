@@ -81,9 +81,9 @@ csa2_status csa2_ctx_destroy(csa2_ctx* ctx);
 csa2_status csa2_ctx_check(csa2_ctx* ctx, void* stream);
 
 /* Failure-detection test hook.  The next tensor-core launch on this context (an
-   indexer scan, or the attention's or its backward pass's tensor-core kernel) runs with
-   a producer that never signals its consumers (the scan's key copies, the attention's
-   query images), whose bounded waits then expire after `budget_cycles` (0 = the default
+   indexer scan, or the tensor-core kernel of the attention, its backward pass or its
+   weights) runs with a producer that never signals its consumers (the scan's key
+   copies, the attention's query images), whose bounded waits then expire after `budget_cycles` (0 = the default
    of 2^31 cycles) and record CSA2_ERR_TIMEOUT; the kernel waits for the copies it
    did issue, frees its tensor memory and exits, and the context stays usable.  The
    flag clears after that one launch.  The selection kernels have no waits to
