@@ -536,9 +536,26 @@ __global__ void __launch_bounds__(1024) compress_bias_kernel(const float* slab, 
     }
 }
 
-int64_t cb_ctas(int64_t entries, int most = CB_CTAS) {
+// How a call is dealt out.  The launch and the workspace size both go by this: a CTA that sums bias
+// gradients has a slab of its own.
+struct Plan {
+    bool usual;               // the window is compiled for its size
+    int groups;               // groups of threads that share any other window's rows
+    int64_t run, ctas;        // entries of a CTA; CTAs
+};
+
+Plan cb_plan(int64_t entries, int c, int m, bool overlap) {
+    Plan p;
+    const int rows = overlap ? 2 * m : m;
+    p.usual = m <= 4 || (m == 8 && !overlap);
+    // groups of the other windows: four rows each, as many as 1,024 threads take
+    p.groups = p.usual ? 1 : std::max(1, std::min(4096 / c, rows / 4));
+    const int64_t most = p.usual ? (rows > 4 ? CB_CTAS / 4 : rows > 2 ? CB_CTAS / 2 : CB_CTAS)
+                                 : std::max(1, CB_CTAS * 128 / (c / 4 * p.groups));
     const int64_t run = (entries + most - 1) / most;
-    return run > 0 ? (entries + run - 1) / run : 0;
+    p.ctas = run > 0 ? (entries + run - 1) / run : 0;
+    p.run = p.ctas > 0 ? (entries + p.ctas - 1) / p.ctas : 0;
+    return p;
 }
 
 struct CompressBwdCall {
@@ -586,17 +603,12 @@ csa2_status cb_launch(const csa2_ctx* ctx, const CompressBwdCall& p, cudaStream_
     a.dprev_cb = reinterpret_cast<T*>(p.dprev_cb);
     a.dprev_zb = reinterpret_cast<T*>(p.dprev_zb);
     a.slab = p.dba || p.dbb ? p.slab : nullptr;
-    const int rows = p.cb ? 2 * p.m : p.m;
-    const bool usual = p.m <= 4 || (p.m == 8 && !p.cb);
-    // groups of the other windows: four rows each, as many as 1,024 threads take
-    const int groups = usual ? 1 : std::max(1, std::min(4096 / p.c, rows / 4));
-    const int64_t ctas = cb_ctas(a.entries, usual ? (rows > 4 ? CB_CTAS / 4 : rows > 2 ? CB_CTAS / 2 : CB_CTAS)
-                                                  : std::max(1, CB_CTAS * 128 / (p.c / 4 * groups)));
-    a.run = (a.entries + ctas - 1) / ctas;
+    const Plan plan = cb_plan(a.entries, p.c, p.m, p.cb != nullptr);
+    a.run = plan.run;
     a.stages = 0;
     a.st = ctx->status;
     csa2_status r = CSA2_OK;
-    const unsigned grid = (unsigned)ctas, c4 = (unsigned)(p.c / 4);
+    const unsigned grid = (unsigned)plan.ctas, c4 = (unsigned)(p.c / 4);
     if (!p.cb && p.m == 1)
         r = usual_window<T, 1, false, 4>(ctx, a, grid, s);
     else if (!p.cb && p.m == 2)
@@ -616,11 +628,11 @@ csa2_status cb_launch(const csa2_ctx* ctx, const CompressBwdCall& p, cudaStream_
     else if (p.cb && p.m == 4)
         r = usual_window<T, 4, true, 2>(ctx, a, grid, s);
     else
-        compress_bwd_any_kernel<T><<<grid, dim3(c4, (unsigned)groups), 0, s>>>(a);
+        compress_bwd_any_kernel<T><<<grid, dim3(c4, (unsigned)plan.groups), 0, s>>>(a);
     if (r != CSA2_OK) return r;
     if (a.slab) {
         const int64_t split = (int64_t)p.m * p.c, cols = split * (p.cb ? 2 : 1);
-        compress_bias_kernel<<<(unsigned)(cols / 32), 1024, 0, s>>>(a.slab, (int)ctas, cols, split, p.dba, p.dbb);
+        compress_bias_kernel<<<(unsigned)(cols / 32), 1024, 0, s>>>(a.slab, (int)plan.ctas, cols, split, p.dba, p.dbb);
     }
     return csa2_launch_status();
 }
@@ -628,8 +640,8 @@ csa2_status cb_launch(const csa2_ctx* ctx, const CompressBwdCall& p, cudaStream_
 }  // namespace
 
 extern "C" size_t csa2_compress_bwd_workspace_bytes(int B, int64_t n_tokens, int c, int m, int overlap) {
-    if (B <= 0 || n_tokens <= 0 || c <= 0 || m < 1) return 0;
-    return (size_t)cb_ctas(n_tokens / m * B) * (overlap ? 2 : 1) * m * c * sizeof(float);
+    if (B <= 0 || n_tokens <= 0 || c <= 0 || c % 128 || c > 1024 || m < 1) return 0;
+    return (size_t)cb_plan(n_tokens / m * B, c, m, overlap != 0).ctas * (overlap ? 2 : 1) * m * c * sizeof(float);
 }
 
 extern "C" csa2_status csa2_compress_bwd(csa2_ctx* ctx, const void* ca, const void* za, const void* cb, const void* zb,

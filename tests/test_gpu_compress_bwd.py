@@ -70,6 +70,38 @@ def test_compress_bwd(dtype, B, n, c, m, overlap, prev, bias, flags):
         assert (x is None) == (y is None) and (x is None or torch.equal(x, y))
 
 
+@pytest.mark.parametrize("c,m,overlap,entries", [
+    (128, 5, False, 1217), (128, 5, True, 1300), (128, 12, False, 2500), (256, 6, False, 1500), (256, 7, True, 1217),
+    (384, 7, False, 1700), (128, 12, True, 1217), (512, 5, False, 1300)])
+def test_other_windows_with_more_entries_than_ctas(c, m, overlap, entries, _guarded_buffers):
+    """Windows that are not compiled for their size, narrow rows, biases, and more entries than 1,216
+    CTAs: every CTA's slab lies inside the workspace (guard bytes around it), and every gradient and
+    bias sum is the oracle's.  A bias sum adds a run's terms, then at most 2,500 / 32 = 79 slabs, then
+    32 sums: about 115 additions one behind the other of partial sums of at most 4 rms of the
+    result, each off by 2^-24 of it, so sqrt(115) * 4 * 2^-24 = 2.6e-6 rms beside the terms' own
+    errors (independent, so they add up as the terms do); TOL holds for both."""
+    def t(i, *shape, dt=torch.float32):
+        return W.normal_tensor(shape, 64, i, dt, DEV)
+
+    n = entries * m
+    ca, za, dout = t(1, n, c), t(2, n, c), t(3, entries, c)
+    cb, zb = (t(4, n, c), t(5, n, c)) if overlap else (None, None)
+    ba, bb = t(6, m, c), t(7, m, c) if overlap else None
+    g = C.csa2_compress_bwd(ca, za, m, dout, cb=cb, zb=zb, ba=ba, bb=bb, flags=C.W_NORM | C.W_ROPE)
+    C.csa2_ctx_check()
+    assert _guarded_buffers.checked > 0
+    opt = dict(Ba=to_np(ba))
+    if overlap:
+        opt.update(Cb=to_np(cb), Zb=to_np(zb), Bb=to_np(bb))
+    w = G.compress_bwd(to_np(ca), to_np(za), m, to_np(dout), flags=C.W_NORM | C.W_ROPE, **opt)
+    for name, got in (("Ca", g.dca), ("Za", g.dza), ("Cb", g.dcb), ("Zb", g.dzb)):
+        if got is not None:
+            assert_close(to_np(got), w[name], TOL, name)
+    for name, got in (("Ba", g.dba), ("Bb", g.dbb)):
+        if got is not None:
+            assert_close(to_np(got), w[name], TOL, name)
+
+
 def test_unbatched_and_empty():
     ca, za = (W.normal_tensor((8, 512), 62, i, torch.float32, DEV) for i in (1, 2))
     dout = W.normal_tensor((4, 512), 62, 3, torch.float32, DEV)

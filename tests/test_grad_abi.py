@@ -117,6 +117,20 @@ def test_workspace_sizes(lib, ctx):
     assert lib.csa2_compress_bwd_workspace_bytes(0, 8192, 512, 4, 1) == 0
 
 
+@pytest.mark.parametrize("c,m,overlap,entries,slabs", [
+    # the launch takes one CTA, and one slab, an entry up to the count that follows from the threads
+    (128, 5, 0, 4000, 4000), (128, 5, 1, 4000, 2000), (128, 12, 0, 1217, 1217), (128, 16, 0, 1217, 609),
+    (256, 7, 0, 2000, 2000), (256, 8, 1, 1217, 406), (384, 5, 0, 1600, 1600), (512, 5, 0, 1217, 609),
+    (1024, 7, 0, 608, 608), (512, 128, 0, 152, 152), (512, 128, 0, 153, 77), (128, 4, 0, 1217, 406), (128, 2, 0, 1217, 609),
+])
+def test_bias_slabs_match_the_launch(lib, c, m, overlap, entries, slabs):
+    """csa2_compress_bwd's workspace has a slab of bias sums for every CTA of the launch: windows that
+    are not compiled for their size run 1,216 CTAs of 128 threads, or as many more or fewer as
+    their CTAs are smaller or larger."""
+    table = (2 if overlap else 1) * m * c * 4
+    assert lib.csa2_compress_bwd_workspace_bytes(1, entries * m, c, m, overlap) == slabs * table
+
+
 def test_binding_checks_shapes_before_the_library():
     t = torch.zeros(2, 5)
     with pytest.raises(ValueError):
