@@ -670,6 +670,10 @@ BwdLayout bwd_layout(const BwdSizes& z, int64_t nb) {
 
 constexpr size_t WS_TARGET = (size_t)16 << 30;   // the recommended workspace stays below this
 
+// The buffers begin at a 256-byte boundary (the list of contributions is stored 32 bytes at a time);
+// a workspace may begin at any 16-byte one, so the size asked for has room for the way to it.
+constexpr size_t WS_ALIGN = 256, WS_SLACK = WS_ALIGN - 16;
+
 // The most queries a chunk can have in `bytes` of workspace (0: not one fits).
 int64_t chunk_for(const BwdSizes& z, size_t bytes) {
     // fewer queries may split their keys further, so sizes are not monotonic where splits set
@@ -727,10 +731,12 @@ csa2_status bwd_run(csa2_ctx* ctx, const BwdCall& a, void* ws, size_t ws_bytes, 
     const int64_t rows = n_kv + n_sw;
     const BwdSizes z = {n_bq, a.H, n_slots, rows,
                         bwd_tc_applies(a.q_dt, a.kv_dt, a.k, a.swa_dt, a.window, a.out_dt, a.flags), ctx->num_sms};
-    const int64_t nb_max = chunk_for(z, ws_bytes);
+    const size_t skip = align_up(reinterpret_cast<uintptr_t>(ws), WS_ALIGN) - reinterpret_cast<uintptr_t>(ws);
+    // (the chunks go by the size alone, so the results do not depend on where the workspace begins)
+    const int64_t nb_max = ws_bytes > WS_SLACK ? chunk_for(z, ws_bytes - WS_SLACK) : 0;
     if (nb_max < 1) return CSA2_ERR_INVALID_ARG;
     const BwdLayout L = bwd_layout(z, nb_max);
-    uint8_t* base = reinterpret_cast<uint8_t*>(ws);
+    uint8_t* base = reinterpret_cast<uint8_t*>(ws) + skip;
     float* D = reinterpret_cast<float*>(base + L.D);
     float* rinv = reinterpret_cast<float*>(base + L.rinv);
     if (rows > 0)
@@ -872,7 +878,7 @@ extern "C" size_t csa2_attn_bwd_workspace_bytes(csa2_ctx* ctx, csa2_dtype q_dt, 
     const int64_t rows = (k > 0 ? (int64_t)B * N : 0) + (window > 0 ? (int64_t)B * swa_cap : 0);
     const BwdSizes z = {(int64_t)B * Q, H, k + window, rows,
                         bwd_tc_applies(q_dt, kv_dt, k, swa_dt, window, out_dt, flags), ctx->num_sms};
-    return bwd_layout(z, std::max<int64_t>(1, chunk_for(z, WS_TARGET))).total;
+    return bwd_layout(z, std::max<int64_t>(1, chunk_for(z, WS_TARGET - WS_SLACK))).total + WS_SLACK;
 }
 
 extern "C" csa2_status csa2_sparse_attn_bwd(csa2_ctx* ctx, const void* q, csa2_dtype q_dt, const void* kv,

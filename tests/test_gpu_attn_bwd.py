@@ -233,6 +233,33 @@ def test_chunked_workspace_and_same_bits(dtype, tol):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_workspace_at_any_16_bytes(dtype):
+    """A workspace of the size asked for, 16 bytes and more behind a 256-byte boundary: the same bits,
+    and nothing around it is written; one 16-byte step smaller still runs (in chunks)."""
+    s = _forward(_case(24, 1, 9, 64, 200, 90, 20, 32, [[40 + i for i in range(9)]], dtype, 8))
+    ref = _backward(s)
+    dt = {torch.float32: C.F32, torch.bfloat16: C.BF16}[dtype]
+    need = C._lib().csa2_attn_bwd_workspace_bytes(C.ctx(0), dt, dt, dt, dt, 1, 9, 64, 90, 20, 200, 32, 7)
+    raw = torch.full((need + 1024,), 0xA5, dtype=torch.uint8, device=DEV)
+    assert raw.data_ptr() % 256 == 0
+    for off in (0, 16, 48, 128, 240):
+        raw.fill_(0xA5)
+        for a, b in zip(_backward(s, ws=raw[off:off + need]), ref):
+            assert torch.equal(a, b)
+        C.csa2_ctx_check()
+        assert bool((raw[:off] == 0xA5).all()) and bool((raw[off + need:] == 0xA5).all()), off
+    raw.fill_(0xA5)
+    first = _backward(s, ws=raw[16:need])                    # (the same chunks wherever it begins)
+    C.csa2_ctx_check()
+    assert bool((raw[:16] == 0xA5).all()) and bool((raw[need:] == 0xA5).all())
+    for a, b in zip(_backward(s, ws=raw[256:240 + need]), first):
+        assert torch.equal(a, b)
+    with pytest.raises(C.Csa2Error) as e:
+        _backward(s, ws=raw[8:8 + need])
+    assert e.value.status == C.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_out_of_range_index_is_flagged(dtype):
     s = _forward(_case(19, 1, 2, 64, 50, 6, 4, 8, [[9, 10]], dtype))
     clean_idx = s["idx"].clone()

@@ -117,6 +117,14 @@ def test_workspace_sizes(lib, ctx):
     assert lib.csa2_compress_bwd_workspace_bytes(0, 8192, 512, 4, 1) == 0
 
 
+@pytest.mark.parametrize("dt", [C.F32, C.BF16])
+@pytest.mark.parametrize("B,Q,H,k,window", [(1, 4, 64, 512, 128), (2, 96, 40, 301, 100), (1, 8192, 128, 512, 128)])
+def test_attention_backward_workspace_may_begin_at_any_16_bytes(lib, ctx, dt, B, Q, H, k, window):
+    """The kernels store up to 32 bytes at once, so the buffers (whole 256-byte pieces) begin at a
+    256-byte boundary; a base 16 bytes behind one is 240 away from the next."""
+    assert lib.csa2_attn_bwd_workspace_bytes(ctx, dt, dt, dt, dt, B, Q, H, k, window, 2048, 128, 7) % 256 == 240
+
+
 @pytest.mark.parametrize("c,m,overlap,entries,slabs", [
     # the launch takes one CTA, and one slab, an entry up to the count that follows from the threads
     (128, 5, 0, 4000, 4000), (128, 5, 1, 4000, 2000), (128, 12, 0, 1217, 1217), (128, 16, 0, 1217, 609),
