@@ -569,7 +569,11 @@ __global__ void __launch_bounds__(128) bwd_rowsum_kernel(RowSumArgs a) {
     }
     const int64_t off = (row < a.n_kv ? row : row - a.n_kv) * AG_C + ch;
     const int dt = row < a.n_kv ? a.kv_dt : a.swa_dt;
-    if ((a.flags & CSA2_KVNORM) && (n > 0 || a.acc)) {
+    // A row without contributions has no gradient, whatever its values (one that no slot points to may
+    // hold anything).  Of the chunks before, only the sum is known: 0 if there was none, and where the
+    // contributions cancel to 0 the norm makes 0 of it as well.
+    const bool any = n > 0 || (a.acc && __syncthreads_or(g.x != 0.0f || g.y != 0.0f || g.z != 0.0f || g.w != 0.0f));
+    if ((a.flags & CSA2_KVNORM) && any) {
         const float f = a.rinv[row];
         const float4 x = load4_any(row < a.n_kv ? a.kv : a.swa, dt, off);
         const float4 k = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);

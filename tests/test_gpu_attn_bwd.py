@@ -211,6 +211,31 @@ def test_rows_behind_empty_slots_are_not_read(dtype):
     assert torch.equal(got[2][0, :31], clean[2][0, :31])
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("chunk", [23, 8, 1])
+def test_rows_that_no_query_attends_to_have_no_gradient(dtype, chunk):
+    """Their gradient is 0 in one chunk and in several, where they hold NaN and infinity too."""
+    Q = 23
+    s = _forward(_case(25, 1, Q, 24, 300, 6, 5, 64, [[i for i in range(Q)]], dtype, 2))
+    used = sorted(set(s["idx"].flatten().tolist()) - {-1})
+    free = [i for i in range(300) if i not in set(used)]
+    s["kv"][0, free[::2]] = float("nan")
+    s["kv"][0, free[1::2]] = float("inf")
+    s["swa"][0, Q:] = float("nan")
+    dt = {torch.float32: C.F32, torch.bfloat16: C.BF16}[dtype]
+
+    def size(q):
+        return C._lib().csa2_attn_bwd_workspace_bytes(C.ctx(0), dt, dt, dt, dt, 1, q, 24, 6, 5, 300, 64, 7)
+
+    # (in chunks of fewer queries the rows' sums are carried in 745 KB more)
+    ws = torch.empty(size(chunk) + (4 * 512 * 364 + (1 << 16) if chunk < Q else 0), dtype=torch.uint8, device=DEV)
+    got = _backward(s, ws=ws)
+    C.csa2_ctx_check()
+    assert not got[1][0, free].any() and not got[2][0, Q:].any()
+    assert all(bool(torch.isfinite(x.float()).all()) for x in got)
+    assert bool(got[1][0, used].float().abs().sum(-1).gt(0).all())
+
+
 @pytest.mark.parametrize("dtype,tol", [(torch.float32, F32_TOL), (torch.bfloat16, TC_TOL)])
 def test_chunked_workspace_and_same_bits(dtype, tol):
     """A workspace for a few queries at a time gives the gradients too (rows' sums carried in
