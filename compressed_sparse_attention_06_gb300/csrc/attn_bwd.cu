@@ -847,7 +847,7 @@ csa2_status bwd_impl(csa2_ctx* ctx, const BwdCall& a, int c, void* ws, size_t ws
         if (d != CSA2_F32 && d != CSA2_BF16) return CSA2_ERR_UNSUPPORTED;
     const int64_t n_bq = (int64_t)a.B * a.Q;
     if (n_bq > 65535) return CSA2_ERR_UNSUPPORTED;
-    if (a.window > 0 && (!a.swa || a.swa_cap < a.window)) return CSA2_ERR_INVALID_ARG;
+    if (a.window > 0 && ((!a.swa && n_bq > 0) || a.swa_cap < a.window)) return CSA2_ERR_INVALID_ARG;
     if (a.swa_cap < 0) return CSA2_ERR_INVALID_ARG;
     const int64_t rows = (int64_t)a.B * (a.N + a.swa_cap);
     if (rows > 0x7FFFFFFF) return CSA2_ERR_UNSUPPORTED;
@@ -855,19 +855,18 @@ csa2_status bwd_impl(csa2_ctx* ctx, const BwdCall& a, int c, void* ws, size_t ws
         !aligned(a.dq, 16) || !aligned(a.dkv, 16) || !aligned(a.dswa, 16) || !aligned(ws, 16) || !aligned(a.lse, 4) ||
         !aligned(a.dsink, 4) || !aligned(a.q_pos, 8))
         return CSA2_ERR_INVALID_ARG;
-    if (a.B == 0) return CSA2_OK;
-    if (a.Q > 0 && (!a.q || !a.q_pos || !a.out || !a.dout || !a.lse || !a.dq || !ws)) return CSA2_ERR_INVALID_ARG;
-    if (a.Q > 0 && a.k > 0 && ((!a.idx && !a.nv) || !a.kv)) return CSA2_ERR_INVALID_ARG;
+    if (n_bq > 0 && (!a.q || !a.q_pos || !a.out || !a.dout || !a.lse || !a.dq || !ws)) return CSA2_ERR_INVALID_ARG;
+    if (n_bq > 0 && a.k > 0 && ((!a.idx && !a.nv) || !a.kv)) return CSA2_ERR_INVALID_ARG;
     DeviceGuard dev(ctx);
     if (!dev.ok) return CSA2_ERR_CUDA;
     cudaStream_t s = as_stream(stream);
     // rows that no call below visits have no gradient
     csa2_status r = CSA2_OK;
-    if (a.k == 0 || a.Q == 0) r = zero_bytes(a.dkv, (size_t)a.B * a.N * AG_C * dt_bytes(a.kv_dt), s);
-    if (r == CSA2_OK && (a.window == 0 || a.Q == 0))
+    if (a.k == 0 || n_bq == 0) r = zero_bytes(a.dkv, (size_t)a.B * a.N * AG_C * dt_bytes(a.kv_dt), s);
+    if (r == CSA2_OK && (a.window == 0 || n_bq == 0))
         r = zero_bytes(a.dswa, (size_t)a.B * a.swa_cap * AG_C * dt_bytes(a.swa_dt), s);
-    if (r == CSA2_OK && a.Q == 0) r = zero_bytes(a.dsink, (size_t)a.H * 4, s);
-    if (r != CSA2_OK || a.Q == 0) return r;
+    if (r == CSA2_OK && n_bq == 0) r = zero_bytes(a.dsink, (size_t)a.H * 4, s);
+    if (r != CSA2_OK || n_bq == 0) return r;
     return bwd_run(ctx, a, ws, ws_bytes, s);
 }
 
@@ -905,7 +904,7 @@ extern "C" csa2_status csa2_dense_attn_bwd(csa2_ctx* ctx, const void* q, csa2_dt
                                            const void* dout, csa2_dtype out_dt, const float* lse, int B, int Q, int H,
                                            int c, float rope_base, unsigned flags, void* dq, void* dkv, void* dswa,
                                            float* dsink, void* ws, size_t ws_bytes, void* stream) {
-    if (k_max < 0 || k_max > (1 << 22) || (k_max > 0 && !n_visible)) return CSA2_ERR_INVALID_ARG;
+    if (k_max < 0 || k_max > (1 << 22)) return CSA2_ERR_INVALID_ARG;
     const BwdCall a = {q, kv, swa, out, dout, q_dt, kv_dt, swa_dt, out_dt, N, swa_cap, swa_pos0, nullptr, n_visible,
                        q_pos, k_max, window, B, Q, H, sink, lse, rope_base, flags, dq, dkv, dswa, dsink};
     return bwd_impl(ctx, a, c, ws, ws_bytes, stream);

@@ -312,6 +312,20 @@ def test_unwanted_gradients_and_no_queries():
     assert dq.numel() == 0 and not dkv.any() and not dswa.any() and not dsink.any()
 
 
+@pytest.mark.parametrize("dense", [False, True])
+@pytest.mark.parametrize("window", [0, 4])
+def test_no_sequences(dense, window):
+    """B = 0: the sink's gradient, which has no batch axis, is 0 (the buffer held NaN)."""
+    s = _case(26, 1, 2, 8, 30, 5, window, 8, [[9, 10]], torch.bfloat16, dense=dense)
+    for n in ("q", "kv", "swa", "q_pos", "dout", "nv" if dense else "idx"):
+        s[n] = s[n][:0].contiguous()
+    s["out"], s["lse"] = torch.empty_like(s["q"]), torch.empty((0, 2, 8), device=DEV)
+    dsink = torch.full((8,), float("nan"), device=DEV)
+    got = _backward(s, dsink=dsink)
+    C.csa2_ctx_check()
+    assert [x.numel() for x in got[:3]] == [0, 0, 0] and got[3] is dsink and not dsink.any()
+
+
 def test_captured_and_on_another_stream():
     """A captured call, replayed after its inputs changed in place, equals an eager call."""
     s = _forward(_case(21, 1, 5, 64, 200, 90, 20, 32, [[40, 41, 42, 43, 44]], torch.bfloat16, 8))
