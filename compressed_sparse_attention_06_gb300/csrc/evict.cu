@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(GA_THREADS) cache_gather_kernel(const V* src, 
     for (uint32_t r = threadIdx.x; r < nr; r += GA_THREADS) {
         const int64_t row = r0 + r;
         const int32_t id = idx[row];
-        if (id >= N) csa2_flag(st, CSA2_DEVBIT_RANGE);
+        if (id < -1 || id >= N) csa2_flag(st, CSA2_DEVBIT_RANGE);
         from[r] = id >= 0 && id < N ? ((row / keep) * N + id) * (int64_t)pieces : -1;
     }
     __syncthreads();

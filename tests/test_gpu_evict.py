@@ -206,6 +206,26 @@ def test_gather(shape, dtype):
     assert e.value.status == C.ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("shape,dtype", [((512,), torch.bfloat16), ((), torch.float32)])
+@pytest.mark.parametrize("bad", [-2, -7, -2 ** 31, 50, 2 ** 31 - 1])
+def test_gather_flags_every_id_outside_the_cache(shape, dtype, bad):
+    """-1 alone leaves a row without a word; any other id outside [0, N) leaves it and is flagged."""
+    src = W.normal_tensor((2, 50, *shape), 44, 1, dtype, DEV)
+    idx = torch.tensor([[3, bad, -1], [-1, 49, 0]], dtype=torch.int32, device=DEV)
+    out = torch.full((2, 3, *shape), 7.0, dtype=dtype, device=DEV)
+    C.csa2_cache_gather(src, idx, out=out)
+    with pytest.raises(C.Csa2Error) as e:
+        C.csa2_ctx_check()
+    assert e.value.status == C.ERR_DEVICE
+    for b, i, row in ((0, 0, 3), (1, 1, 49), (1, 2, 0)):
+        assert torch.equal(out[b, i], src[b, row])
+    for b, i in ((0, 1), (0, 2), (1, 0)):
+        assert bool((out[b, i] == 7.0).all())
+    idx[0, 1] = -1
+    C.csa2_cache_gather(src, idx, out=out)
+    C.csa2_ctx_check()
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp4"])
 def test_decode_goes_on_over_the_cut_cache(kind):
     """Decode steps account their weights, the cache is cut, and attention over the kept entries of a
