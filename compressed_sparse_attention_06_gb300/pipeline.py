@@ -255,4 +255,4 @@ def evict_caches(acc, n_entries, caches: Dict[str, torch.Tensor], keep: int, rec
     def cut(t):
         return C.csa2_cache_gather(t, idx, out=C.alloc((B, keep, *t.shape[2:]), dtype=t.dtype, device=t.device).zero_())
 
-    return CutCaches(idx, n_entries.clamp(min=0, max=keep), cut(acc), {name: cut(t) for name, t in caches.items()})
+    return CutCaches(idx, n_entries.clamp(min=0, max=min(keep, acc.shape[1])), cut(acc), {name: cut(t) for name, t in caches.items()})

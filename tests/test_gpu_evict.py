@@ -226,6 +226,21 @@ def test_gather_flags_every_id_outside_the_cache(shape, dtype, bad):
     C.csa2_ctx_check()
 
 
+@pytest.mark.parametrize("N,keep", [(10, 20), (10, 10), (10, 6)])
+def test_cut_caches_count_the_entries_they_hold(N, keep):
+    """A length above the cache's is taken as the cache's (and flagged), one below 0 as 0: the count that
+    goes on with the cut cache is the number of its ids, so nothing behind them becomes visible."""
+    acc = torch.rand(4, N, generator=torch.Generator(DEV).manual_seed(3), device=DEV)
+    kv = W.normal_tensor((4, N, 512), 45, 1, torch.bfloat16, DEV)
+    n = torch.tensor([N + 5, N, 3, -2], dtype=torch.int64, device=DEV)
+    cut = P.evict_caches(acc, n, {"kv": kv}, keep, recent=2)
+    with pytest.raises(C.Csa2Error) as e:
+        C.csa2_ctx_check()
+    assert e.value.status == C.ERR_DEVICE
+    assert torch.equal(cut.n_entries, (cut.idx >= 0).sum(1))
+    assert cut.n_entries.tolist() == [min(N, keep), min(N, keep), 3, 0]
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp4"])
 def test_decode_goes_on_over_the_cut_cache(kind):
     """Decode steps account their weights, the cache is cut, and attention over the kept entries of a
