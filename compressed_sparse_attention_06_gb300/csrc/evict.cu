@@ -480,7 +480,7 @@ extern "C" csa2_status csa2_cache_gather(csa2_ctx* ctx, const void* src, int64_t
     if (row_bytes % 4) return CSA2_ERR_UNSUPPORTED;
     if (B > 65535) return CSA2_ERR_UNSUPPORTED;
     if (B == 0 || keep == 0) return CSA2_OK;
-    if (!src || !idx || !dst || !aligned(src, 4) || !aligned(dst, 4) || !aligned(idx, 4)) return CSA2_ERR_INVALID_ARG;
+    if ((N > 0 && !src) || !idx || !dst || !aligned(src, 4) || !aligned(dst, 4) || !aligned(idx, 4)) return CSA2_ERR_INVALID_ARG;
     // moving rows within one buffer would overwrite rows before they are read
     const uintptr_t s0 = reinterpret_cast<uintptr_t>(src), d0 = reinterpret_cast<uintptr_t>(dst);
     const uintptr_t s1 = s0 + (size_t)B * N * row_bytes, d1 = d0 + (size_t)B * keep * row_bytes;

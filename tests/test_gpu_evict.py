@@ -241,6 +241,16 @@ def test_cut_caches_count_the_entries_they_hold(N, keep):
     assert cut.n_entries.tolist() == [min(N, keep), min(N, keep), 3, 0]
 
 
+@pytest.mark.parametrize("B", [0, 3])
+def test_an_empty_cache_is_cut_to_nothing(B):
+    """No entry (or no sequence) yet: no id, no count, rows of 0."""
+    kv = torch.empty((B, 0, 512), dtype=torch.bfloat16, device=DEV)
+    cut = P.evict_caches(torch.empty((B, 0), device=DEV), torch.zeros(B, dtype=torch.int64, device=DEV), {"kv": kv}, 5, recent=1)
+    C.csa2_ctx_check()
+    assert bool((cut.idx == -1).all()) and cut.idx.shape == (B, 5) and not cut.n_entries.any()
+    assert cut.caches["kv"].shape == (B, 5, 512) and not cut.caches["kv"].any() and not cut.acc.any()
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp4"])
 def test_decode_goes_on_over_the_cut_cache(kind):
     """Decode steps account their weights, the cache is cut, and attention over the kept entries of a
