@@ -240,8 +240,8 @@ extern "C" csa2_status csa2_attn_mass(csa2_ctx* ctx, const void* q, csa2_dtype q
     }
     const csa2_status r = kv_dt == CSA2_F32 ? simt_run(ctx, a, s) : mass_tc_run(ctx, a, s);
     if (r != CSA2_OK) return r;
-    if (a.fix) {
-        const int64_t n = (int64_t)B * N;
+    const int64_t n = (int64_t)B * N;
+    if (a.fix && n > 0) {
         mass_finish_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a.fix, acc, n);
     }
     return csa2_launch_status();

@@ -130,6 +130,35 @@ def test_mass_shows_a_query_of_nan_and_skips_an_empty_one(Q):
     assert not w.any() and bool((acc == 1).all())
 
 
+@pytest.mark.parametrize("kv_dt", [C.F32, C.BF16, C.FP4_E4M3x16])
+@pytest.mark.parametrize("Q", [1, 3])
+def test_mass_of_a_cache_without_entries(kv_dt, Q):
+    """N = 0 through the C entry (the cache has an address, but no entry yet): weights of 0, an index
+    is flagged, and the call succeeds."""
+    q = W.normal_tensor((1, Q, 64, 512), 46, 1, torch.bfloat16, DEV)
+    buf = torch.zeros(1 << 20, dtype=torch.uint8, device=DEV)
+    idx = torch.full((1, Q, 4), -1, dtype=torch.int32, device=DEV)
+    pos, lse = torch.zeros(1, Q, dtype=torch.int64, device=DEV), torch.zeros(1, Q, 64, device=DEV)
+    weights = torch.full((1, Q, 4), float("nan"), device=DEV)
+    a = [t.data_ptr() for t in (q, buf, idx, pos, lse, weights)]
+    assert C._lib().csa2_attn_mass_workspace_bytes(C.ctx(0), kv_dt, 1, Q, 64, 4, 0, 1) <= 1 << 19
+
+    def call():
+        return C._lib().csa2_attn_mass(C.ctx(0), a[0], C.BF16, a[1], kv_dt, 0, a[2], None, 4, a[3], a[4], 1, Q, 64, 512,
+                                       10000.0, 7, a[5], a[1], a[1] + (1 << 19), 1 << 19, None)
+
+    torch.cuda.synchronize()
+    assert call() == C.OK
+    C.csa2_ctx_check()
+    assert not weights.any() and not buf[:1 << 19].any()
+    idx[0, 0, 1] = 0
+    torch.cuda.synchronize()
+    assert call() == C.OK
+    with pytest.raises(C.Csa2Error) as e:
+        C.csa2_ctx_check()
+    assert e.value.status == C.ERR_DEVICE
+
+
 def test_mass_flags_an_out_of_range_index():
     kv, _ = _cache(34, 1, 20, "bf16")
     q = W.normal_tensor((1, 1, 64, 512), 34, 1, torch.bfloat16, DEV)
