@@ -777,10 +777,13 @@ csa2_status bwd_run(csa2_ctx* ctx, const BwdCall& a, void* ws, size_t ws_bytes, 
     for (int64_t bq0 = 0; bq0 < n_bq; bq0 += nb_max) {
         c.bq0 = bq0;
         c.nb = (int)std::min<int64_t>(nb_max, n_bq - bq0);
-        if (rows > 0) {
+        // (without rows too: an index into a cache of none is flagged here)
+        if (n_slots > 0) {
             const csa2_status zr = zero_bytes(cnt, (size_t)L.groups * rows * 4, s);
             if (zr != CSA2_OK) return zr;
             bwd_rank_kernel<<<(unsigned)L.groups, 1024, 0, s>>>(c.slots, bq0, c.nb, L.group_q, n_slots, rows, cnt, rank);
+        }
+        if (rows > 0) {
             bwd_place_kernel<<<(unsigned)n_blk, BWD_SCAN_ROWS, 0, s>>>(cnt, L.groups, rows, loc, tot, blk);
             bwd_scan(blk, n_blk, s);
         }

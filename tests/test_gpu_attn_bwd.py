@@ -326,6 +326,40 @@ def test_no_sequences(dense, window):
     assert [x.numel() for x in got[:3]] == [0, 0, 0] and got[3] is dsink and not dsink.any()
 
 
+@pytest.mark.parametrize("dt,dtype", [(C.F32, torch.float32), (C.BF16, torch.bfloat16)])
+@pytest.mark.parametrize("dense", [False, True])
+def test_cache_without_entries(dt, dtype, dense):
+    """N = 0 and no window through the C entry (the cache has an address, but no entry yet): gradients
+    of 0 beside the sink's, and an index into the cache is flagged, as in the forward pass."""
+    Q, H, k = 3, 8, 5
+    q, dout = (W.normal_tensor((1, Q, H, 512), 27, i, dtype, DEV) for i in (1, 2))
+    out, sink = torch.zeros_like(q), W.normal_tensor((H,), 27, 3, torch.float32, DEV)
+    lse = sink.expand(1, Q, H).contiguous()
+    pos = torch.zeros(1, Q, dtype=torch.int64, device=DEV)
+    sel = torch.zeros(1, Q, dtype=torch.int64, device=DEV) if dense else torch.full((1, Q, k), -1, dtype=torch.int32, device=DEV)
+    kv = torch.zeros(512, device=DEV)
+    dq, dsink = torch.full_like(q, float("nan")), torch.full((H,), float("nan"), device=DEV)
+    ws = torch.empty(C._lib().csa2_attn_bwd_workspace_bytes(C.ctx(0), dt, dt, dt, dt, 1, Q, H, k, 0, 0, 0, 7),
+                     dtype=torch.uint8, device=DEV)
+    p = [t.data_ptr() for t in (q, kv, sel, pos, sink, out, dout, lse, dq, dsink, ws)]
+
+    def call():
+        torch.cuda.synchronize()
+        fn = C._lib().csa2_dense_attn_bwd if dense else C._lib().csa2_sparse_attn_bwd
+        return fn(C.ctx(0), p[0], dt, p[1], dt, 0, p[2], k, None, dt, 0, 0, 0, p[3], p[4], p[5], p[6], dt, p[7], 1, Q, H, 512,
+                  10000.0, 7, p[8], None, None, p[9], p[10], ws.numel(), None)
+
+    assert call() == C.OK
+    C.csa2_ctx_check()
+    assert not dq.any() and not dsink.any()
+    sel.view(-1)[1] = 1
+    assert call() == C.OK
+    with pytest.raises(C.Csa2Error) as e:
+        C.csa2_ctx_check()
+    assert e.value.status == C.ERR_DEVICE
+    assert not dq.any()
+
+
 def test_captured_and_on_another_stream():
     """A captured call, replayed after its inputs changed in place, equals an eager call."""
     s = _forward(_case(21, 1, 5, 64, 200, 90, 20, 32, [[40, 41, 42, 43, 44]], torch.bfloat16, 8))
