@@ -155,3 +155,38 @@ def test_layer_backward_matches_differences():
             h = 1e-4
             want = (loss({**f, k: f[k] + h * d}) - loss({**f, k: f[k] - h * d})) / (2 * h)
             assert abs(float((grad * d).sum()) - want) <= 1e-3 * np.linalg.norm(grad) + 1e-6, k
+
+
+@pytest.mark.parametrize("m", [2, 5])
+def test_compress_bwd_captured_and_on_another_stream(m):
+    """A graph of the call, replayed after its inputs changed in place, and a call on a side stream give
+    an eager call's bits; compiled and general window."""
+    n, c = 40 * m, 256
+    ca, za, dout = (W.normal_tensor((n if i < 3 else 40, c), 65, i, torch.bfloat16, DEV) for i in (1, 2, 3))
+    ba = W.normal_tensor((m, c), 65, 4, torch.float32, DEV)
+    ws = torch.empty(C._lib().csa2_compress_bwd_workspace_bytes(1, n, c, m, 0), dtype=torch.uint8, device=DEV)
+
+    def call():
+        return C.csa2_compress_bwd(ca, za, m, dout, ba=ba, flags=C.W_NORM | C.W_ROPE, ws=ws)
+
+    graph = torch.cuda.CUDAGraph()
+    check, C._check = C._check, lambda fn, st: None if st == C.OK else (_ for _ in ()).throw(C.Csa2Error(fn, st))
+    try:
+        with torch.cuda.graph(graph):
+            held = call()
+    finally:
+        C._check = check
+    dout.mul_(-3.0)
+    za.add_(1.0 / 3.0)
+    ba.neg_()
+    graph.replay()
+    torch.cuda.synchronize()
+    eager = call()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        aside = call()
+    torch.cuda.synchronize()
+    C.csa2_ctx_check()
+    for a, b, d in zip(held, eager, aside):
+        assert (a is None and b is None and d is None) or (torch.equal(a, b) and torch.equal(b, d))

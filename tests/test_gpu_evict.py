@@ -360,3 +360,119 @@ def test_mass_expired_wait_is_reported_and_the_context_stays_usable():
     w, _ = C.csa2_attn_mass(q, kv, q_pos, lse, idx=idx, want_weights=True)
     C.csa2_ctx_check()
     assert torch.equal(w, ref)
+
+
+@pytest.mark.parametrize("H", [24, 100])
+def test_mass_dense_fp4(H):
+    """The dense form over FP4 rows, one head pass and two, and a query of one entry and of none."""
+    B, Q, N = 2, 4, 300
+    kv, kv_np = _cache(47, B, N, "fp4")
+    q = W.normal_tensor((B, Q, H, 512), 47, 1, torch.bfloat16, DEV)
+    nv = torch.tensor([[0, 1, 129, 300], [256, 128, 7, 299]], dtype=torch.int64, device=DEV)
+    q_pos = nv * 128 + 5
+    _, lse = C.csa2_dense_attn(q, kv, nv, N, None, q_pos, None, window=0, want_lse=True)
+    acc = torch.zeros(B, N, device=DEV)
+    w, _ = C.csa2_attn_mass(q, kv, q_pos, lse, n_visible=nv, k_max=N, acc=acc, want_weights=True)
+    C.csa2_ctx_check()
+    for b in range(B):
+        sel = np.where(np.arange(N) < to_np(nv[b])[:, None], np.arange(N), -1)
+        ow, om = G.attn_mass(to_np(q[b]), kv_np[b], sel, to_np(q_pos[b]), to_np(lse[b]))
+        assert_close(to_np(w[b]), ow, TOL, "weights")
+        assert_close(to_np(acc[b]), om, TOL, "acc")
+
+
+def _captured(call):
+    """A graph of one call, captured on a stream of its own; the guard checks, which wait, are left out."""
+    graph = torch.cuda.CUDAGraph()
+    check, C._check = C._check, lambda fn, st: None if st == C.OK else (_ for _ in ()).throw(C.Csa2Error(fn, st))
+    try:
+        with torch.cuda.graph(graph):
+            call()
+    finally:
+        C._check = check
+    return graph
+
+
+@pytest.mark.parametrize("ld,keep", [(9001, 4001), (130000, 70000)])
+def test_select_and_gather_captured(ld, keep):
+    """Two graphs of a selection with its gather, replayed in turn after the weights changed in place;
+    each has buffers of its own."""
+    sides = []
+    for i in range(2):
+        s = dict(acc=torch.rand((2, ld), generator=torch.Generator(DEV).manual_seed(i), device=DEV),
+                 n=torch.tensor([ld, ld // 2], dtype=torch.int64, device=DEV),
+                 kv=W.normal_tensor((2, ld, 16), 48, i, torch.float32, DEV),
+                 idx=torch.empty((2, keep), dtype=torch.int32, device=DEV), out=torch.zeros((2, keep, 16), device=DEV),
+                 ws=torch.empty(max(16, C._lib().csa2_evict_select_workspace_bytes(2, ld)), dtype=torch.uint8, device=DEV))
+
+        def call(s=s):
+            C.csa2_evict_select(s["acc"], s["n"], keep, recent=100, out=s["idx"], ws=s["ws"])
+            C.csa2_cache_gather(s["kv"], s["idx"], out=s["out"])
+
+        call()
+        C.csa2_ctx_check()
+        s["graph"] = _captured(call)
+        sides.append(s)
+    for turn in range(3):
+        for s in sides:
+            s["acc"].mul_(-1.5).add_(0.25)
+            s["out"].zero_()
+            s["graph"].replay()
+    torch.cuda.synchronize()
+    C.csa2_ctx_check()
+    for s in sides:
+        a = s["acc"].cpu().numpy()
+        for b in range(2):
+            ids = G.evict_keep(a[b], int(s["n"][b]), keep, 100)
+            assert np.array_equal(to_np(s["idx"][b]), ids)
+            have = ids >= 0
+            assert torch.equal(s["out"][b][torch.tensor(have)], s["kv"][b, torch.tensor(ids[have]).long()])
+            assert not s["out"][b][torch.tensor(~have)].any()
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "bf16"])
+def test_an_entry_is_appended_to_a_cut_cache(fmt):
+    """After a cut the next entry comes from csa2_compress over its finished block and goes behind the
+    entries that its sequence kept: the same row as csa2_compress_step writes to the uncut cache, and
+    attention over it and kept entries is what it was over the uncut one."""
+    B, N, H, m, keep, cap = 2, 200, 64, 4, 60, 72
+    n = (N + 1) * m                                          # tokens: N entries, and the block of one more
+    ca, za, cb, zb = (W.normal_tensor((B, n, 512), 49, i, torch.bfloat16, DEV) for i in range(4))
+    ba, bb = (W.normal_tensor((m, 512), 49, i, torch.float32, DEV) for i in (4, 5))
+    kw = dict(ba=ba, bb=bb, flags=C.W_NORM | C.W_ROPE, out_fmt=fmt)
+    row = (288,) if fmt == "fp4" else (512,)
+    full = torch.zeros((B, N + 1, *row), dtype=torch.uint8 if fmt == "fp4" else torch.bfloat16, device=DEV)
+    first = [t[:, :N * m].contiguous() for t in (ca, za, cb, zb)]
+    full[:, :N] = C.csa2_compress(first[0], first[1], m, cb=first[2], zb=first[3], **kw)
+    state = C.csa2_compress_state(B, 512, m, torch.bfloat16, DEV, overlap=True)
+    C.csa2_compress_state_seed(first[0], first[1], m, state, cb=first[2], zb=first[3])
+    # the cut: `keep` entries of the first sequence, the 40 that the second one has
+    have = torch.tensor([N, 40], dtype=torch.int64, device=DEV)
+    acc = torch.rand((B, N), generator=torch.Generator(DEV).manual_seed(1), device=DEV)
+    idx = torch.full((B, cap), -1, dtype=torch.int32, device=DEV)
+    idx[:, :keep] = C.csa2_evict_select(acc, have, keep, recent=8)
+    cache = torch.zeros((B, cap, *row), dtype=full.dtype, device=DEV)
+    C.csa2_cache_gather(full[:, :N].contiguous(), idx, out=cache)
+    count = have.clamp(max=keep)
+    # the next block: token by token into the uncut cache, at once for the cut one
+    for p in range(N * m, n):
+        C.csa2_compress_step(ca[:, p].contiguous(), za[:, p].contiguous(), m,
+                             torch.full((B,), p, dtype=torch.int64, device=DEV), state, cb=cb[:, p].contiguous(),
+                             zb=zb[:, p].contiguous(), out=full, out_seq_stride=N + 1, **kw)
+    last = [t[:, N * m:].contiguous() for t in (ca, za, cb, zb)]
+    new = C.csa2_compress(last[0], last[1], m, cb=last[2], zb=last[3], prev_cb=cb[:, (N - 1) * m:N * m].contiguous(),
+                          prev_zb=zb[:, (N - 1) * m:N * m].contiguous(), pos0=torch.full((B,), N * m, device=DEV), **kw)
+    cache[torch.arange(B, device=DEV), count] = new[:, 0]
+    C.csa2_ctx_check()
+    assert torch.equal(new[:, 0], full[:, N])
+    # a selection of the new entry and some kept ones, and the same entries of the uncut cache
+    cut_sel = torch.stack([torch.cat([c.view(1), torch.arange(0, 40, 3, device=DEV)]) for c in count])[:, None].int().contiguous()
+    ids = torch.cat([idx, torch.zeros_like(idx[:, :1])], 1)
+    ids[torch.arange(B, device=DEV), count] = N
+    old_sel = torch.gather(ids, 1, cut_sel[:, 0].long())[:, None].contiguous()
+    q = W.normal_tensor((B, 1, H, 512), 49, 9, torch.bfloat16, DEV)
+    q_pos = torch.full((B, 1), n, dtype=torch.int64, device=DEV)
+    o1, _ = C.csa2_sparse_attn(q, cache, cut_sel, None, q_pos, None, window=0)
+    o2, _ = C.csa2_sparse_attn(q, full, old_sel, None, q_pos, None, window=0)
+    C.csa2_ctx_check()
+    assert torch.equal(o1, o2)
