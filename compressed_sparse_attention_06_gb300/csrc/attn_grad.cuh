@@ -20,8 +20,10 @@ struct AgRope {
 };
 static inline AgRope make_ag_rope(float base) {
     AgRope r;
-    for (int j = 0; j < 32; ++j)
-        r.frac[j] = (uint64_t)ldexp(pow((double)base, -2.0 * (double)j / 64.0) / 6.283185307179586, 64);
+    for (int j = 0; j < 32; ++j) {
+        const double turns = pow((double)base, -2.0 * (double)j / 64.0) / 6.283185307179586;
+        r.frac[j] = (uint64_t)ldexp(turns - floor(turns), 64);       // (a base below 1 turns more than once)
+    }
     return r;
 }
 __device__ __forceinline__ void ag_cos_sin(const AgRope& r, int64_t pos, int j, float& c, float& s) {

@@ -360,6 +360,24 @@ def test_cache_without_entries(dt, dtype, dense):
     assert not dq.any()
 
 
+@pytest.mark.parametrize("dtype,tol", [(torch.float32, F32_TOL), (torch.bfloat16, TC_TOL)])
+@pytest.mark.parametrize("base", [0.05, 1.0, 500000.0])
+def test_any_rope_base(dtype, tol, base, monkeypatch):
+    """The same angles as the forward pass for any base; one below 1 turns some pairs more than once a
+    position.  The weights go by the same angles.  (The call takes the base as a 32-bit number.)"""
+    s = _case(28, 1, 3, 20, 90, 40, 9, 12, [[70, 3, 11]], dtype, 4)
+    kw = dict(window=9, rope_base=base)
+    s["out"], s["lse"] = C.csa2_sparse_attn(s["q"], s["kv"], s["idx"], s["swa"], s["q_pos"], s["sink"], want_lse=True, **kw)
+    got = C.csa2_sparse_attn_bwd(s["q"], s["kv"], s["idx"], s["swa"], s["q_pos"], s["sink"], s["out"], s["lse"], s["dout"], **kw)
+    w, _ = C.csa2_attn_mass(s["q"], s["kv"], s["q_pos"], s["lse"], idx=s["idx"], want_weights=True, rope_base=base)
+    C.csa2_ctx_check()
+    base, oracle = float(np.float32(base)), G.attn_bwd
+    monkeypatch.setattr(G, "attn_bwd", lambda *a: oracle(*a, base=base))
+    _check(s, got, tol)
+    ow, _ = G.attn_mass(to_np(s["q"][0]), to_np(s["kv"][0]), to_np(s["idx"][0]), to_np(s["q_pos"][0]), to_np(s["lse"][0]), base=base)
+    assert_close(to_np(w[0]), ow, 5e-5, "weights")
+
+
 def test_captured_and_on_another_stream():
     """A captured call, replayed after its inputs changed in place, equals an eager call."""
     s = _forward(_case(21, 1, 5, 64, 200, 90, 20, 32, [[40, 41, 42, 43, 44]], torch.bfloat16, 8))

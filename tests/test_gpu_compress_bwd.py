@@ -158,6 +158,20 @@ def test_layer_backward_matches_differences():
 
 
 @pytest.mark.parametrize("m", [2, 5])
+@pytest.mark.parametrize("base", [0.05, 1.0, 500000.0])
+def test_any_rope_base(m, base):
+    """(The call takes the base as a 32-bit number: so does the oracle.)"""
+    ca, za = (W.normal_tensor((4 * m, 512), 66, i, torch.float32, DEV) for i in (1, 2))
+    dout = W.normal_tensor((4, 512), 66, 3, torch.float32, DEV)
+    g = C.csa2_compress_bwd(ca, za, m, dout, pos0=1000, rope_base=base, flags=C.W_NORM | C.W_ROPE)
+    C.csa2_ctx_check()
+    w = G.compress_bwd(to_np(ca), to_np(za), m, to_np(dout), flags=C.W_NORM | C.W_ROPE, pos0=1000,
+                       base=float(np.float32(base)))
+    assert_close(to_np(g.dca), w["Ca"], TOL, "Ca")
+    assert_close(to_np(g.dza), w["Za"], TOL, "Za")
+
+
+@pytest.mark.parametrize("m", [2, 5])
 def test_compress_bwd_captured_and_on_another_stream(m):
     """A graph of the call, replayed after its inputs changed in place, and a call on a side stream give
     an eager call's bits; compiled and general window."""
