@@ -378,6 +378,37 @@ def test_any_rope_base(dtype, tol, base, monkeypatch):
     assert_close(to_np(w[0]), ow, 5e-5, "weights")
 
 
+@pytest.mark.parametrize("dtype,tol", [(torch.float32, F32_TOL), (torch.bfloat16, TC_TOL)])
+def test_window_ring_that_begins_elsewhere(dtype, tol, monkeypatch):
+    """swa_pos0 other than 0, positions before it among the window's."""
+    s = _case(29, 2, 3, 20, 60, 12, 20, 32, [[70, 9, 25], [40, 44, 3]], dtype, 4)
+    kw = dict(window=20, swa_pos0=21)
+    s["out"], s["lse"] = C.csa2_sparse_attn(s["q"], s["kv"], s["idx"], s["swa"], s["q_pos"], s["sink"], want_lse=True, **kw)
+    got = C.csa2_sparse_attn_bwd(s["q"], s["kv"], s["idx"], s["swa"], s["q_pos"], s["sink"], s["out"], s["lse"], s["dout"], **kw)
+    C.csa2_ctx_check()
+    oracle = G.attn_bwd
+    monkeypatch.setattr(G, "attn_bwd", lambda q, kv, sel, swa, pos0, *a: oracle(q, kv, sel, swa, 21, *a))
+    _check(s, got, tol)
+
+
+F, H = torch.float32, torch.bfloat16
+
+
+@pytest.mark.parametrize("q_dt,kv_dt,swa_dt,out_dt", [(H, F, H, H), (H, H, F, H), (H, H, H, F), (F, H, H, H), (F, H, F, H),
+                                                      (H, F, F, F), (F, F, H, F), (F, F, F, H)])
+def test_mixed_types(q_dt, kv_dt, swa_dt, out_dt):
+    """Any mixture runs in fp32 on the CUDA cores; each gradient has its tensor's type, and one rounding
+    of it more where that is bf16."""
+    s = _case(30, 1, 3, 20, 90, 40, 9, 12, [[70, 3, 11]], F, 4)
+    s.update(q=s["q"].to(q_dt), kv=s["kv"].to(kv_dt), swa=s["swa"].to(swa_dt), dout=s["dout"].to(out_dt))
+    s["out"], s["lse"] = C.csa2_sparse_attn(s["q"], s["kv"], s["idx"], s["swa"], s["q_pos"], s["sink"], window=9, want_lse=True,
+                                            out=torch.empty(s["q"].shape, dtype=out_dt, device=DEV))
+    got = _backward(s)
+    C.csa2_ctx_check()
+    assert [g.dtype for g in got] == [q_dt, kv_dt, swa_dt, F]
+    _check(s, got, BF16_TOL)
+
+
 def test_captured_and_on_another_stream():
     """A captured call, replayed after its inputs changed in place, equals an eager call."""
     s = _forward(_case(21, 1, 5, 64, 200, 90, 20, 32, [[40, 41, 42, 43, 44]], torch.bfloat16, 8))
