@@ -6,8 +6,9 @@
 // sequence an entry gets one addend (the same index twice gives equal addends), added
 // straight to acc.  With more, the addends of a call meet as 64-bit integers in units of
 // 2^-39 in the workspace (integer sums are the same in any order; an addend is at most H
-// and B*Q*H at most 2^24, so the sum stays below 2^63; the rounding of an addend, 2^-40,
-// is far below fp32's of the weights), and a last pass adds them to acc.
+// and B*Q*H at most 2^24, so the sum stays below 2^63), and a last pass adds them to acc.  An
+// addend's rounding, 2^-40, is below fp32's of a weight of 2^-16 and more, and above it of a
+// smaller one; a weight below 2^-40 counts 0 here, where one query's is kept.
 #include <algorithm>
 #include <atomic>
 

@@ -248,7 +248,10 @@ def evict_caches(acc, n_entries, caches: Dict[str, torch.Tensor], keep: int, rec
     """Cut every sequence to `keep` entries: its newest `recent` and the others of the largest
     accumulated attention weight (csa2_attn_mass).  caches: any [B, N, ..] tensors whose row j
     belongs to entry j (main KV, indexer keys); new ones are returned, with acc cut alike.
-    Rows behind a shorter sequence's entries are zero in them."""
+    Rows behind a shorter sequence's entries are zero in them.  (To leave room behind the kept entries,
+    or to cut into buffers at hand, pad csa2_evict_select's ids with -1 and call csa2_cache_gather.)
+    A sequence's next entry goes to row n_entries[b]: it comes from csa2_compress over its finished
+    block, as csa2_compress_step writes entry i to row i."""
     idx = C.csa2_evict_select(acc, n_entries, keep, recent=recent)
     B = acc.shape[0]
 

@@ -371,7 +371,7 @@ csa2_status csa2_pool_topk(csa2_ctx* ctx, const float* block_max, const uint32_t
  *
  *   q     : [B, Q, H, c] in q_dt (F32 or BF16)
  *   kv    : [B, N, c] (F32, BF16) or [B, N, c/2 + c/16] B (CSA2_FP4_E4M3x16)
- *   idx   : [B, Q, k] int32, -1 = none; ids outside [0, N) are skipped and flagged
+ *   idx   : [B, Q, k] int32, -1 (any negative) = none; ids >= N are skipped and flagged
  *   swa   : [B, swa_cap, c] in swa_dt (F32 or BF16); window <= swa_cap
  *   q_pos : [B, Q] int64
  *   sink  : [H] f32 or NULL (no sink term)
@@ -511,6 +511,8 @@ csa2_status csa2_sparse_attn_noalloc(csa2_ctx* ctx,
  * that appears twice in a query's idx counts twice, as in the forward.  Gradients must not
  * overlap the inputs or each other.  Row sums are added in query order without atomics:
  * the same call with the same workspace size gives the same bits.
+ * Calls of BF16 tensors with both norms run on the tensor cores: q^, do', r p, r dS and each
+ * query's addend to a row are rounded to bf16 there, sums are fp32; all others in fp32 throughout.
  *
  * Workspace: csa2_attn_bwd_workspace_bytes() bytes (16-byte aligned) run the queries in one
  * chunk (in chunks that keep it under 16 GiB for the largest calls); any smaller one that
@@ -588,7 +590,8 @@ csa2_status csa2_compress_bwd(csa2_ctx* ctx,
  * BF16 and FP4 rows run on the tensor cores, with q^ as the sum of two bf16 numbers (2^-17 of it
  * left out) and fp32 sums; F32 rows in fp32 on the CUDA cores.
  * The sums into acc do not depend on timing: with one query per sequence each entry gets
- * one addend; with more they meet as 64-bit integers in units of 2^-39 first.
+ * one addend; with more they meet as 64-bit integers in units of 2^-39 first (an addend below
+ * 2^-40 counts 0).
  */
 size_t csa2_attn_mass_workspace_bytes(csa2_ctx* ctx, csa2_dtype kv_dt, int B, int Q, int H, int k, int64_t N,
                                       int want_acc);
@@ -620,7 +623,10 @@ csa2_status csa2_attn_mass(csa2_ctx* ctx,
  * row_bytes a multiple of 4, at most 2^20; dst must not overlap src (CSA2_ERR_INVALID_ARG).
  * After an eviction entry i of the cut cache is the old entry idx[b, i]: stored rows carry
  * their own rotation, so attention over them is unchanged, while the visible count of a
- * sequence becomes the number of entries it kept.
+ * sequence becomes the number of entries it kept.  idx padded with -1 leaves rows of dst for
+ * entries to come.  csa2_compress_step writes entry i to row i, so the next entries of a cut
+ * cache come from csa2_compress over their finished block (n_tokens = m, pos0 its first
+ * position, prev_cb / prev_zb the block before: the same row) and are placed behind the kept ones.
  */
 size_t csa2_evict_select_workspace_bytes(int B, int64_t ld);
 csa2_status csa2_evict_select(csa2_ctx* ctx, const float* acc, int B, int64_t ld, const int64_t* n_entries,
