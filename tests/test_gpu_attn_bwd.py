@@ -257,6 +257,34 @@ def test_chunked_workspace_and_same_bits(dtype, tol):
     assert e.value.status == C.ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("dtype,tol", [(torch.float32, F32_TOL), (torch.bfloat16, TC_TOL)])
+@pytest.mark.parametrize("part", [2, 6])
+def test_chunked_dense_with_two_head_passes(dtype, tol, part):
+    """Chunks of the dense form, more than 64 heads, a last chunk smaller than the others, and two calls
+    at once on two streams with a workspace each: the same bits as one after the other."""
+    s = _forward(_case(31, 1, 29, 100, 150, 150, 12, 40, [[i * 9 for i in range(29)]], dtype, dense=True))
+    dt = {torch.float32: C.F32, torch.bfloat16: C.BF16}[dtype]
+    size = C._lib().csa2_attn_bwd_workspace_bytes(C.ctx(0), dt, dt, dt, dt, 1, 29, 100, 150, 12, 150, 40, 7) // part
+    ws = [torch.empty(size, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    got = _backward(s, ws=ws[0])
+    C.csa2_ctx_check()
+    _check(s, got, tol)
+    check, C._check = C._check, lambda fn, st: None if st == C.OK else (_ for _ in ()).throw(C.Csa2Error(fn, st))
+    both, streams = [], [torch.cuda.Stream() for _ in ws]
+    try:
+        for w, stream in zip(ws, streams):
+            stream.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(stream):
+                both.append(_backward(s, ws=w))
+    finally:
+        C._check = check
+    torch.cuda.synchronize()
+    C.csa2_ctx_check()
+    for one in both:
+        for a, b in zip(one, got):
+            assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_workspace_at_any_16_bytes(dtype):
     """A workspace of the size asked for, 16 bytes and more behind a 256-byte boundary: the same bits,
