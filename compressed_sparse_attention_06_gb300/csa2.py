@@ -659,7 +659,8 @@ def csa2_sparse_attn_bwd(q, kv, idx, swa, q_pos, sink, out, lse, dout, window: i
                          want_dkv: bool = True, want_dswa: bool = True, want_dsink: bool = True):
     """Backward pass of csa2_sparse_attn: its inputs, its out [B,Q,H,c] and lse [B,Q,H], and
     dout (out's dtype).  Returns (dq, dkv, dswa, dsink), each like the tensor it is the
-    gradient of (dsink [H] f32); None where that tensor is None or the gradient not wanted.
+    gradient of (dsink [H] f32, 0 without a sink); dkv and dswa are None where kv and swa are,
+    and each but dq where it is not wanted.
     `ws` is the workspace (allocated here when not given)."""
     k = idx.shape[-1] if idx is not None else 0
     if idx is not None:
