@@ -38,6 +38,10 @@ EXPORTS = (
     "csa2_compress_bwd", "csa2_compress_bwd_workspace_bytes",
     "csa2_attn_mass", "csa2_attn_mass_workspace_bytes", "csa2_evict_select",
     "csa2_evict_select_workspace_bytes", "csa2_cache_gather",
+    "csa2_tree_plan", "csa2_tree_attn", "csa2_tree_attn_workspace_bytes", "csa2_tree_commit",
+    "csa2_pages_fork", "csa2_pages_free", "csa2_pages_reserve", "csa2_pages_reserve_workspace_bytes",
+    "csa2_pages_compact", "csa2_pages_compact_workspace_bytes",
+    "csa2_page_copy", "csa2_page_write", "csa2_page_read",
 )
 
 
@@ -106,6 +110,20 @@ def _declare(lib):
         "csa2_evict_select_workspace_bytes": (_sz, [_i, _i64]),
         "csa2_evict_select": (_i, [_vp, _vp, _i, _i64, _vp, _i, _i, _vp, _vp, _sz, _vp]),
         "csa2_cache_gather": (_i, [_vp, _vp, _i64, _i, _i64, _vp, _i, _vp, _vp]),
+        "csa2_tree_plan": (_i, [_vp, _vp, _vp, _i, _i, _vp, _vp, _vp]),
+        "csa2_tree_attn_workspace_bytes": (_sz, [_vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _u]),
+        "csa2_tree_attn": (_i, [_vp, _vp, _i, _vp, _i, _i64, _vp, _i, _i, _vp, _vp, _i, _vp, _i, _i64, _i64, _i, _vp, _vp,
+                                _vp, _vp, _vp, _i, _i, _i, _i, _f, _u, _vp, _i, _vp, _vp, _sz, _vp]),
+        "csa2_tree_commit": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i64, _i64, _vp, _vp]),
+        "csa2_pages_fork": (_i, [_vp, _vp, _i64, _vp, _i, _i, _vp, _i, _vp, _vp]),
+        "csa2_pages_free": (_i, [_vp, _vp, _i64, _vp, _i, _i, _i, _vp, _vp]),
+        "csa2_pages_reserve_workspace_bytes": (_sz, [_i64, _i, _i]),
+        "csa2_pages_reserve": (_i, [_vp, _vp, _i64, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+        "csa2_pages_compact_workspace_bytes": (_sz, [_i64]),
+        "csa2_pages_compact": (_i, [_vp, _vp, _i64, _vp, _i, _i, _vp, _vp, _vp, _sz, _vp]),
+        "csa2_page_copy": (_i, [_vp, _vp, _i64, _i64, _vp, _i64, _vp]),
+        "csa2_page_write": (_i, [_vp, _vp, _i64, _i, _i64, _vp, _i, _i, _vp, _i, _vp, _vp, _vp]),
+        "csa2_page_read": (_i, [_vp, _vp, _i64, _i, _i64, _vp, _i, _i, _vp, _i, _vp, _vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -798,4 +816,214 @@ def csa2_cache_gather(src, idx, out: Optional[torch.Tensor] = None) -> torch.Ten
     st = _lib().csa2_cache_gather(ctx(src.device.index), _main(src), row_bytes, B, N, _a(idx), keep, _a(out),
                                   _on(src.device))
     _check("csa2_cache_gather", st)
+    return out
+
+
+def csa2_tree_plan(parent, ctx_len, pos: Optional[torch.Tensor] = None, path: Optional[torch.Tensor] = None):
+    """Positions [B,T] int64 and paths [B,T,T] int16 of the nodes of drafted trees: parent [B,T]
+    int32 (below the node; -1 the committed context, less an unused node), ctx_len [B] int64."""
+    B, T = parent.shape
+    dev = parent.device
+    _want("parent", parent, (B, T), torch.int32, dev)
+    _want("ctx_len", ctx_len, (B,), torch.int64, dev)
+    pos = _given("pos", pos, (B, T), torch.int64, dev)
+    path = _given("path", path, (B, T, T), torch.int16, dev)
+    st = _lib().csa2_tree_plan(ctx(dev.index), _main(parent), _a(ctx_len), B, T, _a(pos), _a(path), _on(dev))
+    _check("csa2_tree_plan", st)
+    return pos, path
+
+
+def _row_dt(kv, c: int, kv_fmt: Optional[int]) -> int:
+    """The format of cache rows [.., row] of c channels, and a check of their width."""
+    fp4 = kv.dtype == torch.uint8
+    dt = (FP4_E4M3x16 if kv_fmt is None else kv_fmt) if fp4 else _dt(kv)
+    if kv.shape[-1] != (fp4_row_bytes(c) if fp4 else c):
+        raise ValueError(f"kv rows of {kv.shape[-1]} {kv.dtype} are not rows of {c} channels")
+    return dt
+
+
+def csa2_tree_attn(q, kv, pos, path, ctx_len, swa, draft, idx=None, n_visible=None, k_max: int = 0,
+                   table: Optional[torch.Tensor] = None, sink=None, window: int = 128, swa_pos0: int = 0,
+                   kv_fmt: Optional[int] = None, rope_base: float = 10000.0, flags: int = ATTN_DEFAULT, out_dtype=None,
+                   want_lse: bool = False, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                   ws: Optional[torch.Tensor] = None):
+    """Attention of every node of drafted trees: q [B,T,H,c]; kv [B,N,row], or pages [n_pages,page,row]
+    with their table [B,max_pages] int32; pos, path from csa2_tree_plan, ctx_len [B] int64; swa [B,cap,c]
+    the ring of committed rows, draft [B,T,c] the nodes' own; idx [B,T,k] int32, or n_visible [B,T] int64
+    <= k_max for the dense form (neither: the window alone).  Returns (out [B,T,H,c], lse [B,T,H] or None).
+    `ws` is the workspace (allocated here when not given)."""
+    B, T, H, c = q.shape
+    dev = q.device
+    if idx is not None and n_visible is not None:
+        raise ValueError("give idx or n_visible, not both")
+    _want("pos", pos, (B, T), torch.int64, dev)
+    _want("path", path, (B, T, T), torch.int16, dev)
+    _want("ctx_len", ctx_len, (B,), torch.int64, dev)
+    k = 0
+    if idx is not None:
+        k = idx.shape[-1]
+        _want("idx", idx, (B, T, k), torch.int32, dev)
+    elif n_visible is not None:
+        k = k_max
+        _want("n_visible", n_visible, (B, T), torch.int64, dev)
+    if sink is not None:
+        _want("sink", sink, (H,), torch.float32, dev)
+    kv_dt, N, page, max_pages = F32, 0, 1, 0
+    if kv is not None:
+        kv_dt = _row_dt(kv, c, kv_fmt)
+        if table is None:
+            _want("kv", kv, (B, *kv.shape[1:2], kv.shape[-1]), kv.dtype, dev)
+            N = kv.shape[1]
+        else:
+            page, max_pages = kv.shape[1], table.shape[1]
+            _want("kv", kv, (kv.shape[0], page, kv.shape[-1]), kv.dtype, dev)
+            _want("table", table, (B, max_pages), torch.int32, dev)
+            N = kv.shape[0] * page
+    swa_dt, cap = F32, 0
+    if swa is not None:
+        swa_dt, cap = _dt(swa), swa.shape[1]
+        _want("swa", swa, (B, cap, c), swa.dtype, dev)
+        if draft is not None:
+            _want("draft", draft, (B, T, c), swa.dtype, dev)
+    out = alloc((B, T, H, c), dtype=out_dtype or q.dtype, device=dev) if out is None else \
+        _want("out", out, (B, T, H, c), out.dtype, dev)
+    if want_lse or lse is not None:
+        lse = _given("lse", lse, (B, T, H), torch.float32, dev)
+    if ws is None:
+        need = _lib().csa2_tree_attn_workspace_bytes(ctx(dev.index), _dt(q), kv_dt, swa_dt, B, T, H, k, window,
+                                                     int(n_visible is not None), flags)
+        ws = _ws(need, dev) if need else None
+    st = _lib().csa2_tree_attn(ctx(dev.index), _main(q), _dt(q), _a(kv), kv_dt, N, _a(table), max_pages, page, _a(idx),
+                               _a(n_visible), k, _a(swa), swa_dt, cap, swa_pos0, window, _a(draft), _a(pos), _a(path),
+                               _a(ctx_len), _a(sink), B, T, H, c, rope_base, flags, _a(out), _dt(out), _a(lse), _p(ws),
+                               ws.numel() * ws.element_size() if ws is not None else 0, _on(dev))
+    _check("csa2_tree_attn", st)
+    return out, lse
+
+
+def csa2_tree_commit(draft, pos, path, ctx_len, leaf, swa, swa_pos0: int = 0, new_len: Optional[torch.Tensor] = None):
+    """The draft rows [B,T,c] on the path of node leaf[b] ([B] int32, < 0: none) into the ring swa
+    [B,cap,c]; new_len [B] int64 (may be ctx_len), if given, gets the sequences' lengths then."""
+    B, T, c = draft.shape
+    dev = draft.device
+    _want("pos", pos, (B, T), torch.int64, dev)
+    _want("path", path, (B, T, T), torch.int16, dev)
+    _want("ctx_len", ctx_len, (B,), torch.int64, dev)
+    _want("leaf", leaf, (B,), torch.int32, dev)
+    _want("swa", swa, (B, swa.shape[1], c), draft.dtype, dev)
+    if new_len is not None:
+        _want("new_len", new_len, (B,), torch.int64, dev)
+    st = _lib().csa2_tree_commit(ctx(dev.index), _main(draft), _dt(draft), _a(pos), _a(path), _a(ctx_len), _a(leaf), B, T, c,
+                                 _a(swa), swa.shape[1], swa_pos0, _a(new_len), _on(dev))
+    _check("csa2_tree_commit", st)
+    return swa
+
+
+def _state(refs, table):
+    """Checks the state of a paged cache; returns (n_pages, B, max_pages, device)."""
+    dev = refs.device
+    _want("refs", refs, (refs.numel(),), torch.int32, dev)
+    B, P = table.shape
+    _want("table", table, (B, P), torch.int32, dev)
+    return refs.numel(), B, P, dev
+
+
+def csa2_pages_fork(refs, table, parent, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Table [B_out,max_pages] of continuations that share the pages of row parent[i] of table
+    [B,max_pages] (parent [B_out] int32, < 0: an empty row); refs [n_pages] int32 go up."""
+    n, B, P, dev = _state(refs, table)
+    nb = parent.numel()
+    _want("parent", parent, (nb,), torch.int32, dev)
+    out = _given("out", out, (nb, P), torch.int32, dev)
+    st = _lib().csa2_pages_fork(ctx(dev.index), _main(refs), n, _a(table), B, P, _a(parent), nb, _a(out), _on(dev))
+    _check("csa2_pages_fork", st)
+    return out
+
+
+def csa2_pages_free(refs, table, page: int, keep: Optional[torch.Tensor] = None) -> None:
+    """Gives back the pages behind the first keep[b] entries ([B] int64; None: all, < 0: leave the
+    sequence alone): refs and table are updated."""
+    n, B, P, dev = _state(refs, table)
+    if keep is not None:
+        _want("keep", keep, (B,), torch.int64, dev)
+    _check("csa2_pages_free", _lib().csa2_pages_free(ctx(dev.index), _main(refs), n, _a(table), B, P, page, _a(keep), _on(dev)))
+
+
+def csa2_pages_reserve(refs, table, first, count, page: int, granted: Optional[torch.Tensor] = None,
+                       copies: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """Makes entries first[b] .. first[b]+count[b]-1 ([B] int64) writable: missing and shared pages are
+    replaced by free ones (refs and table are updated).  Returns (granted [B] int64, copies [B,2] int32):
+    how many of the entries got their page, and the pairs csa2_page_copy is to copy in every pool."""
+    n, B, P, dev = _state(refs, table)
+    _want("first", first, (B,), torch.int64, dev)
+    _want("count", count, (B,), torch.int64, dev)
+    granted = _given("granted", granted, (B,), torch.int64, dev)
+    copies = _given("copies", copies, (B, 2), torch.int32, dev)
+    if ws is None:
+        ws = _ws(_lib().csa2_pages_reserve_workspace_bytes(n, B, P), dev)
+    st = _lib().csa2_pages_reserve(ctx(dev.index), _main(refs), n, _a(table), B, P, page, _a(first), _a(count), _a(granted),
+                                   _a(copies), _p(ws), ws.numel() * ws.element_size(), _on(dev))
+    _check("csa2_pages_reserve", st)
+    return granted, copies
+
+
+def csa2_pages_compact(refs, table, moves: Optional[torch.Tensor] = None, n_used: Optional[torch.Tensor] = None,
+                       ws: Optional[torch.Tensor] = None):
+    """Moves the pages in use to the front of the pool: refs and table (all the tables that hold its
+    pages, in one tensor) are updated.  Returns (moves [n_pages // 2, 2] int32, -1 padded, for
+    csa2_page_copy on every pool; n_used [1] int64)."""
+    n, B, P, dev = _state(refs, table)
+    moves = _given("moves", moves, (n // 2, 2), torch.int32, dev)
+    n_used = _given("n_used", n_used, (1,), torch.int64, dev)
+    if ws is None:
+        ws = _ws(_lib().csa2_pages_compact_workspace_bytes(n), dev)
+    st = _lib().csa2_pages_compact(ctx(dev.index), _main(refs), n, _a(table), B, P, _a(moves), _a(n_used), _p(ws),
+                                   ws.numel() * ws.element_size(), _on(dev))
+    _check("csa2_pages_compact", st)
+    return moves, n_used
+
+
+def _row_bytes(t, lead: int) -> int:
+    n = t.element_size()
+    for d in t.shape[lead:]:
+        n *= d
+    return n
+
+
+def csa2_page_copy(pool, pairs) -> torch.Tensor:
+    """pool[to] = pool[from] for pairs [n,2] int32 (from, to) of pages; pairs with a -1 are skipped."""
+    _want("pairs", pairs, (pairs.shape[0], 2), torch.int32, pool.device)
+    st = _lib().csa2_page_copy(ctx(pool.device.index), _main(pool), pool.shape[0], _row_bytes(pool, 1), _a(pairs),
+                               pairs.shape[0], _on(pool.device))
+    _check("csa2_page_copy", st)
+    return pool
+
+
+def csa2_page_write(pool, table, rows, first, count) -> torch.Tensor:
+    """rows [B,n,..] to entries first[b] + i, i < count[b] ([B] int64: what csa2_pages_reserve granted),
+    of a pool [n_pages,page,..] through table [B,max_pages]."""
+    B, n = rows.shape[:2]
+    dev = pool.device
+    _want("table", table, (B, table.shape[1]), torch.int32, dev)
+    _want("rows", rows, (B, n, *pool.shape[2:]), pool.dtype, dev)
+    _want("first", first, (B,), torch.int64, dev)
+    _want("count", count, (B,), torch.int64, dev)
+    st = _lib().csa2_page_write(ctx(dev.index), _main(pool), pool.shape[0], pool.shape[1], _row_bytes(pool, 2), _a(table), B,
+                                table.shape[1], _a(rows), n, _a(first), _a(count), _on(dev))
+    _check("csa2_page_write", st)
+    return pool
+
+
+def csa2_page_read(pool, table, idx, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rows out[b,i] = entry idx[b,i] of sequence b, for idx [B,keep] int32, of a pool [n_pages,page,..]
+    through table [B,max_pages]; rows whose idx is -1 are left as they are in `out` (uninitialised when
+    allocated here)."""
+    B, keep = idx.shape
+    dev = pool.device
+    _want("idx", idx, (B, keep), torch.int32, dev)
+    _want("table", table, (B, table.shape[1]), torch.int32, dev)
+    out = _given("out", out, (B, keep, *pool.shape[2:]), pool.dtype, dev)
+    st = _lib().csa2_page_read(ctx(dev.index), _main(pool), pool.shape[0], pool.shape[1], _row_bytes(pool, 2), _a(table), B,
+                               table.shape[1], _a(idx), keep, _a(out), _on(dev))
+    _check("csa2_page_read", st)
     return out

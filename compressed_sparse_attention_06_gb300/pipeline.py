@@ -259,3 +259,100 @@ def evict_caches(acc, n_entries, caches: Dict[str, torch.Tensor], keep: int, rec
         return C.csa2_cache_gather(t, idx, out=C.alloc((B, keep, *t.shape[2:]), dtype=t.dtype, device=t.device).zero_())
 
     return CutCaches(idx, n_entries.clamp(min=0, max=min(keep, acc.shape[1])), cut(acc), {name: cut(t) for name, t in caches.items()})
+
+
+@dataclass
+class PagedCache:
+    """Caches of B sequences in pages that sequences may share (csa2_pages_*): every pool
+    [n_pages, page, ..] holds one kind of rows (main KV, indexer keys, of any layers) of entry e of
+    sequence b on page table[b, e // page]; refs counts the places that hold a page."""
+    pools: Dict[str, torch.Tensor]
+    refs: torch.Tensor           # [n_pages] int32
+    table: torch.Tensor          # [B, max_pages] int32, -1: none
+    n_entries: torch.Tensor      # [B] int64
+
+    @property
+    def page(self) -> int:
+        return next(iter(self.pools.values())).shape[1]
+
+
+def alloc_pages(B: int, n_pages: int, page: int, max_pages: int, rows: Dict[str, tuple], device) -> PagedCache:
+    """An empty paged cache; rows: name -> (shape of a row, dtype), e.g. {"kv": ((288,), torch.uint8)}."""
+    return PagedCache({k: C.alloc((n_pages, page, *shape), dtype=dt, device=device) for k, (shape, dt) in rows.items()},
+                      torch.zeros(n_pages, dtype=torch.int32, device=device),
+                      torch.full((B, max_pages), -1, dtype=torch.int32, device=device),
+                      torch.zeros(B, dtype=torch.int64, device=device))
+
+
+def pages_append(cache: PagedCache, rows: Dict[str, torch.Tensor], count: torch.Tensor) -> torch.Tensor:
+    """Append rows[name][b, :count[b]] to every sequence in every pool (count [B] int64), copying the
+    beginning of a page that another sequence shares first.  Returns how many entries each sequence
+    got: fewer than count where the pool or the table's row had no room."""
+    granted, copies = C.csa2_pages_reserve(cache.refs, cache.table, cache.n_entries, count, cache.page)
+    for name, pool in cache.pools.items():
+        C.csa2_page_copy(pool, copies)
+        C.csa2_page_write(pool, cache.table, rows[name], cache.n_entries, granted)
+    cache.n_entries = cache.n_entries + granted
+    return granted
+
+
+def pages_fork(cache: PagedCache, parent: torch.Tensor) -> PagedCache:
+    """Continuations of sequences parent [B_out] int32 (negative: an empty one): they share their origins'
+    pages until one of them appends.  The pools and refs are the same tensors; the origins stay."""
+    n = cache.n_entries[parent.clamp(min=0).long()].masked_fill(parent < 0, 0)
+    return PagedCache(cache.pools, cache.refs, C.csa2_pages_fork(cache.refs, cache.table, parent), n)
+
+
+def pages_cut(cache: PagedCache, keep: Optional[torch.Tensor] = None) -> None:
+    """Cut every sequence to its first keep[b] entries (None: to nothing; negative or more than it has:
+    as it is) and give back the pages behind them."""
+    C.csa2_pages_free(cache.refs, cache.table, cache.page, keep)
+    if keep is None:
+        cache.n_entries = torch.zeros_like(cache.n_entries)
+    else:
+        cache.n_entries = torch.where(keep < 0, cache.n_entries, torch.minimum(keep, cache.n_entries))
+
+
+def pages_compact(cache: PagedCache) -> torch.Tensor:
+    """Move the pages in use to the front of every pool (the cache's table must hold all of them: the
+    tables of several caches over the same pools are rows of one).  Returns their number, [1] int64."""
+    moves, n_used = C.csa2_pages_compact(cache.refs, cache.table)
+    for pool in cache.pools.values():
+        C.csa2_page_copy(pool, moves)
+    return n_used
+
+
+@dataclass
+class DraftPlan:
+    """A step's drafted trees, planned once for all layers: positions and paths of their nodes."""
+    ctx_len: torch.Tensor        # [B] int64 committed tokens
+    pos: torch.Tensor            # [B, T] int64, -1: unused node
+    path: torch.Tensor           # [B, T, T] int16
+
+
+def plan_draft(parent: torch.Tensor, ctx_len: torch.Tensor) -> DraftPlan:
+    """parent [B, T] int32: the node that a drafted token follows (-1: the committed context,
+    less: an unused node)."""
+    return DraftPlan(ctx_len, *C.csa2_tree_plan(parent, ctx_len))
+
+
+def draft_attention(q, cache: PagedCache, plan: DraftPlan, swa, draft, sink=None, idx=None, n_visible=None,
+                    k_max: int = 0, kv: str = "kv", window: int = 128, swa_pos0: int = 0, flags: int = C.ATTN_DEFAULT,
+                    out=None, ws=None):
+    """A layer's attention for every drafted token over the pages of pool `kv`: its selected entries
+    idx [B, T, k] (Full, Reindex and Reuse layers), or all visible ones (n_visible [B, T] <= k_max,
+    the heavily compressed cache), its window of committed rows (the ring swa) and its own path's
+    draft rows."""
+    o, _ = C.csa2_tree_attn(q, cache.pools[kv], plan.pos, plan.path, plan.ctx_len, swa, draft, idx=idx,
+                            n_visible=n_visible, k_max=k_max, table=cache.table, sink=sink, window=window,
+                            swa_pos0=swa_pos0, flags=flags, out=out, ws=ws)
+    return o
+
+
+def accept_draft(plan: DraftPlan, leaf: torch.Tensor, layers, swa_pos0: int = 0) -> torch.Tensor:
+    """After verification: the accepted path's rows (up to node leaf[b] [B] int32, negative: none) enter
+    the window ring of every layer, layers = [(draft, swa), ..].  Returns the sequences' new lengths."""
+    new_len = C.alloc(tuple(plan.ctx_len.shape), dtype=torch.int64, device=plan.ctx_len.device)
+    for draft, swa in layers:
+        C.csa2_tree_commit(draft, plan.pos, plan.path, plan.ctx_len, leaf, swa, swa_pos0=swa_pos0, new_len=new_len)
+    return new_len

@@ -634,6 +634,136 @@ csa2_status csa2_evict_select(csa2_ctx* ctx, const float* acc, int B, int64_t ld
 csa2_status csa2_cache_gather(csa2_ctx* ctx, const void* src, int64_t row_bytes, int B, int64_t N,
                               const int32_t* idx, int keep, void* dst, void* stream);
 
+/*
+ * Drafted tokens.  A draft of sequence b is a tree of up to T nodes over its committed context
+ * of ctx_len[b] tokens: node i follows node parent[b,i] < i, or the context itself (-1); any
+ * value below -1 marks an unused node.  Node i stands at position ctx_len[b] + depth(i).
+ *
+ * csa2_tree_plan -- positions and paths of the nodes, once a step for all layers:
+ *   parent  : [B, T] int32;  ctx_len: [B] int64, >= 0
+ *   pos     : [B, T] int64, the node's position; -1 for unused nodes and those below them
+ *   path    : [B, T, T] int16, path[b,i,d] = the node at depth d on the way to node i, itself
+ *             at its own depth; -1 behind it
+ * A parent >= its node, or a ctx_len < 0, is flagged (CSA2_ERR_DEVICE) and its nodes are unused.
+ * 1 <= T <= 256, B <= 65535.
+ *
+ * csa2_tree_attn -- csa2_sparse_attn (idx) or csa2_dense_attn (n_visible) for every node of the
+ * drafts (DSA-to-CSA/HCA page eqs. (18)-(19), (26), (27)): node i attends to its cache entries
+ * and to the last `window` positions up to its own, of which those below ctx_len[b] are rows of
+ * the ring swa and the others the draft rows of its own path (never another branch's):
+ *     { kv[b, s] : s selected }  U  { swa slot (p - swa_pos0) mod swa_cap, p < ctx_len[b] }
+ *                                U  { draft[b, path[b,i,p - ctx_len[b]]], p >= ctx_len[b] },
+ *     max(0, t - window + 1) <= p <= t = pos[b,i].
+ * Norms, rotations, sink, out and lse as csa2_sparse_attn; a tree that is one chain gives what
+ * csa2_sparse_attn gives over a ring that holds the draft rows.  An unused node attends to
+ * nothing: out 0, lse the sink (or -inf).
+ *   q         : [B, T, H, c] in q_dt (F32 or BF16)
+ *   kv        : table NULL: [B, N, row] (F32, BF16 or CSA2_FP4_E4M3x16);
+ *               else pages of `page` entries, [N / page, page, row], N a multiple of page
+ *   table     : [B, max_pages] int32 or NULL: entry e of sequence b is entry e % page of page
+ *               table[b, e / page] (sequences may share pages)
+ *   idx       : [B, T, k] int32, negative = none;  or n_visible: [B, T] int64, at most k taken
+ *               (the other NULL).  Entries outside the cache, behind the table or on a page that
+ *               is none are skipped and flagged
+ *   swa       : [B, swa_cap, c], draft: [B, T, c], both in swa_dt (F32 or BF16); window <= swa_cap
+ *   pos, path, ctx_len: csa2_tree_plan's
+ * c == 512, 1 <= H <= 128, k <= 2048 (dense: 4,194,304), window <= 1024, T <= 256, B*T <= 65535.
+ * BF16 query, window and drafts over BF16 or FP4 rows with both norms run on the tensor cores
+ * (q^ and p rounded to bf16, sums fp32), all other calls in fp32.
+ * Workspace: csa2_tree_attn_workspace_bytes() bytes, 16-byte aligned; with fewer the call
+ * returns CSA2_ERR_INVALID_ARG.  Calls that share a workspace must not overlap on the GPU.
+ *
+ * csa2_tree_commit -- the accepted path's rows enter the window ring: for every node j on the
+ * path of leaf[b], swa[b, (pos[b,j] - swa_pos0) mod swa_cap] = draft[b, j] (the last swa_cap
+ * rows of a longer path).  leaf[b] < 0 or an unused node commits nothing.
+ *   leaf    : [B] int32, ids >= T are flagged
+ *   swa, draft: as csa2_tree_attn, in dt (F32 or BF16)
+ *   new_len : [B] int64 or NULL: tokens of the sequence then, pos of the leaf + 1 (ctx_len[b] if
+ *             nothing is committed); may be ctx_len itself
+ */
+csa2_status csa2_tree_plan(csa2_ctx* ctx, const int32_t* parent, const int64_t* ctx_len, int B, int T,
+                           int64_t* pos, int16_t* path, void* stream);
+size_t csa2_tree_attn_workspace_bytes(csa2_ctx* ctx, csa2_dtype q_dt, csa2_dtype kv_dt, csa2_dtype swa_dt, int B, int T,
+                                      int H, int k, int window, int dense, unsigned flags);
+csa2_status csa2_tree_attn(csa2_ctx* ctx,
+                           const void* q, csa2_dtype q_dt,
+                           const void* kv, csa2_dtype kv_dt, int64_t N,
+                           const int32_t* table, int max_pages, int page,
+                           const int32_t* idx, const int64_t* n_visible, int k,
+                           const void* swa, csa2_dtype swa_dt, int64_t swa_cap, int64_t swa_pos0, int window,
+                           const void* draft, const int64_t* pos, const int16_t* path, const int64_t* ctx_len,
+                           const float* sink, int B, int T, int H, int c, float rope_base, unsigned flags,
+                           void* out, csa2_dtype out_dt, float* lse, void* ws, size_t ws_bytes, void* stream);
+csa2_status csa2_tree_commit(csa2_ctx* ctx, const void* draft, csa2_dtype dt, const int64_t* pos, const int16_t* path,
+                             const int64_t* ctx_len, const int32_t* leaf, int B, int T, int c,
+                             void* swa, int64_t swa_cap, int64_t swa_pos0, int64_t* new_len, void* stream);
+
+/*
+ * Caches in pages.  Any number of pools [n_pages, page, row_bytes] (main rows, indexer keys, of
+ * any layers) share one state: table [B, max_pages] int32, the pages of every sequence in order
+ * (-1: none), and refs [n_pages] int32, how many places of all tables hold a page (0: it is
+ * free).  All calls are ordered by the stream; none needs the host to read anything, so they can
+ * be captured.  New pages are the lowest free ones, so results do not depend on timing.  Page ids
+ * outside [0, n_pages) other than -1 are skipped and flagged.
+ *
+ * csa2_pages_fork -- continuations that share their origin's pages:
+ *     table_out[i] = table[parent[i]], every page's refs up by its new places.
+ *   parent: [B_out] int32, negative = a row of -1; one >= B is flagged and gives -1.  table_out
+ *   [B_out, max_pages] is overwritten (free what it held first) and must not overlap table.
+ *
+ * csa2_pages_free -- gives back the pages behind the first keep[b] entries (keep NULL: all; a
+ * negative keep[b] leaves sequence b alone): refs down, table -1.  A page whose refs are 0
+ * already is flagged.
+ *
+ * csa2_pages_reserve -- makes entries first[b] .. first[b]+count[b]-1 of every sequence
+ * writable: of the pages they lie on, a missing one, or one whose refs are above 1 when the call
+ * starts, is replaced by a free page (the old one's refs down), in order of (b, page).
+ *   first, count : [B] int64 (first < 0 or count <= 0: nothing for this sequence)
+ *   granted      : [B] int64, how many of the entries can be written: count, or fewer when the
+ *                  pool ran out of pages or (flagged) the table's row is too short
+ *   copies       : [B, 2] int32 (from, to), or -1 -1: the beginning of a shared page whose older
+ *                  entries are to be copied, for csa2_page_copy on every pool before the next
+ *                  call that takes or writes pages
+ *   ws           : csa2_pages_reserve_workspace_bytes() bytes, 16-byte aligned
+ *
+ * csa2_pages_compact -- moves the n_used pages in use to the front of the pool: the i-th used
+ * page at or behind n_used goes to the i-th free one before it; tables and refs follow.
+ *   table  : [B, max_pages]: all the tables that hold pages of the pool, in one block
+ *   moves  : [n_pages / 2, 2] int32 (from, to), -1 -1 behind the last, for csa2_page_copy on
+ *            every pool;  n_used: [1] int64 or NULL
+ *   ws     : csa2_pages_compact_workspace_bytes() bytes, 16-byte aligned
+ *
+ * csa2_page_copy -- pool[to] = pool[from] for pairs [n, 2] int32 (a pair with a -1 is skipped).
+ * No page may be written twice, or be read and written, by one call.
+ *
+ * csa2_page_write -- rows[b, i] to entry first[b] + i, i < min(n, count[b]) (count: the granted
+ * numbers);  csa2_page_read -- dst[b, i] = entry idx[b, i] of sequence b (-1 leaves dst's row).
+ *   pool: [n_pages, page, row_bytes];  rows: [B, n, row_bytes];  idx: [B, keep];  dst:
+ *   [B, keep, row_bytes], neither overlapping pool.  row_bytes a multiple of 4, at most 2^20.
+ *   Entries on a missing page or behind the table's row are skipped and flagged.
+ *
+ * 1 <= page <= 65536, n_pages < 2^31, n_pages * page < 2^40, B <= 65535, max_pages < 2^31.
+ */
+csa2_status csa2_pages_fork(csa2_ctx* ctx, int32_t* refs, int64_t n_pages, const int32_t* table, int B, int max_pages,
+                            const int32_t* parent, int B_out, int32_t* table_out, void* stream);
+csa2_status csa2_pages_free(csa2_ctx* ctx, int32_t* refs, int64_t n_pages, int32_t* table, int B, int max_pages,
+                            int page, const int64_t* keep, void* stream);
+size_t csa2_pages_reserve_workspace_bytes(int64_t n_pages, int B, int max_pages);
+csa2_status csa2_pages_reserve(csa2_ctx* ctx, int32_t* refs, int64_t n_pages, int32_t* table, int B, int max_pages,
+                               int page, const int64_t* first, const int64_t* count, int64_t* granted, int32_t* copies,
+                               void* ws, size_t ws_bytes, void* stream);
+size_t csa2_pages_compact_workspace_bytes(int64_t n_pages);
+csa2_status csa2_pages_compact(csa2_ctx* ctx, int32_t* refs, int64_t n_pages, int32_t* table, int B, int max_pages,
+                               int32_t* moves, int64_t* n_used, void* ws, size_t ws_bytes, void* stream);
+csa2_status csa2_page_copy(csa2_ctx* ctx, void* pool, int64_t n_pages, int64_t page_bytes, const int32_t* pairs,
+                           int64_t n, void* stream);
+csa2_status csa2_page_write(csa2_ctx* ctx, void* pool, int64_t n_pages, int page, int64_t row_bytes,
+                            const int32_t* table, int B, int max_pages, const void* rows, int n,
+                            const int64_t* first, const int64_t* count, void* stream);
+csa2_status csa2_page_read(csa2_ctx* ctx, const void* pool, int64_t n_pages, int page, int64_t row_bytes,
+                           const int32_t* table, int B, int max_pages, const int32_t* idx, int keep, void* dst,
+                           void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,308 @@
+"""Caches in pages against the oracle's bookkeeping, bit for bit: shared pages, copy on write, pools that
+run out, compaction, and rows written and read through the table."""
+import numpy as np
+import pytest
+import torch
+
+from compressed_sparse_attention_06_gb300 import csa2 as C
+from compressed_sparse_attention_06_gb300 import pipeline as P
+from oracle import csa2_oracle_draft as D
+from tests.helpers import to_np
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def _i32(x):
+    return torch.as_tensor(np.ascontiguousarray(x), dtype=torch.int32, device=DEV)
+
+
+def _i64(x):
+    return torch.as_tensor(np.ascontiguousarray(x), dtype=torch.int64, device=DEV)
+
+
+def _state(o):
+    return _i32(o.refs), _i32(o.table)
+
+
+def _same(o, refs, table):
+    assert np.array_equal(to_np(refs), o.refs) and np.array_equal(to_np(table), o.table)
+
+
+def _random(seed, n_pages, B, P_, page, fill=0.6):
+    """A state with pages dealt out, some shared."""
+    rng = np.random.default_rng(seed)
+    o = D.Pages(np.zeros(n_pages, int), np.full((B, P_), -1), page)
+    for b in range(B):
+        for j in range(int(P_ * fill)):
+            u = rng.random()
+            if u < 0.2 and b > 0 and o.table[b - 1, j] >= 0:
+                t = o.table[b - 1, j]
+            elif u < 0.9 and (o.refs == 0).any():
+                t = rng.choice(np.flatnonzero(o.refs == 0))
+            else:
+                continue
+            o.table[b, j] = t
+            o.refs[t] += 1
+    return o, rng
+
+
+@pytest.mark.parametrize("n_pages,B,P_,page", [(1, 1, 1, 1), (40, 3, 7, 4), (300, 33, 40, 17), (5000, 2, 1200, 64), (9001, 300, 33, 16),
+                                               (200, 1, 150, 3)])
+def test_state_follows_the_oracle(n_pages, B, P_, page):
+    """Rounds of fork, reserve, free and compact on one state, the table of every sequence in one block."""
+    o, rng = _random(n_pages + B, n_pages, B, P_, page)
+    refs, table = _state(o)
+    for _ in range(4):
+        first = rng.integers(0, P_ * page + 1, B)
+        count = np.minimum(rng.integers(0, 4 * page + 2, B), P_ * page - first)
+        if rng.random() < 0.5:
+            first[rng.integers(0, B)] = -3
+        g, c = o.reserve(first, count)
+        granted, copies = C.csa2_pages_reserve(refs, table, _i64(first), _i64(count), page)
+        _same(o, refs, table)
+        assert np.array_equal(to_np(granted), g) and np.array_equal(to_np(copies), c)
+        parent = rng.integers(-1, B, 5)
+        out = o.fork(parent)
+        forked = C.csa2_pages_fork(refs, table, _i32(parent))
+        assert np.array_equal(to_np(forked), out)
+        _same(o, refs, table)
+        C.csa2_pages_free(refs, forked, page)
+        assert (forked == -1).all()
+        for t in out[out >= 0]:
+            o.refs[t] -= 1
+        keep = rng.integers(-1, P_ * page + 2, B)
+        o.free(keep)
+        C.csa2_pages_free(refs, table, page, _i64(keep))
+        _same(o, refs, table)
+        moves, cut = o.compact()
+        m, n_used = C.csa2_pages_compact(refs, table)
+        _same(o, refs, table)
+        assert np.array_equal(to_np(m), moves) and int(n_used) == cut
+    C.csa2_pages_free(refs, table, page)
+    C.csa2_ctx_check()
+    assert not refs.any() and (table == -1).all()
+
+
+def test_reserve_a_long_range_and_run_out():
+    """More words of pages than a pass of the block takes, and a pool that ends inside them."""
+    o = D.Pages(np.zeros(3500, int), np.full((3, 2000), -1), 2)
+    o.refs[::7] = 1                                       # held by somebody else's table
+    refs, table = _state(o)
+    first, count = np.array([5, 0, 3]), np.array([3990, 1, 3000])
+    g, c = o.reserve(first, count)
+    granted, copies = C.csa2_pages_reserve(refs, table, _i64(first), _i64(count), 2)
+    C.csa2_ctx_check()
+    _same(o, refs, table)
+    assert np.array_equal(to_np(granted), g) and np.array_equal(to_np(copies), c) and 0 < g[2] < 3000
+    again, none = C.csa2_pages_reserve(refs, table, _i64(first), _i64(g), 2)      # all of it is there
+    _same(o, refs, table)
+    assert np.array_equal(to_np(again), g) and (none == -1).all()
+
+
+def test_what_does_not_fit_is_flagged():
+    refs, table = _i32(np.zeros(4)), _i32(np.full((2, 3), -1))
+    granted, _ = C.csa2_pages_reserve(refs, table, _i64([5, 9]), _i64([3, 2 ** 62]), 2)
+    with pytest.raises(C.Csa2Error):
+        C.csa2_ctx_check()                                # the table's row ends at entry 6
+    assert granted.tolist() == [1, 0] and table.tolist() == [[-1, -1, 0], [-1, -1, -1]] and refs.tolist() == [1, 0, 0, 0]
+    for bad in (4, -2):
+        t = _i32([[bad, 0, -1], [-1, -1, -1]])
+        granted, copies = C.csa2_pages_reserve(refs, t, _i64([0, 0]), _i64([4, 2]), 2)
+        with pytest.raises(C.Csa2Error):
+            C.csa2_ctx_check()
+        assert granted.tolist() == [0, 2]                 # nothing of a sequence whose first page is none
+        C.csa2_pages_free(refs, t, 2, _i64([-1, 0]))
+        out = C.csa2_pages_fork(refs, t, _i32([0, 2]))
+        with pytest.raises(C.Csa2Error):
+            C.csa2_ctx_check()
+        assert out.tolist() == [[-1, 0, -1], [-1, -1, -1]] and refs.tolist() == [2, 0, 0, 0]
+        C.csa2_pages_free(refs, out, 2)
+        C.csa2_ctx_check()
+        C.csa2_pages_compact(refs, t)
+        with pytest.raises(C.Csa2Error):
+            C.csa2_ctx_check()
+        assert refs.tolist() == [1, 0, 0, 0]
+    t = _i32([[1, 0, -1]])                                # page 1 has no uses: its count stays at 0
+    C.csa2_pages_free(refs, t, 2)
+    with pytest.raises(C.Csa2Error):
+        C.csa2_ctx_check()
+    assert refs.tolist() == [0, 0, 0, 0] and (t == -1).all()
+
+
+@pytest.mark.parametrize("row", [((288,), torch.uint8), ((68,), torch.uint8), ((512,), torch.bfloat16), ((1,), torch.float32),
+                                 ((6, 50), torch.float32)])
+@pytest.mark.parametrize("page,B,n", [(1, 1, 1), (16, 5, 37), (17, 3, 300)])
+def test_rows_and_pages(row, page, B, n):
+    shape, dt = row
+    gen = torch.Generator(DEV).manual_seed(page + n)
+
+    def noise(*lead):
+        return torch.randint(0, 256, (*lead, *shape), generator=gen, device=DEV).to(dt)
+
+    cache = P.alloc_pages(B, (n // page + 3) * B + 2, page, n // page + 3, {"x": row}, DEV)
+    pool = cache.pools["x"].copy_(noise(*cache.pools["x"].shape[:2]))
+    first = torch.arange(B, device=DEV) % (page + 2)
+    count = torch.full((B,), n, device=DEV)
+    count[-1] = n // 2
+    rows, old = noise(B, n), pool.clone()
+    granted, _ = C.csa2_pages_reserve(cache.refs, cache.table, first, count, page)
+    C.csa2_page_write(pool, cache.table, rows, first, granted)
+    C.csa2_ctx_check()
+    assert torch.equal(granted, count)
+    o = D.Pages(to_np(cache.refs), to_np(cache.table), page)
+    want = old.clone()
+    for b in range(B):
+        for i in range(int(count[b])):
+            want[o.place(b, int(first[b]) + i)] = rows[b, i]
+    assert torch.equal(pool, want)                        # and nothing else of the pool
+    idx = torch.full((B, n + 2), -1, dtype=torch.int32, device=DEV)
+    for b in range(B):
+        idx[b, 1:1 + int(count[b])] = (first[b] + torch.randperm(int(count[b]), generator=gen, device=DEV)).int()
+    dst = noise(B, n + 2)
+    got = C.csa2_page_read(pool, cache.table, idx, out=dst.clone())
+    C.csa2_ctx_check()
+    for b in range(B):
+        live = idx[b] >= 0
+        assert torch.equal(got[b][live], rows[b][(idx[b][live] - first[b]).long()]) and torch.equal(got[b][~live], dst[b][~live])
+    pairs = _i32([[0, 1], [-1, -1], [-1, 0]])
+    before = pool.clone()
+    C.csa2_page_copy(pool, pairs)
+    C.csa2_ctx_check()
+    before[1] = before[0]
+    assert torch.equal(pool, before)
+
+
+def test_rows_that_have_no_page_are_flagged_and_left():
+    pool = torch.arange(4 * 2 * 4, device=DEV, dtype=torch.float32).view(4, 2, 4)
+    table, old = _i32([[2, -1], [7, 0]]), pool.clone()
+    out = torch.full((2, 5, 4), -7.0, device=DEV)
+    C.csa2_page_read(pool, table, _i32([[0, 1, 2, 4, -1], [0, 1, 2, -5, 3]]), out=out)
+    with pytest.raises(C.Csa2Error):
+        C.csa2_ctx_check()
+    assert torch.equal(out[0, :2], pool[2]) and torch.equal(out[1, 2], pool[0, 0]) and torch.equal(out[1, 4], pool[0, 1])
+    assert (out[0, 2:] == -7).all() and (out[1, [0, 1, 3]] == -7).all()
+    C.csa2_page_write(pool, table, torch.zeros(2, 3, 4, device=DEV), _i64([1, 4]), _i64([3, 1]))
+    with pytest.raises(C.Csa2Error):
+        C.csa2_ctx_check()
+    old[2, 1] = 0
+    assert torch.equal(pool, old)
+    C.csa2_page_write(pool, table, torch.ones(2, 3, 4, device=DEV), _i64([-1, 0]), _i64([2, -4]))
+    C.csa2_ctx_check()                                    # nothing to write is no error
+    assert torch.equal(pool, old)
+    for pair in ([4, 0], [0, 4], [-2, 0]):
+        C.csa2_page_copy(pool, _i32([pair]))
+        with pytest.raises(C.Csa2Error):
+            C.csa2_ctx_check()
+    assert torch.equal(pool, old)
+
+
+def test_long_pages_and_unaligned_pools():
+    """Pages of several chunks, and a pool at 4 bytes past a 16-byte boundary."""
+    flat = torch.arange(3 * 70000 * 4 + 1, device=DEV, dtype=torch.int32)
+    for pool in (flat[:-1].view(3, 70000, 4), flat[1:].view(3, 70000, 4)):
+        want = pool.clone()
+        want[2] = want[0]
+        C.csa2_page_copy(pool, _i32([[0, 2]]))
+        C.csa2_ctx_check()
+        assert torch.equal(pool, want)
+
+
+def test_forked_sequences_append_apart():
+    """Continuations of a prompt: entries that were there are shared, the ones appended are not, in every pool."""
+    gen = torch.Generator(DEV).manual_seed(9)
+    rows = {"kv": ((288,), torch.uint8), "ki": ((68,), torch.uint8)}
+
+    def noise(B, n):
+        return {k: torch.randint(0, 256, (B, n, *s), generator=gen, device=DEV, dtype=d) for k, (s, d) in rows.items()}
+
+    base = P.alloc_pages(2, 64, 8, 20, rows, DEV)
+    first = noise(2, 43)
+    P.pages_append(base, first, _i64([43, 30]))
+    beams = P.pages_fork(base, _i32([0, 0, 1, -1, 0]))
+    used = int((base.refs > 0).sum())
+    assert used == 6 + 4 and beams.n_entries.tolist() == [43, 43, 30, 0, 43]
+    more = noise(5, 10)
+    granted = P.pages_append(beams, more, _i64([10, 1, 0, 10, 6]))
+    C.csa2_ctx_check()
+    assert granted.tolist() == [10, 1, 0, 10, 6] and beams.n_entries.tolist() == [53, 44, 30, 10, 49]
+    want = {k: [torch.cat([first[k][p, :n], more[k][i, :m]]) for i, (p, n, m) in
+                enumerate([(0, 43, 10), (0, 43, 1), (1, 30, 0), (0, 0, 10), (0, 43, 6)])] for k in rows}
+
+    def check(cache, want):
+        for k, seqs in want.items():
+            for b, w in enumerate(seqs):
+                idx = torch.full((cache.table.shape[0], len(w)), -1, dtype=torch.int32, device=DEV)
+                idx[b] = torch.arange(len(w), device=DEV)
+                assert torch.equal(C.csa2_page_read(cache.pools[k], cache.table, idx)[b], w)
+
+    check(beams, want)
+    check(base, {k: [first[k][0, :43], first[k][1, :30]] for k in rows})
+    P.pages_cut(base)                                     # the prompts end, their continuations stay
+    P.pages_cut(beams, _i64([53, 0, -1, 4, 17]))
+    assert beams.n_entries.tolist() == [53, 0, 30, 4, 17]
+    n_used = P.pages_compact(beams)
+    C.csa2_ctx_check()
+    assert int(n_used) == int((beams.refs > 0).sum()) and int(beams.table.max()) == int(n_used) - 1
+    check(beams, {k: [want[k][0], want[k][1][:0], want[k][2], want[k][3][:4], want[k][4][:17]] for k in rows})
+
+
+def test_captured_step_of_a_branch():
+    """Fork, reserve, copy and write recorded once and replayed: the state moves on as by eager calls."""
+    gen = torch.Generator(DEV).manual_seed(11)
+    cache = P.alloc_pages(2, 40, 4, 8, {"x": ((16,), torch.float32)}, DEV)
+    P.pages_append(cache, {"x": torch.rand(2, 9, 16, generator=gen, device=DEV)}, _i64([9, 6]))
+    pool, parent, rows = cache.pools["x"], _i32([0, 1, 1]), torch.rand(3, 5, 16, generator=gen, device=DEV)
+    first, count = cache.n_entries[parent.long()].contiguous(), _i64([5, 1, 5])
+    work, granted, copies = torch.full_like(cache.table[:1].expand(3, -1), -1), _i64([0] * 3), _i32(np.zeros((3, 2)))
+    work = work.contiguous()
+    ws = torch.empty(C.load().csa2_pages_reserve_workspace_bytes(40, 3, 8), dtype=torch.uint8, device=DEV)
+
+    def step():
+        C.csa2_pages_free(cache.refs, work, 4)
+        C.csa2_pages_fork(cache.refs, cache.table, parent, out=work)
+        C.csa2_pages_reserve(cache.refs, work, first, count, 4, granted=granted, copies=copies, ws=ws)
+        C.csa2_page_copy(pool, copies)
+        C.csa2_page_write(pool, work, rows, first, granted)
+
+    step()
+    want = [x.clone() for x in (cache.refs, work, granted, copies, pool)]
+    graph = torch.cuda.CUDAGraph()
+    check, C._check = C._check, lambda fn, st: None if st == C.OK else pytest.fail(fn)
+    try:
+        with torch.cuda.graph(graph):
+            step()
+    finally:
+        C._check = check
+    rows.mul_(2.0)
+    for _ in range(3):
+        graph.replay()
+    C.csa2_ctx_check()
+    for x, w in zip((cache.refs, work, granted, copies), want):
+        assert torch.equal(x, w)
+    idx = torch.arange(14, dtype=torch.int32, device=DEV).expand(3, 14)
+    idx = torch.where(idx < (first + count).unsqueeze(-1), idx, -1).to(torch.int32).contiguous()
+    got = C.csa2_page_read(pool, work, idx)
+    for i in range(3):
+        f, n = int(first[i]), int(count[i])
+        assert torch.equal(got[i, f:f + n], rows[i, :n])
+
+
+def test_empty_calls():
+    none = torch.zeros(0, dtype=torch.int32, device=DEV)
+    t0 = torch.zeros(0, 4, dtype=torch.int32, device=DEV)
+    C.csa2_pages_free(none, t0, 4)
+    m, n = C.csa2_pages_compact(none, t0)
+    assert m.shape == (0, 2) and int(n) == 0
+    refs, t = _i32(np.zeros(3)), _i32(np.zeros((2, 0)))
+    assert C.csa2_pages_fork(refs, t, _i32([0])).shape == (1, 0)
+    granted, copies = C.csa2_pages_reserve(refs, t, _i64([0, 0]), _i64([0, 1]), 4)
+    with pytest.raises(C.Csa2Error):
+        C.csa2_ctx_check()
+    assert granted.tolist() == [0, 0] and (copies == -1).all()
+    granted, _ = C.csa2_pages_reserve(none, _i32([[-1, -1]]), _i64([0]), _i64([2]), 4)
+    C.csa2_ctx_check()
+    assert granted.tolist() == [0]
+    C.csa2_page_write(torch.zeros(3, 4, 5, device=DEV), t, torch.zeros(2, 0, 5, device=DEV), _i64([0, 0]), _i64([0, 0]))
+    C.csa2_page_copy(torch.zeros(3, 4, 5, device=DEV), _i32(np.zeros((0, 2))))
+    C.csa2_ctx_check()
