@@ -11,10 +11,10 @@
 // The softmax is online over chunks of 32 rows; few nodes split their rows over several CTAs,
 // joined by log-sum-exp.
 #include <algorithm>
-#include <atomic>
 
 #include "csa2_internal.cuh"
 #include "tree.cuh"
+#include "tree_tc.cuh"
 
 namespace {
 
@@ -386,7 +386,8 @@ extern "C" csa2_status csa2_tree_commit(csa2_ctx* ctx, const void* draft, csa2_d
 
 extern "C" size_t csa2_tree_attn_workspace_bytes(csa2_ctx* ctx, csa2_dtype q_dt, csa2_dtype kv_dt, csa2_dtype swa_dt, int B,
                                                  int T, int H, int k, int window, int dense, unsigned flags) {
-    if (!ctx || B <= 0 || T <= 0 || H <= 0 || k < 0 || window < 0) return 0;
+    if (!ctx || B <= 0 || T <= 0 || H <= 0 || H > 128 || k < 0 || window < 0) return 0;
+    if (tree_tc_applies(q_dt, kv_dt, swa_dt, flags)) return tree_tc_ws_bytes(ctx, B, T, H, k, window, dense != 0);
     return simt_ws(ctx, (int64_t)B * T, H, (int64_t)k + window);
 }
 
@@ -439,6 +440,7 @@ extern "C" csa2_status csa2_tree_attn(csa2_ctx* ctx, const void* q, csa2_dtype q
     t.out = out;
     t.out_dt = out_dt;
     t.lse = lse;
+    if (tree_tc_applies(q_dt, kv_dt, swa_dt, flags)) return tree_tc_run(ctx, t, ws, s);
     a.part = reinterpret_cast<float*>(ws);
     a.st = ctx->status;
     simt_splits(ctx, (int64_t)B * T, H, (int64_t)k + window, a.n_split, a.spl);
