@@ -95,37 +95,22 @@ __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
     return r;
 }
+// An arrival at a barrier of the peer's that says "read": the values read are in registers, and
+// nothing this thread wrote is behind it, so it carries no fence (a release at the cluster's scope
+// waits for every access of the thread, microseconds a tile).
 __device__ __forceinline__ void peer_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void peer_st4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+// Stores into the peer's shared memory that count their bytes at one of its barriers.
+__device__ __forceinline__ void peer_st4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+                 "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
+                 : "memory");
 }
-__device__ __forceinline__ void peer_st(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-// mbar_wait for a barrier that the peer's threads arrive at: acquires at the cluster's scope.
-__device__ __forceinline__ bool peer_try(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool peer_wait(uint64_t* bar, uint32_t parity, long long budget, unsigned* st) {
-    if (peer_try(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!peer_try(bar, parity)) {
-        if (clock64() - t0 > budget) {
-            csa2_flag(st, CSA2_DEVBIT_TIMEOUT);
-            return false;
-        }
-    }
-    return true;
+__device__ __forceinline__ void peer_st(uint32_t addr, float v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
+                 "r"(__float_as_uint(v)), "r"(bar)
+                 : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -517,7 +502,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1) tree_
             for (int tt = 0; tt < it.nt; ++tt, ++g) {
                 bool wt = mbar_wait(&sfull[g & 1], (g >> 1) & 1, a.budget, a.st) &&
                           mbar_wait(&rfull[g & 1], (g >> 1) & 1, a.budget, a.st) &&
-                          (g == 0 || peer_wait(&xempty[w], (g - 1) & 1, a.budget, a.st));
+                          (g == 0 || !live || mbar_wait(&xempty[w], (g - 1) & 1, a.budget, a.st));
                 if (!__all_sync(FULL, wt)) {
                     ok = false;
                     break;
@@ -542,11 +527,13 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1) tree_
                     }
 #pragma unroll
                     for (int u = 0; u < 8; ++u)
-                        peer_st4(theirs + u * TT_ROWS * 16, y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
+                        peer_st4(theirs + u * TT_ROWS * 16, y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3], their_full);
                 }
-                __syncwarp();
-                if (lane == 0) peer_arrive(their_full);
-                wt = peer_wait(&xfull[w], g & 1, a.budget, a.st);
+                if (live) {
+                    // (a warp without rows must not: it could fall two phases behind its peer)
+                    if (lane == 0) mbar_arrive_expect_tx(&xfull[w], 32 * 8 * 16);
+                    wt = mbar_wait(&xfull[w], g & 1, a.budget, a.st);
+                }
                 if (!__all_sync(FULL, wt)) {
                     ok = false;
                     break;
@@ -587,7 +574,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1) tree_
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&pfull[g & 1]);
-                    peer_arrive(their_empty);
+                    if (live) peer_arrive(their_empty);
                     peer_arrive(their_done + 8 * (g & 1));
                 }
             }
@@ -741,7 +728,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1) tree_
         float ss_prev = 0.0f;                                 // lane j < 16: this CTA's squares of row j, tile g - 1
         // RMS factors of tile t from both halves' squares
         const auto factors = [&](int t) {
-            const bool wt = peer_wait(&ssfull[8 * (t & 1) + lw], (t >> 1) & 1, a.budget, a.st);
+            const bool wt = mbar_wait(&ssfull[8 * (t & 1) + lw], (t >> 1) & 1, a.budget, a.st);
             if (!__all_sync(FULL, wt)) return false;
             if (lane < 16) {
                 float* p = sSS + (t & 1) * TT_TILE + 16 * lw + lane;
@@ -790,7 +777,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1) tree_
             if (ok && g >= 2) {
                 // (the peer's softmax reads the factors that this tile's squares will replace)
                 const bool wt = mbar_wait(&kempty[g & 1], ((g - 2) >> 1) & 1, a.budget, a.st) &&
-                                peer_wait(&xdone[g & 1], ((g - 2) >> 1) & 1, a.budget, a.st);
+                                mbar_wait(&xdone[g & 1], ((g - 2) >> 1) & 1, a.budget, a.st);
                 ok = __all_sync(FULL, wt);
             }
             if (!ok) break;
@@ -860,12 +847,13 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1) tree_
                 }
             }
             if (lane < (DENSE ? gv : 1)) sMask[((g & 1) * TT_G + lane) * 8 + lw] = (uint16_t)my_bits;
-            if (lane < 16) peer_st(their_ss + ((g & 1) * TT_TILE + 16 * lw + lane) * 4, ss_prev);
+            if (lane < 16)
+                peer_st(their_ss + ((g & 1) * TT_TILE + 16 * lw + lane) * 4, ss_prev, their_bar + (8 * (g & 1) + lw) * 8);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&kfull[g & 1]);
-                peer_arrive(their_bar + (8 * (g & 1) + lw) * 8);
+                mbar_arrive_expect_tx(&ssfull[8 * (g & 1) + lw], 16 * 4);
             }
             ++g;
         }
@@ -1082,7 +1070,8 @@ csa2_status tree_tc_run(csa2_ctx* ctx, const TreeCall& c, void* ws, cudaStream_t
     a.budget = TT_BUDGET;
     if (ctx->stall_next) {
         a.stall = 1;
-        if (ctx->stall_budget > 0) a.budget = ctx->stall_budget;
+        // (long enough for every store between the CTAs to land before one of them gives up)
+        if (ctx->stall_budget > 0) a.budget = std::max<long long>(ctx->stall_budget, 1 << 17);
         ctx->stall_next = 0;
     }
     if (fp4) st = dense ? launch_tt<true, true>(ctx, a, s) : launch_tt<true, false>(ctx, a, s);
