@@ -408,7 +408,8 @@ extern "C" csa2_status csa2_tree_attn(csa2_ctx* ctx, const void* q, csa2_dtype q
     if ((q_dt != CSA2_F32 && q_dt != CSA2_BF16) || (out_dt != CSA2_F32 && out_dt != CSA2_BF16) ||
         (swa_dt != CSA2_F32 && swa_dt != CSA2_BF16) || (kv_dt != CSA2_F32 && kv_dt != CSA2_BF16 && kv_dt != CSA2_FP4_E4M3x16))
         return CSA2_ERR_UNSUPPORTED;
-    if ((int64_t)B * T > 65535 || N >= (1ll << 40)) return CSA2_ERR_UNSUPPORTED;
+    if ((int64_t)B * T > 65535 || N > 0x7FFFFFFF || (!table && B * N > 0x7FFFFFFF) || swa_cap < 0 || B * swa_cap > 0x7FFFFFFF)
+        return CSA2_ERR_UNSUPPORTED;
     if (B == 0) return CSA2_OK;
     if (!q || !pos || !path || !ctx_len || !out) return CSA2_ERR_INVALID_ARG;
     if (k > 0 && ((!idx && !n_visible) || (N > 0 && !kv))) return CSA2_ERR_INVALID_ARG;

@@ -667,7 +667,8 @@ csa2_status csa2_cache_gather(csa2_ctx* ctx, const void* src, int64_t row_bytes,
  *               is none are skipped and flagged
  *   swa       : [B, swa_cap, c], draft: [B, T, c], both in swa_dt (F32 or BF16); window <= swa_cap
  *   pos, path, ctx_len: csa2_tree_plan's
- * c == 512, 1 <= H <= 128, k <= 2048 (dense: 4,194,304), window <= 1024, T <= 256, B*T <= 65535.
+ * c == 512, 1 <= H <= 128, k <= 2048 (dense: 4,194,304), window <= 1024, T <= 256, B*T <= 65535;
+ * the rows of kv and of swa number below 2^31.
  * BF16 query, window and drafts over BF16 or FP4 rows with both norms run on the tensor cores
  * (q^ and p rounded to bf16, sums fp32), all other calls in fp32.
  * Workspace: csa2_tree_attn_workspace_bytes() bytes, 16-byte aligned; with fewer the call
