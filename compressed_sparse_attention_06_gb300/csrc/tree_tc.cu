@@ -16,16 +16,18 @@
 // 4 million of them stay below 2^55), and the splits of a group's slots simply add up.
 //
 // tree_prep_kernel runs first: q^ (normalised, rotated) as the swizzled image of the A operand, the
-// RoPE table, the row of every slot (-1: none) and, as bits, which nodes attend to it.
+// RoPE table, and for every slot its row (-1: none), f, and as bits which nodes attend to it.  (A row's
+// squares need all of its dims, of which a CTA has half: with the sums exchanged like the logits, and
+// the rows through registers for them, the loaders were what a tile waited for.)
 //
-// Warps (896 threads, one CTA an SM; the first four give registers to the softmax):
+// Warps (640 threads, one CTA an SM):
 //   0       query images (bulk copies)
 //   1       issues the MMAs; owns tensor memory (O: columns 0-255, S / P': two buffers of 128)
-//   2       the tiles' masks
+//   2       the tiles' masks and factors
 //   4-11    softmax, two warps a lane quarter (64 slots each), and the output, a row a thread
-//   12-27   loaders, 8 rows of the tile each: rows through registers, a tile ahead, into the swizzled
-//           tile (two of them); FP4 rows are dequantised exactly.  The squares of the rows' halves,
-//           which the CTAs exchange, give the factors f.
+//   12-19   loaders, four warps for the even and four for the odd tiles, 32 rows each: bf16 rows by
+//           16-byte asynchronous copies into the swizzled tile, FP4 rows dequantised (exactly) from
+//           registers that are filled a tile ahead
 // Every wait is bounded; the CTAs meet at the cluster's barrier before either one exits.
 #include <algorithm>
 #include <type_traits>
@@ -42,10 +44,7 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int TT_C = 512, TT_HALF = 256;
 constexpr int TT_ROWS = 128, TT_TILE = 128;
 constexpr int TT_G = 8;                          // nodes of a group at most
-constexpr int TT_LOADERS = 16;                   // warps
-constexpr int TT_THREADS = 32 * (12 + TT_LOADERS);
-constexpr int TT_REGS = 72, TT_REGS_FEW = 32, TT_REGS_SOFT = 88;     // a thread: at launch (loaders), first four warps, softmax
-static_assert(TT_REGS_FEW + 2 * TT_REGS_SOFT + TT_LOADERS / 4 * TT_REGS <= TT_THREADS / 128 * TT_REGS, "what the launch gives");
+constexpr int TT_THREADS = 640;
 constexpr int TT_CHUNK = TT_TILE * 128;          // 16 KB: 128 rows x 64 dims
 constexpr int TT_TILE_BYTES = 4 * TT_CHUNK;
 constexpr float LOG2E = 1.4426950408889634f;
@@ -55,11 +54,11 @@ constexpr long long TT_BUDGET = 1ll << 31;
 constexpr int OFF_Q = 0;
 constexpr int OFF_K = 65536;
 constexpr int OFF_X = OFF_K + 2 * TT_TILE_BYTES;         // the peer's logits: [2 halves][8 units][128 rows] x 16 B
-constexpr int OFF_F = OFF_X + 32768;                     // [2][128] the peer's squares, then the factors f
+constexpr int OFF_F = OFF_X + 32768;                     // [2][128] the factors f
 constexpr int OFF_L = OFF_F + 1024;                      // [2][128] sums of exponentials
 constexpr int OFF_MASK = OFF_L + 1024;                   // [2][TT_G][4] x 32 bits
 constexpr int OFF_BAR = OFF_MASK + 2 * TT_G * 16;
-constexpr int N_BAR = 18 + 2 * TT_LOADERS + 8 + 8;
+constexpr int N_BAR = 16 + 8 + 8;
 constexpr int OFF_TMEM = OFF_BAR + N_BAR * 8;
 constexpr int TT_SMEM = OFF_TMEM + 16;
 static_assert(TT_SMEM <= 227 * 1024, "shared memory");
@@ -68,10 +67,12 @@ static_assert(TT_SMEM <= 227 * 1024, "shared memory");
 struct TtLists {
     uint8_t* qimg;                // [groups][2 halves][4 chunks][R8 rows x 128 B]
     int32_t* erow;                // [eg][lde] rows of the entry slots (eg: nodes; dense: sequences)
+    float* ef;                    // [eg][lde] their factors f
     uint32_t* eok;                // [eg][lde / 32] which of them there are
     int32_t* wrow;                // [groups][ldw] rows of the window slots: the ring's, then drafts
+    float* wf;                    // [groups][ldw]
     uint32_t* wmask;              // [groups][ldw / 32][TT_G] who attends to them
-    int4* info;                   // [groups] entry slots (a multiple of 32), all, the ring's (multiples of 4)
+    int4* info;                   // [groups] entry slots (a multiple of 32), all, the ring's
     float* rope_cs;               // [B*T, 64] cos, sin of the 32 angles
     int lde, ldw;
     int H, G, R8, gps;            // heads, nodes of a group, image rows, groups of a sequence
@@ -122,11 +123,7 @@ __device__ __forceinline__ void peer_st4(uint32_t addr, uint32_t a, uint32_t b, 
                  "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ void peer_st(uint32_t addr, float v, uint32_t bar) {
-    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
-                 "r"(__float_as_uint(v)), "r"(bar)
-                 : "memory");
-}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -207,55 +204,100 @@ struct PrepArgs {
     TtLists l;
     TreeRows r;
     const __nv_bfloat16* q;
-    int B, eblocks;
+    const uint8_t* kv;
+    const uint8_t* swa;
+    const uint8_t* draft;
+    int fp4;
+    int64_t q_blocks, w_blocks;   // blocks of query rows, of window slots (the rest: entry slots)
+    int wb, eb;                   // blocks of a group's window slots, of a list of entry slots
     RopeTable rope;
     unsigned flags;
     unsigned* st;
 };
 
-// Rows and bits of `n` entry slots of list `eg` from slot s0 on, a slot a thread: slot s is entry
-// idx[s] (idx NULL: s), of which `live` are wanted.
-__device__ __forceinline__ void prep_entries(const PrepArgs& a, int64_t b, int64_t eg, const int32_t* idx, int live, int n,
-                                             int first, int step) {
-    for (int s = first; s < n; s += step) {
-        const int64_t row = s < live ? tree_entry_row(a.r, b, idx ? idx[s] : s, a.st, true) : -1;
-        a.l.erow[eg * a.l.lde + s] = (int32_t)row;
-        const uint32_t bits = __ballot_sync(FULL, row >= 0);
-        if ((threadIdx.x & 31) == 0) a.l.eok[eg * (a.l.lde / 32) + s / 32] = bits;
+// The squares of a lane's 16 values of a bf16 or an FP4 row.
+__device__ __forceinline__ float lane_squares_bf16(const uint8_t* row, int lane) {
+    const uint4* p = reinterpret_cast<const uint4*>(row) + 2 * lane;
+    const uint4 u[2] = {__ldg(p), __ldg(p + 1)};
+    float q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xFFFF0000u);
+            q = fmaf(lo, lo, fmaf(hi, hi, q));
+        }
+    }
+    return q;
+}
+__device__ __forceinline__ float lane_squares_fp4(const uint8_t* row, int lane) {
+    // 16 codes and their scale a lane; 4 x code^2 by table, summed as bytes
+    const uint2 c = __ldg(reinterpret_cast<const uint2*>(row) + lane);
+    const float s = e4m3_to_f32(__ldg(row + TT_C / 2 + lane));
+    uint32_t q = 0;
+    const uint32_t w[4] = {c.x & 0x77777777u, (c.x >> 16) & 0x7777u, c.y & 0x77777777u, (c.y >> 16) & 0x7777u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q = __dp4a(__byte_perm(0x09040100u, 0x90402410u, w[i]), 0x01010101u, q);
+    return (float)q * 0.25f * (s * s);
+}
+
+// 128 slots of a list: rows[s] (>= 0: real) become addresses by `address`; their factors f and rows go to
+// the list from slot s0 on (n of them).  A row with an infinity or a NaN keeps out of the products (0 x NaN
+// would reach the nodes that do not attend to it): its row is none, and its factor, NaN, is for those that
+// do.  Warp w has slots 16 w .. 16 w + 15, four rows in flight.
+template <typename Address>
+__device__ __forceinline__ void prep_factors(const int32_t* rows, int s0, int n, int32_t* out_row, float* out_f, bool fp4,
+                                             const Address& address) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = 16 * warp, mine = lane < 16 && s0 + b + lane < n ? rows[b + lane] : -1;
+    float sum = 0.0f;
+    for (int i = 0; i < 16 && s0 + b + i < n; i += 4) {
+        float q[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int row = __shfl_sync(FULL, mine, i + j);
+            q[j] = 0.0f;
+            if (row >= 0) {
+                const uint8_t* p = address(s0 + b + i + j, row);
+                q[j] = fp4 ? lane_squares_fp4(p, lane) : lane_squares_bf16(p, lane);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float t = warp_sum(q[j]);
+            if (lane == i + j) sum = t;
+        }
+    }
+    if (lane < 16 && s0 + b + lane < n) {
+        const bool fin = sum < INFINITY;
+        out_row[s0 + b + lane] = fin ? mine : -1;
+        out_f[s0 + b + lane] = mine < 0 ? 0.0f
+                               : fin   ? (LOG2E / sqrtf((float)TT_C)) / sqrtf(sum / (float)TT_C + 1e-6f)
+                                       : __int_as_float(0x7FC00000);
     }
 }
 
-// Block (group, y): y < R8 / 8 normalises and rotates 8 query rows, a warp each; y = R8 / 8 lists the
-// group's window slots (sparse form: and the node's entries); in the dense form the blocks behind
-// list the entries of sequence x.
+// A block: 8 query rows (a warp each), or 128 slots of a group's window, or 128 entry slots of a node
+// (dense: of a sequence).
 __global__ void __launch_bounds__(256) tree_prep_kernel(const PrepArgs a) {
     pdl_wait();
     pdl_trigger();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, T = a.r.T, y0 = a.l.R8 / 8;
-    if ((int)blockIdx.y > y0) {
-        const int64_t b = blockIdx.x;
-        if (b >= a.B) return;
-        __shared__ int most;
-        if (threadIdx.x == 0) most = 0;
-        __syncthreads();
-        int nv = 0;
-        for (int i = threadIdx.x; i < T; i += blockDim.x)
-            if (a.r.pos[b * T + i] >= 0) nv = max(nv, (int)max((int64_t)0, min((int64_t)a.r.k, a.r.n_visible[b * T + i])));
-        atomicMax(&most, nv);
-        __syncthreads();
-        prep_entries(a, b, b, nullptr, most, (most + 31) / 32 * 32, (blockIdx.y - y0 - 1) * blockDim.x + threadIdx.x,
-                     a.eblocks * blockDim.x);
-        return;
-    }
-    const int v = blockIdx.x, b = v / a.l.gps, n0 = (v - b * a.l.gps) * a.l.G, gv = min(a.l.G, T - n0);
-    const int64_t bt0 = (int64_t)b * T + n0;
-    if ((int)blockIdx.y < y0) {
-        const int row = 8 * blockIdx.y + warp, g = row / a.l.H, h = row - g * a.l.H;
+    __shared__ int32_t rows[128];
+    __shared__ int64_t t[TT_G];
+    __shared__ int most;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, T = a.r.T;
+    const bool dense = a.r.n_visible;
+    int64_t blk = blockIdx.x;
+    if (blk < a.q_blocks) {
+        const int v = (int)(blk / (a.l.R8 / 8)), b = v / a.l.gps, n0 = (v - b * a.l.gps) * a.l.G, gv = min(a.l.G, T - n0);
+        const int64_t bt0 = (int64_t)b * T + n0;
+        const int row = 8 * (int)(blk - (int64_t)v * (a.l.R8 / 8)) + warp, g = row / a.l.H, h = row - g * a.l.H;
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = 0.0f;
         if (g < gv) {
-            const int64_t t = a.r.pos[bt0 + g];
+            const int64_t pos = a.r.pos[bt0 + g];
             const uint4* p = reinterpret_cast<const uint4*>(a.q + ((bt0 + g) * a.l.H + h) * (int64_t)TT_C + 16 * lane);
             float ss = 0.0f;
 #pragma unroll
@@ -276,7 +318,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const PrepArgs a) {
             if (a.flags & CSA2_ROPE) {
                 // lane j has angle j; lanes 28 .. 31 rotate the pairs of dims 448 .. 511
                 float c, s;
-                rope_cos_sin(a.rope, t, lane, c, s);
+                rope_cos_sin(a.rope, pos, lane, c, s);
                 if (h == 0) {
                     a.l.rope_cs[(bt0 + g) * 64 + lane] = c;
                     a.l.rope_cs[(bt0 + g) * 64 + 32 + lane] = s;
@@ -302,40 +344,70 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const PrepArgs a) {
         *reinterpret_cast<uint4*>(img + sw128_offset(row, u + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
         return;
     }
-    __shared__ int64_t t[TT_G];
-    __shared__ int nv[TT_G];
-    if (threadIdx.x < TT_G) {
-        const TreeNode n = tree_node(a.r, bt0 + min((int)threadIdx.x, gv - 1));
-        t[threadIdx.x] = (int)threadIdx.x < gv ? n.t : -1;
-        nv[threadIdx.x] = n.kq;
+    blk -= a.q_blocks;
+    if (blk >= a.w_blocks) {
+        // entries: those the node selected, or those that any node of the sequence sees
+        blk -= a.w_blocks;
+        const int64_t eg = blk / a.eb, b = dense ? eg : eg / T;
+        const int s0 = (int)(blk - eg * a.eb) * 128, s = s0 + threadIdx.x;
+        int live = 0;
+        if (dense) {
+            if (threadIdx.x == 0) most = 0;
+            __syncthreads();
+            for (int i = threadIdx.x; i < T; i += blockDim.x) live = max(live, tree_node(a.r, b * T + i).kq);
+            atomicMax(&most, live);
+            __syncthreads();
+            live = most;
+        } else {
+            live = tree_node(a.r, eg).kq;
+        }
+        const int n = (live + 31) / 32 * 32;
+        if (s0 >= n) return;
+        if (threadIdx.x < 128) {
+            const int64_t row = s < live ? tree_entry_row(a.r, b, dense ? s : a.r.idx[eg * a.r.k + s], a.st, true) : -1;
+            rows[threadIdx.x] = (int32_t)row;
+            const uint32_t bits = __ballot_sync(FULL, row >= 0);
+            if (lane == 0 && s < n) a.l.eok[eg * (a.l.lde / 32) + s / 32] = bits;
+        }
+        __syncthreads();
+        const int64_t bytes = a.fp4 ? fp4_row_bytes(TT_C) : TT_C * 2;
+        prep_factors(rows, s0, n, a.l.erow + eg * a.l.lde, a.l.ef + eg * a.l.lde, a.fp4,
+                     [&](int, int32_t row) { return a.kv + row * bytes; });
+        return;
     }
-    __syncthreads();
+    // the window: the ring's rows that any node sees, then the drafts: those of the node's path, or of all
+    // nodes up to the group's last one
+    const int v = (int)(blk / a.wb), b = v / a.l.gps, n0 = (v - b * a.l.gps) * a.l.G, gv = min(a.l.G, T - n0);
+    const int64_t bt0 = (int64_t)b * T + n0;
+    const int s0 = (int)(blk - (int64_t)v * a.wb) * 128, s = s0 + threadIdx.x;
     int kq = 0;
     int64_t tmin = INT64_MAX;
     for (int g = 0; g < gv; ++g) {
-        kq = max(kq, nv[g]);
-        if (t[g] >= 0) tmin = min(tmin, t[g]);
+        const TreeNode n = tree_node(a.r, bt0 + g);
+        if (threadIdx.x == 0) t[g] = n.t;
+        kq = max(kq, n.kq);
+        if (n.t >= 0) tmin = min(tmin, n.t);
     }
-    const int kq32 = (kq + 31) / 32 * 32;
-    if (!a.r.n_visible && kq > 0) prep_entries(a, b, bt0, a.r.idx + bt0 * a.r.k, kq, kq32, threadIdx.x, blockDim.x);
-    // the window: the ring's rows that any node sees (padded to a multiple of 4), then the drafts:
-    // those of the node's path, or of all nodes up to the group's last one
-    const bool dense = a.r.n_visible, any = a.r.window > 0 && tmin != INT64_MAX;
+    const bool any = a.r.window > 0 && tmin != INT64_MAX;
     const int64_t len = a.r.ctx_len[b], W = a.r.window;
     const int64_t p0 = any ? max((int64_t)0, dense ? max(len - W + 1, tmin - W + 1) : tmin - W + 1) : 0;
-    const int nring = any ? (int)max((int64_t)0, min(W, min(len, tmin + 1) - p0)) : 0, ring4 = (nring + 3) / 4 * 4;
+    const int nring = any ? (int)max((int64_t)0, min(W, min(len, tmin + 1) - p0)) : 0;
     const int ndraft = !any ? 0 : (dense ? n0 + gv : (int)max((int64_t)0, min(W, tmin + 1 - max(len, p0))));
-    const int slots = ring4 + (ndraft + 3) / 4 * 4;
-    int32_t* list = a.l.wrow + v * (int64_t)a.l.ldw;
-    uint32_t* mask = a.l.wmask + v * (int64_t)(a.l.ldw / 32) * TT_G;
-    for (int s0 = 0; s0 < slots; s0 += blockDim.x) {
-        const int s = s0 + threadIdx.x, d = s - ring4;
+    const int slots = nring + ndraft;
+    if (s0 == 0 && threadIdx.x == 0) {
+        const int kq32 = (kq + 31) / 32 * 32;
+        a.l.info[v] = make_int4(kq32, kq32 + slots, nring, 0);
+    }
+    if (s0 >= slots) return;
+    __syncthreads();
+    if (threadIdx.x < 128) {
+        const int d = s - nring;
         int64_t p = -1, row = -1;                // position of the slot, its row
         int j = -1;                              // draft node
         if (s < nring) {
             p = p0 + s;
             row = b * a.r.swa_cap + ((p - a.r.swa_pos0) % a.r.swa_cap + a.r.swa_cap) % a.r.swa_cap;
-        } else if (d >= 0 && d < ndraft) {
+        } else if (d < ndraft) {
             if (dense) {
                 j = d;
                 p = a.r.pos[(int64_t)b * T + j];
@@ -348,25 +420,27 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const PrepArgs a) {
             }
             if (j >= 0) row = (int64_t)b * T + j;
         }
+        uint32_t* mask = a.l.wmask + (v * (int64_t)(a.l.ldw / 32) + s / 32) * TT_G;
         bool wanted = false;
         for (int g = 0; g < gv; ++g) {
             bool on = row >= 0 && t[g] >= 0 && p <= t[g] && p > t[g] - W;
             if (on && j >= 0) on = a.r.path[(bt0 + g) * T + (p - len)] == j;
             const uint32_t bits = __ballot_sync(FULL, on);
-            if (lane == 0 && s < slots) mask[(s / 32) * TT_G + g] = bits;
+            if (lane == 0 && s < slots) mask[g] = bits;
             wanted |= on;
         }
-        if (s < slots) list[s] = wanted ? (int32_t)row : -1;
+        rows[threadIdx.x] = wanted ? (int32_t)row : -1;
     }
-    if (threadIdx.x == 0) a.l.info[v] = make_int4(kq32, kq32 + slots, ring4, 0);
+    __syncthreads();
+    prep_factors(rows, s0, slots, a.l.wrow + v * (int64_t)a.l.ldw, a.l.wf + v * (int64_t)a.l.ldw, false,
+                 [&](int slot, int32_t row) { return (slot < nring ? a.swa : a.draft) + row * (int64_t)(TT_C * 2); });
 }
 
 // ---------------------------------------------------------------- the main kernel
 
-// Eight E2M1 codes (value 2k in the low nibble of byte k) times their scale as bf16 pairs; q += the
-// codes' squares.  Exact: a product has 6 significant bits, and the squares (multiples of 1/4 up to 36)
-// of 8 values in each half of q sum up in fp16 without rounding.
-__device__ __forceinline__ uint4 fp4_8(uint32_t codes, __half2 scale, __half2& q) {
+// Eight E2M1 codes (value 2k in the low nibble of byte k) times their scale as bf16 pairs.  Exact: a
+// product has 6 significant bits.
+__device__ __forceinline__ uint4 fp4_8(uint32_t codes, __half2 scale) {
     uint32_t c[4], w[4];
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
         "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
@@ -378,25 +452,10 @@ __device__ __forceinline__ uint4 fp4_8(uint32_t codes, __half2 scale, __half2& q
         : "r"(codes));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __half2 x = *reinterpret_cast<__half2*>(&c[i]);
-        q = __hfma2(x, x, q);
-        const float2 f = __half22float2(__hmul2(x, scale));
+        const float2 f = __half22float2(__hmul2(*reinterpret_cast<__half2*>(&c[i]), scale));
         w[i] = pack_bf16(f.x, f.y);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Squares of 8 bf16 values.
-__device__ __forceinline__ float sq8(const uint4& v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint64_t q = two(0.0f, 0.0f);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const uint64_t x = two(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
-        q = fma2(x, x, q);
-    }
-    const float2 r = two_of(q);
-    return r.x + r.y;
 }
 
 template <bool FP4, bool DENSE>
@@ -420,10 +479,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
     uint64_t* ofull = bars + 12;
     uint64_t* oempty = bars + 13;
     uint64_t* lred = bars + 14;
-    uint64_t* xdone = bars + 16;       // [2] the peer's softmax warps are done with a tile's factors
-    uint64_t* xfull = bars + 18;       // [8] the peer's logits of a softmax warp
-    uint64_t* xempty = bars + 26;      // [8] the peer has read this warp's
-    uint64_t* ssfull = bars + 34;      // [2][TT_LOADERS] the peer's squares of a loader's rows
+    uint64_t* xfull = bars + 16;       // [8] the peer's logits of a softmax warp
+    uint64_t* xempty = bars + 24;      // [8] the peer has read this warp's
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
@@ -434,17 +491,15 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         mbar_init(qfull, 1);
         mbar_init(qempty, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&kfull[i], TT_LOADERS);
+            mbar_init(&kfull[i], 4);
             mbar_init(&kempty[i], 1);
-            mbar_init(&rfull[i], TT_LOADERS + 1);
+            mbar_init(&rfull[i], 1);
             mbar_init(&sfull[i], 1);
             mbar_init(&pfull[i], 8);
-            mbar_init(&xdone[i], 8);
         }
         mbar_init(ofull, 1);
         mbar_init(oempty, 8);
         mbar_init(lred, 8);
-        for (int i = 0; i < 2 * TT_LOADERS; ++i) mbar_init(&ssfull[i], 1);
         for (int i = 0; i < 8; ++i) {
             mbar_init(&xfull[i], 1);
             mbar_init(&xempty[i], 1);
@@ -462,8 +517,6 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
     cluster_sync_all();                // the peer's barriers are initialised
     const uint32_t tmem = *sTmem;
 
-    if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TT_REGS_FEW));
     if (warp == 0) {
         // ============================ query images ============================
         if (lane == 0) {
@@ -542,7 +595,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
             if (last) mbar_wait(last, last_par, a.budget, a.st);
         }
     } else if (warp == 2) {
-        // ============================ masks ============================
+        // ============================ masks and factors ============================
         // lane 4 n + w: word w (32 slots) of node n
         const int n = lane >> 2, w = lane & 3;
         int g = 0;
@@ -566,19 +619,24 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                         m = a.l.wmask[((int64_t)it.v * (a.l.ldw / 32) + (s - it.kq) / 32) * TT_G + n];
                     }
                 }
+                // lane l: the factors of slots 4 l .. 4 l + 3 (lists are padded to multiples of 32)
+                const int s4 = (it.t0 + tt) * TT_TILE + 4 * lane;
+                float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (s4 < it.slots)
+                    f = *reinterpret_cast<const float4*>(s4 < it.kq ? a.l.ef + eg * a.l.lde + s4
+                                                                    : a.l.wf + (int64_t)it.v * a.l.ldw + (s4 - it.kq));
                 // (its products done, a tile's softmax has read its masks)
                 const bool wt = g < 2 || mbar_wait(&kempty[g & 1], ((g - 2) >> 1) & 1, a.budget, a.st);
                 ok = __all_sync(FULL, wt);
                 if (!ok) break;
                 sMask[((g & 1) * TT_G + n) * 4 + w] = m;
+                *reinterpret_cast<float4*>(sF + (g & 1) * TT_TILE + 4 * lane) = f;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&rfull[g & 1]);
             }
         }
-    }
-    } else if (warp < 12) {
+    } else if (warp >= 4 && warp < 12) {
         // ============================ softmax + output ============================
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TT_REGS_SOFT));
         const int quad = warp & 3, hh = (warp - 4) >> 2, w = 4 * hh + quad;
         const int r = quad * 32 + lane;                       // query row
         const bool live = quad * 32 < a.l.G * a.l.H;          // a warp without query rows only keeps step
@@ -587,7 +645,6 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         uint8_t* mine = sX + (hh * 8 * TT_ROWS + r) * 16;
         const uint32_t theirs = peer_addr(mine, peer);
         const uint32_t their_full = peer_addr(&xfull[w], peer), their_empty = peer_addr(&xempty[w], peer);
-        const uint32_t their_done = peer_addr(xdone, peer);
         int g = 0, qi = 0;
         bool ok = true;
         for (int item = first; item < a.items && ok; item += step) {
@@ -690,7 +747,6 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                 if (lane == 0) {
                     mbar_arrive(&pfull[g & 1]);
                     if (live) peer_arrive(their_empty);
-                    peer_arrive(their_done + 8 * (g & 1));
                 }
             }
             if (!ok) break;
@@ -757,158 +813,101 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
             if (lane == 0) mbar_arrive(oempty);
             ++qi;
         }
-    } else {
+    } else if (warp >= 12) {
         // ============================ loaders ============================
-        const int lw = warp - 12;                             // rows 8 lw .. 8 lw + 7 of the tile
-        const uint32_t row0 = 8 * lw;
-        const uint32_t their_f = peer_addr(sF + row0, peer), their_bar = peer_addr(ssfull + lw, peer);
-        // The next tile with rows (item >= items: none), its slots' rows and their addresses: lane j has
-        // slot j & 7.  The list is read a tile before the rows are.
-        int item = first, tt = 0;
+        const int grp = (warp - 12) >> 2;                     // tiles of this parity
+        const uint32_t row0 = 32 * (warp & 3);                // rows row0 .. row0 + 31 of them
+        uint8_t* tile = sK + grp * TT_TILE_BYTES;
+        // The group's next tile (item >= items: none); lane j: row j of this warp (-1: none)
+        int item = first, tt = 0, g = 0;
         TtItem it;
-        int64_t eg = 0;
         int row = -1, slot = 0;
         const auto look_up = [&]() {
-            while (item < a.items) {
-                if (tt == 0) {
-                    it = tt_item(a, item);
-                    eg = DENSE ? it.b : (int64_t)it.b * a.r.T + it.n0;
+            for (; item < a.items; item += step, tt = 0) {
+                if (tt == 0) it = tt_item(a, item);
+                if (tt < it.nt && ((g ^ grp) & 1)) {
+                    ++tt;
+                    ++g;
                 }
                 if (tt < it.nt) break;
-                item += step;
-                tt = 0;
             }
             row = -1;
             if (item >= a.items) return;
-            slot = (it.t0 + tt) * TT_TILE + row0 + (lane & 7);
-            if (slot < it.kq) row = a.l.erow[eg * a.l.lde + slot];
+            slot = (it.t0 + tt) * TT_TILE + row0 + lane;
+            if (slot < it.kq) row = a.l.erow[(DENSE ? it.b : (int64_t)it.b * a.r.T + it.n0) * a.l.lde + slot];
             else if (slot < it.slots) row = a.l.wrow[(int64_t)it.v * a.l.ldw + (slot - it.kq)];
             ++tt;
         };
-        // The rows on their way: bf16 a row an instruction, 16 bytes a lane; FP4 8 lanes a row, 4 rows an
-        // instruction, 16 code bytes and 2 scales a lane.  A slot without a row reads the query image (loads
-        // without conditions) and is emptied below.
+        // FP4 rows through registers: 8 lanes a row, 4 rows an instruction, 16 code bytes and 2 scales a lane
+        // (a slot without a row has scales of 0)
         uint4 d[8];
-        uint32_t sc[2], there = 0;
+        uint32_t sc[8];
+        uint64_t at = 0;              // bf16: the address of lane j's row, 0: none
         bool fp4_rows = false;
         const auto fetch = [&]() {
-            there = __ballot_sync(FULL, row >= 0) & 0xFFu;
-            const bool entry = slot - (lane & 7) < it.kq;
+            const bool entry = slot - lane < it.kq;
             fp4_rows = FP4 && entry;
-            const uint8_t* src = a.l.qimg;
+            const uint8_t* src = nullptr;
             if (row >= 0)
                 src = (entry ? a.kv : (slot - it.kq < it.ring ? a.swa : a.draft)) +
                       (int64_t)row * (fp4_rows ? fp4_row_bytes(TT_C) : (int64_t)(TT_C * 2));
-            const uint64_t at = (uint64_t)(uintptr_t)src;
+            at = (uint64_t)(uintptr_t)src;
             if (fp4_rows) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint8_t* p = reinterpret_cast<const uint8_t*>((uintptr_t)__shfl_sync(FULL, at, 4 * i + (lane >> 3)));
-                    d[i] = __ldcg(reinterpret_cast<const uint4*>(p + 128 * rank + 16 * (lane & 7)));
-                    sc[i] = __ldcg(reinterpret_cast<const unsigned short*>(p + 256 + 16 * rank + 2 * (lane & 7)));
-                }
-            } else {
-#pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const uint8_t* p = reinterpret_cast<const uint8_t*>((uintptr_t)__shfl_sync(FULL, at, i));
-                    d[i] = __ldcg(reinterpret_cast<const uint4*>(p + 512 * rank + 16 * lane));
+                    const uint8_t* p = reinterpret_cast<const uint8_t*>((uintptr_t)__shfl_sync(FULL, at, 4 * i + (lane >> 3)));
+                    const bool real = p;
+                    if (!real) p = a.l.qimg;                  // (loads without conditions; the image has 8 KB)
+                    d[i] = __ldcg(reinterpret_cast<const uint4*>(p + 128 * rank + 16 * (lane & 7)));
+                    const uint32_t two = __ldcg(reinterpret_cast<const unsigned short*>(p + 256 + 16 * rank + 2 * (lane & 7)));
+                    sc[i] = real ? two : 0u;
                 }
             }
         };
-        // of two rows' parts a lane keeps one and sends the other
-        const auto join = [&](float x, float y, int o) {
-            const bool upper = lane & o;
-            return (upper ? y : x) + __shfl_xor_sync(FULL, upper ? x : y, o);
-        };
         look_up();
-        bool more = item < a.items, ok = true;
-        if (more) {
-            fetch();
-            look_up();
-        }
-        for (int g = 0; more; ++g) {
-            bool wt = g < 2 || mbar_wait(&kempty[g & 1], ((g - 2) >> 1) & 1, a.budget, a.st);
-            ok = __all_sync(FULL, wt);
-            if (!ok) break;
-            uint8_t* tile = sK + (g & 1) * TT_TILE_BYTES;
-            float mine = 0.0f;                                // lane j < 8: this CTA's squares of row j
+        bool more = item < a.items;
+        if (more) fetch();
+        while (more) {
+            const int gt = g++;                               // the tile of this pass
+            const bool wt = gt < 2 || mbar_wait(&kempty[grp], ((gt - 2) >> 1) & 1, a.budget, a.st);
+            if (!__all_sync(FULL, wt)) break;
             if (fp4_rows) {
                 const int piece = lane & 7, c = piece >> 1;
+                uint8_t* base = tile + c * TT_CHUNK;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const bool real = (there >> (4 * i + (lane >> 3))) & 1u;
-                    // a scale of NaN empties the row (see below) and makes its squares NaN
-                    const bool nan = (sc[i] & 0x7Fu) == 0x7Fu || (sc[i] & 0x7F00u) == 0x7F00u;
-                    const bool bad = (__ballot_sync(FULL, nan) >> (lane & 24)) & 0xFFu;
-                    if (!real || bad) sc[i] = 0u;
-                    const float f0 = e4m3_to_f32(sc[i] & 0xFFu), f1 = e4m3_to_f32(sc[i] >> 8);
-                    __half2 q0 = __float2half2_rn(0.0f), q1 = q0;
-                    uint8_t* base = tile + c * TT_CHUNK;
+                for (int i = 0; i < 8; ++i) {
+                    const __half2 f0 = __float2half2_rn(e4m3_to_f32(sc[i] & 0xFFu)), f1 = __float2half2_rn(e4m3_to_f32(sc[i] >> 8));
                     const uint32_t r = row0 + 4 * i + (lane >> 3);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         // units of 8 values in an order that differs between the lanes of a row: no bank twice
                         const int u = (k + c) & 3;
                         const uint32_t lo = (u & 1) ? d[i].y : d[i].x, hi = (u & 1) ? d[i].w : d[i].z;
-                        __half2 q = __float2half2_rn(0.0f);
-                        const uint4 val = fp4_8((u & 2) ? hi : lo, __float2half2_rn((u & 2) ? f1 : f0), q);
-                        if (u & 2) q1 = __hadd2(q1, q);
-                        else q0 = __hadd2(q0, q);
-                        *reinterpret_cast<uint4*>(base + sw128_offset(r, (uint32_t)(4 * (piece & 1) + u))) = val;
+                        *reinterpret_cast<uint4*>(base + sw128_offset(r, (uint32_t)(4 * (piece & 1) + u))) =
+                            fp4_8((u & 2) ? hi : lo, (u & 2) ? f1 : f0);
                     }
-                    const float2 s0 = __half22float2(q0), s1 = __half22float2(q1);
-                    float q = fmaf(s0.x + s0.y, f0 * f0, (s1.x + s1.y) * (f1 * f1));
-                    q += __shfl_xor_sync(FULL, q, 1);
-                    q += __shfl_xor_sync(FULL, q, 2);
-                    q += __shfl_xor_sync(FULL, q, 4);
-                    if (real && bad) q = __int_as_float(0x7FC00000);
-                    // lane j < 8 takes row j = 4 i + j % 4 from the first of its 8 lanes
-                    const float row_q = __shfl_sync(FULL, q, 8 * (lane & 3));
-                    if ((lane >> 2) == i) mine = row_q;
                 }
+                look_up();
+                more = item < a.items;
+                if (more) fetch();
             } else {
-                // sums over the lanes: lane l ends with row l / 4's
-                const auto pair = [&](int i) { return join(sq8(d[i]), sq8(d[i + 4]), 16); };
-                float q = join(join(pair(0), pair(2), 8), join(pair(1), pair(3), 8), 4);
-                q += __shfl_xor_sync(FULL, q, 2);
-                q += __shfl_xor_sync(FULL, q, 1);
-                if (!((there >> (lane >> 2)) & 1u)) q = 0.0f;
-                // A row with an infinity or a NaN leaves the products: 0 x NaN would reach the nodes that do
-                // not attend to it.  Those that do get their NaN from its factor.
-                const uint32_t bad = __ballot_sync(FULL, !(q < INFINITY));
-                mine = __shfl_sync(FULL, q, (4 * lane) & 31);
+                // a row an instruction, 16 bytes a lane
                 uint8_t* base = tile + (lane >> 3) * TT_CHUNK;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (!((there >> i) & 1u) || ((bad >> (4 * i)) & 1u)) d[i] = make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4*>(base + sw128_offset(row0 + i, (uint32_t)(lane & 7))) = d[i];
+#pragma unroll 8
+                for (uint32_t i = 0; i < 32; ++i) {
+                    const uint64_t p = __shfl_sync(FULL, at, i);
+                    cp_async16_or_zero(base + sw128_offset(row0 + i, (uint32_t)(lane & 7)),
+                                       reinterpret_cast<const uint8_t*>((uintptr_t)(p ? p : (uint64_t)(uintptr_t)a.l.qimg)) + 512 * rank + 16 * lane, p != 0);
                 }
+                cp_async_commit();
+                look_up();
+                more = item < a.items;
+                if (more) fetch();
+                cp_async_wait<0>();
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&kfull[g & 1]);
-            more = item < a.items;
-            if (more) {
-                fetch();
-                look_up();
-            }
-            // the halves meet; the peer's softmax has read the factors that these squares replace
-            wt = g < 2 || mbar_wait(&xdone[g & 1], ((g - 2) >> 1) & 1, a.budget, a.st);
-            ok = __all_sync(FULL, wt);
-            if (!ok) break;
-            uint64_t* bar = ssfull + (g & 1) * TT_LOADERS + lw;
-            if (lane < 8) peer_st(their_f + ((g & 1) * TT_TILE + lane) * 4, mine, their_bar + (g & 1) * TT_LOADERS * 8);
-            if (lane == 0) mbar_arrive_expect_tx(bar, 8 * 4);
-            wt = mbar_wait(bar, (g >> 1) & 1, a.budget, a.st);
-            ok = __all_sync(FULL, wt);
-            if (!ok) break;
-            if (lane < 8) {
-                float* p = sF + (g & 1) * TT_TILE + row0 + lane;
-                const float q = mine + *p;
-                *p = q < INFINITY ? rsqrtf(q / (float)TT_C + 1e-6f) * (LOG2E / sqrtf((float)TT_C)) : __int_as_float(0x7FC00000);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&rfull[g & 1]);
+            if (lane == 0) mbar_arrive(&kfull[grp]);
         }
     }
     tc_fence_before();
@@ -1001,7 +1000,7 @@ size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 struct TtPlan {
     int G, R8, gps, lde, ldw, n_split, tps;
     int64_t groups;
-    size_t erow, eok, wrow, wmask, info, rope, part_l, part_o, total;
+    size_t erow, ef, eok, wrow, wf, wmask, info, rope, part_l, part_o, total;
 };
 
 TtPlan tt_plan(const csa2_ctx* ctx, int B, int T, int H, int k, int window, bool dense) {
@@ -1011,8 +1010,7 @@ TtPlan tt_plan(const csa2_ctx* ctx, int B, int T, int H, int k, int window, bool
     p.R8 = (p.G * H + 7) / 8 * 8;
     p.gps = (T + p.G - 1) / p.G;
     p.groups = (int64_t)B * p.gps;
-    // (the ring's part and the drafts are padded to multiples of 4)
-    const int near = window > 0 ? window + 8 + (dense ? T : 0) : 0;
+    const int near = window > 0 ? window + (dense ? T : 0) : 0;
     p.lde = (k + 31) / 32 * 32;
     p.ldw = (near + 31) / 32 * 32;
     // Splits: every cluster walks its items one after another, each for its tiles and about four
@@ -1034,9 +1032,11 @@ TtPlan tt_plan(const csa2_ctx* ctx, int B, int T, int H, int k, int window, bool
     }
     const size_t eg = dense ? (size_t)B : (size_t)B * T;
     p.erow = up((size_t)p.groups * p.R8 * 1024, 256);
-    p.eok = up(p.erow + eg * p.lde * 4, 256);
+    p.ef = up(p.erow + eg * p.lde * 4, 256);
+    p.eok = up(p.ef + eg * p.lde * 4, 256);
     p.wrow = up(p.eok + eg * (p.lde / 32) * 4, 256);
-    p.wmask = up(p.wrow + (size_t)p.groups * p.ldw * 4, 256);
+    p.wf = up(p.wrow + (size_t)p.groups * p.ldw * 4, 256);
+    p.wmask = up(p.wf + (size_t)p.groups * p.ldw * 4, 256);
     p.info = up(p.wmask + (size_t)p.groups * (p.ldw / 32) * TT_G * 4, 256);
     p.rope = up(p.info + (size_t)p.groups * 16, 256);
     p.part_l = up(p.rope + (size_t)B * T * 64 * 4, 256);
@@ -1072,8 +1072,10 @@ csa2_status tree_tc_run(csa2_ctx* ctx, const TreeCall& c, void* ws, cudaStream_t
     PrepArgs pa = {};
     pa.l.qimg = base;
     pa.l.erow = reinterpret_cast<int32_t*>(base + p.erow);
+    pa.l.ef = reinterpret_cast<float*>(base + p.ef);
     pa.l.eok = reinterpret_cast<uint32_t*>(base + p.eok);
     pa.l.wrow = reinterpret_cast<int32_t*>(base + p.wrow);
+    pa.l.wf = reinterpret_cast<float*>(base + p.wf);
     pa.l.wmask = reinterpret_cast<uint32_t*>(base + p.wmask);
     pa.l.info = reinterpret_cast<int4*>(base + p.info);
     pa.l.rope_cs = reinterpret_cast<float*>(base + p.rope);
@@ -1085,20 +1087,26 @@ csa2_status tree_tc_run(csa2_ctx* ctx, const TreeCall& c, void* ws, cudaStream_t
     pa.l.gps = p.gps;
     pa.r = c.r;
     pa.q = reinterpret_cast<const __nv_bfloat16*>(c.q);
-    pa.B = c.B;
-    pa.eblocks = dense && c.r.k > 0 ? std::min(64, (p.lde + 255) / 256) : 0;
+    pa.kv = reinterpret_cast<const uint8_t*>(c.kv);
+    pa.swa = reinterpret_cast<const uint8_t*>(c.swa);
+    pa.draft = reinterpret_cast<const uint8_t*>(c.draft);
+    pa.fp4 = fp4;
+    pa.wb = std::max(1, (p.ldw + 127) / 128);
+    pa.eb = (p.lde + 127) / 128;
+    pa.q_blocks = p.groups * (p.R8 / 8);
+    pa.w_blocks = p.groups * pa.wb;
     pa.rope = c.rope;
     pa.flags = c.flags;
     pa.st = ctx->status;
-    csa2_status st =
-        launch_pdl(tree_prep_kernel, dim3((unsigned)p.groups, (unsigned)(p.R8 / 8 + 1 + pa.eblocks)), dim3(256), 0, s, pa);
+    const int64_t blocks = pa.q_blocks + pa.w_blocks + (dense ? (int64_t)c.B : (int64_t)c.B * c.r.T) * pa.eb;
+    csa2_status st = launch_pdl(tree_prep_kernel, dim3((unsigned)blocks), dim3(256), 0, s, pa);
     if (st != CSA2_OK) return st;
     TtArgs a = {};
     a.l = pa.l;
     a.r = c.r;
-    a.kv = reinterpret_cast<const uint8_t*>(c.kv);
-    a.swa = reinterpret_cast<const uint8_t*>(c.swa);
-    a.draft = reinterpret_cast<const uint8_t*>(c.draft);
+    a.kv = pa.kv;
+    a.swa = pa.swa;
+    a.draft = pa.draft;
     a.sink = c.sink;
     a.items = (int)(p.groups * p.n_split);
     a.n_split = p.n_split;
