@@ -25,15 +25,16 @@
 //   1       issues the MMAs; owns tensor memory (O: columns 0-255, S / P': two buffers of 128)
 //   2       the tiles' masks and factors
 //   4-11    softmax, two warps a lane quarter (64 slots each), and the output, a row a thread
-//   12-19   loaders, four warps for the even and four for the odd tiles, 32 rows each: bf16 rows by
-//           16-byte asynchronous copies into the swizzled tile, FP4 rows dequantised (exactly) from
-//           registers that are filled a tile ahead
+//   12-19   loaders, four warps for the even and four for the odd tiles, 32 rows each: bf16 rows that
+//           follow one another by tensor copies, others by 16-byte asynchronous copies into the
+//           swizzled tile, FP4 rows dequantised (exactly) from registers that are filled a tile ahead
 // Every wait is bounded; the CTAs meet at the cluster's barrier before either one exits.
 #include <algorithm>
 #include <type_traits>
 
 #include "fp4_tile.cuh"
 #include "sm100_ptx.cuh"
+#include "tma_host.cuh"
 #include "tree_tc.cuh"
 
 namespace {
@@ -58,7 +59,7 @@ constexpr int OFF_F = OFF_X + 32768;                     // [2][128] the factors
 constexpr int OFF_L = OFF_F + 1024;                      // [2][128] sums of exponentials
 constexpr int OFF_MASK = OFF_L + 1024;                   // [2][TT_G][4] x 32 bits
 constexpr int OFF_BAR = OFF_MASK + 2 * TT_G * 16;
-constexpr int N_BAR = 16 + 8 + 8;
+constexpr int N_BAR = 18 + 8 + 8 + 8;
 constexpr int OFF_TMEM = OFF_BAR + N_BAR * 8;
 constexpr int TT_SMEM = OFF_TMEM + 16;
 static_assert(TT_SMEM <= 227 * 1024, "shared memory");
@@ -97,6 +98,10 @@ struct TtArgs {
     int stall;
 };
 
+struct TtMaps {                   // bf16 rows of 512, boxes of 32 rows x 64 dims: cache, ring, drafts
+    CUtensorMap m[3];
+};
+
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -122,6 +127,19 @@ __device__ __forceinline__ void peer_st4(uint32_t addr, uint32_t a, uint32_t b, 
     asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
                  "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
                  : "memory");
+}
+
+// Whether the phase of the given parity is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -460,7 +478,7 @@ __device__ __forceinline__ uint4 fp4_8(uint32_t codes, __half2 scale) {
 
 template <bool FP4, bool DENSE>
 __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
-    tree_tc_kernel(const TtArgs a) {
+    tree_tc_kernel(const TtArgs a, const __grid_constant__ TtMaps maps) {
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* sQ = smem + OFF_Q;
     uint8_t* sK = smem + OFF_K;
@@ -472,15 +490,15 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
     uint64_t* qfull = bars + 0;
     uint64_t* qempty = bars + 1;
     uint64_t* kfull = bars + 2;        // [2] a tile's rows are in shared memory
-    uint64_t* kempty = bars + 4;       // [2] its products are done
-    uint64_t* rfull = bars + 6;        // [2] its factors and masks are there
-    uint64_t* sfull = bars + 8;        // [2] its half logits
-    uint64_t* pfull = bars + 10;       // [2] its P'
-    uint64_t* ofull = bars + 12;
-    uint64_t* oempty = bars + 13;
-    uint64_t* lred = bars + 14;
-    uint64_t* xfull = bars + 16;       // [8] the peer's logits of a softmax warp
-    uint64_t* xempty = bars + 24;      // [8] the peer has read this warp's
+    uint64_t* rfull = bars + 4;        // [2] its factors and masks are there
+    uint64_t* sfull = bars + 6;        // [2] its half logits
+    uint64_t* pfull = bars + 8;        // [2] its P'
+    uint64_t* ofull = bars + 10;
+    uint64_t* oempty = bars + 11;
+    uint64_t* lred = bars + 12;
+    uint64_t* kempty = bars + 18;      // [2][4] the products of a tile's 32-row groups are done, in order
+    uint64_t* xfull = bars + 26;       // [8] the peer's logits of a softmax warp
+    uint64_t* xempty = bars + 34;      // [8] the peer has read this warp's
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
@@ -492,7 +510,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         mbar_init(qempty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&kfull[i], 4);
-            mbar_init(&kempty[i], 1);
+            for (int j = 0; j < 4; ++j) mbar_init(&kempty[4 * i + j], 1);
             mbar_init(&rfull[i], 1);
             mbar_init(&sfull[i], 1);
             mbar_init(&pfull[i], 8);
@@ -505,6 +523,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
             mbar_init(&xempty[i], 1);
         }
         fence_mbar_init();
+        for (int i = 0; i < 3; ++i) prefetch_tmap(&maps.m[i]);
     }
     if (warp == 1) {
         tmem_alloc(sTmem, 512);
@@ -541,55 +560,68 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
             // descriptors of the operands' first bytes: an address further on adds to the low field
             const uint64_t dq = sdesc_sw128(smem_u32(sQ)), dk = sdesc_sw128(smem_u32(sK));
             const uint64_t dv = sdesc_sw128_mn(smem_u32(sK), TT_CHUNK, 1024);
-            int g = 0, qi = 0;
-            bool ok = true;
+            // Two cursors over the tiles: QK runs up to two tiles (the logits' buffers) ahead of PV, and
+            // whichever has its operands goes next, across the items' borders too.
+            struct Cursor {
+                int item, tt, nt, g, qi;
+            } cq = {first - step, 0, 0, 0, -1}, cp = cq;
+            const auto next = [&](Cursor& c) {               // to the next tile; its item is >= a.items at the end
+                if (++c.tt >= c.nt) {
+                    do {
+                        c.item += step;
+                        c.nt = c.item < a.items ? tt_item(a, c.item).nt : 0;
+                    } while (c.item < a.items && c.nt == 0);
+                    c.tt = 0;
+                    ++c.qi;
+                }
+            };
+            next(cq);
+            next(cp);
             uint64_t* last = nullptr;
             uint32_t last_par = 0;
-            // half logits of tile t (dims of this CTA)
-            const auto qk = [&](int t) {
-                if (!mbar_wait(&kfull[t & 1], (t >> 1) & 1, a.budget, a.st)) return false;
-                tc_fence_after();
-                const uint32_t s = tmem + 256 + 128 * (t & 1), kb = (uint32_t)(t & 1) * (TT_TILE_BYTES >> 4);
-#pragma unroll 4
-                for (uint32_t kk = 0; kk < 16; ++kk) {
-                    const uint32_t o = ((kk >> 2) * TT_CHUNK + (kk & 3) * 32u) >> 4;
-                    mma_ss(s, dq + o, dk + (kb + o), IDESC_QK, kk != 0);
-                }
-                mma_commit(&sfull[t & 1]);
-                last = &sfull[t & 1];
-                last_par = (t >> 1) & 1;
-                return true;
-            };
-            for (int item = first; item < a.items && ok; item += step) {
-                const TtItem it = tt_item(a, item);
-                if (it.nt == 0) continue;
-                ok = mbar_wait(qfull, qi & 1, a.budget, a.st);
-                if (!ok) break;
-                for (int tt = 0; tt < it.nt; ++tt, ++g) {
-                    if (tt == 0) ok = qk(g);
-                    if (ok && tt + 1 < it.nt) ok = qk(g + 1);
-                    if (!ok) break;
-                    if (tt + 1 >= it.nt) mma_commit(qempty);
-                    if (!mbar_wait(&pfull[g & 1], (g >> 1) & 1, a.budget, a.st) ||
-                        (tt == 0 && qi > 0 && !mbar_wait(oempty, (qi - 1) & 1, a.budget, a.st))) {
-                        ok = false;
-                        break;
-                    }
+            long long idle = clock64();
+            while (cp.item < a.items) {
+                if (cp.g < cq.g && mbar_test(&pfull[cp.g & 1], (cp.g >> 1) & 1) &&
+                    (cp.tt > 0 || cp.qi == 0 || mbar_test(oempty, (cp.qi - 1) & 1))) {
                     tc_fence_after();
-                    const uint32_t kb = (uint32_t)(g & 1) * (TT_TILE_BYTES >> 4), p = tmem + 256 + 128 * (g & 1);
-#pragma unroll 4
-                    for (uint32_t ks = 0; ks < 8; ++ks)
-                        mma_ts(tmem, p + (ks >> 2) * 64 + (ks & 3) * 8, dv + (kb + ks * (2048 >> 4)), IDESC_PV, tt > 0 || ks > 0);
-                    mma_commit(&kempty[g & 1]);
-                    last = &kempty[g & 1];
-                    last_par = (g >> 1) & 1;
-                    if (tt == it.nt - 1) {
+                    const int buf = cp.g & 1;
+                    const uint32_t kb = (uint32_t)buf * (TT_TILE_BYTES >> 4), p = tmem + 256 + 128 * buf;
+#pragma unroll
+                    for (uint32_t ks = 0; ks < 8; ++ks) {
+                        mma_ts(tmem, p + (ks >> 2) * 64 + (ks & 3) * 8, dv + (kb + ks * (2048 >> 4)), IDESC_PV, cp.tt > 0 || ks > 0);
+                        if (ks & 1) mma_commit(&kempty[4 * buf + (ks >> 1)]);
+                    }
+                    last = &kempty[4 * buf + 3];
+                    last_par = (cp.g >> 1) & 1;
+                    if (cp.tt == cp.nt - 1) {
                         mma_commit(ofull);
                         last = ofull;
-                        last_par = qi & 1;
+                        last_par = cp.qi & 1;
                     }
+                    ++cp.g;
+                    next(cp);
+                    idle = clock64();
+                } else if (cq.item < a.items && cq.g < cp.g + 2 && mbar_test(&kfull[cq.g & 1], (cq.g >> 1) & 1) &&
+                           (cq.tt > 0 || mbar_test(qfull, cq.qi & 1))) {
+                    tc_fence_after();
+                    const int buf = cq.g & 1;
+                    const uint32_t sc = tmem + 256 + 128 * buf, kb = (uint32_t)buf * (TT_TILE_BYTES >> 4);
+#pragma unroll
+                    for (uint32_t kk = 0; kk < 16; ++kk) {
+                        const uint32_t o = ((kk >> 2) * TT_CHUNK + (kk & 3) * 32u) >> 4;
+                        mma_ss(sc, dq + o, dk + (kb + o), IDESC_QK, kk != 0);
+                    }
+                    mma_commit(&sfull[buf]);
+                    last = &sfull[buf];
+                    last_par = (cq.g >> 1) & 1;
+                    if (cq.tt == cq.nt - 1) mma_commit(qempty);
+                    ++cq.g;
+                    next(cq);
+                    idle = clock64();
+                } else if (clock64() - idle > a.budget) {
+                    csa2_flag(a.st, CSA2_DEVBIT_TIMEOUT);
+                    break;
                 }
-                if (ok) ++qi;
             }
             // the MMAs must be complete before tensor memory is released
             if (last) mbar_wait(last, last_par, a.budget, a.st);
@@ -626,7 +658,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                     f = *reinterpret_cast<const float4*>(s4 < it.kq ? a.l.ef + eg * a.l.lde + s4
                                                                     : a.l.wf + (int64_t)it.v * a.l.ldw + (s4 - it.kq));
                 // (its products done, a tile's softmax has read its masks)
-                const bool wt = g < 2 || mbar_wait(&kempty[g & 1], ((g - 2) >> 1) & 1, a.budget, a.st);
+                const bool wt = g < 2 || mbar_wait(&kempty[4 * (g & 1) + 3], ((g - 2) >> 1) & 1, a.budget, a.st);
                 ok = __all_sync(FULL, wt);
                 if (!ok) break;
                 sMask[((g & 1) * TT_G + n) * 4 + w] = m;
@@ -843,6 +875,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         uint4 d[8];
         uint32_t sc[8];
         uint64_t at = 0;              // bf16: the address of lane j's row, 0: none
+        int box_row = -1, box_map = 0;    // bf16: the first row, where the 32 rows follow one another
         bool fp4_rows = false;
         const auto fetch = [&]() {
             const bool entry = slot - lane < it.kq;
@@ -852,6 +885,9 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                 src = (entry ? a.kv : (slot - it.kq < it.ring ? a.swa : a.draft)) +
                       (int64_t)row * (fp4_rows ? fp4_row_bytes(TT_C) : (int64_t)(TT_C * 2));
             at = (uint64_t)(uintptr_t)src;
+            box_map = entry ? 0 : (slot - it.kq < it.ring ? 1 : 2);
+            const int row_0 = __shfl_sync(FULL, row, 0), map_0 = __shfl_sync(FULL, box_map, 0);
+            box_row = __all_sync(FULL, row_0 >= 0 && row == row_0 + lane && box_map == map_0) ? row_0 : -1;
             if (fp4_rows) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -867,10 +903,12 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         look_up();
         bool more = item < a.items;
         if (more) fetch();
+        int last = -1;                                        // the last tile this warp filled its rows of
         while (more) {
             const int gt = g++;                               // the tile of this pass
-            const bool wt = gt < 2 || mbar_wait(&kempty[grp], ((gt - 2) >> 1) & 1, a.budget, a.st);
+            const bool wt = gt < 2 || mbar_wait(&kempty[4 * grp + (warp & 3)], ((gt - 2) >> 1) & 1, a.budget, a.st);
             if (!__all_sync(FULL, wt)) break;
+            last = gt;
             if (fp4_rows) {
                 const int piece = lane & 7, c = piece >> 1;
                 uint8_t* base = tile + c * TT_CHUNK;
@@ -890,6 +928,17 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                 look_up();
                 more = item < a.items;
                 if (more) fetch();
+            } else if (box_row >= 0) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&kfull[grp], 32 * TT_HALF * 2);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        tma_load_2d(tile + c * TT_CHUNK + row0 * 128, &maps.m[box_map], TT_HALF * rank + 64 * c, box_row, &kfull[grp]);
+                }
+                look_up();
+                more = item < a.items;
+                if (more) fetch();
+                continue;
             } else {
                 // a row an instruction, 16 bytes a lane
                 uint8_t* base = tile + (lane >> 3) * TT_CHUNK;
@@ -909,6 +958,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&kfull[grp]);
         }
+        // tensor copies must land before the CTA exits
+        if (last >= 0) mbar_wait(&kfull[grp], (last >> 1) & 1, a.budget, a.st);
     }
     tc_fence_before();
     __syncthreads();
@@ -1047,11 +1098,11 @@ TtPlan tt_plan(const csa2_ctx* ctx, int B, int T, int H, int k, int window, bool
 }
 
 template <bool FP4, bool DENSE>
-csa2_status launch_tt(const csa2_ctx* ctx, const TtArgs& a, cudaStream_t s) {
+csa2_status launch_tt(const csa2_ctx* ctx, const TtArgs& a, const TtMaps& m, cudaStream_t s) {
     auto kern = tree_tc_kernel<FP4, DENSE>;
     CSA2_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TT_SMEM));
     const int clusters = std::min(a.items, std::max(1, ctx->num_sms / 2));
-    return launch_pdl(kern, dim3((unsigned)(2 * clusters)), dim3(TT_THREADS), TT_SMEM, s, a);
+    return launch_pdl(kern, dim3((unsigned)(2 * clusters)), dim3(TT_THREADS), TT_SMEM, s, a, m);
 }
 
 }  // namespace
@@ -1098,6 +1149,14 @@ csa2_status tree_tc_run(csa2_ctx* ctx, const TreeCall& c, void* ws, cudaStream_t
     pa.rope = c.rope;
     pa.flags = c.flags;
     pa.st = ctx->status;
+    TtMaps maps;
+    // (a map that no slot refers to still needs an address: the query's)
+    const int64_t map_rows[3] = {fp4 || c.r.k == 0 ? 0 : (c.r.table ? c.r.N : c.B * c.r.N), c.r.window > 0 ? c.B * c.r.swa_cap : 0,
+                                 c.r.window > 0 ? (int64_t)c.B * c.r.T : 0};
+    const void* map_at[3] = {c.kv, c.swa, c.draft};
+    for (int i = 0; i < 3; ++i)
+        if (!csa2_make_bf16_map(&maps.m[i], map_rows[i] > 0 ? map_at[i] : c.q, std::max<int64_t>(1, map_rows[i]), TT_C, 64, 32))
+            return CSA2_ERR_CUDA;
     const int64_t blocks = pa.q_blocks + pa.w_blocks + (dense ? (int64_t)c.B : (int64_t)c.B * c.r.T) * pa.eb;
     csa2_status st = launch_pdl(tree_prep_kernel, dim3((unsigned)blocks), dim3(256), 0, s, pa);
     if (st != CSA2_OK) return st;
@@ -1125,8 +1184,8 @@ csa2_status tree_tc_run(csa2_ctx* ctx, const TreeCall& c, void* ws, cudaStream_t
         if (ctx->stall_budget > 0) a.budget = std::max<long long>(ctx->stall_budget, 1 << 17);
         ctx->stall_next = 0;
     }
-    if (fp4) st = dense ? launch_tt<true, true>(ctx, a, s) : launch_tt<true, false>(ctx, a, s);
-    else st = dense ? launch_tt<false, true>(ctx, a, s) : launch_tt<false, false>(ctx, a, s);
+    if (fp4) st = dense ? launch_tt<true, true>(ctx, a, maps, s) : launch_tt<true, false>(ctx, a, maps, s);
+    else st = dense ? launch_tt<false, true>(ctx, a, maps, s) : launch_tt<false, false>(ctx, a, maps, s);
     if (st != CSA2_OK) return st;
     if (p.n_split > 1) {
         const MergeArgs m = {a.part_o, a.part_l, a.l.rope_cs, a.sink, p.groups, c.H, p.G, p.gps, c.r.T, p.n_split, c.flags,
