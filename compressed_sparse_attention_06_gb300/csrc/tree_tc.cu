@@ -20,16 +20,19 @@
 // squares need all of its dims, of which a CTA has half: with the sums exchanged like the logits, and
 // the rows through registers for them, the loaders were what a tile waited for.)
 //
-// Warps (640 threads, one CTA an SM):
+// Warps (one CTA an SM; 640 threads, FP4 896, of which the first four give registers to the softmax):
 //   0       query images (bulk copies)
 //   1       issues the MMAs; owns tensor memory (O: columns 0-255, S / P': two buffers of 128)
 //   2       the tiles' masks and factors
-//   4-11    softmax, two warps a lane quarter (64 slots each), and the output, a row a thread
-//   12-19   loaders, four warps for the even and four for the odd tiles, 32 rows each: bf16 rows that
-//           follow one another by tensor copies, others by 16-byte asynchronous copies into the
-//           swizzled tile, FP4 rows dequantised (exactly) from registers that are filled a tile ahead
+//   4-11    softmax, two warps a lane quarter (64 slots each)
+//   12-     loaders, half of them for the even and half for the odd tiles: bf16 rows that follow one
+//           another by tensor copies, others by 16-byte asynchronous copies into the swizzled tile, FP4
+//           rows dequantised (exactly) from registers that are filled a tile ahead.  They also store the
+//           output, a row a thread: while an item's last output is read no buffer is free to be filled,
+//           and the softmax is with the next item's tiles already.
 // Every wait is bounded; the CTAs meet at the cluster's barrier before either one exits.
 #include <algorithm>
+#include <climits>
 #include <type_traits>
 
 #include "fp4_tile.cuh"
@@ -45,7 +48,11 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int TT_C = 512, TT_HALF = 256;
 constexpr int TT_ROWS = 128, TT_TILE = 128;
 constexpr int TT_G = 8;                          // nodes of a group at most
-constexpr int TT_THREADS = 640;
+constexpr int tt_loaders(bool fp4) { return fp4 ? 16 : 8; }              // warps
+constexpr int tt_threads(bool fp4) { return 32 * (12 + tt_loaders(fp4)); }
+// FP4: registers a thread at launch, of the first four warps, of the others
+constexpr int TT_REGS = 72, TT_REGS_FEW = 24, TT_REGS_MANY = 80;
+static_assert(TT_REGS_FEW + 6 * TT_REGS_MANY <= 7 * TT_REGS, "no more than the launch gives");
 constexpr int TT_CHUNK = TT_TILE * 128;          // 16 KB: 128 rows x 64 dims
 constexpr int TT_TILE_BYTES = 4 * TT_CHUNK;
 constexpr float LOG2E = 1.4426950408889634f;
@@ -86,19 +93,21 @@ struct TtArgs {
     const uint8_t* swa;
     const uint8_t* draft;
     const float* sink;
-    int items, n_split, tps;
+    int64_t groups;
+    int share, tiles;             // tiles of a cluster, of a group (at most)
     unsigned flags;
     void* out;
     int out_f32;
     float* lse;
-    float* part_o;                // [groups * n_split][G*H rows][512] (n_split > 1)
-    float* part_l;                // [groups * n_split][G*H rows]
+    int pieces;                   // > 1: some groups are dealt out in up to so many pieces
+    float* part_o;                // [groups * pieces][G*H rows][512]
+    float* part_l;                // [groups * pieces][G*H rows]
     unsigned* st;
     long long budget;
     int stall;
 };
 
-struct TtMaps {                   // bf16 rows of 512, boxes of 32 rows x 64 dims: cache, ring, drafts
+struct TtMaps {                   // bf16 rows of 512, boxes of 64 dims x the rows of a loader: cache, ring, drafts
     CUtensorMap m[3];
 };
 
@@ -184,28 +193,48 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return r;
 }
 
+// The groups' tiles stand one behind the other, `tiles` a group (a shorter one leaves its last ones
+// out), and cluster c has `share` of them from c * share on: its items are the groups that lie there.
 struct TtItem {
     int v, b, n0, gv;             // group, sequence, first node in it, nodes
-    int split, kq, slots, ring;   // entry slots, all slots, the ring's among the others
+    int kq, slots, ring;          // entry slots, all slots, the ring's among the others
     int t0, nt;                   // tiles t0 .. t0 + nt - 1
 };
 
-__device__ __forceinline__ TtItem tt_item(const TtArgs& a, int item) {
-    TtItem r;
-    r.v = item / a.n_split;
-    r.split = item - r.v * a.n_split;
-    r.b = r.v / a.l.gps;
-    r.n0 = (r.v - r.b * a.l.gps) * a.l.G;
-    r.gv = min(a.l.G, a.r.T - r.n0);
-    const int4 i = a.l.info[r.v];
-    r.kq = i.x;
-    r.slots = i.y;
-    r.ring = i.z;
-    const int tiles = (i.y + TT_TILE - 1) / TT_TILE;
-    r.t0 = r.split * a.tps;
-    r.nt = max(0, min(tiles, r.t0 + a.tps) - r.t0);
-    return r;
-}
+struct TtWalk {
+    int v, at, left;              // group, tile in it, tiles left to the cluster
+    int4 info;                    // the group's, loaded an item ahead
+
+    __device__ __forceinline__ void start(const TtArgs& a, int cluster) {
+        const int64_t f0 = (int64_t)cluster * a.share;
+        v = (int)(f0 / a.tiles);
+        at = (int)(f0 - (int64_t)v * a.tiles);
+        left = (int)max((int64_t)0, min((int64_t)a.share, a.groups * a.tiles - f0));
+        info = left > 0 ? a.l.info[v] : make_int4(0, 0, 0, 0);
+    }
+    // the next item with tiles; false at the end.  Empty ones (a group without slots, a short one's last
+    // tiles) are passed over, or returned with nt = 0 where `empty` is set.
+    __device__ __forceinline__ bool next(const TtArgs& a, TtItem& r, bool empty = false) {
+        while (left > 0) {
+            const int to = min(a.tiles, at + left);
+            r.v = v;
+            r.b = v / a.l.gps;
+            r.n0 = (v - r.b * a.l.gps) * a.l.G;
+            r.gv = min(a.l.G, a.r.T - r.n0);
+            r.kq = info.x;
+            r.slots = info.y;
+            r.ring = info.z;
+            r.t0 = at;
+            r.nt = max(0, min((info.y + TT_TILE - 1) / TT_TILE, to) - at);
+            left -= to - at;
+            ++v;
+            at = 0;
+            if (left > 0) info = a.l.info[v];
+            if (r.nt > 0 || empty) return true;
+        }
+        return false;
+    }
+};
 
 // Output scale 1 / (L + e^zs) (for O of P' = p f: times ln 2 sqrt(512)) and log-sum-exp of a row with
 // the sum L of its exponentials and the sink logit zs; a row without either gives 0 and -inf.
@@ -477,7 +506,7 @@ __device__ __forceinline__ uint4 fp4_8(uint32_t codes, __half2 scale) {
 }
 
 template <bool FP4, bool DENSE>
-__global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(tt_threads(FP4), 1) __cluster_dims__(2, 1, 1)
     tree_tc_kernel(const TtArgs a, const __grid_constant__ TtMaps maps) {
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* sQ = smem + OFF_Q;
@@ -490,8 +519,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
     uint64_t* qfull = bars + 0;
     uint64_t* qempty = bars + 1;
     uint64_t* kfull = bars + 2;        // [2] a tile's rows are in shared memory
-    uint64_t* rfull = bars + 4;        // [2] its factors and masks are there
-    uint64_t* sfull = bars + 6;        // [2] its half logits
+    uint64_t* sfull = bars + 6;        // [2] its half logits, its factors and masks
     uint64_t* pfull = bars + 8;        // [2] its P'
     uint64_t* ofull = bars + 10;
     uint64_t* oempty = bars + 11;
@@ -502,21 +530,21 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
-    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int cluster = blockIdx.x >> 1;
+    constexpr int LOADERS = tt_loaders(FP4);
 
     if (threadIdx.x == 0) {
         if (smem_u32(smem) & 1023u) csa2_flag(a.st, CSA2_DEVBIT_TIMEOUT);
         mbar_init(qfull, 1);
         mbar_init(qempty, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&kfull[i], 4);
+            mbar_init(&kfull[i], LOADERS / 2);
             for (int j = 0; j < 4; ++j) mbar_init(&kempty[4 * i + j], 1);
-            mbar_init(&rfull[i], 1);
-            mbar_init(&sfull[i], 1);
+            mbar_init(&sfull[i], 2);
             mbar_init(&pfull[i], 8);
         }
         mbar_init(ofull, 1);
-        mbar_init(oempty, 8);
+        mbar_init(oempty, LOADERS);
         mbar_init(lred, 8);
         for (int i = 0; i < 8; ++i) {
             mbar_init(&xfull[i], 1);
@@ -535,14 +563,17 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
     tc_fence_after();
     cluster_sync_all();                // the peer's barriers are initialised
     const uint32_t tmem = *sTmem;
+    TtWalk walk;
+    TtItem it;
+    walk.start(a, cluster);
 
+    if (warp < 4) {
+        if (FP4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TT_REGS_FEW));
     if (warp == 0) {
         // ============================ query images ============================
         if (lane == 0) {
             int qi = 0, issued = -1;
-            for (int item = first; item < a.items && !a.stall; item += step) {
-                const TtItem it = tt_item(a, item);
-                if (it.nt == 0) continue;
+            while (!a.stall && walk.next(a, it)) {
                 if (qi > 0 && !mbar_wait(qempty, (qi - 1) & 1, a.budget, a.st)) break;
                 const uint32_t bytes = (uint32_t)a.l.R8 * 128u;
                 mbar_arrive_expect_tx(qfull, 4 * bytes);
@@ -563,24 +594,23 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
             // Two cursors over the tiles: QK runs up to two tiles (the logits' buffers) ahead of PV, and
             // whichever has its operands goes next, across the items' borders too.
             struct Cursor {
-                int item, tt, nt, g, qi;
-            } cq = {first - step, 0, 0, 0, -1}, cp = cq;
-            const auto next = [&](Cursor& c) {               // to the next tile; its item is >= a.items at the end
-                if (++c.tt >= c.nt) {
-                    do {
-                        c.item += step;
-                        c.nt = c.item < a.items ? tt_item(a, c.item).nt : 0;
-                    } while (c.item < a.items && c.nt == 0);
-                    c.tt = 0;
-                    ++c.qi;
-                }
+                TtWalk w;
+                int tt, nt, g, qi;
+                bool more;
+            } cq = {walk, 0, 0, 0, -1, true}, cp = cq;
+            const auto next = [&](Cursor& c) {               // to the next tile
+                if (++c.tt < c.nt) return;
+                c.more = c.w.next(a, it);
+                c.nt = it.nt;
+                c.tt = 0;
+                ++c.qi;
             };
             next(cq);
             next(cp);
             uint64_t* last = nullptr;
             uint32_t last_par = 0;
             long long idle = clock64();
-            while (cp.item < a.items) {
+            while (cp.more) {
                 if (cp.g < cq.g && mbar_test(&pfull[cp.g & 1], (cp.g >> 1) & 1) &&
                     (cp.tt > 0 || cp.qi == 0 || mbar_test(oempty, (cp.qi - 1) & 1))) {
                     tc_fence_after();
@@ -601,7 +631,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                     ++cp.g;
                     next(cp);
                     idle = clock64();
-                } else if (cq.item < a.items && cq.g < cp.g + 2 && mbar_test(&kfull[cq.g & 1], (cq.g >> 1) & 1) &&
+                } else if (cq.more && cq.g < cp.g + 2 && mbar_test(&kfull[cq.g & 1], (cq.g >> 1) & 1) &&
                            (cq.tt > 0 || mbar_test(qfull, cq.qi & 1))) {
                     tc_fence_after();
                     const int buf = cq.g & 1;
@@ -618,9 +648,12 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                     ++cq.g;
                     next(cq);
                     idle = clock64();
-                } else if (clock64() - idle > a.budget) {
-                    csa2_flag(a.st, CSA2_DEVBIT_TIMEOUT);
-                    break;
+                } else {
+                    __nanosleep(20);                          // (polling takes issue slots from the softmax)
+                    if (clock64() - idle > a.budget) {
+                        csa2_flag(a.st, CSA2_DEVBIT_TIMEOUT);
+                        break;
+                    }
                 }
             }
             // the MMAs must be complete before tensor memory is released
@@ -632,8 +665,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         const int n = lane >> 2, w = lane & 3;
         int g = 0;
         bool ok = true;
-        for (int item = first; item < a.items && ok; item += step) {
-            const TtItem it = tt_item(a, item);
+        while (ok && walk.next(a, it)) {
             const int64_t eg = DENSE ? it.b : (int64_t)it.b * a.r.T + it.n0;
             int seen = it.kq;
             if (DENSE && n < it.gv && a.r.k > 0)
@@ -664,41 +696,29 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                 sMask[((g & 1) * TT_G + n) * 4 + w] = m;
                 *reinterpret_cast<float4*>(sF + (g & 1) * TT_TILE + 4 * lane) = f;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&rfull[g & 1]);
+                if (lane == 0) mbar_arrive(&sfull[g & 1]);
             }
         }
-    } else if (warp >= 4 && warp < 12) {
-        // ============================ softmax + output ============================
+    }
+    } else if (warp < 12) {
+        // ============================ softmax ============================
+        if (FP4) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TT_REGS_MANY));
         const int quad = warp & 3, hh = (warp - 4) >> 2, w = 4 * hh + quad;
         const int r = quad * 32 + lane;                       // query row
         const bool live = quad * 32 < a.l.G * a.l.H;          // a warp without query rows only keeps step
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-        const int hq = r / a.l.H, h = r - hq * a.l.H, g_row = min(hq, a.l.G - 1);
+        const int g_row = min(r / a.l.H, a.l.G - 1);
         uint8_t* mine = sX + (hh * 8 * TT_ROWS + r) * 16;
         const uint32_t theirs = peer_addr(mine, peer);
         const uint32_t their_full = peer_addr(&xfull[w], peer), their_empty = peer_addr(&xempty[w], peer);
         int g = 0, qi = 0;
         bool ok = true;
-        for (int item = first; item < a.items && ok; item += step) {
-            const TtItem it = tt_item(a, item);
-            const int rows = it.gv * a.l.H;
-            const int64_t bt = (int64_t)it.b * a.r.T + it.n0 + hq, prow = (int64_t)item * (a.l.G * a.l.H) + r;
-            if (it.nt == 0) {
-                if (r < rows && a.n_split > 1) {
-                    if (rank == 0 && hh == 0) a.part_l[prow] = 0.0f;
-                } else if (r < rows) {
-                    const int64_t o = (bt * a.l.H + h) * (int64_t)TT_C + TT_HALF * rank + 128 * hh;
-                    uint4* d = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.out) + o * (a.out_f32 ? 4 : 2));
-                    for (int i = 0; i < (a.out_f32 ? 32 : 16); ++i) d[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (rank == 0 && hh == 0 && a.lse) a.lse[bt * a.l.H + h] = a.sink ? a.sink[h] : -INFINITY;
-                }
-                continue;
-            }
+        while (ok && walk.next(a, it)) {
             uint64_t lsum = two(0.0f, 0.0f);
             for (int tt = 0; tt < it.nt; ++tt, ++g) {
-                bool wt = mbar_wait(&sfull[g & 1], (g >> 1) & 1, a.budget, a.st) &&
-                          mbar_wait(&rfull[g & 1], (g >> 1) & 1, a.budget, a.st) &&
-                          (g == 0 || !live || mbar_wait(&xempty[w], (g - 1) & 1, a.budget, a.st));
+                // (the peer has read the last tile's halves long before this one's logits come)
+                bool wt = (g == 0 || !live || mbar_wait(&xempty[w], (g - 1) & 1, a.budget, a.st)) &&
+                          mbar_wait(&sfull[g & 1], (g >> 1) & 1, a.budget, a.st);
                 if (!__all_sync(FULL, wt)) {
                     ok = false;
                     break;
@@ -782,103 +802,54 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                 }
             }
             if (!ok) break;
-            // sums of the two halves of the slots; the last item's readers are done with sL
-            bool wt = qi == 0 || mbar_wait(oempty, (qi - 1) & 1, a.budget, a.st);
+            // the sums of this half of the slots; the last item's readers are done with sL
+            const bool wt = qi == 0 || mbar_wait(oempty, (qi - 1) & 1, a.budget, a.st);
             const float2 ls = two_of(lsum);
             if (wt) sL[hh * TT_ROWS + r] = ls.x + ls.y;
+            ok = __all_sync(FULL, wt);
             __syncwarp();
             if (lane == 0) mbar_arrive(lred);
-            wt = wt && mbar_wait(lred, qi & 1, a.budget, a.st) && mbar_wait(ofull, qi & 1, a.budget, a.st);
-            if (!__all_sync(FULL, wt)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            if (live) {
-                const float L = sL[r] + sL[TT_ROWS + r];
-                float sc = 1.0f;
-                if (a.n_split == 1) {
-                    const float2 fin = finish_row(L, a.sink && r < rows ? a.sink[h] : -INFINITY);
-                    sc = fin.x;
-                    if (rank == 0 && hh == 0 && r < rows && a.lse) a.lse[bt * a.l.H + h] = fin.y;
-                } else if (rank == 0 && hh == 0 && r < rows) {
-                    a.part_l[prow] = L;
-                }
-                const int d0 = TT_HALF * rank + 128 * hh;
-                const bool rot = a.n_split == 1 && (a.flags & CSA2_ROPE) && d0 == 384;
-                const float* cs = a.l.rope_cs + (r < rows ? bt : bt - hq) * 64;
-#pragma unroll 1
-                for (int db = 0; db < 8; ++db) {
-                    uint32_t o[16];
-                    tmem_ld16(lanes + 128 * hh + 16 * db, o);
-                    tmem_wait_ld();
-                    float v[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(o[i]) * sc;
-                    if (rot && db >= 4) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float c = cs[8 * (db - 4) + j], s = cs[32 + 8 * (db - 4) + j], x0 = v[2 * j], x1 = v[2 * j + 1];
-                            v[2 * j] = x0 * c + x1 * s;
-                            v[2 * j + 1] = x1 * c - x0 * s;
-                        }
-                    }
-                    if (r < rows && (a.n_split > 1 || a.out_f32)) {
-                        float* d = (a.n_split > 1 ? a.part_o + prow * (int64_t)TT_C
-                                                  : reinterpret_cast<float*>(a.out) + (bt * a.l.H + h) * (int64_t)TT_C) + d0 + 16 * db;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            reinterpret_cast<float4*>(d)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                    } else if (r < rows) {
-                        uint4* d = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) +
-                                                            (bt * a.l.H + h) * (int64_t)TT_C + d0 + 16 * db);
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            d[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                                              pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
-                    }
-                    __syncwarp();
-                }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(oempty);
             ++qi;
         }
-    } else if (warp >= 12) {
-        // ============================ loaders ============================
-        const int grp = (warp - 12) >> 2;                     // tiles of this parity
-        const uint32_t row0 = 32 * (warp & 3);                // rows row0 .. row0 + 31 of them
+    } else {
+        // ============================ loaders, output ============================
+        if (FP4) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TT_REGS_MANY));
+        constexpr int ROWS = TT_TILE / (LOADERS / 2);         // of a tile, a warp
+        const int lw = warp - 12, grp = lw / (LOADERS / 2);   // tiles of this parity
+        const uint32_t row0 = ROWS * (lw % (LOADERS / 2));    // rows row0 .. row0 + ROWS - 1 of them
         uint8_t* tile = sK + grp * TT_TILE_BYTES;
-        // The group's next tile (item >= items: none); lane j: row j of this warp (-1: none)
-        int item = first, tt = 0, g = 0;
-        TtItem it;
+        // The next tile of this parity; lane j: row j of this warp (-1: none)
+        int tt = 0, g = 0;
         int row = -1, slot = 0;
+        bool more = true;
+        it.nt = 0;
         const auto look_up = [&]() {
-            for (; item < a.items; item += step, tt = 0) {
-                if (tt == 0) it = tt_item(a, item);
+            for (;;) {
                 if (tt < it.nt && ((g ^ grp) & 1)) {
                     ++tt;
                     ++g;
                 }
                 if (tt < it.nt) break;
+                more = walk.next(a, it);
+                if (!more) return;
+                tt = 0;
             }
             row = -1;
-            if (item >= a.items) return;
-            slot = (it.t0 + tt) * TT_TILE + row0 + lane;
+            slot = (it.t0 + tt) * TT_TILE + row0 + (lane & (ROWS - 1));
             if (slot < it.kq) row = a.l.erow[(DENSE ? it.b : (int64_t)it.b * a.r.T + it.n0) * a.l.lde + slot];
             else if (slot < it.slots) row = a.l.wrow[(int64_t)it.v * a.l.ldw + (slot - it.kq)];
             ++tt;
         };
         // FP4 rows through registers: 8 lanes a row, 4 rows an instruction, 16 code bytes and 2 scales a lane
         // (a slot without a row has scales of 0)
-        uint4 d[8];
-        uint32_t sc[8];
+        constexpr int FP4_ROWS = ROWS / 4;
+        uint4 d[FP4_ROWS];
+        uint32_t sc[FP4_ROWS];
         uint64_t at = 0;              // bf16: the address of lane j's row, 0: none
-        int box_row = -1, box_map = 0;    // bf16: the first row, where the 32 rows follow one another
+        int box_row = -1, box_map = 0;    // bf16: the first row, where the rows follow one another
         bool fp4_rows = false;
         const auto fetch = [&]() {
-            const bool entry = slot - lane < it.kq;
+            const bool entry = slot - (lane & (ROWS - 1)) < it.kq;
             fp4_rows = FP4 && entry;
             const uint8_t* src = nullptr;
             if (row >= 0)
@@ -887,10 +858,10 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
             at = (uint64_t)(uintptr_t)src;
             box_map = entry ? 0 : (slot - it.kq < it.ring ? 1 : 2);
             const int row_0 = __shfl_sync(FULL, row, 0), map_0 = __shfl_sync(FULL, box_map, 0);
-            box_row = __all_sync(FULL, row_0 >= 0 && row == row_0 + lane && box_map == map_0) ? row_0 : -1;
+            box_row = __all_sync(FULL, row_0 >= 0 && row == row_0 + (lane & (ROWS - 1)) && box_map == map_0) ? row_0 : -1;
             if (fp4_rows) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < FP4_ROWS; ++i) {
                     const uint8_t* p = reinterpret_cast<const uint8_t*>((uintptr_t)__shfl_sync(FULL, at, 4 * i + (lane >> 3)));
                     const bool real = p;
                     if (!real) p = a.l.qimg;                  // (loads without conditions; the image has 8 KB)
@@ -900,20 +871,117 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                 }
             }
         };
+        // The output of finished items: a walk of its own, which also meets the items without tiles.  Item i's
+        // last tile is e: its output comes after the rows of tile e + 1, whose buffer is free before, and before
+        // those of e + 2.
+        TtWalk owalk;
+        owalk.start(a, cluster);
+        TtItem oit;
+        int oq = 0, oend = 0;         // items with tiles so far, tiles up to the next one's end
+        bool omore = owalk.next(a, oit, true);
+        if (omore) oend = oit.nt;
+        constexpr int PART = TT_HALF / (LOADERS / 4);         // dims of a warp
+        const int quad = warp & 3, r = quad * 32 + lane, hq = r / a.l.H, h = r - hq * a.l.H;
+        const int d0 = TT_HALF * rank + PART * (lw >> 2);
+        const bool live = quad * 32 < a.l.G * a.l.H, first_part = rank == 0 && lw < 4;
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + PART * (lw >> 2);
+        const auto output = [&]() {
+            const bool valid = r < oit.gv * a.l.H;
+            const int64_t bt = (int64_t)oit.b * a.r.T + oit.n0 + (valid ? hq : 0), orow = bt * a.l.H + h;
+            int piece = 0, pieces = 1;
+            if (a.pieces > 1) {
+                const int64_t g0 = (int64_t)oit.v * a.tiles;
+                piece = cluster - (int)(g0 / a.share);
+                pieces = (int)((g0 + a.tiles - 1) / a.share - g0 / a.share) + 1;
+            }
+            const int64_t prow = ((int64_t)oit.v * a.pieces + piece) * (a.l.G * a.l.H) + r;
+            const bool part = pieces > 1;
+            float L = 0.0f;
+            if (oit.nt > 0) {
+                const bool wt = mbar_wait(lred, oq & 1, a.budget, a.st) && mbar_wait(ofull, oq & 1, a.budget, a.st);
+                if (!__all_sync(FULL, wt)) return false;
+                tc_fence_after();
+                L = sL[r] + sL[TT_ROWS + r];
+            }
+            const float2 fin = part ? make_float2(1.0f, 0.0f) : finish_row(L, a.sink && valid ? a.sink[h] : -INFINITY);
+            if (valid && first_part) {
+                if (part) a.part_l[prow] = L;
+                else if (a.lse) a.lse[orow] = fin.y;
+            }
+            if (live && !(part && oit.nt == 0)) {
+                const float* cs = a.l.rope_cs + bt * 64;
+#pragma unroll 1
+                for (int db = 0; db < PART / 16; ++db) {
+                    float v[16];
+                    if (oit.nt > 0) {
+                        uint32_t o[16];
+                        tmem_ld16(lanes + 16 * db, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(o[i]) * fin.x;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+                    }
+                    const int d = d0 + 16 * db;
+                    if (!part && (a.flags & CSA2_ROPE) && d >= TT_C - 64) {
+                        const float* c = cs + (d - (TT_C - 64)) / 2;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float x0 = v[2 * j], x1 = v[2 * j + 1];
+                            v[2 * j] = x0 * c[j] + x1 * c[32 + j];
+                            v[2 * j + 1] = x1 * c[j] - x0 * c[32 + j];
+                        }
+                    }
+                    if (valid && (part || a.out_f32)) {
+                        float* p = (part ? a.part_o + prow * (int64_t)TT_C : reinterpret_cast<float*>(a.out) + orow * (int64_t)TT_C) + d;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    } else if (valid) {
+                        uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + orow * (int64_t)TT_C + d);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            p[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                                              pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+                    }
+                    __syncwarp();
+                }
+            }
+            if (oit.nt > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(oempty);
+                ++oq;
+            }
+            return true;
+        };
+        // the outputs due before the rows of tile t (at the end: all)
+        const auto outputs = [&](int t) {
+            while (omore && oend + 1 <= t) {
+                if (!output()) return false;
+                omore = owalk.next(a, oit, true);
+                if (omore) oend += oit.nt;
+            }
+            return true;
+        };
         look_up();
-        bool more = item < a.items;
         if (more) fetch();
         int last = -1;                                        // the last tile this warp filled its rows of
+        bool ok = true;
         while (more) {
             const int gt = g++;                               // the tile of this pass
-            const bool wt = gt < 2 || mbar_wait(&kempty[4 * grp + (warp & 3)], ((gt - 2) >> 1) & 1, a.budget, a.st);
-            if (!__all_sync(FULL, wt)) break;
+            ok = outputs(gt);
+            if (!ok) break;
+            const bool wt = gt < 2 || mbar_wait(&kempty[4 * grp + row0 / 32], ((gt - 2) >> 1) & 1, a.budget, a.st);
+            ok = __all_sync(FULL, wt);
+            if (!ok) break;
             last = gt;
             if (fp4_rows) {
                 const int piece = lane & 7, c = piece >> 1;
                 uint8_t* base = tile + c * TT_CHUNK;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < FP4_ROWS; ++i) {
                     const __half2 f0 = __float2half2_rn(e4m3_to_f32(sc[i] & 0xFFu)), f1 = __float2half2_rn(e4m3_to_f32(sc[i] >> 8));
                     const uint32_t r = row0 + 4 * i + (lane >> 3);
 #pragma unroll
@@ -926,31 +994,28 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                     }
                 }
                 look_up();
-                more = item < a.items;
                 if (more) fetch();
             } else if (box_row >= 0) {
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&kfull[grp], 32 * TT_HALF * 2);
+                    mbar_arrive_expect_tx(&kfull[grp], ROWS * TT_HALF * 2);
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         tma_load_2d(tile + c * TT_CHUNK + row0 * 128, &maps.m[box_map], TT_HALF * rank + 64 * c, box_row, &kfull[grp]);
                 }
                 look_up();
-                more = item < a.items;
                 if (more) fetch();
                 continue;
             } else {
                 // a row an instruction, 16 bytes a lane
                 uint8_t* base = tile + (lane >> 3) * TT_CHUNK;
 #pragma unroll 8
-                for (uint32_t i = 0; i < 32; ++i) {
+                for (uint32_t i = 0; i < ROWS; ++i) {
                     const uint64_t p = __shfl_sync(FULL, at, i);
                     cp_async16_or_zero(base + sw128_offset(row0 + i, (uint32_t)(lane & 7)),
                                        reinterpret_cast<const uint8_t*>((uintptr_t)(p ? p : (uint64_t)(uintptr_t)a.l.qimg)) + 512 * rank + 16 * lane, p != 0);
                 }
                 cp_async_commit();
                 look_up();
-                more = item < a.items;
                 if (more) fetch();
                 cp_async_wait<0>();
             }
@@ -958,6 +1023,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&kfull[grp]);
         }
+        if (ok) outputs(INT_MAX);
         // tensor copies must land before the CTA exits
         if (last >= 0) mbar_wait(&kfull[grp], (last >> 1) & 1, a.budget, a.st);
     }
@@ -975,14 +1041,14 @@ struct MergeArgs {
     const float* rope_cs;
     const float* sink;
     int64_t groups;
-    int H, G, gps, T, n_split;
+    int H, G, gps, T, pieces, share, tiles;
     unsigned flags;
     void* out;
     int out_f32;
     float* lse;
 };
 
-// The splits of one query row, a warp each: outputs and sums add up.
+// The pieces of one query row, a warp each: outputs and sums add up.
 __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeArgs a) {
     pdl_wait();
     pdl_trigger();
@@ -992,18 +1058,20 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeArgs a) {
     const int64_t v = i / rows, b = v / a.gps;
     const int r = (int)(i - v * rows), g = r / a.H, h = r - g * a.H, node = (int)(v % a.gps) * a.G + g;
     if (node >= a.T) return;
-    const int64_t bt = b * a.T + node;
+    const int64_t bt = b * a.T + node, g0 = v * a.tiles;
+    const int n = (int)((g0 + a.tiles - 1) / a.share - g0 / a.share) + 1;
+    if (n == 1) return;                          // (the main kernel has finished the group)
     float acc[16], L = 0.0f;
 #pragma unroll
     for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
-    for (int s0 = 0; s0 < a.n_split; s0 += 4) {
+    for (int s0 = 0; s0 < n; s0 += 4) {
         float l[4];
         float4 x[4][4];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            const int64_t p = (v * a.n_split + s0 + s) * rows + r;
-            l[s] = s0 + s < a.n_split ? a.part_l[p] : 0.0f;
-            // (a split without slots has no output)
+            const int64_t p = (v * a.pieces + s0 + s) * rows + r;
+            l[s] = s0 + s < n ? a.part_l[p] : 0.0f;
+            // (a piece without slots has no output)
             const float4* o = reinterpret_cast<const float4*>(a.part_o + p * TT_C) + lane;
 #pragma unroll
             for (int j = 0; j < 4; ++j) x[s][j] = l[s] != 0.0f ? __ldcs(o + 32 * j) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -1049,7 +1117,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeArgs a) {
 size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 struct TtPlan {
-    int G, R8, gps, lde, ldw, n_split, tps;
+    int G, R8, gps, lde, ldw, clusters, share, tiles, pieces;
     int64_t groups;
     size_t erow, ef, eok, wrow, wf, wmask, info, rope, part_l, part_o, total;
 };
@@ -1064,23 +1132,16 @@ TtPlan tt_plan(const csa2_ctx* ctx, int B, int T, int H, int k, int window, bool
     const int near = window > 0 ? window + (dense ? T : 0) : 0;
     p.lde = (k + 31) / 32 * 32;
     p.ldw = (near + 31) / 32 * 32;
-    // Splits: every cluster walks its items one after another, each for its tiles and about four
-    // tiles' time of filling and draining; with splits the partial outputs are written and read, half a
-    // tile's time an item.
-    const int64_t tiles = std::max(1, (p.lde + near + TT_TILE - 1) / TT_TILE), clusters = std::max(1, ctx->num_sms / 2);
-    double best = 1e300;
-    p.n_split = 1;
-    p.tps = (int)tiles;
-    for (int64_t ns = 1; ns <= std::min<int64_t>(tiles, std::max<int64_t>(1, 4 * clusters / p.groups)); ++ns) {
-        const int64_t tps = (tiles + ns - 1) / ns, n = (tiles + tps - 1) / tps;
-        if (n != ns) continue;
-        const double cost = (double)((p.groups * ns + clusters - 1) / clusters) * (tps + (ns > 1 ? 4.5 : 4.0)) + (ns > 1 ? 1.0 : 0.0);
-        if (cost < best) {
-            best = cost;
-            p.n_split = (int)ns;
-            p.tps = (int)tps;
-        }
-    }
+    // A cluster's time is its tiles' and, for every group it works on, about three tiles' for the first
+    // rows and the output; either the groups stay whole, or the tiles are dealt out evenly.
+    const int64_t clusters = std::max(1, ctx->num_sms / 2);
+    p.tiles = std::max(1, (p.lde + near + TT_TILE - 1) / TT_TILE);
+    const int64_t total = p.groups * p.tiles, whole = (p.groups + clusters - 1) / clusters, even = (total + clusters - 1) / clusters;
+    const bool split = even + 3 * (even / p.tiles + 2) < whole * p.tiles + 3 * whole;
+    p.share = (int)(split ? even : whole * p.tiles);
+    p.clusters = (int)((total + p.share - 1) / p.share);
+    // the pieces of a group: of the `share`s that touch it
+    p.pieces = split ? (p.tiles + p.share - 2) / p.share + 1 : 1;
     const size_t eg = dense ? (size_t)B : (size_t)B * T;
     p.erow = up((size_t)p.groups * p.R8 * 1024, 256);
     p.ef = up(p.erow + eg * p.lde * 4, 256);
@@ -1091,18 +1152,17 @@ TtPlan tt_plan(const csa2_ctx* ctx, int B, int T, int H, int k, int window, bool
     p.info = up(p.wmask + (size_t)p.groups * (p.ldw / 32) * TT_G * 4, 256);
     p.rope = up(p.info + (size_t)p.groups * 16, 256);
     p.part_l = up(p.rope + (size_t)B * T * 64 * 4, 256);
-    const size_t rows = p.n_split > 1 ? (size_t)p.groups * p.n_split * p.G * H : 0;
+    const size_t rows = p.pieces > 1 ? (size_t)p.groups * p.pieces * p.G * H : 0;
     p.part_o = up(p.part_l + rows * 4, 256);
     p.total = p.part_o + rows * TT_C * 4;
     return p;
 }
 
 template <bool FP4, bool DENSE>
-csa2_status launch_tt(const csa2_ctx* ctx, const TtArgs& a, const TtMaps& m, cudaStream_t s) {
+csa2_status launch_tt(int clusters, const TtArgs& a, const TtMaps& m, cudaStream_t s) {
     auto kern = tree_tc_kernel<FP4, DENSE>;
     CSA2_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TT_SMEM));
-    const int clusters = std::min(a.items, std::max(1, ctx->num_sms / 2));
-    return launch_pdl(kern, dim3((unsigned)(2 * clusters)), dim3(TT_THREADS), TT_SMEM, s, a, m);
+    return launch_pdl(kern, dim3((unsigned)(2 * clusters)), dim3(tt_threads(FP4)), TT_SMEM, s, a, m);
 }
 
 }  // namespace
@@ -1155,7 +1215,7 @@ csa2_status tree_tc_run(csa2_ctx* ctx, const TreeCall& c, void* ws, cudaStream_t
                                  c.r.window > 0 ? (int64_t)c.B * c.r.T : 0};
     const void* map_at[3] = {c.kv, c.swa, c.draft};
     for (int i = 0; i < 3; ++i)
-        if (!csa2_make_bf16_map(&maps.m[i], map_rows[i] > 0 ? map_at[i] : c.q, std::max<int64_t>(1, map_rows[i]), TT_C, 64, 32))
+        if (!csa2_make_bf16_map(&maps.m[i], map_rows[i] > 0 ? map_at[i] : c.q, std::max<int64_t>(1, map_rows[i]), TT_C, 64, fp4 ? 16 : 32))
             return CSA2_ERR_CUDA;
     const int64_t blocks = pa.q_blocks + pa.w_blocks + (dense ? (int64_t)c.B : (int64_t)c.B * c.r.T) * pa.eb;
     csa2_status st = launch_pdl(tree_prep_kernel, dim3((unsigned)blocks), dim3(256), 0, s, pa);
@@ -1167,9 +1227,10 @@ csa2_status tree_tc_run(csa2_ctx* ctx, const TreeCall& c, void* ws, cudaStream_t
     a.swa = pa.swa;
     a.draft = pa.draft;
     a.sink = c.sink;
-    a.items = (int)(p.groups * p.n_split);
-    a.n_split = p.n_split;
-    a.tps = p.tps;
+    a.groups = p.groups;
+    a.share = p.share;
+    a.tiles = p.tiles;
+    a.pieces = p.pieces;
     a.flags = c.flags;
     a.out = c.out;
     a.out_f32 = c.out_dt == CSA2_F32;
@@ -1184,12 +1245,12 @@ csa2_status tree_tc_run(csa2_ctx* ctx, const TreeCall& c, void* ws, cudaStream_t
         if (ctx->stall_budget > 0) a.budget = std::max<long long>(ctx->stall_budget, 1 << 17);
         ctx->stall_next = 0;
     }
-    if (fp4) st = dense ? launch_tt<true, true>(ctx, a, maps, s) : launch_tt<true, false>(ctx, a, maps, s);
-    else st = dense ? launch_tt<false, true>(ctx, a, maps, s) : launch_tt<false, false>(ctx, a, maps, s);
+    if (fp4) st = dense ? launch_tt<true, true>(p.clusters, a, maps, s) : launch_tt<true, false>(p.clusters, a, maps, s);
+    else st = dense ? launch_tt<false, true>(p.clusters, a, maps, s) : launch_tt<false, false>(p.clusters, a, maps, s);
     if (st != CSA2_OK) return st;
-    if (p.n_split > 1) {
-        const MergeArgs m = {a.part_o, a.part_l, a.l.rope_cs, a.sink, p.groups, c.H, p.G, p.gps, c.r.T, p.n_split, c.flags,
-                             c.out, a.out_f32, c.lse};
+    if (p.pieces > 1) {
+        const MergeArgs m = {a.part_o, a.part_l, a.l.rope_cs, a.sink, p.groups, c.H, p.G, p.gps, c.r.T, p.pieces, p.share, p.tiles,
+                             c.flags, c.out, a.out_f32, c.lse};
         const int64_t rows = p.groups * p.G * c.H;
         st = launch_pdl(tree_merge_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, m);
         if (st != CSA2_OK) return st;
