@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const SimtArgs
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h0 = blockIdx.y * TS_HG;
     const TreeNode n = tree_node(c.r, blockIdx.z);
-    if (threadIdx.x < 32) rope_cos_sin(c.rope, n.t, lane, s.cs[lane], s.sn[lane]);
+    if (threadIdx.x < 32) ag_cos_sin(c.rope, n.t, lane, s.cs[lane], s.sn[lane]);
     if (threadIdx.x < TS_HG) {
         s.m[threadIdx.x] = -INFINITY;
         s.l[threadIdx.x] = 0.0f;
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const SimtArgs a, int
     const int64_t r = (int64_t)blockIdx.x * 8 + warp;
     if (r >= rows) return;
     const bool rope = a.c.flags & CSA2_ROPE;
-    if (rope) rope_cos_sin(a.c.rope, a.c.r.pos[r / a.c.H], lane, cs[warp][lane], sn[warp][lane]);
+    if (rope) ag_cos_sin(a.c.rope, a.c.r.pos[r / a.c.H], lane, cs[warp][lane], sn[warp][lane]);
     __syncwarp();
     attn_combine_row<TO>(a.part + r * (int64_t)a.n_split * ATTN_PART, a.n_split, a.c.sink ? a.c.sink[r % a.c.H] : -INFINITY,
                          rope ? cs[warp] : nullptr, sn[warp], reinterpret_cast<TO*>(a.c.out) + r * TS_C,
@@ -436,7 +436,7 @@ extern "C" csa2_status csa2_tree_attn(csa2_ctx* ctx, const void* q, csa2_dtype q
     t.sink = sink;
     t.B = B;
     t.H = H;
-    t.rope = make_rope_table(rope_base);
+    t.rope = make_ag_rope(rope_base);
     t.flags = flags;
     t.out = out;
     t.out_dt = out_dt;

@@ -31,7 +31,7 @@ struct TreeCall {
     csa2_dtype swa_dt;
     const float* sink;
     int B, H;
-    RopeTable rope;
+    AgRope rope;
     unsigned flags;
     void* out;
     csa2_dtype out_dt;

@@ -16,16 +16,17 @@
 // 4 million of them stay below 2^55), and the splits of a group's slots simply add up.
 //
 // tree_prep_kernel runs first: q^ (normalised, rotated) as the swizzled image of the A operand, the
-// RoPE table, and for every slot its row (-1: none), f, and as bits which nodes attend to it.  (A row's
-// squares need all of its dims, of which a CTA has half: with the sums exchanged like the logits, and
-// the rows through registers for them, the loaders were what a tile waited for.)
+// RoPE table, and for every slot its row (-1: none), f (the window's rows: once for all nodes), and as
+// bits which nodes attend to it.  (A row's squares need all of its dims, of which a CTA has half: with
+// the sums exchanged like the logits, and the rows through registers for them, the loaders were what a
+// tile waited for.)
 //
-// Warps (one CTA an SM; 640 threads, FP4 896, of which the first four give registers to the softmax):
+// Warps (640 threads, one CTA an SM):
 //   0       query images (bulk copies)
 //   1       issues the MMAs; owns tensor memory (O: columns 0-255, S / P': two buffers of 128)
 //   2       the tiles' masks and factors
 //   4-11    softmax, two warps a lane quarter (64 slots each)
-//   12-     loaders, half of them for the even and half for the odd tiles: bf16 rows that follow one
+//   12-19   loaders, four warps for the even and four for the odd tiles, 32 rows each: bf16 rows that follow one
 //           another by tensor copies, others by 16-byte asynchronous copies into the swizzled tile, FP4
 //           rows dequantised (exactly) from registers that are filled a tile ahead.  They also store the
 //           output, a row a thread: while an item's last output is read no buffer is free to be filled,
@@ -48,11 +49,8 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int TT_C = 512, TT_HALF = 256;
 constexpr int TT_ROWS = 128, TT_TILE = 128;
 constexpr int TT_G = 8;                          // nodes of a group at most
-constexpr int tt_loaders(bool fp4) { return fp4 ? 16 : 8; }              // warps
-constexpr int tt_threads(bool fp4) { return 32 * (12 + tt_loaders(fp4)); }
-// FP4: registers a thread at launch, of the first four warps, of the others
-constexpr int TT_REGS = 72, TT_REGS_FEW = 24, TT_REGS_MANY = 80;
-static_assert(TT_REGS_FEW + 6 * TT_REGS_MANY <= 7 * TT_REGS, "no more than the launch gives");
+constexpr int TT_LOADERS = 8;                    // warps
+constexpr int TT_THREADS = 32 * (12 + TT_LOADERS);
 constexpr int TT_CHUNK = TT_TILE * 128;          // 16 KB: 128 rows x 64 dims
 constexpr int TT_TILE_BYTES = 4 * TT_CHUNK;
 constexpr float LOG2E = 1.4426950408889634f;
@@ -78,11 +76,13 @@ struct TtLists {
     float* ef;                    // [eg][lde] their factors f
     uint32_t* eok;                // [eg][lde / 32] which of them there are
     int32_t* wrow;                // [groups][ldw] rows of the window slots: the ring's, then drafts
-    float* wf;                    // [groups][ldw]
     uint32_t* wmask;              // [groups][ldw / 32][TT_G] who attends to them
-    int4* info;                   // [groups] entry slots (a multiple of 32), all, the ring's
+    float* rf;                    // [B][window] factors of the ring's last rows: position ctx_len - window + j
+    float* df;                    // [B*T] of the drafts
+    int4* info;                   // [groups] entry slots (a multiple of 32), all, the ring's, their first j in rf
     float* rope_cs;               // [B*T, 64] cos, sin of the 32 angles
     int lde, ldw;
+    int64_t drafts;               // B*T
     int H, G, R8, gps;            // heads, nodes of a group, image rows, groups of a sequence
 };
 
@@ -197,7 +197,7 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // out), and cluster c has `share` of them from c * share on: its items are the groups that lie there.
 struct TtItem {
     int v, b, n0, gv;             // group, sequence, first node in it, nodes
-    int kq, slots, ring;          // entry slots, all slots, the ring's among the others
+    int kq, slots, ring, rf;      // entry slots, all slots, the ring's among the others, the first one's j in rf
     int t0, nt;                   // tiles t0 .. t0 + nt - 1
 };
 
@@ -224,6 +224,7 @@ struct TtWalk {
             r.kq = info.x;
             r.slots = info.y;
             r.ring = info.z;
+            r.rf = info.w;
             r.t0 = at;
             r.nt = max(0, min((info.y + TT_TILE - 1) / TT_TILE, to) - at);
             left -= to - at;
@@ -235,6 +236,11 @@ struct TtWalk {
         return false;
     }
 };
+
+// Factor of window slot j of an item, whose row is `row`.
+__device__ __forceinline__ float window_factor(const TtArgs& a, const TtItem& it, int j, int row) {
+    return j < it.ring ? a.l.rf[(int64_t)it.b * a.r.window + it.rf + j] : (row >= 0 ? a.l.df[row] : 0.0f);
+}
 
 // Output scale 1 / (L + e^zs) (for O of P' = p f: times ln 2 sqrt(512)) and log-sum-exp of a row with
 // the sum L of its exponentials and the sink logit zs; a row without either gives 0 and -inf.
@@ -255,199 +261,141 @@ struct PrepArgs {
     const uint8_t* swa;
     const uint8_t* draft;
     int fp4;
-    int64_t q_blocks, w_blocks;   // blocks of query rows, of window slots (the rest: entry slots)
-    int wb, eb;                   // blocks of a group's window slots, of a list of entry slots
-    RopeTable rope;
+    // warps: of query rows, of entry slots (32 each), of window slots (32), of the ring's rows (8), of drafts (8)
+    int64_t q_warps, e_warps, w_warps, r_warps, d_warps;
+    int ew, ww, rw;               // of a list of entries, of a group's window, of a sequence's ring rows
+    AgRope rope;
     unsigned flags;
     unsigned* st;
 };
 
 // The squares of a lane's 16 values of a bf16 or an FP4 row.
-__device__ __forceinline__ float lane_squares_bf16(const uint8_t* row, int lane) {
-    const uint4* p = reinterpret_cast<const uint4*>(row) + 2 * lane;
-    const uint4 u[2] = {__ldg(p), __ldg(p + 1)};
+__device__ __forceinline__ float lane_squares(const uint4& u0, const uint4& u1) {
     float q = 0.0f;
+    const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xFFFF0000u);
-            q = fmaf(lo, lo, fmaf(hi, hi, q));
-        }
+    for (int k = 0; k < 8; ++k) {
+        const float lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xFFFF0000u);
+        q = fmaf(lo, lo, fmaf(hi, hi, q));
     }
     return q;
 }
-__device__ __forceinline__ float lane_squares_fp4(const uint8_t* row, int lane) {
-    // 16 codes and their scale a lane; 4 x code^2 by table, summed as bytes
-    const uint2 c = __ldg(reinterpret_cast<const uint2*>(row) + lane);
-    const float s = e4m3_to_f32(__ldg(row + TT_C / 2 + lane));
-    uint32_t q = 0;
+__device__ __forceinline__ float lane_squares(const uint2& c, uint32_t scale) {
+    const float s = e4m3_to_f32(scale);
+    uint32_t q = 0;                              // 4 x code^2 by table, summed as bytes
     const uint32_t w[4] = {c.x & 0x77777777u, (c.x >> 16) & 0x7777u, c.y & 0x77777777u, (c.y >> 16) & 0x7777u};
 #pragma unroll
     for (int i = 0; i < 4; ++i) q = __dp4a(__byte_perm(0x09040100u, 0x90402410u, w[i]), 0x01010101u, q);
     return (float)q * 0.25f * (s * s);
 }
 
-// 128 slots of a list: rows[s] (>= 0: real) become addresses by `address`; their factors f and rows go to
-// the list from slot s0 on (n of them).  A row with an infinity or a NaN keeps out of the products (0 x NaN
-// would reach the nodes that do not attend to it): its row is none, and its factor, NaN, is for those that
-// do.  Warp w has slots 16 w .. 16 w + 15, four rows in flight.
-template <typename Address>
-__device__ __forceinline__ void prep_factors(const int32_t* rows, int s0, int n, int32_t* out_row, float* out_f, bool fp4,
-                                             const Address& address) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = 16 * warp, mine = lane < 16 && s0 + b + lane < n ? rows[b + lane] : -1;
+// Factors f of `n` rows (a multiple of 8, at most 32) at base + row * bytes, lane j's `row` that of row j
+// (-1: none, f 0), eight rows in flight.  A row with an infinity or a NaN has f NaN.
+__device__ __forceinline__ float row_factors(const uint8_t* base, int64_t bytes, bool fp4, int row, int n) {
+    const int lane = threadIdx.x & 31;
     float sum = 0.0f;
-    for (int i = 0; i < 16 && s0 + b + i < n; i += 4) {
-        float q[4];
+    for (int i = 0; i < n; i += 8) {
+        float q[8];
+        if (fp4) {
+            uint2 c[8];
+            uint32_t s[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int row = __shfl_sync(FULL, mine, i + j);
-            q[j] = 0.0f;
-            if (row >= 0) {
-                const uint8_t* p = address(s0 + b + i + j, row);
-                q[j] = fp4 ? lane_squares_fp4(p, lane) : lane_squares_bf16(p, lane);
+            for (int j = 0; j < 8; ++j) {
+                const uint8_t* p = base + max(0, __shfl_sync(FULL, row, i + j)) * bytes;
+                c[j] = __ldg(reinterpret_cast<const uint2*>(p) + lane);
+                s[j] = __ldg(p + TT_C / 2 + lane);
             }
-        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float t = warp_sum(q[j]);
-            if (lane == i + j) sum = t;
+            for (int j = 0; j < 8; ++j) q[j] = lane_squares(c[j], s[j]);
+        } else {
+            uint4 u[8][2];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint4* p = reinterpret_cast<const uint4*>(base + max(0, __shfl_sync(FULL, row, i + j)) * bytes) + lane;
+                u[j][0] = __ldg(p);
+                u[j][1] = __ldg(p + 32);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) q[j] = lane_squares(u[j][0], u[j][1]);
         }
+        // sums over the lanes: of two rows' parts a lane keeps one and sends the other; lane l ends with
+        // row l / 4's
+#pragma unroll
+        for (int o = 16, m = 4; m > 0; o >>= 1, m >>= 1) {
+            const bool upper = lane & o;
+#pragma unroll
+            for (int j = 0; j < m; ++j) q[j] = (upper ? q[j + m] : q[j]) + __shfl_xor_sync(FULL, upper ? q[j] : q[j + m], o);
+        }
+        q[0] += __shfl_xor_sync(FULL, q[0], 2);
+        q[0] += __shfl_xor_sync(FULL, q[0], 1);
+        const float t = __shfl_sync(FULL, q[0], 4 * (lane & 7));
+        if ((lane & 24) == i) sum = t;
     }
-    if (lane < 16 && s0 + b + lane < n) {
-        const bool fin = sum < INFINITY;
-        out_row[s0 + b + lane] = fin ? mine : -1;
-        out_f[s0 + b + lane] = mine < 0 ? 0.0f
-                               : fin   ? (LOG2E / sqrtf((float)TT_C)) / sqrtf(sum / (float)TT_C + 1e-6f)
-                                       : __int_as_float(0x7FC00000);
-    }
+    if (row < 0) return 0.0f;
+    return sum < INFINITY ? (LOG2E / sqrtf((float)TT_C)) / sqrtf(sum / (float)TT_C + 1e-6f) : __int_as_float(0x7FC00000);
 }
 
-// A block: 8 query rows (a warp each), or 128 slots of a group's window, or 128 entry slots of a node
-// (dense: of a sequence).
+// A warp: a query row; 32 entry slots of a node (dense: of a sequence); 32 slots of a group's window; 8 rows
+// of a ring; or 8 drafts.
 __global__ void __launch_bounds__(256) tree_prep_kernel(const PrepArgs a) {
     pdl_wait();
     pdl_trigger();
-    __shared__ int32_t rows[128];
-    __shared__ int64_t t[TT_G];
-    __shared__ int most;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, T = a.r.T;
+    const int lane = threadIdx.x & 31, T = a.r.T;
     const bool dense = a.r.n_visible;
-    int64_t blk = blockIdx.x;
-    if (blk < a.q_blocks) {
-        const int v = (int)(blk / (a.l.R8 / 8)), b = v / a.l.gps, n0 = (v - b * a.l.gps) * a.l.G, gv = min(a.l.G, T - n0);
-        const int64_t bt0 = (int64_t)b * T + n0;
-        const int row = 8 * (int)(blk - (int64_t)v * (a.l.R8 / 8)) + warp, g = row / a.l.H, h = row - g * a.l.H;
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = 0.0f;
-        if (g < gv) {
-            const int64_t pos = a.r.pos[bt0 + g];
-            const uint4* p = reinterpret_cast<const uint4*>(a.q + ((bt0 + g) * a.l.H + h) * (int64_t)TT_C + 16 * lane);
-            float ss = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint4 u = p[i];
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-                    x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-            const float r = 1.0f / sqrtf(warp_sum(ss) / (float)TT_C + 1e-6f);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] *= r;
-            if (a.flags & CSA2_ROPE) {
-                // lane j has angle j; lanes 28 .. 31 rotate the pairs of dims 448 .. 511
-                float c, s;
-                rope_cos_sin(a.rope, pos, lane, c, s);
-                if (h == 0) {
-                    a.l.rope_cs[(bt0 + g) * 64 + lane] = c;
-                    a.l.rope_cs[(bt0 + g) * 64 + 32 + lane] = s;
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int j = (8 * (lane - 28) + i) & 31;
-                    const float cj = __shfl_sync(FULL, c, j), sj = __shfl_sync(FULL, s, j);
-                    if (lane >= 28) {
-                        const float x0 = x[2 * i], x1 = x[2 * i + 1];
-                        x[2 * i] = x0 * cj - x1 * sj;
-                        x[2 * i + 1] = x1 * cj + x0 * sj;
-                    }
-                }
-            }
-        }
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-        uint8_t* img = a.l.qimg + v * (int64_t)a.l.R8 * 1024 + (lane >> 2) * (int64_t)a.l.R8 * 128;      // chunk of 64 dims
-        const uint32_t u = 2 * (lane & 3);
-        *reinterpret_cast<uint4*>(img + sw128_offset(row, u)) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(img + sw128_offset(row, u + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
-        return;
-    }
-    blk -= a.q_blocks;
-    if (blk >= a.w_blocks) {
+    int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    // the long chains of loads first
+    if (w < a.e_warps) {
         // entries: those the node selected, or those that any node of the sequence sees
-        blk -= a.w_blocks;
-        const int64_t eg = blk / a.eb, b = dense ? eg : eg / T;
-        const int s0 = (int)(blk - eg * a.eb) * 128, s = s0 + threadIdx.x;
+        const int64_t eg = w / a.ew, b = dense ? eg : eg / T;
+        const int s0 = (int)(w - eg * a.ew) * 32, s = s0 + lane;
         int live = 0;
         if (dense) {
-            if (threadIdx.x == 0) most = 0;
-            __syncthreads();
-            for (int i = threadIdx.x; i < T; i += blockDim.x) live = max(live, tree_node(a.r, b * T + i).kq);
-            atomicMax(&most, live);
-            __syncthreads();
-            live = most;
+            for (int i = lane; i < T; i += 32) live = max(live, tree_node(a.r, b * T + i).kq);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) live = max(live, __shfl_xor_sync(FULL, live, o));
         } else {
             live = tree_node(a.r, eg).kq;
         }
-        const int n = (live + 31) / 32 * 32;
-        if (s0 >= n) return;
-        if (threadIdx.x < 128) {
-            const int64_t row = s < live ? tree_entry_row(a.r, b, dense ? s : a.r.idx[eg * a.r.k + s], a.st, true) : -1;
-            rows[threadIdx.x] = (int32_t)row;
-            const uint32_t bits = __ballot_sync(FULL, row >= 0);
-            if (lane == 0 && s < n) a.l.eok[eg * (a.l.lde / 32) + s / 32] = bits;
-        }
-        __syncthreads();
-        const int64_t bytes = a.fp4 ? fp4_row_bytes(TT_C) : TT_C * 2;
-        prep_factors(rows, s0, n, a.l.erow + eg * a.l.lde, a.l.ef + eg * a.l.lde, a.fp4,
-                     [&](int, int32_t row) { return a.kv + row * bytes; });
+        if (s0 >= live) return;
+        const int row = s < live ? (int)tree_entry_row(a.r, b, dense ? s : a.r.idx[eg * a.r.k + s], a.st, true) : -1;
+        const uint32_t bits = __ballot_sync(FULL, row >= 0);
+        if (lane == 0) a.l.eok[eg * (a.l.lde / 32) + s0 / 32] = bits;
+        const float f = bits ? row_factors(a.kv, a.fp4 ? fp4_row_bytes(TT_C) : TT_C * 2, a.fp4, row, 32) : 0.0f;
+        // (0 x NaN would reach the nodes that do not attend to the row: it keeps out of the products, and its
+        // factor, NaN, is for those that do)
+        a.l.erow[eg * a.l.lde + s] = f == f ? row : -1;
+        a.l.ef[eg * a.l.lde + s] = f;
         return;
     }
-    // the window: the ring's rows that any node sees, then the drafts: those of the node's path, or of all
-    // nodes up to the group's last one
-    const int v = (int)(blk / a.wb), b = v / a.l.gps, n0 = (v - b * a.l.gps) * a.l.G, gv = min(a.l.G, T - n0);
-    const int64_t bt0 = (int64_t)b * T + n0;
-    const int s0 = (int)(blk - (int64_t)v * a.wb) * 128, s = s0 + threadIdx.x;
-    int kq = 0;
-    int64_t tmin = INT64_MAX;
-    for (int g = 0; g < gv; ++g) {
-        const TreeNode n = tree_node(a.r, bt0 + g);
-        if (threadIdx.x == 0) t[g] = n.t;
-        kq = max(kq, n.kq);
-        if (n.t >= 0) tmin = min(tmin, n.t);
-    }
-    const bool any = a.r.window > 0 && tmin != INT64_MAX;
-    const int64_t len = a.r.ctx_len[b], W = a.r.window;
-    const int64_t p0 = any ? max((int64_t)0, dense ? max(len - W + 1, tmin - W + 1) : tmin - W + 1) : 0;
-    const int nring = any ? (int)max((int64_t)0, min(W, min(len, tmin + 1) - p0)) : 0;
-    const int ndraft = !any ? 0 : (dense ? n0 + gv : (int)max((int64_t)0, min(W, tmin + 1 - max(len, p0))));
-    const int slots = nring + ndraft;
-    if (s0 == 0 && threadIdx.x == 0) {
-        const int kq32 = (kq + 31) / 32 * 32;
-        a.l.info[v] = make_int4(kq32, kq32 + slots, nring, 0);
-    }
-    if (s0 >= slots) return;
-    __syncthreads();
-    if (threadIdx.x < 128) {
+    w -= a.e_warps;
+    if (w < a.w_warps) {
+        // the window: the ring's rows that any node sees, then the drafts: those of the node's path, or of all
+        // nodes up to the group's last one
+        const int v = (int)(w / a.ww), b = v / a.l.gps, n0 = (v - b * a.l.gps) * a.l.G, gv = min(a.l.G, T - n0);
+        const int64_t bt0 = (int64_t)b * T + n0;
+        const int s0 = (int)(w - (int64_t)v * a.ww) * 32, s = s0 + lane;
+        // lane g: node g's position and entries
+        const TreeNode node = tree_node(a.r, bt0 + min(lane, gv - 1));
+        const int64_t t = lane < gv ? node.t : -1, len = node.len, W = a.r.window;
+        int kq = node.kq;
+        int64_t tmin = t >= 0 ? t : INT64_MAX;
+#pragma unroll
+        for (int o = TT_G / 2; o > 0; o >>= 1) {
+            kq = max(kq, __shfl_xor_sync(FULL, kq, o));
+            tmin = min(tmin, __shfl_xor_sync(FULL, tmin, o));
+        }
+        kq = __shfl_sync(FULL, kq, 0);
+        tmin = __shfl_sync(FULL, tmin, 0);
+        const bool any = W > 0 && tmin != INT64_MAX;
+        const int64_t p0 = any ? max((int64_t)0, max(len - W + 1, tmin - W + 1)) : 0;
+        const int nring = any ? (int)max((int64_t)0, min(len, tmin + 1) - p0) : 0;
+        const int ndraft = !any ? 0 : (dense ? n0 + gv : (int)max((int64_t)0, min(W, tmin + 1 - max(len, p0))));
+        const int slots = nring + ndraft;
+        if (s0 == 0 && lane == 0) {
+            const int kq32 = (kq + 31) / 32 * 32;
+            a.l.info[v] = make_int4(kq32, kq32 + slots, nring, (int)(p0 - (len - W)));
+        }
+        if (s0 >= slots) return;
         const int d = s - nring;
         int64_t p = -1, row = -1;                // position of the slot, its row
         int j = -1;                              // draft node
@@ -467,46 +415,124 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const PrepArgs a) {
             }
             if (j >= 0) row = (int64_t)b * T + j;
         }
-        uint32_t* mask = a.l.wmask + (v * (int64_t)(a.l.ldw / 32) + s / 32) * TT_G;
+        uint32_t* mask = a.l.wmask + (v * (int64_t)(a.l.ldw / 32) + s0 / 32) * TT_G;
         bool wanted = false;
         for (int g = 0; g < gv; ++g) {
-            bool on = row >= 0 && t[g] >= 0 && p <= t[g] && p > t[g] - W;
+            const int64_t tg = __shfl_sync(FULL, t, g);
+            bool on = row >= 0 && tg >= 0 && p <= tg && p > tg - W;
             if (on && j >= 0) on = a.r.path[(bt0 + g) * T + (p - len)] == j;
             const uint32_t bits = __ballot_sync(FULL, on);
-            if (lane == 0 && s < slots) mask[g] = bits;
+            if (lane == 0) mask[g] = bits;
             wanted |= on;
         }
-        rows[threadIdx.x] = wanted ? (int32_t)row : -1;
+        a.l.wrow[v * (int64_t)a.l.ldw + s] = wanted ? (int32_t)row : -1;
+        return;
     }
-    __syncthreads();
-    prep_factors(rows, s0, slots, a.l.wrow + v * (int64_t)a.l.ldw, a.l.wf + v * (int64_t)a.l.ldw, false,
-                 [&](int slot, int32_t row) { return (slot < nring ? a.swa : a.draft) + row * (int64_t)(TT_C * 2); });
+    w -= a.w_warps;
+    if (w < a.r_warps) {
+        const int64_t b = w / a.rw, W = a.r.window;
+        const int j0 = (int)(w - b * a.rw) * 8, j = j0 + (lane & 7);
+        const int64_t p = a.r.ctx_len[b] - W + j;
+        const int row = p >= 0 && j < W ? (int)(((p - a.r.swa_pos0) % a.r.swa_cap + a.r.swa_cap) % a.r.swa_cap) : -1;
+        const float f = row_factors(a.swa + b * a.r.swa_cap * (TT_C * 2), TT_C * 2, false, row, 8);
+        if (lane < 8 && j < W) a.l.rf[b * W + j] = f;
+        return;
+    }
+    w -= a.r_warps;
+    if (w < a.d_warps) {
+        const int64_t n = a.l.drafts, i = w * 8 + (lane & 7);
+        const float f = row_factors(a.draft, TT_C * 2, false, i < n ? (int)i : -1, 8);
+        if (lane < 8 && i < n) a.l.df[i] = f;
+        return;
+    }
+    w -= a.d_warps;
+    if (w >= a.q_warps) return;
+    const int v = (int)(w / a.l.R8), b = v / a.l.gps, n0 = (v - b * a.l.gps) * a.l.G, gv = min(a.l.G, T - n0);
+    const int64_t bt0 = (int64_t)b * T + n0;
+    const int row = (int)(w - (int64_t)v * a.l.R8), g = row / a.l.H, h = row - g * a.l.H;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+    if (g < gv) {
+        const int64_t pos = a.r.pos[bt0 + g];
+        const uint4* p = reinterpret_cast<const uint4*>(a.q + ((bt0 + g) * a.l.H + h) * (int64_t)TT_C + 16 * lane);
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4 u = p[i];
+            const uint32_t c[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[8 * i + 2 * j] = __uint_as_float(c[j] << 16);
+                x[8 * i + 2 * j + 1] = __uint_as_float(c[j] & 0xFFFF0000u);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+        const float r = 1.0f / sqrtf(warp_sum(ss) / (float)TT_C + 1e-6f);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] *= r;
+        if (a.flags & CSA2_ROPE) {
+            // lane j has angle j; lanes 28 .. 31 rotate the pairs of dims 448 .. 511
+            float c, s;
+            ag_cos_sin(a.rope, pos, lane, c, s);
+            if (h == 0) {
+                a.l.rope_cs[(bt0 + g) * 64 + lane] = c;
+                a.l.rope_cs[(bt0 + g) * 64 + 32 + lane] = s;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int j = (8 * (lane - 28) + i) & 31;
+                const float cj = __shfl_sync(FULL, c, j), sj = __shfl_sync(FULL, s, j);
+                if (lane >= 28) {
+                    const float x0 = x[2 * i], x1 = x[2 * i + 1];
+                    x[2 * i] = x0 * cj - x1 * sj;
+                    x[2 * i + 1] = x1 * cj + x0 * sj;
+                }
+            }
+        }
+    }
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+    uint8_t* img = a.l.qimg + v * (int64_t)a.l.R8 * 1024 + (lane >> 2) * (int64_t)a.l.R8 * 128;      // chunk of 64 dims
+    const uint32_t u = 2 * (lane & 3);
+    *reinterpret_cast<uint4*>(img + sw128_offset(row, u)) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(img + sw128_offset(row, u + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 // ---------------------------------------------------------------- the main kernel
 
-// Eight E2M1 codes (value 2k in the low nibble of byte k) times their scale as bf16 pairs.  Exact: a
-// product has 6 significant bits.
-__device__ __forceinline__ uint4 fp4_8(uint32_t codes, __half2 scale) {
-    uint32_t c[4], w[4];
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
-        : "r"(codes));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(__hmul2(*reinterpret_cast<__half2*>(&c[i]), scale));
-        w[i] = pack_bf16(f.x, f.y);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+// The sixteen E2M1 codes of a scale block (eight a word, value 2k in the low nibble of byte k) times
+// their E4M3 scale as bf16 pairs: the eight magnitudes times the scale (exact: 6 significant bits) as a
+// table of low and one of high bytes, from which a code's 3 magnitude bits pick by byte permutes, its sign
+// XORed in.  (Conversions of single codes run in the pipe that the softmax's exponentials need.)
+__device__ __forceinline__ void fp4_16(uint32_t wa, uint32_t wb, uint32_t scale, uint4& va, uint4& vb) {
+    const uint32_t s2 = __byte_perm(__float_as_uint(e4m3_to_f32(scale)), 0u, 0x3232);     // (bf16 scale, bf16 scale)
+    const uint32_t t01 = bf16x2_mul(0x3F000000u, s2);                     // (0, 0.5) x scale
+    const uint32_t t23 = bf16x2_mul(0x3FC03F80u, s2);                     // (1, 1.5)
+    const uint32_t t45 = bf16x2_mul(0x40404000u, s2);                     // (2, 3)
+    const uint32_t t67 = bf16x2_mul(0x40C04080u, s2);                     // (4, 6)
+    const uint32_t lo0 = __byte_perm(t01, t23, 0x6420), hi0 = __byte_perm(t01, t23, 0x7531);
+    const uint32_t lo1 = __byte_perm(t45, t67, 0x6420), hi1 = __byte_perm(t45, t67, 0x7531);
+    const auto word = [&](uint32_t w) {
+        const uint32_t m = w & 0x77777777u, mh = m >> 16, w4 = w << 4;
+        uint32_t lo = __byte_perm(lo0, lo1, m), hi = __byte_perm(hi0, hi1, m);
+        uint4 r;
+        r.x = __byte_perm(lo, hi, 0x5140) ^ (__byte_perm(w4, w, 0x4000) & 0x80008000u);
+        r.y = __byte_perm(lo, hi, 0x7362) ^ (__byte_perm(w4, w, 0x5010) & 0x80008000u);
+        lo = __byte_perm(lo0, lo1, mh);
+        hi = __byte_perm(hi0, hi1, mh);
+        r.z = __byte_perm(lo, hi, 0x5140) ^ (__byte_perm(w4, w, 0x6020) & 0x80008000u);
+        r.w = __byte_perm(lo, hi, 0x7362) ^ (__byte_perm(w4, w, 0x7030) & 0x80008000u);
+        return r;
+    };
+    va = word(wa);
+    vb = word(wb);
 }
 
 template <bool FP4, bool DENSE>
-__global__ void __launch_bounds__(tt_threads(FP4), 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
     tree_tc_kernel(const TtArgs a, const __grid_constant__ TtMaps maps) {
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* sQ = smem + OFF_Q;
@@ -531,20 +557,19 @@ __global__ void __launch_bounds__(tt_threads(FP4), 1) __cluster_dims__(2, 1, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
     const int cluster = blockIdx.x >> 1;
-    constexpr int LOADERS = tt_loaders(FP4);
 
     if (threadIdx.x == 0) {
         if (smem_u32(smem) & 1023u) csa2_flag(a.st, CSA2_DEVBIT_TIMEOUT);
         mbar_init(qfull, 1);
         mbar_init(qempty, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&kfull[i], LOADERS / 2);
+            mbar_init(&kfull[i], TT_LOADERS / 2);
             for (int j = 0; j < 4; ++j) mbar_init(&kempty[4 * i + j], 1);
             mbar_init(&sfull[i], 2);
             mbar_init(&pfull[i], 8);
         }
         mbar_init(ofull, 1);
-        mbar_init(oempty, LOADERS);
+        mbar_init(oempty, TT_LOADERS);
         mbar_init(lred, 8);
         for (int i = 0; i < 8; ++i) {
             mbar_init(&xfull[i], 1);
@@ -567,8 +592,6 @@ __global__ void __launch_bounds__(tt_threads(FP4), 1) __cluster_dims__(2, 1, 1)
     TtItem it;
     walk.start(a, cluster);
 
-    if (warp < 4) {
-        if (FP4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TT_REGS_FEW));
     if (warp == 0) {
         // ============================ query images ============================
         if (lane == 0) {
@@ -683,12 +706,19 @@ __global__ void __launch_bounds__(tt_threads(FP4), 1) __cluster_dims__(2, 1, 1)
                         m = a.l.wmask[((int64_t)it.v * (a.l.ldw / 32) + (s - it.kq) / 32) * TT_G + n];
                     }
                 }
-                // lane l: the factors of slots 4 l .. 4 l + 3 (lists are padded to multiples of 32)
+                // lane l: the factors of slots 4 l .. 4 l + 3 (lists of entries are padded to multiples of 32)
                 const int s4 = (it.t0 + tt) * TT_TILE + 4 * lane;
                 float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (s4 < it.slots)
-                    f = *reinterpret_cast<const float4*>(s4 < it.kq ? a.l.ef + eg * a.l.lde + s4
-                                                                    : a.l.wf + (int64_t)it.v * a.l.ldw + (s4 - it.kq));
+                if (s4 < it.kq) {
+                    f = *reinterpret_cast<const float4*>(a.l.ef + eg * a.l.lde + s4);
+                } else {
+                    float* fw = &f.x;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int j = s4 + i - it.kq;
+                        if (s4 + i < it.slots) fw[i] = window_factor(a, it, j, a.l.wrow[(int64_t)it.v * a.l.ldw + j]);
+                    }
+                }
                 // (its products done, a tile's softmax has read its masks)
                 const bool wt = g < 2 || mbar_wait(&kempty[4 * (g & 1) + 3], ((g - 2) >> 1) & 1, a.budget, a.st);
                 ok = __all_sync(FULL, wt);
@@ -699,10 +729,8 @@ __global__ void __launch_bounds__(tt_threads(FP4), 1) __cluster_dims__(2, 1, 1)
                 if (lane == 0) mbar_arrive(&sfull[g & 1]);
             }
         }
-    }
-    } else if (warp < 12) {
+    } else if (warp >= 4 && warp < 12) {
         // ============================ softmax ============================
-        if (FP4) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TT_REGS_MANY));
         const int quad = warp & 3, hh = (warp - 4) >> 2, w = 4 * hh + quad;
         const int r = quad * 32 + lane;                       // query row
         const bool live = quad * 32 < a.l.G * a.l.H;          // a warp without query rows only keeps step
@@ -811,12 +839,11 @@ __global__ void __launch_bounds__(tt_threads(FP4), 1) __cluster_dims__(2, 1, 1)
             if (lane == 0) mbar_arrive(lred);
             ++qi;
         }
-    } else {
+    } else if (warp >= 12) {
         // ============================ loaders, output ============================
-        if (FP4) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TT_REGS_MANY));
-        constexpr int ROWS = TT_TILE / (LOADERS / 2);         // of a tile, a warp
-        const int lw = warp - 12, grp = lw / (LOADERS / 2);   // tiles of this parity
-        const uint32_t row0 = ROWS * (lw % (LOADERS / 2));    // rows row0 .. row0 + ROWS - 1 of them
+        constexpr int ROWS = TT_TILE / (TT_LOADERS / 2);         // of a tile, a warp
+        const int lw = warp - 12, grp = lw / (TT_LOADERS / 2);   // tiles of this parity
+        const uint32_t row0 = ROWS * (lw % (TT_LOADERS / 2));    // rows row0 .. row0 + ROWS - 1 of them
         uint8_t* tile = sK + grp * TT_TILE_BYTES;
         // The next tile of this parity; lane j: row j of this warp (-1: none)
         int tt = 0, g = 0;
@@ -837,7 +864,14 @@ __global__ void __launch_bounds__(tt_threads(FP4), 1) __cluster_dims__(2, 1, 1)
             row = -1;
             slot = (it.t0 + tt) * TT_TILE + row0 + (lane & (ROWS - 1));
             if (slot < it.kq) row = a.l.erow[(DENSE ? it.b : (int64_t)it.b * a.r.T + it.n0) * a.l.lde + slot];
-            else if (slot < it.slots) row = a.l.wrow[(int64_t)it.v * a.l.ldw + (slot - it.kq)];
+            else if (slot < it.slots) {
+                row = a.l.wrow[(int64_t)it.v * a.l.ldw + (slot - it.kq)];
+                // (a row with a NaN keeps out of the products, as among the entries)
+                if (row >= 0) {
+                    const float f = window_factor(a, it, slot - it.kq, row);
+                    if (f != f) row = -1;
+                }
+            }
             ++tt;
         };
         // FP4 rows through registers: 8 lanes a row, 4 rows an instruction, 16 code bytes and 2 scales a lane
@@ -880,7 +914,7 @@ __global__ void __launch_bounds__(tt_threads(FP4), 1) __cluster_dims__(2, 1, 1)
         int oq = 0, oend = 0;         // items with tiles so far, tiles up to the next one's end
         bool omore = owalk.next(a, oit, true);
         if (omore) oend = oit.nt;
-        constexpr int PART = TT_HALF / (LOADERS / 4);         // dims of a warp
+        constexpr int PART = TT_HALF / (TT_LOADERS / 4);         // dims of a warp
         const int quad = warp & 3, r = quad * 32 + lane, hq = r / a.l.H, h = r - hq * a.l.H;
         const int d0 = TT_HALF * rank + PART * (lw >> 2);
         const bool live = quad * 32 < a.l.G * a.l.H, first_part = rank == 0 && lw < 4;
@@ -982,15 +1016,18 @@ __global__ void __launch_bounds__(tt_threads(FP4), 1) __cluster_dims__(2, 1, 1)
                 uint8_t* base = tile + c * TT_CHUNK;
 #pragma unroll
                 for (int i = 0; i < FP4_ROWS; ++i) {
-                    const __half2 f0 = __float2half2_rn(e4m3_to_f32(sc[i] & 0xFFu)), f1 = __float2half2_rn(e4m3_to_f32(sc[i] >> 8));
-                    const uint32_t r = row0 + 4 * i + (lane >> 3);
+                    uint8_t* at_row = base + ((row0 + 4 * i + (lane >> 3)) << 7);
+                    const uint32_t swz = (4 * i + (lane >> 3)) & 7;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        // units of 8 values in an order that differs between the lanes of a row: no bank twice
-                        const int u = (k + c) & 3;
-                        const uint32_t lo = (u & 1) ? d[i].y : d[i].x, hi = (u & 1) ? d[i].w : d[i].z;
-                        *reinterpret_cast<uint4*>(base + sw128_offset(r, (uint32_t)(4 * (piece & 1) + u))) =
-                            fp4_8((u & 2) ? hi : lo, (u & 2) ? f1 : f0);
+                    for (int hb = 0; hb < 2; ++hb) {
+                        // units of 8 values, in an order that differs between the lanes of a row: no bank twice
+                        const int blk = hb ^ (c >> 1), odd = c & 1;
+                        const uint32_t w0 = blk ? d[i].z : d[i].x, w1 = blk ? d[i].w : d[i].y;
+                        uint4 va, vb;
+                        fp4_16(odd ? w1 : w0, odd ? w0 : w1, (blk ? sc[i] >> 8 : sc[i]) & 0xFFu, va, vb);
+                        const uint32_t u = 4 * (piece & 1) + 2 * blk + odd;
+                        *reinterpret_cast<uint4*>(at_row + ((u ^ swz) << 4)) = va;
+                        *reinterpret_cast<uint4*>(at_row + (((u ^ 1) ^ swz) << 4)) = vb;
                     }
                 }
                 look_up();
@@ -1071,14 +1108,15 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeArgs a) {
         for (int s = 0; s < 4; ++s) {
             const int64_t p = (v * a.pieces + s0 + s) * rows + r;
             l[s] = s0 + s < n ? a.part_l[p] : 0.0f;
-            // (a piece without slots has no output)
+            // (a piece without slots has left its output as it was)
             const float4* o = reinterpret_cast<const float4*>(a.part_o + p * TT_C) + lane;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[s][j] = l[s] != 0.0f ? __ldcs(o + 32 * j) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int j = 0; j < 4; ++j) x[s][j] = s0 + s < n ? __ldcs(o + 32 * j) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             L += l[s];
+            if (l[s] == 0.0f) continue;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 acc[4 * j] += x[s][j].x;
@@ -1119,7 +1157,7 @@ size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 struct TtPlan {
     int G, R8, gps, lde, ldw, clusters, share, tiles, pieces;
     int64_t groups;
-    size_t erow, ef, eok, wrow, wf, wmask, info, rope, part_l, part_o, total;
+    size_t erow, ef, eok, wrow, wmask, rf, df, info, rope, part_l, part_o, total;
 };
 
 TtPlan tt_plan(const csa2_ctx* ctx, int B, int T, int H, int k, int window, bool dense) {
@@ -1147,9 +1185,10 @@ TtPlan tt_plan(const csa2_ctx* ctx, int B, int T, int H, int k, int window, bool
     p.ef = up(p.erow + eg * p.lde * 4, 256);
     p.eok = up(p.ef + eg * p.lde * 4, 256);
     p.wrow = up(p.eok + eg * (p.lde / 32) * 4, 256);
-    p.wf = up(p.wrow + (size_t)p.groups * p.ldw * 4, 256);
-    p.wmask = up(p.wf + (size_t)p.groups * p.ldw * 4, 256);
-    p.info = up(p.wmask + (size_t)p.groups * (p.ldw / 32) * TT_G * 4, 256);
+    p.wmask = up(p.wrow + (size_t)p.groups * p.ldw * 4, 256);
+    p.rf = up(p.wmask + (size_t)p.groups * (p.ldw / 32) * TT_G * 4, 256);
+    p.df = up(p.rf + (size_t)B * window * 4, 256);
+    p.info = up(p.df + (size_t)B * T * 4, 256);
     p.rope = up(p.info + (size_t)p.groups * 16, 256);
     p.part_l = up(p.rope + (size_t)B * T * 64 * 4, 256);
     const size_t rows = p.pieces > 1 ? (size_t)p.groups * p.pieces * p.G * H : 0;
@@ -1162,7 +1201,7 @@ template <bool FP4, bool DENSE>
 csa2_status launch_tt(int clusters, const TtArgs& a, const TtMaps& m, cudaStream_t s) {
     auto kern = tree_tc_kernel<FP4, DENSE>;
     CSA2_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TT_SMEM));
-    return launch_pdl(kern, dim3((unsigned)(2 * clusters)), dim3(tt_threads(FP4)), TT_SMEM, s, a, m);
+    return launch_pdl(kern, dim3((unsigned)(2 * clusters)), dim3(TT_THREADS), TT_SMEM, s, a, m);
 }
 
 }  // namespace
@@ -1186,7 +1225,9 @@ csa2_status tree_tc_run(csa2_ctx* ctx, const TreeCall& c, void* ws, cudaStream_t
     pa.l.ef = reinterpret_cast<float*>(base + p.ef);
     pa.l.eok = reinterpret_cast<uint32_t*>(base + p.eok);
     pa.l.wrow = reinterpret_cast<int32_t*>(base + p.wrow);
-    pa.l.wf = reinterpret_cast<float*>(base + p.wf);
+    pa.l.rf = reinterpret_cast<float*>(base + p.rf);
+    pa.l.df = reinterpret_cast<float*>(base + p.df);
+    pa.l.drafts = (int64_t)c.B * c.r.T;
     pa.l.wmask = reinterpret_cast<uint32_t*>(base + p.wmask);
     pa.l.info = reinterpret_cast<int4*>(base + p.info);
     pa.l.rope_cs = reinterpret_cast<float*>(base + p.rope);
@@ -1202,10 +1243,14 @@ csa2_status tree_tc_run(csa2_ctx* ctx, const TreeCall& c, void* ws, cudaStream_t
     pa.swa = reinterpret_cast<const uint8_t*>(c.swa);
     pa.draft = reinterpret_cast<const uint8_t*>(c.draft);
     pa.fp4 = fp4;
-    pa.wb = std::max(1, (p.ldw + 127) / 128);
-    pa.eb = (p.lde + 127) / 128;
-    pa.q_blocks = p.groups * (p.R8 / 8);
-    pa.w_blocks = p.groups * pa.wb;
+    pa.ew = p.lde / 32;
+    pa.ww = std::max(1, p.ldw / 32);
+    pa.rw = (c.r.window + 7) / 8;
+    pa.e_warps = (dense ? (int64_t)c.B : (int64_t)c.B * c.r.T) * pa.ew;
+    pa.w_warps = p.groups * pa.ww;
+    pa.r_warps = (int64_t)c.B * pa.rw;
+    pa.d_warps = c.r.window > 0 ? (pa.l.drafts + 7) / 8 : 0;
+    pa.q_warps = p.groups * p.R8;
     pa.rope = c.rope;
     pa.flags = c.flags;
     pa.st = ctx->status;
@@ -1215,9 +1260,9 @@ csa2_status tree_tc_run(csa2_ctx* ctx, const TreeCall& c, void* ws, cudaStream_t
                                  c.r.window > 0 ? (int64_t)c.B * c.r.T : 0};
     const void* map_at[3] = {c.kv, c.swa, c.draft};
     for (int i = 0; i < 3; ++i)
-        if (!csa2_make_bf16_map(&maps.m[i], map_rows[i] > 0 ? map_at[i] : c.q, std::max<int64_t>(1, map_rows[i]), TT_C, 64, fp4 ? 16 : 32))
+        if (!csa2_make_bf16_map(&maps.m[i], map_rows[i] > 0 ? map_at[i] : c.q, std::max<int64_t>(1, map_rows[i]), TT_C, 64, TT_TILE / (TT_LOADERS / 2)))
             return CSA2_ERR_CUDA;
-    const int64_t blocks = pa.q_blocks + pa.w_blocks + (dense ? (int64_t)c.B : (int64_t)c.B * c.r.T) * pa.eb;
+    const int64_t blocks = (pa.e_warps + pa.w_warps + pa.r_warps + pa.d_warps + pa.q_warps + 7) / 8;
     csa2_status st = launch_pdl(tree_prep_kernel, dim3((unsigned)blocks), dim3(256), 0, s, pa);
     if (st != CSA2_OK) return st;
     TtArgs a = {};
