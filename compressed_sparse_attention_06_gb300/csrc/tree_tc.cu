@@ -193,6 +193,28 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return r;
 }
 
+// Lanes 2 i and 2 i + 1 turn their 2 x 2 pieces: lane l's piece k becomes piece l & 1 of lane (l & ~1) + k;
+// four lanes their 4 x 4: piece l & 3 of lane (l & ~3) + k.  (A store of 16 bytes a row and lane would take
+// the time of 32 lines: 8,000 cycles for the output of 128 rows.)
+__device__ __forceinline__ void turn(uint4& p0, uint4& p1, int o) {
+    const bool upper = (threadIdx.x & o) != 0;
+    const uint4 send = upper ? p0 : p1;
+    uint4 got;
+    got.x = __shfl_xor_sync(FULL, send.x, o);
+    got.y = __shfl_xor_sync(FULL, send.y, o);
+    got.z = __shfl_xor_sync(FULL, send.z, o);
+    got.w = __shfl_xor_sync(FULL, send.w, o);
+    if (upper) p0 = got;
+    else p1 = got;
+}
+__device__ __forceinline__ void turn2(uint4 (&p)[2]) { turn(p[0], p[1], 1); }
+__device__ __forceinline__ void turn4(uint4 (&p)[4]) {
+    turn(p[0], p[1], 1);
+    turn(p[2], p[3], 1);
+    turn(p[0], p[2], 2);
+    turn(p[1], p[3], 2);
+}
+
 // The groups' tiles stand one behind the other, `tiles` a group (a shorter one leaves its last ones
 // out), and cluster c has `share` of them from c * share on: its items are the groups that lie there.
 struct TtItem {
@@ -845,11 +867,12 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         const int lw = warp - 12, grp = lw / (TT_LOADERS / 2);   // tiles of this parity
         const uint32_t row0 = ROWS * (lw % (TT_LOADERS / 2));    // rows row0 .. row0 + ROWS - 1 of them
         uint8_t* tile = sK + grp * TT_TILE_BYTES;
-        // The next tile of this parity; lane j: row j of this warp (-1: none)
+        // Three steps, each a tile of this parity ahead of the one before, so that no load is waited for: the
+        // rows' list is read (look_up), the rows are on their way (fetch), they go into the tile.
         int tt = 0, g = 0;
-        int row = -1, slot = 0;
-        bool more = true;
         it.nt = 0;
+        int row = -1, kind = 0, next_tile = 0;                // looked up: lane j's row (-1: none) and source, the tile
+        bool entry = false, more = true;
         const auto look_up = [&]() {
             for (;;) {
                 if (tt < it.nt && ((g ^ grp) & 1)) {
@@ -857,21 +880,23 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                     ++g;
                 }
                 if (tt < it.nt) break;
-                more = walk.next(a, it);
+                more = more && walk.next(a, it);
                 if (!more) return;
                 tt = 0;
             }
+            const int slot = (it.t0 + tt) * TT_TILE + row0 + (lane & (ROWS - 1)), j = slot - it.kq;
+            entry = slot - (lane & (ROWS - 1)) < it.kq;
+            kind = entry ? 0 : (j < it.ring ? 1 : 2);
             row = -1;
-            slot = (it.t0 + tt) * TT_TILE + row0 + (lane & (ROWS - 1));
-            if (slot < it.kq) row = a.l.erow[(DENSE ? it.b : (int64_t)it.b * a.r.T + it.n0) * a.l.lde + slot];
-            else if (slot < it.slots) {
-                row = a.l.wrow[(int64_t)it.v * a.l.ldw + (slot - it.kq)];
+            if (entry) {
+                row = a.l.erow[(DENSE ? it.b : (int64_t)it.b * a.r.T + it.n0) * a.l.lde + slot];
+            } else if (slot < it.slots) {
+                row = a.l.wrow[(int64_t)it.v * a.l.ldw + j];
                 // (a row with a NaN keeps out of the products, as among the entries)
-                if (row >= 0) {
-                    const float f = window_factor(a, it, slot - it.kq, row);
-                    if (f != f) row = -1;
-                }
+                const float f = window_factor(a, it, j, row);
+                if (f != f) row = -1;
             }
+            next_tile = g++;
             ++tt;
         };
         // FP4 rows through registers: 8 lanes a row, 4 rows an instruction, 16 code bytes and 2 scales a lane
@@ -882,17 +907,21 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         uint64_t at = 0;              // bf16: the address of lane j's row, 0: none
         int box_row = -1, box_map = 0;    // bf16: the first row, where the rows follow one another
         bool fp4_rows = false;
+        int gt = 0;                   // the tile they are for
+        bool fetched = false;
         const auto fetch = [&]() {
-            const bool entry = slot - (lane & (ROWS - 1)) < it.kq;
+            fetched = more;
+            if (!more) return;
+            gt = next_tile;
             fp4_rows = FP4 && entry;
             const uint8_t* src = nullptr;
             if (row >= 0)
-                src = (entry ? a.kv : (slot - it.kq < it.ring ? a.swa : a.draft)) +
+                src = (kind == 0 ? a.kv : (kind == 1 ? a.swa : a.draft)) +
                       (int64_t)row * (fp4_rows ? fp4_row_bytes(TT_C) : (int64_t)(TT_C * 2));
             at = (uint64_t)(uintptr_t)src;
-            box_map = entry ? 0 : (slot - it.kq < it.ring ? 1 : 2);
-            const int row_0 = __shfl_sync(FULL, row, 0), map_0 = __shfl_sync(FULL, box_map, 0);
-            box_row = __all_sync(FULL, row_0 >= 0 && row == row_0 + (lane & (ROWS - 1)) && box_map == map_0) ? row_0 : -1;
+            box_map = kind;
+            const int row_0 = __shfl_sync(FULL, row, 0), kind_0 = __shfl_sync(FULL, kind, 0);
+            box_row = __all_sync(FULL, row_0 >= 0 && row == row_0 + (lane & (ROWS - 1)) && kind == kind_0) ? row_0 : -1;
             if (fp4_rows) {
 #pragma unroll
                 for (int i = 0; i < FP4_ROWS; ++i) {
@@ -944,8 +973,15 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
             }
             if (live && !(part && oit.nt == 0)) {
                 const float* cs = a.l.rope_cs + bt * 64;
+                const bool wide = part || a.out_f32;          // fp32 rows
+                // rows quad * 32 + (lane & ~3) + k, k < 4, of the group; 16 bytes a lane, four lanes side by side
+                const int r4 = quad * 32 + (lane & ~3), n4 = min(4, oit.gv * a.l.H - r4);
+                uint8_t* dst = part ? reinterpret_cast<uint8_t*>(a.part_o + (prow - r + r4) * (int64_t)TT_C)
+                                    : reinterpret_cast<uint8_t*>(a.out) + (((int64_t)oit.b * a.r.T + oit.n0) * a.l.H + r4) * (int64_t)(wide ? TT_C * 4 : TT_C * 2);
+                const int64_t pitch = wide ? TT_C * 4 : TT_C * 2;
 #pragma unroll 1
                 for (int db = 0; db < PART / 16; ++db) {
+                    const int d = d0 + 16 * db;
                     float v[16];
                     if (oit.nt > 0) {
                         uint32_t o[16];
@@ -957,7 +993,6 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) v[i] = 0.0f;
                     }
-                    const int d = d0 + 16 * db;
                     if (!part && (a.flags & CSA2_ROPE) && d >= TT_C - 64) {
                         const float* c = cs + (d - (TT_C - 64)) / 2;
 #pragma unroll
@@ -967,19 +1002,29 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                             v[2 * j + 1] = x1 * c[j] - x0 * c[32 + j];
                         }
                     }
-                    if (valid && (part || a.out_f32)) {
-                        float* p = (part ? a.part_o + prow * (int64_t)TT_C : reinterpret_cast<float*>(a.out) + orow * (int64_t)TT_C) + d;
+                    if (wide) {
+                        uint4 p[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                    } else if (valid) {
-                        uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + orow * (int64_t)TT_C + d);
+                            p[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                                              __float_as_uint(v[4 * i + 3]));
+                        turn4(p);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k < n4) *reinterpret_cast<uint4*>(dst + k * pitch + d * 4 + 16 * (lane & 3)) = p[k];
+                    } else {
+                        uint4 p[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
                             p[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
                                               pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+                        turn2(p);
+                        // lane pairs hold rows (lane & ~1) and the next one, 32 bytes side by side
+                        const int r2 = lane & 2;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            if (r2 + k < n4) *reinterpret_cast<uint4*>(dst + (r2 + k) * pitch + d * 2 + 16 * (lane & 1)) = p[k];
                     }
-                    __syncwarp();
                 }
             }
             if (oit.nt > 0) {
@@ -1000,11 +1045,11 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
             return true;
         };
         look_up();
-        if (more) fetch();
+        fetch();
+        look_up();
         int last = -1;                                        // the last tile this warp filled its rows of
         bool ok = true;
-        while (more) {
-            const int gt = g++;                               // the tile of this pass
+        while (fetched) {
             ok = outputs(gt);
             if (!ok) break;
             const bool wt = gt < 2 || mbar_wait(&kempty[4 * grp + row0 / 32], ((gt - 2) >> 1) & 1, a.budget, a.st);
@@ -1030,8 +1075,11 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                         *reinterpret_cast<uint4*>(at_row + (((u ^ 1) ^ swz) << 4)) = vb;
                     }
                 }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&kfull[grp]);
+                fetch();
                 look_up();
-                if (more) fetch();
             } else if (box_row >= 0) {
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&kfull[grp], ROWS * TT_HALF * 2);
@@ -1039,9 +1087,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                     for (int c = 0; c < 4; ++c)
                         tma_load_2d(tile + c * TT_CHUNK + row0 * 128, &maps.m[box_map], TT_HALF * rank + 64 * c, box_row, &kfull[grp]);
                 }
+                fetch();
                 look_up();
-                if (more) fetch();
-                continue;
             } else {
                 // a row an instruction, 16 bytes a lane
                 uint8_t* base = tile + (lane >> 3) * TT_CHUNK;
@@ -1052,13 +1099,13 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                                        reinterpret_cast<const uint8_t*>((uintptr_t)(p ? p : (uint64_t)(uintptr_t)a.l.qimg)) + 512 * rank + 16 * lane, p != 0);
                 }
                 cp_async_commit();
+                fetch();
                 look_up();
-                if (more) fetch();
                 cp_async_wait<0>();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&kfull[grp]);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&kfull[grp]);
         }
         if (ok) outputs(INT_MAX);
         // tensor copies must land before the CTA exits
