@@ -26,11 +26,11 @@
 //   1       issues the MMAs; owns tensor memory (O: columns 0-255, S / P': two buffers of 128)
 //   2       the tiles' masks and factors
 //   4-11    softmax, two warps a lane quarter (64 slots each)
-//   12-19   loaders, four warps for the even and four for the odd tiles, 32 rows each: bf16 rows that follow one
-//           another by tensor copies, others by 16-byte asynchronous copies into the swizzled tile, FP4
-//           rows dequantised (exactly) from registers that are filled a tile ahead.  They also store the
-//           output, a row a thread: while an item's last output is read no buffer is free to be filled,
-//           and the softmax is with the next item's tiles already.
+//   12-19   loaders, 16 rows of a tile each: bf16 rows that follow one another by tensor copies, others
+//           by 16-byte asynchronous copies into the swizzled tile, FP4 rows dequantised (exactly) from
+//           registers that are filled a tile ahead.  They also store the output, a row a thread: while an
+//           item's last output is read no buffer is free to be filled, and the softmax is with the next
+//           item's tiles already.
 // Every wait is bounded; the CTAs meet at the cluster's barrier before either one exits.
 #include <algorithm>
 #include <climits>
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         mbar_init(qfull, 1);
         mbar_init(qempty, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&kfull[i], TT_LOADERS / 2);
+            mbar_init(&kfull[i], TT_LOADERS);
             for (int j = 0; j < 4; ++j) mbar_init(&kempty[4 * i + j], 1);
             mbar_init(&sfull[i], 2);
             mbar_init(&pfull[i], 8);
@@ -863,23 +863,17 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         }
     } else if (warp >= 12) {
         // ============================ loaders, output ============================
-        constexpr int ROWS = TT_TILE / (TT_LOADERS / 2);         // of a tile, a warp
-        const int lw = warp - 12, grp = lw / (TT_LOADERS / 2);   // tiles of this parity
-        const uint32_t row0 = ROWS * (lw % (TT_LOADERS / 2));    // rows row0 .. row0 + ROWS - 1 of them
-        uint8_t* tile = sK + grp * TT_TILE_BYTES;
-        // Three steps, each a tile of this parity ahead of the one before, so that no load is waited for: the
-        // rows' list is read (look_up), the rows are on their way (fetch), they go into the tile.
-        int tt = 0, g = 0;
+        constexpr int ROWS = TT_TILE / TT_LOADERS;            // of a tile, a warp
+        const int lw = warp - 12;
+        const uint32_t row0 = ROWS * lw;                      // rows row0 .. row0 + ROWS - 1
+        // Three steps, each a tile ahead of the one before, so that no load is waited for: the rows' list is
+        // read (look_up), the rows are on their way (fetch), they go into the tile.
+        int tt = 0;
         it.nt = 0;
-        int row = -1, kind = 0, next_tile = 0;                // looked up: lane j's row (-1: none) and source, the tile
+        int row = -1, kind = 0;                               // looked up: lane j's row (-1: none) and source
         bool entry = false, more = true;
         const auto look_up = [&]() {
-            for (;;) {
-                if (tt < it.nt && ((g ^ grp) & 1)) {
-                    ++tt;
-                    ++g;
-                }
-                if (tt < it.nt) break;
+            if (tt >= it.nt) {
                 more = more && walk.next(a, it);
                 if (!more) return;
                 tt = 0;
@@ -896,7 +890,6 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                 const float f = window_factor(a, it, j, row);
                 if (f != f) row = -1;
             }
-            next_tile = g++;
             ++tt;
         };
         // FP4 rows through registers: 8 lanes a row, 4 rows an instruction, 16 code bytes and 2 scales a lane
@@ -907,12 +900,10 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         uint64_t at = 0;              // bf16: the address of lane j's row, 0: none
         int box_row = -1, box_map = 0;    // bf16: the first row, where the rows follow one another
         bool fp4_rows = false;
-        int gt = 0;                   // the tile they are for
         bool fetched = false;
         const auto fetch = [&]() {
             fetched = more;
             if (!more) return;
-            gt = next_tile;
             fp4_rows = FP4 && entry;
             const uint8_t* src = nullptr;
             if (row >= 0)
@@ -1047,15 +1038,16 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         look_up();
         fetch();
         look_up();
-        int last = -1;                                        // the last tile this warp filled its rows of
+        int g = 0;
         bool ok = true;
-        while (fetched) {
-            ok = outputs(gt);
+        for (; fetched; ++g) {
+            ok = outputs(g);
             if (!ok) break;
-            const bool wt = gt < 2 || mbar_wait(&kempty[4 * grp + row0 / 32], ((gt - 2) >> 1) & 1, a.budget, a.st);
+            const bool wt = g < 2 || mbar_wait(&kempty[4 * (g & 1) + row0 / 32], ((g - 2) >> 1) & 1, a.budget, a.st);
             ok = __all_sync(FULL, wt);
             if (!ok) break;
-            last = gt;
+            uint8_t* tile = sK + (g & 1) * TT_TILE_BYTES;
+            uint64_t* full = &kfull[g & 1];
             if (fp4_rows) {
                 const int piece = lane & 7, c = piece >> 1;
                 uint8_t* base = tile + c * TT_CHUNK;
@@ -1077,15 +1069,15 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&kfull[grp]);
+                if (lane == 0) mbar_arrive(full);
                 fetch();
                 look_up();
             } else if (box_row >= 0) {
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&kfull[grp], ROWS * TT_HALF * 2);
+                    mbar_arrive_expect_tx(full, ROWS * TT_HALF * 2);
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        tma_load_2d(tile + c * TT_CHUNK + row0 * 128, &maps.m[box_map], TT_HALF * rank + 64 * c, box_row, &kfull[grp]);
+                        tma_load_2d(tile + c * TT_CHUNK + row0 * 128, &maps.m[box_map], TT_HALF * rank + 64 * c, box_row, full);
                 }
                 fetch();
                 look_up();
@@ -1104,12 +1096,12 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                 cp_async_wait<0>();
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&kfull[grp]);
+                if (lane == 0) mbar_arrive(full);
             }
         }
         if (ok) outputs(INT_MAX);
         // tensor copies must land before the CTA exits
-        if (last >= 0) mbar_wait(&kfull[grp], (last >> 1) & 1, a.budget, a.st);
+        for (int t = max(0, g - 2); t < g; ++t) mbar_wait(&kfull[t & 1], (t >> 1) & 1, a.budget, a.st);
     }
     tc_fence_before();
     __syncthreads();
@@ -1307,7 +1299,7 @@ csa2_status tree_tc_run(csa2_ctx* ctx, const TreeCall& c, void* ws, cudaStream_t
                                  c.r.window > 0 ? (int64_t)c.B * c.r.T : 0};
     const void* map_at[3] = {c.kv, c.swa, c.draft};
     for (int i = 0; i < 3; ++i)
-        if (!csa2_make_bf16_map(&maps.m[i], map_rows[i] > 0 ? map_at[i] : c.q, std::max<int64_t>(1, map_rows[i]), TT_C, 64, TT_TILE / (TT_LOADERS / 2)))
+        if (!csa2_make_bf16_map(&maps.m[i], map_rows[i] > 0 ? map_at[i] : c.q, std::max<int64_t>(1, map_rows[i]), TT_C, 64, TT_TILE / TT_LOADERS))
             return CSA2_ERR_CUDA;
     const int64_t blocks = (pa.e_warps + pa.w_warps + pa.r_warps + pa.d_warps + pa.q_warps + 7) / 8;
     csa2_status st = launch_pdl(tree_prep_kernel, dim3((unsigned)blocks), dim3(256), 0, s, pa);
