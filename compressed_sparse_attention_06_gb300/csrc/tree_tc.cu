@@ -93,15 +93,15 @@ struct TtArgs {
     const uint8_t* swa;
     const uint8_t* draft;
     const float* sink;
-    int64_t groups;
-    int share, tiles;             // tiles of a cluster, of a group (at most)
+    int groups, rounds, clusters; // cluster c has groups c, c + clusters, .. whole, `rounds` of them
+    int share, tiles;             // and of the others' tiles (at most `tiles` a group) `share`
     unsigned flags;
     void* out;
     int out_f32;
     float* lse;
-    int pieces;                   // > 1: some groups are dealt out in up to so many pieces
-    float* part_o;                // [groups * pieces][G*H rows][512]
-    float* part_l;                // [groups * pieces][G*H rows]
+    int pieces;                   // in which the others are dealt out, at most
+    float* part_o;                // [the others * pieces][G*H rows][512] (pieces > 1)
+    float* part_l;                // [the others * pieces][G*H rows]
     unsigned* st;
     long long budget;
     int stall;
@@ -215,47 +215,75 @@ __device__ __forceinline__ void turn4(uint4 (&p)[4]) {
     turn(p[1], p[3], 2);
 }
 
-// The groups' tiles stand one behind the other, `tiles` a group (a shorter one leaves its last ones
-// out), and cluster c has `share` of them from c * share on: its items are the groups that lie there.
+// A cluster's items: `rounds` whole groups, then its share of the groups that are left over: their tiles
+// stand one behind the other, `tiles` a group (a shorter one leaves its last ones out), and cluster c has
+// `share` of them from c * share on.
 struct TtItem {
     int v, b, n0, gv;             // group, sequence, first node in it, nodes
     int kq, slots, ring, rf;      // entry slots, all slots, the ring's among the others, the first one's j in rf
     int t0, nt;                   // tiles t0 .. t0 + nt - 1
+    int piece, pieces;            // of the group
+    int part;                     // its first piece's place among the partial outputs
 };
 
 struct TtWalk {
-    int v, at, left;              // group, tile in it, tiles left to the cluster
-    int4 info;                    // the group's, loaded an item ahead
+    int cluster, round;
+    int v, at, left;              // leftover group, tile in it, tiles left to the cluster
+    int4 info;                    // the next item's group's, loaded an item ahead
 
-    __device__ __forceinline__ void start(const TtArgs& a, int cluster) {
-        const int64_t f0 = (int64_t)cluster * a.share;
+    __device__ __forceinline__ int group(const TtArgs& a) const {        // of the next item, -1: none
+        return round < a.rounds ? round * a.clusters + cluster : (left > 0 ? a.rounds * a.clusters + v : -1);
+    }
+    __device__ __forceinline__ void load(const TtArgs& a) {
+        const int g = group(a);
+        info = g >= 0 ? a.l.info[g] : make_int4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void start(const TtArgs& a, int c) {
+        cluster = c;
+        round = 0;
+        const int64_t f0 = (int64_t)c * a.share, rest = (int64_t)(a.groups - a.rounds * a.clusters) * a.tiles;
         v = (int)(f0 / a.tiles);
         at = (int)(f0 - (int64_t)v * a.tiles);
-        left = (int)max((int64_t)0, min((int64_t)a.share, a.groups * a.tiles - f0));
-        info = left > 0 ? a.l.info[v] : make_int4(0, 0, 0, 0);
+        left = (int)max((int64_t)0, min((int64_t)a.share, rest - f0));
+        load(a);
     }
-    // the next item with tiles; false at the end.  Empty ones (a group without slots, a short one's last
+    // The next item with tiles; false at the end.  Empty ones (a group without slots, a short one's last
     // tiles) are passed over, or returned with nt = 0 where `empty` is set.
     __device__ __forceinline__ bool next(const TtArgs& a, TtItem& r, bool empty = false) {
-        while (left > 0) {
-            const int to = min(a.tiles, at + left);
-            r.v = v;
-            r.b = v / a.l.gps;
-            r.n0 = (v - r.b * a.l.gps) * a.l.G;
+        for (;;) {
+            r.v = group(a);
+            if (r.v < 0) return false;
+            r.b = r.v / a.l.gps;
+            r.n0 = (r.v - r.b * a.l.gps) * a.l.G;
             r.gv = min(a.l.G, a.r.T - r.n0);
             r.kq = info.x;
             r.slots = info.y;
             r.ring = info.z;
             r.rf = info.w;
-            r.t0 = at;
-            r.nt = max(0, min((info.y + TT_TILE - 1) / TT_TILE, to) - at);
-            left -= to - at;
-            ++v;
-            at = 0;
-            if (left > 0) info = a.l.info[v];
+            int to = a.tiles;
+            r.t0 = 0;
+            r.piece = 0;
+            r.pieces = 1;
+            if (round < a.rounds) {
+                ++round;
+            } else {
+                to = min(a.tiles, at + left);
+                r.t0 = at;
+                if (a.pieces > 1) {
+                    const int64_t g0 = (int64_t)v * a.tiles;
+                    const int c0 = (int)(g0 / a.share);
+                    r.piece = cluster - c0;
+                    r.pieces = (int)((g0 + a.tiles - 1) / a.share) - c0 + 1;
+                    r.part = v * a.pieces;
+                }
+                left -= to - at;
+                ++v;
+                at = 0;
+            }
+            r.nt = max(0, min((r.slots + TT_TILE - 1) / TT_TILE, to) - r.t0);
+            load(a);
             if (r.nt > 0 || empty) return true;
         }
-        return false;
     }
 };
 
@@ -942,14 +970,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         const auto output = [&]() {
             const bool valid = r < oit.gv * a.l.H;
             const int64_t bt = (int64_t)oit.b * a.r.T + oit.n0 + (valid ? hq : 0), orow = bt * a.l.H + h;
-            int piece = 0, pieces = 1;
-            if (a.pieces > 1) {
-                const int64_t g0 = (int64_t)oit.v * a.tiles;
-                piece = cluster - (int)(g0 / a.share);
-                pieces = (int)((g0 + a.tiles - 1) / a.share - g0 / a.share) + 1;
-            }
-            const int64_t prow = ((int64_t)oit.v * a.pieces + piece) * (a.l.G * a.l.H) + r;
-            const bool part = pieces > 1;
+            const bool part = oit.pieces > 1;
+            const int64_t prow = part ? (int64_t)(oit.part + oit.piece) * (a.l.G * a.l.H) + r : 0;
             float L = 0.0f;
             if (oit.nt > 0) {
                 const bool wt = mbar_wait(lred, oq & 1, a.budget, a.st) && mbar_wait(ofull, oq & 1, a.budget, a.st);
@@ -1116,7 +1138,7 @@ struct MergeArgs {
     const float* part_l;
     const float* rope_cs;
     const float* sink;
-    int64_t groups;
+    int64_t first, groups;        // of the groups that are dealt out, all
     int H, G, gps, T, pieces, share, tiles;
     unsigned flags;
     void* out;
@@ -1130,11 +1152,11 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeArgs a) {
     pdl_trigger();
     const int lane = threadIdx.x & 31, rows = a.G * a.H;
     const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (i >= a.groups * rows) return;
-    const int64_t v = i / rows, b = v / a.gps;
-    const int r = (int)(i - v * rows), g = r / a.H, h = r - g * a.H, node = (int)(v % a.gps) * a.G + g;
+    if (i >= (a.groups - a.first) * rows) return;
+    const int64_t o = i / rows, v = a.first + o, b = v / a.gps;
+    const int r = (int)(i - o * rows), g = r / a.H, h = r - g * a.H, node = (int)(v % a.gps) * a.G + g;
     if (node >= a.T) return;
-    const int64_t bt = b * a.T + node, g0 = v * a.tiles;
+    const int64_t bt = b * a.T + node, g0 = o * a.tiles;
     const int n = (int)((g0 + a.tiles - 1) / a.share - g0 / a.share) + 1;
     if (n == 1) return;                          // (the main kernel has finished the group)
     float acc[16], L = 0.0f;
@@ -1145,12 +1167,12 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeArgs a) {
         float4 x[4][4];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            const int64_t p = (v * a.pieces + s0 + s) * rows + r;
+            const int64_t p = (o * a.pieces + s0 + s) * rows + r;
             l[s] = s0 + s < n ? a.part_l[p] : 0.0f;
             // (a piece without slots has left its output as it was)
-            const float4* o = reinterpret_cast<const float4*>(a.part_o + p * TT_C) + lane;
+            const float4* x0 = reinterpret_cast<const float4*>(a.part_o + p * TT_C) + lane;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[s][j] = s0 + s < n ? __ldcs(o + 32 * j) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int j = 0; j < 4; ++j) x[s][j] = s0 + s < n ? __ldcs(x0 + 32 * j) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
@@ -1180,12 +1202,12 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeArgs a) {
     const int64_t row = bt * a.H + h;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int64_t o = row * TT_C + 128 * j + 4 * lane;
+        const int64_t e = row * TT_C + 128 * j + 4 * lane;
         if (a.out_f32)
-            *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + o) =
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + e) =
                 make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
         else
-            *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + o) =
+            *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + e) =
                 make_uint2(pack_bf16(acc[4 * j], acc[4 * j + 1]), pack_bf16(acc[4 * j + 2], acc[4 * j + 3]));
     }
     if (a.lse && lane == 0) a.lse[row] = fin.y;
@@ -1194,7 +1216,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeArgs a) {
 size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 struct TtPlan {
-    int G, R8, gps, lde, ldw, clusters, share, tiles, pieces;
+    int G, R8, gps, lde, ldw, clusters, rounds, share, tiles, pieces;
     int64_t groups;
     size_t erow, ef, eok, wrow, wmask, rf, df, info, rope, part_l, part_o, total;
 };
@@ -1209,16 +1231,22 @@ TtPlan tt_plan(const csa2_ctx* ctx, int B, int T, int H, int k, int window, bool
     const int near = window > 0 ? window + (dense ? T : 0) : 0;
     p.lde = (k + 31) / 32 * 32;
     p.ldw = (near + 31) / 32 * 32;
-    // A cluster's time is its tiles' and, for every group it works on, about three tiles' for the first
-    // rows and the output; either the groups stay whole, or the tiles are dealt out evenly.
-    const int64_t clusters = std::max(1, ctx->num_sms / 2);
+    // The groups go whole to the clusters, in rounds; the last, incomplete round whole as well, or dealt out
+    // in even shares of tiles.  Shares cost a second start and output a cluster and the joining of the partial
+    // outputs, measured at about six tiles' time.
+    const int most = std::max(1, ctx->num_sms / 2);
     p.tiles = std::max(1, (p.lde + near + TT_TILE - 1) / TT_TILE);
-    const int64_t total = p.groups * p.tiles, whole = (p.groups + clusters - 1) / clusters, even = (total + clusters - 1) / clusters;
-    const bool split = even + 3 * (even / p.tiles + 2) < whole * p.tiles + 3 * whole;
-    p.share = (int)(split ? even : whole * p.tiles);
-    p.clusters = (int)((total + p.share - 1) / p.share);
-    // the pieces of a group: of the `share`s that touch it
-    p.pieces = split ? (p.tiles + p.share - 2) / p.share + 1 : 1;
+    p.clusters = (int)std::min<int64_t>(most, p.groups);
+    p.rounds = (int)(p.groups / most);
+    const int64_t rest = p.groups - (int64_t)p.rounds * most;
+    p.share = p.tiles;
+    p.pieces = 1;
+    const int64_t even = (rest * p.tiles + most - 1) / most;
+    if (rest > 0 && even + 6 < p.tiles) {
+        p.share = (int)even;
+        p.clusters = p.rounds > 0 ? most : (int)((rest * p.tiles + even - 1) / even);
+        p.pieces = (p.tiles + p.share - 2) / p.share + 1;     // of the shares that touch a group
+    }
     const size_t eg = dense ? (size_t)B : (size_t)B * T;
     p.erow = up((size_t)p.groups * p.R8 * 1024, 256);
     p.ef = up(p.erow + eg * p.lde * 4, 256);
@@ -1230,7 +1258,7 @@ TtPlan tt_plan(const csa2_ctx* ctx, int B, int T, int H, int k, int window, bool
     p.info = up(p.df + (size_t)B * T * 4, 256);
     p.rope = up(p.info + (size_t)p.groups * 16, 256);
     p.part_l = up(p.rope + (size_t)B * T * 64 * 4, 256);
-    const size_t rows = p.pieces > 1 ? (size_t)p.groups * p.pieces * p.G * H : 0;
+    const size_t rows = p.pieces > 1 ? (size_t)rest * p.pieces * p.G * H : 0;
     p.part_o = up(p.part_l + rows * 4, 256);
     p.total = p.part_o + rows * TT_C * 4;
     return p;
@@ -1311,7 +1339,9 @@ csa2_status tree_tc_run(csa2_ctx* ctx, const TreeCall& c, void* ws, cudaStream_t
     a.swa = pa.swa;
     a.draft = pa.draft;
     a.sink = c.sink;
-    a.groups = p.groups;
+    a.groups = (int)p.groups;
+    a.rounds = p.rounds;
+    a.clusters = p.clusters;
     a.share = p.share;
     a.tiles = p.tiles;
     a.pieces = p.pieces;
@@ -1333,9 +1363,10 @@ csa2_status tree_tc_run(csa2_ctx* ctx, const TreeCall& c, void* ws, cudaStream_t
     else st = dense ? launch_tt<false, true>(p.clusters, a, maps, s) : launch_tt<false, false>(p.clusters, a, maps, s);
     if (st != CSA2_OK) return st;
     if (p.pieces > 1) {
-        const MergeArgs m = {a.part_o, a.part_l, a.l.rope_cs, a.sink, p.groups, c.H, p.G, p.gps, c.r.T, p.pieces, p.share, p.tiles,
+        const int64_t first = (int64_t)p.rounds * p.clusters;
+        const MergeArgs m = {a.part_o, a.part_l, a.l.rope_cs, a.sink, first, p.groups, c.H, p.G, p.gps, c.r.T, p.pieces, p.share, p.tiles,
                              c.flags, c.out, a.out_f32, c.lse};
-        const int64_t rows = p.groups * p.G * c.H;
+        const int64_t rows = (p.groups - first) * p.G * c.H;
         st = launch_pdl(tree_merge_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, m);
         if (st != CSA2_OK) return st;
     }
