@@ -6,7 +6,7 @@
 // out of step: a call that needs free pages finds the lowest ones by a pass over refs.  That pass
 // and what follows from it are one thread-block cluster of 8 CTAs whose phases meet at cluster
 // barriers (a launch of its own per phase would cost more than the phase for any pool that fits a
-// GPU); the ranks come from counts in order of (sequence, page) and of page id, so results do not
+// GPU), or one CTA where the state is small; the ranks come from counts in order of (sequence, page) and of page id, so results do not
 // depend on timing.  Moving the bytes is bound by device memory.
 #include <algorithm>
 
@@ -16,10 +16,13 @@
 namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
-constexpr int PG_CTAS = 8;               // CTAs of the cluster
+constexpr int PG_CTAS = 8;               // CTAs of the cluster at most (gridDim.x of them)
 constexpr int PG_THREADS = 1024;
 constexpr int PG_WARPS = PG_THREADS / 32;
 constexpr int PG_SEQS = 65536 / PG_CTAS; // sequences of a CTA at most
+// One CTA takes a small state in less time than the cluster's barriers cost (reserve of 16 pages of a pool
+// of 25 in cold caches: 10.9 us, in a cluster 12.7; of 4,160 pages of 12,000: 26.6 and 13 us).
+constexpr int PG_SMALL_PAGES = 2048, PG_SMALL_SEQS = 256;
 
 __device__ __forceinline__ uint32_t cta_rank() {
     uint32_t r;
@@ -163,7 +166,8 @@ __global__ void __launch_bounds__(PG_THREADS) pages_reserve_kernel(const Reserve
     const uint32_t rank = cta_rank();
     cluster_sync();                      // every CTA runs: its shared memory may be written
     // the sequences of this CTA, and the words of their pages
-    const int per = (a.B + PG_CTAS - 1) / PG_CTAS;
+    const int nc = gridDim.x;
+    const int per = (a.B + nc - 1) / nc;
     const int b0 = min(a.B, (int)rank * per), nb = min(a.B, b0 + per) - b0;
     uint32_t n_words = 0;
     for (int i0 = 0; i0 < nb; i0 += PG_THREADS) {
@@ -215,18 +219,18 @@ __global__ void __launch_bounds__(PG_THREADS) pages_reserve_kernel(const Reserve
         wants += total;
     }
     // the free pages of this CTA's share of the pool, 4 a thread at a time
-    const int64_t share = ((a.n_pages + PG_CTAS - 1) / PG_CTAS + 3) / 4 * 4;
+    const int64_t share = ((a.n_pages + nc - 1) / nc + 3) / 4 * 4;
     const int64_t p0 = min(a.n_pages, rank * share), p1 = min(a.n_pages, p0 + share);
     uint32_t mine = 0, frees;
     for (int64_t p = p0 + threadIdx.x; p < p1; p += PG_THREADS) mine += a.refs[p] == 0;
     block_scan(s.tmp, mine, frees);
-    if (threadIdx.x < PG_CTAS) {
+    if (threadIdx.x < nc) {
         put_remote(&s.wants[rank], threadIdx.x, wants);
         put_remote(&s.frees[rank], threadIdx.x, frees);
     }
     cluster_sync();
     uint32_t all_wants = 0, all_frees = 0, want0 = 0, free0 = 0;
-    for (int i = 0; i < PG_CTAS; ++i) {
+    for (int i = 0; i < nc; ++i) {
         if (i < (int)rank) {
             want0 += s.wants[i];
             free0 += s.frees[i];
@@ -299,17 +303,18 @@ struct CompactArgs {
 
 __global__ void __launch_bounds__(PG_THREADS) pages_compact_kernel(const CompactArgs a) {
     __shared__ uint32_t tmp[PG_WARPS + 1], used[PG_CTAS], from[PG_CTAS], into[PG_CTAS];
+    const int nc = gridDim.x;
     const uint32_t rank = cta_rank();
     cluster_sync();                      // every CTA runs: its shared memory may be written
-    const int64_t share = ((a.n_pages + PG_CTAS - 1) / PG_CTAS + 3) / 4 * 4;
+    const int64_t share = ((a.n_pages + nc - 1) / nc + 3) / 4 * 4;
     const int64_t p0 = min(a.n_pages, rank * share), p1 = min(a.n_pages, p0 + share);
     uint32_t n = 0, total;
     for (int64_t p = p0 + threadIdx.x; p < p1; p += PG_THREADS) n += a.refs[p] > 0;
     block_scan(tmp, n, total);
-    if (threadIdx.x < PG_CTAS) put_remote(&used[rank], threadIdx.x, total);
+    if (threadIdx.x < nc) put_remote(&used[rank], threadIdx.x, total);
     cluster_sync();
     int64_t cut = 0;
-    for (int i = 0; i < PG_CTAS; ++i) cut += used[i];
+    for (int i = 0; i < nc; ++i) cut += used[i];
     // sources (used, at or behind the cut) and holes (free, before it) of this share
     uint32_t ns = 0, nh = 0, ts, th;
     for (int64_t p = p0 + threadIdx.x; p < p1; p += PG_THREADS) {
@@ -319,14 +324,14 @@ __global__ void __launch_bounds__(PG_THREADS) pages_compact_kernel(const Compact
     }
     block_scan(tmp, ns, ts);
     block_scan(tmp, nh, th);
-    if (threadIdx.x < PG_CTAS) {
+    if (threadIdx.x < nc) {
         put_remote(&from[rank], threadIdx.x, ts);
         put_remote(&into[rank], threadIdx.x, th);
     }
     cluster_sync();
     int64_t n_moves = 0;
     uint32_t s0 = 0, h0 = 0;
-    for (int i = 0; i < PG_CTAS; ++i) {
+    for (int i = 0; i < nc; ++i) {
         if (i < (int)rank) {
             s0 += from[i];
             h0 += into[i];
@@ -357,7 +362,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_compact_kernel(const Compact
     }
     __threadfence();
     cluster_sync();
-    const int64_t step = (int64_t)PG_CTAS * PG_THREADS, half = a.n_pages / 2;
+    const int64_t step = (int64_t)nc * PG_THREADS, half = a.n_pages / 2;
     for (int64_t i = (int64_t)rank * PG_THREADS + threadIdx.x; i < half; i += step) {
         if (i < n_moves) {
             const int32_t src = a.moves[2 * i], dst = a.moves[2 * i + 1];
@@ -389,30 +394,51 @@ __global__ void __launch_bounds__(256) pages_remap_kernel(int32_t* table, int64_
 
 constexpr int PC_THREADS = 256, PC_PIECES = 8;
 
-// Whole pages: chunks of 2,048 pieces of V, eight in flight a thread; the pairs that move nothing
-// are the last ones of a compaction and cost their lookup.
+// Whole pages in pieces of V: a block takes pairs_b pairs (pages of fewer than PC_BLOCK pieces) or PC_BLOCK
+// pieces of one, eight in flight a thread.  The pairs that move nothing are the last ones of a compaction
+// and cost their lookup.
+constexpr int PC_BLOCK = 4 * PC_THREADS * PC_PIECES, PC_PAIRS = 512;
+
 template <typename V>
 __global__ void __launch_bounds__(PC_THREADS) page_copy_kernel(V* pool, int64_t n_pages, int64_t pieces, const int32_t* pairs,
-                                                               int64_t n, int64_t chunks, unsigned* st) {
-    constexpr int CH = PC_THREADS * PC_PIECES;
-    for (int64_t i = blockIdx.x; i < n * chunks; i += gridDim.x) {
-        const int64_t pr = chunks == 1 ? i : i / chunks;
-        const int32_t src = pairs[2 * pr], dst = pairs[2 * pr + 1];
-        if (src == -1 || dst == -1) continue;
-        if (src < 0 || src >= n_pages || dst < 0 || dst >= n_pages) {
-            if (threadIdx.x == 0) csa2_flag(st, CSA2_DEVBIT_RANGE);
-            continue;
+                                                               int64_t n, int pairs_b, int64_t chunks, unsigned* st) {
+    __shared__ int64_t from[PC_PAIRS], to[PC_PAIRS];     // first pieces of the block's pages, -1 = nothing to move
+    const int64_t groups = (n + pairs_b - 1) / pairs_b;
+    for (int64_t i = blockIdx.x; i < groups * chunks; i += gridDim.x) {
+        const int64_t g = chunks == 1 ? i : i / chunks, p0 = g * pairs_b;
+        const int np = (int)min((int64_t)pairs_b, n - p0);
+        bool any = false;
+        for (int p = threadIdx.x; p < np; p += PC_THREADS) {
+            const int32_t src = pairs[2 * (p0 + p)], dst = pairs[2 * (p0 + p) + 1];
+            bool move = src != -1 && dst != -1;
+            if (move && (src < 0 || src >= n_pages || dst < 0 || dst >= n_pages)) {
+                csa2_flag(st, CSA2_DEVBIT_RANGE);
+                move = false;
+            }
+            from[p] = move ? src * pieces : -1;
+            to[p] = dst * pieces;
+            any |= move;
         }
-        const int64_t u0 = (i - pr * chunks) * CH + threadIdx.x;
-        const V* s = pool + src * pieces;
-        V* d = pool + dst * pieces;
-        V v[PC_PIECES];
+        if (!__syncthreads_or(any)) continue;
+        const int64_t c0 = (i - g * chunks) * PC_BLOCK;
+        const uint32_t total = (uint32_t)min((int64_t)np * pieces - c0, (int64_t)PC_BLOCK);
+        for (uint32_t u0 = threadIdx.x; u0 < total; u0 += PC_THREADS * PC_PIECES) {
+            V v[PC_PIECES];
+            int64_t d[PC_PIECES];
 #pragma unroll
-        for (int j = 0; j < PC_PIECES; ++j)
-            if (u0 + j * PC_THREADS < pieces) v[j] = __ldcs(s + u0 + j * PC_THREADS);
+            for (int j = 0; j < PC_PIECES; ++j) {
+                const uint32_t u = u0 + j * PC_THREADS, p = chunks == 1 ? u / (uint32_t)pieces : 0;
+                d[j] = -1;
+                if (u >= total || from[p] < 0) continue;
+                const int64_t k = c0 + u - p * pieces;
+                d[j] = to[p] + k;
+                v[j] = __ldcs(pool + from[p] + k);
+            }
 #pragma unroll
-        for (int j = 0; j < PC_PIECES; ++j)
-            if (u0 + j * PC_THREADS < pieces) __stcs(d + u0 + j * PC_THREADS, v[j]);
+            for (int j = 0; j < PC_PIECES; ++j)
+                if (d[j] >= 0) __stcs(pool + d[j], v[j]);
+        }
+        __syncthreads();                         // the tables are filled again
     }
 }
 
@@ -492,14 +518,16 @@ unsigned flat_grid(const csa2_ctx* ctx, int64_t total) {
     return (unsigned)std::min<int64_t>((total + 255) / 256, 8ll * std::max(1, ctx->num_sms));
 }
 
-void cluster_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* at, size_t smem, cudaStream_t s) {
+// The state kernels' launch: one CTA for a small state, else the cluster.
+void cluster_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* at, int64_t n_pages, int B, size_t smem, cudaStream_t s) {
+    const unsigned nc = n_pages <= PG_SMALL_PAGES && B <= PG_SMALL_SEQS ? 1 : PG_CTAS;
     cfg = {};
-    cfg.gridDim = dim3(PG_CTAS);
+    cfg.gridDim = dim3(nc);
     cfg.blockDim = dim3(PG_THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = PG_CTAS;
+    at[0].val.clusterDim.x = nc;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
@@ -607,7 +635,7 @@ extern "C" csa2_status csa2_pages_reserve(csa2_ctx* ctx, int32_t* refs, int64_t 
     CSA2_CHECK_CUDA(cudaFuncSetAttribute(pages_reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ReserveSmem)));
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute at[1];
-    cluster_config(cfg, at, sizeof(ReserveSmem), as_stream(stream));
+    cluster_config(cfg, at, n_pages, B, sizeof(ReserveSmem), as_stream(stream));
     if (cudaLaunchKernelEx(&cfg, pages_reserve_kernel, a) != cudaSuccess) return CSA2_ERR_CUDA;
     return csa2_launch_status();
 }
@@ -638,7 +666,7 @@ extern "C" csa2_status csa2_pages_compact(csa2_ctx* ctx, int32_t* refs, int64_t 
     const CompactArgs a = {refs, n_pages, moves, n_used, to, cut};
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute at[1];
-    cluster_config(cfg, at, 0, s);
+    cluster_config(cfg, at, n_pages, 0, 0, s);
     if (cudaLaunchKernelEx(&cfg, pages_compact_kernel, a) != cudaSuccess) return CSA2_ERR_CUDA;
     const int64_t total = (int64_t)B * max_pages;
     if (total == 0) return csa2_launch_status();
@@ -656,15 +684,18 @@ extern "C" csa2_status csa2_page_copy(csa2_ctx* ctx, void* pool, int64_t n_pages
     DeviceGuard dev(ctx);
     if (!dev.ok) return CSA2_ERR_CUDA;
     const bool wide = page_bytes % 16 == 0 && aligned(pool, 16);
-    const int64_t pieces = page_bytes / (wide ? 16 : 4), chunks = (pieces + PC_THREADS * PC_PIECES - 1) / (PC_THREADS * PC_PIECES);
-    const unsigned grid = (unsigned)std::min<int64_t>(n * chunks, 8ll * std::max(1, ctx->num_sms));
+    const int64_t pieces = page_bytes / (wide ? 16 : 4), chunks = (pieces + PC_BLOCK - 1) / PC_BLOCK;
+    // few pairs: a block each, so that they move at once
+    const int64_t fit = std::min<int64_t>(PC_PAIRS, std::max<int64_t>(1, PC_BLOCK / pieces));
+    const int pairs_b = (int)std::max<int64_t>(1, std::min(fit, n / (4 * std::max(1, ctx->num_sms))));
+    const unsigned grid = (unsigned)std::min<int64_t>((n + pairs_b - 1) / pairs_b * chunks, 8ll * std::max(1, ctx->num_sms));
     cudaStream_t s = as_stream(stream);
     if (wide)
-        page_copy_kernel<uint4><<<grid, PC_THREADS, 0, s>>>(reinterpret_cast<uint4*>(pool), n_pages, pieces, pairs, n, chunks,
+        page_copy_kernel<uint4><<<grid, PC_THREADS, 0, s>>>(reinterpret_cast<uint4*>(pool), n_pages, pieces, pairs, n, pairs_b, chunks,
                                                             ctx->status);
     else
-        page_copy_kernel<uint32_t><<<grid, PC_THREADS, 0, s>>>(reinterpret_cast<uint32_t*>(pool), n_pages, pieces, pairs, n, chunks,
-                                                               ctx->status);
+        page_copy_kernel<uint32_t><<<grid, PC_THREADS, 0, s>>>(reinterpret_cast<uint32_t*>(pool), n_pages, pieces, pairs, n, pairs_b,
+                                                               chunks, ctx->status);
     return csa2_launch_status();
 }
 
