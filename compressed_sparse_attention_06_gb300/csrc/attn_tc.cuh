@@ -30,9 +30,10 @@ __device__ __forceinline__ void rope_lanes(float (&x)[16], int lane, const float
 // (27) over the union of the splits' keys): part = the ns partials of the row (max or
 // offset, sum of exponentials, unnormalised output), zs = the sink logit (-inf: none),
 // cs / sn = RoPE at the query position (NULL: no rotation).  Writes the 512 outputs
-// to o and, if lse is not NULL, log(sum e^z + e^zs) to *lse.
+// to o and, if lse is not NULL, log(sum e^z + e^zs) to *lse.  Returns the sum, relative to the
+// row's maximum.
 template <typename TO>
-__device__ __forceinline__ void attn_combine_row(const float* part, int ns, float zs, const float* cs,
+__device__ __forceinline__ float attn_combine_row(const float* part, int ns, float zs, const float* cs,
                                                  const float* sn, TO* o, float* lse) {
     const int lane = threadIdx.x & 31;
     float M = zs;
@@ -69,6 +70,7 @@ __device__ __forceinline__ void attn_combine_row(const float* part, int ns, floa
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[lane + 32 * i] = from_f32<TO>(acc[i]);
     if (lse && lane == 0) *lse = (denom > 0.0f) ? M + logf(denom) : -INFINITY;
+    return denom;
 }
 
 struct AttnTcCall {

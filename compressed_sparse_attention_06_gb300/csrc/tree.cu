@@ -228,7 +228,8 @@ __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const SimtArgs
 #pragma unroll
             for (int w = 0; w < 8; ++w) z += s.zp[(w * TS_HG + h) * TS_KC + lane];
             z = s.ok[lane] ? z * s.rinv[lane] * inv_sqrt_c : -INFINITY;
-            const float m_old = s.m[h], m_new = fmaxf(m_old, warp_max(z));
+            // (a NaN, which fmaxf drops, counts as some logit: the row has one, whose sum is NaN)
+            const float m_old = s.m[h], m_new = fmaxf(m_old, warp_max(z == z ? z : 0.0f));
             const float sc = m_new == -INFINITY ? 1.0f : expf(m_old - m_new);
             const float p = z == -INFINITY ? 0.0f : expf(z - m_new);
             const float l = warp_sum(p);
@@ -315,9 +316,10 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const SimtArgs a, int
     const bool rope = a.c.flags & CSA2_ROPE;
     if (rope) ag_cos_sin(a.c.rope, a.c.r.pos[r / a.c.H], lane, cs[warp][lane], sn[warp][lane]);
     __syncwarp();
-    attn_combine_row<TO>(a.part + r * (int64_t)a.n_split * ATTN_PART, a.n_split, a.c.sink ? a.c.sink[r % a.c.H] : -INFINITY,
-                         rope ? cs[warp] : nullptr, sn[warp], reinterpret_cast<TO*>(a.c.out) + r * TS_C,
-                         a.c.lse ? a.c.lse + r : nullptr);
+    const float sum = attn_combine_row<TO>(a.part + r * (int64_t)a.n_split * ATTN_PART, a.n_split,
+                                           a.c.sink ? a.c.sink[r % a.c.H] : -INFINITY, rope ? cs[warp] : nullptr, sn[warp],
+                                           reinterpret_cast<TO*>(a.c.out) + r * TS_C, a.c.lse ? a.c.lse + r : nullptr);
+    if (sum != sum && a.c.lse && lane == 0) a.c.lse[r] = sum;         // NaN, as the outputs
 }
 
 // Splits that give every SM two CTAs, of 32 rows at least.

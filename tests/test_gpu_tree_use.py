@@ -1,0 +1,187 @@
+"""Drafted trees as a server runs them: more groups than the GPU takes at once, captured graphs, several
+streams, rows that hold no numbers, and a kernel whose rows never come.  Tolerances as in
+tests/test_gpu_tree.py."""
+import contextlib
+
+import pytest
+import torch
+
+from compressed_sparse_attention_06_gb300 import csa2 as C
+from compressed_sparse_attention_06_gb300 import workloads as W
+from tests.test_gpu_tree import BF, DEV, F32, Case
+
+pytestmark = pytest.mark.gpu
+
+
+@contextlib.contextmanager
+def _unguarded():
+    """Calls without the guards' look at the buffers after each, which waits for the GPU."""
+    check, C._check = C._check, lambda fn, st: None if st == C.OK else pytest.fail(fn)
+    try:
+        yield
+    finally:
+        C._check = check
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp4"])
+@pytest.mark.parametrize("B,T,H,N,k,pad,dense", [
+    (1, 80, 64, 2000, 1500, 1400, False),      # a round of whole groups and four that are dealt out, some of them short
+    (1, 155, 20, 3000, 2040, 2039, False),     # two rounds and three
+    (7, 88, 16, 1400, 0, 0, True),             # the nodes of a group see different entries
+    (3, 5, 128, 5000, 0, 0, True),             # no whole round, a node a group
+    (1, 1, 3, 9000, 2048, 0, False),           # one group over all of the GPU
+])
+def test_groups_in_rounds_and_shares(kind, B, T, H, N, k, pad, dense):
+    c = Case(91, B, T, H, N, k, kind, page=64, pad=pad, dense=dense, unused=T // 9)
+    out, lse = c.run(out_dtype=torch.float32)
+    C.csa2_ctx_check()
+    c.check(out, lse, **BF)
+    again, la = c.run(out_dtype=torch.float32)
+    assert torch.equal(out, again) and torch.equal(lse, la)
+    half, _ = c.run()
+    assert torch.equal(half, out.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("kind,dt", [("f32", torch.float32), ("bf16", torch.bfloat16), ("fp4", torch.bfloat16)])
+@pytest.mark.parametrize("window", [0, 12])
+def test_no_entries_and_repeated_entries(kind, dt, window):
+    c = Case(92, 2, 5, 24, 40, 0, kind, dt=dt, window=window)
+    out, lse = c.run(out_dtype=torch.float32)
+    C.csa2_ctx_check()
+    tol = F32 if dt == torch.float32 else BF
+    c.check(out, lse, **tol)
+    if window == 0:
+        assert not out.any() and torch.equal(lse, c.sink.expand_as(lse))
+    c = Case(92, 2, 5, 24, 40, 30, kind, dt=dt, window=window)
+    c.kw["idx"][:, :, 10:20] = c.kw["idx"][:, :, :1]                   # an entry counts as often as it is named
+    c.sel[:, :, 10:20] = c.sel[:, :, :1]
+    out, lse = c.run(out_dtype=torch.float32)
+    C.csa2_ctx_check()
+    c.check(out, lse, **tol)
+
+
+@pytest.mark.parametrize("kind,dt", [("f32", torch.float32), ("bf16", torch.bfloat16)])
+@pytest.mark.parametrize("dense", [False, True])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_rows_without_numbers_reach_only_who_attends(kind, dt, dense, bad):
+    """A draft, a ring row and an entry with a NaN or an infinity: the nodes that attend to it get NaN, the
+    others the same bits as before, those of the same group too."""
+    B, T, H, N, k, win = 2, 8, 16, 200, 0 if dense else 60, 10
+    c = Case(93, B, T, H, N, k, kind, dt=dt, window=win, dense=dense, lens=[50, 4])
+    c.parent = torch.tensor([[-1, 0, 1, 0, 3, 4, 5, 3]] * B, dtype=torch.int32, device=DEV)     # 0-1-2, 0-3-4-5-6, 3-7
+    out, lse = c.run()
+    C.csa2_ctx_check()
+
+    def check(hit):
+        o, l = c.run()
+        C.csa2_ctx_check()
+        hit = torch.tensor(hit, device=DEV).expand(B, T)
+        assert bool(torch.isnan(o[hit].float()).all()) and bool(torch.isnan(l[hit]).all())
+        assert torch.equal(o[~hit], out[~hit]) and torch.equal(l[~hit], lse[~hit])
+
+    keep = c.draft.clone()
+    c.draft[:, 4, 77] = bad
+    check([[i in (4, 5, 6) for i in range(T)]])
+    c.draft = keep
+    keep = c.swa.clone()
+    # the ring's row of position len - win + 2 (sequence 0): the nodes of depth 0 and 1 see it
+    c.swa[0, (50 - win + 2 - c.kw["swa_pos0"]) % c.swa.shape[1], 500] = bad
+    check([[i in (0, 1, 3) for i in range(T)], [False] * T])
+    c.swa = keep
+    if dense:
+        c.kv[1, N - 1, 3] = bad
+        hit = [[False] * T, [len(c.sel[1][i]) == N for i in range(T)]]
+    else:
+        c.kv[1, int(c.sel[1][5][7]), 3] = bad
+        hit = [[False] * T, [bool((c.sel[1][i] == c.sel[1][5][7]).any()) for i in range(T)]]
+    check(hit)
+
+
+@pytest.mark.parametrize("kind,dt", [("f32", torch.float32), ("bf16", torch.bfloat16)])
+@pytest.mark.parametrize("k", [1, 100])
+def test_nothing_but_rows_without_numbers(kind, dt, k):
+    c = Case(95, 1, 2, 8, 128, k, kind, dt=dt, window=0)
+    c.kv[:] = float("nan")
+    for sink in (None, c.sink):
+        out, lse = c.run(sink=sink)
+        C.csa2_ctx_check()
+        assert bool(torch.isnan(out.float()).all()) and bool(torch.isnan(lse).all())
+
+
+def test_captured_and_replayed():
+    """Two graphs captured over one workspace, replayed in turn with other inputs, lengths and trees."""
+    cases = [Case(94 + i, 2, 9, 32, 700, 300, "bf16", page=64, lens=[10, 999]) for i in range(4)]
+    a, b = cases[0], Case(99, 3, 80, 8, 900, 0, "fp4", page=16, dense=True)
+
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+
+    def bind(c):
+        B, T = c.parent.shape
+        pos, path = torch.empty(B, T, dtype=torch.int64, device=DEV), torch.empty(B, T, T, dtype=torch.int16, device=DEV)
+        out, lse = torch.empty_like(c.q), torch.empty(c.q.shape[:3], dtype=torch.float32, device=DEV)
+
+        def call():
+            C.csa2_tree_plan(c.parent, c.len, pos=pos, path=path)
+            C.csa2_tree_attn(c.q, c.kv, pos, path, c.len, c.swa, c.draft, **c.kw, sink=c.sink, out=out, lse=lse, ws=ws)
+        return call, out, lse
+
+    graphs = []
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for c in (a, b):
+        call, out, lse = bind(c)
+        with torch.cuda.stream(s):
+            call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with _unguarded(), torch.cuda.graph(g, stream=s):
+            call()
+        graphs.append((g, out, lse))
+    for c in cases:
+        swa_pos0 = c.kw["swa_pos0"]
+        for x in ("q", "kv", "swa", "draft", "sink", "len", "parent"):
+            getattr(a, x).copy_(getattr(c, x))
+        a.kw["table"].copy_(c.kw["table"])
+        a.kw["idx"].copy_(c.kw["idx"])
+        c.kw["swa_pos0"] = a.kw["swa_pos0"]                            # (an argument: it stays as captured)
+        want = c.run()
+        c.kw["swa_pos0"] = swa_pos0
+        want_b = b.run()
+        for g, _, _ in graphs:
+            g.replay()
+        C.csa2_ctx_check()
+        for (_, out, lse), (o, l) in zip(graphs, (want, want_b)):
+            assert torch.equal(out, o) and torch.equal(lse, l)
+
+
+def test_streams_at_once():
+    cases = [Case(101 + i, 2, 20, 64, 3000, 1000, kind, page=64) for i, kind in enumerate(("bf16", "fp4", "bf16"))]
+    want = [c.run() for c in cases]
+    C.csa2_ctx_check()
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = []
+    with _unguarded():
+        for _ in range(4):
+            for c, s in zip(cases, streams):
+                with torch.cuda.stream(s):
+                    got.append(c.run())
+        torch.cuda.synchronize()
+    C.csa2_ctx_check()
+    for i, (o, l) in enumerate(got):
+        assert torch.equal(o, want[i % 3][0]) and torch.equal(l, want[i % 3][1])
+
+
+@pytest.mark.parametrize("kind,dense", [("bf16", False), ("bf16", True), ("fp4", False)])
+def test_queries_that_never_come_time_out(kind, dense):
+    c = Case(111, 2, 12, 32, 900, 0 if dense else 500, kind, page=64, dense=dense)
+    want, lw = c.run()
+    C.csa2_ctx_check()
+    C.csa2_ctx_test_stall_next(1 << 27)
+    c.run()
+    with pytest.raises(C.Csa2Error) as e:
+        C.csa2_ctx_check()
+    assert e.value.status == C.ERR_TIMEOUT
+    out, lse = c.run()
+    C.csa2_ctx_check()
+    assert torch.equal(out, want) and torch.equal(lse, lw)
