@@ -64,7 +64,7 @@ constexpr int OFF_F = OFF_X + 32768;                     // [2][128] the factors
 constexpr int OFF_L = OFF_F + 1024;                      // [2][128] sums of exponentials
 constexpr int OFF_MASK = OFF_L + 1024;                   // [2][TT_G][4] x 32 bits
 constexpr int OFF_BAR = OFF_MASK + 2 * TT_G * 16;
-constexpr int N_BAR = 18 + 8 + 8 + 8;
+constexpr int N_BAR = 16 + 8 + 4 * 8;
 constexpr int OFF_TMEM = OFF_BAR + N_BAR * 8;
 constexpr int TT_SMEM = OFF_TMEM + 16;
 static_assert(TT_SMEM <= 227 * 1024, "shared memory");
@@ -136,6 +136,9 @@ __device__ __forceinline__ void peer_st4(uint32_t addr, uint32_t a, uint32_t b, 
     asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
                  "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
                  : "memory");
+}
+__device__ __forceinline__ void peer_st1(uint32_t addr, uint32_t a, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr), "r"(a), "r"(bar) : "memory");
 }
 
 // Whether the phase of the given parity is complete, without waiting.
@@ -595,14 +598,16 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
     uint64_t* qfull = bars + 0;
     uint64_t* qempty = bars + 1;
     uint64_t* kfull = bars + 2;        // [2] a tile's rows are in shared memory
-    uint64_t* sfull = bars + 6;        // [2] its half logits, its factors and masks
-    uint64_t* pfull = bars + 8;        // [2] its P'
+    uint64_t* sfull = bars + 4;        // [2] its half logits, its factors and masks
+    uint64_t* pfull = bars + 6;        // [2][2] the P' of the slots that this CTA, that the peer weighs
     uint64_t* ofull = bars + 10;
     uint64_t* oempty = bars + 11;
     uint64_t* lred = bars + 12;
-    uint64_t* kempty = bars + 18;      // [2][4] the products of a tile's 32-row groups are done, in order
-    uint64_t* xfull = bars + 26;       // [8] the peer's logits of a softmax warp
-    uint64_t* xempty = bars + 34;      // [8] the peer has read this warp's
+    uint64_t* kempty = bars + 16;      // [2][4] the products of a tile's 32-row groups are done
+    uint64_t* xfull = bars + 24;       // [8] the peer's half logits for a softmax warp, its sums
+    uint64_t* xempty = bars + 32;      // [8] the peer has read this warp's
+    uint64_t* yfull = bars + 40;       // [8] the peer's P'
+    uint64_t* yempty = bars + 48;      // [8] the peer has read this warp's
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
@@ -616,7 +621,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
             mbar_init(&kfull[i], TT_LOADERS);
             for (int j = 0; j < 4; ++j) mbar_init(&kempty[4 * i + j], 1);
             mbar_init(&sfull[i], 2);
-            mbar_init(&pfull[i], 8);
+            for (int j = 0; j < 2; ++j) mbar_init(&pfull[2 * i + j], 8);
         }
         mbar_init(ofull, 1);
         mbar_init(oempty, TT_LOADERS);
@@ -624,6 +629,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         for (int i = 0; i < 8; ++i) {
             mbar_init(&xfull[i], 1);
             mbar_init(&xempty[i], 1);
+            mbar_init(&yfull[i], 1);
+            mbar_init(&yempty[i], 1);
         }
         fence_mbar_init();
         for (int i = 0; i < 3; ++i) prefetch_tmap(&maps.m[i]);
@@ -683,19 +690,25 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
             uint64_t* last = nullptr;
             uint32_t last_par = 0;
             long long idle = clock64();
+            uint32_t part = 0;                                // of PV's tile: this CTA's slots, the peer's
             while (cp.more) {
-                if (cp.g < cq.g && mbar_test(&pfull[cp.g & 1], (cp.g >> 1) & 1) &&
-                    (cp.tt > 0 || cp.qi == 0 || mbar_test(oempty, (cp.qi - 1) & 1))) {
+                if (cp.g < cq.g && mbar_test(&pfull[2 * (cp.g & 1) + part], (cp.g >> 1) & 1) &&
+                    (part > 0 || cp.tt > 0 || cp.qi == 0 || mbar_test(oempty, (cp.qi - 1) & 1))) {
                     tc_fence_after();
                     const int buf = cp.g & 1;
                     const uint32_t kb = (uint32_t)buf * (TT_TILE_BYTES >> 4), p = tmem + 256 + 128 * buf;
+                    const uint32_t ks0 = 4 * (part ^ rank);
 #pragma unroll
-                    for (uint32_t ks = 0; ks < 8; ++ks) {
-                        mma_ts(tmem, p + (ks >> 2) * 64 + (ks & 3) * 8, dv + (kb + ks * (2048 >> 4)), IDESC_PV, cp.tt > 0 || ks > 0);
-                        if (ks & 1) mma_commit(&kempty[4 * buf + (ks >> 1)]);
+                    for (uint32_t i = 0; i < 4; ++i) {
+                        const uint32_t ks = ks0 + i;
+                        mma_ts(tmem, p + (ks >> 1) * 32 + (ks & 1) * 8, dv + (kb + ks * (2048 >> 4)), IDESC_PV, cp.tt > 0 || part > 0 || i > 0);
+                        if (i & 1) mma_commit(&kempty[4 * buf + (ks >> 1)]);
                     }
-                    last = &kempty[4 * buf + 3];
+                    last = &kempty[4 * buf + (ks0 >> 1) + 1];
                     last_par = (cp.g >> 1) & 1;
+                    idle = clock64();
+                    part ^= 1;
+                    if (part) continue;
                     if (cp.tt == cp.nt - 1) {
                         mma_commit(ofull);
                         last = ofull;
@@ -703,7 +716,6 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                     }
                     ++cp.g;
                     next(cp);
-                    idle = clock64();
                 } else if (cq.more && cq.g < cp.g + 2 && mbar_test(&kfull[cq.g & 1], (cq.g >> 1) & 1) &&
                            (cq.tt > 0 || mbar_test(qfull, cq.qi & 1))) {
                     tc_fence_after();
@@ -770,7 +782,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                     }
                 }
                 // (its products done, a tile's softmax has read its masks)
-                const bool wt = g < 2 || mbar_wait(&kempty[4 * (g & 1) + 3], ((g - 2) >> 1) & 1, a.budget, a.st);
+                const bool wt = g < 2 || mbar_wait(&kempty[4 * (g & 1) + 2 * peer + 1], ((g - 2) >> 1) & 1, a.budget, a.st);
                 ok = __all_sync(FULL, wt);
                 if (!ok) break;
                 sMask[((g & 1) * TT_G + n) * 4 + w] = m;
@@ -786,30 +798,33 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         const bool live = quad * 32 < a.l.G * a.l.H;          // a warp without query rows only keeps step
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         const int g_row = min(r / a.l.H, a.l.G - 1);
-        uint8_t* mine = sX + (hh * 8 * TT_ROWS + r) * 16;
-        const uint32_t theirs = peer_addr(mine, peer);
-        const uint32_t their_full = peer_addr(&xfull[w], peer), their_empty = peer_addr(&xempty[w], peer);
+        // 32-slot groups of a tile: the one that this warp weighs, the one of its twin in the peer
+        const int own = 2 * rank + hh, other = 2 * peer + hh;
+        uint8_t* mine_x = sX + (hh * 4 * TT_ROWS + r) * 16;
+        uint8_t* mine_y = mine_x + 8 * TT_ROWS * 16;
+        const uint32_t their_x = peer_addr(mine_x, peer), their_y = peer_addr(mine_y, peer);
+        const uint32_t x_full = peer_addr(&xfull[w], peer), x_empty = peer_addr(&xempty[w], peer);
+        const uint32_t y_full = peer_addr(&yfull[w], peer), y_empty = peer_addr(&yempty[w], peer);
         int g = 0, qi = 0;
+        int nx = 0;                                           // exchanges by way of sX so far
         bool ok = true;
         while (ok && walk.next(a, it)) {
             uint64_t lsum = two(0.0f, 0.0f);
             for (int tt = 0; tt < it.nt; ++tt, ++g) {
-                // (the peer has read the last tile's halves long before this one's logits come)
-                bool wt = (g == 0 || !live || mbar_wait(&xempty[w], (g - 1) & 1, a.budget, a.st)) &&
+                // (the peer has read the last exchange long before this tile's logits come)
+                bool wt = (nx == 0 || !live || mbar_wait(&xempty[w], (nx - 1) & 1, a.budget, a.st)) &&
                           mbar_wait(&sfull[g & 1], (g >> 1) & 1, a.budget, a.st);
-                if (!__all_sync(FULL, wt)) {
-                    ok = false;
-                    break;
-                }
+                ok = __all_sync(FULL, wt);
+                if (!ok) break;
                 tc_fence_after();
-                const float4* fac = reinterpret_cast<const float4*>(sF + (g & 1) * TT_TILE + 64 * hh);
-                const uint32_t s_col = lanes + 256 + 128 * (g & 1) + 64 * hh;
+                const uint32_t s_col = lanes + 256 + 128 * (g & 1);
                 if (live) {
-                    // this CTA's halves to the peer
+                    // the half logits of the peer's slots to the peer
+                    const float4* fac = reinterpret_cast<const float4*>(sF + (g & 1) * TT_TILE + 32 * other);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 2; ++i) {
                         uint32_t sv[16], y[8];
-                        tmem_ld16(s_col + 16 * i, sv);
+                        tmem_ld16(s_col + 32 * other + 16 * i, sv);
                         tmem_wait_ld();
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -819,29 +834,32 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                             y[2 * j] = pack_f16(y0.x, y0.y);
                             y[2 * j + 1] = pack_f16(y1.x, y1.y);
                         }
-                        peer_st4(theirs + 2 * i * TT_ROWS * 16, y[0], y[1], y[2], y[3], their_full);
-                        peer_st4(theirs + (2 * i + 1) * TT_ROWS * 16, y[4], y[5], y[6], y[7], their_full);
+                        peer_st4(their_x + 2 * i * TT_ROWS * 16, y[0], y[1], y[2], y[3], x_full);
+                        peer_st4(their_x + (2 * i + 1) * TT_ROWS * 16, y[4], y[5], y[6], y[7], x_full);
                     }
                     // (a warp without rows must not: it could fall two phases behind its peer)
-                    if (lane == 0) mbar_arrive_expect_tx(&xfull[w], 32 * 8 * 16);
-                    wt = mbar_wait(&xfull[w], g & 1, a.budget, a.st);
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&xfull[w], 32 * 4 * 16);
+                        mbar_arrive_expect_tx(&yfull[w], 32 * 4 * 16);
+                    }
+                    wt = mbar_wait(&xfull[w], nx & 1, a.budget, a.st) && (g == 0 || mbar_wait(&yempty[w], (g - 1) & 1, a.budget, a.st));
+                    ++nx;
                 }
-                if (!__all_sync(FULL, wt)) {
-                    ok = false;
-                    break;
-                }
+                ok = __all_sync(FULL, wt);
+                if (!ok) break;
                 if (live) {
-                    const uint2 m = *reinterpret_cast<const uint2*>(sMask + ((g & 1) * TT_G + g_row) * 4 + 2 * hh);
-                    // p = 2^z, P' = p f in the place of the logits; 16 slots at a time
+                    const float4* fac = reinterpret_cast<const float4*>(sF + (g & 1) * TT_TILE + 32 * own);
+                    const uint32_t m = sMask[((g & 1) * TT_G + g_row) * 4 + own];
+                    // p = 2^z, P' = p f in the place of the logits, here and at the peer; 16 slots at a time
                     const auto tile_p = [&](auto all) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < 2; ++i) {
                             uint32_t sv[16], pk[8];
-                            tmem_ld16(s_col + 16 * i, sv);
-                            const uint4 o0 = *reinterpret_cast<const uint4*>(mine + 2 * i * TT_ROWS * 16);
-                            const uint4 o1 = *reinterpret_cast<const uint4*>(mine + (2 * i + 1) * TT_ROWS * 16);
+                            tmem_ld16(s_col + 32 * own + 16 * i, sv);
+                            const uint4 o0 = *reinterpret_cast<const uint4*>(mine_x + 2 * i * TT_ROWS * 16);
+                            const uint4 o1 = *reinterpret_cast<const uint4*>(mine_x + (2 * i + 1) * TT_ROWS * 16);
                             const uint32_t ov[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
-                            const uint32_t mb = (i < 2 ? m.x : m.y) >> (16 * (i & 1));
+                            const uint32_t mb = m >> (16 * i);
                             tmem_wait_ld();
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
@@ -865,28 +883,65 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                                     pk[j] = pack_bf16(m0 ? p0 * ff.x : 0.0f, m1 ? p1 * ff.y : 0.0f);
                                 }
                             }
-                            tmem_st8(s_col + 8 * i, pk);
+                            tmem_st8(s_col + 32 * own + 8 * i, pk);
+                            peer_st4(their_y + 2 * i * TT_ROWS * 16, pk[0], pk[1], pk[2], pk[3], y_full);
+                            peer_st4(their_y + (2 * i + 1) * TT_ROWS * 16, pk[4], pk[5], pk[6], pk[7], y_full);
                         }
                     };
-                    if (__all_sync(FULL, (m.x & m.y) == FULL)) tile_p(std::true_type{});
+                    if (__all_sync(FULL, m == FULL)) tile_p(std::true_type{});
                     else tile_p(std::false_type{});
                     tmem_wait_st();
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&pfull[g & 1]);
-                    if (live) peer_arrive(their_empty);
+                    mbar_arrive(&pfull[2 * (g & 1)]);
+                    if (live) peer_arrive(x_empty);
+                }
+                if (live) {
+                    // the peer's P'
+                    wt = mbar_wait(&yfull[w], g & 1, a.budget, a.st);
+                    ok = __all_sync(FULL, wt);
+                    if (!ok) break;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 o0 = *reinterpret_cast<const uint4*>(mine_y + 2 * i * TT_ROWS * 16);
+                        const uint4 o1 = *reinterpret_cast<const uint4*>(mine_y + (2 * i + 1) * TT_ROWS * 16);
+                        const uint32_t pk[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+                        tmem_st8(s_col + 32 * other + 8 * i, pk);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                }
+                if (lane == 0) {
+                    mbar_arrive(&pfull[2 * (g & 1) + 1]);
+                    if (live) peer_arrive(y_empty);
                 }
             }
             if (!ok) break;
-            // the sums of this half of the slots; the last item's readers are done with sL
-            const bool wt = qi == 0 || mbar_wait(oempty, (qi - 1) & 1, a.budget, a.st);
+            // the rows' sums: this warp's slots and its twin's; the last item's readers are done with sL
             const float2 ls = two_of(lsum);
-            if (wt) sL[hh * TT_ROWS + r] = ls.x + ls.y;
+            float sum = ls.x + ls.y;
+            bool wt = true;
+            if (live) {
+                wt = mbar_wait(&xempty[w], (nx - 1) & 1, a.budget, a.st);
+                ok = __all_sync(FULL, wt);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&xfull[w], 32 * 4);
+                peer_st1(their_x, __float_as_uint(sum), x_full);
+                wt = mbar_wait(&xfull[w], nx & 1, a.budget, a.st);
+                if (wt) sum += *reinterpret_cast<const float*>(mine_x);
+                ++nx;
+            }
+            wt = wt && (qi == 0 || mbar_wait(oempty, (qi - 1) & 1, a.budget, a.st));
             ok = __all_sync(FULL, wt);
+            if (ok) sL[hh * TT_ROWS + r] = sum;
             __syncwarp();
-            if (lane == 0) mbar_arrive(lred);
+            if (lane == 0) {
+                mbar_arrive(lred);
+                if (live) peer_arrive(x_empty);
+            }
             ++qi;
         }
     } else if (warp >= 12) {
