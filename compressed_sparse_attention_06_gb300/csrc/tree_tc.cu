@@ -603,6 +603,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
     uint64_t* ofull = bars + 10;
     uint64_t* oempty = bars + 11;
     uint64_t* lred = bars + 12;
+    uint64_t* done = bars + 13;        // [2] the last half logits, the last products
     uint64_t* kempty = bars + 16;      // [2][4] the products of a tile's 32-row groups are done
     uint64_t* xfull = bars + 24;       // [8] the peer's half logits for a softmax warp, its sums
     uint64_t* xempty = bars + 32;      // [8] the peer has read this warp's
@@ -626,6 +627,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         mbar_init(ofull, 1);
         mbar_init(oempty, TT_LOADERS);
         mbar_init(lred, 8);
+        mbar_init(&done[0], 1);
+        mbar_init(&done[1], 1);
         for (int i = 0; i < 8; ++i) {
             mbar_init(&xfull[i], 1);
             mbar_init(&xempty[i], 1);
@@ -664,62 +667,22 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
             if (issued >= 0) mbar_wait(qfull, issued & 1, a.budget, a.st);
         }
     } else if (warp == 1) {
-        // ============================ MMA issuer ============================
+        // ============================ half logits ============================
         if (lane == 0) {
             constexpr uint32_t IDESC_QK = idesc_f16(TT_ROWS, TT_TILE, true);
-            constexpr uint32_t IDESC_PV = idesc_f16_major(TT_ROWS, TT_HALF, true, false, true);
             // descriptors of the operands' first bytes: an address further on adds to the low field
             const uint64_t dq = sdesc_sw128(smem_u32(sQ)), dk = sdesc_sw128(smem_u32(sK));
-            const uint64_t dv = sdesc_sw128_mn(smem_u32(sK), TT_CHUNK, 1024);
-            // Two cursors over the tiles: QK runs up to two tiles (the logits' buffers) ahead of PV, and
-            // whichever has its operands goes next, across the items' borders too.
-            struct Cursor {
-                TtWalk w;
-                int tt, nt, g, qi;
-                bool more;
-            } cq = {walk, 0, 0, 0, -1, true}, cp = cq;
-            const auto next = [&](Cursor& c) {               // to the next tile
-                if (++c.tt < c.nt) return;
-                c.more = c.w.next(a, it);
-                c.nt = it.nt;
-                c.tt = 0;
-                ++c.qi;
-            };
-            next(cq);
-            next(cp);
-            uint64_t* last = nullptr;
-            uint32_t last_par = 0;
-            long long idle = clock64();
-            uint32_t part = 0;                                // of PV's tile: this CTA's slots, the peer's
-            while (cp.more) {
-                if (cp.g < cq.g && mbar_test(&pfull[2 * (cp.g & 1) + part], (cp.g >> 1) & 1) &&
-                    (part > 0 || cp.tt > 0 || cp.qi == 0 || mbar_test(oempty, (cp.qi - 1) & 1))) {
+            int g = 0, qi = 0;
+            bool ok = true;
+            while (ok && walk.next(a, it)) {
+                ok = mbar_wait(qfull, qi++ & 1, a.budget, a.st);
+                for (int tt = 0; tt < it.nt && ok; ++tt, ++g) {
+                    // (a tile's rows are there: the products of the tile two before, which read its P' from where
+                    // the logits go, are done)
+                    const int buf = g & 1;
+                    ok = mbar_wait(&kfull[buf], (g >> 1) & 1, a.budget, a.st);
+                    if (!ok) break;
                     tc_fence_after();
-                    const int buf = cp.g & 1;
-                    const uint32_t kb = (uint32_t)buf * (TT_TILE_BYTES >> 4), p = tmem + 256 + 128 * buf;
-                    const uint32_t ks0 = 4 * (part ^ rank);
-#pragma unroll
-                    for (uint32_t i = 0; i < 4; ++i) {
-                        const uint32_t ks = ks0 + i;
-                        mma_ts(tmem, p + (ks >> 1) * 32 + (ks & 1) * 8, dv + (kb + ks * (2048 >> 4)), IDESC_PV, cp.tt > 0 || part > 0 || i > 0);
-                        if (i & 1) mma_commit(&kempty[4 * buf + (ks >> 1)]);
-                    }
-                    last = &kempty[4 * buf + (ks0 >> 1) + 1];
-                    last_par = (cp.g >> 1) & 1;
-                    idle = clock64();
-                    part ^= 1;
-                    if (part) continue;
-                    if (cp.tt == cp.nt - 1) {
-                        mma_commit(ofull);
-                        last = ofull;
-                        last_par = cp.qi & 1;
-                    }
-                    ++cp.g;
-                    next(cp);
-                } else if (cq.more && cq.g < cp.g + 2 && mbar_test(&kfull[cq.g & 1], (cq.g >> 1) & 1) &&
-                           (cq.tt > 0 || mbar_test(qfull, cq.qi & 1))) {
-                    tc_fence_after();
-                    const int buf = cq.g & 1;
                     const uint32_t sc = tmem + 256 + 128 * buf, kb = (uint32_t)buf * (TT_TILE_BYTES >> 4);
 #pragma unroll
                     for (uint32_t kk = 0; kk < 16; ++kk) {
@@ -727,22 +690,44 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                         mma_ss(sc, dq + o, dk + (kb + o), IDESC_QK, kk != 0);
                     }
                     mma_commit(&sfull[buf]);
-                    last = &sfull[buf];
-                    last_par = (cq.g >> 1) & 1;
-                    if (cq.tt == cq.nt - 1) mma_commit(qempty);
-                    ++cq.g;
-                    next(cq);
-                    idle = clock64();
-                } else {
-                    __nanosleep(20);                          // (polling takes issue slots from the softmax)
-                    if (clock64() - idle > a.budget) {
-                        csa2_flag(a.st, CSA2_DEVBIT_TIMEOUT);
-                        break;
-                    }
+                    if (tt == it.nt - 1) mma_commit(qempty);
                 }
             }
             // the MMAs must be complete before tensor memory is released
-            if (last) mbar_wait(last, last_par, a.budget, a.st);
+            mma_commit(&done[0]);
+            mbar_wait(&done[0], 0, a.budget, a.st);
+        }
+    } else if (warp == 3) {
+        // ============================ outputs ============================
+        if (lane == 0) {
+            constexpr uint32_t IDESC_PV = idesc_f16_major(TT_ROWS, TT_HALF, true, false, true);
+            const uint64_t dv = sdesc_sw128_mn(smem_u32(sK), TT_CHUNK, 1024);
+            int g = 0, qi = 0;
+            bool ok = true;
+            while (ok && walk.next(a, it)) {
+                for (int tt = 0; tt < it.nt && ok; ++tt, ++g) {
+                    const int buf = g & 1;
+                    const uint32_t kb = (uint32_t)buf * (TT_TILE_BYTES >> 4), p = tmem + 256 + 128 * buf;
+                    for (uint32_t part = 0; part < 2 && ok; ++part) {          // this CTA's slots, the peer's
+                        ok = mbar_wait(&pfull[2 * buf + part], (g >> 1) & 1, a.budget, a.st) &&
+                             (part > 0 || tt > 0 || qi == 0 || mbar_wait(oempty, (qi - 1) & 1, a.budget, a.st));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t ks0 = 4 * (part ^ rank);
+#pragma unroll
+                        for (uint32_t i = 0; i < 4; ++i) {
+                            const uint32_t ks = ks0 + i;
+                            mma_ts(tmem, p + (ks >> 1) * 32 + (ks & 1) * 8, dv + (kb + ks * (2048 >> 4)), IDESC_PV, tt > 0 || part > 0 || i > 0);
+                            if (i & 1) mma_commit(&kempty[4 * buf + (ks >> 1)]);
+                        }
+                    }
+                }
+                if (!ok) break;
+                mma_commit(ofull);
+                ++qi;
+            }
+            mma_commit(&done[1]);
+            mbar_wait(&done[1], 0, a.budget, a.st);
         }
     } else if (warp == 2) {
         // ============================ masks and factors ============================
