@@ -58,13 +58,14 @@ constexpr float LN2 = 0.6931471805599453f;
 constexpr long long TT_BUDGET = 1ll << 31;
 
 constexpr int OFF_Q = 0;
-constexpr int OFF_K = 65536;
-constexpr int OFF_X = OFF_K + 2 * TT_TILE_BYTES;         // the peer's logits: [2 halves][8 units][128 rows] x 16 B
-constexpr int OFF_F = OFF_X + 32768;                     // [2][128] the factors f
+constexpr int OFF_Y = 65536;                             // the peer's P': [2 groups][4 units of 8 slots][128 rows] x 16 B
+constexpr int OFF_X = OFF_Y + 16384;                     // its half logits, the same
+constexpr int OFF_K = OFF_X + 16384;
+constexpr int OFF_F = OFF_K + 2 * TT_TILE_BYTES;                     // [2][128] the factors f
 constexpr int OFF_L = OFF_F + 1024;                      // [2][128] sums of exponentials
 constexpr int OFF_MASK = OFF_L + 1024;                   // [2][TT_G][4] x 32 bits
 constexpr int OFF_BAR = OFF_MASK + 2 * TT_G * 16;
-constexpr int N_BAR = 16 + 8 + 4 * 8;
+constexpr int N_BAR = 18 + 8 + 2 * 8;
 constexpr int OFF_TMEM = OFF_BAR + N_BAR * 8;
 constexpr int TT_SMEM = OFF_TMEM + 16;
 static_assert(TT_SMEM <= 227 * 1024, "shared memory");
@@ -125,6 +126,25 @@ __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
     return r;
 }
+// 128 rows of 32 bytes into tensor memory: units of 16 bytes a row, 8 rows of a unit side by side
+// (sdesc_plain).  In order with the MMAs that the same thread issues.
+__device__ __forceinline__ void tmem_cp_128x256b(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// A K-major matrix without swizzle: `lbo` bytes from one 16-byte unit of a row to the next, `sbo` from
+// 8 rows of a unit to the next 8.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | (uint64_t)1 << 46;
+}
+// An arrival at the barrier of the same address in CTA `rank` of the cluster, when everything this
+// thread has issued to the tensor cores is done.
+__device__ __forceinline__ void mma_commit_to(uint64_t* bar, uint32_t rank) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     smem_u32(bar)),
+                 "h"((uint16_t)(1u << rank))
+                 : "memory");
+}
+
 // An arrival at a barrier of the peer's that says "read": the values read are in registers, and
 // nothing this thread wrote is behind it, so it carries no fence (a release at the cluster's scope
 // waits for every access of the thread).
@@ -139,19 +159,6 @@ __device__ __forceinline__ void peer_st4(uint32_t addr, uint32_t a, uint32_t b, 
 }
 __device__ __forceinline__ void peer_st1(uint32_t addr, uint32_t a, uint32_t bar) {
     asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr), "r"(a), "r"(bar) : "memory");
-}
-
-// Whether the phase of the given parity is complete, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -591,6 +598,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
     uint8_t* sQ = smem + OFF_Q;
     uint8_t* sK = smem + OFF_K;
     uint8_t* sX = smem + OFF_X;
+    uint8_t* sY = smem + OFF_Y;
     float* sF = reinterpret_cast<float*>(smem + OFF_F);
     float* sL = reinterpret_cast<float*>(smem + OFF_L);
     uint32_t* sMask = reinterpret_cast<uint32_t*>(smem + OFF_MASK);
@@ -599,16 +607,16 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
     uint64_t* qempty = bars + 1;
     uint64_t* kfull = bars + 2;        // [2] a tile's rows are in shared memory
     uint64_t* sfull = bars + 4;        // [2] its half logits, its factors and masks
-    uint64_t* pfull = bars + 6;        // [2][2] the P' of the slots that this CTA, that the peer weighs
+    uint64_t* pfull = bars + 6;        // [2] the P' of the slots that this CTA weighs
+    uint64_t* yfull = bars + 8;        // the peer's P'
+    uint64_t* yempty = bars + 9;       // the peer has taken this CTA's
     uint64_t* ofull = bars + 10;
     uint64_t* oempty = bars + 11;
     uint64_t* lred = bars + 12;
     uint64_t* done = bars + 13;        // [2] the last half logits, the last products
-    uint64_t* kempty = bars + 16;      // [2][4] the products of a tile's 32-row groups are done
-    uint64_t* xfull = bars + 24;       // [8] the peer's half logits for a softmax warp, its sums
-    uint64_t* xempty = bars + 32;      // [8] the peer has read this warp's
-    uint64_t* yfull = bars + 40;       // [8] the peer's P'
-    uint64_t* yempty = bars + 48;      // [8] the peer has read this warp's
+    uint64_t* kempty = bars + 18;      // [2][4] the products of a tile's 32-row groups are done
+    uint64_t* xfull = bars + 26;       // [8] the peer's half logits for a softmax warp, its sums
+    uint64_t* xempty = bars + 34;      // [8] the peer has read this warp's
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
@@ -622,8 +630,10 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
             mbar_init(&kfull[i], TT_LOADERS);
             for (int j = 0; j < 4; ++j) mbar_init(&kempty[4 * i + j], 1);
             mbar_init(&sfull[i], 2);
-            for (int j = 0; j < 2; ++j) mbar_init(&pfull[2 * i + j], 8);
+            mbar_init(&pfull[i], 8);
         }
+        mbar_init(yfull, 1);
+        mbar_init(yempty, 1);
         mbar_init(ofull, 1);
         mbar_init(oempty, TT_LOADERS);
         mbar_init(lred, 8);
@@ -632,8 +642,6 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         for (int i = 0; i < 8; ++i) {
             mbar_init(&xfull[i], 1);
             mbar_init(&xempty[i], 1);
-            mbar_init(&yfull[i], 1);
-            mbar_init(&yempty[i], 1);
         }
         fence_mbar_init();
         for (int i = 0; i < 3; ++i) prefetch_tmap(&maps.m[i]);
@@ -702,25 +710,37 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         if (lane == 0) {
             constexpr uint32_t IDESC_PV = idesc_f16_major(TT_ROWS, TT_HALF, true, false, true);
             const uint64_t dv = sdesc_sw128_mn(smem_u32(sK), TT_CHUNK, 1024);
+            const uint64_t dy = sdesc_plain(smem_u32(sY), TT_ROWS * 16, 128);
+            const uint32_t y_bytes = (uint32_t)((a.l.G * a.l.H + 31) / 32) * 2 * (32 * 4 * 16);      // of the warps with rows
             int g = 0, qi = 0;
             bool ok = true;
             while (ok && walk.next(a, it)) {
                 for (int tt = 0; tt < it.nt && ok; ++tt, ++g) {
                     const int buf = g & 1;
                     const uint32_t kb = (uint32_t)buf * (TT_TILE_BYTES >> 4), p = tmem + 256 + 128 * buf;
-                    for (uint32_t part = 0; part < 2 && ok; ++part) {          // this CTA's slots, the peer's
-                        ok = mbar_wait(&pfull[2 * buf + part], (g >> 1) & 1, a.budget, a.st) &&
-                             (part > 0 || tt > 0 || qi == 0 || mbar_wait(oempty, (qi - 1) & 1, a.budget, a.st));
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t ks0 = 4 * (part ^ rank);
+                    const auto products = [&](uint32_t ks0, bool first) {
 #pragma unroll
                         for (uint32_t i = 0; i < 4; ++i) {
                             const uint32_t ks = ks0 + i;
-                            mma_ts(tmem, p + (ks >> 1) * 32 + (ks & 1) * 8, dv + (kb + ks * (2048 >> 4)), IDESC_PV, tt > 0 || part > 0 || i > 0);
+                            mma_ts(tmem, p + (ks >> 1) * 32 + (ks & 1) * 8, dv + (kb + ks * (2048 >> 4)), IDESC_PV, !first || i > 0);
                             if (i & 1) mma_commit(&kempty[4 * buf + (ks >> 1)]);
                         }
-                    }
+                    };
+                    mbar_arrive_expect_tx(yfull, y_bytes);
+                    ok = mbar_wait(&pfull[buf], (g >> 1) & 1, a.budget, a.st) &&
+                         (tt > 0 || qi == 0 || mbar_wait(oempty, (qi - 1) & 1, a.budget, a.st));
+                    if (!ok) break;
+                    tc_fence_after();
+                    products(4 * rank, tt == 0);
+                    // the peer's P' beside this CTA's (its slots' half logits are with the peer)
+                    ok = mbar_wait(yfull, g & 1, a.budget, a.st);
+                    if (!ok) break;
+                    fence_proxy_async_smem();
+#pragma unroll
+                    for (uint32_t i = 0; i < 4; ++i)
+                        tmem_cp_128x256b(p + 64 * peer + 32 * (i >> 1) + 8 * (i & 1), dy + i * (2 * TT_ROWS * 16 >> 4));
+                    mma_commit_to(yempty, peer);
+                    products(4 * peer, false);
                 }
                 if (!ok) break;
                 mma_commit(ofull);
@@ -786,10 +806,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         // 32-slot groups of a tile: the one that this warp weighs, the one of its twin in the peer
         const int own = 2 * rank + hh, other = 2 * peer + hh;
         uint8_t* mine_x = sX + (hh * 4 * TT_ROWS + r) * 16;
-        uint8_t* mine_y = mine_x + 8 * TT_ROWS * 16;
-        const uint32_t their_x = peer_addr(mine_x, peer), their_y = peer_addr(mine_y, peer);
-        const uint32_t x_full = peer_addr(&xfull[w], peer), x_empty = peer_addr(&xempty[w], peer);
-        const uint32_t y_full = peer_addr(&yfull[w], peer), y_empty = peer_addr(&yempty[w], peer);
+        const uint32_t their_x = peer_addr(mine_x, peer), their_y = peer_addr(sY + (hh * 4 * TT_ROWS + r) * 16, peer);
+        const uint32_t x_full = peer_addr(&xfull[w], peer), x_empty = peer_addr(&xempty[w], peer), y_full = peer_addr(yfull, peer);
         int g = 0, qi = 0;
         int nx = 0;                                           // exchanges by way of sX so far
         bool ok = true;
@@ -823,11 +841,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                         peer_st4(their_x + (2 * i + 1) * TT_ROWS * 16, y[4], y[5], y[6], y[7], x_full);
                     }
                     // (a warp without rows must not: it could fall two phases behind its peer)
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&xfull[w], 32 * 4 * 16);
-                        mbar_arrive_expect_tx(&yfull[w], 32 * 4 * 16);
-                    }
-                    wt = mbar_wait(&xfull[w], nx & 1, a.budget, a.st) && (g == 0 || mbar_wait(&yempty[w], (g - 1) & 1, a.budget, a.st));
+                    if (lane == 0) mbar_arrive_expect_tx(&xfull[w], 32 * 4 * 16);
+                    wt = mbar_wait(&xfull[w], nx & 1, a.budget, a.st) && (g == 0 || mbar_wait(yempty, (g - 1) & 1, a.budget, a.st));
                     ++nx;
                 }
                 ok = __all_sync(FULL, wt);
@@ -880,28 +895,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&pfull[2 * (g & 1)]);
+                    mbar_arrive(&pfull[g & 1]);
                     if (live) peer_arrive(x_empty);
-                }
-                if (live) {
-                    // the peer's P'
-                    wt = mbar_wait(&yfull[w], g & 1, a.budget, a.st);
-                    ok = __all_sync(FULL, wt);
-                    if (!ok) break;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint4 o0 = *reinterpret_cast<const uint4*>(mine_y + 2 * i * TT_ROWS * 16);
-                        const uint4 o1 = *reinterpret_cast<const uint4*>(mine_y + (2 * i + 1) * TT_ROWS * 16);
-                        const uint32_t pk[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
-                        tmem_st8(s_col + 32 * other + 8 * i, pk);
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                }
-                if (lane == 0) {
-                    mbar_arrive(&pfull[2 * (g & 1) + 1]);
-                    if (live) peer_arrive(y_empty);
                 }
             }
             if (!ok) break;
@@ -929,6 +924,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
             }
             ++qi;
         }
+        // (the peer's last arrival at this CTA's barriers)
+        if (ok && live && g > 0) mbar_wait(yempty, (g - 1) & 1, a.budget, a.st);
     } else if (warp >= 12) {
         // ============================ loaders, output ============================
         constexpr int ROWS = TT_TILE / TT_LOADERS;            // of a tile, a warp
