@@ -1099,14 +1099,20 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         look_up();
         int g = 0;
         bool ok = true;
-        for (; fetched; ++g) {
-            ok = outputs(g);
-            if (!ok) break;
+        const auto landed = [&](uint64_t* full) {             // the rows by asynchronous copies
+            cp_async_wait<0>();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full);
+        };
+        for (; ok && fetched; ++g) {
             const bool wt = g < 2 || mbar_wait(&kempty[4 * (g & 1) + row0 / 32], ((g - 2) >> 1) & 1, a.budget, a.st);
             ok = __all_sync(FULL, wt);
             if (!ok) break;
             uint8_t* tile = sK + (g & 1) * TT_TILE_BYTES;
             uint64_t* full = &kfull[g & 1];
+            const bool due = omore && oend <= g;              // an output before the next tile's rows
+            bool late = false;
             if (fp4_rows) {
                 const int piece = lane & 7, c = piece >> 1;
                 uint8_t* base = tile + c * TT_CHUNK;
@@ -1129,8 +1135,6 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full);
-                fetch();
-                look_up();
             } else if (box_row >= 0) {
                 if (lane == 0) {
                     mbar_arrive_expect_tx(full, ROWS * TT_HALF * 2);
@@ -1138,8 +1142,6 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                     for (int c = 0; c < 4; ++c)
                         tma_load_2d(tile + c * TT_CHUNK + row0 * 128, &maps.m[box_map], TT_HALF * rank + 64 * c, box_row, full);
                 }
-                fetch();
-                look_up();
             } else {
                 // a row an instruction, 16 bytes a lane
                 uint8_t* base = tile + (lane >> 3) * TT_CHUNK;
@@ -1150,13 +1152,15 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                                        reinterpret_cast<const uint8_t*>((uintptr_t)(p ? p : (uint64_t)(uintptr_t)a.l.qimg)) + 512 * rank + 16 * lane, p != 0);
                 }
                 cp_async_commit();
-                fetch();
-                look_up();
-                cp_async_wait<0>();
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full);
+                if (due) landed(full);
+                late = !due;
             }
+            // (no rows are in registers meanwhile)
+            if (due) ok = outputs(g + 1);
+            if (!ok) break;
+            fetch();
+            look_up();
+            if (late) landed(full);
         }
         if (ok) outputs(INT_MAX);
         // tensor copies must land before the CTA exits
