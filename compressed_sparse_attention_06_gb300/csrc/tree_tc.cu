@@ -50,7 +50,8 @@ constexpr int TT_C = 512, TT_HALF = 256;
 constexpr int TT_ROWS = 128, TT_TILE = 128;
 constexpr int TT_G = 8;                          // nodes of a group at most
 constexpr int TT_LOADERS = 8;                    // warps
-constexpr int TT_THREADS = 32 * (12 + TT_LOADERS);
+constexpr int TT_OUT = 4;                        // warps that store outputs
+constexpr int TT_THREADS = 32 * (12 + TT_LOADERS + TT_OUT);
 constexpr int TT_CHUNK = TT_TILE * 128;          // 16 KB: 128 rows x 64 dims
 constexpr int TT_TILE_BYTES = 4 * TT_CHUNK;
 constexpr float LOG2E = 1.4426950408889634f;
@@ -257,43 +258,41 @@ struct TtWalk {
         left = (int)max((int64_t)0, min((int64_t)a.share, rest - f0));
         load(a);
     }
-    // The next item with tiles; false at the end.  Empty ones (a group without slots, a short one's last
-    // tiles) are passed over, or returned with nt = 0 where `empty` is set.
-    __device__ __forceinline__ bool next(const TtArgs& a, TtItem& r, bool empty = false) {
-        for (;;) {
-            r.v = group(a);
-            if (r.v < 0) return false;
-            r.b = r.v / a.l.gps;
-            r.n0 = (r.v - r.b * a.l.gps) * a.l.G;
-            r.gv = min(a.l.G, a.r.T - r.n0);
-            r.kq = info.x;
-            r.slots = info.y;
-            r.ring = info.z;
-            r.rf = info.w;
-            int to = a.tiles;
-            r.t0 = 0;
-            r.piece = 0;
-            r.pieces = 1;
-            if (round < a.rounds) {
-                ++round;
-            } else {
-                to = min(a.tiles, at + left);
-                r.t0 = at;
-                if (a.pieces > 1) {
-                    const int64_t g0 = (int64_t)v * a.tiles;
-                    const int c0 = (int)(g0 / a.share);
-                    r.piece = cluster - c0;
-                    r.pieces = (int)((g0 + a.tiles - 1) / a.share) - c0 + 1;
-                    r.part = v * a.pieces;
-                }
-                left -= to - at;
-                ++v;
-                at = 0;
+    // The next item; false at the end.  One without slots (an empty group, a short one's last tiles) gets a
+    // tile of masked slots, so that no role meets a special case.
+    __device__ __forceinline__ bool next(const TtArgs& a, TtItem& r) {
+        r.v = group(a);
+        if (r.v < 0) return false;
+        r.b = r.v / a.l.gps;
+        r.n0 = (r.v - r.b * a.l.gps) * a.l.G;
+        r.gv = min(a.l.G, a.r.T - r.n0);
+        r.kq = info.x;
+        r.slots = info.y;
+        r.ring = info.z;
+        r.rf = info.w;
+        int to = a.tiles;
+        r.t0 = 0;
+        r.piece = 0;
+        r.pieces = 1;
+        if (round < a.rounds) {
+            ++round;
+        } else {
+            to = min(a.tiles, at + left);
+            r.t0 = at;
+            if (a.pieces > 1) {
+                const int64_t g0 = (int64_t)v * a.tiles;
+                const int c0 = (int)(g0 / a.share);
+                r.piece = cluster - c0;
+                r.pieces = (int)((g0 + a.tiles - 1) / a.share) - c0 + 1;
+                r.part = v * a.pieces;
             }
-            r.nt = max(0, min((r.slots + TT_TILE - 1) / TT_TILE, to) - r.t0);
-            load(a);
-            if (r.nt > 0 || empty) return true;
+            left -= to - at;
+            ++v;
+            at = 0;
         }
+        r.nt = max(1, min((r.slots + TT_TILE - 1) / TT_TILE, to) - r.t0);
+        load(a);
+        return true;
     }
 };
 
@@ -635,7 +634,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         mbar_init(yfull, 1);
         mbar_init(yempty, 1);
         mbar_init(ofull, 1);
-        mbar_init(oempty, TT_LOADERS);
+        mbar_init(oempty, TT_OUT);
         mbar_init(lred, 8);
         mbar_init(&done[0], 1);
         mbar_init(&done[1], 1);
@@ -810,95 +809,96 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         const uint32_t x_full = peer_addr(&xfull[w], peer), x_empty = peer_addr(&xempty[w], peer), y_full = peer_addr(yfull, peer);
         int g = 0, qi = 0;
         int nx = 0;                                           // exchanges by way of sX so far
+        uint64_t lsum = two(0.0f, 0.0f);
         bool ok = true;
-        while (ok && walk.next(a, it)) {
-            uint64_t lsum = two(0.0f, 0.0f);
-            for (int tt = 0; tt < it.nt; ++tt, ++g) {
-                // (the peer has read the last exchange long before this tile's logits come)
-                bool wt = (nx == 0 || !live || mbar_wait(&xempty[w], (nx - 1) & 1, a.budget, a.st)) &&
-                          mbar_wait(&sfull[g & 1], (g >> 1) & 1, a.budget, a.st);
-                ok = __all_sync(FULL, wt);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t s_col = lanes + 256 + 128 * (g & 1);
-                if (live) {
-                    // the half logits of the peer's slots to the peer
-                    const float4* fac = reinterpret_cast<const float4*>(sF + (g & 1) * TT_TILE + 32 * other);
+        const auto weigh = [&]() {
+            // (the peer has read the last exchange long before this tile's logits come)
+            bool wt = (nx == 0 || !live || mbar_wait(&xempty[w], (nx - 1) & 1, a.budget, a.st)) &&
+                      mbar_wait(&sfull[g & 1], (g >> 1) & 1, a.budget, a.st);
+            ok = __all_sync(FULL, wt);
+            if (!ok) return;
+            tc_fence_after();
+            const uint32_t s_col = lanes + 256 + 128 * (g & 1);
+            if (live) {
+                // the half logits of the peer's slots to the peer
+                const float4* fac = reinterpret_cast<const float4*>(sF + (g & 1) * TT_TILE + 32 * other);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t sv[16], y[8];
+                    tmem_ld16(s_col + 32 * other + 16 * i, sv);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 f = fac[4 * i + j];
+                        const float2 y0 = two_of(mul2(two(__uint_as_float(sv[4 * j]), __uint_as_float(sv[4 * j + 1])), two(f.x, f.y)));
+                        const float2 y1 = two_of(mul2(two(__uint_as_float(sv[4 * j + 2]), __uint_as_float(sv[4 * j + 3])), two(f.z, f.w)));
+                        y[2 * j] = pack_f16(y0.x, y0.y);
+                        y[2 * j + 1] = pack_f16(y1.x, y1.y);
+                    }
+                    peer_st4(their_x + 2 * i * TT_ROWS * 16, y[0], y[1], y[2], y[3], x_full);
+                    peer_st4(their_x + (2 * i + 1) * TT_ROWS * 16, y[4], y[5], y[6], y[7], x_full);
+                }
+                // (a warp without rows must not: it could fall two phases behind its peer)
+                if (lane == 0) mbar_arrive_expect_tx(&xfull[w], 32 * 4 * 16);
+                wt = mbar_wait(&xfull[w], nx & 1, a.budget, a.st) && (g == 0 || mbar_wait(yempty, (g - 1) & 1, a.budget, a.st));
+                ++nx;
+            }
+            ok = __all_sync(FULL, wt);
+            if (!ok) return;
+            if (live) {
+                const float4* fac = reinterpret_cast<const float4*>(sF + (g & 1) * TT_TILE + 32 * own);
+                const uint32_t m = sMask[((g & 1) * TT_G + g_row) * 4 + own];
+                // p = 2^z, P' = p f in the place of the logits, here and at the peer; 16 slots at a time
+                const auto tile_p = [&](auto all) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        uint32_t sv[16], y[8];
-                        tmem_ld16(s_col + 32 * other + 16 * i, sv);
+                        uint32_t sv[16], pk[8];
+                        tmem_ld16(s_col + 32 * own + 16 * i, sv);
+                        const uint4 o0 = *reinterpret_cast<const uint4*>(mine_x + 2 * i * TT_ROWS * 16);
+                        const uint4 o1 = *reinterpret_cast<const uint4*>(mine_x + (2 * i + 1) * TT_ROWS * 16);
+                        const uint32_t ov[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+                        const uint32_t mb = m >> (16 * i);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float4 f = fac[4 * i + j];
-                            const float2 y0 = two_of(mul2(two(__uint_as_float(sv[4 * j]), __uint_as_float(sv[4 * j + 1])), two(f.x, f.y)));
-                            const float2 y1 = two_of(mul2(two(__uint_as_float(sv[4 * j + 2]), __uint_as_float(sv[4 * j + 3])), two(f.z, f.w)));
-                            y[2 * j] = pack_f16(y0.x, y0.y);
-                            y[2 * j + 1] = pack_f16(y1.x, y1.y);
-                        }
-                        peer_st4(their_x + 2 * i * TT_ROWS * 16, y[0], y[1], y[2], y[3], x_full);
-                        peer_st4(their_x + (2 * i + 1) * TT_ROWS * 16, y[4], y[5], y[6], y[7], x_full);
-                    }
-                    // (a warp without rows must not: it could fall two phases behind its peer)
-                    if (lane == 0) mbar_arrive_expect_tx(&xfull[w], 32 * 4 * 16);
-                    wt = mbar_wait(&xfull[w], nx & 1, a.budget, a.st) && (g == 0 || mbar_wait(yempty, (g - 1) & 1, a.budget, a.st));
-                    ++nx;
-                }
-                ok = __all_sync(FULL, wt);
-                if (!ok) break;
-                if (live) {
-                    const float4* fac = reinterpret_cast<const float4*>(sF + (g & 1) * TT_TILE + 32 * own);
-                    const uint32_t m = sMask[((g & 1) * TT_G + g_row) * 4 + own];
-                    // p = 2^z, P' = p f in the place of the logits, here and at the peer; 16 slots at a time
-                    const auto tile_p = [&](auto all) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            uint32_t sv[16], pk[8];
-                            tmem_ld16(s_col + 32 * own + 16 * i, sv);
-                            const uint4 o0 = *reinterpret_cast<const uint4*>(mine_x + 2 * i * TT_ROWS * 16);
-                            const uint4 o1 = *reinterpret_cast<const uint4*>(mine_x + (2 * i + 1) * TT_ROWS * 16);
-                            const uint32_t ov[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
-                            const uint32_t mb = m >> (16 * i);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const float4 f4 = fac[4 * i + (j >> 1)];
-                                const uint64_t f = (j & 1) ? two(f4.z, f4.w) : two(f4.x, f4.y);
-                                const float2 o = __half22float2(*reinterpret_cast<const __half2*>(&ov[j]));
-                                const float2 z = two_of(fma2(two(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1])), f, two(o.x, o.y)));
-                                float p0 = ex2(z.x), p1 = ex2(z.y);
-                                if (all) {
-                                    const uint64_t p = two(p0, p1);
-                                    lsum = add2(lsum, p);
-                                    const float2 pf = two_of(mul2(p, f));
-                                    pk[j] = pack_bf16(pf.x, pf.y);
-                                } else {
-                                    // (a masked slot's factor may be NaN: its product must not count)
-                                    const bool m0 = (mb >> (2 * j)) & 1u, m1 = (mb >> (2 * j + 1)) & 1u;
-                                    p0 = m0 ? p0 : 0.0f;
-                                    p1 = m1 ? p1 : 0.0f;
-                                    lsum = add2(lsum, two(p0, p1));
-                                    const float2 ff = two_of(f);
-                                    pk[j] = pack_bf16(m0 ? p0 * ff.x : 0.0f, m1 ? p1 * ff.y : 0.0f);
-                                }
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 f4 = fac[4 * i + (j >> 1)];
+                            const uint64_t f = (j & 1) ? two(f4.z, f4.w) : two(f4.x, f4.y);
+                            const float2 o = __half22float2(*reinterpret_cast<const __half2*>(&ov[j]));
+                            const float2 z = two_of(fma2(two(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1])), f, two(o.x, o.y)));
+                            float p0 = ex2(z.x), p1 = ex2(z.y);
+                            if (all) {
+                                const uint64_t p = two(p0, p1);
+                                lsum = add2(lsum, p);
+                                const float2 pf = two_of(mul2(p, f));
+                                pk[j] = pack_bf16(pf.x, pf.y);
+                            } else {
+                                // (a masked slot's factor may be NaN: its product must not count)
+                                const bool m0 = (mb >> (2 * j)) & 1u, m1 = (mb >> (2 * j + 1)) & 1u;
+                                p0 = m0 ? p0 : 0.0f;
+                                p1 = m1 ? p1 : 0.0f;
+                                lsum = add2(lsum, two(p0, p1));
+                                const float2 ff = two_of(f);
+                                pk[j] = pack_bf16(m0 ? p0 * ff.x : 0.0f, m1 ? p1 * ff.y : 0.0f);
                             }
-                            tmem_st8(s_col + 32 * own + 8 * i, pk);
-                            peer_st4(their_y + 2 * i * TT_ROWS * 16, pk[0], pk[1], pk[2], pk[3], y_full);
-                            peer_st4(their_y + (2 * i + 1) * TT_ROWS * 16, pk[4], pk[5], pk[6], pk[7], y_full);
                         }
-                    };
-                    if (__all_sync(FULL, m == FULL)) tile_p(std::true_type{});
-                    else tile_p(std::false_type{});
-                    tmem_wait_st();
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&pfull[g & 1]);
-                    if (live) peer_arrive(x_empty);
-                }
+                        tmem_st8(s_col + 32 * own + 8 * i, pk);
+                        peer_st4(their_y + 2 * i * TT_ROWS * 16, pk[0], pk[1], pk[2], pk[3], y_full);
+                        peer_st4(their_y + (2 * i + 1) * TT_ROWS * 16, pk[4], pk[5], pk[6], pk[7], y_full);
+                    }
+                };
+                if (__all_sync(FULL, m == FULL)) tile_p(std::true_type{});
+                else tile_p(std::false_type{});
+                tmem_wait_st();
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&pfull[g & 1]);
+                if (live) peer_arrive(x_empty);
+            }
+        };
+        while (ok && walk.next(a, it)) {
+            for (int tt = 0; tt < it.nt && ok; ++tt, ++g) weigh();
             if (!ok) break;
             // the rows' sums: this warp's slots and its twin's; the last item's readers are done with sL
             const float2 ls = two_of(lsum);
@@ -923,11 +923,12 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                 if (live) peer_arrive(x_empty);
             }
             ++qi;
+            lsum = two(0.0f, 0.0f);
         }
         // (the peer's last arrival at this CTA's barriers)
         if (ok && live && g > 0) mbar_wait(yempty, (g - 1) & 1, a.budget, a.st);
-    } else if (warp >= 12) {
-        // ============================ loaders, output ============================
+    } else if (warp >= 12 && warp < 12 + TT_LOADERS) {
+        // ============================ loaders ============================
         constexpr int ROWS = TT_TILE / TT_LOADERS;            // of a tile, a warp
         const int lw = warp - 12;
         const uint32_t row0 = ROWS * lw;                      // rows row0 .. row0 + ROWS - 1
@@ -990,128 +991,17 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                 }
             }
         };
-        // The output of finished items: a walk of its own, which also meets the items without tiles.  Item i's
-        // last tile is e: its output comes after the rows of tile e + 1, whose buffer is free before, and before
-        // those of e + 2.
-        TtWalk owalk;
-        owalk.start(a, cluster);
-        TtItem oit;
-        int oq = 0, oend = 0;         // items with tiles so far, tiles up to the next one's end
-        bool omore = owalk.next(a, oit, true);
-        if (omore) oend = oit.nt;
-        constexpr int PART = TT_HALF / (TT_LOADERS / 4);         // dims of a warp
-        const int quad = warp & 3, r = quad * 32 + lane, hq = r / a.l.H, h = r - hq * a.l.H;
-        const int d0 = TT_HALF * rank + PART * (lw >> 2);
-        const bool live = quad * 32 < a.l.G * a.l.H, first_part = rank == 0 && lw < 4;
-        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + PART * (lw >> 2);
-        const auto output = [&]() {
-            const bool valid = r < oit.gv * a.l.H;
-            const int64_t bt = (int64_t)oit.b * a.r.T + oit.n0 + (valid ? hq : 0), orow = bt * a.l.H + h;
-            const bool part = oit.pieces > 1;
-            const int64_t prow = part ? (int64_t)(oit.part + oit.piece) * (a.l.G * a.l.H) + r : 0;
-            float L = 0.0f;
-            if (oit.nt > 0) {
-                const bool wt = mbar_wait(lred, oq & 1, a.budget, a.st) && mbar_wait(ofull, oq & 1, a.budget, a.st);
-                if (!__all_sync(FULL, wt)) return false;
-                tc_fence_after();
-                L = sL[r] + sL[TT_ROWS + r];
-            }
-            const float2 fin = part ? make_float2(1.0f, 0.0f) : finish_row(L, a.sink && valid ? a.sink[h] : -INFINITY);
-            if (valid && first_part) {
-                if (part) a.part_l[prow] = L;
-                else if (a.lse) a.lse[orow] = fin.y;
-            }
-            if (live && !(part && oit.nt == 0)) {
-                const float* cs = a.l.rope_cs + bt * 64;
-                const bool wide = part || a.out_f32;          // fp32 rows
-                // rows quad * 32 + (lane & ~3) + k, k < 4, of the group; 16 bytes a lane, four lanes side by side
-                const int r4 = quad * 32 + (lane & ~3), n4 = min(4, oit.gv * a.l.H - r4);
-                uint8_t* dst = part ? reinterpret_cast<uint8_t*>(a.part_o + (prow - r + r4) * (int64_t)TT_C)
-                                    : reinterpret_cast<uint8_t*>(a.out) + (((int64_t)oit.b * a.r.T + oit.n0) * a.l.H + r4) * (int64_t)(wide ? TT_C * 4 : TT_C * 2);
-                const int64_t pitch = wide ? TT_C * 4 : TT_C * 2;
-#pragma unroll 1
-                for (int db = 0; db < PART / 16; ++db) {
-                    const int d = d0 + 16 * db;
-                    float v[16];
-                    if (oit.nt > 0) {
-                        uint32_t o[16];
-                        tmem_ld16(lanes + 16 * db, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(o[i]) * fin.x;
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-                    }
-                    if (!part && (a.flags & CSA2_ROPE) && d >= TT_C - 64) {
-                        const float* c = cs + (d - (TT_C - 64)) / 2;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float x0 = v[2 * j], x1 = v[2 * j + 1];
-                            v[2 * j] = x0 * c[j] + x1 * c[32 + j];
-                            v[2 * j + 1] = x1 * c[j] - x0 * c[32 + j];
-                        }
-                    }
-                    if (wide) {
-                        uint4 p[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            p[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
-                                              __float_as_uint(v[4 * i + 3]));
-                        turn4(p);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (k < n4) *reinterpret_cast<uint4*>(dst + k * pitch + d * 4 + 16 * (lane & 3)) = p[k];
-                    } else {
-                        uint4 p[2];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            p[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                                              pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
-                        turn2(p);
-                        // lane pairs hold rows (lane & ~1) and the next one, 32 bytes side by side
-                        const int r2 = lane & 2;
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            if (r2 + k < n4) *reinterpret_cast<uint4*>(dst + (r2 + k) * pitch + d * 2 + 16 * (lane & 1)) = p[k];
-                    }
-                }
-            }
-            if (oit.nt > 0) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(oempty);
-                ++oq;
-            }
-            return true;
-        };
-        // the outputs due before the rows of tile t (at the end: all)
-        const auto outputs = [&](int t) {
-            while (omore && oend + 1 <= t) {
-                if (!output()) return false;
-                omore = owalk.next(a, oit, true);
-                if (omore) oend += oit.nt;
-            }
-            return true;
-        };
         look_up();
         fetch();
         look_up();
         int g = 0;
         bool ok = true;
-        const auto landed = [&](uint64_t* full) {             // the rows by asynchronous copies
-            cp_async_wait<0>();
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full);
-        };
-        for (; ok && fetched; ++g) {
+        for (; fetched; ++g) {
             const bool wt = g < 2 || mbar_wait(&kempty[4 * (g & 1) + row0 / 32], ((g - 2) >> 1) & 1, a.budget, a.st);
             ok = __all_sync(FULL, wt);
             if (!ok) break;
             uint8_t* tile = sK + (g & 1) * TT_TILE_BYTES;
             uint64_t* full = &kfull[g & 1];
-            const bool due = omore && oend <= g;              // an output before the next tile's rows
             bool late = false;
             if (fp4_rows) {
                 const int piece = lane & 7, c = piece >> 1;
@@ -1152,19 +1042,97 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                                        reinterpret_cast<const uint8_t*>((uintptr_t)(p ? p : (uint64_t)(uintptr_t)a.l.qimg)) + 512 * rank + 16 * lane, p != 0);
                 }
                 cp_async_commit();
-                if (due) landed(full);
-                late = !due;
+                late = true;
             }
-            // (no rows are in registers meanwhile)
-            if (due) ok = outputs(g + 1);
-            if (!ok) break;
             fetch();
             look_up();
-            if (late) landed(full);
+            if (late) {
+                cp_async_wait<0>();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full);
+            }
         }
-        if (ok) outputs(INT_MAX);
         // tensor copies must land before the CTA exits
         for (int t = max(0, g - 2); t < g; ++t) mbar_wait(&kfull[t & 1], (t >> 1) & 1, a.budget, a.st);
+    } else if (warp >= 12 + TT_LOADERS) {
+        // ============================ outputs ============================
+        const int quad = warp & 3, r = quad * 32 + lane, hq = r / a.l.H, h = r - hq * a.l.H;
+        const bool live = quad * 32 < a.l.G * a.l.H, first_part = rank == 0;
+        const int d0 = TT_HALF * rank;
+        const uint32_t o_col = tmem + ((uint32_t)(quad * 32) << 16);
+        int oq = 0;
+        while (walk.next(a, it)) {
+            const bool valid = r < it.gv * a.l.H;
+            const int64_t bt = (int64_t)it.b * a.r.T + it.n0 + (valid ? hq : 0), orow = bt * a.l.H + h;
+            const bool part = it.pieces > 1;
+            const int64_t prow = part ? (int64_t)(it.part + it.piece) * (a.l.G * a.l.H) + r : 0;
+            const bool wt = mbar_wait(lred, oq & 1, a.budget, a.st) && mbar_wait(ofull, oq & 1, a.budget, a.st);
+            if (!__all_sync(FULL, wt)) break;
+            tc_fence_after();
+            const float L = sL[r] + sL[TT_ROWS + r];
+            const float2 fin = part ? make_float2(1.0f, 0.0f) : finish_row(L, a.sink && valid ? a.sink[h] : -INFINITY);
+            if (valid && first_part) {
+                if (part) a.part_l[prow] = L;
+                else if (a.lse) a.lse[orow] = fin.y;
+            }
+            // (a piece without slots is left out of the sums)
+            if (live && !(part && it.t0 * TT_TILE >= it.slots)) {
+                const float* cs = a.l.rope_cs + bt * 64;
+                const bool wide = part || a.out_f32;          // fp32 rows
+                // rows quad * 32 + (lane & ~3) + k, k < 4, of the group; 16 bytes a lane, four lanes side by side
+                const int r4 = quad * 32 + (lane & ~3), n4 = min(4, it.gv * a.l.H - r4);
+                uint8_t* dst = part ? reinterpret_cast<uint8_t*>(a.part_o + (prow - r + r4) * (int64_t)TT_C)
+                                    : reinterpret_cast<uint8_t*>(a.out) + (((int64_t)it.b * a.r.T + it.n0) * a.l.H + r4) * (int64_t)(wide ? TT_C * 4 : TT_C * 2);
+                const int64_t pitch = wide ? TT_C * 4 : TT_C * 2;
+#pragma unroll 1
+                for (int db = 0; db < TT_HALF / 16; ++db) {
+                    const int d = d0 + 16 * db;
+                    float v[16];
+                    uint32_t o[16];
+                    tmem_ld16(o_col + 16 * db, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(o[i]) * fin.x;
+                    if (!part && (a.flags & CSA2_ROPE) && d >= TT_C - 64) {
+                        const float* c = cs + (d - (TT_C - 64)) / 2;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float x0 = v[2 * j], x1 = v[2 * j + 1];
+                            v[2 * j] = x0 * c[j] + x1 * c[32 + j];
+                            v[2 * j + 1] = x1 * c[j] - x0 * c[32 + j];
+                        }
+                    }
+                    if (wide) {
+                        uint4 p[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            p[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                                              __float_as_uint(v[4 * i + 3]));
+                        turn4(p);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k < n4) *reinterpret_cast<uint4*>(dst + k * pitch + d * 4 + 16 * (lane & 3)) = p[k];
+                    } else {
+                        uint4 p[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            p[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                                              pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+                        turn2(p);
+                        // lane pairs hold rows (lane & ~1) and the next one, 32 bytes side by side
+                        const int r2 = lane & 2;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            if (r2 + k < n4) *reinterpret_cast<uint4*>(dst + (r2 + k) * pitch + d * 2 + 16 * (lane & 1)) = p[k];
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(oempty);
+            ++oq;
+        }
     }
     tc_fence_before();
     __syncthreads();
