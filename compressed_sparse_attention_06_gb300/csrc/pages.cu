@@ -71,6 +71,8 @@ static_assert(PG_WARPS == 32, "one warp scans the warps' totals");
 
 __global__ void __launch_bounds__(256) pages_fork_kernel(int32_t* refs, int64_t n_pages, const int32_t* table, int B, int P,
                                                          const int32_t* parent, int64_t total, int32_t* out, unsigned* st) {
+    pdl_wait();
+    pdl_trigger();
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t b = i / P;
         const int32_t p = parent[b];
@@ -87,6 +89,8 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(int32_t* refs, int64_t 
 
 __global__ void __launch_bounds__(256) pages_free_kernel(int32_t* refs, int64_t n_pages, int32_t* table, int P, int64_t total,
                                                          int page, const int64_t* keep, unsigned* st) {
+    pdl_wait();
+    pdl_trigger();
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t b = i / P;
         const int64_t k = keep ? keep[b] : 0;
@@ -164,6 +168,8 @@ __global__ void __launch_bounds__(PG_THREADS) pages_reserve_kernel(const Reserve
     ReserveSmem& s = *reinterpret_cast<ReserveSmem*>(raw);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t rank = cta_rank();
+    pdl_wait();
+    pdl_trigger();
     cluster_sync();                      // every CTA runs: its shared memory may be written
     // the sequences of this CTA, and the words of their pages
     const int nc = gridDim.x;
@@ -305,6 +311,8 @@ __global__ void __launch_bounds__(PG_THREADS) pages_compact_kernel(const Compact
     __shared__ uint32_t tmp[PG_WARPS + 1], used[PG_CTAS], from[PG_CTAS], into[PG_CTAS];
     const int nc = gridDim.x;
     const uint32_t rank = cta_rank();
+    pdl_wait();
+    pdl_trigger();
     cluster_sync();                      // every CTA runs: its shared memory may be written
     const int64_t share = ((a.n_pages + nc - 1) / nc + 3) / 4 * 4;
     const int64_t p0 = min(a.n_pages, rank * share), p1 = min(a.n_pages, p0 + share);
@@ -382,6 +390,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_compact_kernel(const Compact
 __global__ void __launch_bounds__(256) pages_remap_kernel(int32_t* table, int64_t total, int64_t n_pages, const int32_t* to,
                                                           const int64_t* cut_p, unsigned* st) {
     pdl_wait();
+    pdl_trigger();
     const int64_t cut = *cut_p;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
         const int32_t t = table[i];
@@ -404,6 +413,8 @@ __global__ void __launch_bounds__(PC_THREADS) page_copy_kernel(V* pool, int64_t 
                                                                int64_t n, int pairs_b, int64_t chunks, unsigned* st) {
     __shared__ int64_t from[PC_PAIRS], to[PC_PAIRS];     // first pieces of the block's pages, -1 = nothing to move
     const int64_t groups = (n + pairs_b - 1) / pairs_b;
+    pdl_wait();
+    pdl_trigger();
     for (int64_t i = blockIdx.x; i < groups * chunks; i += gridDim.x) {
         const int64_t g = chunks == 1 ? i : i / chunks, p0 = g * pairs_b;
         const int np = (int)min((int64_t)pairs_b, n - p0);
@@ -463,6 +474,8 @@ __global__ void __launch_bounds__(PC_THREADS) page_rows_kernel(V* pool, V* dense
     __shared__ int64_t at[PC_THREADS * PC_PIECES];   // first piece of the row in the pool, -1 = none
     const int64_t r0 = (int64_t)blockIdx.x * a.rows_b;
     const uint32_t nr = (uint32_t)min((int64_t)a.rows_b, a.rows - r0), total = nr * a.pieces;
+    pdl_wait();
+    pdl_trigger();
     for (uint32_t r = threadIdx.x; r < nr; r += PC_THREADS) {
         const int64_t row = r0 + r, b = row / a.n;
         int64_t e = -1;
@@ -530,8 +543,10 @@ void cluster_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* at, int64_t n_
     at[0].val.clusterDim.x = nc;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
 }
 
 // Arguments every call of the page state shares.
@@ -564,16 +579,16 @@ csa2_status rows_call(csa2_ctx* ctx, bool write, void* pool, int64_t n_pages, in
     const RowsArgs a = {n_pages, P, page, table, first, count, idx, n, rows, (uint32_t)pieces, (uint32_t)rows_b, ctx->status};
     cudaStream_t s = as_stream(stream);
     const unsigned g = (unsigned)blocks;
+    csa2_status r;
     if (wide) {
         uint4 *p = reinterpret_cast<uint4*>(pool), *d = reinterpret_cast<uint4*>(dense);
-        if (write) page_rows_kernel<uint4, true><<<g, PC_THREADS, 0, s>>>(p, d, a);
-        else page_rows_kernel<uint4, false><<<g, PC_THREADS, 0, s>>>(p, d, a);
+        r = launch_pdl(write ? page_rows_kernel<uint4, true> : page_rows_kernel<uint4, false>, dim3(g), dim3(PC_THREADS), 0, s, p, d, a);
     } else {
         uint32_t *p = reinterpret_cast<uint32_t*>(pool), *d = reinterpret_cast<uint32_t*>(dense);
-        if (write) page_rows_kernel<uint32_t, true><<<g, PC_THREADS, 0, s>>>(p, d, a);
-        else page_rows_kernel<uint32_t, false><<<g, PC_THREADS, 0, s>>>(p, d, a);
+        r = launch_pdl(write ? page_rows_kernel<uint32_t, true> : page_rows_kernel<uint32_t, false>, dim3(g), dim3(PC_THREADS), 0, s, p, d,
+                       a);
     }
-    return csa2_launch_status();
+    return r != CSA2_OK ? r : csa2_launch_status();
 }
 
 int reserve_words(int P) { return P / 32 + 1; }      // a range of P pages at most, from any page on
@@ -592,9 +607,9 @@ extern "C" csa2_status csa2_pages_fork(csa2_ctx* ctx, int32_t* refs, int64_t n_p
     if (overlap(table, (size_t)B * max_pages * 4, table_out, (size_t)total * 4)) return CSA2_ERR_INVALID_ARG;
     DeviceGuard dev(ctx);
     if (!dev.ok) return CSA2_ERR_CUDA;
-    pages_fork_kernel<<<flat_grid(ctx, total), 256, 0, as_stream(stream)>>>(refs, n_pages, table, B, max_pages, parent, total,
-                                                                           table_out, ctx->status);
-    return csa2_launch_status();
+    const csa2_status l = launch_pdl(pages_fork_kernel, dim3(flat_grid(ctx, total)), dim3(256), 0, as_stream(stream), refs, n_pages, table,
+                                     B, max_pages, parent, total, table_out, ctx->status);
+    return l != CSA2_OK ? l : csa2_launch_status();
 }
 
 extern "C" csa2_status csa2_pages_free(csa2_ctx* ctx, int32_t* refs, int64_t n_pages, int32_t* table, int B, int max_pages,
@@ -606,9 +621,9 @@ extern "C" csa2_status csa2_pages_free(csa2_ctx* ctx, int32_t* refs, int64_t n_p
     if (total == 0) return CSA2_OK;
     DeviceGuard dev(ctx);
     if (!dev.ok) return CSA2_ERR_CUDA;
-    pages_free_kernel<<<flat_grid(ctx, total), 256, 0, as_stream(stream)>>>(refs, n_pages, table, max_pages, total, page, keep,
-                                                                           ctx->status);
-    return csa2_launch_status();
+    const csa2_status l = launch_pdl(pages_free_kernel, dim3(flat_grid(ctx, total)), dim3(256), 0, as_stream(stream), refs, n_pages, table,
+                                     max_pages, total, page, keep, ctx->status);
+    return l != CSA2_OK ? l : csa2_launch_status();
 }
 
 extern "C" size_t csa2_pages_reserve_workspace_bytes(int64_t n_pages, int B, int max_pages) {
@@ -634,7 +649,7 @@ extern "C" csa2_status csa2_pages_reserve(csa2_ctx* ctx, int32_t* refs, int64_t 
     a.base = a.want + (size_t)B * a.W;
     CSA2_CHECK_CUDA(cudaFuncSetAttribute(pages_reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ReserveSmem)));
     cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     cluster_config(cfg, at, n_pages, B, sizeof(ReserveSmem), as_stream(stream));
     if (cudaLaunchKernelEx(&cfg, pages_reserve_kernel, a) != cudaSuccess) return CSA2_ERR_CUDA;
     return csa2_launch_status();
@@ -665,7 +680,7 @@ extern "C" csa2_status csa2_pages_compact(csa2_ctx* ctx, int32_t* refs, int64_t 
     int32_t* to = reinterpret_cast<int32_t*>(ws) + 4;
     const CompactArgs a = {refs, n_pages, moves, n_used, to, cut};
     cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     cluster_config(cfg, at, n_pages, 0, 0, s);
     if (cudaLaunchKernelEx(&cfg, pages_compact_kernel, a) != cudaSuccess) return CSA2_ERR_CUDA;
     const int64_t total = (int64_t)B * max_pages;
@@ -690,13 +705,11 @@ extern "C" csa2_status csa2_page_copy(csa2_ctx* ctx, void* pool, int64_t n_pages
     const int pairs_b = (int)std::max<int64_t>(1, std::min(fit, n / (4 * std::max(1, ctx->num_sms))));
     const unsigned grid = (unsigned)std::min<int64_t>((n + pairs_b - 1) / pairs_b * chunks, 8ll * std::max(1, ctx->num_sms));
     cudaStream_t s = as_stream(stream);
-    if (wide)
-        page_copy_kernel<uint4><<<grid, PC_THREADS, 0, s>>>(reinterpret_cast<uint4*>(pool), n_pages, pieces, pairs, n, pairs_b, chunks,
-                                                            ctx->status);
-    else
-        page_copy_kernel<uint32_t><<<grid, PC_THREADS, 0, s>>>(reinterpret_cast<uint32_t*>(pool), n_pages, pieces, pairs, n, pairs_b,
-                                                               chunks, ctx->status);
-    return csa2_launch_status();
+    const csa2_status l = wide ? launch_pdl(page_copy_kernel<uint4>, dim3(grid), dim3(PC_THREADS), 0, s, reinterpret_cast<uint4*>(pool),
+                                            n_pages, pieces, pairs, n, pairs_b, chunks, ctx->status)
+                               : launch_pdl(page_copy_kernel<uint32_t>, dim3(grid), dim3(PC_THREADS), 0, s,
+                                            reinterpret_cast<uint32_t*>(pool), n_pages, pieces, pairs, n, pairs_b, chunks, ctx->status);
+    return l != CSA2_OK ? l : csa2_launch_status();
 }
 
 extern "C" csa2_status csa2_page_write(csa2_ctx* ctx, void* pool, int64_t n_pages, int page, int64_t row_bytes,
