@@ -32,6 +32,8 @@ __global__ void __launch_bounds__(TS_MAX_T) tree_plan_kernel(const int32_t* pare
     __shared__ int par[TS_MAX_T];
     const int64_t b = blockIdx.x;
     const int i = threadIdx.x;
+    pdl_wait();
+    pdl_trigger();
     const int64_t len = ctx_len[b];
     if (i < T) {
         int p = parent[b * T + i];
@@ -61,6 +63,8 @@ __global__ void __launch_bounds__(128) tree_commit_kernel(const uint4* draft, co
                                                           int64_t swa_cap, int64_t swa_pos0, int64_t* new_len, unsigned* st) {
     const int64_t b = blockIdx.y;
     const int d = blockIdx.x;
+    pdl_wait();
+    pdl_trigger();
     const int l = leaf[b];
     const int64_t end = l >= 0 && l < T ? pos[b * T + l] : -1;
     if (d == 0 && threadIdx.x == 0) {    // the only reader of ctx_len, which new_len may be
@@ -144,6 +148,8 @@ __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const SimtArgs
     const TreeCall& c = a.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h0 = blockIdx.y * TS_HG;
+    pdl_wait();
+    pdl_trigger();
     const TreeNode n = tree_node(c.r, blockIdx.z);
     if (threadIdx.x < 32) ag_cos_sin(c.rope, n.t, lane, s.cs[lane], s.sn[lane]);
     if (threadIdx.x < TS_HG) {
@@ -312,6 +318,8 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const SimtArgs a, int
     __shared__ float cs[8][32], sn[8][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r = (int64_t)blockIdx.x * 8 + warp;
+    pdl_wait();
+    pdl_trigger();
     if (r >= rows) return;
     const bool rope = a.c.flags & CSA2_ROPE;
     if (rope) ag_cos_sin(a.c.rope, a.c.r.pos[r / a.c.H], lane, cs[warp][lane], sn[warp][lane]);
@@ -342,14 +350,15 @@ csa2_status launch_simt(const SimtArgs& a, cudaStream_t s) {
     auto kern = tree_simt_kernel<KVK>;
     CSA2_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SimtSmem)));
     const int64_t n_bt = (int64_t)a.c.B * a.c.r.T;
-    kern<<<dim3((unsigned)a.n_split, (unsigned)((a.c.H + TS_HG - 1) / TS_HG), (unsigned)n_bt), TS_THREADS, sizeof(SimtSmem), s>>>(a);
-    if (a.n_split > 1) {
+    csa2_status r = launch_pdl(kern, dim3((unsigned)a.n_split, (unsigned)((a.c.H + TS_HG - 1) / TS_HG), (unsigned)n_bt), dim3(TS_THREADS),
+                               sizeof(SimtSmem), s, a);
+    if (r == CSA2_OK && a.n_split > 1) {
         const int64_t rows = n_bt * a.c.H;
-        const unsigned grid = (unsigned)((rows + 7) / 8);
-        if (a.c.out_dt == CSA2_F32) tree_combine_kernel<float><<<grid, 256, 0, s>>>(a, rows);
-        else tree_combine_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a, rows);
+        const dim3 grid((unsigned)((rows + 7) / 8));
+        r = a.c.out_dt == CSA2_F32 ? launch_pdl(tree_combine_kernel<float>, grid, dim3(256), 0, s, a, rows)
+                                   : launch_pdl(tree_combine_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, a, rows);
     }
-    return csa2_launch_status();
+    return r != CSA2_OK ? r : csa2_launch_status();
 }
 
 }  // namespace
@@ -363,9 +372,9 @@ extern "C" csa2_status csa2_tree_plan(csa2_ctx* ctx, const int32_t* parent, cons
         return CSA2_ERR_INVALID_ARG;
     DeviceGuard dev(ctx);
     if (!dev.ok) return CSA2_ERR_CUDA;
-    tree_plan_kernel<<<(unsigned)B, (unsigned)((T + 31) / 32 * 32), 0, as_stream(stream)>>>(parent, ctx_len, T, pos, path,
-                                                                                           ctx->status);
-    return csa2_launch_status();
+    const csa2_status l = launch_pdl(tree_plan_kernel, dim3((unsigned)B), dim3((unsigned)((T + 31) / 32 * 32)), 0, as_stream(stream), parent,
+                                     ctx_len, T, pos, path, ctx->status);
+    return l != CSA2_OK ? l : csa2_launch_status();
 }
 
 extern "C" csa2_status csa2_tree_commit(csa2_ctx* ctx, const void* draft, csa2_dtype dt, const int64_t* pos,
@@ -380,10 +389,11 @@ extern "C" csa2_status csa2_tree_commit(csa2_ctx* ctx, const void* draft, csa2_d
         return CSA2_ERR_INVALID_ARG;
     DeviceGuard dev(ctx);
     if (!dev.ok) return CSA2_ERR_CUDA;
-    tree_commit_kernel<<<dim3((unsigned)T, (unsigned)B), 128, 0, as_stream(stream)>>>(
-        reinterpret_cast<const uint4*>(draft), pos, path, ctx_len, leaf, T, c * (dt == CSA2_F32 ? 4 : 2) / 16,
-        reinterpret_cast<uint4*>(swa), swa_cap, swa_pos0, new_len, ctx->status);
-    return csa2_launch_status();
+    const csa2_status l = launch_pdl(tree_commit_kernel, dim3((unsigned)T, (unsigned)B), dim3(128), 0, as_stream(stream),
+                                     reinterpret_cast<const uint4*>(draft), pos, path, ctx_len, leaf, T,
+                                     c * (dt == CSA2_F32 ? 4 : 2) / 16, reinterpret_cast<uint4*>(swa), swa_cap, swa_pos0, new_len,
+                                     ctx->status);
+    return l != CSA2_OK ? l : csa2_launch_status();
 }
 
 extern "C" size_t csa2_tree_attn_workspace_bytes(csa2_ctx* ctx, csa2_dtype q_dt, csa2_dtype kv_dt, csa2_dtype swa_dt, int B,
