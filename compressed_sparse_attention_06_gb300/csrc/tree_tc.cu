@@ -394,7 +394,9 @@ __device__ __forceinline__ float row_factors(const uint8_t* base, int64_t bytes,
     return sum < INFINITY ? (LOG2E / sqrtf((float)TT_C)) / sqrtf(sum / (float)TT_C + 1e-6f) : __int_as_float(0x7FC00000);
 }
 
-// A warp: a query row; 32 entry slots of a node (dense: of a sequence); 32 slots of a group's window; 8 rows
+constexpr int TT_QROWS = 4;                      // query rows of a warp (images have multiples of 8)
+
+// A warp: a few query rows; 32 entry slots of a node (dense: of a sequence); 32 slots of a group's window; 8 rows
 // of a ring; or 8 drafts.
 __global__ void __launch_bounds__(256) tree_prep_kernel(const PrepArgs a) {
     pdl_wait();
@@ -506,58 +508,73 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const PrepArgs a) {
     }
     w -= a.d_warps;
     if (w >= a.q_warps) return;
-    const int v = (int)(w / a.l.R8), b = v / a.l.gps, n0 = (v - b * a.l.gps) * a.l.G, gv = min(a.l.G, T - n0);
+    // query rows: all of a warp's are loaded before the first is used; the angles are a node's
+    const int per = a.l.R8 / TT_QROWS, v = (int)(w / per), b = v / a.l.gps, n0 = (v - b * a.l.gps) * a.l.G, gv = min(a.l.G, T - n0);
     const int64_t bt0 = (int64_t)b * T + n0;
-    const int row = (int)(w - (int64_t)v * a.l.R8), g = row / a.l.H, h = row - g * a.l.H;
-    float x[16];
+    const int row0 = (int)(w - (int64_t)v * per) * TT_QROWS;
+    uint4 u[TT_QROWS][2];
+    float ss[TT_QROWS];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = 0.0f;
-    if (g < gv) {
-        const int64_t pos = a.r.pos[bt0 + g];
-        const uint4* p = reinterpret_cast<const uint4*>(a.q + ((bt0 + g) * a.l.H + h) * (int64_t)TT_C + 16 * lane);
-        float ss = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint4 u = p[i];
-            const uint32_t c[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[8 * i + 2 * j] = __uint_as_float(c[j] << 16);
-                x[8 * i + 2 * j + 1] = __uint_as_float(c[j] & 0xFFFF0000u);
-            }
+    for (int k = 0; k < TT_QROWS; ++k) {
+        u[k][0] = u[k][1] = make_uint4(0u, 0u, 0u, 0u);
+        if (row0 + k < gv * a.l.H) {
+            const uint4* p = reinterpret_cast<const uint4*>(a.q + (bt0 * a.l.H + row0 + k) * (int64_t)TT_C + 16 * lane);
+            u[k][0] = p[0];
+            u[k][1] = p[1];
         }
+    }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-        const float r = 1.0f / sqrtf(warp_sum(ss) / (float)TT_C + 1e-6f);
+    for (int k = 0; k < TT_QROWS; ++k) ss[k] = lane_squares(u[k][0], u[k][1]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] *= r;
-        if (a.flags & CSA2_ROPE) {
-            // lane j has angle j; lanes 28 .. 31 rotate the pairs of dims 448 .. 511
-            float c, s;
-            ag_cos_sin(a.rope, pos, lane, c, s);
-            if (h == 0) {
-                a.l.rope_cs[(bt0 + g) * 64 + lane] = c;
-                a.l.rope_cs[(bt0 + g) * 64 + 32 + lane] = s;
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < TT_QROWS; ++k) ss[k] += __shfl_xor_sync(FULL, ss[k], o);
+    int at = -1;                             // the node of the angles
+    float cj[8], sj[8];
+#pragma unroll
+    for (int k = 0; k < TT_QROWS; ++k) {
+        const int row = row0 + k, g = row / a.l.H;
+        const float r = 1.0f / sqrtf(ss[k] / (float)TT_C + 1e-6f);
+        const uint32_t c8[8] = {u[k][0].x, u[k][0].y, u[k][0].z, u[k][0].w, u[k][1].x, u[k][1].y, u[k][1].z, u[k][1].w};
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[2 * i] = __uint_as_float(c8[i] << 16) * r;
+            x[2 * i + 1] = __uint_as_float(c8[i] & 0xFFFF0000u) * r;
+        }
+        if ((a.flags & CSA2_ROPE) && g < gv) {
+            if (g != at) {
+                // lane j has angle j; lanes 28 .. 31 rotate the pairs of dims 448 .. 511
+                float c, s;
+                ag_cos_sin(a.rope, a.r.pos[bt0 + g], lane, c, s);
+                if (row == g * a.l.H) {
+                    a.l.rope_cs[(bt0 + g) * 64 + lane] = c;
+                    a.l.rope_cs[(bt0 + g) * 64 + 32 + lane] = s;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    cj[i] = __shfl_sync(FULL, c, (8 * (lane - 28) + i) & 31);
+                    sj[i] = __shfl_sync(FULL, s, (8 * (lane - 28) + i) & 31);
+                }
+                at = g;
             }
+            if (lane >= 28) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int j = (8 * (lane - 28) + i) & 31;
-                const float cj = __shfl_sync(FULL, c, j), sj = __shfl_sync(FULL, s, j);
-                if (lane >= 28) {
+                for (int i = 0; i < 8; ++i) {
                     const float x0 = x[2 * i], x1 = x[2 * i + 1];
-                    x[2 * i] = x0 * cj - x1 * sj;
-                    x[2 * i + 1] = x1 * cj + x0 * sj;
+                    x[2 * i] = x0 * cj[i] - x1 * sj[i];
+                    x[2 * i + 1] = x1 * cj[i] + x0 * sj[i];
                 }
             }
         }
-    }
-    uint32_t o[8];
+        uint32_t o[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-    uint8_t* img = a.l.qimg + v * (int64_t)a.l.R8 * 1024 + (lane >> 2) * (int64_t)a.l.R8 * 128;      // chunk of 64 dims
-    const uint32_t u = 2 * (lane & 3);
-    *reinterpret_cast<uint4*>(img + sw128_offset(row, u)) = make_uint4(o[0], o[1], o[2], o[3]);
-    *reinterpret_cast<uint4*>(img + sw128_offset(row, u + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+        for (int i = 0; i < 8; ++i) o[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+        uint8_t* img = a.l.qimg + v * (int64_t)a.l.R8 * 1024 + (lane >> 2) * (int64_t)a.l.R8 * 128;      // chunk of 64 dims
+        const uint32_t un = 2 * (lane & 3);
+        *reinterpret_cast<uint4*>(img + sw128_offset(row, un)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(img + sw128_offset(row, un + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+    }
 }
 
 // ---------------------------------------------------------------- the main kernel
@@ -1326,7 +1343,7 @@ csa2_status tree_tc_run(csa2_ctx* ctx, const TreeCall& c, void* ws, cudaStream_t
     pa.w_warps = p.groups * pa.ww;
     pa.r_warps = (int64_t)c.B * pa.rw;
     pa.d_warps = c.r.window > 0 ? (pa.l.drafts + 7) / 8 : 0;
-    pa.q_warps = p.groups * p.R8;
+    pa.q_warps = p.groups * (p.R8 / TT_QROWS);
     pa.rope = c.rope;
     pa.flags = c.flags;
     pa.st = ctx->status;
