@@ -6,8 +6,10 @@
 // out of step: a call that needs free pages finds the lowest ones by a pass over refs.  That pass
 // and what follows from it are one thread-block cluster of 8 CTAs whose phases meet at cluster
 // barriers (a launch of its own per phase would cost more than the phase for any pool that fits a
-// GPU), or one CTA where the state is small; the ranks come from counts in order of (sequence, page) and of page id, so results do not
-// depend on timing.  Moving the bytes is bound by device memory.
+// GPU), or one CTA where the state is small; the ranks come from counts in order of (sequence, page)
+// and of page id, so results do not depend on timing.  A call is short, and a step makes several: each
+// kernel's launch overlaps the end of the one before (64 continuations of 8 prompts, 8 kernels: 101 us,
+// 110 without).
 #include <algorithm>
 
 #include "attn_grad.cuh"
@@ -405,7 +407,8 @@ constexpr int PC_THREADS = 256, PC_PIECES = 8;
 
 // Whole pages in pieces of V: a block takes pairs_b pairs (pages of fewer than PC_BLOCK pieces) or PC_BLOCK
 // pieces of one, eight in flight a thread.  The pairs that move nothing are the last ones of a compaction
-// and cost their lookup.
+// and cost their lookup.  Bound by device memory: 10,000 of 40,000 pages of 18 KB moved in 59 us, 6.3 TB/s
+// read and written.
 constexpr int PC_BLOCK = 4 * PC_THREADS * PC_PIECES, PC_PAIRS = 512;
 
 template <typename V>
@@ -468,7 +471,8 @@ struct RowsArgs {
 
 // Rows between a dense block [B, n, row] and the pages, in pieces of V: a block takes rows_b rows,
 // looks their places up into shared memory, then each thread has eight pieces in flight, adjacent
-// threads adjacent pieces.
+// threads adjacent pieces.  Bound by device memory: 32 x 4,001 rows of 1 KB read 32 us, 8.2 TB/s (a part
+// of them is in L2).
 template <typename V, bool WRITE>
 __global__ void __launch_bounds__(PC_THREADS) page_rows_kernel(V* pool, V* dense, const RowsArgs a) {
     __shared__ int64_t at[PC_THREADS * PC_PIECES];   // first piece of the row in the pool, -1 = none

@@ -9,29 +9,42 @@
 //   S[128 rows x 128 slots]  = Q^[128 x 256] . X[128 x 256]^T     this CTA's half of the logits
 //   O[128 rows x 256 dims]  += P'[128 x 128] . X[128 x 256]       P' = p f, read from tensor memory
 // f = RMS factor of the slot's row / (sqrt(512) ln 2): it scales the logits (to base 2) and, folded
-// into P', makes a row's value its normalised form, so X is never rescaled.  The CTAs exchange their
-// scaled halves through distributed shared memory, rounded to fp16 (2^-12 of a half logit; q^'s own
-// rounding to bf16 moves a logit by ten times that); a CTA adds the peer's half to its own fp32 one.
-// Both norms bound a logit by sqrt(512), 32.7 in base 2: p = 2^z needs no running maximum (sums of
-// 4 million of them stay below 2^55), and the splits of a group's slots simply add up.
+// into P', makes a row's value its normalised form, so X is never rescaled.  Both norms bound a logit
+// by sqrt(512), 32.7 in base 2: p = 2^z needs no running maximum (sums of 4 million of them stay below
+// 2^55), and the splits of a group's slots simply add up.
+//
+// Each CTA weighs half of a tile's slots for both: it gets the peer's half logits of its 64 slots,
+// rounded to fp16 (2^-12 of a half logit; q^'s own rounding to bf16 moves a logit by ten times that),
+// adds them to its own fp32 ones and sends P' (bf16) back, 16 KB each way.  (With whole tiles of
+// logits exchanged and every exponential taken by both, 64 nodes over 4,096 entries took 184 us
+// instead of 174.)  The peer's P' go from shared to tensor memory by the tensor core's own copies, in
+// order with the products.
 //
 // tree_prep_kernel runs first: q^ (normalised, rotated) as the swizzled image of the A operand, the
 // RoPE table, and for every slot its row (-1: none), f (the window's rows: once for all nodes), and as
 // bits which nodes attend to it.  (A row's squares need all of its dims, of which a CTA has half: with
 // the sums exchanged like the logits, and the rows through registers for them, the loaders were what a
-// tile waited for.)
+// tile waited for.)  It reads every slot's row once, at 7.7 TB/s out of L2 (8 x 24 nodes of 1,024
+// entries: 26 us).
 //
-// Warps (640 threads, one CTA an SM):
+// Warps (768 threads, one CTA an SM):
 //   0       query images (bulk copies)
-//   1       issues the MMAs; owns tensor memory (O: columns 0-255, S / P': two buffers of 128)
+//   1       half logits; owns tensor memory (O: columns 0-255, S / P': two buffers of 128)
 //   2       the tiles' masks and factors
-//   4-11    softmax, two warps a lane quarter (64 slots each)
+//   3       products.  (Both kinds of MMA from one thread: its time to issue them, 3.4K cycles a tile, was
+//           what a tile took; 174 us instead of 159.)
+//   4-11    softmax, two warps a lane quarter (32 of the CTA's 64 slots each)
 //   12-19   loaders, 16 rows of a tile each: bf16 rows that follow one another by tensor copies, others
 //           by 16-byte asynchronous copies into the swizzled tile, FP4 rows dequantised (exactly) from
-//           registers that are filled a tile ahead.  They also store the output, a row a thread: while an
-//           item's last output is read no buffer is free to be filled, and the softmax is with the next
-//           item's tiles already.
+//           registers that are filled a tile ahead
+//   20-23   outputs, a row a thread.  (By the loaders: 8 x 32 nodes over FP4 pages 104 us, not 97.)
 // Every wait is bounded; the CTAs meet at the cluster's barrier before either one exits.
+//
+// Two tiles are in flight (they fill shared memory, their logits tensor memory): each is loaded (1.0-1.3K
+// cycles; FP4 2.4K), multiplied (1.5K), weighed (2.2K), multiplied again (1.4K) before the next but one is,
+// so that a tile takes 3.6K cycles where its MMAs take 2.2K and its shared-memory traffic 2.6K.  Tiles of 64
+// slots, four in flight, were slower (216 us where 128 took 184: a half logit's MMA of N = 64 reads as much
+// of Q^), as were 4 or 16 loader warps (at 16 the registers of a thread no longer hold the softmax).
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -62,8 +75,8 @@ constexpr int OFF_Q = 0;
 constexpr int OFF_Y = 65536;                             // the peer's P': [2 groups][4 units of 8 slots][128 rows] x 16 B
 constexpr int OFF_X = OFF_Y + 16384;                     // its half logits, the same
 constexpr int OFF_K = OFF_X + 16384;
-constexpr int OFF_F = OFF_K + 2 * TT_TILE_BYTES;                     // [2][128] the factors f
-constexpr int OFF_L = OFF_F + 1024;                      // [2][128] sums of exponentials
+constexpr int OFF_F = OFF_K + 2 * TT_TILE_BYTES;         // [2][128] the factors f
+constexpr int OFF_L = OFF_F + 1024;                      // [2][128] sums of exponentials, by softmax warp of a lane quarter
 constexpr int OFF_MASK = OFF_L + 1024;                   // [2][TT_G][4] x 32 bits
 constexpr int OFF_BAR = OFF_MASK + 2 * TT_G * 16;
 constexpr int N_BAR = 18 + 8 + 2 * 8;

@@ -81,8 +81,8 @@ csa2_status csa2_ctx_destroy(csa2_ctx* ctx);
 csa2_status csa2_ctx_check(csa2_ctx* ctx, void* stream);
 
 /* Failure-detection test hook.  The next tensor-core launch on this context (an
-   indexer scan, or the tensor-core kernel of the attention, its backward pass or its
-   weights) runs with a producer that never signals its consumers (the scan's key
+   indexer scan, or the tensor-core kernel of the attention, its backward pass, its
+   weights or drafted trees) runs with a producer that never signals its consumers (the scan's key
    copies, the attention's query images), whose bounded waits then expire after `budget_cycles` (0 = the default
    of 2^31 cycles) and record CSA2_ERR_TIMEOUT; the kernel waits for the copies it
    did issue, frees its tensor memory and exits, and the context stays usable.  The
@@ -670,7 +670,8 @@ csa2_status csa2_cache_gather(csa2_ctx* ctx, const void* src, int64_t row_bytes,
  * c == 512, 1 <= H <= 128, k <= 2048 (dense: 4,194,304), window <= 1024, T <= 256, B*T <= 65535;
  * the rows of kv and of swa number below 2^31.
  * BF16 query, window and drafts over BF16 or FP4 rows with both norms run on the tensor cores
- * (q^ and p rounded to bf16, sums fp32), all other calls in fp32.
+ * (q^ and p rounded to bf16, half of a logit to fp16, sums fp32), all other calls in fp32.
+ * A row that holds a NaN or an infinity makes out and lse of the nodes that attend to it NaN, no others'.
  * Workspace: csa2_tree_attn_workspace_bytes() bytes, 16-byte aligned; with fewer the call
  * returns CSA2_ERR_INVALID_ARG.  Calls that share a workspace must not overlap on the GPU.
  *
