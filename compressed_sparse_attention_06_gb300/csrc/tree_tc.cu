@@ -1186,7 +1186,7 @@ struct MergeArgs {
 };
 
 // The pieces of one query row, a warp each: outputs and sums add up.
-__global__ void __launch_bounds__(256) tree_merge_kernel(const MergeArgs a) {
+__global__ void __launch_bounds__(256, 4) tree_merge_kernel(const MergeArgs a) {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, rows = a.G * a.H;
@@ -1201,11 +1201,11 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeArgs a) {
     float acc[16], L = 0.0f;
 #pragma unroll
     for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
-    for (int s0 = 0; s0 < n; s0 += 4) {
-        float l[4];
-        float4 x[4][4];
+    for (int s0 = 0; s0 < n; s0 += 2) {
+        float l[2];
+        float4 x[2][4];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
+        for (int s = 0; s < 2; ++s) {
             const int64_t p = (o * a.pieces + s0 + s) * rows + r;
             l[s] = s0 + s < n ? a.part_l[p] : 0.0f;
             // (a piece without slots has left its output as it was)
@@ -1214,7 +1214,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeArgs a) {
             for (int j = 0; j < 4; ++j) x[s][j] = s0 + s < n ? __ldcs(x0 + 32 * j) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
+        for (int s = 0; s < 2; ++s) {
             L += l[s];
             if (l[s] == 0.0f) continue;
 #pragma unroll
