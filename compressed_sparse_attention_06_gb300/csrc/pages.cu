@@ -307,7 +307,19 @@ struct CompactArgs {
     int64_t* n_used;
     int32_t* to;                         // [n_pages] where a page at or behind the used ones goes
     int64_t* cut;                        // the number of used pages, for the tables' kernel
+    int32_t* table;                      // the tables, where this kernel sees to them (else NULL)
+    int64_t entries;
+    unsigned* st;
 };
+
+// A table's entry after the moves.
+__device__ __forceinline__ void remap(int32_t* entry, int64_t n_pages, int64_t cut, const int32_t* to, unsigned* st) {
+    const int32_t t = *entry;
+    if (t >= -1 && t < cut) return;
+    const int32_t d = t >= 0 && t < n_pages ? __ldcg(to + t) : -2;
+    if (d >= 0) *entry = d;
+    else csa2_flag(st, CSA2_DEVBIT_RANGE);           // a page that is none, or one without uses
+}
 
 __global__ void __launch_bounds__(PG_THREADS) pages_compact_kernel(const CompactArgs a) {
     __shared__ uint32_t tmp[PG_WARPS + 1], used[PG_CTAS], from[PG_CTAS], into[PG_CTAS];
@@ -387,6 +399,10 @@ __global__ void __launch_bounds__(PG_THREADS) pages_compact_kernel(const Compact
         *a.cut = cut;
         if (a.n_used) *a.n_used = cut;
     }
+    if (!a.table) return;
+    __threadfence();
+    cluster_sync();                      // every page's way is written
+    for (int64_t i = (int64_t)rank * PG_THREADS + threadIdx.x; i < a.entries; i += step) remap(a.table + i, a.n_pages, cut, a.to, a.st);
 }
 
 __global__ void __launch_bounds__(256) pages_remap_kernel(int32_t* table, int64_t total, int64_t n_pages, const int32_t* to,
@@ -394,13 +410,8 @@ __global__ void __launch_bounds__(256) pages_remap_kernel(int32_t* table, int64_
     pdl_wait();
     pdl_trigger();
     const int64_t cut = *cut_p;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int32_t t = table[i];
-        if (t >= -1 && t < cut) continue;
-        const int32_t d = t >= 0 && t < n_pages ? to[t] : -2;
-        if (d >= 0) table[i] = d;
-        else csa2_flag(st, CSA2_DEVBIT_RANGE);       // a page that is none, or one without uses
-    }
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x)
+        remap(table + i, n_pages, cut, to, st);
 }
 
 constexpr int PC_THREADS = 256, PC_PIECES = 8;
@@ -682,13 +693,15 @@ extern "C" csa2_status csa2_pages_compact(csa2_ctx* ctx, int32_t* refs, int64_t 
     cudaStream_t s = as_stream(stream);
     int64_t* cut = reinterpret_cast<int64_t*>(ws);
     int32_t* to = reinterpret_cast<int32_t*>(ws) + 4;
-    const CompactArgs a = {refs, n_pages, moves, n_used, to, cut};
+    const int64_t total = (int64_t)B * max_pages;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute at[2];
     cluster_config(cfg, at, n_pages, 0, 0, s);
+    // a small table is seen to by the same kernel (a launch less: 300 pages and two pools 47 us a step, not 51)
+    const bool inside = total <= 4ll * cfg.gridDim.x * PG_THREADS;
+    const CompactArgs a = {refs, n_pages, moves, n_used, to, cut, inside ? table : nullptr, total, ctx->status};
     if (cudaLaunchKernelEx(&cfg, pages_compact_kernel, a) != cudaSuccess) return CSA2_ERR_CUDA;
-    const int64_t total = (int64_t)B * max_pages;
-    if (total == 0) return csa2_launch_status();
+    if (inside) return csa2_launch_status();
     const csa2_status l = launch_pdl(pages_remap_kernel, dim3(flat_grid(ctx, total)), dim3(256), 0, s, table, total, n_pages,
                                      (const int32_t*)to, (const int64_t*)cut, ctx->status);
     return l != CSA2_OK ? l : csa2_launch_status();
