@@ -407,7 +407,7 @@ __device__ __forceinline__ float row_factors(const uint8_t* base, int64_t bytes,
     return sum < INFINITY ? (LOG2E / sqrtf((float)TT_C)) / sqrtf(sum / (float)TT_C + 1e-6f) : __int_as_float(0x7FC00000);
 }
 
-constexpr int TT_QROWS = 4;                      // query rows of a warp (images have multiples of 8)
+constexpr int TT_QROWS = 2;                      // query rows of a warp (images have multiples of 8)
 
 // A warp: a few query rows; 32 entry slots of a node (dense: of a sequence); 32 slots of a group's window; 8 rows
 // of a ring; or 8 drafts.
