@@ -217,26 +217,17 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return r;
 }
 
-// Lanes 2 i and 2 i + 1 turn their 2 x 2 pieces: lane l's piece k becomes piece l & 1 of lane (l & ~1) + k;
-// four lanes their 4 x 4: piece l & 3 of lane (l & ~3) + k.  (A store of 16 bytes a row and lane would take
-// the time of 32 lines: 8,000 cycles for the output of 128 rows.)
-__device__ __forceinline__ void turn(uint4& p0, uint4& p1, int o) {
-    const bool upper = (threadIdx.x & o) != 0;
-    const uint4 send = upper ? p0 : p1;
-    uint4 got;
-    got.x = __shfl_xor_sync(FULL, send.x, o);
-    got.y = __shfl_xor_sync(FULL, send.y, o);
-    got.z = __shfl_xor_sync(FULL, send.z, o);
-    got.w = __shfl_xor_sync(FULL, send.w, o);
-    if (upper) p0 = got;
-    else p1 = got;
-}
-__device__ __forceinline__ void turn2(uint4 (&p)[2]) { turn(p[0], p[1], 1); }
-__device__ __forceinline__ void turn4(uint4 (&p)[4]) {
-    turn(p[0], p[1], 1);
-    turn(p[2], p[3], 1);
-    turn(p[0], p[2], 2);
-    turn(p[1], p[3], 2);
+// 32 bytes to global memory: one access, so that a thread with a row of its own writes whole sectors, or two
+// where the address is a multiple of 16 only.
+__device__ __forceinline__ void store_sector(void* p, const uint32_t (&w)[8], bool whole) {
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                     "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
 }
 
 // A cluster's items: `rounds` whole groups, then its share of the groups that are left over: their tiles
@@ -1088,73 +1079,67 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
     } else if (warp >= 12 + TT_LOADERS) {
         // ============================ outputs ============================
         const int quad = warp & 3, r = quad * 32 + lane, hq = r / a.l.H, h = r - hq * a.l.H;
-        const bool live = quad * 32 < a.l.G * a.l.H, first_part = rank == 0;
+        const bool live = quad * 32 < a.l.G * a.l.H;
         const int d0 = TT_HALF * rank;
         const uint32_t o_col = tmem + ((uint32_t)(quad * 32) << 16);
         int oq = 0;
+        const float zs = a.sink && live ? a.sink[h] : -INFINITY;
+        const bool sectors = ((uintptr_t)a.out & 31u) == 0;
         while (walk.next(a, it)) {
-            const bool valid = r < it.gv * a.l.H;
+            const bool valid = r < it.gv * a.l.H, part = it.pieces > 1;
             const int64_t bt = (int64_t)it.b * a.r.T + it.n0 + (valid ? hq : 0), orow = bt * a.l.H + h;
-            const bool part = it.pieces > 1;
             const int64_t prow = part ? (int64_t)(it.part + it.piece) * (a.l.G * a.l.H) + r : 0;
-            const bool wt = mbar_wait(lred, oq & 1, a.budget, a.st) && mbar_wait(ofull, oq & 1, a.budget, a.st);
+            // (the sums are there before the last products)
+            bool wt = mbar_wait(lred, oq & 1, a.budget, a.st);
             if (!__all_sync(FULL, wt)) break;
-            tc_fence_after();
             const float L = sL[r] + sL[TT_ROWS + r];
-            const float2 fin = part ? make_float2(1.0f, 0.0f) : finish_row(L, a.sink && valid ? a.sink[h] : -INFINITY);
-            if (valid && first_part) {
+            const float2 fin = part ? make_float2(1.0f, 0.0f) : finish_row(L, zs);
+            if (valid && rank == 0) {
                 if (part) a.part_l[prow] = L;
                 else if (a.lse) a.lse[orow] = fin.y;
             }
+            wt = mbar_wait(ofull, oq & 1, a.budget, a.st);
+            if (!__all_sync(FULL, wt)) break;
+            tc_fence_after();
             // (a piece without slots is left out of the sums)
             if (live && !(part && it.t0 * TT_TILE >= it.slots)) {
                 const float* cs = a.l.rope_cs + bt * 64;
-                const bool wide = part || a.out_f32;          // fp32 rows
-                // rows quad * 32 + (lane & ~3) + k, k < 4, of the group; 16 bytes a lane, four lanes side by side
-                const int r4 = quad * 32 + (lane & ~3), n4 = min(4, it.gv * a.l.H - r4);
-                uint8_t* dst = part ? reinterpret_cast<uint8_t*>(a.part_o + (prow - r + r4) * (int64_t)TT_C)
-                                    : reinterpret_cast<uint8_t*>(a.out) + (((int64_t)it.b * a.r.T + it.n0) * a.l.H + r4) * (int64_t)(wide ? TT_C * 4 : TT_C * 2);
-                const int64_t pitch = wide ? TT_C * 4 : TT_C * 2;
+                const bool wide = part || a.out_f32, whole = part || sectors;        // fp32 rows; whole sectors
+                uint8_t* dst = part ? reinterpret_cast<uint8_t*>(a.part_o + prow * (int64_t)TT_C)
+                                    : reinterpret_cast<uint8_t*>(a.out) + orow * (int64_t)(wide ? TT_C * 4 : TT_C * 2);
 #pragma unroll 1
-                for (int db = 0; db < TT_HALF / 16; ++db) {
-                    const int d = d0 + 16 * db;
-                    float v[16];
-                    uint32_t o[16];
-                    tmem_ld16(o_col + 16 * db, o);
+                for (int db = 0; db < TT_HALF / 32; ++db) {
+                    const int d = d0 + 32 * db;
+                    uint32_t o[32];
+                    tmem_ld32(o_col + 32 * db, o);
                     tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(o[i]) * fin.x;
                     if (!part && (a.flags & CSA2_ROPE) && d >= TT_C - 64) {
                         const float* c = cs + (d - (TT_C - 64)) / 2;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float x0 = v[2 * j], x1 = v[2 * j + 1];
-                            v[2 * j] = x0 * c[j] + x1 * c[32 + j];
-                            v[2 * j + 1] = x1 * c[j] - x0 * c[32 + j];
+                        for (int j = 0; j < 16; ++j) {
+                            const float x0 = __uint_as_float(o[2 * j]), x1 = __uint_as_float(o[2 * j + 1]);
+                            o[2 * j] = __float_as_uint(x0 * c[j] + x1 * c[32 + j]);
+                            o[2 * j + 1] = __float_as_uint(x1 * c[j] - x0 * c[32 + j]);
                         }
                     }
+                    const auto v = [&](int i) { return __uint_as_float(o[i]) * fin.x; };
+                    if (!valid) continue;
                     if (wide) {
-                        uint4 p[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            p[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
-                                              __float_as_uint(v[4 * i + 3]));
-                        turn4(p);
+                        for (int k = 0; k < 32; k += 8) {
+                            uint32_t w[8];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (k < n4) *reinterpret_cast<uint4*>(dst + k * pitch + d * 4 + 16 * (lane & 3)) = p[k];
+                            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v(k + i));
+                            store_sector(dst + (d + k) * 4, w, whole);
+                        }
                     } else {
-                        uint4 p[2];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            p[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                                              pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
-                        turn2(p);
-                        // lane pairs hold rows (lane & ~1) and the next one, 32 bytes side by side
-                        const int r2 = lane & 2;
+                        for (int k = 0; k < 32; k += 16) {
+                            uint32_t w[8];
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            if (r2 + k < n4) *reinterpret_cast<uint4*>(dst + (r2 + k) * pitch + d * 2 + 16 * (lane & 1)) = p[k];
+                            for (int i = 0; i < 8; ++i) w[i] = pack_bf16(v(k + 2 * i), v(k + 2 * i + 1));
+                            store_sector(dst + (d + k) * 2, w, whole);
+                        }
                     }
                 }
             }

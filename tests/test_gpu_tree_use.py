@@ -108,6 +108,21 @@ def test_nothing_but_rows_without_numbers(kind, dt, k):
         assert bool(torch.isnan(out.float()).all()) and bool(torch.isnan(lse).all())
 
 
+@pytest.mark.parametrize("kind,dense", [("bf16", True), ("fp4", False)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_outputs_off_a_sector(kind, dense, dt):
+    """An output that starts 16 bytes behind a multiple of 32 gets the same values."""
+    c = Case(98, 2, 11, 24, 700, 0 if dense else 300, kind, page=16, dense=dense)
+    want, _ = c.run(out_dtype=dt)
+    n, off = want.numel(), 16 // want.element_size()
+    buf = torch.full((n + 4 * off,), 7.0, dtype=dt, device=DEV)
+    out = buf[off:off + n].view(want.shape)
+    assert out.data_ptr() % 32 == 16
+    c.run(out=out)
+    C.csa2_ctx_check()
+    assert torch.equal(out, want) and bool((buf[:off] == 7).all()) and bool((buf[off + n:] == 7).all())
+
+
 def test_captured_and_replayed():
     """Two graphs captured over one workspace, replayed in turn with other inputs, lengths and trees."""
     cases = [Case(94 + i, 2, 9, 32, 700, 300, "bf16", page=64, lens=[10, 999]) for i in range(4)]
