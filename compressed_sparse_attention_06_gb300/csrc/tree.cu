@@ -11,7 +11,7 @@
 // The softmax is online over chunks of 32 rows; few nodes split their rows over several CTAs,
 // joined by log-sum-exp.  Measured: 2 x 13 nodes of 16 heads, 301 entries and a window of 100 each, 29 us of
 // which 3.4 are their multiply-adds; bf16 and FP4 rows take 14 to 50 times as long here as on the tensor
-// cores (8 x 32 nodes of 64 heads over FP4 pages: 1,414 us, there 90).
+// cores (8 x 32 nodes of 64 heads over FP4 pages: 1,414 us, there 89).
 #include <algorithm>
 
 #include "csa2_internal.cuh"

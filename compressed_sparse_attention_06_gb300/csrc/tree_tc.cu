@@ -14,14 +14,14 @@
 // 2^55), and the splits of a group's slots simply add up.
 //
 // Each CTA weighs half of a tile's slots for both: it gets the peer's half logits of its 64 slots,
-// rounded to fp16 (2^-12 of a half logit; q^'s own rounding to bf16 moves a logit by ten times that),
-// adds them to its own fp32 ones and sends P' (bf16) back, 16 KB each way.  (With whole tiles of
+// rounded to fp16 (2^-12 of a half logit; the rounding of q^'s rotated dims to bf16 moves a logit by
+// several times that), adds them to its own fp32 ones and sends P' (bf16) back, 16 KB each way.  (With whole tiles of
 // logits exchanged and every exponential taken by both, 64 nodes over 4,096 entries took 184 us
 // instead of 174.)  The peer's P' go from shared to tensor memory by the tensor core's own copies, in
 // order with the products.
 //
-// tree_prep_kernel runs first: q^ (normalised, rotated) as the swizzled image of the A operand, the
-// RoPE table, and for every slot its row (-1: none), f (the window's rows: once for all nodes), and as
+// tree_prep_kernel runs first: q^ (rotated, its RMS factor but for a power of two left to the logits) as
+// the swizzled image of the A operand, the RoPE table, and for every slot its row (-1: none), f (the window's rows: once for all nodes), and as
 // bits which nodes attend to it.  (A row's squares need all of its dims, of which a CTA has half: with
 // the sums exchanged like the logits, and the rows through registers for them, the loaders were what a
 // tile waited for.)  It reads every slot's row once, at 7.7 TB/s out of L2 (8 x 24 nodes of 1,024
@@ -87,6 +87,7 @@ static_assert(TT_SMEM <= 227 * 1024, "shared memory");
 // What the prep kernel leaves for the main one.
 struct TtLists {
     uint8_t* qimg;                // [groups][2 halves][4 chunks][R8 rows x 128 B]
+    float* qm;                    // [groups][R8] what the image's rows are yet to be multiplied by, in [1, 2)
     int32_t* erow;                // [eg][lde] rows of the entry slots (eg: nodes; dense: sequences)
     float* ef;                    // [eg][lde] their factors f
     uint32_t* eok;                // [eg][lde / 32] which of them there are
@@ -538,7 +539,10 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const PrepArgs a) {
 #pragma unroll
     for (int k = 0; k < TT_QROWS; ++k) {
         const int row = row0 + k, g = row / a.l.H;
-        const float r = 1.0f / sqrtf(ss[k] / (float)TT_C + 1e-6f);
+        // the row times a power of two, which is exact, and the rest of its RMS factor for the logits (rounded
+        // to bf16 with the whole factor, q^ moved every logit by 2^-8 / 3; now only its rotated dims are)
+        const float rms = 1.0f / sqrtf(ss[k] / (float)TT_C + 1e-6f), r = __uint_as_float(__float_as_uint(rms) & 0x7F800000u);
+        if (lane == 0) a.l.qm[v * (int64_t)a.l.R8 + row] = rms / r;
         const uint32_t c8[8] = {u[k][0].x, u[k][0].y, u[k][0].z, u[k][0].w, u[k][1].x, u[k][1].y, u[k][1].z, u[k][1].w};
         float x[16];
 #pragma unroll
@@ -832,6 +836,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         int nx = 0;                                           // exchanges by way of sX so far
         uint64_t lsum = two(0.0f, 0.0f);
         bool ok = true;
+        uint64_t qm = 0;                                      // the row's factor, twice
         const auto weigh = [&]() {
             // (the peer has read the last exchange long before this tile's logits come)
             bool wt = (nx == 0 || !live || mbar_wait(&xempty[w], (nx - 1) & 1, a.budget, a.st)) &&
@@ -851,8 +856,9 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float4 f = fac[4 * i + j];
-                        const float2 y0 = two_of(mul2(two(__uint_as_float(sv[4 * j]), __uint_as_float(sv[4 * j + 1])), two(f.x, f.y)));
-                        const float2 y1 = two_of(mul2(two(__uint_as_float(sv[4 * j + 2]), __uint_as_float(sv[4 * j + 3])), two(f.z, f.w)));
+                        const uint64_t s0 = two(__uint_as_float(sv[4 * j]), __uint_as_float(sv[4 * j + 1]));
+                        const uint64_t s1 = two(__uint_as_float(sv[4 * j + 2]), __uint_as_float(sv[4 * j + 3]));
+                        const float2 y0 = two_of(mul2(s0, mul2(two(f.x, f.y), qm))), y1 = two_of(mul2(s1, mul2(two(f.z, f.w), qm)));
                         y[2 * j] = pack_f16(y0.x, y0.y);
                         y[2 * j + 1] = pack_f16(y1.x, y1.y);
                     }
@@ -885,7 +891,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                             const float4 f4 = fac[4 * i + (j >> 1)];
                             const uint64_t f = (j & 1) ? two(f4.z, f4.w) : two(f4.x, f4.y);
                             const float2 o = __half22float2(*reinterpret_cast<const __half2*>(&ov[j]));
-                            const float2 z = two_of(fma2(two(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1])), f, two(o.x, o.y)));
+                            const float2 z = two_of(fma2(two(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1])), mul2(f, qm), two(o.x, o.y)));
                             float p0 = ex2(z.x), p1 = ex2(z.y);
                             if (all) {
                                 const uint64_t p = two(p0, p1);
@@ -919,6 +925,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
             }
         };
         while (ok && walk.next(a, it)) {
+            const float m = r < it.gv * a.l.H ? a.l.qm[it.v * (int64_t)a.l.R8 + r] : 0.0f;
+            qm = two(m, m);
             for (int tt = 0; tt < it.nt && ok; ++tt, ++g) weigh();
             if (!ok) break;
             // the rows' sums: this warp's slots and its twin's; the last item's readers are done with sL
@@ -1242,7 +1250,7 @@ size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 struct TtPlan {
     int G, R8, gps, lde, ldw, clusters, rounds, share, tiles, pieces;
     int64_t groups;
-    size_t erow, ef, eok, wrow, wmask, rf, df, info, rope, part_l, part_o, total;
+    size_t qm, erow, ef, eok, wrow, wmask, rf, df, info, rope, part_l, part_o, total;
 };
 
 TtPlan tt_plan(const csa2_ctx* ctx, int B, int T, int H, int k, int window, bool dense) {
@@ -1272,7 +1280,8 @@ TtPlan tt_plan(const csa2_ctx* ctx, int B, int T, int H, int k, int window, bool
         p.pieces = (p.tiles + p.share - 2) / p.share + 1;     // of the shares that touch a group
     }
     const size_t eg = dense ? (size_t)B : (size_t)B * T;
-    p.erow = up((size_t)p.groups * p.R8 * 1024, 256);
+    p.qm = up((size_t)p.groups * p.R8 * 1024, 256);
+    p.erow = up(p.qm + (size_t)p.groups * p.R8 * 4, 256);
     p.ef = up(p.erow + eg * p.lde * 4, 256);
     p.eok = up(p.ef + eg * p.lde * 4, 256);
     p.wrow = up(p.eok + eg * (p.lde / 32) * 4, 256);
@@ -1312,6 +1321,7 @@ csa2_status tree_tc_run(csa2_ctx* ctx, const TreeCall& c, void* ws, cudaStream_t
     uint8_t* base = reinterpret_cast<uint8_t*>(ws);
     PrepArgs pa = {};
     pa.l.qimg = base;
+    pa.l.qm = reinterpret_cast<float*>(base + p.qm);
     pa.l.erow = reinterpret_cast<int32_t*>(base + p.erow);
     pa.l.ef = reinterpret_cast<float*>(base + p.ef);
     pa.l.eok = reinterpret_cast<uint32_t*>(base + p.eok);

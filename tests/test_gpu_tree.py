@@ -4,7 +4,7 @@ Tolerances.  The fp32 path sums 512 products of |z| <= 23 and exponentials in fp
 logit, so 1e-4 (|o| + rms), lse 1e-5, as the framework's other fp32 attention.  The tensor-core path
 rounds q^ to bf16 (relative 2^-8 / sqrt(3) rms a term, so 2^-8 / sqrt(3) of a logit of unit terms) and
 p to bf16 (the same of each addend); the addends' errors add up as root sums of squares, below
-3.2e-3 of the rms of the node's o, 1.6e-2 at five deviations, and half a bf16 step (2^-8) of the
+3.2e-3 of the rms of the node's o (q^ counted whole, though only its rotated dims are rounded), 1.6e-2 at five deviations, and half a bf16 step (2^-8) of the
 output: 2e-2 (|o| + rms), lse 2e-3.  The rms is each node's own: o is a mean of as many rows as the
 node attends to, so a node with few rows has larger o, and errors, than one with many."""
 import numpy as np
