@@ -132,16 +132,32 @@ __device__ __forceinline__ float sumsq16(const float (&v)[16]) {
     return warp_sum(ss);
 }
 
+// A lane's 16 values to row[16 lane ..], its four pieces in an order that differs between the lanes of a
+// store, so that eight lanes meet 32 banks (in the same order they would meet eight).
+__device__ __forceinline__ void store16(float* row, int lane, const float (&v)[16]) {
+    const bool one = lane & 2, two = lane & 4;
+    float4 p[4], q[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[j] = one ? p[(j + 1) & 3] : p[j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        reinterpret_cast<float4*>(row + 16 * lane)[(j + (lane >> 1)) & 3] = two ? q[(j + 2) & 3] : q[j];
+}
+
 struct SimtSmem {
     float xs[TS_KC * TS_LD];
     float qs[TS_HG * TS_C];
-    float zp[8 * TS_HG * TS_KC];         // the eight parts of every logit
+    float zp[7 * TS_HG * TS_KC];         // the parts of every logit that other warps than its head's have; cos, sin
     float ps[TS_KC * TS_HG];             // probability times RMS factor
-    float rinv[TS_KC];
-    int ok[TS_KC];
+    float rinv[TS_KC];                   // -1: no row
     float scale[TS_HG], m[TS_HG], l[TS_HG];
-    float cs[32], sn[32];
 };
+// Two CTAs an SM (1 KB each is the system's): with one, the rows' way from memory was in the open, and 256
+// nodes of 64 heads over 640 slots took 1,292 us; with two 1,105, with the rows looked up a chunk ahead 975,
+// stored without bank conflicts 908 (24 TFLOP/s).
+static_assert(2 * (sizeof(SimtSmem) + 1024) <= 228 * 1024, "shared memory");
 
 template <int KVK>                       // 0 fp32 rows, 1 bf16, 2 FP4
 __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const SimtArgs a) {
@@ -153,7 +169,8 @@ __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const SimtArgs
     pdl_wait();
     pdl_trigger();
     const TreeNode n = tree_node(c.r, blockIdx.z);
-    if (threadIdx.x < 32) ag_cos_sin(c.rope, n.t, lane, s.cs[lane], s.sn[lane]);
+    float *cs = s.zp, *sn = s.zp + 32;
+    if (threadIdx.x < 32) ag_cos_sin(c.rope, n.t, lane, cs[lane], sn[lane]);
     if (threadIdx.x < TS_HG) {
         s.m[threadIdx.x] = -INFINITY;
         s.l[threadIdx.x] = 0.0f;
@@ -175,8 +192,8 @@ __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const SimtArgs
             for (int i = 0; i < 8; ++i) {
                 const int j = 8 * (lane - 28) + i;
                 const float x0 = v[2 * i], x1 = v[2 * i + 1];
-                v[2 * i] = x0 * s.cs[j] - x1 * s.sn[j];
-                v[2 * i + 1] = x1 * s.cs[j] + x0 * s.sn[j];
+                v[2 * i] = x0 * cs[j] - x1 * sn[j];
+                v[2 * i + 1] = x1 * cs[j] + x0 * sn[j];
             }
         }
         float4* dst = reinterpret_cast<float4*>(s.qs + h * TS_C + 16 * lane);
@@ -188,30 +205,45 @@ __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const SimtArgs
     for (int h = 0; h < TS_HG; ++h) acc[h][0] = acc[h][1] = 0.0f;
     const float inv_sqrt_c = 1.0f / sqrtf((float)TS_C);
     const int s_begin = blockIdx.x * a.spl, s_end = min(n.kq + n.nw, s_begin + a.spl);
+    // lane i < 4 looks up the row of slot c0 + warp + 8 i, a chunk ahead
+    int64_t at = -1;
+    int what = TREE_NONE;
+    const auto look_up = [&](int c0) {
+        at = -1;
+        what = TREE_NONE;
+        if (lane < TS_KC / 8 && c0 + warp + 8 * lane < s_end) at = tree_slot(c.r, n, c0 + warp + 8 * lane, what, a.st, true);
+    };
+    look_up(s_begin);
     for (int c0 = s_begin; c0 < s_end; c0 += TS_KC) {
-        for (int r = warp; r < TS_KC; r += 8) {
-            int kind = TREE_NONE;
-            int64_t row = -1;
-            if (c0 + r < s_end) row = tree_slot(c.r, n, c0 + r, kind, a.st, lane == 0);
-            float v[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-            if (kind == TREE_CACHE) {
-                if (KVK == 2) load16_fp4(c.kv, row, lane, v);
-                else load16f(c.kv, KVK == 0, row, lane, v);
-            } else if (kind != TREE_NONE) {
-                load16f(kind == TREE_RING ? c.swa : c.draft, c.swa_dt == CSA2_F32, row, lane, v);
+        for (int i0 = 0; i0 < TS_KC / 8; i0 += 2) {              // two rows at a time
+            float v[2][16];
+            int kind[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int64_t row = __shfl_sync(0xffffffffu, at, i0 + i);
+                kind[i] = __shfl_sync(0xffffffffu, what, i0 + i);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[i][j] = 0.0f;
+                if (kind[i] == TREE_CACHE) {
+                    if (KVK == 2) load16_fp4(c.kv, row, lane, v[i]);
+                    else load16f(c.kv, KVK == 0, row, lane, v[i]);
+                } else if (kind[i] != TREE_NONE) {
+                    load16f(kind[i] == TREE_RING ? c.swa : c.draft, c.swa_dt == CSA2_F32, row, lane, v[i]);
+                }
             }
-            const float ss = sumsq16(v);
-            float4* dst = reinterpret_cast<float4*>(s.xs + r * TS_LD + 16 * lane);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dst[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-            if (lane == 0) {
-                s.rinv[r] = (c.flags & CSA2_KVNORM) ? 1.0f / sqrtf(ss / (float)TS_C + 1e-6f) : 1.0f;
-                s.ok[r] = kind != TREE_NONE;
+            for (int i = 0; i < 2; ++i) {
+                const int r = warp + 8 * (i0 + i);
+                const float ss = sumsq16(v[i]);
+                store16(s.xs + r * TS_LD, lane, v[i]);
+                if (lane == 0) s.rinv[r] = kind[i] == TREE_NONE ? -1.0f : ((c.flags & CSA2_KVNORM) ? 1.0f / sqrtf(ss / (float)TS_C + 1e-6f) : 1.0f);
             }
         }
+        look_up(c0 + TS_KC);
         __syncthreads();
+        // the softmax of heads `warp` and `warp + 8` is this warp's: its parts of their logits stay
+        float mine[2] = {0.0f, 0.0f};
         {
             float z[TS_HG];
 #pragma unroll
@@ -228,20 +260,27 @@ __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const SimtArgs
                 }
             }
 #pragma unroll
-            for (int h = 0; h < TS_HG; ++h) s.zp[(warp * TS_HG + h) * TS_KC + lane] = z[h];
+            for (int h = 0; h < TS_HG; ++h) {
+                const int o = h & 7;
+                if (o == warp) mine[h >> 3] = z[h];
+                else s.zp[((warp < o ? warp : warp - 1) * TS_HG + h) * TS_KC + lane] = z[h];
+            }
         }
         __syncthreads();
-        for (int h = warp; h < TS_HG; h += 8) {
-            float z = 0.0f;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) z += s.zp[(w * TS_HG + h) * TS_KC + lane];
-            z = s.ok[lane] ? z * s.rinv[lane] * inv_sqrt_c : -INFINITY;
+        for (int i = 0; i < 2; ++i) {
+            const int h = warp + 8 * i;
+            float z = mine[i];
+#pragma unroll
+            for (int w = 0; w < 7; ++w) z += s.zp[(w * TS_HG + h) * TS_KC + lane];
+            const float rinv = s.rinv[lane];
+            z = rinv == -1.0f ? -INFINITY : z * rinv * inv_sqrt_c;
             // (a NaN, which fmaxf drops, counts as some logit: the row has one, whose sum is NaN)
             const float m_old = s.m[h], m_new = fmaxf(m_old, warp_max(z == z ? z : 0.0f));
             const float sc = m_new == -INFINITY ? 1.0f : expf(m_old - m_new);
             const float p = z == -INFINITY ? 0.0f : expf(z - m_new);
             const float l = warp_sum(p);
-            s.ps[lane * TS_HG + h] = p * s.rinv[lane];
+            s.ps[lane * TS_HG + h] = p * rinv;
             __syncwarp();
             if (lane == 0) {
                 s.scale[h] = sc;
@@ -286,6 +325,8 @@ __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const SimtArgs
         }
         return;
     }
+    if (threadIdx.x < 32) ag_cos_sin(c.rope, n.t, lane, cs[lane], sn[lane]);
+    __syncthreads();
     const int j = (int)threadIdx.x - 224;            // this thread's pair of the last 64 dims
 #pragma unroll
     for (int h = 0; h < TS_HG; ++h) {
@@ -300,8 +341,8 @@ __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const SimtArgs
         }
         float x0 = acc[h][0] * sc, x1 = acc[h][1] * sc;
         if ((c.flags & CSA2_ROPE) && j >= 0) {
-            const float y0 = x0 * s.cs[j] + x1 * s.sn[j];
-            x1 = x1 * s.cs[j] - x0 * s.sn[j];
+            const float y0 = x0 * cs[j] + x1 * sn[j];
+            x1 = x1 * cs[j] - x0 * sn[j];
             x0 = y0;
         }
         const int64_t row = n.bt * c.H + h0 + h;
