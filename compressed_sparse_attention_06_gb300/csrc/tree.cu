@@ -9,7 +9,7 @@
 //           shared memory;
 //   output  a thread holds 2 dims of 16 heads: one 8-byte read and 4 broadcasts, 32 multiply-adds.
 // The softmax is online over chunks of 32 rows; few nodes split their rows over several CTAs,
-// joined by log-sum-exp.  Measured: 2 x 13 nodes of 16 heads, 301 entries and a window of 100 each, 29 us of
+// joined by log-sum-exp.  Measured: 2 x 13 nodes of 16 heads, 301 entries and a window of 100 each, 30 us of
 // which 3.4 are their multiply-adds; bf16 and FP4 rows take 14 to 50 times as long here as on the tensor
 // cores (8 x 32 nodes of 64 heads over FP4 pages: 1,414 us, there 89).
 #include <algorithm>
