@@ -1092,7 +1092,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         const uint32_t o_col = tmem + ((uint32_t)(quad * 32) << 16);
         int oq = 0;
         const float zs = a.sink && live ? a.sink[h] : -INFINITY;
-        const bool sectors = ((uintptr_t)a.out & 31u) == 0;
+        // (outputs and workspaces may begin at any multiple of 16 bytes)
+        const bool sectors = ((uintptr_t)a.out & 31u) == 0, part_sectors = ((uintptr_t)a.part_o & 31u) == 0;
         while (walk.next(a, it)) {
             const bool valid = r < it.gv * a.l.H, part = it.pieces > 1;
             const int64_t bt = (int64_t)it.b * a.r.T + it.n0 + (valid ? hq : 0), orow = bt * a.l.H + h;
@@ -1112,7 +1113,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
             // (a piece without slots is left out of the sums)
             if (live && !(part && it.t0 * TT_TILE >= it.slots)) {
                 const float* cs = a.l.rope_cs + bt * 64;
-                const bool wide = part || a.out_f32, whole = part || sectors;        // fp32 rows; whole sectors
+                const bool wide = part || a.out_f32, whole = part ? part_sectors : sectors;        // fp32 rows; whole sectors
                 uint8_t* dst = part ? reinterpret_cast<uint8_t*>(a.part_o + prow * (int64_t)TT_C)
                                     : reinterpret_cast<uint8_t*>(a.out) + orow * (int64_t)(wide ? TT_C * 4 : TT_C * 2);
 #pragma unroll 1

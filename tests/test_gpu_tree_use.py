@@ -123,6 +123,23 @@ def test_outputs_off_a_sector(kind, dense, dt):
     assert torch.equal(out, want) and bool((buf[:off] == 7).all()) and bool((buf[off + n:] == 7).all())
 
 
+@pytest.mark.parametrize("kind,T,k,dense", [("bf16", 1, 2048, False), ("fp4", 3, 1500, False), ("bf16", 19, 1400, True)])
+@pytest.mark.parametrize("off", [16, 32, 48, 240])
+def test_workspace_off_a_sector(kind, T, k, dense, off):
+    """Groups that are dealt out leave partial outputs in the workspace, which may begin at any multiple of
+    16 bytes: the same bits from each, and nothing written beside it."""
+    c = Case(97, 1, T, 24, 3000 if not dense else k, 0 if dense else k, kind, page=16, dense=dense)
+    need = C.load().csa2_tree_attn_workspace_bytes(C.ctx(c.q.device.index), C.BF16, C.FP4_E4M3x16 if kind == "fp4" else C.BF16,
+                                                   C.BF16, 1, T, 24, k, c.kw["window"], int(dense), C.ATTN_DEFAULT)
+    buf = torch.full((need + 512,), 7, dtype=torch.uint8, device=DEV)
+    assert buf.data_ptr() % 256 == 0
+    want, lw = c.run(ws=buf[:need])
+    out, lse = c.run(ws=buf.fill_(7)[off:off + need])
+    C.csa2_ctx_check()
+    assert torch.equal(out, want) and torch.equal(lse, lw)
+    assert bool((buf[:off] == 7).all()) and bool((buf[off + need:] == 7).all())
+
+
 def test_captured_and_replayed():
     """Two graphs captured over one workspace, replayed in turn with other inputs, lengths and trees."""
     cases = [Case(94 + i, 2, 9, 32, 700, 300, "bf16", page=64, lens=[10, 999]) for i in range(4)]
