@@ -354,7 +354,9 @@ __device__ __forceinline__ float lane_squares(const uint2& c, uint32_t scale) {
 }
 
 // Factors f of `n` rows (a multiple of 8, at most 32) at base + row * bytes, lane j's `row` that of row j
-// (-1: none, f 0), eight rows in flight.  A row with an infinity or a NaN has f NaN.
+// (-1: none, f 0), eight rows in flight.  A row with an infinity or a NaN has f NaN.  (The loads are coherent
+// ones, past L1: this kernel may start while the one before still writes rows, so to the read-only path they
+// would not be read-only for as long as it runs.)
 __device__ __forceinline__ float row_factors(const uint8_t* base, int64_t bytes, bool fp4, int row, int n) {
     const int lane = threadIdx.x & 31;
     float sum = 0.0f;
@@ -366,8 +368,8 @@ __device__ __forceinline__ float row_factors(const uint8_t* base, int64_t bytes,
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint8_t* p = base + max(0, __shfl_sync(FULL, row, i + j)) * bytes;
-                c[j] = __ldg(reinterpret_cast<const uint2*>(p) + lane);
-                s[j] = __ldg(p + TT_C / 2 + lane);
+                c[j] = __ldcg(reinterpret_cast<const uint2*>(p) + lane);
+                s[j] = __ldcg(p + TT_C / 2 + lane);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) q[j] = lane_squares(c[j], s[j]);
@@ -376,8 +378,8 @@ __device__ __forceinline__ float row_factors(const uint8_t* base, int64_t bytes,
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint4* p = reinterpret_cast<const uint4*>(base + max(0, __shfl_sync(FULL, row, i + j)) * bytes) + lane;
-                u[j][0] = __ldg(p);
-                u[j][1] = __ldg(p + 32);
+                u[j][0] = __ldcg(p);
+                u[j][1] = __ldcg(p + 32);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) q[j] = lane_squares(u[j][0], u[j][1]);

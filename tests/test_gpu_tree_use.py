@@ -204,6 +204,56 @@ def test_streams_at_once():
         assert torch.equal(o, want[i % 3][0]) and torch.equal(l, want[i % 3][1])
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp4"])
+def test_rows_written_just_before(kind):
+    """Cache rows written and copied, a path committed and the attention queued behind one another without a
+    wait, with other rows every time: each call reads what the ones before it wrote."""
+    B, T, N, page = 3, 6, 256, 16
+    c = Case(121, B, T, 32, N, 100, kind, page=page, lens=[300, 9, 4000], window=40, spare=T)
+    pos, path = C.csa2_tree_plan(c.parent, c.len)
+    n_pages = B * N // page
+    table = torch.arange(n_pages, dtype=torch.int32, device=DEV).view(B, -1)
+    first, count = torch.zeros(B, dtype=torch.int64, device=DEV), torch.full((B,), N, device=DEV)
+    leaf = torch.full((B,), -1, dtype=torch.int32, device=DEV)
+    leaf[0] = 0
+    half = torch.arange(n_pages, dtype=torch.int32, device=DEV).view(-1, 2)          # every even page over the next one
+    steps = []
+    for i in range(6):
+        x = W.normal_tensor((B, N, 512), 130 + i, 1, torch.float32, DEV) * (1.0 + i)
+        steps.append((C.csa2_fp4_pack(x) if kind == "fp4" else x.to(torch.bfloat16),
+                      W.normal_tensor((B, T, 512), 140 + i, 1, torch.bfloat16, DEV) * (6.0 - i)))
+    pool = torch.zeros(n_pages, page, steps[0][0].shape[-1], dtype=steps[0][0].dtype, device=DEV)
+    swa, length = c.swa.clone(), torch.zeros_like(c.len)
+    kw = dict(idx=c.kw["idx"], window=40, swa_pos0=c.kw["swa_pos0"], table=table, sink=c.sink, want_lse=True)
+
+    def step(rows, draft, wait):
+        C.csa2_page_write(pool, table, rows, first, count)
+        wait()
+        C.csa2_page_copy(pool, half)
+        wait()
+        a = C.csa2_tree_attn(c.q, pool, pos, path, c.len, swa, draft, **kw)
+        wait()
+        C.csa2_tree_commit(draft, pos, path, c.len, leaf, swa, swa_pos0=kw["swa_pos0"], new_len=length)
+        wait()
+        after = C.csa2_tree_plan(c.parent, length)
+        wait()
+        b = C.csa2_tree_attn(c.q, pool, *after, length, swa, draft, **kw)
+        wait()
+        return *a, *b
+
+    want = [step(r, d, torch.cuda.synchronize) for r, d in steps]
+    swa.copy_(c.swa)
+    pool.zero_()
+    torch.cuda.synchronize()
+    with _unguarded():
+        got = [step(r, d, lambda: None) for r, d in steps]
+    torch.cuda.synchronize()
+    C.csa2_ctx_check()
+    for g, w in zip(got, want):
+        for x, y in zip(g, w):
+            assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("kind,dense", [("bf16", False), ("bf16", True), ("fp4", False)])
 def test_queries_that_never_come_time_out(kind, dense):
     c = Case(111, 2, 12, 32, 900, 0 if dense else 500, kind, page=64, dense=dense)
