@@ -285,9 +285,14 @@ def alloc_pages(B: int, n_pages: int, page: int, max_pages: int, rows: Dict[str,
 
 
 def pages_append(cache: PagedCache, rows: Dict[str, torch.Tensor], count: torch.Tensor) -> torch.Tensor:
-    """Append rows[name][b, :count[b]] to every sequence in every pool (count [B] int64), copying the
-    beginning of a page that another sequence shares first.  Returns how many entries each sequence
-    got: fewer than count where the pool or the table's row had no room."""
+    """Append rows[name][b, :count[b]] to every sequence in every pool (count [B] int64; rows of every pool,
+    [B, n, ..] with one n, and no more than those), copying the beginning of a page that another sequence
+    shares first.  Returns how many entries each sequence got: fewer than count where there were no more
+    rows, or the pool or the table's row had no room."""
+    given = {name: tuple(rows[name].shape[:2]) if name in rows else None for name in cache.pools}
+    if len(set(given.values())) != 1 or None in given.values():
+        raise ValueError(f"pages_append takes as many rows for every pool, not {given}")
+    count = count.clamp(max=next(iter(given.values()))[1])
     granted, copies = C.csa2_pages_reserve(cache.refs, cache.table, cache.n_entries, count, cache.page)
     for name, pool in cache.pools.items():
         C.csa2_page_copy(pool, copies)

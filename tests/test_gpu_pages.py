@@ -247,6 +247,38 @@ def test_forked_sequences_append_apart():
     check(beams, {k: [want[k][0], want[k][1][:0], want[k][2], want[k][3][:4], want[k][4][:17]] for k in rows})
 
 
+def test_append_takes_no_more_than_the_rows():
+    """A count above the rows given appends those, so that every entry counted has been written; pools that are
+    given different numbers of rows are refused before anything is reserved."""
+    rows = {"kv": ((16,), torch.float32), "ki": ((4,), torch.float32)}
+    cache = P.alloc_pages(3, 30, 4, 8, rows, DEV)
+    for pool in cache.pools.values():
+        pool.fill_(-7.0)                                  # what a page held before
+    gen = torch.Generator(DEV).manual_seed(13)
+    want = {k: [] for k in rows}
+    for n, count, got in ((5, [9, 2, -1], [5, 2, 0]), (0, [3, 0, 1], [0, 0, 0]), (3, [3, 2 ** 40, 4], [3, 3, 3])):
+        x = {k: torch.rand(3, n, *shape, generator=gen, device=DEV) for k, (shape, _) in rows.items()}
+        counts = _i64(count)
+        assert P.pages_append(cache, x, counts).tolist() == got
+        assert counts.tolist() == count                   # the caller's tensor stays
+        for k in rows:
+            want[k].append([x[k][b, :m] for b, m in enumerate(got)])
+    C.csa2_ctx_check()
+    assert cache.n_entries.tolist() == [8, 5, 3]
+    for k in rows:
+        for b, m in enumerate([8, 5, 3]):
+            idx = torch.full((3, m), -1, dtype=torch.int32, device=DEV)
+            idx[b] = torch.arange(m, device=DEV)
+            assert torch.equal(C.csa2_page_read(cache.pools[k], cache.table, idx)[b], torch.cat([w[b] for w in want[k]]))
+    state = [x.clone() for x in (cache.refs, cache.table, cache.n_entries)]
+    x = {k: torch.rand(3, 6, *shape, device=DEV) for k, (shape, _) in rows.items()}
+    for bad in ({**x, "ki": x["ki"][:, :4].contiguous()}, {"kv": x["kv"]}, {}):
+        with pytest.raises(ValueError, match="as many rows"):
+            P.pages_append(cache, bad, _i64([6, 6, 6]))
+    for a, b in zip(state, (cache.refs, cache.table, cache.n_entries)):
+        assert torch.equal(a, b)
+
+
 def test_captured_step_of_a_branch():
     """Fork, reserve, copy and write recorded once and replayed: the state moves on as by eager calls."""
     gen = torch.Generator(DEV).manual_seed(11)
