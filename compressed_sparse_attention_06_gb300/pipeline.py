@@ -302,10 +302,15 @@ def pages_append(cache: PagedCache, rows: Dict[str, torch.Tensor], count: torch.
 
 
 def pages_fork(cache: PagedCache, parent: torch.Tensor) -> PagedCache:
-    """Continuations of sequences parent [B_out] int32 (negative: an empty one): they share their origins'
-    pages until one of them appends.  The pools and refs are the same tensors; the origins stay."""
-    n = cache.n_entries[parent.clamp(min=0).long()].masked_fill(parent < 0, 0)
-    return PagedCache(cache.pools, cache.refs, C.csa2_pages_fork(cache.refs, cache.table, parent), n)
+    """Continuations of sequences parent [B_out] int32 (negative: an empty one; one that is no sequence is
+    flagged and empty): they share their origins' pages until one of them appends.  The pools and refs are
+    the same tensors; the origins stay."""
+    table, B = C.csa2_pages_fork(cache.refs, cache.table, parent), cache.n_entries.numel()
+    if B == 0:
+        n = torch.zeros(parent.shape, dtype=torch.int64, device=parent.device)
+    else:
+        n = cache.n_entries[parent.clamp(min=0, max=B - 1).long()].masked_fill((parent < 0) | (parent >= B), 0)
+    return PagedCache(cache.pools, cache.refs, table, n)
 
 
 def pages_cut(cache: PagedCache, keep: Optional[torch.Tensor] = None) -> None:

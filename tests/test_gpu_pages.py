@@ -247,6 +247,30 @@ def test_forked_sequences_append_apart():
     check(beams, {k: [want[k][0], want[k][1][:0], want[k][2], want[k][3][:4], want[k][4][:17]] for k in rows})
 
 
+def test_fork_of_what_is_no_sequence():
+    """A parent past the sequences is flagged and gives an empty continuation, of no sequences at all too."""
+    cache = P.alloc_pages(2, 20, 4, 4, {"x": ((4,), torch.float32)}, DEV)
+    P.pages_append(cache, {"x": torch.rand(2, 9, 4, device=DEV)}, _i64([9, 6]))
+    refs = cache.refs.tolist()
+    out = P.pages_fork(cache, _i32([1, 2, -1, 2 ** 31 - 1, -2 ** 31]))
+    with pytest.raises(C.Csa2Error):
+        C.csa2_ctx_check()
+    assert out.n_entries.tolist() == [6, 0, 0, 0, 0]
+    assert torch.equal(out.table[0], cache.table[1]) and (out.table[1:] == -1).all()
+    assert sum(out.refs.tolist()) == sum(refs) + 2
+    P.pages_append(out, {"x": torch.rand(5, 2, 4, device=DEV)}, _i64([2] * 5))
+    C.csa2_ctx_check()
+    assert out.n_entries.tolist() == [8, 2, 2, 2, 2] and cache.n_entries.tolist() == [9, 6]
+    none = P.alloc_pages(0, 20, 4, 4, {"x": ((4,), torch.float32)}, DEV)
+    for parent, bad in (([-1, -1], False), ([0, -1], True), ([], False)):
+        out = P.pages_fork(none, _i32(parent))
+        if bad:
+            with pytest.raises(C.Csa2Error):
+                C.csa2_ctx_check()
+        C.csa2_ctx_check()
+        assert out.n_entries.tolist() == [0] * len(parent) and out.table.shape == (len(parent), 4) and (out.table == -1).all()
+
+
 def test_append_takes_no_more_than_the_rows():
     """A count above the rows given appends those, so that every entry counted has been written; pools that are
     given different numbers of rows are refused before anything is reserved."""
