@@ -903,18 +903,24 @@ def csa2_tree_attn(q, kv, pos, path, ctx_len, swa, draft, idx=None, n_visible=No
 
 def csa2_tree_commit(draft, pos, path, ctx_len, leaf, swa, swa_pos0: int = 0, new_len: Optional[torch.Tensor] = None):
     """The draft rows [B,T,c] on the path of node leaf[b] ([B] int32, < 0: none) into the ring swa
-    [B,cap,c]; new_len [B] int64 (may be ctx_len), if given, gets the sequences' lengths then."""
-    B, T, c = draft.shape
-    dev = draft.device
+    [B,cap,c]; new_len [B] int64 (may be ctx_len), if given, gets the sequences' lengths then.  draft and
+    swa both None: the lengths alone."""
+    if (draft is None) != (swa is None):
+        raise ValueError("give draft and swa, or neither")
+    B, T, c, dev = (*pos.shape, 512, pos.device) if draft is None else (*draft.shape, draft.device)
     _want("pos", pos, (B, T), torch.int64, dev)
     _want("path", path, (B, T, T), torch.int16, dev)
     _want("ctx_len", ctx_len, (B,), torch.int64, dev)
     _want("leaf", leaf, (B,), torch.int32, dev)
-    _want("swa", swa, (B, swa.shape[1], c), draft.dtype, dev)
     if new_len is not None:
         _want("new_len", new_len, (B,), torch.int64, dev)
-    st = _lib().csa2_tree_commit(ctx(dev.index), _main(draft), _dt(draft), _a(pos), _a(path), _a(ctx_len), _a(leaf), B, T, c,
-                                 _a(swa), swa.shape[1], swa_pos0, _a(new_len), _on(dev))
+    dt, cap = BF16, 0
+    if draft is not None:
+        _main(draft)
+        dt, cap = _dt(draft), swa.shape[1]
+        _want("swa", swa, (B, cap, c), draft.dtype, dev)
+    st = _lib().csa2_tree_commit(ctx(dev.index), _a(draft), dt, _main(pos), _a(path), _a(ctx_len), _a(leaf), B, T, c, _a(swa), cap,
+                                 swa_pos0, _a(new_len), _on(dev))
     _check("csa2_tree_commit", st)
     return swa
 

@@ -59,7 +59,8 @@ __global__ void __launch_bounds__(TS_MAX_T) tree_plan_kernel(const int32_t* pare
     for (j = i; j >= 0; j = par[j]) rows[(int64_t)i * T + depth--] = (int16_t)j;
 }
 
-// The accepted path's rows into the ring: a CTA a (depth, sequence), 16 bytes a thread.
+// The accepted path's rows into the ring: a CTA a (depth, sequence), 16 bytes a thread (no pieces: no ring, the
+// lengths alone).
 __global__ void __launch_bounds__(128) tree_commit_kernel(const uint4* draft, const int64_t* pos, const int16_t* path,
                                                           const int64_t* ctx_len, const int32_t* leaf, int T, int pieces, uint4* swa,
                                                           int64_t swa_cap, int64_t swa_pos0, int64_t* new_len, unsigned* st) {
@@ -423,19 +424,20 @@ extern "C" csa2_status csa2_tree_plan(csa2_ctx* ctx, const int32_t* parent, cons
 extern "C" csa2_status csa2_tree_commit(csa2_ctx* ctx, const void* draft, csa2_dtype dt, const int64_t* pos,
                                         const int16_t* path, const int64_t* ctx_len, const int32_t* leaf, int B, int T, int c,
                                         void* swa, int64_t swa_cap, int64_t swa_pos0, int64_t* new_len, void* stream) {
-    if (!ctx || B < 0 || T < 1 || T > TS_MAX_T || swa_cap < 1) return CSA2_ERR_INVALID_ARG;
+    const bool ring = draft || swa;                  // neither: the lengths alone
+    if (!ctx || B < 0 || T < 1 || T > TS_MAX_T || (ring && swa_cap < 1)) return CSA2_ERR_INVALID_ARG;
     if (c != TS_C || (dt != CSA2_F32 && dt != CSA2_BF16) || B > 65535) return CSA2_ERR_UNSUPPORTED;
     if (B == 0) return CSA2_OK;
-    if (!draft || !pos || !path || !ctx_len || !leaf || !swa) return CSA2_ERR_INVALID_ARG;
+    if (!pos || !path || !ctx_len || !leaf || (ring ? !draft || !swa : !new_len)) return CSA2_ERR_INVALID_ARG;
     if (!aligned(draft, 16) || !aligned(swa, 16) || !aligned(pos, 8) || !aligned(path, 2) || !aligned(ctx_len, 8) ||
         !aligned(leaf, 4) || !aligned(new_len, 8))
         return CSA2_ERR_INVALID_ARG;
     DeviceGuard dev(ctx);
     if (!dev.ok) return CSA2_ERR_CUDA;
-    const csa2_status l = launch_pdl(tree_commit_kernel, dim3((unsigned)T, (unsigned)B), dim3(128), 0, as_stream(stream),
+    const csa2_status l = launch_pdl(tree_commit_kernel, dim3(ring ? (unsigned)T : 1u, (unsigned)B), dim3(128), 0, as_stream(stream),
                                      reinterpret_cast<const uint4*>(draft), pos, path, ctx_len, leaf, T,
-                                     c * (dt == CSA2_F32 ? 4 : 2) / 16, reinterpret_cast<uint4*>(swa), swa_cap, swa_pos0, new_len,
-                                     ctx->status);
+                                     ring ? c * (dt == CSA2_F32 ? 4 : 2) / 16 : 0, reinterpret_cast<uint4*>(swa), ring ? swa_cap : 1,
+                                     swa_pos0, new_len, ctx->status);
     return l != CSA2_OK ? l : csa2_launch_status();
 }
 

@@ -361,8 +361,9 @@ def draft_attention(q, cache: PagedCache, plan: DraftPlan, swa, draft, sink=None
 
 def accept_draft(plan: DraftPlan, leaf: torch.Tensor, layers, swa_pos0: int = 0) -> torch.Tensor:
     """After verification: the accepted path's rows (up to node leaf[b] [B] int32, negative: none) enter
-    the window ring of every layer, layers = [(draft, swa), ..].  Returns the sequences' new lengths."""
+    the window ring of every layer, layers = [(draft, swa), ..] (none where no layer has a ring).  Returns the
+    sequences' new lengths."""
     new_len = C.alloc(tuple(plan.ctx_len.shape), dtype=torch.int64, device=plan.ctx_len.device)
-    for draft, swa in layers:
+    for draft, swa in list(layers) or [(None, None)]:
         C.csa2_tree_commit(draft, plan.pos, plan.path, plan.ctx_len, leaf, swa, swa_pos0=swa_pos0, new_len=new_len)
     return new_len

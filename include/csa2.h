@@ -680,7 +680,8 @@ csa2_status csa2_cache_gather(csa2_ctx* ctx, const void* src, int64_t row_bytes,
  * path of leaf[b], swa[b, (pos[b,j] - swa_pos0) mod swa_cap] = draft[b, j] (the last swa_cap
  * rows of a longer path).  leaf[b] < 0 or an unused node commits nothing.
  *   leaf    : [B] int32, ids >= T are flagged
- *   swa, draft: as csa2_tree_attn, in dt (F32 or BF16)
+ *   swa, draft: as csa2_tree_attn, in dt (F32 or BF16); both NULL: no ring (swa_cap is not read),
+ *             new_len alone is written
  *   new_len : [B] int64 or NULL: tokens of the sequence then, pos of the leaf + 1 (ctx_len[b] if
  *             nothing is committed); may be ctx_len itself
  */

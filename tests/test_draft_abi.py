@@ -153,3 +153,18 @@ def test_binding_checks_shapes():
         C.csa2_tree_attn(q, torch.zeros(2, 5, 288), pos, path, one, None, None, window=0)
     with pytest.raises(ValueError, match="draft"):
         C.csa2_tree_attn(q, None, pos, path, one, torch.zeros(2, 9, 512), torch.zeros(2, 2, 512), window=9)
+
+
+def test_commit_of_lengths_alone(lib, ctx):
+    """Without a ring there has to be something to write; half a ring is none."""
+    a = dict(ctx=ctx, draft=None, dt=C.BF16, pos=P, path=P, len=P, leaf=P, B=2, T=4, c=512, swa=None, cap=0, pos0=0, new_len=None,
+             stream=None)
+    assert lib.csa2_tree_commit(*a.values()) == BAD
+    assert lib.csa2_tree_commit(*{**a, "new_len": P + 4}.values()) == BAD
+    assert lib.csa2_tree_commit(*{**a, "new_len": P, "leaf": None}.values()) == BAD
+    assert lib.csa2_tree_commit(*{**a, "new_len": P, "B": 0}.values()) == C.OK
+    x = torch.zeros(2, 4, 512)
+    i = torch.zeros(2, 4, dtype=torch.int64)
+    for draft, swa in ((x, None), (None, x)):
+        with pytest.raises(ValueError, match="neither"):
+            C.csa2_tree_commit(draft, i, torch.zeros(2, 4, 4, dtype=torch.int16), i[:, 0], i[:, 0].int(), swa)

@@ -298,6 +298,30 @@ def test_commit(dt, cap, T):
     assert torch.equal(swa, want) and torch.equal(lens, new)
 
 
+@pytest.mark.parametrize("T", [1, 5, 256])
+def test_accept_without_layers(T):
+    """Where no layer has a window ring the lengths are those of a commit with one; bad leaves are flagged."""
+    B = 4
+    par = _tree(75, B, T, unused=1)
+    par[1] = torch.arange(T) - 1
+    plan = P.plan_draft(par, torch.tensor([12, 0, 2 ** 34, 7], device=DEV))
+    swa, draft = W.normal_tensor((B, 9, 512), 76, 1, torch.bfloat16, DEV), W.normal_tensor((B, T, 512), 76, 2, torch.bfloat16, DEV)
+    for leaf in ([T - 1, T - 1, -1, 0], [-7, 0, T // 2, T - 1]):
+        leaf = torch.tensor(leaf, dtype=torch.int32, device=DEV)
+        for none in ([], iter(())):
+            assert torch.equal(P.accept_draft(plan, leaf, none), P.accept_draft(plan, leaf, [(draft, swa)] * 2))
+        C.csa2_ctx_check()
+        for b in range(B):
+            end = int(plan.pos[b, leaf[b]]) if leaf[b] >= 0 else -1
+            assert int(P.accept_draft(plan, leaf, [])[b]) == (end + 1 if end >= 0 else int(plan.ctx_len[b]))
+    length = plan.ctx_len.clone()
+    C.csa2_tree_commit(None, plan.pos, plan.path, length, leaf, None, new_len=length)      # in place
+    assert torch.equal(length, P.accept_draft(plan, leaf, []))
+    assert torch.equal(P.accept_draft(plan, torch.full_like(leaf, T), []), plan.ctx_len)
+    with pytest.raises(C.Csa2Error):
+        C.csa2_ctx_check()
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp4"])
 def test_draft_accept_draft(kind):
     """Two rounds of drafting over one paged cache: the second round's nodes see what the first committed,
