@@ -850,7 +850,8 @@ def csa2_tree_attn(q, kv, pos, path, ctx_len, swa, draft, idx=None, n_visible=No
     """Attention of every node of drafted trees: q [B,T,H,c]; kv [B,N,row], or pages [n_pages,page,row]
     with their table [B,max_pages] int32; pos, path from csa2_tree_plan, ctx_len [B] int64; swa [B,cap,c]
     the ring of committed rows, draft [B,T,c] the nodes' own; idx [B,T,k] int32, or n_visible [B,T] int64
-    <= k_max for the dense form (neither: the window alone).  Returns (out [B,T,H,c], lse [B,T,H] or None).
+    <= k_max for the dense form (neither: the window alone).  An operand that is not given (kv without entries,
+    swa without a window) counts as one in the query's dtype.  Returns (out [B,T,H,c], lse [B,T,H] or None).
     `ws` is the workspace (allocated here when not given)."""
     B, T, H, c = q.shape
     dev = q.device
@@ -868,7 +869,7 @@ def csa2_tree_attn(q, kv, pos, path, ctx_len, swa, draft, idx=None, n_visible=No
         _want("n_visible", n_visible, (B, T), torch.int64, dev)
     if sink is not None:
         _want("sink", sink, (H,), torch.float32, dev)
-    kv_dt, N, page, max_pages = F32, 0, 1, 0
+    kv_dt, N, page, max_pages = _dt(q), 0, 1, 0
     if kv is not None:
         kv_dt = _row_dt(kv, c, kv_fmt)
         if table is None:
@@ -879,7 +880,7 @@ def csa2_tree_attn(q, kv, pos, path, ctx_len, swa, draft, idx=None, n_visible=No
             _want("kv", kv, (kv.shape[0], page, kv.shape[-1]), kv.dtype, dev)
             _want("table", table, (B, max_pages), torch.int32, dev)
             N = kv.shape[0] * page
-    swa_dt, cap = F32, 0
+    swa_dt, cap = _dt(q), 0
     if swa is not None:
         swa_dt, cap = _dt(swa), swa.shape[1]
         _want("swa", swa, (B, cap, c), swa.dtype, dev)

@@ -259,6 +259,31 @@ def test_far_positions_and_large_pools(dt):
     c.check(out, lse, tol["tol"] + 2 * 2.0 ** -12, tol["ltol"] + 2.0 ** -12)
 
 
+@pytest.mark.parametrize("kind,dt", [("bf16", torch.bfloat16), ("fp4", torch.bfloat16), ("f32", torch.float32), ("fp4", torch.float32)])
+@pytest.mark.parametrize("dense", [False, True])
+def test_operands_that_are_not_given(kind, dt, dense):
+    """No window without a ring, no entries without a cache: the same path, and bits, as with one that is not used."""
+    c = Case(67, 2, 5, 24, 150, 0 if dense else 70, kind, dt=dt, window=0, page=16, dense=dense)
+    pos, path = C.csa2_tree_plan(c.parent, c.len)
+    ws = [int(C.load().csa2_tree_attn_workspace_bytes(C.ctx(0), C._dt(c.q), {"f32": C.F32, "bf16": C.BF16, "fp4": C.FP4_E4M3x16}[kind],
+                                                      C._dt(c.q), 2, 5, 24, 150 if dense else 70, 0, int(dense), 7))]
+    buf = torch.empty(max(16, ws[0]), dtype=torch.uint8, device=DEV)   # (no more than the path takes)
+    kw = {**c.kw, "sink": c.sink, "want_lse": True, "ws": buf}
+    want = C.csa2_tree_attn(c.q, c.kv, pos, path, c.len, c.swa, c.draft, **kw)
+    got = C.csa2_tree_attn(c.q, c.kv, pos, path, c.len, None, None, **kw)
+    C.csa2_ctx_check()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    c = Case(68, 2, 5, 24, 150, 0, "bf16" if dt == torch.bfloat16 else "f32", dt=dt, window=30)
+    pos, path = C.csa2_tree_plan(c.parent, c.len)                      # (of this case's lengths)
+    kw = dict(window=30, swa_pos0=c.kw["swa_pos0"], sink=c.sink, want_lse=True)
+    want = C.csa2_tree_attn(c.q, c.kv, pos, path, c.len, c.swa, c.draft, **kw)
+    got = C.csa2_tree_attn(c.q, None, pos, path, c.len, c.swa, c.draft, **kw)
+    none = C.csa2_tree_attn(c.q, None, pos, path, c.len, None, None, **{**kw, "window": 0})
+    C.csa2_ctx_check()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert not none[0].any() and torch.equal(none[1], c.sink.expand_as(none[1]))
+
+
 def test_path_that_does_not_belong_is_flagged():
     c = Case(66, 1, 4, 8, 30, 5, "bf16", window=16)
     pos, path = C.csa2_tree_plan(c.parent, c.len)
