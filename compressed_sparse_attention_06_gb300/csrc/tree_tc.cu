@@ -13,11 +13,13 @@
 // by sqrt(512), 32.7 in base 2: p = 2^z needs no running maximum (sums of 4 million of them stay below
 // 2^55), and the splits of a group's slots simply add up.
 //
-// Each CTA weighs half of a tile's slots for both: it gets the peer's half logits of its 64 slots,
-// rounded to fp16 (2^-12 of a half logit; the rounding of q^'s rotated dims to bf16 moves a logit by
-// several times that), adds them to its own fp32 ones and sends P' (bf16) back, 16 KB each way.  (With whole tiles of
-// logits exchanged and every exponential taken by both, 64 nodes over 4,096 entries took 184 us
-// instead of 174.)  The peer's P' go from shared to tensor memory by the tensor core's own copies, in
+// Each CTA weighs half of a tile's slots for both: it gets the peer's half logits of its 64 slots as 16-bit
+// multiples of 1/992 in base 2 (TT_FIX), adds them to its own fp32 ones and sends P' (bf16) back, 16 KB each
+// way.  The half logits of a query that lies along a row reach 32.7: as fp16 they were off by up to 2^-6
+// there, which moved log-sum-exps by 3e-3; a fixed step moves a weight by 3.5e-4 at most, wherever the logit
+// stands.  (The rounding of q^'s 64 rotated dims to bf16 is what is left: 2^-8 / sqrt(3) of the root of the sum of
+// their products' squares, 1e-3 for a query along a row.)  (With whole tiles of logits exchanged and every
+// exponential taken by both, 64 nodes over 4,096 entries took 184 us instead of 174.)  The peer's P' go from shared to tensor memory by the tensor core's own copies, in
 // order with the products.
 //
 // tree_prep_kernel runs first: q^ (rotated, its RMS factor but for a power of two left to the logits) as
@@ -70,6 +72,10 @@ constexpr int TT_TILE_BYTES = 4 * TT_CHUNK;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr long long TT_BUDGET = 1ll << 31;
+// Half logits as 16-bit integers: y * TT_FIX + TT_FIX_AT in fp32 has the rounded multiple plus 2^15 in its low 16
+// bits.  A half logit is at most sqrt(512) / ln 2 = 32.65, 2^-8 more with the rotated dims rounded to bf16:
+// 32.78 * 992 = 32,515, inside 16 bits.
+constexpr float TT_FIX = 992.0f, TT_FIX_AT = 8388608.0f + 32768.0f;
 
 constexpr int OFF_Q = 0;
 constexpr int OFF_Y = 65536;                             // the peer's P': [2 groups][4 units of 8 slots][128 rows] x 16 B
@@ -184,11 +190,6 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 // Two fp32 values in a register pair, and arithmetic on both at once.
@@ -838,7 +839,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
         int nx = 0;                                           // exchanges by way of sX so far
         uint64_t lsum = two(0.0f, 0.0f);
         bool ok = true;
-        uint64_t qm = 0;                                      // the row's factor, twice
+        uint64_t qm = 0;                                      // the row's factor times TT_FIX, twice
+        const uint64_t fix_at = two(TT_FIX_AT, TT_FIX_AT), minus_at = two(-TT_FIX_AT, -TT_FIX_AT), unfix = two(1.0f / TT_FIX, 1.0f / TT_FIX);
         const auto weigh = [&]() {
             // (the peer has read the last exchange long before this tile's logits come)
             bool wt = (nx == 0 || !live || mbar_wait(&xempty[w], (nx - 1) & 1, a.budget, a.st)) &&
@@ -860,9 +862,9 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                         const float4 f = fac[4 * i + j];
                         const uint64_t s0 = two(__uint_as_float(sv[4 * j]), __uint_as_float(sv[4 * j + 1]));
                         const uint64_t s1 = two(__uint_as_float(sv[4 * j + 2]), __uint_as_float(sv[4 * j + 3]));
-                        const float2 y0 = two_of(mul2(s0, mul2(two(f.x, f.y), qm))), y1 = two_of(mul2(s1, mul2(two(f.z, f.w), qm)));
-                        y[2 * j] = pack_f16(y0.x, y0.y);
-                        y[2 * j + 1] = pack_f16(y1.x, y1.y);
+                        const float2 y0 = two_of(fma2(s0, mul2(two(f.x, f.y), qm), fix_at)), y1 = two_of(fma2(s1, mul2(two(f.z, f.w), qm), fix_at));
+                        y[2 * j] = __byte_perm(__float_as_uint(y0.x), __float_as_uint(y0.y), 0x5410);
+                        y[2 * j + 1] = __byte_perm(__float_as_uint(y1.x), __float_as_uint(y1.y), 0x5410);
                     }
                     peer_st4(their_x + 2 * i * TT_ROWS * 16, y[0], y[1], y[2], y[3], x_full);
                     peer_st4(their_x + (2 * i + 1) * TT_ROWS * 16, y[4], y[5], y[6], y[7], x_full);
@@ -892,8 +894,11 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
                         for (int j = 0; j < 8; ++j) {
                             const float4 f4 = fac[4 * i + (j >> 1)];
                             const uint64_t f = (j & 1) ? two(f4.z, f4.w) : two(f4.x, f4.y);
-                            const float2 o = __half22float2(*reinterpret_cast<const __half2*>(&ov[j]));
-                            const float2 z = two_of(fma2(two(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1])), mul2(f, qm), two(o.x, o.y)));
+                            // (the 16 bits under the exponent of 2^23 are the peer's value plus TT_FIX_AT again; a
+                            // NaN does not survive them, but its row's or query's factor makes one here too)
+                            const uint64_t o = add2(two(__uint_as_float(__byte_perm(ov[j], 0x4B00u, 0x5410)),
+                                                        __uint_as_float(__byte_perm(ov[j], 0x4B00u, 0x5432))), minus_at);
+                            const float2 z = two_of(mul2(fma2(two(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1])), mul2(f, qm), o), unfix));
                             float p0 = ex2(z.x), p1 = ex2(z.y);
                             if (all) {
                                 const uint64_t p = two(p0, p1);
@@ -927,7 +932,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) __cluster_dims__(2, 1, 1)
             }
         };
         while (ok && walk.next(a, it)) {
-            const float m = r < it.gv * a.l.H ? a.l.qm[it.v * (int64_t)a.l.R8 + r] : 0.0f;
+            const float m = r < it.gv * a.l.H ? TT_FIX * a.l.qm[it.v * (int64_t)a.l.R8 + r] : 0.0f;
             qm = two(m, m);
             for (int tt = 0; tt < it.nt && ok; ++tt, ++g) weigh();
             if (!ok) break;

@@ -670,7 +670,7 @@ csa2_status csa2_cache_gather(csa2_ctx* ctx, const void* src, int64_t row_bytes,
  * c == 512, 1 <= H <= 128, k <= 2048 (dense: 4,194,304), window <= 1024, T <= 256, B*T <= 65535;
  * the rows of kv and of swa number below 2^31.
  * BF16 query, window and drafts over BF16 or FP4 rows with both norms run on the tensor cores
- * (p and the rotated dims of q^ rounded to bf16, half of a logit to fp16, sums fp32), all other
+ * (p and the rotated dims of q^ rounded to bf16, half of a logit to a 992nd in base 2, sums fp32), all other
  * calls in fp32.
  * A row that holds a NaN or an infinity makes out and lse of the nodes that attend to it NaN, no others'.
  * Workspace: csa2_tree_attn_workspace_bytes() bytes, 16-byte aligned; with fewer the call
