@@ -133,6 +133,17 @@ __device__ __forceinline__ float sumsq16(const float (&v)[16]) {
     return warp_sum(ss);
 }
 
+// Factor of a warp's row whose squares sum to ss: its RMS factor, or 1 without a norm.  NaN for a row that
+// holds a NaN or an infinity (without a norm its logits could all be -inf, which is no weight), or that is to be
+// normalised and whose sum is not a number in fp32.
+__device__ __forceinline__ float row_factor(const float (&v)[16], float ss, bool norm) {
+    if (ss < INFINITY) return norm ? 1.0f / sqrtf(ss / (float)TS_C + 1e-6f) : 1.0f;
+    bool bad = norm;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) bad |= !(fabsf(v[j]) < INFINITY);
+    return __any_sync(0xffffffffu, bad) ? __int_as_float(0x7FC00000) : 1.0f;
+}
+
 // A lane's 16 values to row[16 lane ..], its four pieces in an order that differs between the lanes of a
 // store, so that eight lanes meet 32 banks (in the same order they would meet eight).
 __device__ __forceinline__ void store16(float* row, int lane, const float (&v)[16]) {
@@ -183,11 +194,9 @@ __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const SimtArgs
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = 0.0f;
         if (h0 + h < c.H) load16f(c.q, c.q_dt == CSA2_F32, n.bt * c.H + h0 + h, lane, v);
-        if (c.flags & CSA2_QNORM) {
-            const float r = 1.0f / sqrtf(sumsq16(v) / (float)TS_C + 1e-6f);
+        const float r = row_factor(v, sumsq16(v), c.flags & CSA2_QNORM);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] *= r;
-        }
+        for (int i = 0; i < 16; ++i) v[i] *= r;
         if ((c.flags & CSA2_ROPE) && lane >= 28) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -238,7 +247,8 @@ __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const SimtArgs
                 const int r = warp + 8 * (i0 + i);
                 const float ss = sumsq16(v[i]);
                 store16(s.xs + r * TS_LD, lane, v[i]);
-                if (lane == 0) s.rinv[r] = kind[i] == TREE_NONE ? -1.0f : ((c.flags & CSA2_KVNORM) ? 1.0f / sqrtf(ss / (float)TS_C + 1e-6f) : 1.0f);
+                const float f = row_factor(v[i], ss, c.flags & CSA2_KVNORM);
+                if (lane == 0) s.rinv[r] = kind[i] == TREE_NONE ? -1.0f : f;
             }
         }
         look_up(c0 + TS_KC);

@@ -672,7 +672,8 @@ csa2_status csa2_cache_gather(csa2_ctx* ctx, const void* src, int64_t row_bytes,
  * BF16 query, window and drafts over BF16 or FP4 rows with both norms run on the tensor cores
  * (p and the rotated dims of q^ rounded to bf16, half of a logit to a 992nd in base 2, sums fp32), all other
  * calls in fp32.
- * A row that holds a NaN or an infinity makes out and lse of the nodes that attend to it NaN, no others'.
+ * A row that holds a NaN or an infinity, or is to be normalised and whose squares sum past fp32's range,
+ * makes out and lse of the nodes that attend to it NaN, no others'; a head of a query likewise its own.
  * Workspace: csa2_tree_attn_workspace_bytes() bytes, 16-byte aligned; with fewer the call
  * returns CSA2_ERR_INVALID_ARG.  Calls that share a workspace must not overlap on the GPU.
  *

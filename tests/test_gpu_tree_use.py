@@ -97,6 +97,48 @@ def test_rows_without_numbers_reach_only_who_attends(kind, dt, dense, bad):
     check(hit)
 
 
+@pytest.mark.parametrize("flags", [0, 1, 2, 4, 5, 7])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 3e30])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_rows_without_numbers_whatever_the_norms(flags, bad, dt):
+    """The same with and without the norms: an infinity's logits may be minus infinity, and a large value's
+    square no number in fp32.  A query's head without numbers is alone in it."""
+    B, T, H, N, win = 1, 6, 16, 50, 4
+    c = Case(96, B, T, H, N, 30, "f32" if dt == torch.float32 else "bf16", dt=dt, window=win, lens=[20])
+    c.parent = torch.tensor([[-1, 0, 0, 2, 3, -2]], dtype=torch.int32, device=DEV)               # 0-1, 0-2-3-4
+    out, lse = c.run(flags=flags, out_dtype=torch.float32)
+    C.csa2_ctx_check()
+
+    def check(hit):
+        o, l = c.run(flags=flags, out_dtype=torch.float32)
+        C.csa2_ctx_check()
+        assert bool(torch.isnan(o[0, hit]).all()) and bool(torch.isnan(l[0, hit]).all())
+        rest = [i for i in range(T) if i not in hit]
+        assert torch.equal(o[0, rest], out[0, rest]) and torch.equal(l[0, rest], lse[0, rest])
+
+    def with_(name, at):
+        keep = getattr(c, name).clone()
+        getattr(c, name)[at] = bad
+        return keep
+
+    finite = abs(bad) < 1e38
+    if not finite or flags & C.KVNORM:
+        for name, at, hit in (("draft", (0, 2, 77), [2, 3, 4]), ("swa", (0, (19 - c.kw["swa_pos0"]) % c.swa.shape[1], 5), [0, 1, 2, 3]),
+                              ("kv", (0, int(c.sel[0][1][3]), 500), [i for i in range(5) if (c.sel[0][i] == c.sel[0][1][3]).any()])):
+            keep = with_(name, at)
+            check(hit)
+            setattr(c, name, keep)
+    if not finite or flags & C.QNORM:
+        keep = with_("q", (0, 3, 7, 100))
+        o, l = c.run(flags=flags, out_dtype=torch.float32)
+        C.csa2_ctx_check()
+        hit = torch.zeros(1, T, H, dtype=torch.bool, device=DEV)
+        hit[0, 3, 7] = True
+        assert bool(torch.isnan(o[hit]).all()) and bool(torch.isnan(l[hit]).all())
+        assert torch.equal(o[~hit], out[~hit]) and torch.equal(l[~hit], lse[~hit])
+        c.q = keep
+
+
 @pytest.mark.parametrize("kind,dt", [("f32", torch.float32), ("bf16", torch.bfloat16)])
 @pytest.mark.parametrize("k", [1, 100])
 def test_nothing_but_rows_without_numbers(kind, dt, k):
