@@ -879,7 +879,8 @@ def csa2_tree_attn(q, kv, pos, path, ctx_len, swa, draft, idx=None, n_visible=No
             page, max_pages = kv.shape[1], table.shape[1]
             _want("kv", kv, (kv.shape[0], page, kv.shape[-1]), kv.dtype, dev)
             _want("table", table, (B, max_pages), torch.int32, dev)
-            N = kv.shape[0] * page
+            # (a table without columns has no address, and with NULL the library takes kv as [B, N, row]: no entries)
+            N = kv.shape[0] * page if table.numel() else 0
     swa_dt, cap = _dt(q), 0
     if swa is not None:
         swa_dt, cap = _dt(swa), swa.shape[1]

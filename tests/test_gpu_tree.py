@@ -284,6 +284,27 @@ def test_operands_that_are_not_given(kind, dt, dense):
     assert not none[0].any() and torch.equal(none[1], c.sink.expand_as(none[1]))
 
 
+@pytest.mark.parametrize("kind,dt", [("f32", torch.float32), ("bf16", torch.bfloat16), ("fp4", torch.bfloat16)])
+@pytest.mark.parametrize("dense", [False, True])
+def test_table_without_columns(kind, dt, dense):
+    """Every entry lies behind such a table: skipped and flagged, whatever the pool holds."""
+    c = Case(69, 3, 4, 16, 64, 0 if dense else 20, kind, dt=dt, window=9, page=16, dense=dense)
+    none = torch.empty(3, 0, dtype=torch.int32, device=DEV)
+    out, lse = c.run(table=none)
+    with pytest.raises(C.Csa2Error):
+        C.csa2_ctx_check()
+    gone = dict(n_visible=torch.zeros_like(c.kw["n_visible"])) if dense else dict(idx=torch.full_like(c.kw["idx"], -1))
+    want, lw = c.run(**gone)
+    C.csa2_ctx_check()
+    # (the dense form has no slots for entries it does not see, so its window's add up in another order)
+    tol = F32 if dt == torch.float32 else BF
+    assert_close(to_np(out), to_np(want), 2 * tol["tol"], "out")
+    assert_close(to_np(lse), to_np(lw), 2 * tol["ltol"], "lse")
+    out, lse = c.run(table=none, **gone)                               # nothing asked for is no error
+    C.csa2_ctx_check()
+    assert torch.equal(out, want) and torch.equal(lse, lw)
+
+
 def test_path_that_does_not_belong_is_flagged():
     c = Case(66, 1, 4, 8, 30, 5, "bf16", window=16)
     pos, path = C.csa2_tree_plan(c.parent, c.len)
