@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_reserve_kernel(const Reserve
         uint32_t w = 0, total;
         if (i < nb) {
             const PageRange r = page_range(a, b0 + i, true);
-            w = (uint32_t)(r.j1 - r.j0 + 31) / 32;
+            w = ((uint32_t)(r.j1 - r.j0) + 31u) / 32u;
             s.fail[i] = 0x7FFFFFFF;
         }
         const uint32_t before = block_scan(s.tmp, w, total);
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_reserve_kernel(const Reserve
             const int64_t b = b0 + q;
             const PageRange r = page_range(a, b, false);
             const uint32_t w = i - s.words[q];
-            const int j = r.j0 + 32 * (int)w + lane;
+            const int64_t j = r.j0 + 32 * (int64_t)w + lane;      // (past 32 bits behind the longest rows)
             at = b * a.W + w;
             bool want = false;
             if (j < r.j1) {
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_reserve_kernel(const Reserve
                     want = uses > 1;
                     if (uses < 1) {      // no page of the pool, or one that is free
                         csa2_flag(a.st, CSA2_DEVBIT_RANGE);
-                        atomicMin(&s.fail[q], j);
+                        atomicMin(&s.fail[q], (int)j);
                     }
                 }
             }
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_reserve_kernel(const Reserve
         const int64_t b = b0 + q;
         const PageRange r = page_range(a, b, false);
         const uint32_t w = i - s.words[q];
-        const int j = r.j0 + 32 * (int)w + lane;
+        const int64_t j = r.j0 + 32 * (int64_t)w + lane;
         const uint32_t mask = a.want[b * a.W + w];
         int2 copy = make_int2(-1, -1);
         if ((mask >> lane) & 1u) {
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_reserve_kernel(const Reserve
                     if (j == r.j0 && r.first % a.page != 0) copy = make_int2(old, id);
                 }
             } else {
-                atomicMin(&s.fail[q], j);
+                atomicMin(&s.fail[q], (int)j);
             }
         }
         if (w == 0 && lane == 0) {

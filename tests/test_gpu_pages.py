@@ -100,6 +100,33 @@ def test_reserve_a_long_range_and_run_out():
     assert np.array_equal(to_np(again), g) and (none == -1).all()
 
 
+def test_the_longest_table():
+    """The last pages of a row of 2^31 - 1: what lies behind it is neither looked at nor written."""
+    P_ = 2 ** 31 - 1
+    flat = torch.full((P_ + 1,), -1, dtype=torch.int32, device=DEV)
+    table, refs = flat[:P_].view(1, P_), _i32(np.zeros(50))
+    ws = torch.empty(C.load().csa2_pages_reserve_workspace_bytes(50, 1, P_), dtype=torch.uint8, device=DEV)
+    for first, count, got in ((P_ - 1, 1, 1), (P_ - 3, 2, 2), (P_ - 40, 40, 40)):
+        granted, copies = C.csa2_pages_reserve(refs, table, _i64([first]), _i64([count]), 1, ws=ws)
+        C.csa2_ctx_check()
+        assert granted.tolist() == [got] and copies.tolist() == [[-1, -1]]
+    assert table[0, P_ - 40:].tolist() == [*range(3, 40), 1, 2, 0] and int(flat[P_]) == -1 and int(refs.sum()) == 40
+    granted, _ = C.csa2_pages_reserve(refs, table, _i64([P_ - 2]), _i64([3]), 1, ws=ws)
+    with pytest.raises(C.Csa2Error):
+        C.csa2_ctx_check()                                # (the row ends)
+    assert granted.tolist() == [2]
+    pool = torch.zeros(50, 1, 4, device=DEV)
+    C.csa2_page_write(pool, table, torch.ones(1, 2, 4, device=DEV), _i64([P_ - 2]), granted)
+    C.csa2_ctx_check()
+    assert pool.sum((1, 2)).nonzero().flatten().tolist() == [0, 2]
+    C.csa2_pages_free(refs, table, 1, _i64([P_ - 1]))
+    C.csa2_ctx_check()
+    assert int(flat[P_ - 1]) == -1 and int(refs.sum()) == 39
+    C.csa2_pages_free(refs, table, 1)
+    C.csa2_ctx_check()
+    assert not refs.any() and bool((flat[P_ - 64:] == -1).all())
+
+
 def test_what_does_not_fit_is_flagged():
     refs, table = _i32(np.zeros(4)), _i32(np.full((2, 3), -1))
     granted, _ = C.csa2_pages_reserve(refs, table, _i64([5, 9]), _i64([3, 2 ** 62]), 2)
