@@ -265,7 +265,8 @@ def evict_caches(acc, n_entries, caches: Dict[str, torch.Tensor], keep: int, rec
 class PagedCache:
     """Caches of B sequences in pages that sequences may share (csa2_pages_*): every pool
     [n_pages, page, ..] holds one kind of rows (main KV, indexer keys, of any layers) of entry e of
-    sequence b on page table[b, e // page]; refs counts the places that hold a page."""
+    sequence b on page table[b, e // page]; refs counts the places that hold a page.  pages_append, pages_cut
+    and pages_compact change the tensors in place, so that a captured step goes on where the last one ended."""
     pools: Dict[str, torch.Tensor]
     refs: torch.Tensor           # [n_pages] int32
     table: torch.Tensor          # [B, max_pages] int32, -1: none
@@ -297,7 +298,7 @@ def pages_append(cache: PagedCache, rows: Dict[str, torch.Tensor], count: torch.
     for name, pool in cache.pools.items():
         C.csa2_page_copy(pool, copies)
         C.csa2_page_write(pool, cache.table, rows[name], cache.n_entries, granted)
-    cache.n_entries = cache.n_entries + granted
+    cache.n_entries.add_(granted)
     return granted
 
 
@@ -318,9 +319,9 @@ def pages_cut(cache: PagedCache, keep: Optional[torch.Tensor] = None) -> None:
     as it is) and give back the pages behind them."""
     C.csa2_pages_free(cache.refs, cache.table, cache.page, keep)
     if keep is None:
-        cache.n_entries = torch.zeros_like(cache.n_entries)
+        cache.n_entries.zero_()
     else:
-        cache.n_entries = torch.where(keep < 0, cache.n_entries, torch.minimum(keep, cache.n_entries))
+        cache.n_entries.copy_(torch.where(keep < 0, cache.n_entries, torch.minimum(keep, cache.n_entries)))
 
 
 def pages_compact(cache: PagedCache) -> torch.Tensor:

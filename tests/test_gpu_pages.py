@@ -371,6 +371,44 @@ def test_captured_step_of_a_branch():
         assert torch.equal(got[i, f:f + n], rows[i, :n])
 
 
+def test_captured_appends_go_on(monkeypatch):
+    """pages_append and pages_cut recorded once: every replay appends behind the entries of the one before."""
+    monkeypatch.setattr(C, "alloc", lambda shape, dtype, device: torch.empty(shape, dtype=dtype, device=device))
+    gen = torch.Generator(DEV).manual_seed(17)
+    cache = P.alloc_pages(2, 40, 4, 12, {"x": ((16,), torch.float32)}, DEV)
+    rows, count, keep = torch.zeros(2, 5, 16, device=DEV), _i64([5, 2]), _i64([-1, -1])
+    want = [torch.zeros(0, 16, device=DEV)] * 2
+
+    def step():
+        P.pages_cut(cache, keep)
+        return P.pages_append(cache, {"x": rows}, count)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()                                            # (warm-up: five and two entries of zeros)
+        P.pages_cut(cache)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        granted = step()
+    assert cache.n_entries.tolist() == [0, 0]             # recorded, not run
+    for cut in ([-1, -1], [-1, -1], [3, -1], [100, 1], [0, 4]):
+        x = torch.rand(2, 5, 16, generator=gen, device=DEV)
+        rows.copy_(x)
+        keep.copy_(_i64(cut))
+        graph.replay()
+        C.csa2_ctx_check()
+        assert granted.tolist() == [5, 2]
+        want = [torch.cat([w if k < 0 else w[:k], x[b, :n]]) for b, (w, k, n) in enumerate(zip(want, cut, (5, 2)))]
+        assert cache.n_entries.tolist() == [len(w) for w in want]
+        for b, w in enumerate(want):
+            idx = torch.full((2, len(w)), -1, dtype=torch.int32, device=DEV)
+            idx[b] = torch.arange(len(w), device=DEV)
+            assert torch.equal(C.csa2_page_read(cache.pools["x"], cache.table, idx)[b], w)
+    assert int(cache.refs.sum()) == int((cache.table >= 0).sum())
+
+
 def test_empty_calls():
     none = torch.zeros(0, dtype=torch.int32, device=DEV)
     t0 = torch.zeros(0, 4, dtype=torch.int32, device=DEV)
