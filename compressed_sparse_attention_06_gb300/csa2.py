@@ -978,8 +978,8 @@ def csa2_pages_reserve(refs, table, first, count, page: int, granted: Optional[t
 def csa2_pages_compact(refs, table, moves: Optional[torch.Tensor] = None, n_used: Optional[torch.Tensor] = None,
                        ws: Optional[torch.Tensor] = None):
     """Moves the pages in use to the front of the pool: refs and table (all the tables that hold its
-    pages, in one tensor) are updated.  Returns (moves [n_pages // 2, 2] int32, -1 padded, for
-    csa2_page_copy on every pool; n_used [1] int64)."""
+    pages, in one tensor: else nothing moves, flagged) are updated.  Returns (moves [n_pages // 2, 2] int32,
+    -1 padded, for csa2_page_copy on every pool; n_used [1] int64)."""
     n, B, P, dev = _state(refs, table)
     moves = _given("moves", moves, (n // 2, 2), torch.int32, dev)
     n_used = _given("n_used", n_used, (1,), torch.int64, dev)

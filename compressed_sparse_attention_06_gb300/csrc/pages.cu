@@ -307,10 +307,29 @@ struct CompactArgs {
     int64_t* n_used;
     int32_t* to;                         // [n_pages] where a page at or behind the used ones goes
     int64_t* cut;                        // the number of used pages, for the tables' kernel
-    int32_t* table;                      // the tables, where this kernel sees to them (else NULL)
+    int32_t* table;                      // the tables, [entries]
     int64_t entries;
+    bool inside;                         // this kernel sees to them, else one behind it
     unsigned* st;
 };
+
+// This thread's part of the places that tables hold, of `step` threads.
+__device__ __forceinline__ uint32_t count_places(const int32_t* table, int64_t entries, int64_t n_pages, int64_t i, int64_t step) {
+    const auto is = [&](int32_t t) { return (uint32_t)(t >= 0 && t < n_pages); };
+    uint32_t n = 0;
+    int64_t done = 0;
+    if (((uintptr_t)table & 15u) == 0) {
+        const int4* quads = reinterpret_cast<const int4*>(table);
+        done = entries / 4 * 4;
+#pragma unroll 4
+        for (int64_t q = i; q < entries / 4; q += step) {
+            const int4 t = quads[q];
+            n += is(t.x) + is(t.y) + is(t.z) + is(t.w);
+        }
+    }
+    for (int64_t e = done + i; e < entries; e += step) n += is(table[e]);
+    return n;
+}
 
 // A table's entry after the moves.
 __device__ __forceinline__ void remap(int32_t* entry, int64_t n_pages, int64_t cut, const int32_t* to, unsigned* st) {
@@ -322,7 +341,7 @@ __device__ __forceinline__ void remap(int32_t* entry, int64_t n_pages, int64_t c
 }
 
 __global__ void __launch_bounds__(PG_THREADS) pages_compact_kernel(const CompactArgs a) {
-    __shared__ uint32_t tmp[PG_WARPS + 1], used[PG_CTAS], from[PG_CTAS], into[PG_CTAS];
+    __shared__ uint32_t tmp[PG_WARPS + 1], used[PG_CTAS], spare[PG_CTAS], from[PG_CTAS], into[PG_CTAS];
     const int nc = gridDim.x;
     const uint32_t rank = cta_rank();
     pdl_wait();
@@ -330,13 +349,37 @@ __global__ void __launch_bounds__(PG_THREADS) pages_compact_kernel(const Compact
     cluster_sync();                      // every CTA runs: its shared memory may be written
     const int64_t share = ((a.n_pages + nc - 1) / nc + 3) / 4 * 4;
     const int64_t p0 = min(a.n_pages, rank * share), p1 = min(a.n_pages, p0 + share);
-    uint32_t n = 0, total;
-    for (int64_t p = p0 + threadIdx.x; p < p1; p += PG_THREADS) n += a.refs[p] > 0;
+    const int64_t step = (int64_t)nc * PG_THREADS, half = a.n_pages / 2, i0 = (int64_t)rank * PG_THREADS + threadIdx.x;
+    uint32_t n = 0, total, uses = 0, rest;
+    for (int64_t p = p0 + threadIdx.x; p < p1; p += PG_THREADS) {
+        const int32_t r = a.refs[p];
+        n += r > 0;
+        uses += (uint32_t)max(r, 0);
+    }
+    uses -= count_places(a.table, a.entries, a.n_pages, i0, step);
     block_scan(tmp, n, total);
-    if (threadIdx.x < nc) put_remote(&used[rank], threadIdx.x, total);
+    block_scan(tmp, uses, rest);
+    if (threadIdx.x < nc) {
+        put_remote(&used[rank], threadIdx.x, total);
+        put_remote(&spare[rank], threadIdx.x, rest);
+    }
     cluster_sync();
     int64_t cut = 0;
-    for (int i = 0; i < nc; ++i) cut += used[i];
+    uint32_t missing = 0;                // uses less places, modulo 2^32
+    for (int i = 0; i < nc; ++i) {
+        cut += used[i];
+        missing += spare[i];
+    }
+    if (missing != 0) {
+        // a table that holds pages is not among these: they would move away under it, so none does
+        for (int64_t i = i0; i < half; i += step) a.moves[2 * i] = a.moves[2 * i + 1] = -1;
+        if (rank == 0 && threadIdx.x == 0) {
+            csa2_flag(a.st, CSA2_DEVBIT_RANGE);
+            *a.cut = a.n_pages;
+            if (a.n_used) *a.n_used = a.n_pages;
+        }
+        return;
+    }
     // sources (used, at or behind the cut) and holes (free, before it) of this share
     uint32_t ns = 0, nh = 0, ts, th;
     for (int64_t p = p0 + threadIdx.x; p < p1; p += PG_THREADS) {
@@ -384,8 +427,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_compact_kernel(const Compact
     }
     __threadfence();
     cluster_sync();
-    const int64_t step = (int64_t)nc * PG_THREADS, half = a.n_pages / 2;
-    for (int64_t i = (int64_t)rank * PG_THREADS + threadIdx.x; i < half; i += step) {
+    for (int64_t i = i0; i < half; i += step) {
         if (i < n_moves) {
             const int32_t src = a.moves[2 * i], dst = a.moves[2 * i + 1];
             a.to[src] = dst;
@@ -399,10 +441,10 @@ __global__ void __launch_bounds__(PG_THREADS) pages_compact_kernel(const Compact
         *a.cut = cut;
         if (a.n_used) *a.n_used = cut;
     }
-    if (!a.table) return;
+    if (!a.inside) return;
     __threadfence();
     cluster_sync();                      // every page's way is written
-    for (int64_t i = (int64_t)rank * PG_THREADS + threadIdx.x; i < a.entries; i += step) remap(a.table + i, a.n_pages, cut, a.to, a.st);
+    for (int64_t i = i0; i < a.entries; i += step) remap(a.table + i, a.n_pages, cut, a.to, a.st);
 }
 
 __global__ void __launch_bounds__(256) pages_remap_kernel(int32_t* table, int64_t total, int64_t n_pages, const int32_t* to,
@@ -699,7 +741,7 @@ extern "C" csa2_status csa2_pages_compact(csa2_ctx* ctx, int32_t* refs, int64_t 
     cluster_config(cfg, at, n_pages, 0, 0, s);
     // a small table is seen to by the same kernel (a launch less: 300 pages and two pools 47 us a step, not 51)
     const bool inside = total <= 4ll * cfg.gridDim.x * PG_THREADS;
-    const CompactArgs a = {refs, n_pages, moves, n_used, to, cut, inside ? table : nullptr, total, ctx->status};
+    const CompactArgs a = {refs, n_pages, moves, n_used, to, cut, table, total, inside, ctx->status};
     if (cudaLaunchKernelEx(&cfg, pages_compact_kernel, a) != cudaSuccess) return CSA2_ERR_CUDA;
     if (inside) return csa2_launch_status();
     const csa2_status l = launch_pdl(pages_remap_kernel, dim3(flat_grid(ctx, total)), dim3(256), 0, s, table, total, n_pages,

@@ -324,10 +324,20 @@ def pages_cut(cache: PagedCache, keep: Optional[torch.Tensor] = None) -> None:
         cache.n_entries.copy_(torch.where(keep < 0, cache.n_entries, torch.minimum(keep, cache.n_entries)))
 
 
-def pages_compact(cache: PagedCache) -> torch.Tensor:
-    """Move the pages in use to the front of every pool (the cache's table must hold all of them: the
-    tables of several caches over the same pools are rows of one).  Returns their number, [1] int64."""
-    moves, n_used = C.csa2_pages_compact(cache.refs, cache.table)
+def pages_compact(cache: PagedCache, *others: PagedCache) -> torch.Tensor:
+    """Move the pages in use to the front of every pool.  others: all the other caches over the same pools
+    (what pages_fork made of this one, or this one was made of); with one left out that holds pages nothing
+    moves, and csa2_ctx_check raises.  Returns the number of pages in use, [1] int64."""
+    caches = (cache, *others)
+    if any(c.refs is not cache.refs and c.refs.data_ptr() != cache.refs.data_ptr() for c in others):
+        raise ValueError("pages_compact takes caches over the same pools")
+    if not others:
+        moves, n_used = C.csa2_pages_compact(cache.refs, cache.table)
+    else:
+        tables = torch.cat([c.table.flatten() for c in caches])
+        moves, n_used = C.csa2_pages_compact(cache.refs, tables.unsqueeze(0))
+        for c, t in zip(caches, tables.split([c.table.numel() for c in caches])):
+            c.table.copy_(t.view_as(c.table))
     for pool in cache.pools.values():
         C.csa2_page_copy(pool, moves)
     return n_used

@@ -733,7 +733,9 @@ csa2_status csa2_tree_commit(csa2_ctx* ctx, const void* draft, csa2_dtype dt, co
  *
  * csa2_pages_compact -- moves the n_used pages in use to the front of the pool: the i-th used
  * page at or behind n_used goes to the i-th free one before it; tables and refs follow.
- *   table  : [B, max_pages]: all the tables that hold pages of the pool, in one block
+ *   table  : [B, max_pages]: all the tables that hold pages of the pool, in one block.  Where their
+ *            entries do not add up to refs (a table is missing, and its pages would move away under
+ *            it) the call is flagged and moves nothing: refs and table stay, moves are -1 -1, n_used is n_pages
  *   moves  : [n_pages / 2, 2] int32 (from, to), -1 -1 behind the last, for csa2_page_copy on
  *            every pool;  n_used: [1] int64 or NULL
  *   ws     : csa2_pages_compact_workspace_bytes() bytes, 16-byte aligned

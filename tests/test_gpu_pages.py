@@ -371,6 +371,84 @@ def test_captured_step_of_a_branch():
         assert torch.equal(got[i, f:f + n], rows[i, :n])
 
 
+@pytest.mark.parametrize("n_pages,B,P_", [(9, 2, 3), (300, 7, 30), (3000, 33, 41), (5000, 3, 20001), (2, 1, 1), (1, 1, 1)])
+@pytest.mark.parametrize("off", [0, 1])
+def test_compaction_without_all_tables_moves_nothing(n_pages, B, P_, off):
+    """Pages that a table outside the call holds would move away under it: flagged, and everything stays."""
+    o, rng = _random(n_pages + 1, n_pages, B, P_, 4, fill=min(1.0, 0.7 * n_pages / (B * P_)))
+    free = np.flatnonzero(o.refs == 0)
+    o.refs[rng.permutation(free)[:len(free) // 2]] = 0
+    if not o.refs.any():
+        o.refs[0], o.table[0, 0] = 1, 0
+    refs, _ = _state(o)
+    flat = torch.full((B * P_ + 1,), -1, dtype=torch.int32, device=DEV)
+    table = flat[off:off + B * P_].view(B, P_).copy_(_i32(o.table))    # (off: not on a 16-byte boundary)
+    held = int(rng.choice(np.flatnonzero(o.refs)))
+    for page, d in ((held, 1), (held, -1), (int(np.argmin(o.refs)), 1)):
+        r = refs.clone()
+        r[page] += d
+        before, t = r.clone(), table.clone()
+        moves, n_used = C.csa2_pages_compact(r, table)
+        with pytest.raises(C.Csa2Error):
+            C.csa2_ctx_check()
+        assert torch.equal(r, before) and torch.equal(table, t) and (moves == -1).all() and int(n_used) == n_pages
+    moves, n_used = C.csa2_pages_compact(refs, table)
+    C.csa2_ctx_check()
+    want, cut = o.compact()
+    _same(o, refs, table)
+    assert np.array_equal(to_np(moves), want) and int(n_used) == cut
+
+
+@pytest.mark.parametrize("P_", [12, 9000])
+def test_compaction_of_prompts_and_continuations(P_):
+    """The caches of prompts and of their continuations, each with its table, over one pool: alone either one's
+    compaction is refused, together both find their entries again."""
+    gen = torch.Generator(DEV).manual_seed(19)
+    base = P.alloc_pages(3, 60, 4, P_, {"x": ((4,), torch.float32), "y": ((3,), torch.float32)}, DEV)
+
+    def rows(B, n):
+        return {k: torch.rand(B, n, w, generator=gen, device=DEV) for k, w in (("x", 4), ("y", 3))}
+
+    x = rows(3, 20)
+    P.pages_append(base, x, _i64([20, 9, 15]))
+    beams = P.pages_fork(base, _i32([0, 0, 2, 1]))
+    y = rows(4, 6)
+    P.pages_append(beams, y, _i64([6, 1, 3, 0]))
+    wide = P.PagedCache(base.pools, base.refs, torch.full((1, 2), -1, dtype=torch.int32, device=DEV), _i64([0]))
+    z = rows(1, 5)
+    P.pages_append(wide, z, _i64([5]))                    # a table of another width over the same pools
+    P.pages_cut(base, _i64([-1, 0, 6]))
+    C.csa2_ctx_check()
+    first = {"base": (20, 0, 6), "beams": ((0, 20, 6), (0, 20, 1), (2, 15, 3), (1, 9, 0))}
+
+    def check():
+        for k in ("x", "y"):
+            want = [(base, [x[k][b, :n] for b, n in enumerate(first["base"])]), (wide, [z[k][0]]),
+                    (beams, [torch.cat([x[k][p, :n], y[k][i, :m]]) for i, (p, n, m) in enumerate(first["beams"])])]
+            for cache, seqs in want:
+                for b, w in enumerate(seqs):
+                    idx = torch.full((len(seqs), len(w)), -1, dtype=torch.int32, device=DEV)
+                    idx[b] = torch.arange(len(w), device=DEV)
+                    assert torch.equal(C.csa2_page_read(cache.pools[k], cache.table, idx)[b], w)
+        C.csa2_ctx_check()
+
+    check()
+    used = int((base.refs > 0).sum())
+    for some in ((base,), (beams,), (base, beams), (wide, beams)):
+        assert int(P.pages_compact(*some)) == 60
+        with pytest.raises(C.Csa2Error):
+            C.csa2_ctx_check()
+        check()
+    assert int(base.refs[used:].sum()) > 0                # (there is something to move)
+    assert int(P.pages_compact(beams, wide, base)) == used
+    C.csa2_ctx_check()
+    assert not base.refs[used:].any() and max(int(c.table.max()) for c in (base, beams, wide)) == used - 1
+    check()
+    other = P.alloc_pages(1, 60, 4, 4, {"x": ((4,), torch.float32)}, DEV)
+    with pytest.raises(ValueError, match="same pools"):
+        P.pages_compact(base, other)
+
+
 def test_captured_appends_go_on(monkeypatch):
     """pages_append and pages_cut recorded once: every replay appends behind the entries of the one before."""
     monkeypatch.setattr(C, "alloc", lambda shape, dtype, device: torch.empty(shape, dtype=dtype, device=device))
