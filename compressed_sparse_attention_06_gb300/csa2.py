@@ -959,8 +959,9 @@ def csa2_pages_free(refs, table, page: int, keep: Optional[torch.Tensor] = None)
 
 def csa2_pages_reserve(refs, table, first, count, page: int, granted: Optional[torch.Tensor] = None,
                        copies: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
-    """Makes entries first[b] .. first[b]+count[b]-1 ([B] int64) writable: missing and shared pages are
-    replaced by free ones (refs and table are updated).  Returns (granted [B] int64, copies [B,2] int32):
+    """Makes entries first[b] .. first[b]+count[b]-1 ([B] int64), the last ones of their sequences, writable:
+    missing and shared pages are replaced by free ones (refs and table are updated; entries behind the range on
+    a shared page are not carried over).  Returns (granted [B] int64, copies [B,2] int32):
     how many of the entries got their page, and the pairs csa2_page_copy is to copy in every pool."""
     n, B, P, dev = _state(refs, table)
     _want("first", first, (B,), torch.int64, dev)

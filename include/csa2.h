@@ -722,7 +722,9 @@ csa2_status csa2_tree_commit(csa2_ctx* ctx, const void* draft, csa2_dtype dt, co
  *
  * csa2_pages_reserve -- makes entries first[b] .. first[b]+count[b]-1 of every sequence
  * writable: of the pages they lie on, a missing one, or one whose refs are above 1 when the call
- * starts, is replaced by a free page (the old one's refs down), in order of (b, page).
+ * starts, is replaced by a free page (the old one's refs down), in order of (b, page).  It is for
+ * ranges that end their sequences, as appended entries do: of a shared page that is replaced, the entries
+ * before `first` come along (copies), those behind the range do not.
  *   first, count : [B] int64 (first < 0 or count <= 0: nothing for this sequence)
  *   granted      : [B] int64, how many of the entries can be written: count, or fewer when the
  *                  pool ran out of pages or (flagged) the table's row is too short
