@@ -363,7 +363,9 @@ def draft_attention(q, cache: PagedCache, plan: DraftPlan, swa, draft, sink=None
     """A layer's attention for every drafted token over the pages of pool `kv`: its selected entries
     idx [B, T, k] (Full, Reindex and Reuse layers), or all visible ones (n_visible [B, T] <= k_max,
     the heavily compressed cache), its window of committed rows (the ring swa) and its own path's
-    draft rows."""
+    draft rows.  idx and n_visible name entries of the cache, so they stop at cache.n_entries: what a node past
+    the end of a block of m drafted tokens would see of that block (visible_entries counts it) is not an entry
+    before those tokens are accepted and their entry is appended."""
     o, _ = C.csa2_tree_attn(q, cache.pools[kv], plan.pos, plan.path, plan.ctx_len, swa, draft, idx=idx,
                             n_visible=n_visible, k_max=k_max, table=cache.table, sink=sink, window=window,
                             swa_pos0=swa_pos0, flags=flags, out=out, ws=ws)

@@ -655,7 +655,12 @@ csa2_status csa2_cache_gather(csa2_ctx* ctx, const void* src, int64_t row_bytes,
  *                                U  { draft[b, path[b,i,p - ctx_len[b]]], p >= ctx_len[b] },
  *     max(0, t - window + 1) <= p <= t = pos[b,i].
  * Norms, rotations, sink, out and lse as csa2_sparse_attn; a tree that is one chain gives what
- * csa2_sparse_attn gives over a ring that holds the draft rows.  An unused node attends to
+ * csa2_sparse_attn gives for the same entries over a ring that holds the draft rows.  The entries are
+ * those of the cache.  One that drafted tokens complete (floor(t / m) counts it at the node that ends its
+ * block and behind) is none of it while they are drafts: a node past such a border attends to fewer entries
+ * than the token will once it is committed, and so gets other values, unless the caller has appended an entry
+ * for every node that ends a block and names it in idx of that node and those below it, and of no others (the
+ * dense form, which takes the first entries, cannot name it).  An unused node attends to
  * nothing: out 0, lse the sink (or -inf).
  *   q         : [B, T, H, c] in q_dt (F32 or BF16)
  *   kv        : table NULL: [B, N, row] (F32, BF16 or CSA2_FP4_E4M3x16);
