@@ -361,7 +361,8 @@ def draft_attention(q, cache: PagedCache, plan: DraftPlan, swa, draft, sink=None
                     k_max: int = 0, kv: str = "kv", window: int = 128, swa_pos0: int = 0, flags: int = C.ATTN_DEFAULT,
                     out=None, ws=None):
     """A layer's attention for every drafted token over the pages of pool `kv`: its selected entries
-    idx [B, T, k] (Full, Reindex and Reuse layers), or all visible ones (n_visible [B, T] <= k_max,
+    idx [B, T, k] (Full, Reindex and Reuse layers; the indexer itself does not read pages, so keys kept in
+    them are read out by csa2_page_read first), or all visible ones (n_visible [B, T] <= k_max,
     the heavily compressed cache), its window of committed rows (the ring swa) and its own path's
     draft rows.  idx and n_visible name entries of the cache, so they stop at cache.n_entries: what a node past
     the end of a block of m drafted tokens would see of that block (visible_entries counts it) is not an entry

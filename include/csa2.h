@@ -715,6 +715,9 @@ csa2_status csa2_tree_commit(csa2_ctx* ctx, const void* draft, csa2_dtype dt, co
  * free).  All calls are ordered by the stream; none needs the host to read anything, so they can
  * be captured.  New pages are the lowest free ones, so results do not depend on timing.  Page ids
  * outside [0, n_pages) other than -1 are skipped and flagged.
+ * Of the attention, csa2_tree_attn reads rows through a table; of the indexer nothing does
+ * (csa2_index_score, csa2_index_score_mxq take keys [B, N, row]): keys that are kept in pages are read out
+ * by csa2_page_read before a selection is made from them, or are kept in one block a sequence beside them.
  *
  * csa2_pages_fork -- continuations that share their origin's pages:
  *     table_out[i] = table[parent[i]], every page's refs up by its new places.
