@@ -183,6 +183,19 @@ def test_bf16_dense(kind, B, T, H, N, window, page):
     c.check(out, lse, **BF)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp4"])
+@pytest.mark.parametrize("flags,base", [(3, 10000.0), (7, 500.0), (7, 1e7)])
+@pytest.mark.parametrize("sink", [True, False])
+@pytest.mark.parametrize("B,T,H,N,k,dense", [(2, 5, 40, 300, 100, False), (1, 2, 64, 3000, 1500, False), (2, 9, 24, 150, 0, True),
+                                             (1, 3, 16, 2500, 0, True)])
+def test_bf16_path_flags(kind, flags, base, sink, B, T, H, N, k, dense):
+    """Without rotations, with other angles, with and without a sink, whole groups and ones that are dealt out."""
+    c = Case(55, B, T, H, N, k, kind, window=40, page=16, dense=dense, unused=T // 4)
+    out, lse = c.run(flags=flags, sink=c.sink if sink else None, rope_base=base, out_dtype=torch.float32)
+    C.csa2_ctx_check()
+    c.check(out, lse, **BF, sink=sink, flags=flags, base=base)
+
+
 @pytest.mark.parametrize("window,T", [(1, 6), (4, 12), (128, 12), (128, 200)])
 @pytest.mark.parametrize("dt,kind", [(torch.float32, "f32"), (torch.bfloat16, "bf16")])
 def test_chain_equals_the_sparse_attention_over_a_ring(window, T, dt, kind):
@@ -342,6 +355,32 @@ def test_commit(dt, cap, T):
     with pytest.raises(C.Csa2Error):
         C.csa2_ctx_check()
     assert torch.equal(swa, want) and torch.equal(lens, new)
+
+
+def test_selection_from_keys_in_pages():
+    """A Full layer over pages: its keys are read out, scored and selected from, and the selection's rows read
+    through the table; the same as over blocks of their own."""
+    B, T, H, n, N, k = 2, 5, 16, 200, 208, 40
+    rows = {"kv": ((512,), torch.bfloat16), "ki": ((128,), torch.bfloat16)}
+    x = {name: W.normal_tensor((B, n, *shape), 85, i, dt, DEV) for i, (name, (shape, dt)) in enumerate(rows.items())}
+    cache = P.alloc_pages(B, 40, 16, 13, rows, DEV)
+    P.pages_append(cache, x, torch.tensor([n, 150], device=DEV))
+    plan = P.plan_draft(_tree(86, B, T), cache.n_entries * 4)
+    seen = torch.minimum(P.visible_entries(plan.pos.clamp(min=0), 4), cache.n_entries.unsqueeze(-1))
+    qI, w = W.normal_tensor((B, T, 64, 128), 87, 1, torch.bfloat16, DEV), W.normal_tensor((B, T, 64), 87, 2, torch.float32, DEV)
+    ids = torch.arange(N, dtype=torch.int32, device=DEV).expand(B, N)
+    ids = torch.where(ids < cache.n_entries.unsqueeze(-1), ids, -1).int().contiguous()
+    keys = C.csa2_page_read(cache.pools["ki"], cache.table, ids, out=torch.zeros(B, N, 128, dtype=torch.bfloat16, device=DEV))
+    _, idx = P.full_topk_step(qI, w, keys, seen, k=k)
+    q, draft = W.normal_tensor((B, T, H, 512), 88, 1, torch.bfloat16, DEV), W.normal_tensor((B, T, 512), 88, 2, torch.bfloat16, DEV)
+    swa = W.normal_tensor((B, 20, 512), 88, 3, torch.bfloat16, DEV)
+    out = P.draft_attention(q, cache, plan, swa, draft, idx=idx, window=12)
+    C.csa2_ctx_check()
+    _, want_idx = P.full_topk_step(qI, w, torch.nn.functional.pad(x["ki"], (0, 0, 0, N - n)), seen, k=k)
+    assert torch.equal(idx, want_idx)
+    want, _ = C.csa2_tree_attn(q, x["kv"], plan.pos, plan.path, plan.ctx_len, swa, draft, idx=idx, window=12)
+    C.csa2_ctx_check()
+    assert torch.equal(out, want)
 
 
 @pytest.mark.parametrize("T", [1, 5, 256])
