@@ -9,9 +9,11 @@
 //           shared memory;
 //   output  a thread holds 2 dims of 16 heads: one 8-byte read and 4 broadcasts, 32 multiply-adds.
 // The softmax is online over chunks of 32 rows; few nodes split their rows over several CTAs,
-// joined by log-sum-exp.  Measured: 2 x 13 nodes of 16 heads, 301 entries and a window of 100 each, 30 us of
-// which 3.4 are their multiply-adds; bf16 and FP4 rows take 14 to 50 times as long here as on the tensor
-// cores (8 x 32 nodes of 64 heads over FP4 pages: 1,414 us, there 89).
+// joined by log-sum-exp.  Measured: 2 x 13 nodes of 16 heads, 301 entries and a window of 100 each, 33 us of
+// which 3.4 are their multiply-adds.  Large calls are bound by shared memory's port: 256 nodes of 64 heads over
+// 640 slots keep it 78 % busy and the multiply-adds 35 %, and a warp waits for it 2.2 of the 7.1 cycles that an
+// instruction takes (0.2 at barriers).  Calls that the tensor cores take too last 10 to 37 times as long here
+// (8 x 32 nodes of 64 heads over FP4 pages 880 us, there 86; 4 x 64 over 4,096 bf16 entries 5,529 and 151).
 #include <algorithm>
 
 #include "csa2_internal.cuh"
@@ -168,7 +170,7 @@ struct SimtSmem {
 };
 // Two CTAs an SM (1 KB each is the system's): with one, the rows' way from memory was in the open, and 256
 // nodes of 64 heads over 640 slots took 1,292 us; with two 1,105, with the rows looked up a chunk ahead 975,
-// stored without bank conflicts 908 (24 TFLOP/s).
+// stored without bank conflicts 908, with a look for infinities in them 923 (23 TFLOP/s).
 static_assert(2 * (sizeof(SimtSmem) + 1024) <= 228 * 1024, "shared memory");
 
 template <int KVK>                       // 0 fp32 rows, 1 bf16, 2 FP4

@@ -26,8 +26,8 @@
 // the swizzled image of the A operand, the RoPE table, and for every slot its row (-1: none), f (the window's rows: once for all nodes), and as
 // bits which nodes attend to it.  (A row's squares need all of its dims, of which a CTA has half: with
 // the sums exchanged like the logits, and the rows through registers for them, the loaders were what a
-// tile waited for.)  It reads every slot's row once, at 7.7 TB/s out of L2 (8 x 24 nodes of 1,024
-// entries: 26 us).
+// tile waited for.)  It reads the row of every slot once: of 8 x 24 nodes of 128 heads, 133 of them used, 136,192
+// rows of 1 KB in 24.7 us, 5.6 TB/s, beside 50 MB of queries read and images written.
 //
 // Warps (768 threads, one CTA an SM):
 //   0       query images (bulk copies)
